@@ -10,7 +10,9 @@ Entry points mirror the C ABI in include/ds4moe.h:
 ``Layer.forward`` = ds4moe_forward, ``Layer.forward_rmsnorm`` =
 ds4moe_forward_rmsnorm, ``Layer.forward_host`` = ds4moe_forward_host,
 ``rmsnorm`` = ds4moe_rmsnorm, ``route_noalloc`` =
-ds4moe_route_noalloc, ``Dense`` = the ds4moe_dense_* calls.
+ds4moe_route_noalloc, ``Dense`` = the ds4moe_dense_* calls, ``Attention`` (with
+``AttentionDesc`` and ``KVCache``) = ds4moe_attn_* and ds4moe_kv_append,
+``token_probs`` = ds4moe_token_probs, ``verify_drafts`` = ds4moe_verify_drafts.
 """
 from __future__ import annotations
 
@@ -25,7 +27,10 @@ F32, Q8_0, Q2S, Q4S = 0, 1, 2, 3
 FMT = {"f32": F32, "q8_0": Q8_0, "q2s": Q2S, "q4s": Q4S}
 ROUTE_LEARNED, ROUTE_HASH = 0, 1
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED", 3: "ERR_OOM", 4: "ERR_CUDA", 5: "ERR_DEVICE"}
-DEVERR_TOKEN_ID, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_INTERNAL = 1, 2, 4, 8
+DEVERR_TOKEN_ID, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_INTERNAL, DEVERR_PAGE, DEVERR_LENGTH = 1, 2, 4, 8, 16, 32
+DT_F32, DT_BF16, DT_F16 = 0, 1, 2
+DTYPE = {"fp32": DT_F32, "bf16": DT_BF16, "fp16": DT_F16}
+ATTN_MAX_NEW, MAX_DRAFT = 16, 64
 
 LIB_PATH = _build.LIB
 
@@ -49,6 +54,22 @@ class _Weights(ctypes.Structure):
                 ("router_w", "router_bias", "hash_table", "gate", "up", "down", "sh_gate", "sh_up", "sh_down")]
 
 
+class _AttnDesc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("n_sink", ctypes.c_int32), ("scale", ctypes.c_float), ("max_seqs", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("k_page_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -61,7 +82,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libds4moe.so not found at {LIB_PATH}")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i32, u32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32
+        vp, i32, u32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64
         sigs = {
             "ds4moe_create": (i32, [ctypes.POINTER(_Desc), ctypes.POINTER(_Weights), ctypes.POINTER(vp)]),
             "ds4moe_destroy": (None, [vp]),
@@ -91,6 +112,16 @@ def lib():
             "ds4moe_dense_device_bytes": (ctypes.c_uint64, [vp]),
             "ds4moe_dense_launch_count": (ctypes.c_uint64, [vp]),
             "ds4moe_dense_debug_config": (i32, [vp, i32, i32, i32, i32]),
+            "ds4moe_attn_create": (i32, [ctypes.POINTER(_AttnDesc), ctypes.POINTER(vp)]),
+            "ds4moe_attn_destroy": (None, [vp]),
+            "ds4moe_kv_append": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i64, i32, vp, vp, i32, i32, vp]),
+            "ds4moe_attn_decode": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i32, i32, vp, i64, vp]),
+            "ds4moe_attn_prefill": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, vp, i32, i32, vp, i64, vp]),
+            "ds4moe_attn_get_device_error": (i32, [vp, vp, ctypes.POINTER(u32)]),
+            "ds4moe_attn_device_bytes": (ctypes.c_uint64, [vp]),
+            "ds4moe_attn_launch_count": (ctypes.c_uint64, [vp]),
+            "ds4moe_token_probs": (i32, [vp, i64, i32, i32, ctypes.c_float, vp, i64, vp]),
+            "ds4moe_verify_drafts": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]),
         }
         for name, (res, args) in sigs.items():
             f = getattr(L, name)
@@ -301,6 +332,243 @@ class Dense:
         automatic); a tuning and test hook (ds4moe_dense_debug_config)."""
         _check(lib().ds4moe_dense_debug_config(self._h, int(ks), int(nst), int(ns), int(tc)),
                "ds4moe_dense_debug_config")
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, name, dtype, shape):
+    """Elements from one row of `t` to the next: `shape` after the leading
+    dimensions, contiguous, the leading dimensions evenly spaced."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype, f"{name}: a CUDA tensor of {dtype}")
+    lead = t.dim() - len(shape)
+    _need(lead >= 1 and tuple(t.shape[lead:]) == tuple(shape), f"{name}: shape [..., {', '.join(map(str, shape))}]")
+    inner = 1
+    for n, s in zip(reversed(shape), reversed(t.stride()[lead:])):
+        _need(n == 1 or s == inner, f"{name}: a row must be contiguous")
+        inner *= n
+    if t.numel() == 0:
+        return inner
+    row, step = None, None  # the stride of a row; the stride the next leading dimension must have
+    for n, s in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
+        if n == 1:
+            continue
+        if row is None:
+            row = s
+        else:
+            _need(s == step, f"{name}: rows must be evenly spaced")
+        step = s * n
+    return inner if row is None else row
+
+
+def _vec(t, name, dtype, n):
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous(),
+          f"{name}: a contiguous CUDA tensor of {n} {dtype}")
+    return _ptr(t)
+
+
+def _fresh(out, stream):
+    """`out` was allocated on the current stream and is written on `stream`."""
+    import torch
+    if stream is not None and out.is_cuda:
+        out.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return out
+
+
+def _torch_dtype(dt):
+    import torch
+    return {DT_F32: torch.float32, DT_BF16: torch.bfloat16, DT_F16: torch.float16}[dt]
+
+
+@dataclass
+class AttentionDesc:
+    """Shape of the attention beside the MoE (ds4moe_attn_desc). `scale` None:
+    1 / sqrt(head_dim)."""
+    n_heads: int
+    n_kv_heads: int
+    head_dim: int
+    dtype: str = "bf16"  # "bf16" | "fp16": q, cache and output
+    window: int = 0
+    n_sink: int = 0
+    scale: float | None = None
+    max_seqs: int = 1
+    max_tokens: int = 1
+
+    def c(self) -> _AttnDesc:
+        scale = self.scale if self.scale is not None else max(self.head_dim, 1) ** -0.5
+        return _AttnDesc(ABI_VERSION, self.n_heads, self.n_kv_heads, self.head_dim, DTYPE[self.dtype], self.window,
+                         self.n_sink, scale, self.max_seqs, self.max_tokens)
+
+
+class KVCache:
+    """A paged cache (ds4moe_kv_cache): `k`, `v` are CUDA tensors [n_pages,
+    page_size, n_kv_heads, head_dim] (any strides over the first three),
+    `block_table` int32 [n_seq, max_pages]. Keeps the tensors; their contents
+    may change between calls."""
+
+    def __init__(self, k, v, block_table):
+        import torch
+        for t, name in ((k, "k"), (v, "v")):
+            _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.stride(3) == 1,
+                  f"{name}: a CUDA tensor [n_pages, page_size, n_kv_heads, head_dim], head_dim contiguous")
+        _need(k.shape == v.shape and k.dtype == v.dtype, "k and v: the same shape and type")
+        _need(isinstance(block_table, torch.Tensor) and block_table.is_cuda and block_table.dim() == 2 and
+              block_table.dtype == torch.int32 and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
+              "block_table: a CUDA int32 tensor [n_seq, max_pages] with contiguous rows")
+        self.k, self.v, self.block_table = k, v, block_table
+        stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+        self.c = _KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
+                          v.stride(1), v.stride(2), block_table.data_ptr(), stride, k.shape[1], block_table.shape[1])
+
+
+class Attention:
+    """Append to, and attention over, a paged key-value cache (ds4moe_attn_*)."""
+
+    def __init__(self, desc: AttentionDesc):
+        h = ctypes.c_void_p()
+        _check(lib().ds4moe_attn_create(ctypes.byref(desc.c()), ctypes.byref(h)), "ds4moe_attn_create")
+        self.desc, self._h = desc, h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ds4moe_attn_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _cache(self, cache, n_seq):
+        d = self.desc
+        _need(isinstance(cache, KVCache), "cache: a KVCache")
+        _need(tuple(cache.k.shape[2:]) == (d.n_kv_heads, d.head_dim) and
+              cache.k.dtype == _torch_dtype(DTYPE[d.dtype]), "cache: heads, dimension or type differ from the handle's")
+        _need(cache.block_table.shape[0] >= n_seq, "cache: a block-table row for every sequence")
+        return ctypes.byref(cache.c)
+
+    def append(self, cache, k, v, kv_len, cu_q=None, stream=None):
+        """Write new keys and values (ds4moe_kv_append): k, v [n_tok, n_kv_heads,
+        head_dim] or [n_seq, n_new, ...], fp32 or the cache's type; v may be None
+        (the keys only). kv_len int32 [n_seq] counts the new tokens."""
+        import torch
+        d, n_seq = self.desc, kv_len.numel()
+        row = (d.n_kv_heads, d.head_dim)
+        dt = torch.float32 if k.dtype == torch.float32 else _torch_dtype(DTYPE[d.dtype])
+        ks = _rows(k, "k", dt, row)
+        n_tok = k.numel() // (row[0] * row[1])
+        vs = 0
+        if v is not None:
+            _need(v.shape == k.shape, "v: the shape of k")
+            vs = _rows(v, "v", dt, row)
+        _check(lib().ds4moe_kv_append(
+            self._h, self._cache(cache, n_seq), _ptr(k), ks, _ptr(v), vs,
+            DT_F32 if dt == torch.float32 else DTYPE[d.dtype],
+            None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, n_seq + 1),
+            _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_tok, _stream(stream)), "ds4moe_kv_append")
+
+    def _out(self, q, out, stream):
+        import torch
+        if out is None:
+            out = _fresh(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+        _need(out.shape == q.shape, "out: the shape of q")
+        return out
+
+    def decode(self, cache, q, kv_len, out=None, stream=None):
+        """Attention of the last n_new tokens of every sequence
+        (ds4moe_attn_decode): q [n_seq, n_new, n_heads, head_dim]; returns out."""
+        import torch
+        d, dt = self.desc, _torch_dtype(DTYPE[self.desc.dtype])
+        _need(q.dim() == 4, "q: [n_seq, n_new, n_heads, head_dim]")
+        n_seq, n_new = q.shape[:2]
+        qs = _rows(q, "q", dt, (d.n_heads, d.head_dim))
+        out = self._out(q, out, stream)
+        os_ = _rows(out, "out", dt, (d.n_heads, d.head_dim))
+        _check(lib().ds4moe_attn_decode(self._h, self._cache(cache, n_seq), _ptr(q), qs,
+                                        _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_new, _ptr(out), os_,
+                                        _stream(stream)), "ds4moe_attn_decode")
+        return out
+
+    def prefill(self, cache, q, cu_q, kv_len, out=None, stream=None):
+        """Attention of ragged runs of new tokens (ds4moe_attn_prefill): q
+        [n_tok, n_heads, head_dim], cu_q int32 [n_seq + 1]; returns out."""
+        import torch
+        d, dt = self.desc, _torch_dtype(DTYPE[self.desc.dtype])
+        _need(q.dim() == 3, "q: [n_tok, n_heads, head_dim]")
+        n_seq = kv_len.numel()
+        qs = _rows(q, "q", dt, (d.n_heads, d.head_dim))
+        out = self._out(q, out, stream)
+        os_ = _rows(out, "out", dt, (d.n_heads, d.head_dim))
+        _check(lib().ds4moe_attn_prefill(self._h, self._cache(cache, n_seq), _ptr(q), qs,
+                                         _vec(cu_q, "cu_q", torch.int32, n_seq + 1),
+                                         _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, q.shape[0], _ptr(out), os_,
+                                         _stream(stream)), "ds4moe_attn_prefill")
+        return out
+
+    def device_error(self, stream=None) -> int:
+        """Synchronise, read and clear the device error flags (0 = none)."""
+        f = ctypes.c_uint32(0)
+        st = lib().ds4moe_attn_get_device_error(self._h, _stream(stream), ctypes.byref(f))
+        if st not in (0, 5):
+            raise Ds4MoeError(st, "ds4moe_attn_get_device_error")
+        return int(f.value)
+
+    def device_bytes(self) -> int:
+        return int(lib().ds4moe_attn_device_bytes(self._h))
+
+    def launch_count(self) -> int:
+        return int(lib().ds4moe_attn_launch_count(self._h))
+
+
+def token_probs(logits, temperature: float = 1.0, out=None, stream=None):
+    """softmax(logits / temperature) over the last dimension of an fp32 CUDA
+    tensor (ds4moe_token_probs); temperature 0: one at the lowest index of the
+    maximum. `out` may be `logits`; returns out."""
+    import torch
+    V = logits.shape[-1]
+    if out is None:
+        out = _fresh(torch.empty(logits.shape, dtype=torch.float32, device=logits.device), stream)
+    _need(out.shape == logits.shape, "out: the shape of logits")
+    if logits.dim() == 1:
+        logits_, out_ = logits[None], out[None]
+    else:
+        logits_, out_ = logits, out
+    xs, os_ = _rows(logits_, "logits", torch.float32, (V,)), _rows(out_, "out", torch.float32, (V,))
+    _check(lib().ds4moe_token_probs(_ptr(logits), xs, logits.numel() // max(V, 1), V, temperature, _ptr(out), os_,
+                                    _stream(stream)), "ds4moe_token_probs")
+    return out
+
+
+def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_accepted=None, tokens_out=None,
+                  err_flags=None, stream=None):
+    """Which drafted tokens stay, and the token after them
+    (ds4moe_verify_drafts): target fp32 [n_seq, max_draft + 1, vocab], draft
+    fp32 [n_seq, max_draft, vocab] or None, tokens int32 [n_seq, max_draft].
+    Returns (n_accepted int32 [n_seq], tokens_out int32 [n_seq, max_draft + 1])."""
+    import torch
+    _need(target.dim() == 3, "target: [n_seq, max_draft + 1, vocab]")
+    B, G, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    ts, ds = _rows(target, "target", torch.float32, (V,)), 0
+    if draft is not None:
+        _need(tuple(draft.shape) == (B, G, V), "draft: [n_seq, max_draft, vocab]")
+        ds = _rows(draft, "draft", torch.float32, (V,))
+    if n_accepted is None:
+        n_accepted = _fresh(torch.empty(B, dtype=torch.int32, device=target.device), stream)
+    if tokens_out is None:
+        tokens_out = _fresh(torch.empty((B, G + 1), dtype=torch.int32, device=target.device), stream)
+    _check(lib().ds4moe_verify_drafts(
+        _ptr(target), ts, _ptr(draft), ds, _vec(tokens, "tokens", torch.int32, B * G),
+        None if n_draft is None else _vec(n_draft, "n_draft", torch.int32, B),
+        _vec(u_accept, "u_accept", torch.float32, B * G), _vec(u_sample, "u_sample", torch.float32, B), B, G, V,
+        _vec(n_accepted, "n_accepted", torch.int32, B), _vec(tokens_out, "tokens_out", torch.int32, B * (G + 1)),
+        None if err_flags is None else _vec(err_flags, "err_flags", torch.int32, 1), _stream(stream)),
+        "ds4moe_verify_drafts")
+    return n_accepted, tokens_out
 
 
 def rmsnorm(x, out, eps: float = 1e-6, stream=None):

@@ -1,0 +1,259 @@
+// attn.cu -- the attention handle (ds4moe_attn_*): argument checks, the
+// append of new keys and values to the paged cache, and the choice of kernel.
+#include <math.h>
+#include <string.h>
+
+#include <new>
+
+#include "attn.cuh"
+#include "internal.h"
+
+namespace ds4 {
+
+// Copies rows of new keys and values to their places in the pages, rounding
+// to the cache's type. One thread per 8 elements (16 bytes of the cache);
+// neighbouring threads take neighbouring elements of a row.
+struct AppendArgs {
+  KvView kv;
+  const void *k, *v;           // v null: the keys only
+  long long k_stride, v_stride;
+  const int32_t *kv_len, *cu_q;
+  int32_t n_seq, n_tok, n_new, n_kv, D, per_tok;  // per_tok: 8-element pieces of a token's keys
+  uint32_t *err;
+};
+
+template <int DT, bool F32>
+__global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long total = (long long)a.n_tok * a.per_tok;
+  const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (i >= total) return;
+  const int t = (int)(i / a.per_tok), e = (int)(i - (long long)t * a.per_tok) * 8;
+  int b, at, n;
+  if (!a.cu_q) {
+    b = t / a.n_new, at = t - b * a.n_new, n = a.n_new;
+  } else {
+    // the last sequence that starts at or before row t
+    int lo = 0, hi = a.n_seq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu_q[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+    if (t < c0 || t >= c1) return;  // a row of no sequence
+    at = t - c0, n = c1 - c0;
+  }
+  const long long pos = (long long)a.kv_len[b] - n + at;
+  if (pos < 0 || pos >= (long long)a.kv.width * a.kv.page_size) {
+    raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+    return;
+  }
+  const int page = page_of(a.kv, b, (int)pos);
+  if (page < 0) {
+    raise_flag(a.err, DS4MOE_DEVERR_PAGE);
+    return;
+  }
+  const int row = (int)pos % a.kv.page_size, h = e / a.D, d = e - h * a.D;
+  const int kv = blockIdx.y;
+  const void *src = kv ? a.v : a.k;
+  const long long off = (long long)t * (kv ? a.v_stride : a.k_stride) + e;
+  uint4 o;
+  if (F32) {
+    const float4 *p = reinterpret_cast<const float4 *>((const float *)src + off);
+    const float4 x = p[0], y = p[1];
+    o = make_uint4(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w), Half16<DT>::down(y.x, y.y),
+                   Half16<DT>::down(y.z, y.w));
+  } else {
+    o = *reinterpret_cast<const uint4 *>((const uint16_t *)src + off);
+  }
+  uint16_t *dst = const_cast<uint16_t *>(kv ? a.kv.v : a.kv.k);
+  dst += kv ? (long long)page * a.kv.v_page + (long long)row * a.kv.v_row + (long long)h * a.kv.v_head + d
+            : (long long)page * a.kv.k_page + (long long)row * a.kv.k_row + (long long)h * a.kv.k_head + d;
+  *reinterpret_cast<uint4 *>(dst) = o;
+}
+
+}  // namespace ds4
+
+namespace {
+
+using namespace ds4;
+
+bool at_dev_ptr(const void *p) {
+  if (!p) return false;
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
+}
+
+ds4moe_status at_status(cudaError_t e) {
+  if (e == cudaSuccess) return DS4MOE_OK;
+  cudaGetLastError();
+  return e == cudaErrorMemoryAllocation ? DS4MOE_ERR_OOM : DS4MOE_ERR_CUDA;
+}
+
+bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// Strides the kernels take: multiples of 16 bytes, below 2^39 elements.
+bool stride_ok(long long s, long long least) { return s >= least && s % 8 == 0 && s < (1ll << 39); }
+
+// The cache as the kernels see it; false when the description is not one
+// they can read.
+bool view_of(const ds4moe_attn *h, const ds4moe_kv_cache *c, KvView &v) {
+  const int D = h->d.head_dim, H = h->d.n_kv_heads;
+  if (!c || c->n_pages < 1 || c->n_pages > INT32_MAX - 1 || c->page_size < 16 || c->page_size > 65536 ||
+      c->page_size % 16)
+    return false;
+  if (c->max_pages < 1 || c->table_stride < c->max_pages || c->table_stride >= (1ll << 39) ||
+      (long long)c->max_pages * c->page_size > INT32_MAX - 1024)
+    return false;
+  v.k = (const uint16_t *)c->k, v.v = (const uint16_t *)c->v;
+  // the stride over a single head is never used
+  v.k_page = c->k_page_stride, v.k_row = c->k_row_stride, v.k_head = H == 1 ? D : c->k_head_stride;
+  v.v_page = c->v_page_stride, v.v_row = c->v_row_stride, v.v_head = H == 1 ? D : c->v_head_stride;
+  if (c->n_pages == 1) v.k_page = v.v_page = (long long)c->page_size * H * D;
+  for (long long s : {v.k_page, v.k_row, v.k_head, v.v_page, v.v_row, v.v_head})
+    if (!stride_ok(s, D)) return false;
+  v.table = c->block_table, v.table_stride = c->table_stride;
+  v.page_size = c->page_size, v.width = c->max_pages, v.n_pages = (int32_t)c->n_pages;
+  return at_dev_ptr(c->k) && at_dev_ptr(c->v) && al16(c->k) && al16(c->v) && at_dev_ptr(c->block_table);
+}
+
+ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                        const int32_t *cu_q, bool ragged, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
+                        int32_t n_new, void *out, int64_t out_stride, void *stream) {
+  const ds4moe_attn_desc &d = h->d;
+  AttnArgs a = {};
+  if (!view_of(h, cache, a.kv)) return DS4MOE_ERR_INVALID_ARG;
+  const long long row = (long long)d.n_heads * d.head_dim;
+  if (n_tok == 1) q_stride = out_stride = row;
+  if (!stride_ok(q_stride, row) || !stride_ok(out_stride, row) || !al16(q) || !al16(out)) return DS4MOE_ERR_INVALID_ARG;
+  if (!at_dev_ptr(q) || !at_dev_ptr(out) || !at_dev_ptr(kv_len) || (ragged && !at_dev_ptr(cu_q)))
+    return DS4MOE_ERR_INVALID_ARG;
+  a.q = (const uint16_t *)q, a.out = (uint16_t *)out, a.q_stride = q_stride, a.out_stride = out_stride;
+  a.kv_len = kv_len, a.cu_q = ragged ? cu_q : nullptr;
+  a.n_seq = n_seq, a.n_tok = n_tok, a.n_new = n_new;
+  a.n_heads = d.n_heads, a.n_kv = d.n_kv_heads, a.group = d.n_heads / d.n_kv_heads;
+  a.window = d.window, a.n_sink = d.window ? d.n_sink : 0;
+  a.scale_log2 = d.scale * 1.44269504088896340736f;  // log2(e)
+  a.err = h->err;
+  const cudaError_t e = launch_attn_rows(a, d.head_dim, d.dtype, (cudaStream_t)stream);
+  h->launches++;
+  return at_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out) {
+  if (!out) return DS4MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!desc || desc->abi_version != DS4MOE_ABI_VERSION) return DS4MOE_ERR_INVALID_ARG;
+  const ds4moe_attn_desc &d = *desc;
+  if (d.n_kv_heads < 1 || d.n_kv_heads > 1024 || d.n_heads < d.n_kv_heads || d.n_heads % d.n_kv_heads)
+    return DS4MOE_ERR_INVALID_ARG;
+  if (d.dtype != DS4MOE_DT_BF16 && d.dtype != DS4MOE_DT_F16) return DS4MOE_ERR_INVALID_ARG;
+  if (d.window < 0 || d.n_sink < 0) return DS4MOE_ERR_INVALID_ARG;
+  if (!isfinite(d.scale) || d.scale <= 0.0f) return DS4MOE_ERR_INVALID_ARG;
+  if (d.max_seqs < 1 || d.max_seqs > 65536 || d.max_tokens < 1 || d.max_tokens > (1 << 20))
+    return DS4MOE_ERR_INVALID_ARG;
+  if (d.head_dim < 1) return DS4MOE_ERR_INVALID_ARG;
+  if ((d.head_dim != 64 && d.head_dim != 128 && d.head_dim != 256 && d.head_dim != 512) ||
+      d.n_heads / d.n_kv_heads > 128)
+    return DS4MOE_ERR_UNSUPPORTED;
+  ds4moe_attn *h = new (std::nothrow) ds4moe_attn;
+  if (!h) return DS4MOE_ERR_OOM;
+  memset(h, 0, sizeof(*h));
+  h->d = d;
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device);
+  if (e == cudaSuccess) e = cudaMalloc((void **)&h->err, 64);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 64, 0);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(0);
+  if (e != cudaSuccess) {
+    const ds4moe_status st = at_status(e);
+    if (h->err) cudaFree(h->err);
+    cudaGetLastError();
+    delete h;
+    return st;
+  }
+  h->bytes = 64;
+  *out = h;
+  return DS4MOE_OK;
+}
+
+void ds4moe_attn_destroy(ds4moe_attn *h) {
+  if (!h) return;
+  cudaDeviceSynchronize();
+  cudaFree(h->err);
+  delete h;
+}
+
+ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *k_new, int64_t k_stride,
+                               const void *v_new, int64_t v_stride, int32_t src_dtype, const int32_t *cu_q,
+                               const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *stream) {
+  if (!h || n_seq < 0 || n_seq > h->d.max_seqs || n_tok < 0 || n_tok > h->d.max_tokens) return DS4MOE_ERR_INVALID_ARG;
+  if (src_dtype != DS4MOE_DT_F32 && src_dtype != h->d.dtype) return DS4MOE_ERR_INVALID_ARG;
+  if (n_seq == 0 || n_tok == 0) return DS4MOE_OK;
+  if (!cu_q && n_tok % n_seq) return DS4MOE_ERR_INVALID_ARG;
+  const int row = h->d.n_kv_heads * h->d.head_dim;
+  AppendArgs a = {};
+  if (!view_of(h, cache, a.kv)) return DS4MOE_ERR_INVALID_ARG;
+  if (n_tok == 1) k_stride = v_stride = row;
+  if (!stride_ok(k_stride, row) || !al16(k_new) || !at_dev_ptr(k_new)) return DS4MOE_ERR_INVALID_ARG;
+  if (v_new && (!stride_ok(v_stride, row) || !al16(v_new) || !at_dev_ptr(v_new))) return DS4MOE_ERR_INVALID_ARG;
+  if (!at_dev_ptr(kv_len) || (cu_q && !at_dev_ptr(cu_q))) return DS4MOE_ERR_INVALID_ARG;
+  a.k = k_new, a.v = v_new, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.kv_len = kv_len, a.cu_q = cu_q, a.n_seq = n_seq, a.n_tok = n_tok, a.n_new = cu_q ? 0 : n_tok / n_seq;
+  a.n_kv = h->d.n_kv_heads, a.D = h->d.head_dim, a.per_tok = row / 8, a.err = h->err;
+  const bool bf = h->d.dtype == DS4MOE_DT_BF16;
+  const void *fn = src_dtype == DS4MOE_DT_F32
+                       ? (bf ? (const void *)k_kv_append<DS4MOE_DT_BF16, true> : (const void *)k_kv_append<DS4MOE_DT_F16, true>)
+                       : (const void *)k_kv_append<DS4MOE_DT_BF16, false>;  // the same type: bits are copied
+  void *args[] = {&a};
+  const long long total = (long long)n_tok * a.per_tok;
+  const cudaError_t e = launch_pdl(fn, dim3((unsigned)((total + 127) / 128), v_new ? 2 : 1), dim3(128), 0,
+                                   (cudaStream_t)stream, args, true);
+  h->launches++;
+  return at_status(e);
+}
+
+ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                                 const int32_t *kv_len, int32_t n_seq, int32_t n_new, void *out, int64_t out_stride,
+                                 void *stream) {
+  if (!h || n_seq < 0 || n_seq > h->d.max_seqs || n_new < 1 || n_new > DS4MOE_ATTN_MAX_NEW ||
+      (long long)n_seq * n_new > h->d.max_tokens)
+    return DS4MOE_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4MOE_OK;
+  return attn_call(h, cache, q, q_stride, nullptr, false, kv_len, n_seq, n_seq * n_new, n_new, out, out_stride, stream);
+}
+
+ds4moe_status ds4moe_attn_prefill(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                                  const int32_t *cu_q, const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *out,
+                                  int64_t out_stride, void *stream) {
+  if (!h || n_seq < 0 || n_seq > h->d.max_seqs || n_tok < 0 || n_tok > h->d.max_tokens) return DS4MOE_ERR_INVALID_ARG;
+  if (n_seq == 0 || n_tok == 0) return DS4MOE_OK;
+  return attn_call(h, cache, q, q_stride, cu_q, true, kv_len, n_seq, n_tok, 0, out, out_stride, stream);
+}
+
+ds4moe_status ds4moe_attn_get_device_error(ds4moe_attn *h, void *stream, uint32_t *flags_out) {
+  if (!h) return DS4MOE_ERR_INVALID_ARG;
+  uint32_t f = 0;
+  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemcpy(&f, h->err, 4, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemset(h->err, 0, 4);
+  if (e != cudaSuccess) return at_status(e);
+  if (flags_out) *flags_out = f;
+  return f ? DS4MOE_ERR_DEVICE : DS4MOE_OK;
+}
+
+uint64_t ds4moe_attn_device_bytes(const ds4moe_attn *h) { return h ? h->bytes : 0; }
+uint64_t ds4moe_attn_launch_count(const ds4moe_attn *h) { return h ? h->launches : 0; }
+
+}  // extern "C"

@@ -1,0 +1,160 @@
+// attn.cuh -- device helpers shared by the attention kernels: which positions
+// a query sees, where a position lies in the paged cache, and the attention
+// of one row by one warp.
+//
+// The query at position i sees position j when
+//   j <= i  and  (window == 0  or  j > i - window  or  j < n_sink).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace ds4 {
+
+template <int DT>
+struct Half16;  // the two 16-bit types
+template <>
+struct Half16<DS4MOE_DT_BF16> {
+  static __device__ __forceinline__ float2 up(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t down(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+};
+template <>
+struct Half16<DS4MOE_DT_F16> {
+  static __device__ __forceinline__ float2 up(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+  }
+  static __device__ __forceinline__ uint32_t down(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows and length of sequence b, clamped to what the buffers hold; `bad` is
+// set when a value had to be clamped (the caller raises
+// DS4MOE_DEVERR_LENGTH).
+struct SeqInfo {
+  int tok0, n, len;  // first row of q, rows, cached positions
+};
+__device__ __forceinline__ SeqInfo seq_info(const AttnArgs &a, int b, bool &bad) {
+  SeqInfo s;
+  if (a.cu_q) {
+    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+    s.tok0 = min(max(c0, 0), a.n_tok);
+    const int e = min(max(c1, s.tok0), a.n_tok);
+    s.n = e - s.tok0;
+    bad |= s.tok0 != c0 || e != c1;
+  } else {
+    s.tok0 = b * a.n_new;
+    s.n = a.n_new;
+  }
+  const int l = a.kv_len[b];
+  s.len = min(max(l, 0), a.kv.width * a.kv.page_size);
+  bad |= s.len != l;
+  return s;
+}
+
+// First position of the window of the query at position i >= 0, and the
+// number of first positions visible before it.
+__device__ __forceinline__ int window_lo(const AttnArgs &a, int i) {
+  return a.window > 0 && i >= a.window ? i - a.window + 1 : 0;
+}
+
+// Page of a sequence's position, or -1 for a table entry outside the cache.
+__device__ __forceinline__ int page_of(const KvView &kv, int b, int pos) {
+  const int p = kv.table[(long long)b * kv.table_stride + pos / kv.page_size];
+  return p >= 0 && p < kv.n_pages ? p : -1;
+}
+
+// The 16-position groups that hold every position visible to a query at
+// positions first .. last (0 <= first <= last): the groups of the first
+// positions, then those of the windows.
+struct Groups {
+  int n_sink;  // leading groups
+  int win0;    // position group of list entry n_sink
+  int n;       // list entries
+};
+__device__ __forceinline__ Groups groups_of(const AttnArgs &a, int first, int last) {
+  Groups g;
+  const int lo = window_lo(a, first), w0 = lo >> 4, w1 = (last >> 4) + 1;
+  const int ns = (min(a.n_sink, lo) + 15) >> 4;
+  if (ns >= w0) {  // no gap
+    g.n_sink = 0, g.win0 = 0, g.n = w1;
+  } else {
+    g.n_sink = ns, g.win0 = w0, g.n = ns + w1 - w0;
+  }
+  return g;
+}
+__device__ __forceinline__ int group_pos(const Groups &g, int i) {
+  return (i < g.n_sink ? i : g.win0 + i - g.n_sink) << 4;
+}
+
+// One row (a token's head) over list entries [g0, g1) by one warp, key by
+// key, in 32 bits: nothing of a position that the row does not see enters.
+// Lane l accumulates elements 2l + 64c and 2l + 64c + 1. `m` is the running
+// maximum of scale_log2 * score and `l` the sum of the weights relative to it
+// (l = 0: no visible position).
+template <int DT, int D>
+__device__ __forceinline__ void attn_row_warp(const AttnArgs &a, const uint16_t *q, int b, int kvh, int pos,
+                                           const Groups &gr, int g0, int g1, float2 (&acc)[D / 64], float &m,
+                                           float &l, bool &bad_page) {
+  const int lane = threadIdx.x & 31;
+  float2 qf[D / 64];
+#pragma unroll
+  for (int c = 0; c < D / 64; c++) {
+    qf[c] = Half16<DT>::up(reinterpret_cast<const uint32_t *>(q)[lane + 32 * c]);
+    acc[c] = make_float2(0.0f, 0.0f);
+  }
+  m = -INFINITY, l = 0.0f;
+  if (pos < 0) return;
+  const int lo = window_lo(a, pos), sink = min(a.n_sink, lo);
+  for (int g = g0; g < g1; g++) {
+    const int p0 = group_pos(gr, g);
+    if (p0 > pos || (p0 + 15 < lo && p0 >= sink)) continue;
+    const int page = page_of(a.kv, b, p0), row0 = p0 % a.kv.page_size;
+    if (page < 0) bad_page = true;
+    const uint16_t *kp = a.kv.k + (long long)max(page, 0) * a.kv.k_page + (long long)kvh * a.kv.k_head;
+    const uint16_t *vp = a.kv.v + (long long)max(page, 0) * a.kv.v_page + (long long)kvh * a.kv.v_head;
+    for (int r = 0; r < 16; r++) {
+      const int j = p0 + r;
+      if (j > pos || (j < lo && j >= sink)) continue;
+      float s = 0.0f;
+      if (page >= 0) {
+        const uint32_t *kr = reinterpret_cast<const uint32_t *>(kp + (long long)(row0 + r) * a.kv.k_row);
+#pragma unroll
+        for (int c = 0; c < D / 64; c++) {
+          const float2 kf = Half16<DT>::up(kr[lane + 32 * c]);
+          s = fmaf(qf[c].x, kf.x, s), s = fmaf(qf[c].y, kf.y, s);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s *= a.scale_log2;
+      if (s == -INFINITY) continue;  // weight 0, also where no score is finite
+      const float mn = fmaxf(m, s), f = ex2(m - mn), p = ex2(s - mn);
+      m = mn, l = fmaf(l, f, p);
+      const uint32_t *vr = reinterpret_cast<const uint32_t *>(vp + (long long)(row0 + r) * a.kv.v_row);
+#pragma unroll
+      for (int c = 0; c < D / 64; c++) {
+        const float2 vf = page >= 0 ? Half16<DT>::up(vr[lane + 32 * c]) : make_float2(0.0f, 0.0f);
+        acc[c].x = fmaf(acc[c].x, f, p * vf.x), acc[c].y = fmaf(acc[c].y, f, p * vf.y);
+      }
+    }
+  }
+}
+
+}  // namespace ds4

@@ -1,0 +1,49 @@
+// attn.h -- the attention handle, the arguments of its kernels and the
+// launchers shared by attn.cu and the kernel translation units.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ds4moe.h"
+
+namespace ds4 {
+
+// A paged cache as the kernels see it: strides in elements.
+struct KvView {
+  const uint16_t *k, *v;
+  long long k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t *table;      // [n_seq][table_stride]
+  long long table_stride;
+  int32_t page_size, width;  // width: entries of a sequence's table row
+  int32_t n_pages;
+};
+
+// One attention call. Tokens of sequence b are rows tok0(b) .. tok0(b) +
+// n_b - 1 of q; the j-th has position len(b) - n_b + j.
+struct AttnArgs {
+  KvView kv;
+  const uint16_t *q;
+  uint16_t *out;
+  long long q_stride, out_stride;  // elements from one token's row to the next
+  const int32_t *kv_len;           // [n_seq] cached positions, the new tokens among them
+  const int32_t *cu_q;             // [n_seq + 1] first row of each sequence, or null: n_new rows each
+  int32_t n_seq, n_tok, n_new;
+  int32_t n_heads, n_kv, group;    // group = n_heads / n_kv
+  int32_t window, n_sink;
+  float scale_log2;                // score scale * log2(e)
+  uint32_t *err;
+};
+
+}  // namespace ds4
+
+struct ds4moe_attn {
+  ds4moe_attn_desc d;
+  int device, n_sm;
+  uint32_t *err;     // device error flags
+  uint64_t bytes, launches;
+};
+
+namespace ds4 {
+// attn_rows.cu: one warp per (token, head), any shape.
+cudaError_t launch_attn_rows(const AttnArgs &a, int head_dim, int dtype, cudaStream_t s);
+}  // namespace ds4

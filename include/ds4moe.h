@@ -82,6 +82,8 @@ typedef enum { DS4MOE_ROUTE_LEARNED = 0, DS4MOE_ROUTE_HASH = 1 } ds4moe_route_ki
 #define DS4MOE_DEVERR_NONFINITE 2u  /* non-finite activation quantised      */
 #define DS4MOE_DEVERR_TIMEOUT 4u    /* a bounded on-chip wait gave up       */
 #define DS4MOE_DEVERR_INTERNAL 8u   /* an internal consistency check failed */
+#define DS4MOE_DEVERR_PAGE 16u      /* block-table entry outside the cache  */
+#define DS4MOE_DEVERR_LENGTH 32u    /* length or count outside its buffers  */
 
 typedef struct {
   uint32_t abi_version; /* = DS4MOE_ABI_VERSION */
@@ -351,6 +353,150 @@ uint64_t ds4moe_dense_launch_count(const ds4moe_dense *h);
  *   falls back to the automatic ring.
  *   Errors: INVALID_ARG (NULL, a value outside its range). */
 ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst, int32_t ns, int32_t tc);
+
+/* ---------------------------------------------------------------------------
+ * Attention beside the MoE: a paged key-value cache, its append, and the
+ * attention that reads it. Forward only.
+ * Passages: "DeepSeek V4 Flash -- DFlash Integration", Model Architecture (64
+ * heads over 1 key-value head of dimension 512), the paged 128-token cache and
+ * the sliding-window ring of the same page, and its verification of drafted
+ * tokens (2 to 5 rows per sequence).
+ *
+ * Formula. The query of position i sees position j when
+ *   j <= i  and  (window == 0  or  j > i - window  or  j < n_sink),
+ * that is, the last `window` positions and the first n_sink ones. For head h
+ * (key-value head g = h / (n_heads / n_kv_heads)):
+ *   s_j = scale * <q_h, k_j,g>,  out_h = sum_j exp(s_j) v_j,g / sum_j exp(s_j)
+ * over the visible j. No visible position (i < 0), or no score above
+ * -infinity: zeros. Keys and values of positions that a row does not see never
+ * reach its output, whatever they hold (infinities and NaN among them). Scores, softmax and sums
+ * are held in 32 bits; the weights are rounded to the 16-bit type before they
+ * multiply the values, and the output once at the end.
+ *
+ * Cache: k, v are pools of n_pages pages of page_size positions each. Element
+ * (page, row, head, d) of k lies at k + page * k_page_stride + row *
+ * k_row_stride + head * k_head_stride + d (strides in elements; v likewise; k
+ * and v may be the same memory). Position pos of sequence b is in page
+ * block_table[b * table_stride + pos / page_size], row pos % page_size; table
+ * entries of pages without a visible position are not read. page_size: a
+ * multiple of 16, up to 65536. Base pointers 16-byte aligned, strides multiples
+ * of 8 elements.
+ *
+ * Data errors on the device set a flag of the handle: DS4MOE_DEVERR_PAGE (a
+ * table entry outside [0, n_pages): its keys and values are read as zeros, and
+ * an append to it is dropped), DS4MOE_DEVERR_LENGTH (kv_len outside
+ * [0, max_pages * page_size], or a cu_q that is not ascending in [0, n_tok]:
+ * clamped; a row appended at a position outside that range is dropped). */
+typedef enum { DS4MOE_DT_F32 = 0, DS4MOE_DT_BF16 = 1, DS4MOE_DT_F16 = 2 } ds4moe_dtype;
+
+#define DS4MOE_ATTN_MAX_NEW 16 /* new tokens per sequence of a decode call */
+
+typedef struct {
+  uint32_t abi_version; /* = DS4MOE_ABI_VERSION                                  */
+  int32_t n_heads;      /* query heads: a multiple of n_kv_heads, at most 128x   */
+  int32_t n_kv_heads;   /* 1..1024                                               */
+  int32_t head_dim;     /* 64, 128, 256 or 512                                   */
+  int32_t dtype;        /* DS4MOE_DT_BF16 or DS4MOE_DT_F16: q, cache and out     */
+  int32_t window;       /* last positions visible to a query; 0: all             */
+  int32_t n_sink;       /* first positions that stay visible (with a window)     */
+  float scale;          /* of the scores; > 0, usually 1 / sqrt(head_dim)        */
+  int32_t max_seqs;     /* largest n_seq of any later call, 1..65536             */
+  int32_t max_tokens;   /* largest number of rows of any later call, 1..1048576  */
+} ds4moe_attn_desc;
+
+typedef struct {
+  void *k, *v;
+  int64_t n_pages;
+  int64_t k_page_stride, k_row_stride, k_head_stride;
+  int64_t v_page_stride, v_row_stride, v_head_stride;
+  const int32_t *block_table; /* [n_seq][table_stride]                           */
+  int64_t table_stride;
+  int32_t page_size;
+  int32_t max_pages;          /* entries of a table row (<= table_stride)        */
+} ds4moe_kv_cache;
+
+typedef struct ds4moe_attn ds4moe_attn; /* opaque handle: shape and workspace */
+
+/* Validates `desc` and allocates the handle's workspace on the current device
+ * (synchronises). Errors: INVALID_ARG, UNSUPPORTED (another head_dim, more
+ * than 128 heads per key-value head), OOM, CUDA; on error *out is NULL. */
+ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out);
+/* Releases everything (synchronises the device). NULL is a no-op. */
+void ds4moe_attn_destroy(ds4moe_attn *h);
+
+/* Writes the new tokens' keys and values into the pages.
+ *   k_new, v_new [n_tok][n_kv_heads][head_dim], rows k_stride / v_stride
+ *           elements apart; src_dtype DS4MOE_DT_F32 (rounded to the cache's
+ *           type, to nearest even) or the cache's own type. v_new NULL: only k.
+ *   cu_q    [n_seq + 1] ascending: sequence b has rows cu_q[b] .. cu_q[b+1] - 1.
+ *           NULL: n_tok / n_seq rows each.
+ *   kv_len  [n_seq] positions of each sequence INCLUDING the new ones: the j-th
+ *           of n rows goes to position kv_len - n + j.
+ * Enqueued on `stream`, no allocation, no synchronisation, as the two calls
+ * below. Errors: INVALID_ARG, CUDA. */
+ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *k_new, int64_t k_stride,
+                               const void *v_new, int64_t v_stride, int32_t src_dtype, const int32_t *cu_q,
+                               const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *stream);
+
+/* Attention of n_new (1..DS4MOE_ATTN_MAX_NEW) new tokens of every sequence.
+ *   q, out  [n_seq * n_new][n_heads][head_dim], rows q_stride / out_stride
+ *           elements apart, 16-byte aligned; out must not overlap q or the
+ *           cache. Row b * n_new + j has position kv_len[b] - n_new + j.
+ *   kv_len  [n_seq] positions including the new ones (already appended). */
+ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                                 const int32_t *kv_len, int32_t n_seq, int32_t n_new, void *out, int64_t out_stride,
+                                 void *stream);
+
+/* Attention of ragged runs of new tokens: sequence b has rows cu_q[b] ..
+ * cu_q[b+1] - 1 (none is allowed), the last of them at position
+ * kv_len[b] - 1. Rows of no sequence are left as they are. */
+ds4moe_status ds4moe_attn_prefill(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                                  const int32_t *cu_q, const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *out,
+                                  int64_t out_stride, void *stream);
+
+/* As ds4moe_get_device_error, for the attention handle's flag. */
+ds4moe_status ds4moe_attn_get_device_error(ds4moe_attn *h, void *stream, uint32_t *flags_out);
+uint64_t ds4moe_attn_device_bytes(const ds4moe_attn *h);
+uint64_t ds4moe_attn_launch_count(const ds4moe_attn *h);
+
+/* ---------------------------------------------------------------------------
+ * After the output head.
+ *
+ * ds4moe_token_probs: probs[r] = softmax(logits[r] / temperature) over vocab
+ *   (fp32, rows `stride` elements apart; probs may be logits itself with the
+ *   same stride). temperature 0: 1 at the lowest index of the row's maximum, 0
+ *   elsewhere. A NaN in a row, or a maximum of +-infinity (temperature > 0),
+ *   gives NaN.
+ * ds4moe_verify_drafts: which of a sequence's drafted tokens x_0, x_1, ... stay,
+ *   and the token after them ("DeepSeek V4 Flash -- DFlash Integration", the
+ *   speculative decoding sections). With target probabilities p_i and the
+ *   drafter's q_i for draft i:
+ *     draft i is accepted when u_accept[i] * q_i(x_i) < p_i(x_i); n is the first
+ *     draft that is not (or n_draft);
+ *     the token after them is drawn from r = max(p_n - q_n, 0) (p_n where that
+ *     is 0 everywhere; p_n when all were accepted): the lowest v with
+ *     r(0) + ... + r(v) > u_sample * sum(r).
+ *   target  [n_seq][max_draft + 1] rows of vocab, target_stride apart
+ *   draft   [n_seq][max_draft] rows, draft_stride apart; NULL: a drafter that
+ *           is sure of its tokens (q_i = 1 at x_i, 0 elsewhere)
+ *   draft_tokens [n_seq][max_draft]; n_draft [n_seq] (NULL: max_draft each)
+ *   u_accept [n_seq][max_draft], u_sample [n_seq]: uniform numbers in [0, 1)
+ *   n_accepted [n_seq]: n; tokens_out [n_seq][max_draft + 1]: the accepted
+ *           drafts, the drawn token (-1 where p_n is 0 everywhere), then -1.
+ *   Probabilities are taken in [0, 1] (others are clamped, NaN is 0) and
+ *   summed exactly, in multiples of 2^(ceil(log2 vocab) - 62).
+ *   err_flags (device, may be NULL): DS4MOE_DEVERR_TOKEN_ID for a drafted token
+ *   outside [0, vocab) (rejected), DS4MOE_DEVERR_LENGTH for n_draft outside
+ *   [0, max_draft] (clamped).
+ * Both are enqueued on `stream` without allocation or synchronisation.
+ * Errors: INVALID_ARG, CUDA. */
+#define DS4MOE_MAX_DRAFT 64
+ds4moe_status ds4moe_token_probs(const float *logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,
+                                 float temperature, float *probs, int64_t probs_stride, void *stream);
+ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
+                                   const int32_t *draft_tokens, const int32_t *n_draft, const float *u_accept,
+                                   const float *u_sample, int32_t n_seq, int32_t max_draft, int32_t vocab,
+                                   int32_t *n_accepted, int32_t *tokens_out, uint32_t *err_flags, void *stream);
 
 /* Test hooks for failure detection (no counterpart in the pages; they make
  * failures happen on the host side or through a short wait bound, never by
