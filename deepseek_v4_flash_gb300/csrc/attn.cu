@@ -97,6 +97,12 @@ ds4moe_status at_status(cudaError_t e) {
   return e == cudaErrorMemoryAllocation ? DS4MOE_ERR_OOM : DS4MOE_ERR_CUDA;
 }
 
+void at_free(ds4moe_attn *h) {
+  if (h->err) cudaFree(h->err);
+  if (h->part) cudaFree(h->part);
+  if (h->ticket) cudaFree(h->ticket);
+}
+
 bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 // Strides the kernels take: multiples of 16 bytes, below 2^39 elements.
@@ -142,7 +148,11 @@ ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void
   a.window = d.window, a.n_sink = d.window ? d.n_sink : 0;
   a.scale_log2 = d.scale * 1.44269504088896340736f;  // log2(e)
   a.err = h->err;
-  const cudaError_t e = launch_attn_rows(a, d.head_dim, d.dtype, (cudaStream_t)stream);
+  // Few rows of a short head: the streaming kernel.
+  const cudaError_t e =
+      !ragged && n_new * a.group <= AD_MAX_ROWS && d.head_dim <= 128
+          ? launch_attn_decode(a, d.head_dim, d.dtype, h->part, h->ticket, h->n_sm, (cudaStream_t)stream)
+          : launch_attn_rows(a, d.head_dim, d.dtype, (cudaStream_t)stream);
   h->launches++;
   return at_status(e);
 }
@@ -173,17 +183,22 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
   h->d = d;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device);
+  const size_t pb = attn_decode_part_floats(h->n_sm) * 4, tb = (size_t)h->n_sm * 4;
+  if (e == cudaSuccess) e = attn_decode_set_attributes();
   if (e == cudaSuccess) e = cudaMalloc((void **)&h->err, 64);
+  if (e == cudaSuccess) e = cudaMalloc((void **)&h->part, pb);
+  if (e == cudaSuccess) e = cudaMalloc((void **)&h->ticket, tb);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 64, 0);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->ticket, 0, tb, 0);
   if (e == cudaSuccess) e = cudaStreamSynchronize(0);
   if (e != cudaSuccess) {
     const ds4moe_status st = at_status(e);
-    if (h->err) cudaFree(h->err);
+    at_free(h);
     cudaGetLastError();
     delete h;
     return st;
   }
-  h->bytes = 64;
+  h->bytes = 64 + pb + tb;
   *out = h;
   return DS4MOE_OK;
 }
@@ -191,7 +206,7 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
 void ds4moe_attn_destroy(ds4moe_attn *h) {
   if (!h) return;
   cudaDeviceSynchronize();
-  cudaFree(h->err);
+  at_free(h);
   delete h;
 }
 

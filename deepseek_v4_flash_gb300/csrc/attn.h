@@ -40,10 +40,19 @@ struct ds4moe_attn {
   ds4moe_attn_desc d;
   int device, n_sm;
   uint32_t *err;     // device error flags
+  float *part;       // partial results of the blocks that share a (sequence, head)
+  int *ticket;       // arrivals of those blocks, by the first of them (self-resetting)
   uint64_t bytes, launches;
 };
 
 namespace ds4 {
 // attn_rows.cu: one warp per (token, head), any shape.
 cudaError_t launch_attn_rows(const AttnArgs &a, int head_dim, int dtype, cudaStream_t s);
+// attn_decode.cu: few rows (new tokens x heads per key-value head), head
+// dimension 64 or 128.
+constexpr int AD_MAX_ROWS = 16;
+size_t attn_decode_part_floats(int n_sm);
+cudaError_t attn_decode_set_attributes();
+cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
+                               cudaStream_t s);
 }  // namespace ds4

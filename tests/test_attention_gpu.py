@@ -356,6 +356,7 @@ def test_streams_and_graphs():
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     ref = at.decode(cache, q, length)
+    torch.cuda.synchronize()  # one handle, one stream at a time
     other = at.decode(cache, q, length, stream=side)
     side.synchronize()
     torch.cuda.synchronize()
