@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <new>
 
 #include "attn.cuh"
@@ -97,12 +98,6 @@ ds4moe_status at_status(cudaError_t e) {
   return e == cudaErrorMemoryAllocation ? DS4MOE_ERR_OOM : DS4MOE_ERR_CUDA;
 }
 
-void at_free(ds4moe_attn *h) {
-  if (h->err) cudaFree(h->err);
-  if (h->part) cudaFree(h->part);
-  if (h->ticket) cudaFree(h->ticket);
-}
-
 bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 // Strides the kernels take: multiples of 16 bytes, below 2^39 elements.
@@ -148,12 +143,17 @@ ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void
   a.window = d.window, a.n_sink = d.window ? d.n_sink : 0;
   a.scale_log2 = d.scale * 1.44269504088896340736f;  // log2(e)
   a.err = h->err;
-  // Few rows of a short head: the streaming kernel.
-  const cudaError_t e =
-      !ragged && n_new * a.group <= AD_MAX_ROWS && d.head_dim <= 128
-          ? launch_attn_decode(a, d.head_dim, d.dtype, h->part, h->ticket, h->n_sm, (cudaStream_t)stream)
-          : launch_attn_rows(a, d.head_dim, d.dtype, (cudaStream_t)stream);
-  h->launches++;
+  // Few rows of a short head: the streaming kernel (a unit's 16-row product
+  // there costs what a quarter of a 128-row tile does here, and needs no
+  // tensor memory, descriptors or second launch). All else: tiles of 128 rows.
+  if (!ragged && n_new * a.group <= AD_MAX_ROWS && d.head_dim <= 128) {
+    const cudaError_t e = launch_attn_decode(a, d.head_dim, d.dtype, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
+    h->launches++;
+    return at_status(e);
+  }
+  int launches = 0;
+  const cudaError_t e = launch_attn_tile(a, d.head_dim, d.dtype, h->tile, h->n_sm, &launches, (cudaStream_t)stream);
+  h->launches += launches;
   return at_status(e);
 }
 
@@ -183,22 +183,35 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
   h->d = d;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device);
-  const size_t pb = attn_decode_part_floats(h->n_sm) * 4, tb = (size_t)h->n_sm * 4;
+  // one allocation: flags, tickets, the ragged plan, the partials
+  const size_t groups = attn_tile_groups(d.n_heads / d.n_kv_heads, d.head_dim, d.max_tokens, d.max_seqs);
+  const size_t parts = std::max(attn_decode_part_floats(h->n_sm), attn_tile_part_floats(d.head_dim, h->n_sm));
+  size_t at = 0;
+  auto place = [&](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return p;
+  };
+  const size_t o_err = place(64), o_ticket = place((size_t)h->n_sm * 4), o_split = place((size_t)h->n_sm * 32);
+  const size_t o_count = place(4), o_seq = place((size_t)d.max_seqs * 4), o_first = place((groups + 1) * 8);
+  const size_t o_info = place(groups * 8), o_part = place(parts * 4);
   if (e == cudaSuccess) e = attn_decode_set_attributes();
-  if (e == cudaSuccess) e = cudaMalloc((void **)&h->err, 64);
-  if (e == cudaSuccess) e = cudaMalloc((void **)&h->part, pb);
-  if (e == cudaSuccess) e = cudaMalloc((void **)&h->ticket, tb);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 64, 0);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->ticket, 0, tb, 0);
+  if (e == cudaSuccess) e = attn_tile_set_attributes(d.dtype, d.head_dim);
+  if (e == cudaSuccess) e = cudaMalloc((void **)&h->mem, at);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->mem, 0, o_split, 0);
   if (e == cudaSuccess) e = cudaStreamSynchronize(0);
   if (e != cudaSuccess) {
     const ds4moe_status st = at_status(e);
-    at_free(h);
+    if (h->mem) cudaFree(h->mem);
     cudaGetLastError();
     delete h;
     return st;
   }
-  h->bytes = 64 + pb + tb;
+  h->err = (uint32_t *)(h->mem + o_err), h->ticket = (int *)(h->mem + o_ticket), h->part = (float *)(h->mem + o_part);
+  h->tile.split = h->mem + o_split, h->tile.count = (int *)(h->mem + o_count);
+  h->tile.seq_first = (int *)(h->mem + o_seq), h->tile.first = (long long *)(h->mem + o_first);
+  h->tile.info = h->mem + o_info, h->tile.part = h->part;
+  h->bytes = at;
   *out = h;
   return DS4MOE_OK;
 }
@@ -206,7 +219,7 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
 void ds4moe_attn_destroy(ds4moe_attn *h) {
   if (!h) return;
   cudaDeviceSynchronize();
-  at_free(h);
+  cudaFree(h->mem);
   delete h;
 }
 

@@ -34,20 +34,29 @@ struct AttnArgs {
   uint32_t *err;
 };
 
+// Workspace of the tile kernel.
+struct TileWork {
+  long long *first;  // [row groups + 1]
+  void *info;        // int2 [row groups]
+  int *count, *seq_first;
+  float *part;
+  void *split;       // int4 [2 * n_sm]
+};
+
 }  // namespace ds4
 
 struct ds4moe_attn {
   ds4moe_attn_desc d;
   int device, n_sm;
+  uint8_t *mem;      // one allocation; the rest points into it
   uint32_t *err;     // device error flags
   float *part;       // partial results of the blocks that share a (sequence, head)
   int *ticket;       // arrivals of those blocks, by the first of them (self-resetting)
+  ds4::TileWork tile;  // the tile kernel's share (its partials are `part`)
   uint64_t bytes, launches;
 };
 
 namespace ds4 {
-// attn_rows.cu: one warp per (token, head), any shape.
-cudaError_t launch_attn_rows(const AttnArgs &a, int head_dim, int dtype, cudaStream_t s);
 // attn_decode.cu: few rows (new tokens x heads per key-value head), head
 // dimension 64 or 128.
 constexpr int AD_MAX_ROWS = 16;
@@ -55,4 +64,10 @@ size_t attn_decode_part_floats(int n_sm);
 cudaError_t attn_decode_set_attributes();
 cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
                                cudaStream_t s);
+// attn_tile.cu: tiles of 128 rows on the tensor cores, every shape.
+size_t attn_tile_part_floats(int head_dim, int n_sm);
+size_t attn_tile_groups(int group, int head_dim, int max_tokens, int max_seqs);
+cudaError_t attn_tile_set_attributes(int dtype, int head_dim);
+cudaError_t launch_attn_tile(const AttnArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
+                             cudaStream_t s);
 }  // namespace ds4

@@ -1,0 +1,1013 @@
+// attn_tile.cu -- attention of tiles of 128 rows (new tokens x heads of a
+// key-value head) on the tensor cores (tcgen05): prefill, drafted tokens of
+// many heads per key-value head, and the long head dimensions 256 and 512.
+//
+// One pass over the visible positions in tiles of up to 128:
+//   S = Q K^T           tcgen05.mma, Q and K in shared memory, S in tensor memory
+//   P = 2^(S c - m)     a warpgroup, one thread per row: no cross-lane sums
+//   O += P V            tcgen05.mma, P in tensor memory (over S), V in shared memory
+// with m the running maximum of a row. m only follows a new maximum that is
+// more than 2^AT_LAZY above it, so that O is rarely rescaled (weights up to
+// 2^AT_LAZY lose nothing: sums are kept in 32 bits and the quotient O / l does
+// not depend on m).
+//
+// Warps: 0 loads (TMA, 16-position boxes out of the pages, a ring of stages),
+// 1 issues the products, one warpgroup per row tile does the softmax and the
+// output. Two tiles of S are in flight: while one is turned into P, the next
+// one's product runs. Head dimension 64 and 128 (ragged calls): two row tiles per block share every
+// key and value tile, which halves the traffic from L2. Dimension 512: O has
+// 512 columns and S needs room too, so a block computes one half of O's
+// columns (S is then computed twice).
+//
+// Visible positions are listed in groups of 16 (the first positions' groups,
+// then the windows' groups), and a tile is eight entries of that list: a
+// window of 128 positions costs 9 or 10 groups, not 3 tiles of 128.
+//
+// The call's tiles, in order, are dealt to the blocks in equal contiguous
+// runs. A row tile whose positions lie in several runs leaves one partial
+// (O, m, l) per block; k_attn_join adds them in block order.
+#include <cuda.h>
+
+#include "attn.cuh"
+#include "internal.h"
+#include "umma.cuh"
+
+namespace ds4 {
+
+constexpr int AT_GROUPS = 8;            // 16-position groups of a key tile
+constexpr float AT_LAZY = 8.0f;
+// fp16 weights are scaled by 2^7 (at most 2^15 with the lazy maximum): small
+// weights keep 2^-31 of the largest instead of 2^-24.
+template <int DT>
+constexpr float AT_BIAS = DT == DS4MOE_DT_F16 ? 7.0f : 0.0f;
+
+constexpr int AT_CHUNK = 128 * 128;     // 128 rows of 64 elements, 128-byte swizzled
+constexpr int AT_SMEM = 225 * 1024;
+
+template <int D, int NT>
+struct TileCfg {
+  static constexpr int DV = D < 256 ? D : 256;         // columns of O a block computes
+  static constexpr int HALVES = D / DV;
+  static constexpr int SC = D == 64 ? 1 : 2;           // 64-element chunks of a ring stage
+  static constexpr int STAGE = SC * AT_CHUNK;
+  static constexpr int KST = D / 64 / SC, VST = DV / 64 / SC;  // stages of a key and a value tile
+  static constexpr int Q = NT * (D / 64) * AT_CHUNK;
+  static constexpr int NST_ = (AT_SMEM - Q) / STAGE;
+  static constexpr int NST = NST_ > 10 ? 10 : NST_;
+  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr int PITCH = DV + 4;                 // floats of a partial's row: O, m, l
+  static constexpr int O_COL = 256;                    // O's first tensor-memory column (S: 0 and 128)
+};
+
+struct TileMaps {
+  CUtensorMap q, k, v;
+};
+
+// What the blocks of a call share.
+struct TileArgs {
+  int tpt;           // tokens of a row tile: 128 / group
+  int members;       // blocks that work on the same (item, key tiles): row tiles x halves, or halves
+  int gangs;
+  long long *first;  // ragged: first tile of each row group, then the total (k_attn_plan)
+  int2 *info;        // ragged: {sequence, first token of the row group in it}
+  int *count;        // ragged: number of row groups
+  float *part;       // [2 * grid][NT][128][DV + 4]: partials
+  int4 *split;       // [2 * gangs]: what k_attn_join adds up
+};
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+// Descriptor of a 128-byte swizzled operand: 8-row atoms of 1024 bytes, `lbo`
+// the distance of 64-element columns (used by the operand whose rows run
+// along K, i.e. V).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= 1ull << 46;
+  d |= 2ull << 61;
+  return d;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major) {
+  constexpr uint32_t t = DT == DS4MOE_DT_BF16 ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+// D[tmem] (+)= A[tmem] B
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// Waits for this thread's loads; the values pass through so that no use can
+// be moved before the wait.
+__device__ __forceinline__ void tmem_wait_ld(float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A bounded wait of the whole warp: false for every lane when one gave up.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+// ---------------------------------------------------------------------------
+// The order of work.
+
+// A run of key tiles [kt0, kt1) of one item: a row group (NT row tiles of tpt
+// tokens) of one sequence and key-value head.
+struct Seg {
+  int b, kvh;
+  int row0, n;       // first row of q, tokens
+  int pos0;          // position of the first token
+  int len;           // cached positions of the sequence
+  Groups gr;
+  int kt0, kt1;      // empty: nothing is visible, the rows are 0
+  bool starts, ends;
+};
+
+__device__ __forceinline__ int tiles_of(const Groups &g) { return (g.n + AT_GROUPS - 1) / AT_GROUPS; }
+
+__device__ __forceinline__ Groups range_groups(const AttnArgs &a, int first, int last) {
+  return last >= 0 ? groups_of(a, max(first, 0), last) : Groups{0, 0, 0};
+}
+
+struct Sched {
+  long long u, u1, item0, item1;  // next tile, end of the run, the current item's tiles
+  int b, kvh, idx, n_idx;
+  long long row_units;
+  long long U, N;                 // the call's tiles, the gangs that have some
+
+  // the current item's sequence and rows; its tiles
+  __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, int nt, Seg &s) const {
+    bool bad = false;
+    const int2 in = a.cu_q ? t.info[idx] : make_int2(b, 0);
+    const SeqInfo si = seq_info(a, in.x, bad);
+    s.b = in.x, s.kvh = kvh, s.len = si.len;
+    const int span = nt * t.tpt;
+    if (a.cu_q) {
+      s.row0 = si.tok0 + in.y;
+      s.n = min(span, si.n - in.y);
+      s.pos0 = si.len - si.n + in.y;
+      s.gr = range_groups(a, s.pos0, s.pos0 + s.n - 1);
+    } else {
+      // every row tile of the sequence reads the same positions
+      s.gr = range_groups(a, si.len - si.n, si.len - 1);
+      s.row0 = si.tok0 + member_rt * t.tpt;
+      s.n = min(t.tpt, si.n - member_rt * t.tpt);
+      s.pos0 = si.len - si.n + member_rt * t.tpt;
+    }
+    return tiles_of(s.gr);
+  }
+
+  __device__ __forceinline__ int uni_units(const AttnArgs &a, int bb) const {
+    bool bad = false;
+    const SeqInfo si = seq_info(a, bb, bad);
+    return max(1, tiles_of(range_groups(a, si.len - si.n, si.len - 1)));
+  }
+
+  // Whole warp. False when gang g has no tiles.
+  __device__ bool init(const AttnArgs &a, const TileArgs &t, int g) {
+    const int lane = threadIdx.x & 31;
+    if (a.cu_q) {
+      n_idx = *t.count;
+      row_units = t.first[n_idx];
+      U = row_units * a.n_kv;
+    } else {
+      long long n = 0;
+      for (int i = lane; i < a.n_seq; i += 32) n += uni_units(a, i);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      U = n * a.n_kv;
+    }
+    N = U < t.gangs ? U : t.gangs;
+    if (g >= N) return false;
+    u = U * g / N, u1 = U * (g + 1) / N;
+    if (a.cu_q) {
+      kvh = (int)(u / row_units);
+      const long long r = u - kvh * row_units;
+      // the last row group whose first tile is at or before r
+      int lo = 0, hi = n_idx;  // first[lo] <= r < first[hi]
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = min(hi, lo + (lane + 1) * step);
+        const unsigned le = __ballot_sync(0xffffffffu, i < hi && t.first[i] <= r);
+        const int k = __popc(le);  // ascending: a prefix of the lanes
+        const int nlo = k ? lo + k * step : lo;
+        hi = min(hi, lo + (k + 1) * step), lo = nlo;
+      }
+      idx = lo;
+      item0 = kvh * row_units + t.first[idx], item1 = kvh * row_units + t.first[idx + 1];
+    } else {
+      long long r = u;
+      for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+        const long long n = b0 + lane < a.n_seq ? (long long)uni_units(a, b0 + lane) * a.n_kv : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, r < incl);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          r -= __shfl_sync(0xffffffffu, incl - n, l);
+          b = b0 + l;
+          const int units = uni_units(a, b);
+          kvh = (int)(r / units);
+          item0 = u - (r - (long long)kvh * units), item1 = item0 + units;
+          break;
+        }
+        r -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, int nt, Seg &s) {
+    if (u >= u1) return false;
+    const int n_kt = load(a, t, member_rt, nt, s);
+    const long long e = item1 < u1 ? item1 : u1;
+    s.starts = u == item0, s.ends = e == item1;
+    s.kt0 = (int)(u - item0), s.kt1 = min(n_kt, (int)(e - item0));
+    u = e;
+    if (u == item1 && u < u1) {
+      // the next item
+      item0 = item1;
+      if (a.cu_q) {
+        if (++idx == n_idx) idx = 0, kvh++;
+        item1 = kvh * row_units + t.first[idx + 1];
+      } else {
+        if (++kvh == a.n_kv) kvh = 0, b++;
+        item1 = item0 + uni_units(a, b);
+      }
+    }
+    return true;
+  }
+};
+
+// Ragged calls: row groups of `span` tokens, in sequence order, and the
+// running count of their key tiles. One block; a few microseconds for some
+// thousand groups, against the attention's tens to hundreds.
+__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, long long *first, int2 *info, int *count,
+                                                int *seq_first) {
+  __shared__ long long warp_sum[32];
+  __shared__ long long s_base;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  // exclusive prefix of v over the block, plus the running base
+  auto scan = [&](long long v) {
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[w] = x;
+    __syncthreads();
+    if (w == 0) {
+      long long y = warp_sum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      warp_sum[lane] = y;
+    }
+    __syncthreads();
+    const long long r = s_base + (w ? warp_sum[w - 1] : 0) + x - v;
+    __syncthreads();
+    if (tid == 0) s_base += warp_sum[31];
+    __syncthreads();
+    return r;
+  };
+  if (tid == 0) s_base = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int b0 = 0; b0 < a.n_seq; b0 += 1024) {
+    const int b = b0 + tid;
+    const int n = b < a.n_seq ? (seq_info(a, b, bad).n + span - 1) / span : 0;
+    const long long x = scan(n);
+    if (b < a.n_seq) seq_first[b] = (int)x;
+  }
+  if (bad) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+  const int total = (int)s_base;
+  __syncthreads();
+  if (tid == 0) s_base = 0, *count = total;
+  __syncthreads();
+  for (int i0 = 0; i0 < total; i0 += 1024) {
+    const int i = i0 + tid;
+    long long units = 0;
+    int b = 0, t0 = 0;
+    if (i < total) {
+      int lo = 0, hi = a.n_seq;  // the last sequence that starts at or before i (empty ones start with the next)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_first[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      b = lo, t0 = (i - seq_first[b]) * span;
+      bool unused = false;
+      const SeqInfo si = seq_info(a, b, unused);
+      const int p0 = si.len - si.n + t0;
+      units = max(1, tiles_of(range_groups(a, p0, p0 + min(span, si.n - t0) - 1)));
+    }
+    const long long x = scan(units);
+    if (i < total) first[i] = x, info[i] = make_int2(b, t0);
+  }
+  if (tid == 0) first[total] = s_base;
+}
+
+// ---------------------------------------------------------------------------
+
+// Bits [a, b) of a 128-bit row of flags, word w.
+__device__ __forceinline__ uint32_t range_bits(int a, int b, int w) {
+  const int lo = min(max(a - 32 * w, 0), 32), hi = min(max(b - 32 * w, 0), 32);
+  const uint32_t h = hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u, l = lo == 32 ? 0xFFFFFFFFu : (1u << lo) - 1u;
+  return h & ~l;
+}
+
+// A row whose result holds a NaN, once more from what it sees alone: a
+// position that other rows of the tile see may hold an infinity or NaN, and
+// 0 x NaN is NaN in the matrix product. Writes columns [c0, c1).
+template <int DT, int D>
+__device__ __noinline__ void redo_row_cols(const AttnArgs &a, int t, int h, int b, int pos, int c0, int c1) {
+  float2 acc[D / 64];
+  float m, l;
+  bool bad = false;
+  Groups gr = {0, 0, 0};
+  if (pos >= 0) gr = groups_of(a, pos, pos);
+  attn_row_warp<DT, D>(a, a.q + (long long)t * a.q_stride + (long long)h * D, b, h / a.group, pos, gr, 0, gr.n, acc, m,
+                       l, bad);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t *o = reinterpret_cast<uint32_t *>(a.out + (long long)t * a.out_stride + (long long)h * D);
+#pragma unroll
+  for (int c = 0; c < D / 64; c++)
+    if (c * 64 >= c0 && c * 64 < c1)
+      o[(threadIdx.x & 31) + 32 * c] = Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
+}
+
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(128 + 128 * NT, 1)
+    k_attn_tile(const __grid_constant__ TileMaps maps, const AttnArgs a, const TileArgs t) {
+  using C = TileCfg<D, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * 12 + 11];
+  __shared__ uint32_t s_tmem;
+  const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_sm = base, ring = base + C::Q;
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int i) { return bar0 + 8 * i; };
+  auto empty = [&](int i) { return bar0 + 8 * (12 + i); };
+  const uint32_t b_qf = bar0 + 8 * 24, b_qe = b_qf + 16, b_sf = b_qe + 16, b_pf = b_sf + 16, b_of = b_pf + 16,
+                 b_done = b_of + 16;
+  if (w == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < C::NST; i++) mbar_init(full(i), 1), mbar_init(empty(i), 1);
+      for (int i = 0; i < 2; i++) {
+        mbar_init(b_qf + 8 * i, 1), mbar_init(b_qe + 8 * i, 1), mbar_init(b_sf + 8 * i, 1);
+        mbar_init(b_pf + 8 * i, 128), mbar_init(b_of + 8 * i, 1);
+      }
+      mbar_init(b_done, 1);
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+  } else if (w == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members;
+  const int half = member % C::HALVES, rt = member / C::HALVES;
+  Sched sc;
+  bool ok = true;  // no wait has run out
+
+  if (w == 0) {
+    // ---- loads
+    if (!a.cu_q && blockIdx.x == 0) {
+      bool bad = false;
+      for (int i = lane; i < a.n_seq; i += 32) seq_info(a, i, bad);
+      if (bad) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+    }
+    Sched sk;
+    if (sk.init(a, t, gang)) {
+      Sched sv = sk;
+      int st = 0;          // ring stages issued so far
+      int qn = 0;          // items whose Q was issued
+      bool bad_page = false;
+      // one operand tile: groups [8 kt, 8 kt + ng) of the item, nst stages
+      auto load_tile = [&](const Seg &s, int kt, const CUtensorMap *m, int nst, int chunk0) {
+        const int ng = min(AT_GROUPS, s.gr.n - kt * AT_GROUPS);
+        const int gi = lane & 7, p0 = group_pos(s.gr, kt * AT_GROUPS + min(gi, ng - 1));
+        int page = page_of(a.kv, s.b, p0);
+        const int row = p0 % a.kv.page_size;
+        if (page < 0) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
+        for (int i = 0; i < nst && ok; i++) {
+          const int slot = st % C::NST;
+          if (st >= C::NST && !wait_warp(empty(slot), (st / C::NST - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full(slot), C::SC * ng * 2048);
+          __syncwarp();
+          if (lane < 8 * C::SC && gi < ng) {
+            const int c = lane >> 3;
+            tma_4d(ring + slot * C::STAGE + c * AT_CHUNK + gi * 2048, m, (chunk0 + i * C::SC + c) * 64, row, s.kvh, page,
+                   full(slot));
+          }
+          st++;
+        }
+      };
+      Seg ks = {}, vs = {};
+      int kk = 0, vk = 0;
+      bool kmore = false, vmore = false;
+      // the next key tile of the run, entering the next item (and loading its Q) when one is done
+      auto step_k = [&]() {
+        kk++;
+        while (!kmore || kk >= ks.kt1) {
+          kmore = sk.next(a, t, rt, NT, ks);
+          if (!kmore) return;
+          kk = ks.kt0;
+        }
+      };
+      // the current key tile, and with an item's first one its Q
+      auto load_k = [&]() {
+        if (kk == ks.kt0) {
+          for (int r = 0; r < NT && ok; r++) {
+            if (qn > 0 && !wait_warp(b_qe + 8 * r, (qn - 1) & 1)) ok = false;
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(b_qf + 8 * r, (D / 64) * t.tpt * a.group * 128);
+              // rows past the call's last come in as zeros
+              for (int c = 0; c < D / 64; c++)
+                tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, ks.kvh * a.group, ks.row0 + r * t.tpt,
+                       b_qf + 8 * r);
+            }
+          }
+          qn++;
+        }
+        if (ok) load_tile(ks, kk, &maps.k, C::KST, 0);
+      };
+      auto step_v = [&]() {
+        vk++;
+        while (!vmore || vk >= vs.kt1) {
+          vmore = sv.next(a, t, rt, NT, vs);
+          if (!vmore) return;
+          vk = vs.kt0;
+        }
+      };
+      step_k();
+      step_v();
+      if (NT == 1 && kmore) {
+        load_k();
+        step_k();
+      }
+      while (vmore && ok) {
+        // the order in which the products use them
+        if (kmore) {
+          load_k();
+          step_k();
+        }
+        if (ok) load_tile(vs, vk, &maps.v, C::VST, half * (C::DV / 64));
+        step_v();
+      }
+      if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
+      if (!ok) {
+        // the copies in flight land before the block leaves
+        for (int i = max(0, st - C::NST); i < st; i++) mbar_wait_bounded(full(i % C::NST), (i / C::NST) & 1);
+        for (int r = 0; r < NT; r++)
+          if (qn > 0) mbar_wait_bounded(b_qf + 8 * r, (qn - 1) & 1);
+      }
+    }
+  } else if (w == 1) {
+    // ---- products
+    Sched sk;
+    if (sk.init(a, t, gang)) {
+      Sched sv = sk;
+      const bool leader = lane == 0;
+      int st = 0, steps_k = 0, steps_v = 0, qn = 0;
+      const uint32_t id_o = idesc<DT>(C::SC * 64, true);
+      Seg ks = {}, vs = {};
+      int kk = 0, kr = NT - 1, vk = 0, vr = NT - 1;
+      bool kmore = false, vmore = false;
+      int kst0 = 0, vst0 = 0;  // ring stages of the current key and value tile
+      auto step_k = [&]() {
+        if (++kr < NT) return;
+        kr = 0, kk++;
+        while (!kmore || kk >= ks.kt1) {
+          kmore = sk.next(a, t, rt, NT, ks);
+          if (!kmore) return;
+          kk = ks.kt0;
+          if (ks.kt0 < ks.kt1) qn++;
+        }
+      };
+      auto step_v = [&]() {
+        if (++vr < NT) return;
+        vr = 0, vk++;
+        while (!vmore || vk >= vs.kt1) {
+          vmore = sv.next(a, t, rt, NT, vs);
+          if (!vmore) return;
+          vk = vs.kt0;
+        }
+      };
+      auto wait_stage = [&](int s) {
+        if (!wait_warp(full(s % C::NST), (s / C::NST) & 1)) ok = false;
+      };
+      auto qk = [&]() {
+        const int buf = NT == 2 ? kr : steps_k & 1;
+        const int ng = min(AT_GROUPS, ks.gr.n - kk * AT_GROUPS);
+        if (kk == ks.kt0 && !wait_warp(b_qf + 8 * kr, (qn - 1) & 1)) ok = false;
+        if (kr == 0) kst0 = st, st += C::KST;
+        const uint32_t id = idesc<DT>(16 * ng, false);
+        for (int i = 0; i < C::KST && ok; i++) {
+          const int slot = (kst0 + i) % C::NST;
+          if (kr == 0) wait_stage(kst0 + i);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int c = 0; c < C::SC; c++) {
+              const uint32_t qa = q_sm + (kr * (D / 64) + i * C::SC + c) * AT_CHUNK, kb = ring + slot * C::STAGE + c * AT_CHUNK;
+#pragma unroll
+              for (int k = 0; k < 4; k++)
+                umma_f16(tmem + buf * 128, desc_sw128(qa + 32 * k, 0), desc_sw128(kb + 32 * k, 0), id, (i | c | k) != 0);
+            }
+            if (kr == NT - 1) umma_commit(empty(slot));
+          }
+          __syncwarp();
+        }
+        if (leader && ok) {
+          umma_commit(b_sf + 8 * buf);
+          if (kk + 1 == ks.kt1) umma_commit(b_qe + 8 * kr);
+        }
+        __syncwarp();
+        steps_k++;
+      };
+      auto pv = [&]() {
+        const int buf = NT == 2 ? vr : steps_v & 1;
+        const int ng = min(AT_GROUPS, vs.gr.n - vk * AT_GROUPS);
+        const int n_buf = steps_v >> 1;  // uses of this buffer so far
+        if (vr == 0) {
+          vst0 = st, st += C::VST;
+          for (int i = 0; i < C::VST && ok; i++) wait_stage(vst0 + i);
+          // rows past the sequence's length: whatever the page holds there
+          // would meet a weight of 0; zeros instead
+          const int last = group_pos(vs.gr, vk * AT_GROUPS + ng - 1), live = vs.len - last;
+          if (ok && live < 16) {
+            const int n16 = (16 - live) * 8 * C::SC;
+            for (int i = 0; i < C::VST; i++)
+              for (int e = lane; e < n16; e += 32) {
+                const int c = e / ((16 - live) * 8), x = e % ((16 - live) * 8);
+                const uint32_t p = ring + ((vst0 + i) % C::NST) * C::STAGE + c * AT_CHUNK +
+                                   ((ng - 1) * 16 + live) * 128 + x * 16;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(p), "r"(0) : "memory");
+              }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (ok && !wait_warp(b_pf + 8 * buf, n_buf & 1)) ok = false;
+        tc_fence_after();
+        if (ok && leader) {
+#pragma unroll
+          for (int i = 0; i < C::VST; i++) {
+            const uint32_t vb = ring + ((vst0 + i) % C::NST) * C::STAGE;
+            const uint32_t o = tmem + C::O_COL + (NT == 2 ? vr * C::DV : 0) + i * C::SC * 64;
+            for (int k = 0; k < ng; k++)
+              umma_f16_ts(o, tmem + buf * 128 + 8 * k, desc_sw128(vb + 2048 * k, AT_CHUNK), id_o, vk != vs.kt0 || k != 0);
+            if (vr == NT - 1) umma_commit(empty((vst0 + i) % C::NST));
+          }
+          umma_commit(b_of + 8 * vr);
+        }
+        __syncwarp();
+        steps_v++;
+      };
+      step_k();
+      step_v();
+      if (kmore) {
+        qk();
+        step_k();
+      }
+      while (vmore && ok) {
+        if (kmore) {
+          qk();
+          step_k();
+        }
+        if (ok) {
+          pv();
+          step_v();
+        }
+      }
+      if (leader) umma_commit(b_done);
+      __syncwarp();
+      mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
+    }
+  } else if (w >= 4) {
+    // ---- softmax and output: one warpgroup per row tile, one thread per row
+    const int r = NT == 2 ? (w >> 2) - 1 : 0;
+    const int row = (w & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((w & 3) * 32) << 16;
+    const int tok = row / a.group, head = row - tok * a.group;  // within the tile and the key-value head
+    const bool in_tile = tok < t.tpt;
+    if (sc.init(a, t, gang)) {
+      Seg s;
+      int steps = 0;  // key tiles of this row tile so far
+      int4 *split = t.split + 2 * gang;
+      bool split_out = false;
+      while (ok && sc.next(a, t, rt, NT, s)) {
+        const int my_tok = r * t.tpt + tok;
+        const bool valid = in_tile && my_tok < s.n;
+        const int pos = valid ? s.pos0 + my_tok : -1;
+        const int lo = window_lo(a, max(pos, 0));
+        // what every row of this tile sees: positions up to p_first, from lo_last
+        const int p_first = s.pos0 + r * t.tpt, lo_last = window_lo(a, max(s.pos0 + s.n - 1, 0));
+        const int shift = 16 * (s.gr.win0 - s.gr.n_sink);
+        float m = -INFINITY, l = 0.0f;
+        for (int kt = s.kt0; kt < s.kt1; kt++, steps++) {
+          const int buf = NT == 2 ? r : steps & 1, use = NT == 2 ? steps : steps >> 1;
+          const int ng = min(AT_GROUPS, s.gr.n - kt * AT_GROUPS);
+          if (!wait_warp(b_sf + 8 * buf, use & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = tmem + lanes + buf * 128;
+          float v[128];
+#pragma unroll
+          for (int c = 0; c < 4; c++) tmem_ld32(sa + 32 * c, v + 32 * c);
+#pragma unroll
+          for (int c = 0; c < 4; c++) tmem_wait_ld(v + 32 * c);
+          // columns c < cs: the first positions' groups, position 128 kt + c; others shifted
+          const int cs = 16 * s.gr.n_sink - 128 * kt, off = 128 * kt + shift;
+          if (cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last)) {
+            const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              uint32_t bits = range_bits(0, e0, c) |
+                              ((range_bits(lo - off, pos + 1 - off, c) | range_bits(0, min(a.n_sink, pos + 1) - off, c)) &
+                               range_bits(cs, 128, c));
+              if (bits != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int i = 0; i < 32; i++)
+                  if (!(bits >> i & 1)) v[32 * c + i] = -INFINITY;
+              }
+            }
+          }
+          float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int i = 4; i < 128; i++) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2 - AT_BIAS<DT>;
+          const bool grow = mt > m + AT_LAZY || (m == -INFINITY && mt > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mt : m;
+            const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+            m = mn, l *= f;
+            if (kt > s.kt0) {
+              // the last product into O has to be done
+              if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
+#pragma unroll 1
+              for (int c = 0; c < C::DV; c += 16) {
+                uint32_t x[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                    "tcgen05.wait::ld.sync.aligned;"
+                    : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+                      "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+                    : "r"(oa + c)
+                    : "memory");
+#pragma unroll
+                for (int i = 0; i < 16; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                tmem_st16(oa + c, x);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float ms = m == -INFINITY ? 0.0f : m;
+          const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-ms, -ms);
+          unsigned long long sum[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              float x, y;
+              f2_unpack(f2_fma(f2_pack(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nm2), x, y);
+              x = ex2(x), y = ex2(y);
+              sum[i & 1] = f2_add(sum[i & 1], f2_pack(x, y));
+              p[i] = Half16<DT>::down(x, y);
+            }
+            tmem_st16(sa + 16 * c, p);
+          }
+          float s0, s1, s2, s3;
+          f2_unpack(sum[0], s0, s1);
+          f2_unpack(sum[1], s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(b_pf + 8 * buf);
+        }
+        if (!ok) break;
+        const bool whole = s.starts && s.ends, none = s.kt0 >= s.kt1;
+        if (!none) {
+          // one row tile: the product before the last may be unfinished too (S
+          // of a tile follows the product two tiles back), and a parity tells
+          // only two neighbouring phases apart
+          if ((NT == 1 && !wait_warp(b_of, (steps - 2) & 1)) || !wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
+        const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
+        const float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
+        const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
+        float *pp = t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH;
+        uint16_t *op = a.out + (long long)tq * a.out_stride + (long long)hq * D + half * C::DV;
+        bool nan = false;
+#pragma unroll 1
+        for (int c = 0; c < C::DV; c += 32) {
+          float x[32];
+          if (!none) {
+            tmem_ld32(oa + c, x);
+            tmem_wait_ld(x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i++) x[i] = 0.0f;
+          }
+          if (valid) {
+            if (whole) {
+#pragma unroll
+              for (int i = 0; i < 32; i++) {
+                x[i] *= inv;
+                nan |= x[i] != x[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(op + c + i) =
+                    make_uint4(Half16<DT>::down(x[i], x[i + 1]), Half16<DT>::down(x[i + 2], x[i + 3]),
+                               Half16<DT>::down(x[i + 4], x[i + 5]), Half16<DT>::down(x[i + 6], x[i + 7]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(pp + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            }
+          }
+        }
+        if (valid && !whole) pp[C::DV] = m, pp[C::DV + 1] = l;
+        tc_fence_before();
+        unsigned again = __ballot_sync(0xffffffffu, nan);
+        while (again) {
+          const int x = __ffs(again) - 1;
+          again &= again - 1;
+          redo_row_cols<DT, D>(a, __shfl_sync(0xffffffffu, tq, x), __shfl_sync(0xffffffffu, hq, x), s.b,
+                               __shfl_sync(0xffffffffu, pos, x), half * C::DV, (half + 1) * C::DV);
+        }
+        if (s.starts && !s.ends) {
+          // the first of an item's blocks says what there is to join
+          split_out = true;
+          if (member == 0 && r == 0 && row == 0) {
+            const int parts = (int)((sc.item1 * sc.N - 1) / sc.U) - gang + 1;
+            split[0] = make_int4(parts, s.b, s.kvh, s.pos0);
+            split[1] = make_int4(s.row0, a.cu_q ? s.n : a.n_new, 0, 0);
+          }
+        }
+      }
+      if (!split_out && member == 0 && r == 0 && row == 0) split[0].x = 0;
+    } else if (member == 0 && r == 0 && row == 0) {
+      t.split[2 * gang].x = 0;
+    }
+  }
+  if (!ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (w == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds up the partials of the row groups whose key tiles lie in several
+// blocks' runs, in block order. Block (gang, member, row tile, 16 rows).
+constexpr int AJ_ROWS = 16, AJ_THREADS = 128;
+
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, const TileArgs t) {
+  using C = TileCfg<D, NT>;
+  __shared__ int s_nan;
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.x % (128 / AJ_ROWS) * AJ_ROWS, r = blockIdx.x / (128 / AJ_ROWS) % NT;
+  const int bid = blockIdx.x / (128 / AJ_ROWS * NT);
+  const int gang = bid / t.members, member = bid % t.members, half = member % C::HALVES, rt = member / C::HALVES;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
+  const int parts = d0.x;
+  if (parts == 0) return;
+  if (tid == 0) s_nan = 0;
+  __syncthreads();
+  const int tok0 = (rt + r) * t.tpt;  // one of the two is 0
+  const int rows = min(t.tpt, d1.y - tok0) * a.group;
+  for (int i = tid; i < AJ_ROWS * (C::DV / 4); i += AJ_THREADS) {
+    const int row = r0 + i / (C::DV / 4), c = i % (C::DV / 4) * 4;
+    if (row >= rows) break;
+    auto at = [&](int p) {
+      const int slot = 2 * (bid + p * t.members) + (p == 0 ? 1 : 0);
+      return t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH;
+    };
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < parts; p++) m = fmaxf(m, at(p)[C::DV]);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int p = 0; p < parts; p++) {
+      const float *q = at(p);
+      const float f = q[C::DV] == -INFINITY ? 0.0f : ex2(q[C::DV] - m);
+      const float4 y = *reinterpret_cast<const float4 *>(q + c);
+      l = fmaf(f, q[C::DV + 1], l);
+      x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+    if (x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w) atomicOr(&s_nan, 1 << (row - r0));
+    const int tok = row / a.group, h = d0.z * a.group + row % a.group;
+    *reinterpret_cast<uint2 *>(a.out + (long long)(d1.x + tok0 + tok) * a.out_stride + (long long)h * D + half * C::DV + c) =
+        make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
+  }
+  __syncthreads();
+  const int again = s_nan;
+  for (int i = tid >> 5; i < AJ_ROWS; i += AJ_THREADS / 32)
+    if (again >> i & 1) {
+      const int row = r0 + i, tok = tok0 + row / a.group;
+      redo_row_cols<DT, D>(a, d1.x + tok, d0.z * a.group + row % a.group, d0.y, d0.w + tok, half * C::DV,
+                           (half + 1) * C::DV);
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+namespace {
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+  static const EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return (EncodeTiled)p;
+  }();
+  return fn;
+}
+
+// `n` dimensions, innermost first; strides in elements from the second on.
+bool make_map(CUtensorMap *m, int dtype, const void *ptr, int n, const cuuint64_t *dims, const long long *strides,
+              const cuuint32_t *box) {
+  cuuint64_t sb[4];
+  for (int i = 0; i + 1 < n; i++) sb[i] = (cuuint64_t)strides[i] * 2;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return encode_fn()(m, dtype == DS4MOE_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, n,
+                     const_cast<void *>(ptr), dims, sb, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct TileFns {
+  const void *tile, *join;
+  int nt, dv, halves, q, threads;
+};
+
+template <int DT, int D, int NT>
+TileFns fns() {
+  using C = TileCfg<D, NT>;
+  // a key tile's stages are freed one by one, a value tile's are all held at once
+  static_assert(C::NST > C::VST && (NT == 1 || C::NST > 2 * C::KST) && C::NST <= 12, "ring");
+  return {(const void *)k_attn_tile<DT, D, NT>, (const void *)k_attn_join<DT, D, NT>, NT, C::DV, C::HALVES, C::Q,
+          C::THREADS};
+}
+
+template <int DT>
+TileFns fns_of(int D, bool ragged) {
+  if (D == 64) return ragged ? fns<DT, 64, 2>() : fns<DT, 64, 1>();
+  if (D == 128) return ragged ? fns<DT, 128, 2>() : fns<DT, 128, 1>();
+  return D == 256 ? fns<DT, 256, 1>() : fns<DT, 512, 1>();
+}
+
+TileFns tile_fns(int dtype, int D, bool ragged) {
+  return dtype == DS4MOE_DT_BF16 ? fns_of<DS4MOE_DT_BF16>(D, ragged) : fns_of<DS4MOE_DT_F16>(D, ragged);
+}
+
+constexpr int AT_DYN = AT_SMEM + 1024;  // alignment of the swizzled tiles
+
+}  // namespace
+
+size_t attn_tile_part_floats(int D, int n_sm) {
+  const int dv = D < 256 ? D : 256, nt = D <= 128 ? 2 : 1;
+  return (size_t)2 * n_sm * nt * 128 * (dv + 4);
+}
+
+size_t attn_tile_groups(int group, int D, int max_tokens, int max_seqs) {
+  const int nt = D <= 128 ? 2 : 1, span = nt * (128 / group);
+  return (size_t)max_tokens / span + max_seqs + 1;
+}
+
+cudaError_t attn_tile_set_attributes(int dtype, int D) {
+  if (!encode_fn()) return cudaErrorNotSupported;
+  for (bool ragged : {false, true}) {
+    const cudaError_t e = cudaFuncSetAttribute(tile_fns(dtype, D, ragged).tile, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_DYN);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork &w, int n_sm, int *launches,
+                             cudaStream_t s) {
+  const bool ragged = a.cu_q != nullptr;
+  const TileFns f = tile_fns(dtype, D, ragged);
+  TileArgs t = {};
+  t.tpt = 128 / a.group;
+  const int row_tiles = ragged ? 1 : (a.n_new + t.tpt - 1) / t.tpt;
+  t.members = row_tiles * f.halves;
+  t.gangs = n_sm / t.members;
+  t.first = w.first, t.info = (int2 *)w.info, t.count = w.count, t.part = w.part, t.split = (int4 *)w.split;
+  TileMaps maps;
+  const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_tok};
+  const long long qs[2] = {D, a.q_stride};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)a.group, (cuuint32_t)t.tpt};
+  const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.n_kv, (cuuint64_t)a.kv.n_pages};
+  const long long ks[3] = {a.kv.k_row, a.kv.k_head, a.kv.k_page}, vs[3] = {a.kv.v_row, a.kv.v_head, a.kv.v_page};
+  const cuuint32_t kb[4] = {64, 16, 1, 1};
+  if (!make_map(&maps.q, dtype, a.q, 3, qd, qs, qb) || !make_map(&maps.k, dtype, a.kv.k, 4, kd, ks, kb) ||
+      !make_map(&maps.v, dtype, a.kv.v, 4, kd, vs, kb))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  if (ragged) {
+    int span = f.nt * t.tpt;
+    void *args[] = {(void *)&a, &span, &t.first, &t.info, &t.count, (void *)&w.seq_first};
+    e = launch_pdl((const void *)k_attn_plan, dim3(1), dim3(1024), 0, s, args, true);
+    ++*launches;
+  }
+  if (e == cudaSuccess) {
+    void *args[] = {&maps, (void *)&a, &t};
+    e = launch_pdl(f.tile, dim3(t.gangs * t.members), dim3(f.threads), AT_DYN, s, args, true);
+    ++*launches;
+  }
+  if (e == cudaSuccess) {
+    void *args[] = {(void *)&a, &t};
+    e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / AJ_ROWS)), dim3(AJ_THREADS), 0, s, args, true);
+    ++*launches;
+  }
+  return e;
+}
+
+}  // namespace ds4
