@@ -142,9 +142,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        from torch import _C
+        # torch.cuda.current_stream() without building a Stream object (a
+        # quarter of a small call's host time)
+        return ctypes.c_void_p(_C._cuda_getCurrentRawStream(_C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -339,21 +341,29 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _rows(t, name, dtype, shape):
+def _rows(t, name, dtype, shape, inner=None):
     """Elements from one row of `t` to the next: `shape` after the leading
-    dimensions, contiguous, the leading dimensions evenly spaced."""
+    dimensions, contiguous, the leading dimensions evenly spaced. `inner`: the
+    elements of a row, where the caller has them."""
     import torch
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype, f"{name}: a CUDA tensor of {dtype}")
-    lead = t.dim() - len(shape)
-    _need(lead >= 1 and tuple(t.shape[lead:]) == tuple(shape), f"{name}: shape [..., {', '.join(map(str, shape))}]")
-    inner = 1
-    for n, s in zip(reversed(shape), reversed(t.stride()[lead:])):
-        _need(n == 1 or s == inner, f"{name}: a row must be contiguous")
-        inner *= n
-    if t.numel() == 0:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype):
+        raise ValueError(f"{name}: a CUDA tensor of {dtype}")
+    size = t.shape
+    lead = len(size) - len(shape)
+    if lead < 1 or size[lead:] != shape:
+        raise ValueError(f"{name}: shape [..., {', '.join(map(str, shape))}]")
+    if inner is None:
+        inner = 1
+        for n in shape:
+            inner *= n
+    if t.is_contiguous():
         return inner
+    step = 1
+    for n, s in zip(reversed(shape), reversed(t.stride()[lead:])):
+        _need(n == 1 or s == step, f"{name}: a row must be contiguous")
+        step *= n
     row, step = None, None  # the stride of a row; the stride the next leading dimension must have
-    for n, s in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
+    for n, s in zip(reversed(size[:lead]), reversed(t.stride()[:lead])):
         if n == 1:
             continue
         if row is None:
@@ -366,9 +376,9 @@ def _rows(t, name, dtype, shape):
 
 def _vec(t, name, dtype, n):
     import torch
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous(),
-          f"{name}: a contiguous CUDA tensor of {n} {dtype}")
-    return _ptr(t)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {n} {dtype}")
+    return t.data_ptr()
 
 
 def _fresh(out, stream):
@@ -421,8 +431,10 @@ class KVCache:
               "block_table: a CUDA int32 tensor [n_seq, max_pages] with contiguous rows")
         self.k, self.v, self.block_table = k, v, block_table
         stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+        self.row, self.dtype, self.n_seq = tuple(k.shape[2:]), k.dtype, block_table.shape[0]
         self.c = _KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.stride(2), v.stride(0),
                           v.stride(1), v.stride(2), block_table.data_ptr(), stride, k.shape[1], block_table.shape[1])
+        self.ref = ctypes.byref(self.c)
 
 
 class Attention:
@@ -432,6 +444,9 @@ class Attention:
         h = ctypes.c_void_p()
         _check(lib().ds4moe_attn_create(ctypes.byref(desc.c()), ctypes.byref(h)), "ds4moe_attn_create")
         self.desc, self._h = desc, h
+        self._dt, self._code = _torch_dtype(DTYPE[desc.dtype]), DTYPE[desc.dtype]
+        self._q_row, self._q_len = (desc.n_heads, desc.head_dim), desc.n_heads * desc.head_dim
+        self._kv_row, self._kv_len = (desc.n_kv_heads, desc.head_dim), desc.n_kv_heads * desc.head_dim
 
     def close(self):
         if getattr(self, "_h", None):
@@ -445,69 +460,70 @@ class Attention:
             pass
 
     def _cache(self, cache, n_seq):
-        d = self.desc
-        _need(isinstance(cache, KVCache), "cache: a KVCache")
-        _need(tuple(cache.k.shape[2:]) == (d.n_kv_heads, d.head_dim) and
-              cache.k.dtype == _torch_dtype(DTYPE[d.dtype]), "cache: heads, dimension or type differ from the handle's")
-        _need(cache.block_table.shape[0] >= n_seq, "cache: a block-table row for every sequence")
-        return ctypes.byref(cache.c)
+        if not isinstance(cache, KVCache):
+            raise ValueError("cache: a KVCache")
+        if cache.row != self._kv_row or cache.dtype != self._dt:
+            raise ValueError("cache: heads, dimension or type differ from the handle's")
+        if cache.n_seq < n_seq:
+            raise ValueError("cache: a block-table row for every sequence")
+        return cache.ref
 
     def append(self, cache, k, v, kv_len, cu_q=None, stream=None):
         """Write new keys and values (ds4moe_kv_append): k, v [n_tok, n_kv_heads,
         head_dim] or [n_seq, n_new, ...], fp32 or the cache's type; v may be None
         (the keys only). kv_len int32 [n_seq] counts the new tokens."""
         import torch
-        d, n_seq = self.desc, kv_len.numel()
-        row = (d.n_kv_heads, d.head_dim)
-        dt = torch.float32 if k.dtype == torch.float32 else _torch_dtype(DTYPE[d.dtype])
-        ks = _rows(k, "k", dt, row)
-        n_tok = k.numel() // (row[0] * row[1])
+        n_seq = kv_len.numel()
+        dt = torch.float32 if k.dtype == torch.float32 else self._dt
+        ks = _rows(k, "k", dt, self._kv_row, self._kv_len)
         vs = 0
         if v is not None:
-            _need(v.shape == k.shape, "v: the shape of k")
-            vs = _rows(v, "v", dt, row)
-        _check(lib().ds4moe_kv_append(
-            self._h, self._cache(cache, n_seq), _ptr(k), ks, _ptr(v), vs,
-            DT_F32 if dt == torch.float32 else DTYPE[d.dtype],
+            vs = _rows(v, "v", dt, self._kv_row, self._kv_len)
+            if v.shape != k.shape:
+                raise ValueError("v: the shape of k")
+        _check(_lib.ds4moe_kv_append(
+            self._h, self._cache(cache, n_seq), k.data_ptr(), ks, None if v is None else v.data_ptr(), vs,
+            DT_F32 if dt == torch.float32 else self._code,
             None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, n_seq + 1),
-            _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_tok, _stream(stream)), "ds4moe_kv_append")
+            _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, k.numel() // self._kv_len, _stream(stream)),
+            "ds4moe_kv_append")
 
     def _out(self, q, out, stream):
+        """The output and its row stride."""
         import torch
         if out is None:
-            out = _fresh(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
-        _need(out.shape == q.shape, "out: the shape of q")
-        return out
+            return _fresh(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream), self._q_len
+        if out.shape != q.shape:
+            raise ValueError("out: the shape of q")
+        return out, _rows(out, "out", self._dt, self._q_row, self._q_len)
 
     def decode(self, cache, q, kv_len, out=None, stream=None):
         """Attention of the last n_new tokens of every sequence
         (ds4moe_attn_decode): q [n_seq, n_new, n_heads, head_dim]; returns out."""
         import torch
-        d, dt = self.desc, _torch_dtype(DTYPE[self.desc.dtype])
-        _need(q.dim() == 4, "q: [n_seq, n_new, n_heads, head_dim]")
+        if q.dim() != 4:
+            raise ValueError("q: [n_seq, n_new, n_heads, head_dim]")
         n_seq, n_new = q.shape[:2]
-        qs = _rows(q, "q", dt, (d.n_heads, d.head_dim))
-        out = self._out(q, out, stream)
-        os_ = _rows(out, "out", dt, (d.n_heads, d.head_dim))
-        _check(lib().ds4moe_attn_decode(self._h, self._cache(cache, n_seq), _ptr(q), qs,
-                                        _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_new, _ptr(out), os_,
-                                        _stream(stream)), "ds4moe_attn_decode")
+        qs = _rows(q, "q", self._dt, self._q_row, self._q_len)
+        out, os_ = self._out(q, out, stream)
+        _check(_lib.ds4moe_attn_decode(self._h, self._cache(cache, n_seq), q.data_ptr(), qs,
+                                       _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_new, out.data_ptr(), os_,
+                                       _stream(stream)), "ds4moe_attn_decode")
         return out
 
     def prefill(self, cache, q, cu_q, kv_len, out=None, stream=None):
         """Attention of ragged runs of new tokens (ds4moe_attn_prefill): q
         [n_tok, n_heads, head_dim], cu_q int32 [n_seq + 1]; returns out."""
         import torch
-        d, dt = self.desc, _torch_dtype(DTYPE[self.desc.dtype])
-        _need(q.dim() == 3, "q: [n_tok, n_heads, head_dim]")
+        if q.dim() != 3:
+            raise ValueError("q: [n_tok, n_heads, head_dim]")
         n_seq = kv_len.numel()
-        qs = _rows(q, "q", dt, (d.n_heads, d.head_dim))
-        out = self._out(q, out, stream)
-        os_ = _rows(out, "out", dt, (d.n_heads, d.head_dim))
-        _check(lib().ds4moe_attn_prefill(self._h, self._cache(cache, n_seq), _ptr(q), qs,
-                                         _vec(cu_q, "cu_q", torch.int32, n_seq + 1),
-                                         _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, q.shape[0], _ptr(out), os_,
-                                         _stream(stream)), "ds4moe_attn_prefill")
+        qs = _rows(q, "q", self._dt, self._q_row, self._q_len)
+        out, os_ = self._out(q, out, stream)
+        _check(_lib.ds4moe_attn_prefill(self._h, self._cache(cache, n_seq), q.data_ptr(), qs,
+                                        _vec(cu_q, "cu_q", torch.int32, n_seq + 1),
+                                        _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, q.shape[0], out.data_ptr(),
+                                        os_, _stream(stream)), "ds4moe_attn_prefill")
         return out
 
     def device_error(self, stream=None) -> int:
@@ -533,14 +549,13 @@ def token_probs(logits, temperature: float = 1.0, out=None, stream=None):
     V = logits.shape[-1]
     if out is None:
         out = _fresh(torch.empty(logits.shape, dtype=torch.float32, device=logits.device), stream)
-    _need(out.shape == logits.shape, "out: the shape of logits")
-    if logits.dim() == 1:
-        logits_, out_ = logits[None], out[None]
-    else:
-        logits_, out_ = logits, out
-    xs, os_ = _rows(logits_, "logits", torch.float32, (V,)), _rows(out_, "out", torch.float32, (V,))
-    _check(lib().ds4moe_token_probs(_ptr(logits), xs, logits.numel() // max(V, 1), V, temperature, _ptr(out), os_,
-                                    _stream(stream)), "ds4moe_token_probs")
+    elif out.shape != logits.shape:
+        raise ValueError("out: the shape of logits")
+    one = logits.dim() == 1
+    xs = _rows(logits[None] if one else logits, "logits", torch.float32, (V,), V)
+    os_ = _rows(out[None] if one else out, "out", torch.float32, (V,), V)
+    _check(lib().ds4moe_token_probs(logits.data_ptr(), xs, logits.numel() // max(V, 1), V, temperature, out.data_ptr(),
+                                    os_, _stream(stream)), "ds4moe_token_probs")
     return out
 
 
@@ -551,23 +566,26 @@ def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_acc
     fp32 [n_seq, max_draft, vocab] or None, tokens int32 [n_seq, max_draft].
     Returns (n_accepted int32 [n_seq], tokens_out int32 [n_seq, max_draft + 1])."""
     import torch
-    _need(target.dim() == 3, "target: [n_seq, max_draft + 1, vocab]")
-    B, G, V = target.shape[0], target.shape[1] - 1, target.shape[2]
-    ts, ds = _rows(target, "target", torch.float32, (V,)), 0
+    i32, f32 = torch.int32, torch.float32
+    if target.dim() != 3:
+        raise ValueError("target: [n_seq, max_draft + 1, vocab]")
+    B, G, V = target.shape
+    G -= 1
+    ts, ds = _rows(target, "target", f32, (V,), V), 0
     if draft is not None:
-        _need(tuple(draft.shape) == (B, G, V), "draft: [n_seq, max_draft, vocab]")
-        ds = _rows(draft, "draft", torch.float32, (V,))
+        if tuple(draft.shape) != (B, G, V):
+            raise ValueError("draft: [n_seq, max_draft, vocab]")
+        ds = _rows(draft, "draft", f32, (V,), V)
     if n_accepted is None:
-        n_accepted = _fresh(torch.empty(B, dtype=torch.int32, device=target.device), stream)
+        n_accepted = _fresh(torch.empty(B, dtype=i32, device=target.device), stream)
     if tokens_out is None:
-        tokens_out = _fresh(torch.empty((B, G + 1), dtype=torch.int32, device=target.device), stream)
+        tokens_out = _fresh(torch.empty((B, G + 1), dtype=i32, device=target.device), stream)
     _check(lib().ds4moe_verify_drafts(
-        _ptr(target), ts, _ptr(draft), ds, _vec(tokens, "tokens", torch.int32, B * G),
-        None if n_draft is None else _vec(n_draft, "n_draft", torch.int32, B),
-        _vec(u_accept, "u_accept", torch.float32, B * G), _vec(u_sample, "u_sample", torch.float32, B), B, G, V,
-        _vec(n_accepted, "n_accepted", torch.int32, B), _vec(tokens_out, "tokens_out", torch.int32, B * (G + 1)),
-        None if err_flags is None else _vec(err_flags, "err_flags", torch.int32, 1), _stream(stream)),
-        "ds4moe_verify_drafts")
+        target.data_ptr(), ts, None if draft is None else draft.data_ptr(), ds, _vec(tokens, "tokens", i32, B * G),
+        None if n_draft is None else _vec(n_draft, "n_draft", i32, B), _vec(u_accept, "u_accept", f32, B * G),
+        _vec(u_sample, "u_sample", f32, B), B, G, V, _vec(n_accepted, "n_accepted", i32, B),
+        _vec(tokens_out, "tokens_out", i32, B * (G + 1)),
+        None if err_flags is None else _vec(err_flags, "err_flags", i32, 1), _stream(stream)), "ds4moe_verify_drafts")
     return n_accepted, tokens_out
 
 

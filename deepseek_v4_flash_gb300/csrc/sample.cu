@@ -11,6 +11,38 @@ namespace ds4 {
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
 
+// Both kernels give a row to a cluster of 1, 2, 4 or 8 blocks: enough blocks
+// that a block's part is about 4096 entries, so that a single row is read by
+// eight SMs (a call for one sequence is all latency) and a whole batch keeps
+// every SM's loads in flight. Parts are multiples of 4 entries.
+constexpr int SP_PART = 4096;
+int cluster_of(int V) {
+  int c = 1;
+  while (c < 8 && (long long)c * SP_PART < V) c *= 2;
+  return c;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of another block's shared memory.
+__device__ __forceinline__ uint32_t ld_peer(const void *p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
 // (value, index) of the larger value, the lower index among equals.
 __device__ __forceinline__ void arg_max(float &v, int &i, float w, int j) {
   if (w > v || (w == v && j < i)) v = w, i = j;
@@ -23,55 +55,160 @@ __device__ __forceinline__ float over_t(float d, float t, float inv_t) {
   return isfinite(z) ? fmaf(fmaf(-z, t, d), inv_t, z) : z;
 }
 
-// Softmax of one row per block: the maximum, the sum of exp((x - max) / T),
-// then the quotients. T = 0: 1 at the lowest index of the maximum, 0
-// elsewhere. A row whose maximum is not finite, or that holds a NaN, gives
-// what the formula gives (NaN).
-__global__ void __launch_bounds__(SP_THREADS) k_token_probs(const float *x, long long xs, int V, float t, float inv_t, float *out,
-                                                        long long os) {
-  __shared__ float sv[SP_WARPS], ss[SP_WARPS];
-  __shared__ int si[SP_WARPS];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
-  pdl_wait();
-  const float *r = x + (long long)blockIdx.x * xs;
-  float *o = out + (long long)blockIdx.x * os;
-  float m = -INFINITY;
-  int at = V;
-  bool nan = false;
-  for (int i = tid; i < V; i += SP_THREADS) {
-    const float v = r[i];
-    nan |= v != v;
-    arg_max(m, at, v, i);
-  }
-#pragma unroll
-  for (int s = 16; s; s >>= 1)
-    arg_max(m, at, __shfl_xor_sync(0xffffffffu, m, s), __shfl_xor_sync(0xffffffffu, at, s));
-  if (lane == 0) sv[w] = m, si[w] = at;
-  nan = __syncthreads_or(nan);
-  for (int i = 0; i < SP_WARPS; i++) arg_max(m, at, sv[i], si[i]);
-  if (nan) m = NAN;
-  if (inv_t == 0.0f) {
-    for (int i = tid; i < V; i += SP_THREADS) o[i] = nan ? NAN : i == at ? 1.0f : 0.0f;
+// Entries i .. i + 3 of a row (those below end; `fill` elsewhere).
+template <bool VEC>
+__device__ __forceinline__ float4 row4(const float *r, int i, int end, float fill) {
+  if (VEC && i + 3 < end) return *reinterpret_cast<const float4 *>(r + i);
+  return make_float4(i < end ? r[i] : fill, i + 1 < end ? r[i + 1] : fill, i + 2 < end ? r[i + 2] : fill,
+                     i + 3 < end ? r[i + 3] : fill);
+}
+template <bool VEC>
+__device__ __forceinline__ void put4(float *o, int i, int end, float4 v) {
+  if (VEC && i + 3 < end) {
+    *reinterpret_cast<float4 *>(o + i) = v;
     return;
   }
-  float sum = 0.0f;
-  for (int i = tid; i < V; i += SP_THREADS) sum += expf(over_t(r[i] - m, t, inv_t));
+  if (i < end) o[i] = v.x;
+  if (i + 1 < end) o[i + 1] = v.y;
+  if (i + 2 < end) o[i + 2] = v.z;
+  if (i + 3 < end) o[i + 3] = v.w;
+}
+
+// Softmax of one row per cluster, bound by the row's bytes (read once, written
+// once): a block keeps up to SP_KEEP x 2048 entries of its part in registers
+// (the rest of a longer part is read again, from L2), takes the exponentials
+// relative to its own maximum, and one exchange of (maximum, sum) between the
+// blocks gives the factor that turns them into probabilities.
+// T = 0: 1 at the lowest index of the maximum, 0 elsewhere.
+constexpr int SP_KEEP = 8;
+template <bool VEC>
+__global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, long long xs, int V, float t, float inv_t,
+                                                           float *out, long long os) {
+  __shared__ float sv[SP_WARPS], ss[SP_WARPS];
+  __shared__ int si[SP_WARPS];
+  __shared__ float pub[3];  // this block's maximum, sum, index of the maximum
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int rank = cluster_rank(), n_blk = cluster_size();
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long row = blockIdx.x / n_blk;
+  const float *r = x + row * xs;
+  float *o = out + row * os;
+  const int part = ((V + n_blk - 1) / n_blk + 3) & ~3;
+  const int begin = min(V, rank * part), end = min(V, begin + part);
+  float4 v[SP_KEEP];
 #pragma unroll
-  for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  for (int k = 0; k < SP_KEEP; k++) v[k] = row4<VEC>(r, begin + 4 * (tid + k * SP_THREADS), end, -INFINITY);
+  const int rest = begin + 4 * (tid + SP_KEEP * SP_THREADS);
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < SP_KEEP; k++) m = fmaxf(fmaxf(fmaxf(m, v[k].x), fmaxf(v[k].y, v[k].z)), v[k].w);
+  for (int i = rest; i < end; i += 4 * SP_THREADS) {
+    const float4 y = row4<VEC>(r, i, end, -INFINITY);
+    m = fmaxf(fmaxf(fmaxf(m, y.x), fmaxf(y.y, y.z)), y.w);
+  }
+  m = warp_max(m);
+  if (lane == 0) sv[w] = m;
+  __syncthreads();
+  m = warp_max(sv[lane & (SP_WARPS - 1)]);
+  if (inv_t == 0.0f) {
+    // the lowest index that holds the maximum, and whether there is a NaN
+    int at = V;
+    bool nan = false;
+    auto look = [&](float a, int i) {
+      nan |= a != a;
+      if (a == m && i < end) at = min(at, i);
+    };
+#pragma unroll
+    for (int k = 0; k < SP_KEEP; k++) {
+      const int i = begin + 4 * (tid + k * SP_THREADS);
+      look(v[k].x, i), look(v[k].y, i + 1), look(v[k].z, i + 2), look(v[k].w, i + 3);
+    }
+    for (int i = rest; i < end; i += 4 * SP_THREADS) {
+      const float4 y = row4<VEC>(r, i, end, -INFINITY);
+      look(y.x, i), look(y.y, i + 1), look(y.z, i + 2), look(y.w, i + 3);
+    }
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0) si[w] = at;
+    nan = __syncthreads_or(nan);
+    if (tid == 0) {
+      for (int i = 0; i < SP_WARPS; i++) at = min(at, si[i]);
+      pub[0] = nan ? NAN : m, pub[2] = __int_as_float(at);
+    }
+    cluster_sync();
+    float best = -INFINITY;
+    int where = V;
+    for (int b = 0; b < n_blk; b++) {
+      const float pm = __uint_as_float(ld_peer(&pub[0], b));
+      if (pm != pm) best = NAN;
+      else arg_max(best, where, pm, (int)ld_peer(&pub[2], b));
+    }
+    cluster_sync();  // a block's shared memory outlives its readers
+    const bool bad = best != best;
+    for (int i = begin + 4 * tid; i < end; i += 4 * SP_THREADS) {
+      const float one[2] = {bad ? NAN : 0.0f, bad ? NAN : 1.0f};
+      put4<VEC>(o, i, end, make_float4(one[i == where], one[i + 1 == where], one[i + 2 == where], one[i + 3 == where]));
+    }
+    return;
+  }
+  // a part of nothing but -infinity weighs nothing
+  const bool empty = m == -INFINITY;
+  auto e = [&](float a) { return empty ? (a == a ? 0.0f : a) : expf(over_t(a - m, t, inv_t)); };
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < SP_KEEP; k++) {
+    v[k] = make_float4(e(v[k].x), e(v[k].y), e(v[k].z), e(v[k].w));
+    sum += (v[k].x + v[k].y) + (v[k].z + v[k].w);
+  }
+  for (int i = rest; i < end; i += 4 * SP_THREADS) {
+    const float4 y = row4<VEC>(r, i, end, -INFINITY);
+    sum += (e(y.x) + e(y.y)) + (e(y.z) + e(y.w));
+  }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
   if (lane == 0) ss[w] = sum;
   __syncthreads();
-  sum = 0.0f;
-  for (int i = 0; i < SP_WARPS; i++) sum += ss[i];
-  const float inv = 1.0f / sum;
-  for (int i = tid; i < V; i += SP_THREADS) o[i] = expf(over_t(r[i] - m, t, inv_t)) * inv;
+  if (w == 0) {
+    sum = lane < SP_WARPS ? ss[lane] : 0.0f;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (lane == 0) pub[0] = m, pub[1] = sum;
+  }
+  float top = -INFINITY, total = 0.0f;
+  cluster_sync();
+  float pm[8], ps[8];
+#pragma unroll
+  for (int b = 0; b < 8; b++)
+    if (b < n_blk) pm[b] = __uint_as_float(ld_peer(&pub[0], b)), ps[b] = __uint_as_float(ld_peer(&pub[1], b));
+    else pm[b] = -INFINITY, ps[b] = 0.0f;
+#pragma unroll
+  for (int b = 0; b < 8; b++) top = fmaxf(top, pm[b]);
+#pragma unroll
+  for (int b = 0; b < 8; b++) total += pm[b] == -INFINITY ? ps[b] : ps[b] * expf(over_t(pm[b] - top, t, inv_t));
+  // barrier.cluster: a block's shared memory outlives its readers
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const float f = (empty ? 0.0f : expf(over_t(m - top, t, inv_t))) / total;
+#pragma unroll
+  for (int k = 0; k < SP_KEEP; k++) {
+    const int i = begin + 4 * (tid + k * SP_THREADS);
+    put4<VEC>(o, i, end, make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f));
+  }
+  for (int i = rest; i < end; i += 4 * SP_THREADS) {
+    const float4 y = row4<VEC>(r, i, end, -INFINITY);
+    put4<VEC>(o, i, end, make_float4(e(y.x) * f, e(y.y) * f, e(y.z) * f, e(y.w) * f));
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
 // Verification. Sums of probabilities decide a whole number, so they are
-// exact: a probability is rounded to a multiple of 2^-shift (shift = 62 -
-// ceil(log2 V), 45 for a vocabulary of 129280) and summed in 64-bit integers,
-// whose sum does not depend on the order and cannot overflow.
+// exact: a probability is rounded to a multiple of 2^-shift, shift = 45 (less
+// for a vocabulary above 2^17, so that sums stay below 2^62), and summed in
+// integers, whose sum does not depend on the order. A fixed-point value is
+// hi 2^(shift - 22) + lo with hi = rint(p 2^22) and lo the rounded remainder;
+// both come from adding 1.5 2^23 to a float, so that an entry costs 5 float
+// operations and two 32-bit additions where a 64-bit shift would take three
+// times as many.
 
 struct VerifyArgs {
   const float *target, *draft;       // [n_seq][G + 1][V], [n_seq][G][V] or null
@@ -83,17 +220,25 @@ struct VerifyArgs {
   uint32_t *err;
 };
 
-// A probability in units of 2^-shift, clamped to [0, 1]; NaN counts as 0.
-__device__ __forceinline__ long long fixed_prob(float p, int shift) {
-  if (!(p > 0.0f)) return 0;
-  p = fminf(p, 1.0f);
-  const int b = __float_as_int(p), e = b >> 23;
-  if (e == 0) return 0;  // below 2^-126
-  const unsigned long long mant = (b & 0x7FFFFF) | 0x800000;
-  const int s = e - 150 + shift;  // value = mant * 2^s units
-  if (s >= 0) return (long long)(mant << s);
-  if (s < -24) return 0;
-  return (long long)((mant + (1ull << (-s - 1))) >> -s);
+constexpr float SP_MAGIC = 12582912.0f;  // 1.5 2^23: x + SP_MAGIC holds rint(x) in its low bits
+
+// hi and lo of p, each plus the bits of SP_MAGIC. NaN and negative p: 0;
+// above 1: 1. lo_scale = 2^(shift - 22).
+__device__ __forceinline__ void split_prob(float p, float lo_scale, int &hi, int &lo) {
+  const float t = __saturatef(p) * 4194304.0f;
+  const float h = __fadd_rn(t, SP_MAGIC);
+  const float l = __fadd_rn(t, -__fadd_rn(h, -SP_MAGIC));  // exact
+  hi = __float_as_int(h), lo = __float_as_int(__fmaf_rn(l, lo_scale, SP_MAGIC));
+}
+
+// What the last token is drawn from at one entry: p less q (dropped below 0:
+// the rounding is monotonic, so p > q decides) as (hi, lo).
+__device__ __forceinline__ void mass_of(float p, float q, float lo_scale, int &hi, int &lo) {
+  int ph, pl, qh, ql;
+  split_prob(p, lo_scale, ph, pl);
+  split_prob(q, lo_scale, qh, ql);
+  const bool more = __saturatef(p) > __saturatef(q);
+  hi = more ? ph - qh : 0, lo = more ? pl - ql : 0;
 }
 
 // u in [0, 1) in units of 2^-64 (bits below are dropped: they lie under one
@@ -106,31 +251,30 @@ __device__ __forceinline__ unsigned long long fixed_u(float u) {
   return s >= 0 ? mant << s : s > -24 ? mant >> -s : 0;
 }
 
-// What the last token is drawn from: row p less row q (dropped below 0).
-// dtok >= 0: q is 1 at dtok and 0 elsewhere.
-__device__ __forceinline__ long long mass_at(const float *p, const float *q, int dtok, int i, int shift) {
-  long long r = fixed_prob(p[i], shift);
-  if (q) r = max(0ll, r - fixed_prob(q[i], shift));
-  if (i == dtok) r = 0;
-  return r;
-}
-
 __device__ __forceinline__ long long warp_sum64(long long v) {
 #pragma unroll
   for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
 
+// One sequence per cluster. Every block finds the first draft that is not
+// accepted, then sums its part of the one row (of p, and of q) that the token
+// is drawn from; the sums meet in shared memory of the cluster, and the warp
+// whose run of entries holds the border scans that run again.
+template <bool VEC>
 __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a) {
   __shared__ long long part[SP_WARPS];
+  __shared__ __align__(8) int pub[2];  // this block's sum, low and high word
   __shared__ int s_n;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, b = blockIdx.x;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int rank = cluster_rank(), n_blk = cluster_size(), b = blockIdx.x / n_blk;
   pdl_launch_dependents();
   pdl_wait();
   int cnt = a.G;
   if (a.n_draft) {
-    cnt = min(max(a.n_draft[b], 0), a.G);
-    if (cnt != a.n_draft[b] && tid == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+    const int given = a.n_draft[b];
+    cnt = min(max(given, 0), a.G);
+    if (cnt != given && tid == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
   }
   if (w == 0) {
     // draft i is accepted when u * q < p: the product of two 24-bit
@@ -156,31 +300,65 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
   const float *p = a.target + ((long long)b * (a.G + 1) + n) * a.t_pitch;
   const float *q = n < cnt && a.draft ? a.draft + ((long long)b * a.G + n) * a.d_pitch : nullptr;
   int dtok = n < cnt && !a.draft ? a.tok[(long long)b * a.G + n] : -1;
-  const int per = (a.V + SP_WARPS - 1) / SP_WARPS, i0 = w * per, i1 = min(a.V, i0 + per);
-  long long total = 0;
+  // a warp's run: a multiple of 128 entries, four per lane and step
+  const int per = ((a.V + n_blk * SP_WARPS - 1) / (n_blk * SP_WARPS) + 127) & ~127;
+  const int i0 = min(a.V, (rank * SP_WARPS + w) * per), i1 = min(a.V, i0 + per);
+  const int lo_bits = a.shift - 22;
+  const float lo_scale = (float)(1 << lo_bits);
+  // hi and lo of four entries
+  auto four = [&](int i, int (&hi)[4], int (&lo)[4]) {
+    const float4 x = row4<VEC>(p, i, i1, 0.0f);
+    const float4 y = q ? row4<VEC>(q, i, i1, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float px[4] = {x.x, x.y, x.z, x.w}, qx[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      mass_of(px[k], qx[k], lo_scale, hi[k], lo[k]);
+      if (i + k == dtok) hi[k] = lo[k] = 0;
+    }
+  };
+  long long total = 0, before = 0, mine = 0;
   for (int round = 0; round < 2; round++) {
     long long s = 0;
-    for (int i = i0 + lane; i < i1; i += 32) s += mass_at(p, q, dtok, i, a.shift);
-    s = warp_sum64(s);
+    for (int c = i0 + 4 * lane; c < i1; c += 8 * 128) {
+      int sh = 0, sl = 0;  // 32 entries: |hi|, |lo| < 2^28
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        int hi[4], lo[4];
+        four(c + 128 * k, hi, lo);
+        sh += (hi[0] + hi[1]) + (hi[2] + hi[3]), sl += (lo[0] + lo[1]) + (lo[2] + lo[3]);
+      }
+      s += ((long long)sh << lo_bits) + sl;
+    }
+    mine = warp_sum64(s);
+    if (lane == 0) part[w] = mine;
     __syncthreads();
-    if (lane == 0) part[w] = s;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i < SP_WARPS; i++) total += part[i];
+    if (w == 0) {
+      const long long t = warp_sum64(lane < SP_WARPS ? part[lane] : 0);
+      if (lane == 0) pub[0] = (int)(uint32_t)t, pub[1] = (int)(t >> 32);
+    }
+    cluster_sync();
+    total = before = 0;
+    for (int i = 0; i < n_blk; i++) {
+      const long long t = (long long)ld_peer(&pub[0], i) | (long long)ld_peer(&pub[1], i) << 32;
+      if (i < rank) before += t;
+      total += t;
+    }
+    for (int i = 0; i < w; i++) before += part[i];
+    cluster_sync();  // read by all before it is written again or the block leaves
     if (total > 0 || (!q && dtok < 0)) break;
     q = nullptr, dtok = -1;  // nothing is left: draw from p itself
   }
-  const long long thr = (long long)__umul64hi((unsigned long long)total, fixed_u(a.u_sample[b]));
-  if (total == 0) {
-    if (tid == 0) a.tokens[(long long)b * (a.G + 1) + n] = -1;
-  } else {
-    // the warp whose run holds the first cumulative sum above thr
-    long long before = 0;
-    for (int i = 0; i < w; i++) before += part[i];
-    if (before <= thr && thr < before + part[w]) {
-      for (int c = i0; c < i1; c += 32) {
-        const int i = c + lane;
-        long long s = i < i1 ? mass_at(p, q, dtok, i, a.shift) : 0;
+  int32_t *out = a.tokens + (long long)b * (a.G + 1);
+  if (total > 0) {
+    const long long thr = (long long)__umul64hi((unsigned long long)total, fixed_u(a.u_sample[b]));
+    if (before <= thr && thr < before + mine) {
+      for (int c = i0; c < i1; c += 128) {
+        int hi[4], lo[4];
+        four(c + 4 * lane, hi, lo);
+        long long e[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) e[k] = ((long long)hi[k] << lo_bits) + lo[k] + (k ? e[k - 1] : 0);
+        long long s = e[3];
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
           const long long o = __shfl_up_sync(0xffffffffu, s, k);
@@ -188,16 +366,39 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
         }
         const unsigned hit = __ballot_sync(0xffffffffu, before + s > thr);
         if (hit) {
-          if (lane == 0) a.tokens[(long long)b * (a.G + 1) + n] = c + __ffs(hit) - 1;
+          if (lane == __ffs(hit) - 1) {
+            const long long at = before + s - e[3];
+            int k = 0;
+            while (k < 3 && at + e[k] <= thr) k++;
+            out[n] = c + 4 * lane + k;
+          }
           break;
         }
         before += __shfl_sync(0xffffffffu, s, 31);
       }
     }
+  } else if (rank == 0 && tid == 0) {
+    out[n] = -1;
   }
-  if (tid <= a.G && tid != n)
-    a.tokens[(long long)b * (a.G + 1) + tid] = tid < n ? a.tok[(long long)b * a.G + tid] : -1;
-  if (tid == 0) a.n_accepted[b] = n;
+  if (rank == 0) {
+    if (tid <= a.G && tid != n) out[tid] = tid < n ? a.tok[(long long)b * a.G + tid] : -1;
+    if (tid == 0) a.n_accepted[b] = n;
+  }
+}
+
+static cudaError_t launch_rows(const void *fn, int rows, int cluster, cudaStream_t s, void **args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * cluster);
+  cfg.blockDim = dim3(SP_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace ds4
@@ -237,8 +438,9 @@ ds4moe_status ds4moe_token_probs(const float *logits, int64_t logits_stride, int
   float inv_t = temperature > 0.0f ? 1.0f / temperature : 0.0f;
   long long xs = logits_stride, os = probs_stride;
   void *args[] = {(void *)&logits, &xs, &vocab, &temperature, &inv_t, (void *)&probs, &os};
-  return sp_status(launch_pdl((const void *)k_token_probs, dim3(n_rows), dim3(SP_THREADS), 0, (cudaStream_t)stream, args,
-                              true));
+  const bool vec = (n_rows == 1 || (xs % 4 == 0 && os % 4 == 0)) && ((uintptr_t)logits & 15) == 0 && ((uintptr_t)probs & 15) == 0;
+  return sp_status(launch_rows(vec ? (const void *)k_token_probs<true> : (const void *)k_token_probs<false>, n_rows,
+                               cluster_of(vocab), (cudaStream_t)stream, args));
 }
 
 ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
@@ -260,10 +462,12 @@ ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, c
   a.G = max_draft, a.V = vocab, a.n_accepted = n_accepted, a.tokens = tokens_out, a.err = err_flags;
   int lg = 0;
   while ((1 << lg) < vocab) lg++;
-  a.shift = 62 - lg;
+  a.shift = lg > 17 ? 62 - lg : 45;
+  const bool vec = target_stride % 4 == 0 && ((uintptr_t)target & 15) == 0 &&
+                   (!a.draft || (draft_stride % 4 == 0 && ((uintptr_t)draft & 15) == 0));
   void *args[] = {&a};
-  return sp_status(launch_pdl((const void *)k_verify_drafts, dim3(n_seq), dim3(SP_THREADS), 0, (cudaStream_t)stream, args,
-                              true));
+  return sp_status(launch_rows(vec ? (const void *)k_verify_drafts<true> : (const void *)k_verify_drafts<false>, n_seq,
+                               cluster_of(vocab), (cudaStream_t)stream, args));
 }
 
 }  // extern "C"

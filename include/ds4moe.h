@@ -484,7 +484,8 @@ uint64_t ds4moe_attn_launch_count(const ds4moe_attn *h);
  *   n_accepted [n_seq]: n; tokens_out [n_seq][max_draft + 1]: the accepted
  *           drafts, the drawn token (-1 where p_n is 0 everywhere), then -1.
  *   Probabilities are taken in [0, 1] (others are clamped, NaN is 0) and
- *   summed exactly, in multiples of 2^(ceil(log2 vocab) - 62).
+ *   summed exactly, in multiples of 2^-45 (of 2^(ceil(log2 vocab) - 62) above
+ *   131072 entries).
  *   err_flags (device, may be NULL): DS4MOE_DEVERR_TOKEN_ID for a drafted token
  *   outside [0, vocab) (rejected), DS4MOE_DEVERR_LENGTH for n_draft outside
  *   [0, max_draft] (clamped).
