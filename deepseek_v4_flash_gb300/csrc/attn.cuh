@@ -80,18 +80,19 @@ __device__ __forceinline__ int page_of(const KvView &kv, int b, int pos) {
   return p >= 0 && p < kv.n_pages ? p : -1;
 }
 
-// The 16-position groups that hold every position visible to a query at
-// positions first .. last (0 <= first <= last): the groups of the first
-// positions, then those of the windows.
+// The groups of 2^sh positions (16 in the streaming kernel, up to 128 in the
+// tile kernel) that hold every position visible to a query at positions
+// first .. last (0 <= first <= last): the groups of the first positions, then
+// those of the windows.
 struct Groups {
   int n_sink;  // leading groups
   int win0;    // position group of list entry n_sink
   int n;       // list entries
 };
-__device__ __forceinline__ Groups groups_of(const AttnArgs &a, int first, int last) {
+__device__ __forceinline__ Groups groups_of(const AttnArgs &a, int first, int last, int sh = 4) {
   Groups g;
-  const int lo = window_lo(a, first), w0 = lo >> 4, w1 = (last >> 4) + 1;
-  const int ns = (min(a.n_sink, lo) + 15) >> 4;
+  const int lo = window_lo(a, first), w0 = lo >> sh, w1 = (last >> sh) + 1;
+  const int ns = (min(a.n_sink, lo) + (1 << sh) - 1) >> sh;
   if (ns >= w0) {  // no gap
     g.n_sink = 0, g.win0 = 0, g.n = w1;
   } else {
@@ -99,8 +100,8 @@ __device__ __forceinline__ Groups groups_of(const AttnArgs &a, int first, int la
   }
   return g;
 }
-__device__ __forceinline__ int group_pos(const Groups &g, int i) {
-  return (i < g.n_sink ? i : g.win0 + i - g.n_sink) << 4;
+__device__ __forceinline__ int group_pos(const Groups &g, int i, int sh = 4) {
+  return (i < g.n_sink ? i : g.win0 + i - g.n_sink) << sh;
 }
 
 // One row (a token's head) over list entries [g0, g1) by one warp, key by

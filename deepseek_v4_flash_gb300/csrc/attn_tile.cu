@@ -19,9 +19,11 @@
 // 512 columns and S needs room too, so a block computes one half of O's
 // columns (S is then computed twice).
 //
-// Visible positions are listed in groups of 16 (the first positions' groups,
-// then the windows' groups), and a tile is eight entries of that list: a
-// window of 128 positions costs 9 or 10 groups, not 3 tiles of 128.
+// Visible positions are listed in groups (the first positions' groups, then
+// the windows' groups), one TMA box each, and a tile is 128 positions of that
+// list. Small windows take groups of 16: a window of 128 positions costs 9 or
+// 10 of them, not 3 tiles of 128. Else groups are as large as the pages allow
+// (see box_rows).
 //
 // The call's tiles, in order, are dealt to the blocks in equal contiguous
 // runs. A row tile whose positions lie in several runs leaves one partial
@@ -34,7 +36,6 @@
 
 namespace ds4 {
 
-constexpr int AT_GROUPS = 8;            // 16-position groups of a key tile
 constexpr float AT_LAZY = 8.0f;
 // fp16 weights are scaled by 2^7 (at most 2^15 with the lazy maximum): small
 // weights keep 2^-31 of the largest instead of 2^-24.
@@ -65,6 +66,7 @@ struct TileMaps {
 
 // What the blocks of a call share.
 struct TileArgs {
+  int gsh;           // log2 of a group's positions
   int tpt;           // tokens of a row tile: 128 / group
   int members;       // blocks that work on the same (item, key tiles): row tiles x halves, or halves
   int gangs;
@@ -139,6 +141,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One lane of a converged warp, the way the compiler knows to be one: operands
+// of the instructions it issues stay in uniform registers (a branch on the
+// lane number made every product and every copy cost a loop over lanes: a
+// product step 700 cycles instead of its 512 on the tensor cores).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // A bounded wait of the whole warp: false for every lane when one gave up.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
@@ -154,15 +166,24 @@ struct Seg {
   int row0, n;       // first row of q, tokens
   int pos0;          // position of the first token
   int len;           // cached positions of the sequence
+  int last;          // last position that any row of the list's range sees
   Groups gr;
   int kt0, kt1;      // empty: nothing is visible, the rows are 0
   bool starts, ends;
 };
 
-__device__ __forceinline__ int tiles_of(const Groups &g) { return (g.n + AT_GROUPS - 1) / AT_GROUPS; }
+__device__ __forceinline__ int tiles_of(const Groups &g, int sh) { return ((g.n << sh) + 127) >> 7; }
 
-__device__ __forceinline__ Groups range_groups(const AttnArgs &a, int first, int last) {
-  return last >= 0 ? groups_of(a, max(first, 0), last) : Groups{0, 0, 0};
+__device__ __forceinline__ Groups range_groups(const AttnArgs &a, int first, int last, int sh) {
+  return last >= 0 ? groups_of(a, max(first, 0), last, sh) : Groups{0, 0, 0};
+}
+
+// Columns of key tile kt that the products need, in 16s: up to the last
+// visible position.
+__device__ __forceinline__ int cols16(const Seg &s, int kt, int sh) {
+  const int ng = s.gr.n - (kt << (7 - sh));  // groups from this tile on
+  if (ng > 1 << (7 - sh)) return 8;
+  return ((ng - 1) << (sh - 4)) + ((s.last - group_pos(s.gr, s.gr.n - 1, sh)) >> 4) + 1;
 }
 
 struct Sched {
@@ -182,21 +203,23 @@ struct Sched {
       s.row0 = si.tok0 + in.y;
       s.n = min(span, si.n - in.y);
       s.pos0 = si.len - si.n + in.y;
-      s.gr = range_groups(a, s.pos0, s.pos0 + s.n - 1);
+      s.last = s.pos0 + s.n - 1;
+      s.gr = range_groups(a, s.pos0, s.last, t.gsh);
     } else {
       // every row tile of the sequence reads the same positions
-      s.gr = range_groups(a, si.len - si.n, si.len - 1);
+      s.last = si.len - 1;
+      s.gr = range_groups(a, si.len - si.n, s.last, t.gsh);
       s.row0 = si.tok0 + member_rt * t.tpt;
       s.n = min(t.tpt, si.n - member_rt * t.tpt);
       s.pos0 = si.len - si.n + member_rt * t.tpt;
     }
-    return tiles_of(s.gr);
+    return tiles_of(s.gr, t.gsh);
   }
 
-  __device__ __forceinline__ int uni_units(const AttnArgs &a, int bb) const {
+  __device__ __forceinline__ int uni_units(const AttnArgs &a, int gsh, int bb) const {
     bool bad = false;
     const SeqInfo si = seq_info(a, bb, bad);
-    return max(1, tiles_of(range_groups(a, si.len - si.n, si.len - 1)));
+    return max(1, tiles_of(range_groups(a, si.len - si.n, si.len - 1, gsh), gsh));
   }
 
   // Whole warp. False when gang g has no tiles.
@@ -208,7 +231,7 @@ struct Sched {
       U = row_units * a.n_kv;
     } else {
       long long n = 0;
-      for (int i = lane; i < a.n_seq; i += 32) n += uni_units(a, i);
+      for (int i = lane; i < a.n_seq; i += 32) n += uni_units(a, t.gsh, i);
 #pragma unroll
       for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
       U = n * a.n_kv;
@@ -233,7 +256,7 @@ struct Sched {
     } else {
       long long r = u;
       for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-        const long long n = b0 + lane < a.n_seq ? (long long)uni_units(a, b0 + lane) * a.n_kv : 0;
+        const long long n = b0 + lane < a.n_seq ? (long long)uni_units(a, t.gsh, b0 + lane) * a.n_kv : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -245,7 +268,7 @@ struct Sched {
           const int l = __ffs(hit) - 1;
           r -= __shfl_sync(0xffffffffu, incl - n, l);
           b = b0 + l;
-          const int units = uni_units(a, b);
+          const int units = uni_units(a, t.gsh, b);
           kvh = (int)(r / units);
           item0 = u - (r - (long long)kvh * units), item1 = item0 + units;
           break;
@@ -271,7 +294,7 @@ struct Sched {
         item1 = kvh * row_units + t.first[idx + 1];
       } else {
         if (++kvh == a.n_kv) kvh = 0, b++;
-        item1 = item0 + uni_units(a, b);
+        item1 = item0 + uni_units(a, t.gsh, b);
       }
     }
     return true;
@@ -281,7 +304,7 @@ struct Sched {
 // Ragged calls: row groups of `span` tokens, in sequence order, and the
 // running count of their key tiles. One block; a few microseconds for some
 // thousand groups, against the attention's tens to hundreds.
-__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, long long *first, int2 *info, int *count,
+__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, int gsh, long long *first, int2 *info, int *count,
                                                 int *seq_first) {
   __shared__ long long warp_sum[32];
   __shared__ long long s_base;
@@ -343,7 +366,7 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, 
       bool unused = false;
       const SeqInfo si = seq_info(a, b, unused);
       const int p0 = si.len - si.n + t0;
-      units = max(1, tiles_of(range_groups(a, p0, p0 + min(span, si.n - t0) - 1)));
+      units = max(1, tiles_of(range_groups(a, p0, p0 + min(span, si.n - t0) - 1, gsh), gsh));
     }
     const long long x = scan(units);
     if (i < total) first[i] = x, info[i] = make_int2(b, t0);
@@ -435,25 +458,38 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       int st = 0;          // ring stages issued so far
       int qn = 0;          // items whose Q was issued
       bool bad_page = false;
-      // one operand tile: groups [8 kt, 8 kt + ng) of the item, nst stages
-      auto load_tile = [&](const Seg &s, int kt, const CUtensorMap *m, int nst, int chunk0) {
-        const int ng = min(AT_GROUPS, s.gr.n - kt * AT_GROUPS);
-        const int gi = lane & 7, p0 = group_pos(s.gr, kt * AT_GROUPS + min(gi, ng - 1));
-        int page = page_of(a.kv, s.b, p0);
-        const int row = p0 % a.kv.page_size;
-        if (page < 0) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
+      const int gpt = 1 << (7 - t.gsh);  // groups of a tile, one per lane
+      // where this lane's group of a key tile lies; the table's entry is
+      // checked when it is used, so that its latency is not waited for here
+      struct Place {
+        int page, row;
+      };
+      auto lookup = [&](const Seg &s, int kt) {
+        const int ng = min(gpt, s.gr.n - kt * gpt);
+        const int p0 = group_pos(s.gr, kt * gpt + min(lane, ng - 1), t.gsh), pi = p0 / a.kv.page_size;
+        return Place{a.kv.table[(long long)s.b * a.kv.table_stride + pi], p0 - pi * a.kv.page_size};
+      };
+      // one operand tile, nst stages
+      auto load_tile = [&](const Seg &s, int kt, const Place &pl, const CUtensorMap *m, int nst, int chunk0) {
+        const int ng = min(gpt, s.gr.n - kt * gpt);
+        int page = pl.page;
+        if (page < 0 || page >= a.kv.n_pages) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
         for (int i = 0; i < nst && ok; i++) {
           const int slot = st % C::NST;
           if (st >= C::NST && !wait_warp(empty(slot), (st / C::NST - 1) & 1)) {
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(full(slot), C::SC * ng * 2048);
-          __syncwarp();
-          if (lane < 8 * C::SC && gi < ng) {
-            const int c = lane >> 3;
-            tma_4d(ring + slot * C::STAGE + c * AT_CHUNK + gi * 2048, m, (chunk0 + i * C::SC + c) * 64, row, s.kvh, page,
-                   full(slot));
+          const uint32_t dst = ring + slot * C::STAGE, bar = full(slot);
+          const int x = (chunk0 + i * C::SC) * 64;
+          if (elect_one()) mbar_arrive_expect_tx(bar, (C::SC * 128u << t.gsh) * ng);
+          for (int g = 0; g < ng; g++) {
+            const int pg = __shfl_sync(0xffffffffu, page, g), row = __shfl_sync(0xffffffffu, pl.row, g);
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < C::SC; c++)
+                tma_4d(dst + c * AT_CHUNK + (g << (t.gsh + 7)), m, x + c * 64, row, s.kvh, pg, bar);
+            }
           }
           st++;
         }
@@ -470,22 +506,25 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           kk = ks.kt0;
         }
       };
+      Place kp = {}, vp_next = {};
       // the current key tile, and with an item's first one its Q
       auto load_k = [&]() {
         if (kk == ks.kt0) {
           for (int r = 0; r < NT && ok; r++) {
             if (qn > 0 && !wait_warp(b_qe + 8 * r, (qn - 1) & 1)) ok = false;
-            if (ok && lane == 0) {
+            if (ok && elect_one()) {
               mbar_arrive_expect_tx(b_qf + 8 * r, (D / 64) * t.tpt * a.group * 128);
               // rows past the call's last come in as zeros
+#pragma unroll
               for (int c = 0; c < D / 64; c++)
                 tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, ks.kvh * a.group, ks.row0 + r * t.tpt,
                        b_qf + 8 * r);
             }
+            __syncwarp();
           }
           qn++;
         }
-        if (ok) load_tile(ks, kk, &maps.k, C::KST, 0);
+        if (ok) load_tile(ks, kk, kp, &maps.k, C::KST, 0);
       };
       auto step_v = [&]() {
         vk++;
@@ -495,19 +534,25 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           vk = vs.kt0;
         }
       };
+      // a value tile lies where its key tile did: the places of the key tile to
+      // load (kp) and of the one before (vp)
+      Place vp = {};
       step_k();
       step_v();
-      if (NT == 1 && kmore) {
+      if (kmore) kp = lookup(ks, kk);
+      auto next_k = [&]() {
         load_k();
         step_k();
-      }
+        vp_next = kp;
+        if (kmore) kp = lookup(ks, kk);
+      };
+      if (NT == 1 && kmore) next_k();
       while (vmore && ok) {
         // the order in which the products use them
-        if (kmore) {
-          load_k();
-          step_k();
-        }
-        if (ok) load_tile(vs, vk, &maps.v, C::VST, half * (C::DV / 64));
+        vp = vp_next;
+        if (kmore) next_k();
+        if (NT == 2) vp = vp_next;
+        if (ok) load_tile(vs, vk, vp, &maps.v, C::VST, half * (C::DV / 64));
         step_v();
       }
       if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
@@ -523,9 +568,9 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     Sched sk;
     if (sk.init(a, t, gang)) {
       Sched sv = sk;
-      const bool leader = lane == 0;
       int st = 0, steps_k = 0, steps_v = 0, qn = 0;
       const uint32_t id_o = idesc<DT>(C::SC * 64, true);
+      const uint64_t dq = desc_sw128(q_sm, 0), dk = desc_sw128(ring, 0), dv = desc_sw128(ring, AT_CHUNK);
       Seg ks = {}, vs = {};
       int kk = 0, kr = NT - 1, vk = 0, vr = NT - 1;
       bool kmore = false, vmore = false;
@@ -554,51 +599,49 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       };
       auto qk = [&]() {
         const int buf = NT == 2 ? kr : steps_k & 1;
-        const int ng = min(AT_GROUPS, ks.gr.n - kk * AT_GROUPS);
         if (kk == ks.kt0 && !wait_warp(b_qf + 8 * kr, (qn - 1) & 1)) ok = false;
         if (kr == 0) kst0 = st, st += C::KST;
-        const uint32_t id = idesc<DT>(16 * ng, false);
-        for (int i = 0; i < C::KST && ok; i++) {
+        const uint32_t id = idesc<DT>(16 * cols16(ks, kk, t.gsh), false);
+#pragma unroll
+        for (int i = 0; i < C::KST; i++) {
           const int slot = (kst0 + i) % C::NST;
           if (kr == 0) wait_stage(kst0 + i);
-          if (!ok) break;
           tc_fence_after();
-          if (leader) {
+          if (ok && elect_one()) {
+            // descriptor addresses count 16 bytes
+            const uint64_t qa = dq + ((kr * (D / 64) + i * C::SC) * AT_CHUNK >> 4), kb = dk + (slot * C::STAGE >> 4);
 #pragma unroll
-            for (int c = 0; c < C::SC; c++) {
-              const uint32_t qa = q_sm + (kr * (D / 64) + i * C::SC + c) * AT_CHUNK, kb = ring + slot * C::STAGE + c * AT_CHUNK;
+            for (int c = 0; c < C::SC; c++)
 #pragma unroll
               for (int k = 0; k < 4; k++)
-                umma_f16(tmem + buf * 128, desc_sw128(qa + 32 * k, 0), desc_sw128(kb + 32 * k, 0), id, (i | c | k) != 0);
-            }
+                umma_f16(tmem + buf * 128, qa + (c * AT_CHUNK >> 4) + 2 * k, kb + (c * AT_CHUNK >> 4) + 2 * k, id,
+                         (i | c | k) != 0);
             if (kr == NT - 1) umma_commit(empty(slot));
+            if (i == C::KST - 1) {
+              umma_commit(b_sf + 8 * buf);
+              if (kk + 1 == ks.kt1) umma_commit(b_qe + 8 * kr);
+            }
           }
           __syncwarp();
         }
-        if (leader && ok) {
-          umma_commit(b_sf + 8 * buf);
-          if (kk + 1 == ks.kt1) umma_commit(b_qe + 8 * kr);
-        }
-        __syncwarp();
         steps_k++;
       };
       auto pv = [&]() {
         const int buf = NT == 2 ? vr : steps_v & 1;
-        const int ng = min(AT_GROUPS, vs.gr.n - vk * AT_GROUPS);
+        const int n16 = cols16(vs, vk, t.gsh);
         const int n_buf = steps_v >> 1;  // uses of this buffer so far
         if (vr == 0) {
           vst0 = st, st += C::VST;
           for (int i = 0; i < C::VST && ok; i++) wait_stage(vst0 + i);
           // rows past the sequence's length: whatever the page holds there
           // would meet a weight of 0; zeros instead
-          const int last = group_pos(vs.gr, vk * AT_GROUPS + ng - 1), live = vs.len - last;
-          if (ok && live < 16) {
-            const int n16 = (16 - live) * 8 * C::SC;
-            for (int i = 0; i < C::VST; i++)
-              for (int e = lane; e < n16; e += 32) {
-                const int c = e / ((16 - live) * 8), x = e % ((16 - live) * 8);
-                const uint32_t p = ring + ((vst0 + i) % C::NST) * C::STAGE + c * AT_CHUNK +
-                                   ((ng - 1) * 16 + live) * 128 + x * 16;
+          const int gpt = 1 << (7 - t.gsh), ng = min(gpt, vs.gr.n - vk * gpt);
+          const int live = ((ng - 1) << t.gsh) + vs.len - group_pos(vs.gr, vk * gpt + ng - 1, t.gsh);
+          if (ok && live < 16 * n16) {
+            const int n8 = (16 * n16 - live) * 8;
+            for (int i = 0; i < C::VST * C::SC; i++)
+              for (int e = lane; e < n8; e += 32) {
+                const uint32_t p = ring + ((vst0 + i / C::SC) % C::NST) * C::STAGE + i % C::SC * AT_CHUNK + live * 128 + e * 16;
                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(p), "r"(0) : "memory");
               }
             fence_proxy_async_smem();
@@ -607,13 +650,14 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         }
         if (ok && !wait_warp(b_pf + 8 * buf, n_buf & 1)) ok = false;
         tc_fence_after();
-        if (ok && leader) {
+        if (ok && elect_one()) {
 #pragma unroll
           for (int i = 0; i < C::VST; i++) {
-            const uint32_t vb = ring + ((vst0 + i) % C::NST) * C::STAGE;
+            const uint64_t vb = dv + (((vst0 + i) % C::NST) * C::STAGE >> 4);
             const uint32_t o = tmem + C::O_COL + (NT == 2 ? vr * C::DV : 0) + i * C::SC * 64;
-            for (int k = 0; k < ng; k++)
-              umma_f16_ts(o, tmem + buf * 128 + 8 * k, desc_sw128(vb + 2048 * k, AT_CHUNK), id_o, vk != vs.kt0 || k != 0);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+              if (k < n16) umma_f16_ts(o, tmem + buf * 128 + 8 * k, vb + (2048 * k >> 4), id_o, vk != vs.kt0 || k != 0);
             if (vr == NT - 1) umma_commit(empty((vst0 + i) % C::NST));
           }
           umma_commit(b_of + 8 * vr);
@@ -637,7 +681,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           step_v();
         }
       }
-      if (leader) umma_commit(b_done);
+      if (elect_one()) umma_commit(b_done);
       __syncwarp();
       mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
     }
@@ -660,11 +704,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         const int lo = window_lo(a, max(pos, 0));
         // what every row of this tile sees: positions up to p_first, from lo_last
         const int p_first = s.pos0 + r * t.tpt, lo_last = window_lo(a, max(s.pos0 + s.n - 1, 0));
-        const int shift = 16 * (s.gr.win0 - s.gr.n_sink);
+        const int shift = (s.gr.win0 - s.gr.n_sink) << t.gsh;
         float m = -INFINITY, l = 0.0f;
         for (int kt = s.kt0; kt < s.kt1; kt++, steps++) {
           const int buf = NT == 2 ? r : steps & 1, use = NT == 2 ? steps : steps >> 1;
-          const int ng = min(AT_GROUPS, s.gr.n - kt * AT_GROUPS);
           if (!wait_warp(b_sf + 8 * buf, use & 1)) {
             ok = false;
             break;
@@ -677,7 +720,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 #pragma unroll
           for (int c = 0; c < 4; c++) tmem_wait_ld(v + 32 * c);
           // columns c < cs: the first positions' groups, position 128 kt + c; others shifted
-          const int cs = 16 * s.gr.n_sink - 128 * kt, off = 128 * kt + shift;
+          const int cs = (s.gr.n_sink << t.gsh) - 128 * kt, off = 128 * kt + shift;
           if (cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last)) {
             const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs);
 #pragma unroll
@@ -922,6 +965,15 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, int n, const cuuint64_
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// log2 of a group's positions: groups lie within pages, and a window of W
+// positions reads up to two groups too many, so at most W / 16 (small windows:
+// 16, one TMA box is then 2 KB per 64 elements).
+int box_shift(int page_size, int window) {
+  int sh = 4;
+  while (sh < 7 && page_size % (32 << (sh - 4)) == 0 && (window == 0 || window / 16 >= 32 << (sh - 4))) sh++;
+  return sh;
+}
+
 struct TileFns {
   const void *tile, *join;
   int nt, dv, halves, q, threads;
@@ -976,6 +1028,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   const TileFns f = tile_fns(dtype, D, ragged);
   TileArgs t = {};
   t.tpt = 128 / a.group;
+  t.gsh = box_shift(a.kv.page_size, a.window);
   const int row_tiles = ragged ? 1 : (a.n_new + t.tpt - 1) / t.tpt;
   t.members = row_tiles * f.halves;
   t.gangs = n_sm / t.members;
@@ -986,14 +1039,14 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   const cuuint32_t qb[3] = {64, (cuuint32_t)a.group, (cuuint32_t)t.tpt};
   const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.n_kv, (cuuint64_t)a.kv.n_pages};
   const long long ks[3] = {a.kv.k_row, a.kv.k_head, a.kv.k_page}, vs[3] = {a.kv.v_row, a.kv.v_head, a.kv.v_page};
-  const cuuint32_t kb[4] = {64, 16, 1, 1};
+  const cuuint32_t kb[4] = {64, 1u << t.gsh, 1, 1};
   if (!make_map(&maps.q, dtype, a.q, 3, qd, qs, qb) || !make_map(&maps.k, dtype, a.kv.k, 4, kd, ks, kb) ||
       !make_map(&maps.v, dtype, a.kv.v, 4, kd, vs, kb))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   if (ragged) {
     int span = f.nt * t.tpt;
-    void *args[] = {(void *)&a, &span, &t.first, &t.info, &t.count, (void *)&w.seq_first};
+    void *args[] = {(void *)&a, &span, &t.gsh, &t.first, &t.info, &t.count, (void *)&w.seq_first};
     e = launch_pdl((const void *)k_attn_plan, dim3(1), dim3(1024), 0, s, args, true);
     ++*launches;
   }
