@@ -11,13 +11,13 @@
 // 2^AT_LAZY lose nothing: sums are kept in 32 bits and the quotient O / l does
 // not depend on m).
 //
-// Warps: 0 loads (TMA, 16-position boxes out of the pages, a ring of stages),
-// 1 issues the products, one warpgroup per row tile does the softmax and the
-// output. Two tiles of S are in flight: while one is turned into P, the next
-// one's product runs. Head dimension 64 and 128 (ragged calls): two row tiles per block share every
-// key and value tile, which halves the traffic from L2. Dimension 512: O has
-// 512 columns and S needs room too, so a block computes one half of O's
-// columns (S is then computed twice).
+// Warps: 0 loads (TMA out of the pages, a ring of stages), 1 issues the
+// products, 2 works out which tiles come next, one warpgroup per row tile does
+// the softmax and the output. Two tiles of S are in flight: while one is
+// turned into P, the next one's product runs. Head dimension 64 and 128 (ragged calls): two row
+// tiles per block share every key and value tile, which halves the traffic
+// from L2. Dimension 512: O has 512 columns and S needs room too, so a block
+// computes one half of O's columns (S is then computed twice).
 //
 // Visible positions are listed in groups (the first positions' groups, then
 // the windows' groups), one TMA box each, and a tile is 128 positions of that
@@ -44,6 +44,7 @@ constexpr float AT_BIAS = DT == DS4MOE_DT_F16 ? 7.0f : 0.0f;
 
 constexpr int AT_CHUNK = 128 * 128;     // 128 rows of 64 elements, 128-byte swizzled
 constexpr int AT_SMEM = 225 * 1024;
+constexpr int AT_SEGS = 4;              // segments the scheduling warp is ahead
 
 template <int D, int NT>
 struct TileCfg {
@@ -168,8 +169,8 @@ struct Seg {
   int len;           // cached positions of the sequence
   int last;          // last position that any row of the list's range sees
   Groups gr;
-  int kt0, kt1;      // empty: nothing is visible, the rows are 0
-  bool starts, ends;
+  int kt0, kt1;      // empty: nothing is visible, the rows are 0; kt1 < 0: no more work
+  int starts, ends;  // the run holds the item's first, last tile
 };
 
 __device__ __forceinline__ int tiles_of(const Groups &g, int sh) { return ((g.n << sh) + 127) >> 7; }
@@ -403,12 +404,42 @@ __device__ __noinline__ void redo_row_cols(const AttnArgs &a, int t, int h, int 
       o[(threadIdx.x & 31) + 32 * c] = Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Eight 16-byte pieces per lane, exchanged within groups of eight lanes: lane
+// j's piece i becomes piece j of lane i. A row per lane turns into eight rows
+// whose 128 bytes lie across the lanes, so that a store writes four whole
+// lines instead of a sixteenth of 32 (the output took 10 us of a block's 17
+// per item before).
+__device__ __forceinline__ void transpose8(uint32_t (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int c = 0; c < 8; c++)
+      if (!(c & d)) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[4 * c + k] : x[4 * (c | d) + k], d);
+          x[4 * c + k] = up ? got : x[4 * c + k];
+          x[4 * (c | d) + k] = up ? x[4 * (c | d) + k] : got;
+        }
+      }
+  }
+}
+
 template <int DT, int D, int NT>
 __global__ void __launch_bounds__(128 + 128 * NT, 1)
     k_attn_tile(const __grid_constant__ TileMaps maps, const AttnArgs a, const TileArgs t) {
   using C = TileCfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * 12 + 11];
+  __shared__ __align__(16) Seg segs[AT_SEGS];
+  __shared__ __align__(8) uint64_t bars[2 * 12 + 2 * AT_SEGS + 13];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -416,14 +447,17 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int i) { return bar0 + 8 * i; };
   auto empty = [&](int i) { return bar0 + 8 * (12 + i); };
-  const uint32_t b_qf = bar0 + 8 * 24, b_qe = b_qf + 16, b_sf = b_qe + 16, b_pf = b_sf + 16, b_of = b_pf + 16,
-                 b_done = b_of + 16;
+  auto seg_full = [&](int i) { return bar0 + 8 * (24 + i); };
+  auto seg_empty = [&](int i) { return bar0 + 8 * (24 + AT_SEGS + i); };
+  const uint32_t b_qf = bar0 + 8 * (24 + 2 * AT_SEGS), b_qe = b_qf + 16, b_sf = b_qe + 16, b_pa = b_sf + 16,
+                 b_pb = b_pa + 16, b_of = b_pb + 16, b_done = b_of + 16;
   if (w == 0) {
     if (lane == 0) {
       for (int i = 0; i < C::NST; i++) mbar_init(full(i), 1), mbar_init(empty(i), 1);
+      for (int i = 0; i < AT_SEGS; i++) mbar_init(seg_full(i), 1), mbar_init(seg_empty(i), 2 + 4 * NT);
       for (int i = 0; i < 2; i++) {
         mbar_init(b_qf + 8 * i, 1), mbar_init(b_qe + 8 * i, 1), mbar_init(b_sf + 8 * i, 1);
-        mbar_init(b_pf + 8 * i, 128), mbar_init(b_of + 8 * i, 1);
+        mbar_init(b_pa + 8 * i, 128), mbar_init(b_pb + 8 * i, 128), mbar_init(b_of + 8 * i, 1);
       }
       mbar_init(b_done, 1);
       fence_mbar_init();
@@ -442,338 +476,320 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 
   const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members;
   const int half = member % C::HALVES, rt = member / C::HALVES;
-  Sched sc;
   bool ok = true;  // no wait has run out
 
-  if (w == 0) {
+  // The block's segments in order, from the scheduling warp; false after the
+  // last one.
+  int seg_n = 0;
+  auto next_seg = [&](Seg &s) {
+    const int i = seg_n % AT_SEGS;
+    if (!wait_warp(seg_full(i), (seg_n / AT_SEGS) & 1)) return ok = false;
+    s = segs[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(i));
+    seg_n++;
+    return s.kt1 >= 0;
+  };
+
+  if (w == 2) {
+    // ---- order of work: a few segments ahead of the others, so that nobody
+    // else waits for lengths, row groups and tables of them
+    Sched sc;
+    bool more = sc.init(a, t, gang), split_out = false;
+    while (ok) {
+      Seg s;
+      s.kt1 = -1;
+      if (more) more = sc.next(a, t, rt, NT, s);
+      if (!more) s.kt1 = -1;
+      const int i = seg_n % AT_SEGS;
+      if (seg_n >= AT_SEGS && !wait_warp(seg_empty(i), (seg_n / AT_SEGS - 1) & 1)) ok = false;
+      if (lane == 0) {
+        segs[i] = s;
+        mbar_arrive(seg_full(i));
+        if (more && s.starts && !s.ends && member == 0) {
+          // the first of an item's blocks says what k_attn_join adds up
+          const int parts = (int)((sc.item1 * sc.N - 1) / sc.U) - gang + 1;
+          t.split[2 * gang] = make_int4(parts, s.b, s.kvh, s.pos0);
+          t.split[2 * gang + 1] = make_int4(s.row0, a.cu_q ? s.n : a.n_new, 0, 0);
+        }
+      }
+      split_out |= more && s.starts && !s.ends;
+      __syncwarp();
+      seg_n++;
+      if (!more) break;
+    }
+    if (!split_out && member == 0 && lane == 0) t.split[2 * gang].x = 0;
+  } else if (w == 0) {
     // ---- loads
     if (!a.cu_q && blockIdx.x == 0) {
       bool bad = false;
       for (int i = lane; i < a.n_seq; i += 32) seq_info(a, i, bad);
       if (bad) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
     }
-    Sched sk;
-    if (sk.init(a, t, gang)) {
-      Sched sv = sk;
-      int st = 0;          // ring stages issued so far
-      int qn = 0;          // items whose Q was issued
-      bool bad_page = false;
-      const int gpt = 1 << (7 - t.gsh);  // groups of a tile, one per lane
-      // where this lane's group of a key tile lies; the table's entry is
-      // checked when it is used, so that its latency is not waited for here
-      struct Place {
-        int page, row;
-      };
-      auto lookup = [&](const Seg &s, int kt) {
-        const int ng = min(gpt, s.gr.n - kt * gpt);
-        const int p0 = group_pos(s.gr, kt * gpt + min(lane, ng - 1), t.gsh), pi = p0 / a.kv.page_size;
-        return Place{a.kv.table[(long long)s.b * a.kv.table_stride + pi], p0 - pi * a.kv.page_size};
-      };
-      // one operand tile, nst stages
-      auto load_tile = [&](const Seg &s, int kt, const Place &pl, const CUtensorMap *m, int nst, int chunk0) {
-        const int ng = min(gpt, s.gr.n - kt * gpt);
-        int page = pl.page;
-        if (page < 0 || page >= a.kv.n_pages) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
-        for (int i = 0; i < nst && ok; i++) {
-          const int slot = st % C::NST;
-          if (st >= C::NST && !wait_warp(empty(slot), (st / C::NST - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = ring + slot * C::STAGE, bar = full(slot);
-          const int x = (chunk0 + i * C::SC) * 64;
-          if (elect_one()) mbar_arrive_expect_tx(bar, (C::SC * 128u << t.gsh) * ng);
-          for (int g = 0; g < ng; g++) {
-            const int pg = __shfl_sync(0xffffffffu, page, g), row = __shfl_sync(0xffffffffu, pl.row, g);
-            if (elect_one()) {
+    int st = 0;  // ring stages issued so far
+    int qn = 0;  // items whose Q was issued
+    bool bad_page = false;
+    const int gpt = 1 << (7 - t.gsh);  // groups of a tile, one per lane
+    // where this lane's group of a key tile lies; the table's entry is checked
+    // when it is used, so that its latency is not waited for here
+    struct Place {
+      int page, row;
+    };
+    auto lookup = [&](const Seg &s, int kt) {
+      const int ng = min(gpt, s.gr.n - kt * gpt);
+      const int p0 = group_pos(s.gr, kt * gpt + min(lane, ng - 1), t.gsh), pi = p0 / a.kv.page_size;
+      return Place{a.kv.table[(long long)s.b * a.kv.table_stride + pi], p0 - pi * a.kv.page_size};
+    };
+    // one operand tile, nst stages
+    auto load_tile = [&](const Seg &s, int kt, const Place &pl, const CUtensorMap *m, int nst, int chunk0) {
+      const int ng = min(gpt, s.gr.n - kt * gpt);
+      int page = pl.page;
+      if (page < 0 || page >= a.kv.n_pages) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
+      for (int i = 0; i < nst && ok; i++) {
+        const int slot = st % C::NST;
+        if (st >= C::NST && !wait_warp(empty(slot), (st / C::NST - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = ring + slot * C::STAGE, bar = full(slot);
+        const int x = (chunk0 + i * C::SC) * 64;
+        if (elect_one()) mbar_arrive_expect_tx(bar, (C::SC * 128u << t.gsh) * ng);
+        for (int g = 0; g < ng; g++) {
+          const int pg = __shfl_sync(0xffffffffu, page, g), row = __shfl_sync(0xffffffffu, pl.row, g);
+          if (elect_one()) {
 #pragma unroll
-              for (int c = 0; c < C::SC; c++)
-                tma_4d(dst + c * AT_CHUNK + (g << (t.gsh + 7)), m, x + c * 64, row, s.kvh, pg, bar);
-            }
+            for (int c = 0; c < C::SC; c++)
+              tma_4d(dst + c * AT_CHUNK + (g << (t.gsh + 7)), m, x + c * 64, row, s.kvh, pg, bar);
           }
-          st++;
         }
-      };
-      Seg ks = {}, vs = {};
-      int kk = 0, vk = 0;
-      bool kmore = false, vmore = false;
-      // the next key tile of the run, entering the next item (and loading its Q) when one is done
-      auto step_k = [&]() {
-        kk++;
-        while (!kmore || kk >= ks.kt1) {
-          kmore = sk.next(a, t, rt, NT, ks);
-          if (!kmore) return;
-          kk = ks.kt0;
-        }
-      };
-      Place kp = {}, vp_next = {};
-      // the current key tile, and with an item's first one its Q
-      auto load_k = [&]() {
-        if (kk == ks.kt0) {
-          for (int r = 0; r < NT && ok; r++) {
-            if (qn > 0 && !wait_warp(b_qe + 8 * r, (qn - 1) & 1)) ok = false;
-            if (ok && elect_one()) {
-              mbar_arrive_expect_tx(b_qf + 8 * r, (D / 64) * t.tpt * a.group * 128);
-              // rows past the call's last come in as zeros
+        st++;
+      }
+    };
+    Seg s;
+    while (ok && next_seg(s)) {
+      if (s.kt0 >= s.kt1) continue;
+      Place kp = lookup(s, s.kt0);
+      for (int r = 0; r < NT && ok; r++) {
+        if (qn > 0 && !wait_warp(b_qe + 8 * r, (qn - 1) & 1)) ok = false;
+        if (ok && elect_one()) {
+          mbar_arrive_expect_tx(b_qf + 8 * r, (D / 64) * t.tpt * a.group * 128);
+          // rows past the call's last come in as zeros
 #pragma unroll
-              for (int c = 0; c < D / 64; c++)
-                tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, ks.kvh * a.group, ks.row0 + r * t.tpt,
-                       b_qf + 8 * r);
-            }
-            __syncwarp();
-          }
-          qn++;
+          for (int c = 0; c < D / 64; c++)
+            tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, s.kvh * a.group, s.row0 + r * t.tpt, b_qf + 8 * r);
         }
-        if (ok) load_tile(ks, kk, kp, &maps.k, C::KST, 0);
-      };
-      auto step_v = [&]() {
-        vk++;
-        while (!vmore || vk >= vs.kt1) {
-          vmore = sv.next(a, t, rt, NT, vs);
-          if (!vmore) return;
-          vk = vs.kt0;
-        }
-      };
-      // a value tile lies where its key tile did: the places of the key tile to
-      // load (kp) and of the one before (vp)
-      Place vp = {};
-      step_k();
-      step_v();
-      if (kmore) kp = lookup(ks, kk);
-      auto next_k = [&]() {
-        load_k();
-        step_k();
-        vp_next = kp;
-        if (kmore) kp = lookup(ks, kk);
-      };
-      if (NT == 1 && kmore) next_k();
-      while (vmore && ok) {
-        // the order in which the products use them
-        vp = vp_next;
-        if (kmore) next_k();
-        if (NT == 2) vp = vp_next;
-        if (ok) load_tile(vs, vk, vp, &maps.v, C::VST, half * (C::DV / 64));
-        step_v();
+        __syncwarp();
       }
-      if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
-      if (!ok) {
-        // the copies in flight land before the block leaves
-        for (int i = max(0, st - C::NST); i < st; i++) mbar_wait_bounded(full(i % C::NST), (i / C::NST) & 1);
-        for (int r = 0; r < NT; r++)
-          if (qn > 0) mbar_wait_bounded(b_qf + 8 * r, (qn - 1) & 1);
+      qn++;
+      // in the order in which the products use them: one row tile computes the
+      // next tile's S before the current O
+      if (NT == 1 && ok) load_tile(s, s.kt0, kp, &maps.k, C::KST, 0);
+      for (int kt = s.kt0; kt < s.kt1 && ok; kt++) {
+        const Place vp = kp;
+        if (kt + 1 < s.kt1) kp = lookup(s, kt + 1);
+        if (NT == 2) load_tile(s, kt, vp, &maps.k, C::KST, 0);
+        else if (kt + 1 < s.kt1) load_tile(s, kt + 1, kp, &maps.k, C::KST, 0);
+        if (ok) load_tile(s, kt, vp, &maps.v, C::VST, half * (C::DV / 64));
       }
+    }
+    if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
+    if (!ok) {
+      // the copies in flight land before the block leaves
+      for (int i = max(0, st - C::NST); i < st; i++) mbar_wait_bounded(full(i % C::NST), (i / C::NST) & 1);
+      for (int r = 0; r < NT; r++)
+        if (qn > 0) mbar_wait_bounded(b_qf + 8 * r, (qn - 1) & 1);
     }
   } else if (w == 1) {
     // ---- products
-    Sched sk;
-    if (sk.init(a, t, gang)) {
-      Sched sv = sk;
-      int st = 0, steps_k = 0, steps_v = 0, qn = 0;
-      const uint32_t id_o = idesc<DT>(C::SC * 64, true);
-      const uint64_t dq = desc_sw128(q_sm, 0), dk = desc_sw128(ring, 0), dv = desc_sw128(ring, AT_CHUNK);
-      Seg ks = {}, vs = {};
-      int kk = 0, kr = NT - 1, vk = 0, vr = NT - 1;
-      bool kmore = false, vmore = false;
-      int kst0 = 0, vst0 = 0;  // ring stages of the current key and value tile
-      auto step_k = [&]() {
-        if (++kr < NT) return;
-        kr = 0, kk++;
-        while (!kmore || kk >= ks.kt1) {
-          kmore = sk.next(a, t, rt, NT, ks);
-          if (!kmore) return;
-          kk = ks.kt0;
-          if (ks.kt0 < ks.kt1) qn++;
-        }
-      };
-      auto step_v = [&]() {
-        if (++vr < NT) return;
-        vr = 0, vk++;
-        while (!vmore || vk >= vs.kt1) {
-          vmore = sv.next(a, t, rt, NT, vs);
-          if (!vmore) return;
-          vk = vs.kt0;
-        }
-      };
-      auto wait_stage = [&](int s) {
-        if (!wait_warp(full(s % C::NST), (s / C::NST) & 1)) ok = false;
-      };
-      auto qk = [&]() {
-        const int buf = NT == 2 ? kr : steps_k & 1;
-        if (kk == ks.kt0 && !wait_warp(b_qf + 8 * kr, (qn - 1) & 1)) ok = false;
-        if (kr == 0) kst0 = st, st += C::KST;
-        const uint32_t id = idesc<DT>(16 * cols16(ks, kk, t.gsh), false);
+    int st = 0, qn = 0;
+    int steps = 0;  // (key tile, row tile) pairs before the current segment
+    const uint32_t id_o = idesc<DT>(C::SC * 64, true);
+    const uint64_t dq = desc_sw128(q_sm, 0), dk = desc_sw128(ring, 0), dv = desc_sw128(ring, AT_CHUNK);
+    int kst0 = 0, vst0 = 0;  // ring stages of the current key and value tile
+    Seg s;
+    auto wait_stage = [&](int i) {
+      if (!wait_warp(full(i % C::NST), (i / C::NST) & 1)) ok = false;
+    };
+    auto qk = [&](int i) {  // step i of the segment
+      const int kt = s.kt0 + i / NT, r = i % NT, buf = (steps + i) & 1;
+      if (i < NT && !wait_warp(b_qf + 8 * r, (qn - 1) & 1)) ok = false;
+      if (r == 0) kst0 = st, st += C::KST;
+      const uint32_t id = idesc<DT>(16 * cols16(s, kt, t.gsh), false);
 #pragma unroll
-        for (int i = 0; i < C::KST; i++) {
-          const int slot = (kst0 + i) % C::NST;
-          if (kr == 0) wait_stage(kst0 + i);
-          tc_fence_after();
-          if (ok && elect_one()) {
-            // descriptor addresses count 16 bytes
-            const uint64_t qa = dq + ((kr * (D / 64) + i * C::SC) * AT_CHUNK >> 4), kb = dk + (slot * C::STAGE >> 4);
+      for (int j = 0; j < C::KST; j++) {
+        const int slot = (kst0 + j) % C::NST;
+        if (r == 0) wait_stage(kst0 + j);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          // descriptor addresses count 16 bytes
+          const uint64_t qa = dq + ((r * (D / 64) + j * C::SC) * AT_CHUNK >> 4), kb = dk + (slot * C::STAGE >> 4);
 #pragma unroll
-            for (int c = 0; c < C::SC; c++)
+          for (int c = 0; c < C::SC; c++)
 #pragma unroll
-              for (int k = 0; k < 4; k++)
-                umma_f16(tmem + buf * 128, qa + (c * AT_CHUNK >> 4) + 2 * k, kb + (c * AT_CHUNK >> 4) + 2 * k, id,
-                         (i | c | k) != 0);
-            if (kr == NT - 1) umma_commit(empty(slot));
-            if (i == C::KST - 1) {
-              umma_commit(b_sf + 8 * buf);
-              if (kk + 1 == ks.kt1) umma_commit(b_qe + 8 * kr);
-            }
+            for (int k = 0; k < 4; k++)
+              umma_f16(tmem + buf * 128, qa + (c * AT_CHUNK >> 4) + 2 * k, kb + (c * AT_CHUNK >> 4) + 2 * k, id,
+                       (j | c | k) != 0);
+          if (r == NT - 1) umma_commit(empty(slot));
+          if (j == C::KST - 1) {
+            umma_commit(b_sf + 8 * buf);
+            if (kt + 1 == s.kt1) umma_commit(b_qe + 8 * r);
           }
+        }
+        __syncwarp();
+      }
+    };
+    auto pv = [&](int i) {
+      const int kt = s.kt0 + i / NT, r = i % NT, buf = (steps + i) & 1, use = (steps + i) >> 1;
+      const int n16 = cols16(s, kt, t.gsh);
+      if (r == 0) {
+        vst0 = st, st += C::VST;
+        for (int j = 0; j < C::VST; j++) wait_stage(vst0 + j);
+        // rows past the sequence's length: whatever the page holds there would
+        // meet a weight of 0; zeros instead
+        const int gpt = 1 << (7 - t.gsh), ng = min(gpt, s.gr.n - kt * gpt);
+        const int live = ((ng - 1) << t.gsh) + s.len - group_pos(s.gr, kt * gpt + ng - 1, t.gsh);
+        if (ok && live < 16 * n16) {
+          const int n8 = (16 * n16 - live) * 8;
+          for (int j = 0; j < C::VST * C::SC; j++)
+            for (int e = lane; e < n8; e += 32) {
+              const uint32_t p = ring + ((vst0 + j / C::SC) % C::NST) * C::STAGE + j % C::SC * AT_CHUNK + live * 128 + e * 16;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(p), "r"(0) : "memory");
+            }
+          fence_proxy_async_smem();
           __syncwarp();
         }
-        steps_k++;
-      };
-      auto pv = [&]() {
-        const int buf = NT == 2 ? vr : steps_v & 1;
-        const int n16 = cols16(vs, vk, t.gsh);
-        const int n_buf = steps_v >> 1;  // uses of this buffer so far
-        if (vr == 0) {
-          vst0 = st, st += C::VST;
-          for (int i = 0; i < C::VST && ok; i++) wait_stage(vst0 + i);
-          // rows past the sequence's length: whatever the page holds there
-          // would meet a weight of 0; zeros instead
-          const int gpt = 1 << (7 - t.gsh), ng = min(gpt, vs.gr.n - vk * gpt);
-          const int live = ((ng - 1) << t.gsh) + vs.len - group_pos(vs.gr, vk * gpt + ng - 1, t.gsh);
-          if (ok && live < 16 * n16) {
-            const int n8 = (16 * n16 - live) * 8;
-            for (int i = 0; i < C::VST * C::SC; i++)
-              for (int e = lane; e < n8; e += 32) {
-                const uint32_t p = ring + ((vst0 + i / C::SC) % C::NST) * C::STAGE + i % C::SC * AT_CHUNK + live * 128 + e * 16;
-                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(p), "r"(0) : "memory");
-              }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (ok && !wait_warp(b_pf + 8 * buf, n_buf & 1)) ok = false;
+      }
+      // P comes in two halves of 64 columns
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        if (ok && !wait_warp((h ? b_pb : b_pa) + 8 * buf, use & 1)) ok = false;
         tc_fence_after();
         if (ok && elect_one()) {
 #pragma unroll
-          for (int i = 0; i < C::VST; i++) {
-            const uint64_t vb = dv + (((vst0 + i) % C::NST) * C::STAGE >> 4);
-            const uint32_t o = tmem + C::O_COL + (NT == 2 ? vr * C::DV : 0) + i * C::SC * 64;
+          for (int j = 0; j < C::VST; j++) {
+            const uint64_t vb = dv + (((vst0 + j) % C::NST) * C::STAGE >> 4);
+            const uint32_t o = tmem + C::O_COL + r * C::DV + j * C::SC * 64;
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-              if (k < n16) umma_f16_ts(o, tmem + buf * 128 + 8 * k, vb + (2048 * k >> 4), id_o, vk != vs.kt0 || k != 0);
-            if (vr == NT - 1) umma_commit(empty((vst0 + i) % C::NST));
+            for (int k = 4 * h; k < 4 * h + 4; k++)
+              if (k < n16) umma_f16_ts(o, tmem + buf * 128 + 8 * k, vb + (2048 * k >> 4), id_o, kt != s.kt0 || k != 0);
+            if (h == 1 && r == NT - 1) umma_commit(empty((vst0 + j) % C::NST));
           }
-          umma_commit(b_of + 8 * vr);
+          if (h == 1) umma_commit(b_of + 8 * r);
         }
         __syncwarp();
-        steps_v++;
-      };
-      step_k();
-      step_v();
-      if (kmore) {
-        qk();
-        step_k();
       }
-      while (vmore && ok) {
-        if (kmore) {
-          qk();
-          step_k();
-        }
-        if (ok) {
-          pv();
-          step_v();
-        }
+    };
+    while (ok && next_seg(s)) {
+      const int n = (s.kt1 - s.kt0) * NT;
+      if (n <= 0) continue;
+      qn++;
+      qk(0);
+      for (int i = 0; i < n && ok; i++) {
+        if (i + 1 < n) qk(i + 1);
+        if (ok) pv(i);
       }
-      if (elect_one()) umma_commit(b_done);
-      __syncwarp();
-      mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
+      steps += n;
     }
+    if (elect_one()) umma_commit(b_done);
+    __syncwarp();
+    mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
   } else if (w >= 4) {
     // ---- softmax and output: one warpgroup per row tile, one thread per row
     const int r = NT == 2 ? (w >> 2) - 1 : 0;
     const int row = (w & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((w & 3) * 32) << 16;
     const int tok = row / a.group, head = row - tok * a.group;  // within the tile and the key-value head
-    const bool in_tile = tok < t.tpt;
-    if (sc.init(a, t, gang)) {
-      Seg s;
-      int steps = 0;  // key tiles of this row tile so far
-      int4 *split = t.split + 2 * gang;
-      bool split_out = false;
-      while (ok && sc.next(a, t, rt, NT, s)) {
-        const int my_tok = r * t.tpt + tok;
-        const bool valid = in_tile && my_tok < s.n;
-        const int pos = valid ? s.pos0 + my_tok : -1;
-        const int lo = window_lo(a, max(pos, 0));
-        // what every row of this tile sees: positions up to p_first, from lo_last
-        const int p_first = s.pos0 + r * t.tpt, lo_last = window_lo(a, max(s.pos0 + s.n - 1, 0));
-        const int shift = (s.gr.win0 - s.gr.n_sink) << t.gsh;
-        float m = -INFINITY, l = 0.0f;
-        for (int kt = s.kt0; kt < s.kt1; kt++, steps++) {
-          const int buf = NT == 2 ? r : steps & 1, use = NT == 2 ? steps : steps >> 1;
-          if (!wait_warp(b_sf + 8 * buf, use & 1)) {
-            ok = false;
-            break;
+    const int my_tok = tok < t.tpt ? r * t.tpt + tok : INT32_MAX;
+    const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
+    int steps = 0;  // key tiles of this row tile so far
+    Seg s;
+    while (ok && next_seg(s)) {
+      const bool valid = my_tok < s.n;
+      const int pos = valid ? s.pos0 + my_tok : -1;
+      const int lo = window_lo(a, max(pos, 0));
+      // what every row of this tile sees: positions up to p_first, from lo_last
+      const int p_first = s.pos0 + r * t.tpt, lo_last = window_lo(a, max(s.pos0 + s.n - 1, 0));
+      const int shift = (s.gr.win0 - s.gr.n_sink) << t.gsh;
+      float m = -INFINITY, l = 0.0f;
+      for (int kt = s.kt0; kt < s.kt1; kt++, steps++) {
+        const int buf = NT == 2 ? r : steps & 1, use = NT == 2 ? steps : steps >> 1;
+        const int nch = (cols16(s, kt, t.gsh) + 1) >> 1;  // 32-column pieces with something to see
+        if (!wait_warp(b_sf + 8 * buf, use & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = tmem + lanes + buf * 128;
+        float v[128];
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+          if (c < nch) {
+            tmem_ld32(sa + 32 * c, v + 32 * c);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i++) v[32 * c + i] = -INFINITY;
           }
-          tc_fence_after();
-          const uint32_t sa = tmem + lanes + buf * 128;
-          float v[128];
 #pragma unroll
-          for (int c = 0; c < 4; c++) tmem_ld32(sa + 32 * c, v + 32 * c);
+        for (int c = 0; c < 4; c++) tmem_wait_ld(v + 32 * c);
+        // columns c < cs: the first positions' groups, position 128 kt + c; others shifted
+        const int cs = (s.gr.n_sink << t.gsh) - 128 * kt, off = 128 * kt + shift;
+        if (cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last)) {
+          const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs);
 #pragma unroll
-          for (int c = 0; c < 4; c++) tmem_wait_ld(v + 32 * c);
-          // columns c < cs: the first positions' groups, position 128 kt + c; others shifted
-          const int cs = (s.gr.n_sink << t.gsh) - 128 * kt, off = 128 * kt + shift;
-          if (cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last)) {
-            const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs);
+          for (int c = 0; c < 4; c++)
+            if (c < nch) {
+              const uint32_t bits =
+                  range_bits(0, e0, c) |
+                  ((range_bits(lo - off, pos + 1 - off, c) | range_bits(0, min(a.n_sink, pos + 1) - off, c)) &
+                   range_bits(cs, 128, c));
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-              uint32_t bits = range_bits(0, e0, c) |
-                              ((range_bits(lo - off, pos + 1 - off, c) | range_bits(0, min(a.n_sink, pos + 1) - off, c)) &
-                               range_bits(cs, 128, c));
-              if (bits != 0xFFFFFFFFu) {
-#pragma unroll
-                for (int i = 0; i < 32; i++)
-                  if (!(bits >> i & 1)) v[32 * c + i] = -INFINITY;
-              }
+              for (int i = 0; i < 32; i++)
+                if (!(bits >> i & 1)) v[32 * c + i] = -INFINITY;
             }
-          }
-          float mx[4] = {v[0], v[1], v[2], v[3]};
+        }
+        float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-          for (int i = 4; i < 128; i++) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2 - AT_BIAS<DT>;
-          const bool grow = mt > m + AT_LAZY || (m == -INFINITY && mt > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mt : m;
-            const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
-            m = mn, l *= f;
-            if (kt > s.kt0) {
-              // the last product into O has to be done
-              if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
+        for (int i = 4; i < 124; i += 8) {
+          mx[0] = max3(mx[0], v[i], v[i + 1]), mx[1] = max3(mx[1], v[i + 2], v[i + 3]);
+          mx[2] = max3(mx[2], v[i + 4], v[i + 5]), mx[3] = max3(mx[3], v[i + 6], v[i + 7]);
+        }
+        mx[0] = max3(mx[0], v[124], v[125]), mx[1] = max3(mx[1], v[126], v[127]);
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2 - AT_BIAS<DT>;
+        const bool grow = mt > m + AT_LAZY || (m == -INFINITY && mt > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? mt : m;
+          const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+          m = mn, l *= f;
+          if (kt > s.kt0) {
+            // the last product into O has to be done
+            if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < C::DV; c += 16) {
-                uint32_t x[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-                    "tcgen05.wait::ld.sync.aligned;"
-                    : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
-                      "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
-                    : "r"(oa + c)
-                    : "memory");
+            for (int c = 0; c < C::DV; c += 16) {
+              uint32_t x[16];
+              asm volatile(
+                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                  "tcgen05.wait::ld.sync.aligned;"
+                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+                    "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+                  : "r"(oa + c)
+                  : "memory");
 #pragma unroll
-                for (int i = 0; i < 16; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                tmem_st16(oa + c, x);
-              }
-              tmem_wait_st();
+              for (int i = 0; i < 16; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+              tmem_st16(oa + c, x);
             }
+            tmem_wait_st();
           }
-          const float ms = m == -INFINITY ? 0.0f : m;
-          const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-ms, -ms);
-          unsigned long long sum[2] = {0, 0};
+        }
+        const float ms = m == -INFINITY ? 0.0f : m;
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-ms, -ms);
+        unsigned long long sum[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
+        for (int c = 0; c < 4; c++) {
+          if (c < nch) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; i++) {
@@ -785,84 +801,96 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
             }
             tmem_st16(sa + 16 * c, p);
           }
-          float s0, s1, s2, s3;
-          f2_unpack(sum[0], s0, s1);
-          f2_unpack(sum[1], s2, s3);
-          l += (s0 + s1) + (s2 + s3);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(b_pf + 8 * buf);
-        }
-        if (!ok) break;
-        const bool whole = s.starts && s.ends, none = s.kt0 >= s.kt1;
-        if (!none) {
-          // one row tile: the product before the last may be unfinished too (S
-          // of a tile follows the product two tiles back), and a parity tells
-          // only two neighbouring phases apart
-          if ((NT == 1 && !wait_warp(b_of, (steps - 2) & 1)) || !wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-        }
-        const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
-        const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
-        const float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
-        const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
-        float *pp = t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH;
-        uint16_t *op = a.out + (long long)tq * a.out_stride + (long long)hq * D + half * C::DV;
-        bool nan = false;
-#pragma unroll 1
-        for (int c = 0; c < C::DV; c += 32) {
-          float x[32];
-          if (!none) {
-            tmem_ld32(oa + c, x);
-            tmem_wait_ld(x);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i++) x[i] = 0.0f;
-          }
-          if (valid) {
-            if (whole) {
-#pragma unroll
-              for (int i = 0; i < 32; i++) {
-                x[i] *= inv;
-                nan |= x[i] != x[i];
-              }
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4 *>(op + c + i) =
-                    make_uint4(Half16<DT>::down(x[i], x[i + 1]), Half16<DT>::down(x[i + 2], x[i + 3]),
-                               Half16<DT>::down(x[i + 4], x[i + 5]), Half16<DT>::down(x[i + 6], x[i + 7]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(pp + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            }
+          if (c == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(b_pa + 8 * buf);
           }
         }
-        if (valid && !whole) pp[C::DV] = m, pp[C::DV + 1] = l;
+        tmem_wait_st();
         tc_fence_before();
-        unsigned again = __ballot_sync(0xffffffffu, nan);
-        while (again) {
-          const int x = __ffs(again) - 1;
-          again &= again - 1;
-          redo_row_cols<DT, D>(a, __shfl_sync(0xffffffffu, tq, x), __shfl_sync(0xffffffffu, hq, x), s.b,
-                               __shfl_sync(0xffffffffu, pos, x), half * C::DV, (half + 1) * C::DV);
+        // Every product into O is waited for before the next one can end: a
+        // parity tells only neighbouring phases apart. (It has ended long
+        // since, in general.)
+        if (kt > s.kt0 && !wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+          ok = false;
+          break;
         }
-        if (s.starts && !s.ends) {
-          // the first of an item's blocks says what there is to join
-          split_out = true;
-          if (member == 0 && r == 0 && row == 0) {
-            const int parts = (int)((sc.item1 * sc.N - 1) / sc.U) - gang + 1;
-            split[0] = make_int4(parts, s.b, s.kvh, s.pos0);
-            split[1] = make_int4(s.row0, a.cu_q ? s.n : a.n_new, 0, 0);
+        mbar_arrive(b_pb + 8 * buf);
+        float s0, s1, s2, s3;
+        f2_unpack(sum[0], s0, s1);
+        f2_unpack(sum[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+      }
+      if (!ok) break;
+      const bool whole = s.starts && s.ends, none = s.kt0 >= s.kt1;
+      if (!none) {
+        if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
+      const float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
+      const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
+      // rows 8 (lane / 8) + i are this lane's to store, 16 bytes at piece lane % 8
+      float *pp = t.part + ((size_t)(slot * NT + r) * 128 + (w & 3) * 32 + (lane & 24)) * C::PITCH + 4 * (lane & 7);
+      const long long own = valid ? (long long)tq * a.out_stride + (long long)hq * D + half * C::DV : -1;
+      long long at[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) at[i] = __shfl_sync(0xffffffffu, own, (lane & 24) + i);
+      bool nan = false;
+      constexpr int STEP = 32;
+#pragma unroll 1
+      for (int c = 0; c < C::DV; c += whole ? 2 * STEP : STEP) {
+        float x[64];
+        uint32_t y[32];
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 64; i++) x[i] = 0.0f;
+        } else {
+          tmem_ld32(oa + c, x);
+          if (whole) tmem_ld32(oa + c + STEP, x + 32);
+          tmem_wait_ld(x);
+          tmem_wait_ld(x + 32);
+        }
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i++) {
+            const float x0 = x[2 * i] * inv, x1 = x[2 * i + 1] * inv;
+            nan |= x0 != x0 || x1 != x1;
+            y[i] = Half16<DT>::down(x0, x1);
           }
+          transpose8(y);
+#pragma unroll
+          for (int i = 0; i < 8; i++)
+            if (at[i] >= 0)
+              *reinterpret_cast<uint4 *>(a.out + at[i] + c + 8 * (lane & 7)) =
+                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i++) y[i] = __float_as_uint(x[i]);
+          transpose8(y);
+#pragma unroll
+          for (int i = 0; i < 8; i++)
+            if (at[i] >= 0)
+              *reinterpret_cast<uint4 *>(pp + (size_t)i * C::PITCH + c) =
+                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
       }
-      if (!split_out && member == 0 && r == 0 && row == 0) split[0].x = 0;
-    } else if (member == 0 && r == 0 && row == 0) {
-      t.split[2 * gang].x = 0;
+      if (valid && !whole) {
+        float *ml = t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH + C::DV;
+        ml[0] = m, ml[1] = l;
+      }
+      tc_fence_before();
+      unsigned again = __ballot_sync(0xffffffffu, nan && valid);
+      while (again) {
+        const int x = __ffs(again) - 1;
+        again &= again - 1;
+        redo_row_cols<DT, D>(a, __shfl_sync(0xffffffffu, tq, x), __shfl_sync(0xffffffffu, hq, x), s.b,
+                             __shfl_sync(0xffffffffu, pos, x), half * C::DV, (half + 1) * C::DV);
+      }
     }
   }
   if (!ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
