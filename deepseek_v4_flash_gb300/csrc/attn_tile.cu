@@ -43,7 +43,8 @@ template <int DT>
 constexpr float AT_BIAS = DT == DS4MOE_DT_F16 ? 7.0f : 0.0f;
 
 constexpr int AT_CHUNK = 128 * 128;     // 128 rows of 64 elements, 128-byte swizzled
-constexpr int AT_SMEM = 225 * 1024;
+constexpr int AT_SMEM = 224 * 1024;     // Q and the ring
+constexpr int AT_MISC = 3 * 1024;       // what precedes them: barriers, segments, exchanged values
 constexpr int AT_SEGS = 4;              // segments the scheduling warp is ahead
 
 template <int D, int NT>
@@ -56,8 +57,9 @@ struct TileCfg {
   static constexpr int Q = NT * (D / 64) * AT_CHUNK;
   static constexpr int NST_ = (AT_SMEM - Q) / STAGE;
   static constexpr int NST = NST_ > 10 ? 10 : NST_;
-  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr int THREADS = 128 + 256 * NT;
   static constexpr int PITCH = DV + 4;                 // floats of a partial's row: O, m, l
+  static constexpr int JROWS = 1024 / DV;              // rows of a joining block
   static constexpr int O_COL = 256;                    // O's first tensor-memory column (S: 0 and 128)
 };
 
@@ -434,43 +436,58 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[32]) {
 }
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(128 + 128 * NT, 1)
+__global__ void __launch_bounds__(128 + 256 * NT, 1)
     k_attn_tile(const __grid_constant__ TileMaps maps, const AttnArgs a, const TileArgs t) {
   using C = TileCfg<D, NT>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) Seg segs[AT_SEGS];
-  __shared__ __align__(8) uint64_t bars[2 * 12 + 2 * AT_SEGS + 13];
-  __shared__ uint32_t s_tmem;
+  // One window of dynamic shared memory, exactly what an SM has: a TMA tile
+  // in the 128-byte swizzle starts on a multiple of 1024 bytes.
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  struct Misc {
+    uint64_t bars[2 * 12 + 2 * AT_SEGS + 13 + 8];
+    Seg segs[AT_SEGS];
+    uint32_t tmem;
+    // what the two threads of a row tell each other. Two row tiles: a row's S
+    // follows both threads' P, so the next value cannot overtake the last.
+    // One row tile: S runs ahead, two slots.
+    float x[2][2][128];
+  };
+  static_assert(sizeof(Misc) <= AT_MISC && C::Q + C::NST * C::STAGE <= AT_SMEM, "shared memory");
+  Misc &ms = *reinterpret_cast<Misc *>(smem_raw);
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t base = smem_u32(smem_raw) + AT_MISC;
   const uint32_t q_sm = base, ring = base + C::Q;
-  const uint32_t bar0 = smem_u32(bars);
+  const uint32_t bar0 = smem_u32(ms.bars);
   auto full = [&](int i) { return bar0 + 8 * i; };
   auto empty = [&](int i) { return bar0 + 8 * (12 + i); };
   auto seg_full = [&](int i) { return bar0 + 8 * (24 + i); };
   auto seg_empty = [&](int i) { return bar0 + 8 * (24 + AT_SEGS + i); };
   const uint32_t b_qf = bar0 + 8 * (24 + 2 * AT_SEGS), b_qe = b_qf + 16, b_sf = b_qe + 16, b_pa = b_sf + 16,
-                 b_pb = b_pa + 16, b_of = b_pb + 16, b_done = b_of + 16;
+                 b_pb = b_pa + 16, b_of = b_pb + 16, b_done = b_of + 16, b_x = b_done + 8;
+  if (base & 1023) {  // not where the swizzle needs it
+    if (tid == 0) raise_flag(a.err, DS4MOE_DEVERR_INTERNAL);
+    return;
+  }
   if (w == 0) {
     if (lane == 0) {
       for (int i = 0; i < C::NST; i++) mbar_init(full(i), 1), mbar_init(empty(i), 1);
-      for (int i = 0; i < AT_SEGS; i++) mbar_init(seg_full(i), 1), mbar_init(seg_empty(i), 2 + 4 * NT);
+      for (int i = 0; i < AT_SEGS; i++) mbar_init(seg_full(i), 1), mbar_init(seg_empty(i), 2 + 8 * NT);
       for (int i = 0; i < 2; i++) {
         mbar_init(b_qf + 8 * i, 1), mbar_init(b_qe + 8 * i, 1), mbar_init(b_sf + 8 * i, 1);
         mbar_init(b_pa + 8 * i, 128), mbar_init(b_pb + 8 * i, 128), mbar_init(b_of + 8 * i, 1);
       }
       mbar_init(b_done, 1);
+      for (int i = 0; i < 8; i++) mbar_init(b_x + 8 * i, 2);
       fence_mbar_init();
       fence_proxy_async_smem();
     }
     __syncwarp();
   } else if (w == 1) {
-    tmem_alloc(smem_u32(&s_tmem), 512);
+    tmem_alloc(smem_u32(&ms.tmem), 512);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = ms.tmem;
   pdl_launch_dependents();
   pdl_wait();
 
@@ -484,7 +501,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   auto next_seg = [&](Seg &s) {
     const int i = seg_n % AT_SEGS;
     if (!wait_warp(seg_full(i), (seg_n / AT_SEGS) & 1)) return ok = false;
-    s = segs[i];
+    s = ms.segs[i];
     __syncwarp();
     if (lane == 0) mbar_arrive(seg_empty(i));
     seg_n++;
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       const int i = seg_n % AT_SEGS;
       if (seg_n >= AT_SEGS && !wait_warp(seg_empty(i), (seg_n / AT_SEGS - 1) & 1)) ok = false;
       if (lane == 0) {
-        segs[i] = s;
+        ms.segs[i] = s;
         mbar_arrive(seg_full(i));
         if (more && s.starts && !s.ends && member == 0) {
           // the first of an item's blocks says what k_attn_join adds up
@@ -659,9 +676,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           __syncwarp();
         }
       }
-      // P comes in two halves of 64 columns
+      // P comes in two halves of 64 columns, from two warpgroups. An item's
+      // first product overwrites the O that both have been reading.
 #pragma unroll
       for (int h = 0; h < 2; h++) {
+        if (ok && kt == s.kt0 && h == 0 && !wait_warp(b_pb + 8 * buf, use & 1)) ok = false;
         if (ok && !wait_warp((h ? b_pb : b_pa) + 8 * buf, use & 1)) ok = false;
         tc_fence_after();
         if (ok && elect_one()) {
@@ -694,14 +713,34 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     __syncwarp();
     mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
   } else if (w >= 4) {
-    // ---- softmax and output: one warpgroup per row tile, one thread per row
-    const int r = NT == 2 ? (w >> 2) - 1 : 0;
+    // ---- softmax and output: two warpgroups per row tile. A row belongs to
+    // two threads, which take 64 columns of a tile each and agree on its
+    // maximum through shared memory: half the latency between S and P, which
+    // is what a row tile's products wait for.
+    const int sw = w - 4, ch = sw >> 2 & 1, r = sw >> 3;
     const int row = (w & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((w & 3) * 32) << 16;
     const int tok = row / a.group, head = row - tok * a.group;  // within the tile and the key-value head
     const int my_tok = tok < t.tpt ? r * t.tpt + tok : INT32_MAX;
     const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
+    const uint32_t b_pair = b_x + 8 * (r * 4 + (w & 3));
     int steps = 0;  // key tiles of this row tile so far
+    int swaps = 0;  // values exchanged with the row's other thread
+    auto meet = [&]() {  // with the warp that has the rows' other columns
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_pair);
+      if (!wait_warp(b_pair, swaps & 1)) return ok = false;
+      swaps++;
+      return true;
+    };
+    // the other thread's value; false when it does not come
+    auto swap = [&](float mine, float &other) {
+      float *x = &ms.x[NT == 2 ? r : swaps & 1][0][0];
+      x[ch * 128 + row] = mine;
+      if (!meet()) return false;
+      other = x[(ch ^ 1) * 128 + row];
+      return true;
+    };
     Seg s;
     while (ok && next_seg(s)) {
       const bool valid = my_tok < s.n;
@@ -713,54 +752,52 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       float m = -INFINITY, l = 0.0f;
       for (int kt = s.kt0; kt < s.kt1; kt++, steps++) {
         const int buf = NT == 2 ? r : steps & 1, use = NT == 2 ? steps : steps >> 1;
-        const int nch = (cols16(s, kt, t.gsh) + 1) >> 1;  // 32-column pieces with something to see
         if (!wait_warp(b_sf + 8 * buf, use & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t sa = tmem + lanes + buf * 128;
-        float v[128];
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-          if (c < nch) {
-            tmem_ld32(sa + 32 * c, v + 32 * c);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i++) v[32 * c + i] = -INFINITY;
-          }
-#pragma unroll
-        for (int c = 0; c < 4; c++) tmem_wait_ld(v + 32 * c);
+        float v[64];
+        tmem_ld32(sa + 64 * ch, v);
+        tmem_ld32(sa + 64 * ch + 32, v + 32);
         // columns c < cs: the first positions' groups, position 128 kt + c; others shifted
         const int cs = (s.gr.n_sink << t.gsh) - 128 * kt, off = 128 * kt + shift;
-        if (cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last)) {
+        const bool partly = cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last);
+        tmem_wait_ld(v);
+        tmem_wait_ld(v + 32);
+        if (partly) {
           const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs);
 #pragma unroll
-          for (int c = 0; c < 4; c++)
-            if (c < nch) {
-              const uint32_t bits =
-                  range_bits(0, e0, c) |
-                  ((range_bits(lo - off, pos + 1 - off, c) | range_bits(0, min(a.n_sink, pos + 1) - off, c)) &
-                   range_bits(cs, 128, c));
+          for (int c = 0; c < 2; c++) {
+            const int wd = 2 * ch + c;
+            const uint32_t bits =
+                range_bits(0, e0, wd) |
+                ((range_bits(lo - off, pos + 1 - off, wd) | range_bits(0, min(a.n_sink, pos + 1) - off, wd)) &
+                 range_bits(cs, 128, wd));
 #pragma unroll
-              for (int i = 0; i < 32; i++)
-                if (!(bits >> i & 1)) v[32 * c + i] = -INFINITY;
-            }
+            for (int i = 0; i < 32; i++)
+              if (!(bits >> i & 1)) v[32 * c + i] = -INFINITY;
+          }
         }
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int i = 4; i < 124; i += 8) {
+        for (int i = 4; i < 60; i += 8) {
           mx[0] = max3(mx[0], v[i], v[i + 1]), mx[1] = max3(mx[1], v[i + 2], v[i + 3]);
           mx[2] = max3(mx[2], v[i + 4], v[i + 5]), mx[3] = max3(mx[3], v[i + 6], v[i + 7]);
         }
-        mx[0] = max3(mx[0], v[124], v[125]), mx[1] = max3(mx[1], v[126], v[127]);
-        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2 - AT_BIAS<DT>;
+        mx[0] = max3(mx[0], v[60], v[61]), mx[1] = max3(mx[1], v[62], v[63]);
+        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), other;
+        if (!swap(mt, other)) break;
+        mt = fmaxf(mt, other) * a.scale_log2 - AT_BIAS<DT>;
         const bool grow = mt > m + AT_LAZY || (m == -INFINITY && mt > m);
         if (__any_sync(0xffffffffu, grow)) {
           const float mn = grow ? mt : m;
           const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
           m = mn, l *= f;
-          if (kt > s.kt0) {
+          // O is the first warpgroup's to rescale: products start when its
+          // half of P is there
+          if (kt > s.kt0 && ch == 0) {
             // the last product into O has to be done
             if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
               ok = false;
@@ -784,31 +821,22 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
             tmem_wait_st();
           }
         }
-        const float ms = m == -INFINITY ? 0.0f : m;
-        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-ms, -ms);
+        const float mz = m == -INFINITY ? 0.0f : m;
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-mz, -mz);
         unsigned long long sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          if (c < nch) {
-            uint32_t p[16];
+        for (int c = 0; c < 2; c++) {
+          uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-              float x, y;
-              f2_unpack(f2_fma(f2_pack(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nm2), x, y);
-              x = ex2(x), y = ex2(y);
-              sum[i & 1] = f2_add(sum[i & 1], f2_pack(x, y));
-              p[i] = Half16<DT>::down(x, y);
-            }
-            tmem_st16(sa + 16 * c, p);
+          for (int i = 0; i < 16; i++) {
+            float x, y;
+            f2_unpack(f2_fma(f2_pack(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nm2), x, y);
+            x = ex2(x), y = ex2(y);
+            sum[i & 1] = f2_add(sum[i & 1], f2_pack(x, y));
+            p[i] = Half16<DT>::down(x, y);
           }
-          if (c == 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(b_pa + 8 * buf);
-          }
+          tmem_st16(sa + 32 * ch + 16 * c, p);
         }
-        tmem_wait_st();
-        tc_fence_before();
         // Every product into O is waited for before the next one can end: a
         // parity tells only neighbouring phases apart. (It has ended long
         // since, in general.)
@@ -816,7 +844,9 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           ok = false;
           break;
         }
-        mbar_arrive(b_pb + 8 * buf);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive((ch ? b_pb : b_pa) + 8 * buf);
         float s0, s1, s2, s3;
         f2_unpack(sum[0], s0, s1);
         f2_unpack(sum[1], s2, s3);
@@ -830,56 +860,64 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           break;
         }
         tc_fence_after();
+        float other;
+        if (!swap(l, other) || !meet()) break;  // both have read l when the next item writes
+        l += other;
       }
       const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
       const float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
       const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
+      // each warpgroup stores half of O's columns (64: the first all of them)
+      const int c0 = C::DV == 64 ? 0 : ch * (C::DV / 2), c1 = C::DV == 64 ? (ch ? 0 : 64) : c0 + C::DV / 2;
       // rows 8 (lane / 8) + i are this lane's to store, 16 bytes at piece lane % 8
       float *pp = t.part + ((size_t)(slot * NT + r) * 128 + (w & 3) * 32 + (lane & 24)) * C::PITCH + 4 * (lane & 7);
       const long long own = valid ? (long long)tq * a.out_stride + (long long)hq * D + half * C::DV : -1;
-      long long at[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) at[i] = __shfl_sync(0xffffffffu, own, (lane & 24) + i);
       bool nan = false;
-      constexpr int STEP = 32;
 #pragma unroll 1
-      for (int c = 0; c < C::DV; c += whole ? 2 * STEP : STEP) {
-        float x[64];
+      for (int c = c0; c < c1; c += whole ? 64 : 32) {
+        float x[32];
         uint32_t y[32];
-        if (none) {
-#pragma unroll
-          for (int i = 0; i < 64; i++) x[i] = 0.0f;
-        } else {
-          tmem_ld32(oa + c, x);
-          if (whole) tmem_ld32(oa + c + STEP, x + 32);
-          tmem_wait_ld(x);
-          tmem_wait_ld(x + 32);
-        }
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; i++) {
-            const float x0 = x[2 * i] * inv, x1 = x[2 * i + 1] * inv;
-            nan |= x0 != x0 || x1 != x1;
-            y[i] = Half16<DT>::down(x0, x1);
+          for (int h = 0; h < 2; h++) {
+            if (none) {
+#pragma unroll
+              for (int i = 0; i < 32; i++) x[i] = 0.0f;
+            } else {
+              tmem_ld32(oa + c + 32 * h, x);
+              tmem_wait_ld(x);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              const float x0 = x[2 * i] * inv, x1 = x[2 * i + 1] * inv;
+              nan |= x0 != x0 || x1 != x1;
+              y[16 * h + i] = Half16<DT>::down(x0, x1);
+            }
           }
           transpose8(y);
 #pragma unroll
-          for (int i = 0; i < 8; i++)
-            if (at[i] >= 0)
-              *reinterpret_cast<uint4 *>(a.out + at[i] + c + 8 * (lane & 7)) =
+          for (int i = 0; i < 8; i++) {
+            const long long at = __shfl_sync(0xffffffffu, own, (lane & 24) + i);
+            if (at >= 0)
+              *reinterpret_cast<uint4 *>(a.out + at + c + 8 * (lane & 7)) =
                   make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
         } else {
+          tmem_ld32(oa + c, x);
+          tmem_wait_ld(x);
 #pragma unroll
           for (int i = 0; i < 32; i++) y[i] = __float_as_uint(x[i]);
           transpose8(y);
 #pragma unroll
-          for (int i = 0; i < 8; i++)
-            if (at[i] >= 0)
+          for (int i = 0; i < 8; i++) {
+            const int live = __shfl_sync(0xffffffffu, (int)valid, (lane & 24) + i);
+            if (live)
               *reinterpret_cast<uint4 *>(pp + (size_t)i * C::PITCH + c) =
                   make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
         }
       }
-      if (valid && !whole) {
+      if (valid && !whole && ch == 0) {
         float *ml = t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH + C::DV;
         ml[0] = m, ml[1] = l;
       }
@@ -889,7 +927,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         const int x = __ffs(again) - 1;
         again &= again - 1;
         redo_row_cols<DT, D>(a, __shfl_sync(0xffffffffu, tq, x), __shfl_sync(0xffffffffu, hq, x), s.b,
-                             __shfl_sync(0xffffffffu, pos, x), half * C::DV, (half + 1) * C::DV);
+                             __shfl_sync(0xffffffffu, pos, x), half * C::DV + c0, half * C::DV + c1);
       }
     }
   }
@@ -903,44 +941,62 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 }
 
 // Adds up the partials of the row groups whose key tiles lie in several
-// blocks' runs, in block order. Block (gang, member, row tile, 16 rows).
-constexpr int AJ_ROWS = 16, AJ_THREADS = 128;
+// blocks' runs, in block order. Block (gang, member, row tile, rows); a thread
+// takes four columns of one row, and the loads of four partials are in flight
+// together with their maxima.
+constexpr int AJ_THREADS = 256;
 
 template <int DT, int D, int NT>
 __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, const TileArgs t) {
   using C = TileCfg<D, NT>;
+  constexpr int ROWS = C::JROWS;
   __shared__ int s_nan;
   const int tid = threadIdx.x;
-  const int r0 = blockIdx.x % (128 / AJ_ROWS) * AJ_ROWS, r = blockIdx.x / (128 / AJ_ROWS) % NT;
-  const int bid = blockIdx.x / (128 / AJ_ROWS * NT);
+  const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
+  const int bid = blockIdx.x / (128 / ROWS * NT);
   const int gang = bid / t.members, member = bid % t.members, half = member % C::HALVES, rt = member / C::HALVES;
   pdl_launch_dependents();
   pdl_wait();
   const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
   const int parts = d0.x;
   if (parts == 0) return;
-  if (tid == 0) s_nan = 0;
-  __syncthreads();
   const int tok0 = (rt + r) * t.tpt;  // one of the two is 0
   const int rows = min(t.tpt, d1.y - tok0) * a.group;
-  for (int i = tid; i < AJ_ROWS * (C::DV / 4); i += AJ_THREADS) {
-    const int row = r0 + i / (C::DV / 4), c = i % (C::DV / 4) * 4;
-    if (row >= rows) break;
+  if (r0 >= rows) return;
+  if (tid == 0) s_nan = 0;
+  __syncthreads();
+  const int row = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
+  if (row < rows) {
+    // the block where the item starts holds it in its second slot, the others in their first
     auto at = [&](int p) {
       const int slot = 2 * (bid + p * t.members) + (p == 0 ? 1 : 0);
       return t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH;
     };
     float m = -INFINITY, l = 0.0f;
-#pragma unroll 8
-    for (int p = 0; p < parts; p++) m = fmaxf(m, at(p)[C::DV]);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int p = 0; p < parts; p++) {
-      const float *q = at(p);
-      const float f = q[C::DV] == -INFINITY ? 0.0f : ex2(q[C::DV] - m);
-      const float4 y = *reinterpret_cast<const float4 *>(q + c);
-      l = fmaf(f, q[C::DV + 1], l);
-      x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
+    for (int p0 = 0; p0 < parts; p0 += 4) {
+      float2 ml[4];
+      float4 y[4];
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        ml[i] = make_float2(-INFINITY, 0.0f), y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p0 + i < parts) {
+          const float *q = at(p0 + i);
+          ml[i] = *reinterpret_cast<const float2 *>(q + C::DV), y[i] = *reinterpret_cast<const float4 *>(q + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) mn = fmaxf(mn, ml[i].x);
+      const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+      l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+      m = mn;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float g = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - mn);
+        l = fmaf(g, ml[i].y, l);
+        x.x = fmaf(g, y[i].x, x.x), x.y = fmaf(g, y[i].y, x.y), x.z = fmaf(g, y[i].z, x.z), x.w = fmaf(g, y[i].w, x.w);
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
@@ -951,10 +1007,10 @@ __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, cons
   }
   __syncthreads();
   const int again = s_nan;
-  for (int i = tid >> 5; i < AJ_ROWS; i += AJ_THREADS / 32)
+  for (int i = tid >> 5; i < ROWS; i += AJ_THREADS / 32)
     if (again >> i & 1) {
-      const int row = r0 + i, tok = tok0 + row / a.group;
-      redo_row_cols<DT, D>(a, d1.x + tok, d0.z * a.group + row % a.group, d0.y, d0.w + tok, half * C::DV,
+      const int rw = r0 + i, tok = tok0 + rw / a.group;
+      redo_row_cols<DT, D>(a, d1.x + tok, d0.z * a.group + rw % a.group, d0.y, d0.w + tok, half * C::DV,
                            (half + 1) * C::DV);
     }
 }
@@ -1004,7 +1060,7 @@ int box_shift(int page_size, int window) {
 
 struct TileFns {
   const void *tile, *join;
-  int nt, dv, halves, q, threads;
+  int nt, halves, jrows, threads;
 };
 
 template <int DT, int D, int NT>
@@ -1012,7 +1068,7 @@ TileFns fns() {
   using C = TileCfg<D, NT>;
   // a key tile's stages are freed one by one, a value tile's are all held at once
   static_assert(C::NST > C::VST && (NT == 1 || C::NST > 2 * C::KST) && C::NST <= 12, "ring");
-  return {(const void *)k_attn_tile<DT, D, NT>, (const void *)k_attn_join<DT, D, NT>, NT, C::DV, C::HALVES, C::Q,
+  return {(const void *)k_attn_tile<DT, D, NT>, (const void *)k_attn_join<DT, D, NT>, NT, C::HALVES, C::JROWS,
           C::THREADS};
 }
 
@@ -1027,7 +1083,7 @@ TileFns tile_fns(int dtype, int D, bool ragged) {
   return dtype == DS4MOE_DT_BF16 ? fns_of<DS4MOE_DT_BF16>(D, ragged) : fns_of<DS4MOE_DT_F16>(D, ragged);
 }
 
-constexpr int AT_DYN = AT_SMEM + 1024;  // alignment of the swizzled tiles
+constexpr int AT_DYN = AT_MISC + AT_SMEM;
 
 }  // namespace
 
@@ -1085,7 +1141,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   }
   if (e == cudaSuccess) {
     void *args[] = {(void *)&a, &t};
-    e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / AJ_ROWS)), dim3(AJ_THREADS), 0, s, args, true);
+    e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / f.jrows)), dim3(AJ_THREADS), 0, s, args, true);
     ++*launches;
   }
   return e;
