@@ -621,20 +621,27 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     int st = 0, qn = 0;
     int steps = 0;  // (key tile, row tile) pairs before the current segment
     const uint32_t id_o = idesc<DT>(C::SC * 64, true);
+    const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq = desc_sw128(q_sm, 0), dk = desc_sw128(ring, 0), dv = desc_sw128(ring, AT_CHUNK);
     int kst0 = 0, vst0 = 0;  // ring stages of the current key and value tile
     Seg s;
     auto wait_stage = [&](int i) {
       if (!wait_warp(full(i % C::NST), (i / C::NST) & 1)) ok = false;
     };
-    auto qk = [&](int i) {  // step i of the segment
-      const int kt = s.kt0 + i / NT, r = i % NT, buf = (steps + i) & 1;
+    // Operands of the products go through uniform(): the compiler then keeps
+    // descriptors in uniform registers. Without it every product waited for
+    // four moves into them, 80 cycles against the 32 to 64 of its execution.
+    auto uniform = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    // S of key tile kt and row tile r, the segment's i-th such step
+    auto qk = [&](int kt, int r, int i) {
+      const int buf = NT == 2 ? r : uniform((steps + i) & 1);
       if (i < NT && !wait_warp(b_qf + 8 * r, (qn - 1) & 1)) ok = false;
       if (r == 0) kst0 = st, st += C::KST;
-      const uint32_t id = idesc<DT>(16 * cols16(s, kt, t.gsh), false);
+      const uint32_t id = idesc<DT>(16 * uniform(cols16(s, kt, t.gsh)), false);
+      const uint32_t sd = tmem_u + buf * 128;
 #pragma unroll
       for (int j = 0; j < C::KST; j++) {
-        const int slot = (kst0 + j) % C::NST;
+        const int slot = uniform((kst0 + j) % C::NST);
         if (r == 0) wait_stage(kst0 + j);
         tc_fence_after();
         if (ok && elect_one()) {
@@ -644,8 +651,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
           for (int c = 0; c < C::SC; c++)
 #pragma unroll
             for (int k = 0; k < 4; k++)
-              umma_f16(tmem + buf * 128, qa + (c * AT_CHUNK >> 4) + 2 * k, kb + (c * AT_CHUNK >> 4) + 2 * k, id,
-                       (j | c | k) != 0);
+              umma_f16(sd, qa + (c * AT_CHUNK >> 4) + 2 * k, kb + (c * AT_CHUNK >> 4) + 2 * k, id, (j | c | k) != 0);
           if (r == NT - 1) umma_commit(empty(slot));
           if (j == C::KST - 1) {
             umma_commit(b_sf + 8 * buf);
@@ -655,9 +661,10 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         __syncwarp();
       }
     };
-    auto pv = [&](int i) {
-      const int kt = s.kt0 + i / NT, r = i % NT, buf = (steps + i) & 1, use = (steps + i) >> 1;
-      const int n16 = cols16(s, kt, t.gsh);
+    // O of row tile r from its P of key tile kt
+    auto pv = [&](int kt, int r, int i) {
+      const int buf = NT == 2 ? r : uniform((steps + i) & 1), use = (steps + i) >> 1;
+      const int n16 = uniform(cols16(s, kt, t.gsh)), later = uniform(kt != s.kt0);
       if (r == 0) {
         vst0 = st, st += C::VST;
         for (int j = 0; j < C::VST; j++) wait_stage(vst0 + j);
@@ -676,22 +683,29 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
           __syncwarp();
         }
       }
+      uint64_t vb[C::VST];
+      uint32_t eb[C::VST];
+#pragma unroll
+      for (int j = 0; j < C::VST; j++) {
+        const int slot = uniform((vst0 + j) % C::NST);
+        vb[j] = dv + (slot * C::STAGE >> 4), eb[j] = empty(slot);
+      }
+      const uint32_t o = tmem_u + C::O_COL + r * C::DV, pd = tmem_u + buf * 128;
       // P comes in two halves of 64 columns, from two warpgroups. An item's
       // first product overwrites the O that both have been reading.
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        if (ok && kt == s.kt0 && h == 0 && !wait_warp(b_pb + 8 * buf, use & 1)) ok = false;
+        if (ok && !later && h == 0 && !wait_warp(b_pb + 8 * buf, use & 1)) ok = false;
         if (ok && !wait_warp((h ? b_pb : b_pa) + 8 * buf, use & 1)) ok = false;
         tc_fence_after();
         if (ok && elect_one()) {
 #pragma unroll
           for (int j = 0; j < C::VST; j++) {
-            const uint64_t vb = dv + (((vst0 + j) % C::NST) * C::STAGE >> 4);
-            const uint32_t o = tmem + C::O_COL + r * C::DV + j * C::SC * 64;
 #pragma unroll
             for (int k = 4 * h; k < 4 * h + 4; k++)
-              if (k < n16) umma_f16_ts(o, tmem + buf * 128 + 8 * k, vb + (2048 * k >> 4), id_o, kt != s.kt0 || k != 0);
-            if (h == 1 && r == NT - 1) umma_commit(empty((vst0 + j) % C::NST));
+              if (k < n16)
+                umma_f16_ts(o + j * C::SC * 64, pd + 8 * k, vb[j] + (2048 * k >> 4), id_o, later || k != 0);
+            if (h == 1 && r == NT - 1) umma_commit(eb[j]);
           }
           if (h == 1) umma_commit(b_of + 8 * r);
         }
@@ -699,13 +713,21 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       }
     };
     while (ok && next_seg(s)) {
-      const int n = (s.kt1 - s.kt0) * NT;
-      if (n <= 0) continue;
+      if (s.kt0 >= s.kt1) continue;
       qn++;
-      qk(0);
-      for (int i = 0; i < n && ok; i++) {
-        if (i + 1 < n) qk(i + 1);
-        if (ok) pv(i);
+      const int n = (s.kt1 - s.kt0) * NT;
+      qk(s.kt0, 0, 0);
+      for (int kt = s.kt0, i = 0; kt < s.kt1 && ok; kt++, i += NT) {
+        // the next S before the current O
+        if (NT == 2) {
+          qk(kt, NT - 1, i + 1);
+          pv(kt, 0, i);
+          if (kt + 1 < s.kt1) qk(kt + 1, 0, i + 2);
+          pv(kt, NT - 1, i + 1);
+        } else {
+          if (kt + 1 < s.kt1) qk(kt + 1, 0, i + 1);
+          pv(kt, 0, i);
+        }
       }
       steps += n;
     }
