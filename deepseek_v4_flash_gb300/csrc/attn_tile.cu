@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
                 umma_f16_ts(o + j * C::SC * 64, pd + 8 * k, vb[j] + (2048 * k >> 4), id_o, later || k != 0);
             if (h == 1 && r == NT - 1) umma_commit(eb[j]);
           }
-          if (h == 1) umma_commit(b_of + 8 * r);
+          if (h == 1 && (NT == 1 || kt + 1 == s.kt1)) umma_commit(b_of + 8 * r);
         }
         __syncwarp();
       }
@@ -748,21 +748,28 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     const uint32_t b_pair = b_x + 8 * (r * 4 + (w & 3));
     int steps = 0;  // key tiles of this row tile so far
     int swaps = 0;  // values exchanged with the row's other thread
-    auto meet = [&]() {  // with the warp that has the rows' other columns
+    // a value for the row's other thread, and the other's
+    float *x_pair = &ms.x[0][0][0];
+    auto tell = [&](float mine) {
+      x_pair = &ms.x[NT == 2 ? r : swaps & 1][0][0];
+      x_pair[ch * 128 + row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_pair);
+    };
+    auto hear = [&](float &other) {
+      if (!wait_warp(b_pair, swaps & 1)) return ok = false;
+      swaps++;
+      other = x_pair[(ch ^ 1) * 128 + row];
+      return true;
+    };
+    auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(b_pair);
       if (!wait_warp(b_pair, swaps & 1)) return ok = false;
       swaps++;
       return true;
     };
-    // the other thread's value; false when it does not come
-    auto swap = [&](float mine, float &other) {
-      float *x = &ms.x[NT == 2 ? r : swaps & 1][0][0];
-      x[ch * 128 + row] = mine;
-      if (!meet()) return false;
-      other = x[(ch ^ 1) * 128 + row];
-      return true;
-    };
+    int items = 0;  // segments with tiles so far
     Seg s;
     while (ok && next_seg(s)) {
       const bool valid = my_tok < s.n;
@@ -786,22 +793,19 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         // columns c < cs: the first positions' groups, position 128 kt + c; others shifted
         const int cs = (s.gr.n_sink << t.gsh) - 128 * kt, off = 128 * kt + shift;
         const bool partly = cs > 0 || off + 127 > p_first || (a.window > 0 && off < lo_last);
+        auto hide = [&](float *x, int c) {  // what the row does not see of its 32 columns c
+          const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs), wd = 2 * ch + c;
+          const uint32_t bits =
+              range_bits(0, e0, wd) |
+              ((range_bits(lo - off, pos + 1 - off, wd) | range_bits(0, min(a.n_sink, pos + 1) - off, wd)) &
+               range_bits(cs, 128, wd));
+#pragma unroll
+          for (int i = 0; i < 32; i++)
+            if (!(bits >> i & 1)) x[i] = -INFINITY;
+        };
         tmem_wait_ld(v);
         tmem_wait_ld(v + 32);
-        if (partly) {
-          const int e0 = min(min(a.n_sink, pos + 1) - 128 * kt, cs);
-#pragma unroll
-          for (int c = 0; c < 2; c++) {
-            const int wd = 2 * ch + c;
-            const uint32_t bits =
-                range_bits(0, e0, wd) |
-                ((range_bits(lo - off, pos + 1 - off, wd) | range_bits(0, min(a.n_sink, pos + 1) - off, wd)) &
-                 range_bits(cs, 128, wd));
-#pragma unroll
-            for (int i = 0; i < 32; i++)
-              if (!(bits >> i & 1)) v[32 * c + i] = -INFINITY;
-          }
-        }
+        if (partly) hide(v, 0), hide(v + 32, 1);
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int i = 4; i < 60; i += 8) {
@@ -810,7 +814,26 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         }
         mx[0] = max3(mx[0], v[60], v[61]), mx[1] = max3(mx[1], v[62], v[63]);
         float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), other;
-        if (!swap(mt, other)) break;
+        tell(mt);
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2);
+        unsigned long long sum[2] = {0, 0};
+        uint32_t p[16];
+        auto weights = [&](const float *x) {  // of 32 columns, relative to m
+          const float mz = m == -INFINITY ? 0.0f : m;
+          const unsigned long long nm2 = f2_pack(-mz, -mz);
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, nm2), x0, x1);
+            x0 = ex2(x0), x1 = ex2(x1);
+            sum[i & 1] = f2_add(sum[i & 1], f2_pack(x0, x1));
+            p[i] = Half16<DT>::down(x0, x1);
+          }
+        };
+        // the first 32 columns' weights with the maximum so far, while the
+        // other thread's is on its way: it rarely changes
+        weights(v);
+        if (!hear(other)) break;
         mt = fmaxf(mt, other) * a.scale_log2 - AT_BIAS<DT>;
         const bool grow = mt > m + AT_LAZY || (m == -INFINITY && mt > m);
         if (__any_sync(0xffffffffu, grow)) {
@@ -820,8 +843,9 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
           // O is the first warpgroup's to rescale: products start when its
           // half of P is there
           if (kt > s.kt0 && ch == 0) {
-            // the last product into O has to be done
-            if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+            // the last product into O has to be done; with two row tiles it
+            // came before this S
+            if (NT == 1 && !wait_warp(b_of, (steps - 1) & 1)) {
               ok = false;
               break;
             }
@@ -842,27 +866,22 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
             }
             tmem_wait_st();
           }
+          // the first columns again (S is still there: P of these columns goes
+          // over it, the other thread's P over the second 32 at most)
+          float x[32];
+          tmem_ld32(sa + 64 * ch, x);
+          tmem_wait_ld(x);
+          if (partly) hide(x, 0);
+          sum[0] = sum[1] = 0;
+          weights(x);
         }
-        const float mz = m == -INFINITY ? 0.0f : m;
-        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-mz, -mz);
-        unsigned long long sum[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            float x, y;
-            f2_unpack(f2_fma(f2_pack(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), sc2, nm2), x, y);
-            x = ex2(x), y = ex2(y);
-            sum[i & 1] = f2_add(sum[i & 1], f2_pack(x, y));
-            p[i] = Half16<DT>::down(x, y);
-          }
-          tmem_st16(sa + 32 * ch + 16 * c, p);
-        }
-        // Every product into O is waited for before the next one can end: a
-        // parity tells only neighbouring phases apart. (It has ended long
-        // since, in general.)
-        if (kt > s.kt0 && !wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+        tmem_st16(sa + 32 * ch, p);
+        weights(v + 32);
+        tmem_st16(sa + 32 * ch + 16, p);
+        // One row tile: every product into O is waited for before the next one
+        // can end (a parity tells only neighbouring phases apart). It has
+        // ended long since, in general.
+        if (NT == 1 && kt > s.kt0 && !wait_warp(b_of, (steps - 1) & 1)) {
           ok = false;
           break;
         }
@@ -877,13 +896,16 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       if (!ok) break;
       const bool whole = s.starts && s.ends, none = s.kt0 >= s.kt1;
       if (!none) {
-        if (!wait_warp(b_of + 8 * r, (steps - 1) & 1)) {
+        // the item's last product (two row tiles: the only one this barrier counts)
+        if (!wait_warp(b_of + 8 * r, (NT == 1 ? steps - 1 : items) & 1)) {
           ok = false;
           break;
         }
+        items++;
         tc_fence_after();
         float other;
-        if (!swap(l, other) || !meet()) break;  // both have read l when the next item writes
+        tell(l);
+        if (!hear(other) || !meet()) break;  // both have read l when the next item writes
         l += other;
       }
       const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
@@ -1072,11 +1094,11 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, int n, const cuuint64_
 }
 
 // log2 of a group's positions: groups lie within pages, and a window of W
-// positions reads up to two groups too many, so at most W / 16 (small windows:
-// 16, one TMA box is then 2 KB per 64 elements).
+// positions reads up to two groups too many, so at most W / 4. (Issuing a box
+// costs the loading warp about as long as 2 KB take to arrive.)
 int box_shift(int page_size, int window) {
   int sh = 4;
-  while (sh < 7 && page_size % (32 << (sh - 4)) == 0 && (window == 0 || window / 16 >= 32 << (sh - 4))) sh++;
+  while (sh < 7 && page_size % (32 << (sh - 4)) == 0 && (window == 0 || window / 4 >= 32 << (sh - 4))) sh++;
   return sh;
 }
 
