@@ -495,6 +495,9 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
   const int half = member % C::HALVES, rt = member / C::HALVES;
   bool ok = true;  // no wait has run out
 
+  // Operands of copies and products go through uniform(): the compiler then
+  // keeps them in uniform registers, where these instructions want them.
+  auto uniform = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
   // The block's segments in order, from the scheduling warp; false after the
   // last one.
   int seg_n = 0;
@@ -562,21 +565,22 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       const int ng = min(gpt, s.gr.n - kt * gpt);
       int page = pl.page;
       if (page < 0 || page >= a.kv.n_pages) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
+      const int kvh = uniform(s.kvh), n_box = uniform(ng);
       for (int i = 0; i < nst && ok; i++) {
-        const int slot = st % C::NST;
+        const int slot = uniform(st % C::NST);
         if (st >= C::NST && !wait_warp(empty(slot), (st / C::NST - 1) & 1)) {
           ok = false;
           break;
         }
         const uint32_t dst = ring + slot * C::STAGE, bar = full(slot);
-        const int x = (chunk0 + i * C::SC) * 64;
-        if (elect_one()) mbar_arrive_expect_tx(bar, (C::SC * 128u << t.gsh) * ng);
-        for (int g = 0; g < ng; g++) {
+        const int x = uniform((chunk0 + i * C::SC) * 64);
+        if (elect_one()) mbar_arrive_expect_tx(bar, (C::SC * 128u << t.gsh) * n_box);
+        for (int g = 0; g < n_box; g++) {
           const int pg = __shfl_sync(0xffffffffu, page, g), row = __shfl_sync(0xffffffffu, pl.row, g);
+          const uint32_t to = dst + (g << (t.gsh + 7));
           if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < C::SC; c++)
-              tma_4d(dst + c * AT_CHUNK + (g << (t.gsh + 7)), m, x + c * 64, row, s.kvh, pg, bar);
+            for (int c = 0; c < C::SC; c++) tma_4d(to + c * AT_CHUNK, m, x + c * 64, row, kvh, pg, bar);
           }
         }
         st++;
@@ -588,12 +592,12 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       Place kp = lookup(s, s.kt0);
       for (int r = 0; r < NT && ok; r++) {
         if (qn > 0 && !wait_warp(b_qe + 8 * r, (qn - 1) & 1)) ok = false;
+        const int qh = uniform(s.kvh * a.group), qt = uniform(s.row0 + r * t.tpt);
         if (ok && elect_one()) {
           mbar_arrive_expect_tx(b_qf + 8 * r, (D / 64) * t.tpt * a.group * 128);
           // rows past the call's last come in as zeros
 #pragma unroll
-          for (int c = 0; c < D / 64; c++)
-            tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, s.kvh * a.group, s.row0 + r * t.tpt, b_qf + 8 * r);
+          for (int c = 0; c < D / 64; c++) tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, qh, qt, b_qf + 8 * r);
         }
         __syncwarp();
       }
@@ -628,10 +632,6 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     auto wait_stage = [&](int i) {
       if (!wait_warp(full(i % C::NST), (i / C::NST) & 1)) ok = false;
     };
-    // Operands of the products go through uniform(): the compiler then keeps
-    // descriptors in uniform registers. Without it every product waited for
-    // four moves into them, 80 cycles against the 32 to 64 of its execution.
-    auto uniform = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     // S of key tile kt and row tile r, the segment's i-th such step
     auto qk = [&](int kt, int r, int i) {
       const int buf = NT == 2 ? r : uniform((steps + i) & 1);
