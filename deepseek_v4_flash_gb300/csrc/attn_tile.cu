@@ -45,6 +45,11 @@ constexpr float AT_BIAS = DT == DS4MOE_DT_F16 ? 7.0f : 0.0f;
 constexpr int AT_CHUNK = 128 * 128;     // 128 rows of 64 elements, 128-byte swizzled
 constexpr int AT_SMEM = 224 * 1024;     // Q and the ring
 constexpr int AT_MISC = 3 * 1024;       // what precedes them: barriers, segments, exchanged values
+// What an item costs beside its tiles (loading Q, filling the pipeline,
+// writing O), in tiles: counted into the runs, or a block with a prompt's first
+// row groups, of one or two tiles each, would have three times the items of
+// the others.
+constexpr int AT_ITEM = 2;
 constexpr int AT_SEGS = 4;              // segments the scheduling warp is ahead
 
 template <int D, int NT>
@@ -190,7 +195,9 @@ __device__ __forceinline__ int cols16(const Seg &s, int kt, int sh) {
 }
 
 struct Sched {
-  long long u, u1, item0, item1;  // next tile, end of the run, the current item's tiles
+  // In units of a tile, AT_ITEM of them before each item's first tile: where
+  // the run stands, its end, the current item.
+  long long u, u1, item0, item1;
   int b, kvh, idx, n_idx;
   long long row_units;
   long long U, N;                 // the call's tiles, the gangs that have some
@@ -222,7 +229,7 @@ struct Sched {
   __device__ __forceinline__ int uni_units(const AttnArgs &a, int gsh, int bb) const {
     bool bad = false;
     const SeqInfo si = seq_info(a, bb, bad);
-    return max(1, tiles_of(range_groups(a, si.len - si.n, si.len - 1, gsh), gsh));
+    return AT_ITEM + max(1, tiles_of(range_groups(a, si.len - si.n, si.len - 1, gsh), gsh));
   }
 
   // Whole warp. False when gang g has no tiles.
@@ -279,15 +286,16 @@ struct Sched {
         r -= __shfl_sync(0xffffffffu, incl, 31);
       }
     }
+    if (u - item0 <= AT_ITEM) u = item0;  // before the item's first tile: all of it
     return true;
   }
 
   __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, int nt, Seg &s) {
-    if (u >= u1) return false;
+    if (u >= u1 || (u1 < item1 && u1 - item0 <= AT_ITEM)) return false;  // (the next gang's from its start)
     const int n_kt = load(a, t, member_rt, nt, s);
     const long long e = item1 < u1 ? item1 : u1;
     s.starts = u == item0, s.ends = e == item1;
-    s.kt0 = (int)(u - item0), s.kt1 = min(n_kt, (int)(e - item0));
+    s.kt0 = max(0, (int)(u - item0) - AT_ITEM), s.kt1 = min(n_kt, (int)(e - item0) - AT_ITEM);
     u = e;
     if (u == item1 && u < u1) {
       // the next item
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, 
       bool unused = false;
       const SeqInfo si = seq_info(a, b, unused);
       const int p0 = si.len - si.n + t0;
-      units = max(1, tiles_of(range_groups(a, p0, p0 + min(span, si.n - t0) - 1, gsh), gsh));
+      units = AT_ITEM + max(1, tiles_of(range_groups(a, p0, p0 + min(span, si.n - t0) - 1, gsh), gsh));
     }
     const long long x = scan(units);
     if (i < total) first[i] = x, info[i] = make_int2(b, t0);
