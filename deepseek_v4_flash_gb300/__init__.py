@@ -566,6 +566,7 @@ def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_acc
     fp32 [n_seq, max_draft, vocab] or None, tokens int32 [n_seq, max_draft].
     Returns (n_accepted int32 [n_seq], tokens_out int32 [n_seq, max_draft + 1])."""
     import torch
+    lib()
     i32, f32 = torch.int32, torch.float32
     if target.dim() != 3:
         raise ValueError("target: [n_seq, max_draft + 1, vocab]")
@@ -577,14 +578,17 @@ def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_acc
             raise ValueError("draft: [n_seq, max_draft, vocab]")
         ds = _rows(draft, "draft", f32, (V,), V)
     if n_accepted is None:
-        n_accepted = _fresh(torch.empty(B, dtype=i32, device=target.device), stream)
+        n_accepted = _fresh(target.new_empty(B, dtype=i32), stream)
+    else:
+        _vec(n_accepted, "n_accepted", i32, B)
     if tokens_out is None:
-        tokens_out = _fresh(torch.empty((B, G + 1), dtype=i32, device=target.device), stream)
-    _check(lib().ds4moe_verify_drafts(
+        tokens_out = _fresh(target.new_empty((B, G + 1), dtype=i32), stream)
+    else:
+        _vec(tokens_out, "tokens_out", i32, B * (G + 1))
+    _check(_lib.ds4moe_verify_drafts(
         target.data_ptr(), ts, None if draft is None else draft.data_ptr(), ds, _vec(tokens, "tokens", i32, B * G),
         None if n_draft is None else _vec(n_draft, "n_draft", i32, B), _vec(u_accept, "u_accept", f32, B * G),
-        _vec(u_sample, "u_sample", f32, B), B, G, V, _vec(n_accepted, "n_accepted", i32, B),
-        _vec(tokens_out, "tokens_out", i32, B * (G + 1)),
+        _vec(u_sample, "u_sample", f32, B), B, G, V, n_accepted.data_ptr(), tokens_out.data_ptr(),
         None if err_flags is None else _vec(err_flags, "err_flags", i32, 1), _stream(stream)), "ds4moe_verify_drafts")
     return n_accepted, tokens_out
 

@@ -48,11 +48,21 @@ __device__ __forceinline__ void arg_max(float &v, int &i, float w, int j) {
   if (w > v || (w == v && j < i)) v = w, i = j;
 }
 
-// d / T from 1 / T with one correction step: (x - max) / T reaches -40 and
-// more, where the rounding of 1 / T alone would show in the exponential.
-__device__ __forceinline__ float over_t(float d, float t, float inv_t) {
-  const float z = d * inv_t;
-  return isfinite(z) ? fmaf(fmaf(-z, t, d), inv_t, z) : z;
+// exp(d / T) for d <= 0 as 2^(d c), c = log2(e) / T given as hi + lo: the
+// product's rounding and lo come back as a first-order factor, for d c reaches
+// -60 and more, where they would show in a 32-bit exponential. Eight
+// instructions (a division and expf took 25, and the kernel was bound by
+// them). d is kept above dmin = -200 / c, where the result is 0, so that
+// -infinity gives 0 and not infinity less infinity; a NaN stays one.
+struct ExpScale {
+  float hi, lo, dmin, t;
+};
+__device__ __forceinline__ float exp_over_t(float d, const ExpScale &c) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(c.dmin));
+  const float x = __fmul_rn(d, c.hi), err = __fmaf_rn(d, c.lo, __fmaf_rn(d, c.hi, -x));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return __fmaf_rn(e, err * 0.693147180559945f, e);
 }
 
 // Entries i .. i + 3 of a row (those below end; `fill` elsewhere).
@@ -80,12 +90,12 @@ __device__ __forceinline__ void put4(float *o, int i, int end, float4 v) {
 // relative to its own maximum, and one exchange of (maximum, sum) between the
 // blocks gives the factor that turns them into probabilities.
 // T = 0: 1 at the lowest index of the maximum, 0 elsewhere.
-constexpr int SP_KEEP = 8;
+constexpr int SP_KEEP = 8, PR_THREADS = 512, PR_WARPS = PR_THREADS / 32;
 template <bool VEC>
-__global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, long long xs, int V, float t, float inv_t,
+__global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, long long xs, int V, ExpScale c,
                                                            float *out, long long os) {
-  __shared__ float sv[SP_WARPS], ss[SP_WARPS];
-  __shared__ int si[SP_WARPS];
+  __shared__ float sv[PR_WARPS], ss[PR_WARPS];
+  __shared__ int si[PR_WARPS];
   __shared__ float pub[3];  // this block's maximum, sum, index of the maximum
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int rank = cluster_rank(), n_blk = cluster_size();
@@ -98,20 +108,20 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, l
   const int begin = min(V, rank * part), end = min(V, begin + part);
   float4 v[SP_KEEP];
 #pragma unroll
-  for (int k = 0; k < SP_KEEP; k++) v[k] = row4<VEC>(r, begin + 4 * (tid + k * SP_THREADS), end, -INFINITY);
-  const int rest = begin + 4 * (tid + SP_KEEP * SP_THREADS);
+  for (int k = 0; k < SP_KEEP; k++) v[k] = row4<VEC>(r, begin + 4 * (tid + k * PR_THREADS), end, -INFINITY);
+  const int rest = begin + 4 * (tid + SP_KEEP * PR_THREADS);
   float m = -INFINITY;
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) m = fmaxf(fmaxf(fmaxf(m, v[k].x), fmaxf(v[k].y, v[k].z)), v[k].w);
-  for (int i = rest; i < end; i += 4 * SP_THREADS) {
+  for (int i = rest; i < end; i += 4 * PR_THREADS) {
     const float4 y = row4<VEC>(r, i, end, -INFINITY);
     m = fmaxf(fmaxf(fmaxf(m, y.x), fmaxf(y.y, y.z)), y.w);
   }
   m = warp_max(m);
   if (lane == 0) sv[w] = m;
   __syncthreads();
-  m = warp_max(sv[lane & (SP_WARPS - 1)]);
-  if (inv_t == 0.0f) {
+  m = warp_max(sv[lane & (PR_WARPS - 1)]);
+  if (c.t == 0.0f) {
     // the lowest index that holds the maximum, and whether there is a NaN
     int at = V;
     bool nan = false;
@@ -121,10 +131,10 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, l
     };
 #pragma unroll
     for (int k = 0; k < SP_KEEP; k++) {
-      const int i = begin + 4 * (tid + k * SP_THREADS);
+      const int i = begin + 4 * (tid + k * PR_THREADS);
       look(v[k].x, i), look(v[k].y, i + 1), look(v[k].z, i + 2), look(v[k].w, i + 3);
     }
-    for (int i = rest; i < end; i += 4 * SP_THREADS) {
+    for (int i = rest; i < end; i += 4 * PR_THREADS) {
       const float4 y = row4<VEC>(r, i, end, -INFINITY);
       look(y.x, i), look(y.y, i + 1), look(y.z, i + 2), look(y.w, i + 3);
     }
@@ -132,7 +142,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, l
     if (lane == 0) si[w] = at;
     nan = __syncthreads_or(nan);
     if (tid == 0) {
-      for (int i = 0; i < SP_WARPS; i++) at = min(at, si[i]);
+      for (int i = 0; i < PR_WARPS; i++) at = min(at, si[i]);
       pub[0] = nan ? NAN : m, pub[2] = __int_as_float(at);
     }
     cluster_sync();
@@ -145,22 +155,22 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, l
     }
     cluster_sync();  // a block's shared memory outlives its readers
     const bool bad = best != best;
-    for (int i = begin + 4 * tid; i < end; i += 4 * SP_THREADS) {
+    for (int i = begin + 4 * tid; i < end; i += 4 * PR_THREADS) {
       const float one[2] = {bad ? NAN : 0.0f, bad ? NAN : 1.0f};
       put4<VEC>(o, i, end, make_float4(one[i == where], one[i + 1 == where], one[i + 2 == where], one[i + 3 == where]));
     }
     return;
   }
-  // a part of nothing but -infinity weighs nothing
-  const bool empty = m == -INFINITY;
-  auto e = [&](float a) { return empty ? (a == a ? 0.0f : a) : expf(over_t(a - m, t, inv_t)); };
+  // (a part of nothing but -infinity weighs nothing)
+  const float mz = m == -INFINITY ? 0.0f : m;
+  auto e = [&](float a) { return exp_over_t(a - mz, c); };
   float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) {
     v[k] = make_float4(e(v[k].x), e(v[k].y), e(v[k].z), e(v[k].w));
     sum += (v[k].x + v[k].y) + (v[k].z + v[k].w);
   }
-  for (int i = rest; i < end; i += 4 * SP_THREADS) {
+  for (int i = rest; i < end; i += 4 * PR_THREADS) {
     const float4 y = row4<VEC>(r, i, end, -INFINITY);
     sum += (e(y.x) + e(y.y)) + (e(y.z) + e(y.w));
   }
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, l
   if (lane == 0) ss[w] = sum;
   __syncthreads();
   if (w == 0) {
-    sum = lane < SP_WARPS ? ss[lane] : 0.0f;
+    sum = lane < PR_WARPS ? ss[lane] : 0.0f;
 #pragma unroll
     for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     if (lane == 0) pub[0] = m, pub[1] = sum;
@@ -184,16 +194,16 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_token_probs(const float *x, l
 #pragma unroll
   for (int b = 0; b < 8; b++) top = fmaxf(top, pm[b]);
 #pragma unroll
-  for (int b = 0; b < 8; b++) total += pm[b] == -INFINITY ? ps[b] : ps[b] * expf(over_t(pm[b] - top, t, inv_t));
+  for (int b = 0; b < 8; b++) total += pm[b] == -INFINITY ? ps[b] : ps[b] * exp_over_t(pm[b] - top, c);
   // barrier.cluster: a block's shared memory outlives its readers
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  const float f = (empty ? 0.0f : expf(over_t(m - top, t, inv_t))) / total;
+  const float f = (m == -INFINITY ? 0.0f : exp_over_t(m - top, c)) / total;
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) {
-    const int i = begin + 4 * (tid + k * SP_THREADS);
+    const int i = begin + 4 * (tid + k * PR_THREADS);
     put4<VEC>(o, i, end, make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f));
   }
-  for (int i = rest; i < end; i += 4 * SP_THREADS) {
+  for (int i = rest; i < end; i += 4 * PR_THREADS) {
     const float4 y = row4<VEC>(r, i, end, -INFINITY);
     put4<VEC>(o, i, end, make_float4(e(y.x) * f, e(y.y) * f, e(y.z) * f, e(y.w) * f));
   }
@@ -344,9 +354,11 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
       total += t;
     }
     for (int i = 0; i < w; i++) before += part[i];
-    cluster_sync();  // read by all before it is written again or the block leaves
+    // read by all before it is written again or the block leaves
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (total > 0 || (!q && dtok < 0)) break;
     q = nullptr, dtok = -1;  // nothing is left: draw from p itself
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   int32_t *out = a.tokens + (long long)b * (a.G + 1);
   if (total > 0) {
@@ -384,12 +396,14 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
     if (tid <= a.G && tid != n) out[tid] = tid < n ? a.tok[(long long)b * a.G + tid] : -1;
     if (tid == 0) a.n_accepted[b] = n;
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-static cudaError_t launch_rows(const void *fn, int rows, int cluster, cudaStream_t s, void **args) {
+static cudaError_t launch_rows(const void *fn, int rows, int cluster, int threads, cudaStream_t s, void **args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * cluster);
-  cfg.blockDim = dim3(SP_THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -430,17 +444,18 @@ using namespace ds4;
 ds4moe_status ds4moe_token_probs(const float *logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,
                                  float temperature, float *probs, int64_t probs_stride, void *stream) {
   if (n_rows < 0 || n_rows > (1 << 24) || vocab < 1 || vocab > (1 << 24)) return DS4MOE_ERR_INVALID_ARG;
-  if (!isfinite(temperature) || temperature < 0.0f || (temperature > 0.0f && !isfinite(1.0f / temperature)))
-    return DS4MOE_ERR_INVALID_ARG;
+  if (!(temperature == 0.0f || (temperature >= 1e-6f && temperature <= 1e6f))) return DS4MOE_ERR_INVALID_ARG;
   if (n_rows == 0) return DS4MOE_OK;
   if (n_rows > 1 && (logits_stride < vocab || probs_stride < vocab)) return DS4MOE_ERR_INVALID_ARG;
   if (!sp_dev_ptr(logits) || !sp_dev_ptr(probs)) return DS4MOE_ERR_INVALID_ARG;
-  float inv_t = temperature > 0.0f ? 1.0f / temperature : 0.0f;
+  const double scale = temperature > 0.0f ? 1.4426950408889634 / temperature : 0.0;  // log2(e) / T
+  ExpScale c = {(float)scale, (float)(scale - (float)scale), temperature > 0.0f ? (float)(-200.0 / scale) : 0.0f,
+                temperature};
   long long xs = logits_stride, os = probs_stride;
-  void *args[] = {(void *)&logits, &xs, &vocab, &temperature, &inv_t, (void *)&probs, &os};
+  void *args[] = {(void *)&logits, &xs, &vocab, &c, (void *)&probs, &os};
   const bool vec = (n_rows == 1 || (xs % 4 == 0 && os % 4 == 0)) && ((uintptr_t)logits & 15) == 0 && ((uintptr_t)probs & 15) == 0;
   return sp_status(launch_rows(vec ? (const void *)k_token_probs<true> : (const void *)k_token_probs<false>, n_rows,
-                               cluster_of(vocab), (cudaStream_t)stream, args));
+                               cluster_of(vocab), PR_THREADS, (cudaStream_t)stream, args));
 }
 
 ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
@@ -466,8 +481,15 @@ ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, c
   const bool vec = target_stride % 4 == 0 && ((uintptr_t)target & 15) == 0 &&
                    (!a.draft || (draft_stride % 4 == 0 && ((uintptr_t)draft & 15) == 0));
   void *args[] = {&a};
+  // Smaller clusters where a batch would not be resident at once (two blocks
+  // per SM): a second wave of short blocks costs as much as the first.
+  int dev = 0, n_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return sp_status(cudaErrorUnknown);
+  int cluster = cluster_of(vocab);
+  while (cluster > 1 && (long long)n_seq * cluster > 2 * n_sm) cluster /= 2;
   return sp_status(launch_rows(vec ? (const void *)k_verify_drafts<true> : (const void *)k_verify_drafts<false>, n_seq,
-                               cluster_of(vocab), (cudaStream_t)stream, args));
+                               cluster, SP_THREADS, (cudaStream_t)stream, args));
 }
 
 }  // extern "C"

@@ -464,7 +464,7 @@ uint64_t ds4moe_attn_launch_count(const ds4moe_attn *h);
  *
  * ds4moe_token_probs: probs[r] = softmax(logits[r] / temperature) over vocab
  *   (fp32, rows `stride` elements apart; probs may be logits itself with the
- *   same stride). temperature 0: 1 at the lowest index of the row's maximum, 0
+ *   same stride). temperature 1e-6 .. 1e6, or 0: 1 at the lowest index of the row's maximum, 0
  *   elsewhere. A NaN in a row, or a maximum of +-infinity (temperature > 0),
  *   gives NaN.
  * ds4moe_verify_drafts: which of a sequence's drafted tokens x_0, x_1, ... stay,
