@@ -578,11 +578,11 @@ def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_acc
             raise ValueError("draft: [n_seq, max_draft, vocab]")
         ds = _rows(draft, "draft", f32, (V,), V)
     if n_accepted is None:
-        n_accepted = _fresh(target.new_empty(B, dtype=i32), stream)
+        n_accepted = _fresh(torch.empty(B, dtype=i32, device=target.device), stream)
     else:
         _vec(n_accepted, "n_accepted", i32, B)
     if tokens_out is None:
-        tokens_out = _fresh(target.new_empty((B, G + 1), dtype=i32), stream)
+        tokens_out = _fresh(torch.empty((B, G + 1), dtype=i32, device=target.device), stream)
     else:
         _vec(tokens_out, "tokens_out", i32, B * (G + 1))
     _check(_lib.ds4moe_verify_drafts(
