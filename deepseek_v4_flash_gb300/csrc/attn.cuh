@@ -74,9 +74,15 @@ __device__ __forceinline__ int window_lo(const AttnArgs &a, int i) {
   return a.window > 0 && i >= a.window ? i - a.window + 1 : 0;
 }
 
+// pos / page_size, 0 <= pos < 2^31: with l = ceil(log2 page_size) and mul =
+// ceil(2^(31 + l) / page_size) < 2^32 the product's error pos * (mul - exact) is
+// below 2^31, less than a page_size-th of 2^(31 + l).
+__device__ __forceinline__ int page_index(const KvView &kv, int pos) {
+  return (int)(((unsigned long long)(uint32_t)pos * kv.div_mul) >> kv.div_sh);
+}
 // Page of a sequence's position, or -1 for a table entry outside the cache.
 __device__ __forceinline__ int page_of(const KvView &kv, int b, int pos) {
-  const int p = kv.table[(long long)b * kv.table_stride + pos / kv.page_size];
+  const int p = kv.table[(long long)b * kv.table_stride + page_index(kv, pos)];
   return p >= 0 && p < kv.n_pages ? p : -1;
 }
 
@@ -126,7 +132,7 @@ __device__ __forceinline__ void attn_row_warp(const AttnArgs &a, const uint16_t 
   for (int g = g0; g < g1; g++) {
     const int p0 = group_pos(gr, g);
     if (p0 > pos || (p0 + 15 < lo && p0 >= sink)) continue;
-    const int page = page_of(a.kv, b, p0), row0 = p0 % a.kv.page_size;
+    const int page = page_of(a.kv, b, p0), row0 = p0 - page_index(a.kv, p0) * a.kv.page_size;
     if (page < 0) bad_page = true;
     const uint16_t *kp = a.kv.k + (long long)max(page, 0) * a.kv.k_page + (long long)kvh * a.kv.k_head;
     const uint16_t *vp = a.kv.v + (long long)max(page, 0) * a.kv.v_page + (long long)kvh * a.kv.v_head;

@@ -16,6 +16,7 @@ struct KvView {
   long long table_stride;
   int32_t page_size, width;  // width: entries of a sequence's table row
   int32_t n_pages;
+  uint32_t div_mul, div_sh;  // page number of a position (page_index)
 };
 
 // One attention call. Tokens of sequence b are rows tok0(b) .. tok0(b) +

@@ -26,6 +26,7 @@
 namespace ds4 {
 
 constexpr int AD_WARPS = 8, AD_UNIT = 8;  // a unit: 8 groups of 16 positions, one per warp
+constexpr int AD_LEAST = 2;
 constexpr int AD_RING = 192 * 1024;
 // fp16 weights are scaled by 2^14 (the largest is 16384): a weight then
 // vanishes below 2^-39 of the largest instead of 2^-25, and a long cache's
@@ -93,26 +94,41 @@ __device__ __forceinline__ void dec_next(const AttnArgs &a, DecCursor &c) {
   if (++c.b < a.n_seq) c.s = dec_seq(a, c.b, bad);
 }
 
-// The call's number of units, and the cursor at unit u of the block (the
-// whole warp calls; lanes take sequences).
-__device__ __forceinline__ long long dec_total(const AttnArgs &a, bool &bad) {
-  long long n = 0;
-  for (int b = threadIdx.x & 31; b < a.n_seq; b += 32) n += dec_seq(a, b, bad).units;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n * a.n_kv;
-}
-__device__ __forceinline__ void dec_find(const AttnArgs &a, long long u, DecCursor &c) {
+// A sequence's units by lane (sequences b0 .. b0 + 31), inclusive prefix and
+// the warp's sum.
+__device__ __forceinline__ long long dec_prefix(const AttnArgs &a, int b0, bool &bad, long long &incl, long long &sum) {
   const int lane = threadIdx.x & 31;
-  for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-    bool bad = false;
-    const long long n = b0 + lane < a.n_seq ? (long long)dec_seq(a, b0 + lane, bad).units * a.n_kv : 0;
-    long long incl = n;
+  const long long n = b0 + lane < a.n_seq ? (long long)dec_seq(a, b0 + lane, bad).units * a.n_kv : 0;
+  incl = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  sum = __shfl_sync(0xffffffffu, incl, 31);
+  return n;
+}
+// The block's run of units [u0, u1) out of U, dealt to N blocks, and the
+// cursor at u0 (whole warp). False when there is nothing for this block.
+__device__ __forceinline__ bool dec_start(const AttnArgs &a, int n_cta, long long &U, long long &N, long long &u0,
+                                        long long &u1, DecCursor &c) {
+  long long incl, sum, n;
+  bool bad = false;
+  n = dec_prefix(a, 0, bad, incl, sum);  // up to 32 sequences: the only pass
+  U = sum;
+  for (int b0 = 32; b0 < a.n_seq; b0 += 32) {
+    long long i, s;
+    dec_prefix(a, b0, bad, i, s);
+    U += s;
+  }
+  if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+  N = (U + AD_LEAST - 1) / AD_LEAST;
+  if (N > n_cta) N = n_cta;
+  if (blockIdx.x >= N) return false;
+  u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
+  long long u = u0;
+  for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+    if (b0) n = dec_prefix(a, b0, bad, incl, sum);
     const unsigned hit = __ballot_sync(0xffffffffu, u < incl);
     if (hit) {
       const int l = __ffs(hit) - 1;
@@ -120,10 +136,11 @@ __device__ __forceinline__ void dec_find(const AttnArgs &a, long long u, DecCurs
       c.b = b0 + l;
       c.s = dec_seq(a, c.b, bad);
       c.kvh = (int)(rem / c.s.units), c.lu = (int)(rem - (long long)c.kvh * c.s.units);
-      return;
+      break;
     }
-    u -= __shfl_sync(0xffffffffu, incl, 31);
+    u -= sum;
   }
+  return true;
 }
 
 // Rows whose result holds a NaN are computed once more from what they see
@@ -158,49 +175,68 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
   pdl_launch_dependents();
   pdl_wait();
 
-  bool bad_len = false;
-  const long long U = dec_total(a, bad_len);
-  if (bad_len && blockIdx.x == 0 && w == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
-  const long long N = U < n_cta ? U : n_cta;
-  if (blockIdx.x >= N) return;
-  const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
+  long long U, N, u0, u1;
   DecCursor lc, cc;  // where loading and computing stand
-  dec_find(a, u0, lc);
+  if (!dec_start(a, n_cta, U, N, u0, u1, lc)) return;
   cc = lc;
 
   // one unit's 16 positions of this warp into ring slot `slot`
   bool bad_page = false;
+  // the table's entry for the next unit is read one unit ahead
+  int entry = 0, row0 = 0;
+  auto look = [&]() {
+    const int g = lc.lu * AD_UNIT + w;
+    if (lc.b < a.n_seq && g < lc.s.gr.n) {
+      const int p0 = group_pos(lc.s.gr, g), pi = page_index(a.kv, p0);
+      entry = a.kv.table[(long long)lc.b * a.kv.table_stride + pi], row0 = p0 - pi * a.kv.page_size;
+    }
+  };
   auto load = [&](int slot) {
     const int g = lc.lu * AD_UNIT + w;
     if (g < lc.s.gr.n) {
       const int p0 = group_pos(lc.s.gr, g);
-      const int page = page_of(a.kv, lc.b, p0), row0 = p0 % a.kv.page_size;
+      const int page = entry >= 0 && entry < a.kv.n_pages ? entry : -1;
       if (page < 0) bad_page = true;
       // rows some query row sees: within the length, in the first query's
       // window or after it, or among the first positions
       const int lo = window_lo(a, max(lc.s.first, 0)), sink = min(a.n_sink, window_lo(a, lc.s.last));
-      const uint16_t *kp = a.kv.k + (long long)max(page, 0) * a.kv.k_page + (long long)lc.kvh * a.kv.k_head;
-      const uint16_t *vp = a.kv.v + (long long)max(page, 0) * a.kv.v_page + (long long)lc.kvh * a.kv.v_head;
-      const uint32_t dst = ring_u + slot * STAGE;
+      // this lane's piece of the row (lane / CH), and of every (32 / CH)-th after it
+      constexpr int STEP = 32 / CH;
+      const int r0 = lane / CH, c = lane % CH;
+      const long long row = row0 + r0;
+      const uint16_t *kp = a.kv.k + (long long)max(page, 0) * a.kv.k_page + (long long)lc.kvh * a.kv.k_head + row * a.kv.k_row + c * 8;
+      const uint16_t *vp = a.kv.v + (long long)max(page, 0) * a.kv.v_page + (long long)lc.kvh * a.kv.v_head + row * a.kv.v_row + c * 8;
+      const uint32_t dst = ring_u + slot * STAGE + r0 * (2 * D);
+      if (page >= 0 && p0 + 15 <= lc.s.last && (p0 >= lo || p0 + 15 < sink)) {  // all of them
 #pragma unroll
-      for (int i = 0; i < 16 * CH / 32; i++) {
-        const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-        const int j = p0 + r;
-        const bool live = page >= 0 && j <= lc.s.last && (j >= lo || j < sink);
-        const uint32_t d = dst + r * (2 * D) + ((c ^ (r & 7)) << 4);
-        cp_async16(d, live ? kp + (long long)(row0 + r) * a.kv.k_row + c * 8 : a.kv.k, live);
-        cp_async16(d + 32 * D, live ? vp + (long long)(row0 + r) * a.kv.v_row + c * 8 : a.kv.v, live);
+        for (int i = 0; i < 16 / STEP; i++) {
+          const uint32_t d = dst + i * STEP * (2 * D) + ((c ^ ((r0 + i * STEP) & 7)) << 4);
+          cp_async16(d, kp, true);
+          cp_async16(d + 32 * D, vp, true);
+          kp += STEP * a.kv.k_row, vp += STEP * a.kv.v_row;
+        }
+      } else {
+        for (int i = 0; i < 16 / STEP; i++) {
+          const int j = p0 + r0 + i * STEP;
+          const bool live = page >= 0 && j <= lc.s.last && (j >= lo || j < sink);
+          const uint32_t d = dst + i * STEP * (2 * D) + ((c ^ ((r0 + i * STEP) & 7)) << 4);
+          cp_async16(d, live ? kp : a.kv.k, live);
+          cp_async16(d + 32 * D, live ? vp : a.kv.v, live);
+          kp += STEP * a.kv.k_row, vp += STEP * a.kv.v_row;
+        }
       }
     }
     cp_commit();
   };
 
   const int n_it = (int)(u1 - u0);
+  look();
 #pragma unroll
   for (int i = 0; i < NST - 1; i++) {
     if (i < n_it) {
       load(i);
       dec_next(a, lc);
+      look();
     } else {
       cp_commit();
     }
@@ -216,6 +252,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
     if (it + NST - 1 < n_it) {
       load((it + NST - 1) % NST);
       dec_next(a, lc);
+      look();
     } else {
       cp_commit();
     }
@@ -242,22 +279,30 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
     const uint32_t kb = ring_u + (it % NST) * STAGE, vb = kb + 32 * D;
     const int g = cc.lu * AD_UNIT + w;
     if (g < cc.s.gr.n) {
-      float s[2][4] = {};
+      // two chains of products each (even and odd steps): half the latency
+      float s[2][4] = {}, s2[2][4] = {};
+      {
+        // matrices: keys 0-7 and 8-15 x halves of the 16 elements. A step
+        // along the row flips address bits 5 to 7 (the swizzle is a xor).
+        const int r = (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t ka = kb + r * (2 * D) + ((((lane >> 3) & 1) ^ (r & 7)) << 4);
 #pragma unroll
-      for (int k = 0; k < D / 16; k++) {
-        // matrices: keys 0-7 and 8-15 x halves of the 16 elements
-        uint32_t bf[4];
-        const int r = (lane & 7) + ((lane >> 4) << 3), c = 2 * k + ((lane >> 3) & 1);
-        ldsm4(bf, kb + r * (2 * D) + ((c ^ (r & 7)) << 4));
-        mma16816<DT>(s[0], qf[k], bf[0], bf[1]);
-        mma16816<DT>(s[1], qf[k], bf[2], bf[3]);
+        for (int k = 0; k < D / 16; k += 2) {
+          uint32_t bf[4], bg[4];
+          ldsm4(bf, ka ^ (k << 5));
+          ldsm4(bg, ka ^ ((k + 1) << 5));
+          mma16816<DT>(s[0], qf[k], bf[0], bf[1]);
+          mma16816<DT>(s[1], qf[k], bf[2], bf[3]);
+          mma16816<DT>(s2[0], qf[k + 1], bg[0], bg[1]);
+          mma16816<DT>(s2[1], qf[k + 1], bg[2], bg[3]);
+        }
       }
       const int p0 = group_pos(cc.s.gr, g);
       const int pa = cc.s.first + (a.n_new == 1 ? 0 : r0 / a.group), pb = cc.s.first + (a.n_new == 1 ? 0 : r1 / a.group);
 #pragma unroll
       for (int n = 0; n < 2; n++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) s[n][i] *= a.scale_log2;
+        for (int i = 0; i < 4; i++) s[n][i] = (s[n][i] + s2[n][i]) * a.scale_log2;
       // some position not seen by some row (rows past the last take any mask)
       if (p0 + 15 > cc.s.first || (a.window > 0 && p0 < window_lo(a, max(cc.s.last, 0)) && p0 + 15 >= min(a.n_sink, window_lo(a, max(cc.s.first, 0))))) {
         const int la = window_lo(a, max(pa, 0)), lb = window_lo(a, max(pb, 0));
@@ -297,14 +342,17 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       }
       const uint32_t pf[4] = {Half16<DT>::down(s[0][0], s[0][1]), Half16<DT>::down(s[0][2], s[0][3]),
                               Half16<DT>::down(s[1][0], s[1][1]), Half16<DT>::down(s[1][2], s[1][3])};
-#pragma unroll
-      for (int d = 0; d < D / 16; d++) {
+      {
         // matrices: positions 0-7 and 8-15 x two 8-element columns
-        uint32_t bf[4];
-        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = 2 * d + (lane >> 4);
-        ldsm4t(bf, vb + r * (2 * D) + ((c ^ (r & 7)) << 4));
-        mma16816<DT>(o[2 * d], pf, bf[0], bf[1]);
-        mma16816<DT>(o[2 * d + 1], pf, bf[2], bf[3]);
+        const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
+        const uint32_t va = vb + r * (2 * D) + (((lane >> 4) ^ (r & 7)) << 4);
+#pragma unroll
+        for (int d = 0; d < D / 16; d++) {
+          uint32_t bf[4];
+          ldsm4t(bf, va ^ (d << 5));
+          mma16816<DT>(o[2 * d], pf, bf[0], bf[1]);
+          mma16816<DT>(o[2 * d + 1], pf, bf[2], bf[3]);
+        }
       }
     }
 

@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     };
     auto lookup = [&](const Seg &s, int kt) {
       const int ng = min(gpt, s.gr.n - kt * gpt);
-      const int p0 = group_pos(s.gr, kt * gpt + min(lane, ng - 1), t.gsh), pi = p0 / a.kv.page_size;
+      const int p0 = group_pos(s.gr, kt * gpt + min(lane, ng - 1), t.gsh), pi = page_index(a.kv, p0);
       return Place{a.kv.table[(long long)s.b * a.kv.table_stride + pi], p0 - pi * a.kv.page_size};
     };
     // one operand tile, nst stages
