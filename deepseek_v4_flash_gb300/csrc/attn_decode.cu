@@ -26,7 +26,10 @@
 namespace ds4 {
 
 constexpr int AD_WARPS = 8, AD_UNIT = 8;  // a unit: 8 groups of 16 positions, one per warp
+// A block's least run: below two units the join costs more than the split
+// gains (1 sequence of 8192, 8 heads on 1: 16.9 us with one, 13.0 with two, 14.6 with four).
 constexpr int AD_LEAST = 2;
+constexpr int AD_MAX_BLOCKS = 160;  // one per SM; the joining block's table of factors
 constexpr int AD_RING = 192 * 1024;
 // fp16 weights are scaled by 2^14 (the largest is 16384): a weight then
 // vanishes below 2^-39 of the largest instead of 2^-25, and a long cache's
@@ -123,7 +126,7 @@ __device__ __forceinline__ bool dec_start(const AttnArgs &a, int n_cta, long lon
   }
   if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
   N = (U + AD_LEAST - 1) / AD_LEAST;
-  if (N > n_cta) N = n_cta;
+  if (N > n_cta) N = n_cta;  // (at most AD_MAX_BLOCKS)
   if (blockIdx.x >= N) return false;
   u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
   long long u = u0;
@@ -167,6 +170,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
   constexpr int CH = D / 8;      // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[AD_WARPS][16], s_l[AD_WARPS][16], s_mt[16], s_lt[16];
+  __shared__ float s_f[AD_MAX_BLOCKS][16];
   __shared__ int s_last, s_nan;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int rows = a.n_new * a.group;
@@ -431,25 +435,37 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
         if (s_last) {
           __threadfence();
           const int np = (int)(b1 - b0) + 1;
+          // the block where the item starts holds it in its second slot, the others in their first
+          auto at = [&](int p) { return part + (size_t)(2 * (b0 + p) + (p == 0 ? 1 : 0)) * (16 * (D + 2)); };
+          // a row's factors 2^(m_p - m) / l: lanes over the partials
+          for (int r = w; r < rows; r += AD_WARPS) {
+            float mt = -INFINITY, lt = 0.0f;
+            for (int p = lane; p < np; p += 32) {
+              const float mp = __ldcg(at(p) + 16 * D + r);
+              s_f[p][r] = mp;
+              mt = fmaxf(mt, mp);
+            }
+            mt = warp_max(mt);
+            for (int p = lane; p < np; p += 32) {
+              const float f = s_f[p][r] == -INFINITY ? 0.0f : ex2(s_f[p][r] - mt);
+              s_f[p][r] = f;
+              lt = fmaf(f, __ldcg(at(p) + 16 * D + 16 + r), lt);
+            }
+#pragma unroll
+            for (int k = 16; k; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+            if (lane == 0) s_lt[r] = lt;
+          }
+          __syncthreads();
           for (int i = tid; i < rows * (D / 4); i += AD_WARPS * 32) {
             const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-            // the block where the item starts holds it in its second slot, the others in their first
-            auto at = [&](int p) { return part + (size_t)(2 * (b0 + p) + (p == 0 ? 1 : 0)) * (16 * (D + 2)); };
-            float mt = -INFINITY;
-#pragma unroll 8
-            for (int p = 0; p < np; p++) mt = fmaxf(mt, __ldcg(at(p) + 16 * D + r));
-            float lt = 0.0f;
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
+#pragma unroll 16
             for (int p = 0; p < np; p++) {
-              const float *q = at(p);
-              const float mp = __ldcg(q + 16 * D + r), lp = __ldcg(q + 16 * D + 16 + r);
-              const float4 y = __ldcg(reinterpret_cast<const float4 *>(q + r * D + c));
-              const float f = mp == -INFINITY ? 0.0f : ex2(mp - mt);
-              lt = fmaf(f, lp, lt);
+              const float4 y = __ldcg(reinterpret_cast<const float4 *>(at(p) + r * D + c));
+              const float f = s_f[p][r];
               x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
             }
-            store(r, c, x, lt == 0.0f ? 0.0f : 1.0f / lt);
+            store(r, c, x, s_lt[r] == 0.0f ? 0.0f : 1.0f / s_lt[r]);
           }
         }
       }
@@ -487,6 +503,7 @@ cudaError_t attn_decode_set_attributes() {
 
 cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
                                cudaStream_t s) {
+  if (n_sm > AD_MAX_BLOCKS) n_sm = AD_MAX_BLOCKS;
   void *args[] = {(void *)&a, &part, &ticket, &n_sm};
   const void *fn = dtype == DS4MOE_DT_BF16 ? dec_fn<DS4MOE_DT_BF16>(head_dim) : dec_fn<DS4MOE_DT_F16>(head_dim);
   return launch_pdl(fn, dim3(n_sm), dim3(AD_WARPS * 32), AD_RING, s, args, true);
