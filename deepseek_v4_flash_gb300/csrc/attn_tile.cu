@@ -50,6 +50,7 @@ constexpr int AT_MISC = 3 * 1024;       // what precedes them: barriers, segment
 // row groups, of one or two tiles each, would have three times the items of
 // the others.
 constexpr int AT_ITEM = 2;
+constexpr int AT_WALK = 512;            // most row groups that every block walks through itself
 constexpr int AT_SEGS = 4;              // segments the scheduling warp is ahead
 
 template <int D, int NT>
@@ -78,7 +79,7 @@ struct TileArgs {
   int tpt;           // tokens of a row tile: 128 / group
   int members;       // blocks that work on the same (item, key tiles): row tiles x halves, or halves
   int gangs;
-  long long *first;  // ragged: first tile of each row group, then the total (k_attn_plan)
+  long long *first;  // ragged: first unit of each row group, then the total (k_attn_plan); null: no plan
   int2 *info;        // ragged: {sequence, first token of the row group in it}
   int *count;        // ragged: number of row groups
   float *part;       // [2 * grid][NT][128][DV + 4]: partials
@@ -198,21 +199,19 @@ struct Sched {
   // In units of a tile, AT_ITEM of them before each item's first tile: where
   // the run stands, its end, the current item.
   long long u, u1, item0, item1;
-  int b, kvh, idx, n_idx;
-  long long row_units;
-  long long U, N;                 // the call's tiles, the gangs that have some
+  int b, kvh;
+  int t0, span;                   // ragged calls: the row group's first token in its sequence, tokens of one
+  long long U, N;                 // the call's units, the gangs that have some
 
   // the current item's sequence and rows; its tiles
-  __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, int nt, Seg &s) const {
+  __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, Seg &s) const {
     bool bad = false;
-    const int2 in = a.cu_q ? t.info[idx] : make_int2(b, 0);
-    const SeqInfo si = seq_info(a, in.x, bad);
-    s.b = in.x, s.kvh = kvh, s.len = si.len;
-    const int span = nt * t.tpt;
+    const SeqInfo si = seq_info(a, b, bad);
+    s.b = b, s.kvh = kvh, s.len = si.len;
     if (a.cu_q) {
-      s.row0 = si.tok0 + in.y;
-      s.n = min(span, si.n - in.y);
-      s.pos0 = si.len - si.n + in.y;
+      s.row0 = si.tok0 + t0;
+      s.n = min(span, si.n - t0);
+      s.pos0 = si.len - si.n + t0;
       s.last = s.pos0 + s.n - 1;
       s.gr = range_groups(a, s.pos0, s.last, t.gsh);
     } else {
@@ -226,22 +225,71 @@ struct Sched {
     return tiles_of(s.gr, t.gsh);
   }
 
-  __device__ __forceinline__ int uni_units(const AttnArgs &a, int gsh, int bb) const {
-    bool bad = false;
+  // units of the tokens t0 .. t0 + n - 1 of a sequence
+  static __device__ __forceinline__ int units(const AttnArgs &a, int gsh, const SeqInfo &si, int t0, int n) {
+    const int p0 = si.len - si.n + t0;
+    return AT_ITEM + max(1, tiles_of(range_groups(a, p0, p0 + n - 1, gsh), gsh));
+  }
+  __device__ __forceinline__ int seq_units(const AttnArgs &a, int gsh, int bb, bool &bad) const {
     const SeqInfo si = seq_info(a, bb, bad);
-    return AT_ITEM + max(1, tiles_of(range_groups(a, si.len - si.n, si.len - 1, gsh), gsh));
+    return units(a, gsh, si, 0, si.n);
+  }
+
+  // Row groups of all sequences in order: their units' sum, or (r >= 0) the
+  // one that holds unit r, into b, t0 and item0 (relative to the sum's start).
+  __device__ long long walk(const AttnArgs &a, int gsh, long long r, bool &bad) {
+    const int lane = threadIdx.x & 31;
+    long long base = 0, mine = 0;
+    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+      SeqInfo si = {0, 0, 0};
+      if (b0 + lane < a.n_seq) si = seq_info(a, b0 + lane, bad);
+      for (int l = 0; l < 32 && b0 + l < a.n_seq; l++) {
+        SeqInfo x;
+        x.n = __shfl_sync(0xffffffffu, si.n, l), x.len = __shfl_sync(0xffffffffu, si.len, l), x.tok0 = 0;
+        for (int j0 = 0; j0 < x.n; j0 += 32 * span) {
+          const int j = j0 + lane * span;
+          const int un = j < x.n ? units(a, gsh, x, j, min(span, x.n - j)) : 0;
+          if (r < 0) {
+            mine += un;
+            continue;
+          }
+          int incl = un;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, r < base + incl);
+          if (hit) {
+            const int k = __ffs(hit) - 1;
+            b = b0 + l, t0 = j0 + k * span;
+            item0 = base + __shfl_sync(0xffffffffu, incl - un, k), item1 = item0 + __shfl_sync(0xffffffffu, un, k);
+            return 0;
+          }
+          base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    return mine;
   }
 
   // Whole warp. False when gang g has no tiles.
-  __device__ bool init(const AttnArgs &a, const TileArgs &t, int g) {
+  __device__ bool init(const AttnArgs &a, const TileArgs &t, int g, int nt, bool &bad) {
     const int lane = threadIdx.x & 31;
-    if (a.cu_q) {
-      n_idx = *t.count;
-      row_units = t.first[n_idx];
-      U = row_units * a.n_kv;
+    long long head = 0;  // ragged: units of one key-value head
+    int n_idx = 0;
+    t0 = 0, span = nt * t.tpt;
+    if (a.cu_q && t.first) {
+      n_idx = *t.count, head = t.first[n_idx];
+      U = head * a.n_kv;
+    } else if (a.cu_q) {
+      head = walk(a, t.gsh, -1, bad);
+      U = head * a.n_kv;
     } else {
       long long n = 0;
-      for (int i = lane; i < a.n_seq; i += 32) n += uni_units(a, t.gsh, i);
+      for (int i = lane; i < a.n_seq; i += 32) n += seq_units(a, t.gsh, i, bad);
 #pragma unroll
       for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
       U = n * a.n_kv;
@@ -250,23 +298,29 @@ struct Sched {
     if (g >= N) return false;
     u = U * g / N, u1 = U * (g + 1) / N;
     if (a.cu_q) {
-      kvh = (int)(u / row_units);
-      const long long r = u - kvh * row_units;
-      // the last row group whose first tile is at or before r
-      int lo = 0, hi = n_idx;  // first[lo] <= r < first[hi]
-      while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, i = min(hi, lo + (lane + 1) * step);
-        const unsigned le = __ballot_sync(0xffffffffu, i < hi && t.first[i] <= r);
-        const int k = __popc(le);  // ascending: a prefix of the lanes
-        const int nlo = k ? lo + k * step : lo;
-        hi = min(hi, lo + (k + 1) * step), lo = nlo;
+      kvh = (int)(u / head);
+      const long long r = u - kvh * head;
+      if (t.first) {
+        // the last row group whose first unit is at or before r
+        int lo = 0, hi = n_idx;  // first[lo] <= r < first[hi]
+        while (hi - lo > 1) {
+          const int step = (hi - lo + 31) / 32, i = min(hi, lo + (lane + 1) * step);
+          const unsigned le = __ballot_sync(0xffffffffu, i < hi && t.first[i] <= r);
+          const int k = __popc(le);  // ascending: a prefix of the lanes
+          const int nlo = k ? lo + k * step : lo;
+          hi = min(hi, lo + (k + 1) * step), lo = nlo;
+        }
+        const int2 in = t.info[lo];
+        b = in.x, t0 = in.y;
+        item0 = t.first[lo], item1 = t.first[lo + 1];
+      } else {
+        walk(a, t.gsh, r, bad);
       }
-      idx = lo;
-      item0 = kvh * row_units + t.first[idx], item1 = kvh * row_units + t.first[idx + 1];
+      item0 += kvh * head, item1 += kvh * head;
     } else {
       long long r = u;
       for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-        const long long n = b0 + lane < a.n_seq ? (long long)uni_units(a, t.gsh, b0 + lane) * a.n_kv : 0;
+        const long long n = b0 + lane < a.n_seq ? (long long)seq_units(a, t.gsh, b0 + lane, bad) * a.n_kv : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -278,9 +332,9 @@ struct Sched {
           const int l = __ffs(hit) - 1;
           r -= __shfl_sync(0xffffffffu, incl - n, l);
           b = b0 + l;
-          const int units = uni_units(a, t.gsh, b);
-          kvh = (int)(r / units);
-          item0 = u - (r - (long long)kvh * units), item1 = item0 + units;
+          const int un = seq_units(a, t.gsh, b, bad);
+          kvh = (int)(r / un);
+          item0 = u - (r - (long long)kvh * un), item1 = item0 + un;
           break;
         }
         r -= __shfl_sync(0xffffffffu, incl, 31);
@@ -290,31 +344,41 @@ struct Sched {
     return true;
   }
 
-  __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, int nt, Seg &s) {
+  __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, Seg &s) {
     if (u >= u1 || (u1 < item1 && u1 - item0 <= AT_ITEM)) return false;  // (the next gang's from its start)
-    const int n_kt = load(a, t, member_rt, nt, s);
+    const int n_kt = load(a, t, member_rt, s);
     const long long e = item1 < u1 ? item1 : u1;
     s.starts = u == item0, s.ends = e == item1;
     s.kt0 = max(0, (int)(u - item0) - AT_ITEM), s.kt1 = min(n_kt, (int)(e - item0) - AT_ITEM);
     u = e;
     if (u == item1 && u < u1) {
       // the next item
+      bool bad = false;
       item0 = item1;
       if (a.cu_q) {
-        if (++idx == n_idx) idx = 0, kvh++;
-        item1 = kvh * row_units + t.first[idx + 1];
+        SeqInfo si = seq_info(a, b, bad);
+        for (t0 += span; t0 >= si.n; t0 = 0) {
+          if (++b == a.n_seq) b = 0, kvh++;
+          si = seq_info(a, b, bad);
+          if (si.n > 0) {
+            t0 = 0;
+            break;
+          }
+        }
+        item1 = item0 + units(a, t.gsh, si, t0, min(span, si.n - t0));
       } else {
         if (++kvh == a.n_kv) kvh = 0, b++;
-        item1 = item0 + uni_units(a, t.gsh, b);
+        item1 = item0 + seq_units(a, t.gsh, b, bad);
       }
     }
     return true;
   }
 };
 
-// Ragged calls: row groups of `span` tokens, in sequence order, and the
-// running count of their key tiles. One block; a few microseconds for some
-// thousand groups, against the attention's tens to hundreds.
+// Ragged calls of many sequences or row groups: the groups of `span` tokens in
+// sequence order, and the running count of their units, by one block. Small
+// calls do without (Sched::walk, in every block): up to AT_WALK groups of up to
+// 32 sequences a block's walk is shorter than this kernel's 4 to 6 us.
 __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, int gsh, long long *first, int2 *info, int *count,
                                                 int *seq_first) {
   __shared__ long long warp_sum[32];
@@ -376,8 +440,7 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, 
       b = lo, t0 = (i - seq_first[b]) * span;
       bool unused = false;
       const SeqInfo si = seq_info(a, b, unused);
-      const int p0 = si.len - si.n + t0;
-      units = AT_ITEM + max(1, tiles_of(range_groups(a, p0, p0 + min(span, si.n - t0) - 1, gsh), gsh));
+      units = Sched::units(a, gsh, si, t0, min(span, si.n - t0));
     }
     const long long x = scan(units);
     if (i < total) first[i] = x, info[i] = make_int2(b, t0);
@@ -523,11 +586,13 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     // ---- order of work: a few segments ahead of the others, so that nobody
     // else waits for lengths, row groups and tables of them
     Sched sc;
-    bool more = sc.init(a, t, gang), split_out = false;
+    bool bad = false, split_out = false;
+    bool more = sc.init(a, t, gang, NT, bad);
+    if (bad && blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
     while (ok) {
       Seg s;
       s.kt1 = -1;
-      if (more) more = sc.next(a, t, rt, NT, s);
+      if (more) more = sc.next(a, t, rt, s);
       if (!more) s.kt1 = -1;
       const int i = seg_n % AT_SEGS;
       if (seg_n >= AT_SEGS && !wait_warp(seg_empty(i), (seg_n / AT_SEGS - 1) & 1)) ok = false;
@@ -549,11 +614,6 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     if (!split_out && member == 0 && lane == 0) t.split[2 * gang].x = 0;
   } else if (w == 0) {
     // ---- loads
-    if (!a.cu_q && blockIdx.x == 0) {
-      bool bad = false;
-      for (int i = lane; i < a.n_seq; i += 32) seq_info(a, i, bad);
-      if (bad) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
-    }
     int st = 0;  // ring stages issued so far
     int qn = 0;  // items whose Q was issued
     bool bad_page = false;
@@ -1180,8 +1240,9 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
       !make_map(&maps.v, dtype, a.kv.v, 4, kd, vs, kb))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  if (ragged) {
-    int span = f.nt * t.tpt;
+  int span = f.nt * t.tpt;
+  if (ragged && a.n_seq <= 32 && a.n_tok / span + a.n_seq <= AT_WALK) t.first = nullptr;
+  if (ragged && t.first) {
     void *args[] = {(void *)&a, &span, &t.gsh, &t.first, &t.info, &t.count, (void *)&w.seq_first};
     e = launch_pdl((const void *)k_attn_plan, dim3(1), dim3(1024), 0, s, args, true);
     ++*launches;
