@@ -91,6 +91,23 @@ def test_decode_long():
         _run_decode("fp16", heads, kv, dim, 64, 0, 0, new, [9001, 3, 0, 12345, 1, 640, 64, 128, 4097], seed=8)
 
 
+def test_many_sequences():
+    """More sequences than a warp has lanes, empty ones among them."""
+    lens = [(37 * i) % 300 for i in range(70)]
+    for heads, kv, dim, new in [(8, 2, 128, 1), (64, 1, 512, 1), (8, 1, 256, 3), (40, 2, 64, 2)]:
+        _run_decode("bf16", heads, kv, dim, 16, 0, 0, new, lens, seed=11)
+    runs = [((7 * i) % 11, (13 * i) % 50) for i in range(70)]
+    for heads, kv, dim in [(4, 2, 128), (8, 1, 256), (64, 1, 512)]:
+        _run_prefill("bf16", heads, kv, dim, 16, 20, 3, runs, seed=12)
+
+
+def test_many_row_groups():
+    """Prompts whose row groups every block no longer walks through itself:
+    one of 600 groups, and two short ones behind it."""
+    _run_prefill("bf16", 64, 1, 64, 32, 64, 4, [(2400, 0), (3, 2), (0, 9), (70, 100)], seed=4)
+    _run_prefill("fp16", 128, 1, 512, 32, 64, 4, [(1030, 7), (5, 0)], seed=5)
+
+
 @pytest.mark.parametrize("qscale", [0.0, 30.0])
 def test_decode_flat_and_peaked_scores(qscale):
     """Equal weights, and scores hundreds apart (the running maximum moves)."""
@@ -380,6 +397,29 @@ def test_streams_and_graphs():
         _check(out[0], ref, tol, f"replay {i}")
         _check(ragged, ref, tol, f"replay {i}, ragged")
     assert at.device_error() == 0
+
+
+def test_two_handles_on_two_streams():
+    """Handles are independent: their calls may overlap."""
+    ds4 = _ds4()
+    heads, kv, dim, n = 64, 1, 512, 3000
+    k, v, table = paged([n], 64, kv, dim, torch.bfloat16, 8)
+    kd, vd = to_cuda(k, v)
+    cache = ds4.KVCache(kd, vd, table.cuda())
+    q = torch.randn(2, 1, 2, heads, dim).bfloat16().cuda()
+    length = torch.tensor([n], dtype=torch.int32).cuda()
+    ats = [_handle(ds4, "bf16", heads, kv, dim, 0, 0, 1, 2) for _ in range(2)]
+    alone = [ats[0].decode(cache, q[i], length) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            outs[i].append(ats[i].decode(cache, q[i], length, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
+        assert ats[i].device_error() == 0
 
 
 @pytest.mark.parametrize("kind,source", [("bf16", "fp32"), ("bf16", "own"), ("fp16", "fp32"), ("fp16", "own")])
