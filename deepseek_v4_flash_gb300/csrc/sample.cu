@@ -65,16 +65,17 @@ __device__ __forceinline__ float exp_over_t(float d, const ExpScale &c) {
   return __fmaf_rn(e, err * 0.693147180559945f, e);
 }
 
-// Entries i .. i + 3 of a row (those below end; `fill` elsewhere).
+// Entries i .. i + 3 of a row (those below end; `fill` elsewhere). `inner`: the
+// whole block's, or warp's, four entries are known to lie below end.
 template <bool VEC>
-__device__ __forceinline__ float4 row4(const float *r, int i, int end, float fill) {
-  if (VEC && i + 3 < end) return *reinterpret_cast<const float4 *>(r + i);
+__device__ __forceinline__ float4 row4(const float *r, int i, int end, float fill, bool inner = false) {
+  if (VEC && (inner || i + 3 < end)) return *reinterpret_cast<const float4 *>(r + i);
   return make_float4(i < end ? r[i] : fill, i + 1 < end ? r[i + 1] : fill, i + 2 < end ? r[i + 2] : fill,
                      i + 3 < end ? r[i + 3] : fill);
 }
 template <bool VEC>
-__device__ __forceinline__ void put4(float *o, int i, int end, float4 v) {
-  if (VEC && i + 3 < end) {
+__device__ __forceinline__ void put4(float *o, int i, int end, float4 v, bool inner = false) {
+  if (VEC && (inner || i + 3 < end)) {
     *reinterpret_cast<float4 *>(o + i) = v;
     return;
   }
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
   const int begin = min(V, rank * part), end = min(V, begin + part);
   float4 v[SP_KEEP];
 #pragma unroll
-  for (int k = 0; k < SP_KEEP; k++) v[k] = row4<VEC>(r, begin + 4 * (tid + k * PR_THREADS), end, -INFINITY);
+  for (int k = 0; k < SP_KEEP; k++)
+    v[k] = row4<VEC>(r, begin + 4 * (tid + k * PR_THREADS), end, -INFINITY, begin + 4 * (k + 1) * PR_THREADS <= end);
   const int rest = begin + 4 * (tid + SP_KEEP * PR_THREADS);
   float m = -INFINITY;
 #pragma unroll
@@ -195,13 +197,14 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
   for (int b = 0; b < 8; b++) top = fmaxf(top, pm[b]);
 #pragma unroll
   for (int b = 0; b < 8; b++) total += pm[b] == -INFINITY ? ps[b] : ps[b] * exp_over_t(pm[b] - top, c);
-  // barrier.cluster: a block's shared memory outlives its readers
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // a block's shared memory outlives its readers (nothing is handed over: relaxed)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const float f = (m == -INFINITY ? 0.0f : exp_over_t(m - top, c)) / total;
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) {
     const int i = begin + 4 * (tid + k * PR_THREADS);
-    put4<VEC>(o, i, end, make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f));
+    put4<VEC>(o, i, end, make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f),
+              begin + 4 * (k + 1) * PR_THREADS <= end);
   }
   for (int i = rest; i < end; i += 4 * PR_THREADS) {
     const float4 y = row4<VEC>(r, i, end, -INFINITY);
@@ -316,14 +319,14 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
   const int lo_bits = a.shift - 22;
   const float lo_scale = (float)(1 << lo_bits);
   // hi and lo of four entries
-  auto four = [&](int i, int (&hi)[4], int (&lo)[4]) {
-    const float4 x = row4<VEC>(p, i, i1, 0.0f);
-    const float4 y = q ? row4<VEC>(q, i, i1, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto four = [&](int i, int (&hi)[4], int (&lo)[4], bool inner) {
+    const float4 x = row4<VEC>(p, i, i1, 0.0f, inner);
+    const float4 y = q ? row4<VEC>(q, i, i1, 0.0f, inner) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float px[4] = {x.x, x.y, x.z, x.w}, qx[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int k = 0; k < 4; k++) {
       mass_of(px[k], qx[k], lo_scale, hi[k], lo[k]);
-      if (i + k == dtok) hi[k] = lo[k] = 0;
+      if (dtok >= 0 && i + k == dtok) hi[k] = lo[k] = 0;
     }
   };
   long long total = 0, before = 0, mine = 0;
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         int hi[4], lo[4];
-        four(c + 128 * k, hi, lo);
+        four(c + 128 * k, hi, lo, c - 4 * lane + 128 * (k + 1) <= i1);
         sh += (hi[0] + hi[1]) + (hi[2] + hi[3]), sl += (lo[0] + lo[1]) + (lo[2] + lo[3]);
       }
       s += ((long long)sh << lo_bits) + sl;
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
     if (before <= thr && thr < before + mine) {
       for (int c = i0; c < i1; c += 128) {
         int hi[4], lo[4];
-        four(c + 4 * lane, hi, lo);
+        four(c + 4 * lane, hi, lo, c + 128 <= i1);
         long long e[4];
 #pragma unroll
         for (int k = 0; k < 4; k++) e[k] = ((long long)hi[k] << lo_bits) + lo[k] + (k ? e[k - 1] : 0);
