@@ -486,8 +486,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Eight 16-byte pieces per lane, exchanged within groups of eight lanes: lane
 // j's piece i becomes piece j of lane i. A row per lane turns into eight rows
 // whose 128 bytes lie across the lanes, so that a store writes four whole
-// lines instead of a sixteenth of 32 (the output took 10 us of a block's 17
-// per item before).
+// lines instead of an eighth of 32.
 __device__ __forceinline__ void transpose8(uint32_t (&x)[32]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -683,10 +682,11 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     }
     if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
     if (!ok) {
-      // the copies in flight land before the block leaves
-      for (int i = max(0, st - C::NST); i < st; i++) mbar_wait_bounded(full(i % C::NST), (i / C::NST) & 1);
+      // the copies in flight land before the block leaves (they need microseconds; a second full wait is not due)
+      constexpr long long LAND = WAIT_LIMIT / 128;
+      for (int i = max(0, st - C::NST); i < st; i++) mbar_wait_bounded(full(i % C::NST), (i / C::NST) & 1, LAND);
       for (int r = 0; r < NT; r++)
-        if (qn > 0) mbar_wait_bounded(b_qf + 8 * r, (qn - 1) & 1);
+        if (qn > 0) mbar_wait_bounded(b_qf + 8 * r, (qn - 1) & 1, LAND);
     }
   } else if (w == 1) {
     // ---- products
@@ -1034,6 +1034,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         ml[0] = m, ml[1] = l;
       }
       tc_fence_before();
+      __syncwarp();  // other lanes have stored parts of these rows
       unsigned again = __ballot_sync(0xffffffffu, nan && valid);
       while (again) {
         const int x = __ffs(again) - 1;
