@@ -231,6 +231,7 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
   h->tile.split = h->mem + o_split, h->tile.count = (int *)(h->mem + o_count);
   h->tile.seq_first = (int *)(h->mem + o_seq), h->tile.first = (long long *)(h->mem + o_first);
   h->tile.info = h->mem + o_info, h->tile.part = h->part;
+  h->tile.pairs = attn_tile_pairs(d.dtype, d.head_dim);
   h->bytes = at;
   *out = h;
   return DS4MOE_OK;

@@ -42,6 +42,7 @@ struct TileWork {
   int *count, *seq_first;
   float *part;
   void *split;       // int4 [2 * n_sm]
+  int pairs;         // pairs of blocks that run at once
 };
 
 }  // namespace ds4
@@ -69,6 +70,7 @@ cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float
 size_t attn_tile_part_floats(int head_dim, int n_sm);
 size_t attn_tile_groups(int group, int head_dim, int max_tokens, int max_seqs);
 cudaError_t attn_tile_set_attributes(int dtype, int head_dim);
+int attn_tile_pairs(int dtype, int head_dim);
 cudaError_t launch_attn_tile(const AttnArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
                              cudaStream_t s);
 }  // namespace ds4

@@ -30,6 +30,8 @@
 // (O, m, l) per block; k_attn_join adds them in block order.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "attn.cuh"
 #include "internal.h"
 #include "umma.cuh"
@@ -53,20 +55,27 @@ constexpr int AT_ITEM = 2;
 constexpr int AT_WALK = 512;            // most row groups that every block walks through itself
 constexpr int AT_SEGS = 4;              // segments the scheduling warp is ahead
 
-template <int D, int NT>
+template <int D, int NT, bool PAIR>
 struct TileCfg {
   static constexpr int DV = D < 256 ? D : 256;         // columns of O a block computes
   static constexpr int HALVES = D / DV;
-  static constexpr int SC = D == 64 ? 1 : 2;           // 64-element chunks of a ring stage
-  static constexpr int STAGE = SC * AT_CHUNK;
-  static constexpr int KST = D / 64 / SC, VST = DV / 64 / SC;  // stages of a key and a value tile
+  // Ring stages: KC chunks of 64 elements of a key tile's rows, VC of a value
+  // tile's. Of a pair, each block holds half of the keys' rows and half of
+  // the values' columns.
+  static constexpr int KC = D == 64 ? 1 : 2, VC = D == 64 || PAIR ? 1 : 2;
+  static constexpr int KPITCH = PAIR ? AT_CHUNK / 2 : AT_CHUNK;  // bytes of a chunk of keys
+  static constexpr int STAGE = KC * KPITCH;
+  static constexpr int KST = D / 64 / KC, VST = DV / 64 / VC / (PAIR ? 2 : 1);  // stages of a key and a value tile
+  static constexpr int PV_N = VC * 64 * (PAIR ? 2 : 1);          // columns of one product into O
   static constexpr int Q = NT * (D / 64) * AT_CHUNK;
   static constexpr int NST_ = (AT_SMEM - Q) / STAGE;
   static constexpr int NST = NST_ > 10 ? 10 : NST_;
   static constexpr int THREADS = 128 + 256 * NT;
+  static constexpr int SPAN = PAIR ? 2 : NT;           // row tiles of a ragged call's row group
   static constexpr int PITCH = DV + 4;                 // floats of a partial's row: O, m, l
   static constexpr int JROWS = 1024 / DV;              // rows of a joining block
   static constexpr int O_COL = 256;                    // O's first tensor-memory column (S: 0 and 128)
+  static_assert(VC * AT_CHUNK <= STAGE, "a stage holds either");
 };
 
 struct TileMaps {
@@ -98,6 +107,69 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *m, int c
       "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
+// ---- pairs of blocks (cta_group::2): one product of 256 rows, 128 in each
+// block's tensor memory, the other operand's halves in the two blocks' shared
+// memories. The even block issues the products and owns the barriers that say
+// what is ready; all other barriers are told in both.
+__device__ __forceinline__ uint32_t of_block(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void tma_4d_pair(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_block(bar, 0)) : "memory");
+}
+// (relaxed: the copies count their bytes themselves, and a release at cluster
+// scope took 1000 cycles per stage)
+__device__ __forceinline__ void expect_leader(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(of_block(bar, 0)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void umma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The barrier at this place of both blocks.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Descriptor of a 128-byte swizzled operand: 8-row atoms of 1024 bytes, `lbo`
 // the distance of 64-element columns (used by the operand whose rows run
 // along K, i.e. V).
@@ -110,9 +182,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
   return d;
 }
 template <int DT>
-__device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major) {
+__device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major, int m = 128) {
   constexpr uint32_t t = DT == DS4MOE_DT_BF16 ? 1u : 0u;
-  return (1u << 4) | (t << 7) | (t << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+  return (1u << 4) | (t << 7) | (t << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 // D[tmem] (+)= A[tmem] B
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -505,10 +577,10 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[32]) {
   }
 }
 
-template <int DT, int D, int NT>
+template <int DT, int D, int NT, bool PAIR>
 __global__ void __launch_bounds__(128 + 256 * NT, 1)
     k_attn_tile(const __grid_constant__ TileMaps maps, const AttnArgs a, const TileArgs t) {
-  using C = TileCfg<D, NT>;
+  using C = TileCfg<D, NT, PAIR>;
   // One window of dynamic shared memory, exactly what an SM has: a TMA tile
   // in the 128-byte swizzle starts on a multiple of 1024 bytes.
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -537,13 +609,18 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     if (tid == 0) raise_flag(a.err, DS4MOE_DEVERR_INTERNAL);
     return;
   }
+  const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members;  // 
+  // which half of O's columns, which row tile of the row group (ragged pairs) or sequence (decode calls)
+  const int rank = PAIR ? member & 1 : 0;
+  const int half = PAIR ? member >> 1 & 1 : member % C::HALVES, rt = PAIR ? (member >> 2) * 2 + rank : member / C::HALVES;
   if (w == 0) {
     if (lane == 0) {
-      for (int i = 0; i < C::NST; i++) mbar_init(full(i), 1), mbar_init(empty(i), 1);
+      for (int i = 0; i < C::NST; i++) mbar_init(full(i), PAIR ? 2 : 1), mbar_init(empty(i), 1);
       for (int i = 0; i < AT_SEGS; i++) mbar_init(seg_full(i), 1), mbar_init(seg_empty(i), 2 + 8 * NT);
       for (int i = 0; i < 2; i++) {
-        mbar_init(b_qf + 8 * i, 1), mbar_init(b_qe + 8 * i, 1), mbar_init(b_sf + 8 * i, 1);
-        mbar_init(b_pa + 8 * i, 128), mbar_init(b_pb + 8 * i, 128), mbar_init(b_of + 8 * i, 1);
+        mbar_init(b_qf + 8 * i, PAIR ? 2 : 1), mbar_init(b_qe + 8 * i, 1), mbar_init(b_sf + 8 * i, 1);
+        // every thread of a warpgroup, or every warp of the two blocks'
+        mbar_init(b_pa + 8 * i, PAIR ? 8 : 128), mbar_init(b_pb + 8 * i, PAIR ? 8 : 128), mbar_init(b_of + 8 * i, 1);
       }
       mbar_init(b_done, 1);
       for (int i = 0; i < 8; i++) mbar_init(b_x + 8 * i, 2);
@@ -552,17 +629,17 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     }
     __syncwarp();
   } else if (w == 1) {
-    tmem_alloc(smem_u32(&ms.tmem), 512);
+    if (PAIR) tmem_alloc_pair(smem_u32(&ms.tmem), 512);
+    else tmem_alloc(smem_u32(&ms.tmem), 512);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (PAIR) cluster_sync_all();  // barriers are set up before the other block reaches for them
   const uint32_t tmem = ms.tmem;
   pdl_launch_dependents();
   pdl_wait();
 
-  const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members;
-  const int half = member % C::HALVES, rt = member / C::HALVES;
   bool ok = true;  // no wait has run out
 
   // Operands of copies and products go through uniform(): the compiler then
@@ -586,7 +663,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     // else waits for lengths, row groups and tables of them
     Sched sc;
     bool bad = false, split_out = false;
-    bool more = sc.init(a, t, gang, NT, bad);
+    bool more = sc.init(a, t, gang, C::SPAN, bad);
     if (bad && blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
     while (ok) {
       Seg s;
@@ -627,31 +704,48 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       const int p0 = group_pos(s.gr, kt * gpt + min(lane, ng - 1), t.gsh), pi = page_index(a.kv, p0);
       return Place{a.kv.table[(long long)s.b * a.kv.table_stride + pi], p0 - pi * a.kv.page_size};
     };
-    // one operand tile, nst stages
-    auto load_tile = [&](const Seg &s, int kt, const Place &pl, const CUtensorMap *m, int nst, int chunk0) {
-      const int ng = min(gpt, s.gr.n - kt * gpt);
+    // one operand tile, nst stages of `chunks` chunks each: its boxes [g0, g1)
+    auto load_tile = [&](const Seg &s, const Place &pl, const CUtensorMap *m, int nst, int chunks, int pitch, int chunk0,
+                         int chunk_step, int g0, int g1) {
       int page = pl.page;
       if (page < 0 || page >= a.kv.n_pages) bad_page = true, page = a.kv.n_pages;  // past the pool: zeros
-      const int kvh = uniform(s.kvh), n_box = uniform(ng);
+      const int kvh = uniform(s.kvh), n_box = uniform(g1 - g0), first = uniform(g0);
       for (int i = 0; i < nst && ok; i++) {
         const int slot = uniform(st % C::NST);
         if (st >= C::NST && !wait_warp(empty(slot), (st / C::NST - 1) & 1)) {
           ok = false;
           break;
         }
-        const uint32_t dst = ring + slot * C::STAGE, bar = full(slot);
-        const int x = uniform((chunk0 + i * C::SC) * 64);
-        if (elect_one()) mbar_arrive_expect_tx(bar, (C::SC * 128u << t.gsh) * n_box);
+        const uint32_t dst = ring + slot * C::STAGE, bar = PAIR ? uniform(of_block(full(slot), 0)) : full(slot);
+        const int x = uniform((chunk0 + i * chunk_step) * 64);
+        if (elect_one()) {
+          const uint32_t bytes = (chunks * 128u << t.gsh) * n_box;
+          if (PAIR) expect_leader(full(slot), bytes);
+          else mbar_arrive_expect_tx(bar, bytes);
+        }
         for (int g = 0; g < n_box; g++) {
-          const int pg = __shfl_sync(0xffffffffu, page, g), row = __shfl_sync(0xffffffffu, pl.row, g);
+          const int pg = __shfl_sync(0xffffffffu, page, first + g), row = __shfl_sync(0xffffffffu, pl.row, first + g);
           const uint32_t to = dst + (g << (t.gsh + 7));
           if (elect_one()) {
-#pragma unroll
-            for (int c = 0; c < C::SC; c++) tma_4d(to + c * AT_CHUNK, m, x + c * 64, row, kvh, pg, bar);
+            if (PAIR) {
+              tma_4d_pair(to, m, x, row, kvh, pg, bar);
+              if (chunks == 2) tma_4d_pair(to + pitch, m, x + 64, row, kvh, pg, bar);
+            } else {
+              tma_4d(to, m, x, row, kvh, pg, bar);
+              if (chunks == 2) tma_4d(to + pitch, m, x + 64, row, kvh, pg, bar);
+            }
           }
         }
         st++;
       }
+    };
+    auto load_k = [&](const Seg &s, int kt, const Place &pl) {
+      const int ng = min(gpt, s.gr.n - kt * gpt), h = (ng + 1) >> 1;  // a pair: the first h boxes, the others
+      load_tile(s, pl, &maps.k, C::KST, C::KC, C::KPITCH, 0, C::KC, PAIR && rank ? h : 0, PAIR && !rank ? h : ng);
+    };
+    auto load_v = [&](const Seg &s, int kt, const Place &pl) {
+      const int ng = min(gpt, s.gr.n - kt * gpt);
+      load_tile(s, pl, &maps.v, C::VST, C::VC, AT_CHUNK, half * (C::DV / 64) + rank, PAIR ? 2 : C::VC, 0, ng);
     };
     Seg s;
     while (ok && next_seg(s)) {
@@ -659,29 +753,44 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       Place kp = lookup(s, s.kt0);
       for (int r = 0; r < NT && ok; r++) {
         if (qn > 0 && !wait_warp(b_qe + 8 * r, (qn - 1) & 1)) ok = false;
-        const int qh = uniform(s.kvh * a.group), qt = uniform(s.row0 + r * t.tpt);
+        const int qh = uniform(s.kvh * a.group), qt = uniform(s.row0 + (PAIR && a.cu_q ? rank : r) * t.tpt);
+        const uint32_t q_bar = PAIR ? uniform(of_block(b_qf, 0)) : 0;
         if (ok && elect_one()) {
-          mbar_arrive_expect_tx(b_qf + 8 * r, (D / 64) * t.tpt * a.group * 128);
+          const uint32_t bytes = (D / 64) * t.tpt * a.group * 128;
+          if (PAIR) expect_leader(b_qf, bytes);
+          else mbar_arrive_expect_tx(b_qf + 8 * r, bytes);
           // rows past the call's last come in as zeros
 #pragma unroll
-          for (int c = 0; c < D / 64; c++) tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, qh, qt, b_qf + 8 * r);
+          for (int c = 0; c < D / 64; c++) {
+            if (PAIR) tma_3d_pair(q_sm + c * AT_CHUNK, &maps.q, c * 64, qh, qt, q_bar);
+            else tma_3d(q_sm + (r * (D / 64) + c) * AT_CHUNK, &maps.q, c * 64, qh, qt, b_qf + 8 * r);
+          }
         }
         __syncwarp();
       }
       qn++;
       // in the order in which the products use them: one row tile computes the
       // next tile's S before the current O
-      if (NT == 1 && ok) load_tile(s, s.kt0, kp, &maps.k, C::KST, 0);
+      if (NT == 1 && ok) load_k(s, s.kt0, kp);
       for (int kt = s.kt0; kt < s.kt1 && ok; kt++) {
         const Place vp = kp;
         if (kt + 1 < s.kt1) kp = lookup(s, kt + 1);
-        if (NT == 2) load_tile(s, kt, vp, &maps.k, C::KST, 0);
-        else if (kt + 1 < s.kt1) load_tile(s, kt + 1, kp, &maps.k, C::KST, 0);
-        if (ok) load_tile(s, kt, vp, &maps.v, C::VST, half * (C::DV / 64));
+        if (NT == 2) load_k(s, kt, vp);
+        else if (kt + 1 < s.kt1) load_k(s, kt + 1, kp);
+        if (ok) load_v(s, kt, vp);
       }
     }
     if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
-    if (!ok) {
+    if (PAIR && ok) {
+      // the leader's last arrivals have come in before the block leaves
+      for (int i = max(0, st - C::NST); i < st; i++)
+        if (!wait_warp(empty(i % C::NST), (i / C::NST) & 1)) ok = false;
+      if (qn > 0 && !wait_warp(b_qe, (qn - 1) & 1)) ok = false;
+    }
+    if (PAIR && !ok) {
+      // their landing is told to the leader alone: 10 ms, some thousand times what they need
+      for (int i = 0; i < 100; i++) __nanosleep(100000);
+    } else if (!ok) {
       // the copies in flight land before the block leaves (they need microseconds; a second full wait is not due)
       constexpr long long LAND = WAIT_LIMIT / 128;
       for (int i = max(0, st - C::NST); i < st; i++) mbar_wait_bounded(full(i % C::NST), (i / C::NST) & 1, LAND);
@@ -692,20 +801,27 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     // ---- products
     int st = 0, qn = 0;
     int steps = 0;  // (key tile, row tile) pairs before the current segment
-    const uint32_t id_o = idesc<DT>(C::SC * 64, true);
+    const uint32_t id_o = idesc<DT>(C::PV_N, true, PAIR ? 256 : 128);
     const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq = desc_sw128(q_sm, 0), dk = desc_sw128(ring, 0), dv = desc_sw128(ring, AT_CHUNK);
     int kst0 = 0, vst0 = 0;  // ring stages of the current key and value tile
-    Seg s;
+    Seg s = {};
     auto wait_stage = [&](int i) {
       if (!wait_warp(full(i % C::NST), (i / C::NST) & 1)) ok = false;
+    };
+    auto commit = [&](uint32_t bar) {
+      if (PAIR) umma_commit_pair(bar);
+      else umma_commit(bar);
     };
     // S of key tile kt and row tile r, the segment's i-th such step
     auto qk = [&](int kt, int r, int i) {
       const int buf = NT == 2 ? r : uniform((steps + i) & 1);
       if (i < NT && !wait_warp(b_qf + 8 * r, (qn - 1) & 1)) ok = false;
       if (r == 0) kst0 = st, st += C::KST;
-      const uint32_t id = idesc<DT>(16 * uniform(cols16(s, kt, t.gsh)), false);
+      // a pair's columns: as many of either block, in boxes
+      const int boxes = min(1 << (7 - t.gsh), s.gr.n - (kt << (7 - t.gsh)));
+      const int cols = PAIR ? ((boxes + 1) >> 1) << (t.gsh + 1) : 16 * cols16(s, kt, t.gsh);
+      const uint32_t id = idesc<DT>(uniform(cols), false, PAIR ? 256 : 128);
       const uint32_t sd = tmem_u + buf * 128;
 #pragma unroll
       for (int j = 0; j < C::KST; j++) {
@@ -714,16 +830,19 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         tc_fence_after();
         if (ok && elect_one()) {
           // descriptor addresses count 16 bytes
-          const uint64_t qa = dq + ((r * (D / 64) + j * C::SC) * AT_CHUNK >> 4), kb = dk + (slot * C::STAGE >> 4);
+          const uint64_t qa = dq + ((r * (D / 64) + j * C::KC) * AT_CHUNK >> 4), kb = dk + (slot * C::STAGE >> 4);
 #pragma unroll
-          for (int c = 0; c < C::SC; c++)
+          for (int c = 0; c < C::KC; c++)
 #pragma unroll
-            for (int k = 0; k < 4; k++)
-              umma_f16(sd, qa + (c * AT_CHUNK >> 4) + 2 * k, kb + (c * AT_CHUNK >> 4) + 2 * k, id, (j | c | k) != 0);
-          if (r == NT - 1) umma_commit(empty(slot));
+            for (int k = 0; k < 4; k++) {
+              const uint64_t qd = qa + (c * AT_CHUNK >> 4) + 2 * k, kd = kb + (c * C::KPITCH >> 4) + 2 * k;
+              if (PAIR) umma_f16_pair(sd, qd, kd, id, (j | c | k) != 0);
+              else umma_f16(sd, qd, kd, id, (j | c | k) != 0);
+            }
+          if (r == NT - 1) commit(empty(slot));
           if (j == C::KST - 1) {
-            umma_commit(b_sf + 8 * buf);
-            if (kt + 1 == s.kt1) umma_commit(b_qe + 8 * r);
+            commit(b_sf + 8 * buf);
+            if (kt + 1 == s.kt1) commit(b_qe + 8 * r);
           }
         }
         __syncwarp();
@@ -742,12 +861,15 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         const int live = ((ng - 1) << t.gsh) + s.len - group_pos(s.gr, kt * gpt + ng - 1, t.gsh);
         if (ok && live < 16 * n16) {
           const int n8 = (16 * n16 - live) * 8;
-          for (int j = 0; j < C::VST * C::SC; j++)
+          for (int j = 0; j < C::VST * C::VC; j++)
             for (int e = lane; e < n8; e += 32) {
-              const uint32_t p = ring + ((vst0 + j / C::SC) % C::NST) * C::STAGE + j % C::SC * AT_CHUNK + live * 128 + e * 16;
+              const uint32_t p = ring + ((vst0 + j / C::VC) % C::NST) * C::STAGE + j % C::VC * AT_CHUNK + live * 128 + e * 16;
               asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(p), "r"(0) : "memory");
+              if (PAIR)
+                asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(of_block(p, 1)), "r"(0) : "memory");
             }
-          fence_proxy_async_smem();
+          if (PAIR) asm volatile("fence.proxy.async;" ::: "memory");
+          else fence_proxy_async_smem();
           __syncwarp();
         }
       }
@@ -771,17 +893,20 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
           for (int j = 0; j < C::VST; j++) {
 #pragma unroll
             for (int k = 4 * h; k < 4 * h + 4; k++)
-              if (k < n16)
-                umma_f16_ts(o + j * C::SC * 64, pd + 8 * k, vb[j] + (2048 * k >> 4), id_o, later || k != 0);
-            if (h == 1 && r == NT - 1) umma_commit(eb[j]);
+              if (k < n16) {
+                const uint32_t od = o + j * C::PV_N;
+                if (PAIR) umma_f16_ts_pair(od, pd + 8 * k, vb[j] + (2048 * k >> 4), id_o, later || k != 0);
+                else umma_f16_ts(od, pd + 8 * k, vb[j] + (2048 * k >> 4), id_o, later || k != 0);
+              }
+            if (h == 1 && r == NT - 1) commit(eb[j]);
           }
-          if (h == 1 && (NT == 1 || kt + 1 == s.kt1)) umma_commit(b_of + 8 * r);
+          if (h == 1 && (NT == 1 || kt + 1 == s.kt1)) commit(b_of + 8 * r);
         }
         __syncwarp();
       }
     };
     while (ok && next_seg(s)) {
-      if (s.kt0 >= s.kt1) continue;
+      if (s.kt0 >= s.kt1 || rank) continue;  // (the even block's products are the pair's)
       qn++;
       const int n = (s.kt1 - s.kt0) * NT;
       qk(s.kt0, 0, 0);
@@ -799,9 +924,14 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       }
       steps += n;
     }
-    if (elect_one()) umma_commit(b_done);
-    __syncwarp();
-    mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
+    if (!rank) {
+      if (elect_one()) {
+        if (PAIR) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(b_done) : "memory");
+        else umma_commit(b_done);
+      }
+      __syncwarp();
+      mbar_wait_bounded(b_done, 0);  // nothing is in flight when the block leaves
+    }
   } else if (w >= 4) {
     // ---- softmax and output: two warpgroups per row tile. A row belongs to
     // two threads, which take 64 columns of a tile each and agree on its
@@ -811,7 +941,9 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     const int row = (w & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((w & 3) * 32) << 16;
     const int tok = row / a.group, head = row - tok * a.group;  // within the tile and the key-value head
-    const int my_tok = tok < t.tpt ? r * t.tpt + tok : INT32_MAX;
+    // this block's first token of the row group
+    const int tile0 = (PAIR && a.cu_q ? rank : r) * t.tpt;
+    const int my_tok = tok < t.tpt ? tile0 + tok : INT32_MAX;
     const uint32_t oa = tmem + lanes + C::O_COL + r * C::DV;
     const uint32_t b_pair = b_x + 8 * (r * 4 + (w & 3));
     int steps = 0;  // key tiles of this row tile so far
@@ -844,7 +976,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       const int pos = valid ? s.pos0 + my_tok : -1;
       const int lo = window_lo(a, max(pos, 0));
       // what every row of this tile sees: positions up to p_first, from lo_last
-      const int p_first = s.pos0 + r * t.tpt, lo_last = window_lo(a, max(s.pos0 + s.n - 1, 0));
+      const int p_first = s.pos0 + tile0, lo_last = window_lo(a, max(s.pos0 + s.n - 1, 0));
       const int shift = (s.gr.win0 - s.gr.n_sink) << t.gsh;
       float m = -INFINITY, l = 0.0f;
       for (int kt = s.kt0; kt < s.kt1; kt++, steps++) {
@@ -955,7 +1087,12 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive((ch ? b_pb : b_pa) + 8 * buf);
+        if (PAIR) {
+          __syncwarp();
+          if (lane == 0) arrive_leader((ch ? b_pb : b_pa) + 8 * buf);
+        } else {
+          mbar_arrive((ch ? b_pb : b_pa) + 8 * buf);
+        }
         float s0, s1, s2, s3;
         f2_unpack(sum[0], s0, s1);
         f2_unpack(sum[1], s2, s3);
@@ -1049,7 +1186,14 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
   __syncthreads();
   if (w == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (!PAIR) tmem_dealloc(tmem, 512);
+  }
+  if (PAIR) {
+    // tensor memory is given back by both blocks, after both are done with it;
+    // shared memory outlives the other block's arrivals
+    __syncwarp();
+    cluster_sync_all();
+    if (w == 1) tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -1059,15 +1203,17 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
 // together with their maxima.
 constexpr int AJ_THREADS = 256;
 
-template <int DT, int D, int NT>
+template <int DT, int D, int NT, bool PAIR>
 __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, const TileArgs t) {
-  using C = TileCfg<D, NT>;
+  using C = TileCfg<D, NT, PAIR>;
   constexpr int ROWS = C::JROWS;
   __shared__ int s_nan;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
   const int bid = blockIdx.x / (128 / ROWS * NT);
-  const int gang = bid / t.members, member = bid % t.members, half = member % C::HALVES, rt = member / C::HALVES;
+  const int gang = bid / t.members, member = bid % t.members;
+  const int half = PAIR ? member >> 1 & 1 : member % C::HALVES;
+  const int rt = PAIR ? (member >> 2) * 2 + (member & 1) : member / C::HALVES;
   pdl_launch_dependents();
   pdl_wait();
   const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
@@ -1165,35 +1311,36 @@ bool make_map(CUtensorMap *m, int dtype, const void *ptr, int n, const cuuint64_
 // log2 of a group's positions: groups lie within pages, and a window of W
 // positions reads up to two groups too many, so at most W / 4. (Issuing a box
 // costs the loading warp about as long as 2 KB take to arrive.)
-int box_shift(int page_size, int window) {
+int box_shift(int page_size, int window, int most) {
   int sh = 4;
-  while (sh < 7 && page_size % (32 << (sh - 4)) == 0 && (window == 0 || window / 4 >= 32 << (sh - 4))) sh++;
+  while (sh < most && page_size % (32 << (sh - 4)) == 0 && (window == 0 || window / 4 >= 32 << (sh - 4))) sh++;
   return sh;
 }
 
 struct TileFns {
   const void *tile, *join;
-  int nt, halves, jrows, threads;
+  int nt, halves, jrows, threads, span;
 };
 
-template <int DT, int D, int NT>
+template <int DT, int D, int NT, bool PAIR>
 TileFns fns() {
-  using C = TileCfg<D, NT>;
+  using C = TileCfg<D, NT, PAIR>;
   // a key tile's stages are freed one by one, a value tile's are all held at once
   static_assert(C::NST > C::VST && (NT == 1 || C::NST > 2 * C::KST) && C::NST <= 12, "ring");
-  return {(const void *)k_attn_tile<DT, D, NT>, (const void *)k_attn_join<DT, D, NT>, NT, C::HALVES, C::JROWS,
-          C::THREADS};
+  return {(const void *)k_attn_tile<DT, D, NT, PAIR>, (const void *)k_attn_join<DT, D, NT, PAIR>, NT, C::HALVES, C::JROWS, C::THREADS,
+          C::SPAN};
 }
 
 template <int DT>
-TileFns fns_of(int D, bool ragged) {
-  if (D == 64) return ragged ? fns<DT, 64, 2>() : fns<DT, 64, 1>();
-  if (D == 128) return ragged ? fns<DT, 128, 2>() : fns<DT, 128, 1>();
-  return D == 256 ? fns<DT, 256, 1>() : fns<DT, 512, 1>();
+TileFns fns_of(int D, bool ragged, bool pair) {
+  if (D == 64) return ragged ? fns<DT, 64, 2, false>() : fns<DT, 64, 1, false>();
+  if (D == 128) return ragged ? fns<DT, 128, 2, false>() : fns<DT, 128, 1, false>();
+  if (D == 256) return fns<DT, 256, 1, false>();
+  return pair ? fns<DT, 512, 1, true>() : fns<DT, 512, 1, false>();
 }
 
-TileFns tile_fns(int dtype, int D, bool ragged) {
-  return dtype == DS4MOE_DT_BF16 ? fns_of<DS4MOE_DT_BF16>(D, ragged) : fns_of<DS4MOE_DT_F16>(D, ragged);
+TileFns tile_fns(int dtype, int D, bool ragged, bool pair) {
+  return dtype == DS4MOE_DT_BF16 ? fns_of<DS4MOE_DT_BF16>(D, ragged, pair) : fns_of<DS4MOE_DT_F16>(D, ragged, pair);
 }
 
 constexpr int AT_DYN = AT_MISC + AT_SMEM;
@@ -1212,23 +1359,46 @@ size_t attn_tile_groups(int group, int D, int max_tokens, int max_seqs) {
 
 cudaError_t attn_tile_set_attributes(int dtype, int D) {
   if (!encode_fn()) return cudaErrorNotSupported;
-  for (bool ragged : {false, true}) {
-    const cudaError_t e = cudaFuncSetAttribute(tile_fns(dtype, D, ragged).tile, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_DYN);
-    if (e != cudaSuccess) return e;
-  }
+  for (bool ragged : {false, true})
+    for (bool pair : {false, true}) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(tile_fns(dtype, D, ragged, pair).tile, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_DYN);
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
+}
+
+// Pairs of blocks of dimension 512 that run at once, 0 where there are none.
+int attn_tile_pairs(int dtype, int D) {
+  if (D != 512) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  const TileFns f = tile_fns(dtype, D, true, true);
+  cfg.gridDim = dim3(2), cfg.blockDim = dim3(f.threads), cfg.dynamicSmemBytes = AT_DYN;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, f.tile, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
 }
 
 cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork &w, int n_sm, int *launches,
                              cudaStream_t s) {
   const bool ragged = a.cu_q != nullptr;
-  const TileFns f = tile_fns(dtype, D, ragged);
   TileArgs t = {};
   t.tpt = 128 / a.group;
-  t.gsh = box_shift(a.kv.page_size, a.window);
   const int row_tiles = ragged ? 1 : (a.n_new + t.tpt - 1) / t.tpt;
-  t.members = row_tiles * f.halves;
-  t.gangs = n_sm / t.members;
+  // Dimension 512, two row tiles to pair (a ragged call's row groups have two;
+  // of a decode call an even number), and pairs on nearly all SMs.
+  const bool pair = (ragged || row_tiles % 2 == 0) && w.pairs * 16 >= n_sm * 7;
+  const TileFns f = tile_fns(dtype, D, ragged, pair);
+  t.members = row_tiles * f.halves * (pair && ragged ? 2 : 1);
+  t.gangs = (pair ? std::min(n_sm, 2 * w.pairs) : n_sm) / t.members;
+  t.gsh = box_shift(a.kv.page_size, a.window, pair ? 6 : 7);
   t.first = w.first, t.info = (int2 *)w.info, t.count = w.count, t.part = w.part, t.split = (int4 *)w.split;
   TileMaps maps;
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_tok};
@@ -1241,7 +1411,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
       !make_map(&maps.v, dtype, a.kv.v, 4, kd, vs, kb))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  int span = f.nt * t.tpt;
+  int span = f.span * t.tpt;
   if (ragged && a.n_seq <= 32 && a.n_tok / span + a.n_seq <= AT_WALK) t.first = nullptr;
   if (ragged && t.first) {
     void *args[] = {(void *)&a, &span, &t.gsh, &t.first, &t.info, &t.count, (void *)&w.seq_first};
@@ -1250,7 +1420,15 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   }
   if (e == cudaSuccess) {
     void *args[] = {&maps, (void *)&a, &t};
-    e = launch_pdl(f.tile, dim3(t.gangs * t.members), dim3(f.threads), AT_DYN, s, args, true);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(t.gangs * t.members), cfg.blockDim = dim3(f.threads), cfg.dynamicSmemBytes = AT_DYN, cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = pair ? 2 : 1;
+    e = cudaLaunchKernelExC(&cfg, f.tile, args);
     ++*launches;
   }
   if (e == cudaSuccess) {
