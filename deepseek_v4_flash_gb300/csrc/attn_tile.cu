@@ -73,7 +73,7 @@ struct TileCfg {
   static constexpr int THREADS = 128 + 256 * NT;
   static constexpr int SPAN = PAIR ? 2 : NT;           // row tiles of a ragged call's row group
   static constexpr int PITCH = DV + 4;                 // floats of a partial's row: O, m, l
-  static constexpr int JROWS = 1024 / DV;              // rows of a joining block
+  static constexpr int JROWS = 4096 / DV;              // rows of a joining block
   static constexpr int O_COL = 256;                    // O's first tensor-memory column (S: 0 and 128)
   static_assert(VC * AT_CHUNK <= STAGE, "a stage holds either");
 };
@@ -1199,15 +1199,16 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
 
 // Adds up the partials of the row groups whose key tiles lie in several
 // blocks' runs, in block order. Block (gang, member, row tile, rows); a thread
-// takes four columns of one row, and the loads of four partials are in flight
-// together with their maxima.
-constexpr int AJ_THREADS = 256;
+// takes four columns of AJ_ROWS rows, whose loads of two partials each are in
+// flight together: one wave of blocks instead of four (prefill of 4096 tokens,
+// 152 split row groups, 40 MB: the kernel is all latency otherwise).
+constexpr int AJ_THREADS = 256, AJ_ROWS = 4;
 
 template <int DT, int D, int NT, bool PAIR>
 __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, const TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
-  constexpr int ROWS = C::JROWS;
-  __shared__ int s_nan;
+  constexpr int ROWS = C::JROWS, STEP = ROWS / AJ_ROWS;  // rows of the block; distance of a thread's rows
+  __shared__ unsigned long long s_nan;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
   const int bid = blockIdx.x / (128 / ROWS * NT);
@@ -1224,52 +1225,59 @@ __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, cons
   if (r0 >= rows) return;
   if (tid == 0) s_nan = 0;
   __syncthreads();
-  const int row = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
-  if (row < rows) {
-    // the block where the item starts holds it in its second slot, the others in their first
-    auto at = [&](int p) {
-      const int slot = 2 * (bid + p * t.members) + (p == 0 ? 1 : 0);
-      return t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH;
-    };
-    float m = -INFINITY, l = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int p0 = 0; p0 < parts; p0 += 4) {
-      float2 ml[4];
-      float4 y[4];
-      float mn = m;
+  const int row0 = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
+  float m[AJ_ROWS], l[AJ_ROWS];
+  float4 x[AJ_ROWS];
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        ml[i] = make_float2(-INFINITY, 0.0f), y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (p0 + i < parts) {
-          const float *q = at(p0 + i);
-          ml[i] = *reinterpret_cast<const float2 *>(q + C::DV), y[i] = *reinterpret_cast<const float4 *>(q + c);
+  for (int k = 0; k < AJ_ROWS; k++) m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p0 = 0; p0 < parts; p0 += 2) {
+    float2 ml[AJ_ROWS][2];
+    float4 y[AJ_ROWS][2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      // the block where the item starts holds it in its second slot, the others in their first
+      const int slot = 2 * (bid + (p0 + i) * t.members) + (p0 + i == 0 ? 1 : 0);
+      const float *q0 = t.part + ((size_t)(slot * NT + r) * 128 + row0) * C::PITCH;
+#pragma unroll
+      for (int k = 0; k < AJ_ROWS; k++) {
+        ml[k][i] = make_float2(-INFINITY, 0.0f), y[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p0 + i < parts && row0 + k * STEP < rows) {
+          const float *q = q0 + (size_t)k * STEP * C::PITCH;
+          ml[k][i] = *reinterpret_cast<const float2 *>(q + C::DV), y[k][i] = *reinterpret_cast<const float4 *>(q + c);
         }
       }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; i++) mn = fmaxf(mn, ml[i].x);
-      const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
-      l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-      m = mn;
+    for (int k = 0; k < AJ_ROWS; k++) {
+      const float mn = max3(m[k], ml[k][0].x, ml[k][1].x);
+      const float f = mn == -INFINITY ? 1.0f : ex2(m[k] - mn);
+      m[k] = mn, l[k] *= f, x[k].x *= f, x[k].y *= f, x[k].z *= f, x[k].w *= f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float g = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - mn);
-        l = fmaf(g, ml[i].y, l);
-        x.x = fmaf(g, y[i].x, x.x), x.y = fmaf(g, y[i].y, x.y), x.z = fmaf(g, y[i].z, x.z), x.w = fmaf(g, y[i].w, x.w);
+      for (int i = 0; i < 2; i++) {
+        const float g = ml[k][i].x == -INFINITY ? 0.0f : ex2(ml[k][i].x - mn);
+        const float4 z = y[k][i];
+        l[k] = fmaf(g, ml[k][i].y, l[k]);
+        x[k].x = fmaf(g, z.x, x[k].x), x[k].y = fmaf(g, z.y, x[k].y), x[k].z = fmaf(g, z.z, x[k].z), x[k].w = fmaf(g, z.w, x[k].w);
       }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-    if (x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w) atomicOr(&s_nan, 1 << (row - r0));
+  }
+#pragma unroll
+  for (int k = 0; k < AJ_ROWS; k++) {
+    const int row = row0 + k * STEP;
+    if (row >= rows) continue;
+    const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+    const float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
+    if (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w) atomicOr(&s_nan, 1ull << (row - r0));
     const int tok = row / a.group, h = d0.z * a.group + row % a.group;
     *reinterpret_cast<uint2 *>(a.out + (long long)(d1.x + tok0 + tok) * a.out_stride + (long long)h * D + half * C::DV + c) =
-        make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
+        make_uint2(Half16<DT>::down(z.x, z.y), Half16<DT>::down(z.z, z.w));
   }
   __syncthreads();
-  const int again = s_nan;
-  for (int i = tid >> 5; i < ROWS; i += AJ_THREADS / 32)
+  const unsigned long long again = s_nan;
+  for (int i = tid >> 5; again && i < ROWS; i += AJ_THREADS / 32)
     if (again >> i & 1) {
-      const int rw = r0 + i, tok = tok0 + rw / a.group;
-      redo_row_cols<DT, D>(a, d1.x + tok, d0.z * a.group + rw % a.group, d0.y, d0.w + tok, half * C::DV,
+      const int row = r0 + i, tok = tok0 + row / a.group;
+      redo_row_cols<DT, D>(a, d1.x + tok, d0.z * a.group + row % a.group, d0.y, d0.w + tok, half * C::DV,
                            (half + 1) * C::DV);
     }
 }
