@@ -4,7 +4,7 @@
 //
 // One pass over the visible positions in tiles of up to 128:
 //   S = Q K^T           tcgen05.mma, Q and K in shared memory, S in tensor memory
-//   P = 2^(S c - m)     a warpgroup, one thread per row: no cross-lane sums
+//   P = 2^(S c - m)     two warpgroups, two threads per row
 //   O += P V            tcgen05.mma, P in tensor memory (over S), V in shared memory
 // with m the running maximum of a row. m only follows a new maximum that is
 // more than 2^AT_LAZY above it, so that O is rarely rescaled (weights up to
@@ -12,18 +12,29 @@
 // not depend on m).
 //
 // Warps: 0 loads (TMA out of the pages, a ring of stages), 1 issues the
-// products, 2 works out which tiles come next, one warpgroup per row tile does
+// products, 2 works out which tiles come next, two warpgroups per row tile do
 // the softmax and the output. Two tiles of S are in flight: while one is
-// turned into P, the next one's product runs. Head dimension 64 and 128 (ragged calls): two row
-// tiles per block share every key and value tile, which halves the traffic
-// from L2. Dimension 512: O has 512 columns and S needs room too, so a block
-// computes one half of O's columns (S is then computed twice).
+// turned into P, the next one's product runs.
+//   Head dimension 64 and 128, ragged calls: two row tiles per block share
+//     every key and value tile, which halves the traffic from L2. Bound by a
+//     row tile's chain S -> P -> O -> next S, two of which alternate (4096
+//     tokens of 32/8 heads of 128: 122 us, 1126 TFLOP/s; one thread per row
+//     192 us, as the chain was twice as long in the softmax).
+//   Dimension 512: O has 512 columns and S needs room too, so a block computes
+//     one half of O's columns (S is then computed twice), and Q takes 128 of
+//     224 KB. Two row tiles therefore work as a pair of blocks (cta_group::2):
+//     one product has 256 rows, each block holds half of the keys' rows and of
+//     the values' columns, and what comes through L2 and the ring per row
+//     halves (4096 tokens of 16 heads: 297 us alone, 238 us in pairs, 1154
+//     TFLOP/s and half as much again for the second S; the products' own
+//     3072 cycles per 128 positions are reached). A single row tile (a decode
+//     call of up to 128 rows) runs alone.
 //
 // Visible positions are listed in groups (the first positions' groups, then
 // the windows' groups), one TMA box each, and a tile is 128 positions of that
-// list. Small windows take groups of 16: a window of 128 positions costs 9 or
-// 10 of them, not 3 tiles of 128. Else groups are as large as the pages allow
-// (see box_rows).
+// list. Small windows take groups of 16 to 32: a window of 128 positions costs
+// 160 to 192 of them, not 3 tiles of 128. Else groups are as large as the pages
+// allow (see box_shift).
 //
 // The call's tiles, in order, are dealt to the blocks in equal contiguous
 // runs. A row tile whose positions lie in several runs leaves one partial
