@@ -3,6 +3,8 @@
 // (ds4moe_verify_drafts).
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -65,24 +67,27 @@ __device__ __forceinline__ float exp_over_t(float d, const ExpScale &c) {
   return __fmaf_rn(e, err * 0.693147180559945f, e);
 }
 
-// Entries i .. i + 3 of a row (those below end; `fill` elsewhere). `inner`: the
-// whole block's, or warp's, four entries are known to lie below end.
-template <bool VEC>
+// Four entries of a row (those below end; `fill` elsewhere): i .. i + 3 in one
+// access where rows are 16-byte aligned, else i, i + S, i + 2 S, i + 3 S, so
+// that neighbouring threads take neighbouring entries. `inner`: the whole
+// block's, or warp's, entries are known to lie below end.
+template <bool VEC, int S>
 __device__ __forceinline__ float4 row4(const float *r, int i, int end, float fill, bool inner = false) {
   if (VEC && (inner || i + 3 < end)) return *reinterpret_cast<const float4 *>(r + i);
-  return make_float4(i < end ? r[i] : fill, i + 1 < end ? r[i + 1] : fill, i + 2 < end ? r[i + 2] : fill,
-                     i + 3 < end ? r[i + 3] : fill);
+  if (inner) return make_float4(r[i], r[i + S], r[i + 2 * S], r[i + 3 * S]);
+  return make_float4(i < end ? r[i] : fill, i + S < end ? r[i + S] : fill, i + 2 * S < end ? r[i + 2 * S] : fill,
+                     i + 3 * S < end ? r[i + 3 * S] : fill);
 }
-template <bool VEC>
+template <bool VEC, int S>
 __device__ __forceinline__ void put4(float *o, int i, int end, float4 v, bool inner = false) {
   if (VEC && (inner || i + 3 < end)) {
     *reinterpret_cast<float4 *>(o + i) = v;
     return;
   }
-  if (i < end) o[i] = v.x;
-  if (i + 1 < end) o[i + 1] = v.y;
-  if (i + 2 < end) o[i + 2] = v.z;
-  if (i + 3 < end) o[i + 3] = v.w;
+  if (inner || i < end) o[i] = v.x;
+  if (inner || i + S < end) o[i + S] = v.y;
+  if (inner || i + 2 * S < end) o[i + 2 * S] = v.z;
+  if (inner || i + 3 * S < end) o[i + 3 * S] = v.w;
 }
 
 // Softmax of one row per cluster, bound by the row's bytes (read once, written
@@ -105,18 +110,20 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
   const long long row = blockIdx.x / n_blk;
   const float *r = x + row * xs;
   float *o = out + row * os;
+  constexpr int S = VEC ? 1 : PR_THREADS;  // between a thread's entries
+  const int lead = VEC ? 4 * tid : tid;
   const int part = ((V + n_blk - 1) / n_blk + 3) & ~3;
   const int begin = min(V, rank * part), end = min(V, begin + part);
   float4 v[SP_KEEP];
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++)
-    v[k] = row4<VEC>(r, begin + 4 * (tid + k * PR_THREADS), end, -INFINITY, begin + 4 * (k + 1) * PR_THREADS <= end);
-  const int rest = begin + 4 * (tid + SP_KEEP * PR_THREADS);
+    v[k] = row4<VEC, S>(r, begin + lead + 4 * k * PR_THREADS, end, -INFINITY, begin + 4 * (k + 1) * PR_THREADS <= end);
+  const int rest = begin + lead + 4 * SP_KEEP * PR_THREADS;
   float m = -INFINITY;
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) m = fmaxf(fmaxf(fmaxf(m, v[k].x), fmaxf(v[k].y, v[k].z)), v[k].w);
   for (int i = rest; i < end; i += 4 * PR_THREADS) {
-    const float4 y = row4<VEC>(r, i, end, -INFINITY);
+    const float4 y = row4<VEC, S>(r, i, end, -INFINITY);
     m = fmaxf(fmaxf(fmaxf(m, y.x), fmaxf(y.y, y.z)), y.w);
   }
   m = warp_max(m);
@@ -133,12 +140,12 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
     };
 #pragma unroll
     for (int k = 0; k < SP_KEEP; k++) {
-      const int i = begin + 4 * (tid + k * PR_THREADS);
-      look(v[k].x, i), look(v[k].y, i + 1), look(v[k].z, i + 2), look(v[k].w, i + 3);
+      const int i = begin + lead + 4 * k * PR_THREADS;
+      look(v[k].x, i), look(v[k].y, i + S), look(v[k].z, i + 2 * S), look(v[k].w, i + 3 * S);
     }
     for (int i = rest; i < end; i += 4 * PR_THREADS) {
-      const float4 y = row4<VEC>(r, i, end, -INFINITY);
-      look(y.x, i), look(y.y, i + 1), look(y.z, i + 2), look(y.w, i + 3);
+      const float4 y = row4<VEC, S>(r, i, end, -INFINITY);
+      look(y.x, i), look(y.y, i + S), look(y.z, i + 2 * S), look(y.w, i + 3 * S);
     }
     at = __reduce_min_sync(0xffffffffu, at);
     if (lane == 0) si[w] = at;
@@ -157,9 +164,9 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
     }
     cluster_sync();  // a block's shared memory outlives its readers
     const bool bad = best != best;
-    for (int i = begin + 4 * tid; i < end; i += 4 * PR_THREADS) {
+    for (int i = begin + lead; i < end; i += 4 * PR_THREADS) {
       const float one[2] = {bad ? NAN : 0.0f, bad ? NAN : 1.0f};
-      put4<VEC>(o, i, end, make_float4(one[i == where], one[i + 1 == where], one[i + 2 == where], one[i + 3 == where]));
+      put4<VEC, S>(o, i, end, make_float4(one[i == where], one[i + S == where], one[i + 2 * S == where], one[i + 3 * S == where]));
     }
     return;
   }
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
     sum += (v[k].x + v[k].y) + (v[k].z + v[k].w);
   }
   for (int i = rest; i < end; i += 4 * PR_THREADS) {
-    const float4 y = row4<VEC>(r, i, end, -INFINITY);
+    const float4 y = row4<VEC, S>(r, i, end, -INFINITY);
     sum += (e(y.x) + e(y.y)) + (e(y.z) + e(y.w));
   }
 #pragma unroll
@@ -202,13 +209,13 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
   const float f = (m == -INFINITY ? 0.0f : exp_over_t(m - top, c)) / total;
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) {
-    const int i = begin + 4 * (tid + k * PR_THREADS);
-    put4<VEC>(o, i, end, make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f),
+    const int i = begin + lead + 4 * k * PR_THREADS;
+    put4<VEC, S>(o, i, end, make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f),
               begin + 4 * (k + 1) * PR_THREADS <= end);
   }
   for (int i = rest; i < end; i += 4 * PR_THREADS) {
-    const float4 y = row4<VEC>(r, i, end, -INFINITY);
-    put4<VEC>(o, i, end, make_float4(e(y.x) * f, e(y.y) * f, e(y.z) * f, e(y.w) * f));
+    const float4 y = row4<VEC, S>(r, i, end, -INFINITY);
+    put4<VEC, S>(o, i, end, make_float4(e(y.x) * f, e(y.y) * f, e(y.z) * f, e(y.w) * f));
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -318,26 +325,28 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
   const int i0 = min(a.V, (rank * SP_WARPS + w) * per), i1 = min(a.V, i0 + per);
   const int lo_bits = a.shift - 22;
   const float lo_scale = (float)(1 << lo_bits);
-  // hi and lo of four entries
-  auto four = [&](int i, int (&hi)[4], int (&lo)[4], bool inner) {
-    const float4 x = row4<VEC>(p, i, i1, 0.0f, inner);
-    const float4 y = q ? row4<VEC>(q, i, i1, 0.0f, inner) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // hi and lo of four entries, `step` apart
+  constexpr int S = VEC ? 1 : 32;
+  auto four = [&](auto step, int i, int (&hi)[4], int (&lo)[4], bool inner) {
+    constexpr int N = decltype(step)::value;
+    const float4 x = row4<VEC, N>(p, i, i1, 0.0f, inner);
+    const float4 y = q ? row4<VEC, N>(q, i, i1, 0.0f, inner) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float px[4] = {x.x, x.y, x.z, x.w}, qx[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int k = 0; k < 4; k++) {
       mass_of(px[k], qx[k], lo_scale, hi[k], lo[k]);
-      if (dtok >= 0 && i + k == dtok) hi[k] = lo[k] = 0;
+      if (dtok >= 0 && i + k * N == dtok) hi[k] = lo[k] = 0;
     }
   };
   long long total = 0, before = 0, mine = 0;
   for (int round = 0; round < 2; round++) {
     long long s = 0;
-    for (int c = i0 + 4 * lane; c < i1; c += 8 * 128) {
+    for (int c = i0 + (VEC ? 4 * lane : lane); c < i1; c += 8 * 128) {
       int sh = 0, sl = 0;  // 32 entries: |hi|, |lo| < 2^28
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         int hi[4], lo[4];
-        four(c + 128 * k, hi, lo, c - 4 * lane + 128 * (k + 1) <= i1);
+        four(std::integral_constant<int, S>(), c + 128 * k, hi, lo, c - (VEC ? 4 * lane : lane) + 128 * (k + 1) <= i1);
         sh += (hi[0] + hi[1]) + (hi[2] + hi[3]), sl += (lo[0] + lo[1]) + (lo[2] + lo[3]);
       }
       s += ((long long)sh << lo_bits) + sl;
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
     if (before <= thr && thr < before + mine) {
       for (int c = i0; c < i1; c += 128) {
         int hi[4], lo[4];
-        four(c + 4 * lane, hi, lo, c + 128 <= i1);
+        four(std::integral_constant<int, 1>(), c + 4 * lane, hi, lo, c + 128 <= i1);
         long long e[4];
 #pragma unroll
         for (int k = 0; k < 4; k++) e[k] = ((long long)hi[k] << lo_bits) + lo[k] + (k ? e[k - 1] : 0);
@@ -432,6 +441,13 @@ bool sp_dev_ptr(const void *p) {
   return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
 }
 
+// SMs of the current device, 0 on an error.
+int sp_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
 ds4moe_status sp_status(cudaError_t e) {
   if (e == cudaSuccess) return DS4MOE_OK;
   cudaGetLastError();
@@ -457,8 +473,14 @@ ds4moe_status ds4moe_token_probs(const float *logits, int64_t logits_stride, int
   long long xs = logits_stride, os = probs_stride;
   void *args[] = {(void *)&logits, &xs, &vocab, &c, (void *)&probs, &os};
   const bool vec = (n_rows == 1 || (xs % 4 == 0 && os % 4 == 0)) && ((uintptr_t)logits & 15) == 0 && ((uintptr_t)probs & 15) == 0;
+  // Many rows: as few blocks per row as keep a part in registers (320 rows of
+  // 50001: 63 -> 39 us); few: as many as share the latency.
+  const int n_sm = sp_sms();
+  if (!n_sm) return sp_status(cudaErrorUnknown);
+  int cluster = cluster_of(vocab);
+  while (cluster > 1 && (long long)n_rows * cluster > 2 * n_sm && vocab <= cluster / 2 * SP_KEEP * 4 * PR_THREADS) cluster /= 2;
   return sp_status(launch_rows(vec ? (const void *)k_token_probs<true> : (const void *)k_token_probs<false>, n_rows,
-                               cluster_of(vocab), PR_THREADS, (cudaStream_t)stream, args));
+                               cluster, PR_THREADS, (cudaStream_t)stream, args));
 }
 
 ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
@@ -486,9 +508,8 @@ ds4moe_status ds4moe_verify_drafts(const float *target, int64_t target_stride, c
   void *args[] = {&a};
   // Smaller clusters where a batch would not be resident at once (two blocks
   // per SM): a second wave of short blocks costs as much as the first.
-  int dev = 0, n_sm = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return sp_status(cudaErrorUnknown);
+  const int n_sm = sp_sms();
+  if (!n_sm) return sp_status(cudaErrorUnknown);
   int cluster = cluster_of(vocab);
   while (cluster > 1 && (long long)n_seq * cluster > 2 * n_sm) cluster /= 2;
   return sp_status(launch_rows(vec ? (const void *)k_verify_drafts<true> : (const void *)k_verify_drafts<false>, n_seq,
