@@ -84,7 +84,7 @@ struct TileCfg {
   static constexpr int THREADS = 128 + 256 * NT;
   static constexpr int SPAN = PAIR ? 2 : NT;           // row tiles of a ragged call's row group
   static constexpr int PITCH = DV + 4;                 // floats of a partial's row: O, m, l
-  static constexpr int JROWS = 4096 / DV;              // rows of a joining block
+  static constexpr int JROWS = 1024 / DV;              // rows that a joining block's threads cover at once
   static constexpr int O_COL = 256;                    // O's first tensor-memory column (S: 0 and 128)
   static_assert(VC * AT_CHUNK <= STAGE, "a stage holds either");
 };
@@ -1210,15 +1210,16 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
 
 // Adds up the partials of the row groups whose key tiles lie in several
 // blocks' runs, in block order. Block (gang, member, row tile, rows); a thread
-// takes four columns of AJ_ROWS rows, whose loads of two partials each are in
-// flight together: one wave of blocks instead of four (prefill of 4096 tokens,
-// 152 split row groups, 40 MB: the kernel is all latency otherwise).
-constexpr int AJ_THREADS = 256, AJ_ROWS = 4;
+// takes four columns of R rows, with 8 / R partials of each in flight. The
+// kernel is all latency: ragged calls (many split row groups of two or three
+// partials) take R = 4, one wave of blocks instead of four; decode calls (few
+// rows, up to a partial per gang) R = 1, four times the threads.
+constexpr int AJ_THREADS = 256;
 
-template <int DT, int D, int NT, bool PAIR>
+template <int DT, int D, int NT, bool PAIR, int R>
 __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, const TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
-  constexpr int ROWS = C::JROWS, STEP = ROWS / AJ_ROWS;  // rows of the block; distance of a thread's rows
+  constexpr int ROWS = C::JROWS * R, STEP = C::JROWS, P = 8 / R;  // rows of the block; distance of a thread's rows
   __shared__ unsigned long long s_nan;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
@@ -1237,20 +1238,20 @@ __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, cons
   if (tid == 0) s_nan = 0;
   __syncthreads();
   const int row0 = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
-  float m[AJ_ROWS], l[AJ_ROWS];
-  float4 x[AJ_ROWS];
+  float m[R], l[R];
+  float4 x[R];
 #pragma unroll
-  for (int k = 0; k < AJ_ROWS; k++) m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int p0 = 0; p0 < parts; p0 += 2) {
-    float2 ml[AJ_ROWS][2];
-    float4 y[AJ_ROWS][2];
+  for (int k = 0; k < R; k++) m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p0 = 0; p0 < parts; p0 += P) {
+    float2 ml[R][P];
+    float4 y[R][P];
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < P; i++) {
       // the block where the item starts holds it in its second slot, the others in their first
       const int slot = 2 * (bid + (p0 + i) * t.members) + (p0 + i == 0 ? 1 : 0);
       const float *q0 = t.part + ((size_t)(slot * NT + r) * 128 + row0) * C::PITCH;
 #pragma unroll
-      for (int k = 0; k < AJ_ROWS; k++) {
+      for (int k = 0; k < R; k++) {
         ml[k][i] = make_float2(-INFINITY, 0.0f), y[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (p0 + i < parts && row0 + k * STEP < rows) {
           const float *q = q0 + (size_t)k * STEP * C::PITCH;
@@ -1259,12 +1260,14 @@ __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, cons
       }
     }
 #pragma unroll
-    for (int k = 0; k < AJ_ROWS; k++) {
-      const float mn = max3(m[k], ml[k][0].x, ml[k][1].x);
+    for (int k = 0; k < R; k++) {
+      float mn = m[k];
+#pragma unroll
+      for (int i = 0; i < P; i++) mn = fmaxf(mn, ml[k][i].x);
       const float f = mn == -INFINITY ? 1.0f : ex2(m[k] - mn);
       m[k] = mn, l[k] *= f, x[k].x *= f, x[k].y *= f, x[k].z *= f, x[k].w *= f;
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
+      for (int i = 0; i < P; i++) {
         const float g = ml[k][i].x == -INFINITY ? 0.0f : ex2(ml[k][i].x - mn);
         const float4 z = y[k][i];
         l[k] = fmaf(g, ml[k][i].y, l[k]);
@@ -1273,7 +1276,7 @@ __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, cons
     }
   }
 #pragma unroll
-  for (int k = 0; k < AJ_ROWS; k++) {
+  for (int k = 0; k < R; k++) {
     const int row = row0 + k * STEP;
     if (row >= rows) continue;
     const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
@@ -1342,20 +1345,21 @@ struct TileFns {
 };
 
 template <int DT, int D, int NT, bool PAIR>
-TileFns fns() {
+TileFns fns(bool ragged) {
   using C = TileCfg<D, NT, PAIR>;
   // a key tile's stages are freed one by one, a value tile's are all held at once
   static_assert(C::NST > C::VST && (NT == 1 || C::NST > 2 * C::KST) && C::NST <= 12, "ring");
-  return {(const void *)k_attn_tile<DT, D, NT, PAIR>, (const void *)k_attn_join<DT, D, NT, PAIR>, NT, C::HALVES, C::JROWS, C::THREADS,
-          C::SPAN};
+  return {(const void *)k_attn_tile<DT, D, NT, PAIR>,
+          ragged ? (const void *)k_attn_join<DT, D, NT, PAIR, 4> : (const void *)k_attn_join<DT, D, NT, PAIR, 1>,
+          NT, C::HALVES, C::JROWS * (ragged ? 4 : 1), C::THREADS, C::SPAN};
 }
 
 template <int DT>
 TileFns fns_of(int D, bool ragged, bool pair) {
-  if (D == 64) return ragged ? fns<DT, 64, 2, false>() : fns<DT, 64, 1, false>();
-  if (D == 128) return ragged ? fns<DT, 128, 2, false>() : fns<DT, 128, 1, false>();
-  if (D == 256) return fns<DT, 256, 1, false>();
-  return pair ? fns<DT, 512, 1, true>() : fns<DT, 512, 1, false>();
+  if (D == 64) return ragged ? fns<DT, 64, 2, false>(ragged) : fns<DT, 64, 1, false>(ragged);
+  if (D == 128) return ragged ? fns<DT, 128, 2, false>(ragged) : fns<DT, 128, 1, false>(ragged);
+  if (D == 256) return fns<DT, 256, 1, false>(ragged);
+  return pair ? fns<DT, 512, 1, true>(ragged) : fns<DT, 512, 1, false>(ragged);
 }
 
 TileFns tile_fns(int dtype, int D, bool ragged, bool pair) {
@@ -1410,10 +1414,13 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   const bool ragged = a.cu_q != nullptr;
   TileArgs t = {};
   t.tpt = 128 / a.group;
-  const int row_tiles = ragged ? 1 : (a.n_new + t.tpt - 1) / t.tpt;
-  // Dimension 512, two row tiles to pair (a ragged call's row groups have two;
-  // of a decode call an even number), and pairs on nearly all SMs.
-  const bool pair = (ragged || row_tiles % 2 == 0) && w.pairs * 16 >= n_sm * 7;
+  int row_tiles = ragged ? 1 : (a.n_new + t.tpt - 1) / t.tpt;
+  // Dimension 512: pairs, where they fit nearly all SMs, for two row tiles and
+  // more (a ragged call's row groups have two; an odd one of a decode call goes
+  // with an empty one: three, 8 sequences of 16384, 145 us alone, 127 us so; a
+  // single one 70 us alone, 75 us so).
+  const bool pair = (ragged || row_tiles > 1) && w.pairs * 16 >= n_sm * 7;
+  if (pair && !ragged) row_tiles = (row_tiles + 1) & ~1;
   const TileFns f = tile_fns(dtype, D, ragged, pair);
   t.members = row_tiles * f.halves * (pair && ragged ? 2 : 1);
   t.gangs = (pair ? std::min(n_sm, 2 * w.pairs) : n_sm) / t.members;
