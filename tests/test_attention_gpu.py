@@ -65,6 +65,15 @@ def test_decode_several_tokens(heads, kv, dim, new):
     _run_decode("bf16", heads, kv, dim, 32, 0, 0, new, LENS, seed=new)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,kv,new", [(64, 1, 2), (64, 1, 5), (64, 1, 16), (128, 1, 1), (128, 1, 5), (16, 2, 16), (20, 4, 13)])
+def test_decode_pairs_of_row_tiles(kind, heads, kv, new):
+    """Dimension 512: one row tile, an even and an odd number of them, tiles
+    that the group of heads does not fill, over whole and windowed caches."""
+    _run_decode(kind, heads, kv, 512, 64, 0, 0, new, LENS + [5000], seed=new)
+    _run_decode(kind, heads, kv, 512, 16, 150, 20, new, LENS + [2000], seed=new + 1)
+
+
 @pytest.mark.parametrize("window,sink", [(1, 0), (1, 1), (16, 0), (100, 4), (128, 4), (129, 40), (300, 200), (5000, 7)])
 @pytest.mark.parametrize("heads,kv,dim,new", [(8, 2, 128, 1), (4, 4, 64, 3), (64, 1, 512, 2), (8, 1, 256, 4)])
 def test_decode_window(window, sink, heads, kv, dim, new):
