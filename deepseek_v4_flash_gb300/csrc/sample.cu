@@ -193,20 +193,22 @@ __global__ void __launch_bounds__(PR_THREADS, 2) k_token_probs(const float *x, l
     for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     if (lane == 0) pub[0] = m, pub[1] = sum;
   }
-  float top = -INFINITY, total = 0.0f;
   cluster_sync();
-  float pm[8], ps[8];
+  if (w == 0) {
+    // one warp, a lane per block: the row's maximum and sum, this block's factor
+    const float pm = lane < n_blk ? __uint_as_float(ld_peer(&pub[0], lane)) : -INFINITY;
+    const float ps = lane < n_blk ? __uint_as_float(ld_peer(&pub[1], lane)) : 0.0f;
+    const float top = warp_max(pm);
+    float total = pm == -INFINITY ? ps : ps * exp_over_t(pm - top, c);
 #pragma unroll
-  for (int b = 0; b < 8; b++)
-    if (b < n_blk) pm[b] = __uint_as_float(ld_peer(&pub[0], b)), ps[b] = __uint_as_float(ld_peer(&pub[1], b));
-    else pm[b] = -INFINITY, ps[b] = 0.0f;
-#pragma unroll
-  for (int b = 0; b < 8; b++) top = fmaxf(top, pm[b]);
-#pragma unroll
-  for (int b = 0; b < 8; b++) total += pm[b] == -INFINITY ? ps[b] : ps[b] * exp_over_t(pm[b] - top, c);
+    for (int k = 4; k; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+    if (lane == 0) ss[0] = (m == -INFINITY ? 0.0f : exp_over_t(m - top, c)) / total;
+  }
   // a block's shared memory outlives its readers (nothing is handed over: relaxed)
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const float f = (m == -INFINITY ? 0.0f : exp_over_t(m - top, c)) / total;
+  __syncthreads();
+  const float f = ss[0];
 #pragma unroll
   for (int k = 0; k < SP_KEEP; k++) {
     const int i = begin + lead + 4 * k * PR_THREADS;
