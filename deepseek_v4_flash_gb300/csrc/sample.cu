@@ -287,6 +287,7 @@ template <bool VEC>
 __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a) {
   __shared__ long long part[SP_WARPS];
   __shared__ __align__(8) int pub[2];  // this block's sum, low and high word
+  __shared__ long long s_sum[2];  // of all blocks, of those before this one
   __shared__ int s_n;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int rank = cluster_rank(), n_blk = cluster_size(), b = blockIdx.x / n_blk;
@@ -361,12 +362,14 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
       if (lane == 0) pub[0] = (int)(uint32_t)t, pub[1] = (int)(t >> 32);
     }
     cluster_sync();
-    total = before = 0;
-    for (int i = 0; i < n_blk; i++) {
-      const long long t = (long long)ld_peer(&pub[0], i) | (long long)ld_peer(&pub[1], i) << 32;
-      if (i < rank) before += t;
-      total += t;
+    if (w == 0) {
+      const long long t =
+          lane < n_blk ? (long long)ld_peer(&pub[0], lane) | (long long)ld_peer(&pub[1], lane) << 32 : 0;
+      const long long all = warp_sum64(t), mine_from = warp_sum64(lane < rank ? t : 0);
+      if (lane == 0) s_sum[0] = all, s_sum[1] = mine_from;
     }
+    __syncthreads();
+    total = s_sum[0], before = s_sum[1];
     for (int i = 0; i < w; i++) before += part[i];
     // read by all before it is written again or the block leaves
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
