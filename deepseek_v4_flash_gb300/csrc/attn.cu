@@ -13,7 +13,8 @@ namespace ds4 {
 
 // Copies rows of new keys and values to their places in the pages, rounding
 // to the cache's type. One thread per 8 elements (16 bytes of the cache);
-// neighbouring threads take neighbouring elements of a row.
+// neighbouring threads take neighbouring elements of a row. Bound by the bytes:
+// 12291 tokens of 8 x 128 from fp32 25.5 us, 5.9 TB/s.
 struct AppendArgs {
   KvView kv;
   const void *k, *v;           // v null: the keys only
