@@ -27,7 +27,7 @@
 //     the values' columns, and what comes through L2 and the ring per row
 //     halves (4096 tokens of 16 heads: 297 us alone, 238 us in pairs, 1154
 //     TFLOP/s and half as much again for the second S; the products' own
-//     3072 cycles per 128 positions are reached). A single row tile (a decode
+//     24 cycles per position are reached). A single row tile (a decode
 //     call of up to 128 rows) runs alone.
 //
 // Visible positions are listed in groups (the first positions' groups, then
