@@ -63,6 +63,11 @@ constexpr int AT_MISC = 3 * 1024;       // what precedes them: barriers, segment
 // row groups, of one or two tiles each, would have three times the items of
 // the others.
 constexpr int AT_ITEM = 2;
+// Most tiles of an item that is never split, 4 drafted tokens with 64 heads
+// over one of 512: window 64, 1 and 64 sequences, 10.2 and 16.7 us whole, 17.2
+// and 23.4 us as equal runs and their join; window 600 (7 tiles), 17.9 and 37.3
+// us against 19.1 and 53.8 us; dimension 128 and one sequence is even there.
+constexpr int AT_WHOLE = 8;
 constexpr int AT_WALK = 512;            // most row groups that every block walks through itself
 constexpr int AT_SEGS = 4;              // segments the scheduling warp is ahead
 
@@ -97,8 +102,9 @@ struct TileMaps {
 struct TileArgs {
   int gsh;           // log2 of a group's positions
   int tpt;           // tokens of a row tile: 128 / group
-  int members;       // blocks that work on the same (item, key tiles): row tiles x halves, or halves
+  int members;       // blocks that work on the same (item, key tiles): row tiles (decode calls, pairs) x halves
   int gangs;
+  int whole;         // items are not split: each goes to the block whose run holds its first unit
   long long *first;  // ragged: first unit of each row group, then the total (k_attn_plan); null: no plan
   int2 *info;        // ragged: {sequence, first token of the row group in it}
   int *count;        // ragged: number of row groups
@@ -423,37 +429,45 @@ struct Sched {
         r -= __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    if (u - item0 <= AT_ITEM) u = item0;  // before the item's first tile: all of it
+    if (t.whole) {
+      if (u != item0) advance(a, t);
+      u = item0;
+    } else if (u - item0 <= AT_ITEM) {
+      u = item0;  // before the item's first tile: all of it
+    }
     return true;
   }
 
+  // The next item; item0 = U after the last one.
+  __device__ __forceinline__ void advance(const AttnArgs &a, const TileArgs &t) {
+    bool bad = false;
+    item0 = item1;
+    if (item0 >= U) return;
+    if (a.cu_q) {
+      SeqInfo si = seq_info(a, b, bad);
+      for (t0 += span; t0 >= si.n; t0 = 0) {
+        if (++b == a.n_seq) b = 0, kvh++;
+        si = seq_info(a, b, bad);
+        if (si.n > 0) {
+          t0 = 0;
+          break;
+        }
+      }
+      item1 = item0 + units(a, t.gsh, si, t0, min(span, si.n - t0));
+    } else {
+      if (++kvh == a.n_kv) kvh = 0, b++;
+      item1 = item0 + seq_units(a, t.gsh, b, bad);
+    }
+  }
+
   __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, Seg &s) {
-    if (u >= u1 || (u1 < item1 && u1 - item0 <= AT_ITEM)) return false;  // (the next gang's from its start)
+    if (u >= u1 || (!t.whole && u1 < item1 && u1 - item0 <= AT_ITEM)) return false;  // (the next gang's from its start)
     const int n_kt = load(a, t, member_rt, s);
-    const long long e = item1 < u1 ? item1 : u1;
+    const long long e = t.whole || item1 < u1 ? item1 : u1;
     s.starts = u == item0, s.ends = e == item1;
     s.kt0 = max(0, (int)(u - item0) - AT_ITEM), s.kt1 = min(n_kt, (int)(e - item0) - AT_ITEM);
     u = e;
-    if (u == item1 && u < u1) {
-      // the next item
-      bool bad = false;
-      item0 = item1;
-      if (a.cu_q) {
-        SeqInfo si = seq_info(a, b, bad);
-        for (t0 += span; t0 >= si.n; t0 = 0) {
-          if (++b == a.n_seq) b = 0, kvh++;
-          si = seq_info(a, b, bad);
-          if (si.n > 0) {
-            t0 = 0;
-            break;
-          }
-        }
-        item1 = item0 + units(a, t.gsh, si, t0, min(span, si.n - t0));
-      } else {
-        if (++kvh == a.n_kv) kvh = 0, b++;
-        item1 = item0 + seq_units(a, t.gsh, b, bad);
-      }
-    }
+    if (u == item1 && u < u1) advance(a, t);
     return true;
   }
 };
@@ -620,7 +634,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     if (tid == 0) raise_flag(a.err, DS4MOE_DEVERR_INTERNAL);
     return;
   }
-  const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members;  // 
+  const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members;
   // which half of O's columns, which row tile of the row group (ragged pairs) or sequence (decode calls)
   const int rank = PAIR ? member & 1 : 0;
   const int half = PAIR ? member >> 1 & 1 : member % C::HALVES, rt = PAIR ? (member >> 2) * 2 + rank : member / C::HALVES;
@@ -1425,6 +1439,10 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   t.members = row_tiles * f.halves * (pair && ragged ? 2 : 1);
   t.gangs = (pair ? std::min(n_sm, 2 * w.pairs) : n_sm) / t.members;
   t.gsh = box_shift(a.kv.page_size, a.window, pair ? 6 : 7);
+  // A window bounds an item's tiles: up to AT_WHOLE of them an item stays in one
+  // block, and there is nothing to join.
+  const long long reach = (long long)a.window + (ragged ? f.span * t.tpt : a.n_new) + a.n_sink + (2 << t.gsh);
+  t.whole = a.window > 0 && reach <= AT_WHOLE * 128;
   t.first = w.first, t.info = (int2 *)w.info, t.count = w.count, t.part = w.part, t.split = (int4 *)w.split;
   TileMaps maps;
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_tok};
@@ -1457,7 +1475,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
     e = cudaLaunchKernelExC(&cfg, f.tile, args);
     ++*launches;
   }
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && !t.whole) {
     void *args[] = {(void *)&a, &t};
     e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / f.jrows)), dim3(AJ_THREADS), 0, s, args, true);
     ++*launches;

@@ -199,6 +199,17 @@ def test_prefill_window(window, sink, heads, kv, dim):
     _run_prefill("bf16", heads, kv, dim, 32, window, sink, RUNS + [(300, 900)], seed=window + sink)
 
 
+@pytest.mark.parametrize("window", [200, 500, 700, 960])
+@pytest.mark.parametrize("heads,kv,dim", [(32, 1, 128), (16, 4, 64), (8, 1, 256), (64, 1, 512)])
+def test_windows_of_some_tiles(window, heads, kv, dim):
+    """Windows of two to eight tiles, few and many sequences: items that stay
+    in one block, and items that are split."""
+    _run_decode("bf16", heads, kv, dim, 16, window, 4, 5, [2500], seed=window)
+    _run_decode("fp16", heads, kv, dim, 64, window, 4, 3, [(311 * i) % 1600 for i in range(60)], seed=window)
+    _run_prefill("bf16", heads, kv, dim, 64, window, 4, [(700, 1000)], seed=window)
+    _run_prefill("fp16", heads, kv, dim, 32, window, 4, [((29 * i) % 90, (401 * i) % 1500) for i in range(40)], seed=window)
+
+
 def test_prefill_long():
     for heads, kv, dim, window in [(4, 1, 128, 0), (4, 2, 128, 1000), (2, 2, 64, 0), (16, 1, 512, 128), (2, 1, 256, 0)]:
         _run_prefill("bf16", heads, kv, dim, 64, window, 4 if window else 0, [(2113, 0), (5, 4000), (700, 2000)], seed=2)
