@@ -38,7 +38,8 @@
 //
 // The call's tiles, in order, are dealt to the blocks in equal contiguous
 // runs. A row tile whose positions lie in several runs leaves one partial
-// (O, m, l) per block; k_attn_join adds them in block order.
+// (O, m, l) per block; k_attn_join adds them in block order. Where a window
+// leaves an item few tiles it stays whole (AT_WHOLE).
 #include <cuda.h>
 
 #include <algorithm>
