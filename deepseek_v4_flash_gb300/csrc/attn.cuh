@@ -44,27 +44,60 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Rows and length of sequence b, clamped to what the buffers hold; `bad` is
-// set when a value had to be clamped (the caller raises
-// DS4MOE_DEVERR_LENGTH).
+// Row bounds of a ragged call (cu_q): each is brought into [0, n_tok] and
+// raised to the largest before it. Sequences then never share a row, and their
+// rows are at most n_tok in all: the workspace is sized by that.
+__device__ __forceinline__ int clamp_row(int c, int n_tok) { return min(max(c, 0), n_tok); }
+
+// Bounds (first row, end) of sequence b = b0 + threadIdx.x, by a block of
+// 1024 threads for b0 = 0, 1024, ...; `base` (shared, 0 at first) is the
+// largest bound of the sequences before. `bad` is set where a bound changed.
+__device__ __forceinline__ int2 clean_rows(const int32_t *cu, int n_seq, int n_tok, int b, int *base, int *warp_top,
+                                           bool &bad) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int raw0 = b < n_seq ? cu[b] : 0, raw1 = b < n_seq ? cu[b + 1] : 0, from = *base;
+  int c0 = clamp_row(raw0, n_tok), c1 = clamp_row(raw1, n_tok);
+  const bool wrong = b < n_seq && (c0 != raw0 || c1 != raw1 || c0 > c1 || c0 < from);
+  if (__syncthreads_or(wrong)) {
+    // running maximum of the first rows
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, c0, o);
+      if (lane >= o) c0 = max(c0, x);
+    }
+    if (lane == 31) warp_top[w] = c0;
+    __syncthreads();
+    c0 = max(c0, from);
+    for (int i = 0; i < w; i++) c0 = max(c0, warp_top[i]);
+    c1 = max(c0, c1);
+    bad |= b < n_seq && (c0 != raw0 || c1 != raw1);
+  }
+  if (threadIdx.x == 1023) *base = c1;  // (only used when another 1024 follow)
+  __syncthreads();
+  return make_int2(c0, c1);
+}
+
+// Rows and length of sequence b (a ragged call's bounds are clean); the length
+// is clamped to what the table holds, and `bad` set where it had to be (the
+// caller raises DS4MOE_DEVERR_LENGTH).
 struct SeqInfo {
   int tok0, n, len;  // first row of q, rows, cached positions
 };
+__device__ __forceinline__ int seq_len(const AttnArgs &a, int b, bool &bad) {
+  const int l = a.kv_len[b], len = min(max(l, 0), a.kv.width * a.kv.page_size);
+  bad |= len != l;
+  return len;
+}
 __device__ __forceinline__ SeqInfo seq_info(const AttnArgs &a, int b, bool &bad) {
   SeqInfo s;
   if (a.cu_q) {
-    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
-    s.tok0 = min(max(c0, 0), a.n_tok);
-    const int e = min(max(c1, s.tok0), a.n_tok);
-    s.n = e - s.tok0;
-    bad |= s.tok0 != c0 || e != c1;
+    s.tok0 = a.cu_q[b];
+    s.n = a.cu_q[b + 1] - s.tok0;
   } else {
     s.tok0 = b * a.n_new;
     s.n = a.n_new;
   }
-  const int l = a.kv_len[b];
-  s.len = min(max(l, 0), a.kv.width * a.kv.page_size);
-  bad |= s.len != l;
+  s.len = seq_len(a, b, bad);
   return s;
 }
 

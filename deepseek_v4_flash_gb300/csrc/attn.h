@@ -28,6 +28,7 @@ struct AttnArgs {
   long long q_stride, out_stride;  // elements from one token's row to the next
   const int32_t *kv_len;           // [n_seq] cached positions, the new tokens among them
   const int32_t *cu_q;             // [n_seq + 1] first row of each sequence, or null: n_new rows each
+                                   // (a planned call's kernels: the workspace's copy, ascending in [0, n_tok])
   int32_t n_seq, n_tok, n_new;
   int32_t n_heads, n_kv, group;    // group = n_heads / n_kv
   int32_t window, n_sink;
@@ -40,6 +41,7 @@ struct TileWork {
   long long *first;  // [row groups + 1]
   void *info;        // int2 [row groups]
   int *count, *seq_first;
+  int32_t *cu;       // [max_seqs + 1] row bounds, ascending in [0, n_tok]
   float *part;
   void *split;       // int4 [2 * n_sm]
   int pairs;         // pairs of blocks that run at once

@@ -291,12 +291,42 @@ struct Sched {
   long long u, u1, item0, item1;
   int b, kvh;
   int t0, span;                   // ragged calls: the row group's first token in its sequence, tokens of one
+  int row0, row1, slen;           // ragged calls without a plan: first row, end and length of sequence `lane`
   long long U, N;                 // the call's units, the gangs that have some
+
+  // Rows and length of a sequence (whole warp, the same one).
+  __device__ __forceinline__ SeqInfo seq(const AttnArgs &a, const TileArgs &t, int bb) const {
+    if (a.cu_q && !t.first) {
+      SeqInfo s;
+      s.tok0 = __shfl_sync(0xffffffffu, row0, bb), s.n = __shfl_sync(0xffffffffu, row1, bb) - s.tok0;
+      s.len = __shfl_sync(0xffffffffu, slen, bb);
+      return s;
+    }
+    bool bad = false;
+    return seq_info(a, bb, bad);
+  }
+  // A ragged call without a plan (up to 32 sequences): its row bounds, made
+  // ascending as k_attn_plan does.
+  __device__ __forceinline__ void read_rows(const AttnArgs &a, bool &bad) {
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < a.n_seq;
+    const int raw0 = in ? a.cu_q[lane] : 0, raw1 = in ? a.cu_q[lane + 1] : 0;
+    slen = in ? seq_len(a, lane, bad) : 0;
+    row0 = clamp_row(raw0, a.n_tok), row1 = clamp_row(raw1, a.n_tok);
+    if (__any_sync(0xffffffffu, in && (row0 != raw0 || row1 != raw1 || row0 > row1))) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, row0, o);
+        if (lane >= o) row0 = max(row0, x);
+      }
+      row1 = max(row0, row1);
+      bad |= in && (row0 != raw0 || row1 != raw1);
+    }
+  }
 
   // the current item's sequence and rows; its tiles
   __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, Seg &s) const {
-    bool bad = false;
-    const SeqInfo si = seq_info(a, b, bad);
+    const SeqInfo si = seq(a, t, b);
     s.b = b, s.kvh = kvh, s.len = si.len;
     if (a.cu_q) {
       s.row0 = si.tok0 + t0;
@@ -327,37 +357,32 @@ struct Sched {
 
   // Row groups of all sequences in order: their units' sum, or (r >= 0) the
   // one that holds unit r, into b, t0 and item0 (relative to the sum's start).
-  __device__ long long walk(const AttnArgs &a, int gsh, long long r, bool &bad) {
+  __device__ long long walk(const AttnArgs &a, const TileArgs &t, long long r) {
     const int lane = threadIdx.x & 31;
     long long base = 0, mine = 0;
-    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-      SeqInfo si = {0, 0, 0};
-      if (b0 + lane < a.n_seq) si = seq_info(a, b0 + lane, bad);
-      for (int l = 0; l < 32 && b0 + l < a.n_seq; l++) {
-        SeqInfo x;
-        x.n = __shfl_sync(0xffffffffu, si.n, l), x.len = __shfl_sync(0xffffffffu, si.len, l), x.tok0 = 0;
-        for (int j0 = 0; j0 < x.n; j0 += 32 * span) {
-          const int j = j0 + lane * span;
-          const int un = j < x.n ? units(a, gsh, x, j, min(span, x.n - j)) : 0;
-          if (r < 0) {
-            mine += un;
-            continue;
-          }
-          int incl = un;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, r < base + incl);
-          if (hit) {
-            const int k = __ffs(hit) - 1;
-            b = b0 + l, t0 = j0 + k * span;
-            item0 = base + __shfl_sync(0xffffffffu, incl - un, k), item1 = item0 + __shfl_sync(0xffffffffu, un, k);
-            return 0;
-          }
-          base += __shfl_sync(0xffffffffu, incl, 31);
+    for (int l = 0; l < a.n_seq; l++) {
+      const SeqInfo x = seq(a, t, l);
+      for (int j0 = 0; j0 < x.n; j0 += 32 * span) {
+        const int j = j0 + lane * span;
+        const int un = j < x.n ? units(a, t.gsh, x, j, min(span, x.n - j)) : 0;
+        if (r < 0) {
+          mine += un;
+          continue;
         }
+        int incl = un;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, r < base + incl);
+        if (hit) {
+          const int k = __ffs(hit) - 1;
+          b = l, t0 = j0 + k * span;
+          item0 = base + __shfl_sync(0xffffffffu, incl - un, k), item1 = item0 + __shfl_sync(0xffffffffu, un, k);
+          return 0;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
 #pragma unroll
@@ -375,7 +400,8 @@ struct Sched {
       n_idx = *t.count, head = t.first[n_idx];
       U = head * a.n_kv;
     } else if (a.cu_q) {
-      head = walk(a, t.gsh, -1, bad);
+      read_rows(a, bad);
+      head = walk(a, t, -1);
       U = head * a.n_kv;
     } else {
       long long n = 0;
@@ -404,7 +430,7 @@ struct Sched {
         b = in.x, t0 = in.y;
         item0 = t.first[lo], item1 = t.first[lo + 1];
       } else {
-        walk(a, t.gsh, r, bad);
+        walk(a, t, r);
       }
       item0 += kvh * head, item1 += kvh * head;
     } else {
@@ -445,10 +471,10 @@ struct Sched {
     item0 = item1;
     if (item0 >= U) return;
     if (a.cu_q) {
-      SeqInfo si = seq_info(a, b, bad);
+      SeqInfo si = seq(a, t, b);
       for (t0 += span; t0 >= si.n; t0 = 0) {
         if (++b == a.n_seq) b = 0, kvh++;
-        si = seq_info(a, b, bad);
+        si = seq(a, t, b);
         if (si.n > 0) {
           t0 = 0;
           break;
@@ -473,14 +499,16 @@ struct Sched {
   }
 };
 
-// Ragged calls of many sequences or row groups: the groups of `span` tokens in
+// Ragged calls of many sequences or row groups: the row bounds (`cu`, as the
+// caller gave them) made ascending into a.cu_q, the groups of `span` tokens in
 // sequence order, and the running count of their units, by one block. Small
 // calls do without (Sched::walk, in every block): up to AT_WALK groups of up to
 // 32 sequences a block's walk is shorter than this kernel's 4 to 6 us.
-__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, int gsh, long long *first, int2 *info, int *count,
-                                                int *seq_first) {
+__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, const int32_t *cu, int32_t *clean, int span, int gsh,
+                                                long long *first, int2 *info, int *count, int *seq_first) {
   __shared__ long long warp_sum[32];
   __shared__ long long s_base;
+  __shared__ int s_top[32], s_row;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
@@ -510,17 +538,22 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int span, 
     __syncthreads();
     return r;
   };
-  if (tid == 0) s_base = 0;
+  if (tid == 0) s_base = 0, s_row = 0;
   __syncthreads();
   bool bad = false;
   for (int b0 = 0; b0 < a.n_seq; b0 += 1024) {
     const int b = b0 + tid;
-    const int n = b < a.n_seq ? (seq_info(a, b, bad).n + span - 1) / span : 0;
-    const long long x = scan(n);
-    if (b < a.n_seq) seq_first[b] = (int)x;
+    const int2 c = clean_rows(cu, a.n_seq, a.n_tok, b, &s_row, s_top, bad);
+    const long long x = scan(b < a.n_seq ? (c.y - c.x + span - 1) / span : 0);
+    if (b < a.n_seq) {
+      seq_first[b] = (int)x;
+      clean[b] = c.x;
+      if (b + 1 == a.n_seq) clean[b + 1] = c.y;
+      seq_len(a, b, bad);
+    }
   }
   if (bad) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
-  const int total = (int)s_base;
+  const int total = (int)s_base;  // at most n_tok / span + n_seq
   __syncthreads();
   if (tid == 0) s_base = 0, *count = total;
   __syncthreads();
@@ -1457,14 +1490,16 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   int span = f.span * t.tpt;
+  AttnArgs p = a;
   if (ragged && a.n_seq <= 32 && a.n_tok / span + a.n_seq <= AT_WALK) t.first = nullptr;
   if (ragged && t.first) {
-    void *args[] = {(void *)&a, &span, &t.gsh, &t.first, &t.info, &t.count, (void *)&w.seq_first};
+    p.cu_q = w.cu;
+    void *args[] = {&p, (void *)&a.cu_q, (void *)&w.cu, &span, &t.gsh, &t.first, &t.info, &t.count, (void *)&w.seq_first};
     e = launch_pdl((const void *)k_attn_plan, dim3(1), dim3(1024), 0, s, args, true);
     ++*launches;
   }
   if (e == cudaSuccess) {
-    void *args[] = {&maps, (void *)&a, &t};
+    void *args[] = {&maps, &p, &t};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(t.gangs * t.members), cfg.blockDim = dim3(f.threads), cfg.dynamicSmemBytes = AT_DYN, cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -1477,7 +1512,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
     ++*launches;
   }
   if (e == cudaSuccess && !t.whole) {
-    void *args[] = {(void *)&a, &t};
+    void *args[] = {&p, &t};
     e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / f.jrows)), dim3(AJ_THREADS), 0, s, args, true);
     ++*launches;
   }

@@ -385,8 +385,10 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  * Data errors on the device set a flag of the handle: DS4MOE_DEVERR_PAGE (a
  * table entry outside [0, n_pages): its keys and values are read as zeros, and
  * an append to it is dropped), DS4MOE_DEVERR_LENGTH (kv_len outside
- * [0, max_pages * page_size], or a cu_q that is not ascending in [0, n_tok]:
- * clamped; a row appended at a position outside that range is dropped). */
+ * [0, max_pages * page_size]: clamped; a cu_q that is not ascending in
+ * [0, n_tok]: each entry is clamped to that and raised to the largest before
+ * it, so that sequences never share a row; a row appended at a position
+ * outside the table is dropped). */
 typedef enum { DS4MOE_DT_F32 = 0, DS4MOE_DT_BF16 = 1, DS4MOE_DT_F16 = 2 } ds4moe_dtype;
 
 #define DS4MOE_ATTN_MAX_NEW 16 /* new tokens per sequence of a decode call */
