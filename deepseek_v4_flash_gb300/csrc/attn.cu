@@ -15,6 +15,12 @@ namespace ds4 {
 // to the cache's type. One thread per 8 elements (16 bytes of the cache);
 // neighbouring threads take neighbouring elements of a row. Bound by the bytes:
 // 12291 tokens of 8 x 128 from fp32 25.5 us, 5.9 TB/s.
+//
+// Ragged calls: every block needs the row bounds ascending (see clean_rows). Up
+// to AP_SEQS sequences it reads and checks them itself, for a search in shared
+// memory (the reads go with those of the rows); for more, k_clean_rows puts
+// them in the workspace first.
+constexpr int AP_SEQS = 1024;
 struct AppendArgs {
   KvView kv;
   const void *k, *v;           // v null: the keys only
@@ -24,8 +30,25 @@ struct AppendArgs {
   uint32_t *err;
 };
 
+__global__ void __launch_bounds__(1024) k_clean_rows(const int32_t *cu, int n_seq, int n_tok, int32_t *clean, uint32_t *err) {
+  __shared__ int top[32], base;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (threadIdx.x == 0) base = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int b0 = 0; b0 < n_seq; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    const int2 c = clean_rows(cu, n_seq, n_tok, b, &base, top, bad);
+    if (b < n_seq) clean[b] = c.x;
+    if (b + 1 == n_seq) clean[n_seq] = c.y;
+  }
+  if (bad) raise_flag(err, DS4MOE_DEVERR_LENGTH);
+}
+
 template <int DT, bool F32, int P>
 __global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
+  __shared__ int s_cu[AP_SEQS + 1];
   pdl_launch_dependents();
   pdl_wait();
   const long long total = (long long)a.n_tok * a.per_tok;
@@ -34,15 +57,40 @@ __global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
   const long long stride = kv ? a.v_stride : a.k_stride;
   uint4 x[P], y[P];
   uint16_t *dst[P];
+  int row_t[P], row_e[P];  // this thread's pieces: token (-1: none) and element
 #pragma unroll
   for (int j = 0; j < P; j++) {
-    dst[j] = nullptr;
+    dst[j] = nullptr, row_t[j] = -1;
     const long long i = (long long)blockIdx.x * (128 * P) + j * 128 + threadIdx.x;
     if (i >= total) continue;
     const int t = (int)(i / a.per_tok), e = (int)(i - (long long)t * a.per_tok) * 8;
     const char *p = src + ((long long)t * stride + e) * (F32 ? 4 : 2);
     x[j] = reinterpret_cast<const uint4 *>(p)[0];
     if (F32) y[j] = reinterpret_cast<const uint4 *>(p)[1];
+    row_t[j] = t, row_e[j] = e;
+  }
+  const int *cu = a.cu_q;
+  if (a.cu_q && a.n_seq <= AP_SEQS) {
+    bool bad = false;
+    int last = 0;
+    for (int i = threadIdx.x; i <= a.n_seq; i += 128) {
+      const int raw = a.cu_q[i], c = clamp_row(raw, a.n_tok);
+      bad |= raw != c || (i > 0 && clamp_row(a.cu_q[i - 1], a.n_tok) > c);
+      s_cu[i] = c;
+    }
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+        for (int i = 0; i <= a.n_seq; i++) s_cu[i] = last = max(last, s_cu[i]);
+      }
+      __syncthreads();
+    }
+    cu = s_cu;
+  }
+#pragma unroll
+  for (int j = 0; j < P; j++) {
+    if (row_t[j] < 0) continue;
+    const int t = row_t[j], e = row_e[j];
     int b, at, n;
     if (!a.cu_q) {
       b = t / a.n_new, at = t - b * a.n_new, n = a.n_new;
@@ -51,11 +99,11 @@ __global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
       int lo = 0, hi = a.n_seq;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu_q[mid] <= t) lo = mid;
+        if (cu[mid] <= t) lo = mid;
         else hi = mid;
       }
       b = lo;
-      const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+      const int c0 = cu[b], c1 = cu[b + 1];
       if (t < c0 || t >= c1) continue;  // a row of no sequence
       at = t - c0, n = c1 - c0;
     }
@@ -273,7 +321,15 @@ ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, con
   const void *fn = append_fn(!f32 || h->d.dtype == DS4MOE_DT_BF16, f32, two);
   void *args[] = {&a};
   const int per = two ? 256 : 128;
-  const cudaError_t e = launch_pdl(fn, dim3((unsigned)(((long long)n_tok * a.per_tok + per - 1) / per), v_new ? 2 : 1),
+  cudaError_t e = cudaSuccess;
+  if (cu_q && n_seq > AP_SEQS) {
+    a.cu_q = h->tile.cu;
+    void *clean[] = {(void *)&cu_q, &n_seq, &n_tok, &h->tile.cu, &h->err};
+    e = launch_pdl((const void *)k_clean_rows, dim3(1), dim3(1024), 0, (cudaStream_t)stream, clean, true);
+    h->launches++;
+    if (e != cudaSuccess) return at_status(e);
+  }
+  e = launch_pdl(fn, dim3((unsigned)(((long long)n_tok * a.per_tok + per - 1) / per), v_new ? 2 : 1),
                                    dim3(128), 0, (cudaStream_t)stream, args, true);
   h->launches++;
   return at_status(e);
