@@ -306,15 +306,16 @@ __global__ void __launch_bounds__(SP_THREADS) k_verify_drafts(const VerifyArgs a
     if (cnt != given && tid == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
   }
   if (w == 0) {
-    // draft i is accepted when u * q < p: the product of two 24-bit
+    // draft i is accepted when u * q < p, both clamped as where the token is
+    // drawn (__saturatef: to [0, 1], NaN to 0): the product of two 24-bit
     // significands is exact in 64 bits
     int n = cnt;
     for (int i = lane; i < cnt; i += 32) {
       const int t = a.tok[(long long)b * a.G + i];
       bool ok = false;
       if (t >= 0 && t < a.V) {
-        const double p = a.target[((long long)b * (a.G + 1) + i) * a.t_pitch + t];
-        const double q = a.draft ? a.draft[((long long)b * a.G + i) * a.d_pitch + t] : 1.0;
+        const double p = __saturatef(a.target[((long long)b * (a.G + 1) + i) * a.t_pitch + t]);
+        const double q = a.draft ? __saturatef(a.draft[((long long)b * a.G + i) * a.d_pitch + t]) : 1.0f;
         ok = (double)a.u_accept[(long long)b * a.G + i] * q < p;
       } else {
         raise_flag(a.err, DS4MOE_DEVERR_TOKEN_ID);
