@@ -398,9 +398,12 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       const int slot = 2 * blockIdx.x + (item0 < u0 ? 0 : 1);
       float *pp = part + (size_t)slot * (16 * (D + 2));
       const int nan_rows_possible = a.n_new > 1;
-      auto store = [&](int r, int c, float4 x, float inv) {
+      auto store = [&](int r, int c, float4 x, float l) {
         const int t = cc.b * a.n_new + r / a.group, h = cc.kvh * a.group + r % a.group;
+        const float inv = 1.0f / l;
         x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        // no score above -infinity (whatever the values: 0 x NaN is NaN)
+        if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const uint2 u = make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
         *reinterpret_cast<uint2 *>(a.out + (long long)t * a.out_stride + (long long)h * D + c) = u;
         if (nan_rows_possible) {
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
                                                              4 * (r * D + (c ^ ((r & 7) << 3))));
           x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
         }
-        if (whole) store(r, c, x, s_lt[r] == 0.0f ? 0.0f : 1.0f / s_lt[r]);
+        if (whole) store(r, c, x, s_lt[r]);
         else *reinterpret_cast<float4 *>(pp + r * D + c) = x;
       }
       bool done = whole;
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
               const float f = s_f[p][r];
               x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
             }
-            store(r, c, x, s_lt[r] == 0.0f ? 0.0f : 1.0f / s_lt[r]);
+            store(r, c, x, s_lt[r]);
           }
         }
       }
