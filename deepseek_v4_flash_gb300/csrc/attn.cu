@@ -261,7 +261,8 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
     at += (bytes + 255) & ~(size_t)255;
     return p;
   };
-  const size_t o_err = place(64), o_ticket = place((size_t)h->n_sm * 4), o_split = place((size_t)h->n_sm * 32);
+  const size_t o_err = place(64), o_ticket = place((size_t)h->n_sm * 4), o_marked = place((size_t)h->n_sm * 4);
+  const size_t o_split = place((size_t)h->n_sm * 32);
   const size_t o_count = place(4), o_seq = place((size_t)d.max_seqs * 4), o_cu = place(((size_t)d.max_seqs + 1) * 4);
   const size_t o_first = place((groups + 1) * 8);
   const size_t o_info = place(groups * 8), o_part = place(parts * 4);
@@ -278,7 +279,7 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
     return st;
   }
   h->err = (uint32_t *)(h->mem + o_err), h->ticket = (int *)(h->mem + o_ticket), h->part = (float *)(h->mem + o_part);
-  h->tile.split = h->mem + o_split, h->tile.count = (int *)(h->mem + o_count);
+  h->tile.split = h->mem + o_split, h->tile.marked = (int *)(h->mem + o_marked), h->tile.count = (int *)(h->mem + o_count);
   h->tile.seq_first = (int *)(h->mem + o_seq), h->tile.cu = (int32_t *)(h->mem + o_cu), h->tile.first = (long long *)(h->mem + o_first);
   h->tile.info = h->mem + o_info, h->tile.part = h->part;
   h->tile.pairs = attn_tile_pairs(d.dtype, d.head_dim);

@@ -33,6 +33,10 @@ struct AttnArgs {
   int32_t n_heads, n_kv, group;    // group = n_heads / n_kv
   int32_t window, n_sink;
   float scale_log2;                // score scale * log2(e)
+  // tile kernel: the positions of an item's queries span less than this; log2
+  // of a group's positions; which of its blocks have marked rows
+  int32_t span, gsh;
+  int *marked;
   uint32_t *err;
 };
 
@@ -44,6 +48,7 @@ struct TileWork {
   int32_t *cu;       // [max_seqs + 1] row bounds, ascending in [0, n_tok]
   float *part;
   void *split;       // int4 [2 * n_sm]
+  int *marked;       // [n_sm], 0 but between the tile kernel and k_attn_mend
   int pairs;         // pairs of blocks that run at once
 };
 

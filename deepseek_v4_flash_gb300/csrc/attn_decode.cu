@@ -149,9 +149,8 @@ __device__ __forceinline__ bool dec_start(const AttnArgs &a, int n_cta, long lon
   return true;
 }
 
-// Rows whose result holds a NaN are computed once more from what they see
-// alone: among several new tokens a position that one sees and another does
-// not may hold an infinity or NaN, and 0 x NaN is NaN in the matrix product.
+// A row whose result holds a NaN that may come from a position it does not see
+// (another of several new tokens does), once more from what it sees alone.
 template <int DT, int D>
 __device__ __noinline__ void redo_row(const AttnArgs &a, int t, int h, int b, int pos, const Groups &gr) {
   float2 acc[D / 64];
@@ -163,7 +162,7 @@ __device__ __noinline__ void redo_row(const AttnArgs &a, int t, int h, int b, in
   uint32_t *o = reinterpret_cast<uint32_t *>(a.out + (long long)t * a.out_stride + (long long)h * D);
 #pragma unroll
   for (int c = 0; c < D / 64; c++)
-    o[(threadIdx.x & 31) + 32 * c] = Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
+    o[(threadIdx.x & 31) + 32 * c] = l == 0.0f ? 0u : Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
 }
 
 template <int DT, int D>
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
         if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const uint2 u = make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
         *reinterpret_cast<uint2 *>(a.out + (long long)t * a.out_stride + (long long)h * D + c) = u;
-        if (nan_rows_possible) {
+        if (nan_rows_possible && l == l) {
           const float z = x.x + x.y + x.z + x.w;  // NaN, or two infinities that cancel: both are looked at again
           if (z != z) atomicOr(&s_nan, 1 << r);
         }
@@ -477,10 +476,13 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       }
       __syncthreads();
       if (nan_rows_possible && done && s_nan) {
-        for (int r = w; r < rows; r += AD_WARPS)
-          if (s_nan >> r & 1)
-            redo_row<DT, D>(a, cc.b * a.n_new + r / a.group, cc.kvh * a.group + r % a.group, cc.b,
-                            cc.s.first + r / a.group, cc.s.gr);
+        for (int r = w; r < rows; r += AD_WARPS) {
+          const int pos = cc.s.first + r / a.group, t = cc.b * a.n_new + r / a.group, h = cc.kvh * a.group + r % a.group;
+          if ((s_nan >> r & 1) &&
+              unseen_nonfinite<DT>(a, cc.b, cc.kvh, pos, pos, window_lo(a, max(cc.s.first, 0)), 0, cc.s.last + 1, 0, D) &&
+              !own_nan<DT>(a, a.out + (long long)t * a.out_stride + (long long)h * D, cc.b, cc.kvh, pos, 0, D))
+            redo_row<DT, D>(a, t, h, cc.b, pos, cc.s.gr);
+        }
         __syncthreads();
       }
       item0 = end;

@@ -250,9 +250,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Cycles that a warp waits for another, which may compute rows once more
+// (AT_REDO).
+constexpr long long AT_WAIT = 1ll << 33;
+
 // A bounded wait of the whole warp: false for every lane when one gave up.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, AT_WAIT));
 }
 
 // ---------------------------------------------------------------------------
@@ -588,9 +592,9 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b, int w) {
   return h & ~l;
 }
 
-// A row whose result holds a NaN, once more from what it sees alone: a
-// position that other rows of the tile see may hold an infinity or NaN, and
-// 0 x NaN is NaN in the matrix product. Writes columns [c0, c1).
+// A row whose result holds a NaN that may come from a position it does not see
+// (other rows of the tile do), once more from what it sees alone. Writes
+// columns [c0, c1).
 template <int DT, int D>
 __device__ __noinline__ void redo_row_cols(const AttnArgs &a, int t, int h, int b, int pos, int c0, int c1) {
   float2 acc[D / 64];
@@ -605,7 +609,47 @@ __device__ __noinline__ void redo_row_cols(const AttnArgs &a, int t, int h, int 
 #pragma unroll
   for (int c = 0; c < D / 64; c++)
     if (c * 64 >= c0 && c * 64 < c1)
-      o[(threadIdx.x & 31) + 32 * c] = Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
+      o[(threadIdx.x & 31) + 32 * c] = l == 0.0f ? 0u : Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
+}
+
+// Rows that see this many positions are not computed once more in the block,
+// whose other warps wait for the next weights meanwhile (a warp's 32 rows take
+// up to 50000 cycles a position), but by k_attn_mend. Until then the first
+// column that the warp stores of such a row holds AT_MARK, bits that no result
+// has: conversions give a NaN a positive sign.
+constexpr int AT_REDO = 65536;
+constexpr uint16_t AT_MARK = 0xFFFF;
+
+// Rows of this warp whose result holds a NaN, although their sum of weights
+// does not: token tq, head hq, position pos of sequence b (one row per lane;
+// pos -1: the sum is 0, the row becomes zeros; -2: no such row). Those that may
+// owe the NaN to a position they do not see are computed once more.
+template <int DT, int D>
+__device__ __noinline__ void look_again(const AttnArgs &a, int tq, int hq, int b, int pos, int c0, int c1) {
+  const int lane = threadIdx.x & 31;
+  unsigned m = __ballot_sync(0xffffffffu, pos >= 0);
+  int kvh = 0, win0 = 0, sinks = 0, end = 0;
+  if (m) {
+    // the item's queries lie less than `span` positions apart
+    bool bad = false;
+    const int first = __reduce_min_sync(0xffffffffu, pos >= 0 ? pos : INT32_MAX), last = __reduce_max_sync(0xffffffffu, pos);
+    const int len = seq_len(a, b, bad), p1 = min(first + a.span, len) - 1;
+    const Groups gr = groups_of(a, max(last - a.span + 1, 0), p1, a.gsh);
+    kvh = __shfl_sync(0xffffffffu, hq, __ffs(m) - 1) / a.group;
+    win0 = gr.win0 << a.gsh, sinks = gr.n_sink << a.gsh, end = min(len, (p1 | 15) + 1);
+    if (!unseen_nonfinite<DT>(a, b, kvh, first, last, win0, sinks, end, c0, c1)) m = 0;
+  }
+  for (m |= __ballot_sync(0xffffffffu, pos == -1); m; m &= m - 1) {
+    const int x = __ffs(m) - 1, tx = __shfl_sync(0xffffffffu, tq, x), hx = __shfl_sync(0xffffffffu, hq, x);
+    const int px = __shfl_sync(0xffffffffu, pos, x);
+    uint16_t *o = a.out + (long long)tx * a.out_stride + (long long)hx * D;
+    if (px >= 0 && (own_nan<DT>(a, o, b, kvh, px, c0, c1) ||
+                    !unseen_nonfinite<DT>(a, b, kvh, px, px, win0, sinks, end, c0, c1)))
+      continue;
+    const int lo = window_lo(a, max(px, 0));
+    if (px - lo + min(a.n_sink, lo) < AT_REDO) redo_row_cols<DT, D>(a, tx, hx, b, px, c0, c1);
+    else if (lane == 0) o[c0] = AT_MARK, a.marked[blockIdx.x] = 1;
+  }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -1231,13 +1275,9 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       }
       tc_fence_before();
       __syncwarp();  // other lanes have stored parts of these rows
-      unsigned again = __ballot_sync(0xffffffffu, nan && valid);
-      while (again) {
-        const int x = __ffs(again) - 1;
-        again &= again - 1;
-        redo_row_cols<DT, D>(a, __shfl_sync(0xffffffffu, tq, x), __shfl_sync(0xffffffffu, hq, x), s.b,
-                             __shfl_sync(0xffffffffu, pos, x), half * C::DV + c0, half * C::DV + c1);
-      }
+      const bool look = nan && valid && l == l;
+      if (__any_sync(0xffffffffu, look))
+        look_again<DT, D>(a, tq, hq, s.b, look ? (l == 0.0f ? -1 : pos) : -2, half * C::DV + c0, half * C::DV + c1);
     }
   }
   if (!ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
@@ -1261,11 +1301,41 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
 // takes four columns of R rows, with 8 / R partials of each in flight. The
 // kernel is all latency: ragged calls (many split row groups of two or three
 // partials) take R = 4, one wave of blocks instead of four; decode calls (few
-// rows, up to a partial per gang) R = 1, four times the threads.
+// rows, up to a partial per gang) R = 1, four times the threads. Registers are
+// limited to what the sums need (12291 tokens of 32/8 heads of 128: 13.8 -> 11.8
+// us), not the rows computed once more.
 constexpr int AJ_THREADS = 256;
 
+// Rows r0 + i with bit i of `again` (a NaN, but not in their sum of weights), by
+// the block's warps in turn; d0, d1: the item, as in k_attn_join.
+template <int DT, int D, int NT, bool PAIR, int ROWS>
+__device__ __noinline__ void join_again(const AttnArgs &a, const TileArgs &t, unsigned long long again) {
+  using C = TileCfg<D, NT, PAIR>;
+  const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
+  const int bid = blockIdx.x / (128 / ROWS * NT);
+  const int gang = bid / t.members, member = bid % t.members;
+  const int half = PAIR ? member >> 1 & 1 : member % C::HALVES;
+  const int rt = PAIR ? (member >> 2) * 2 + (member & 1) : member / C::HALVES;
+  const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
+  const int tok0 = (rt + r) * t.tpt, c0 = half * C::DV, c1 = c0 + C::DV;
+  bool bad = false;
+  const int last = d0.w + d1.y - 1;
+  const Groups gr = range_groups(a, d0.w, last, t.gsh);  // as the item's blocks listed them
+  const int win0 = gr.win0 << t.gsh, sinks = gr.n_sink << t.gsh, end = min(seq_len(a, d0.y, bad), (last | 15) + 1);
+  const int p0 = d0.w + tok0 + (r0 + __ffsll(again) - 1) / a.group, p1 = d0.w + tok0 + (r0 + 63 - __clzll(again)) / a.group;
+  if (!unseen_nonfinite<DT>(a, d0.y, d0.z, p0, p1, win0, sinks, end, c0, c1)) return;
+  for (int i = threadIdx.x >> 5; i < 64; i += AJ_THREADS / 32)
+    if (again >> i & 1) {
+      const int row = r0 + i, tok = tok0 + row / a.group, pos = d0.w + tok, h = d0.z * a.group + row % a.group;
+      if (!own_nan<DT>(a, a.out + (long long)(d1.x + tok) * a.out_stride + (long long)h * D, d0.y, d0.z, pos, c0, c1) &&
+          unseen_nonfinite<DT>(a, d0.y, d0.z, pos, pos, win0, sinks, end, c0, c1))
+        redo_row_cols<DT, D>(a, d1.x + tok, h, d0.y, pos, c0, c1);
+    }
+}
+
 template <int DT, int D, int NT, bool PAIR, int R>
-__global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, const TileArgs t) {
+__global__ void __launch_bounds__(AJ_THREADS, D * R < 512 || D == 128 ? 4 : D * R <= 1024 ? 3 : 2)
+    k_attn_join(const __grid_constant__ AttnArgs a, const __grid_constant__ TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
   constexpr int ROWS = C::JROWS * R, STEP = C::JROWS, P = 8 / R;  // rows of the block; distance of a thread's rows
   __shared__ unsigned long long s_nan;
@@ -1327,21 +1397,47 @@ __global__ void __launch_bounds__(AJ_THREADS) k_attn_join(const AttnArgs a, cons
   for (int k = 0; k < R; k++) {
     const int row = row0 + k * STEP;
     if (row >= rows) continue;
-    const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
-    const float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
-    if (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w) atomicOr(&s_nan, 1ull << (row - r0));
+    const float inv = 1.0f / l[k];
+    float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
+    if (l[k] == 0.0f) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (l[k] == l[k] && (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w)) atomicOr(&s_nan, 1ull << (row - r0));
     const int tok = row / a.group, h = d0.z * a.group + row % a.group;
     *reinterpret_cast<uint2 *>(a.out + (long long)(d1.x + tok0 + tok) * a.out_stride + (long long)h * D + half * C::DV + c) =
         make_uint2(Half16<DT>::down(z.x, z.y), Half16<DT>::down(z.z, z.w));
   }
   __syncthreads();
   const unsigned long long again = s_nan;
-  for (int i = tid >> 5; again && i < ROWS; i += AJ_THREADS / 32)
-    if (again >> i & 1) {
-      const int row = r0 + i, tok = tok0 + row / a.group;
-      redo_row_cols<DT, D>(a, d1.x + tok, d0.z * a.group + row % a.group, d0.y, d0.w + tok, half * C::DV,
-                           (half + 1) * C::DV);
+  if (again) join_again<DT, D, NT, PAIR, ROWS>(a, t, again);
+}
+
+// The marked rows (AT_MARK), all in items that a block of the tile kernel did
+// alone: a block for each of its blocks.
+template <int DT, int D, int NT, bool PAIR>
+__global__ void __launch_bounds__(AJ_THREADS)
+    k_attn_mend(const __grid_constant__ AttnArgs a, const __grid_constant__ TileArgs t) {
+  using C = TileCfg<D, NT, PAIR>;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (!a.marked[blockIdx.x]) return;
+  constexpr int COLS = C::DV == 64 ? 64 : C::DV / 2;  // of a warp of the tile kernel
+  const int gang = blockIdx.x / t.members, member = blockIdx.x % t.members, rank = PAIR ? member & 1 : 0;
+  const int half = PAIR ? member >> 1 & 1 : member % C::HALVES, rt = PAIR ? (member >> 2) * 2 + rank : member / C::HALVES;
+  const int tile0 = PAIR && a.cu_q ? rank * t.tpt : 0;
+  Sched sc;
+  Seg s;
+  bool bad = false;
+  bool more = sc.init(a, t, gang, C::SPAN, bad);
+  while (more && sc.next(a, t, rt, s)) {
+    if (!s.starts || !s.ends || s.kt0 >= s.kt1) continue;
+    for (int i = threadIdx.x >> 5; i < min(NT * t.tpt, s.n - tile0) * a.group; i += AJ_THREADS / 32) {
+      const int tok = tile0 + i / a.group, tq = s.row0 + tok, hq = s.kvh * a.group + i % a.group;
+      for (int c = half * C::DV; c < (half + 1) * C::DV; c += COLS)
+        if (a.out[(long long)tq * a.out_stride + (long long)hq * D + c] == AT_MARK)
+          redo_row_cols<DT, D>(a, tq, hq, s.b, s.pos0 + tok, c, c + COLS);
     }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) a.marked[blockIdx.x] = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -1388,7 +1484,7 @@ int box_shift(int page_size, int window, int most) {
 }
 
 struct TileFns {
-  const void *tile, *join;
+  const void *tile, *join, *mend;
   int nt, halves, jrows, threads, span;
 };
 
@@ -1399,7 +1495,7 @@ TileFns fns(bool ragged) {
   static_assert(C::NST > C::VST && (NT == 1 || C::NST > 2 * C::KST) && C::NST <= 12, "ring");
   return {(const void *)k_attn_tile<DT, D, NT, PAIR>,
           ragged ? (const void *)k_attn_join<DT, D, NT, PAIR, 4> : (const void *)k_attn_join<DT, D, NT, PAIR, 1>,
-          NT, C::HALVES, C::JROWS * (ragged ? 4 : 1), C::THREADS, C::SPAN};
+          (const void *)k_attn_mend<DT, D, NT, PAIR>, NT, C::HALVES, C::JROWS * (ragged ? 4 : 1), C::THREADS, C::SPAN};
 }
 
 template <int DT>
@@ -1491,6 +1587,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   cudaError_t e = cudaSuccess;
   int span = f.span * t.tpt;
   AttnArgs p = a;
+  p.span = ragged ? span : a.n_new, p.gsh = t.gsh, p.marked = w.marked;
   if (ragged && a.n_seq <= 32 && a.n_tok / span + a.n_seq <= AT_WALK) t.first = nullptr;
   if (ragged && t.first) {
     p.cu_q = w.cu;
@@ -1514,6 +1611,12 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int D, int dtype, const TileWork
   if (e == cudaSuccess && !t.whole) {
     void *args[] = {&p, &t};
     e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / f.jrows)), dim3(AJ_THREADS), 0, s, args, true);
+    ++*launches;
+  }
+  if (e == cudaSuccess && !t.whole && (long long)a.kv.width * a.kv.page_size >= AT_REDO &&
+      (a.window == 0 || (long long)a.window + a.n_sink >= AT_REDO)) {
+    void *args[] = {&p, &t};
+    e = launch_pdl(f.mend, dim3(t.gangs * t.members), dim3(AJ_THREADS), 0, s, args, true);
     ++*launches;
   }
   return e;

@@ -369,7 +369,9 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  *   s_j = scale * <q_h, k_j,g>,  out_h = sum_j exp(s_j) v_j,g / sum_j exp(s_j)
  * over the visible j. No visible position (i < 0), or no score above
  * -infinity: zeros. Keys and values of positions that a row does not see never
- * reach its output, whatever they hold (infinities and NaN among them). Scores, softmax and sums
+ * reach its output, whatever they hold (infinities and NaN among them); where
+ * rows of one tile differ in what they see of such a value, those that do not
+ * see it take some 1000 cycles per position. Scores, softmax and sums
  * are held in 32 bits; the weights are rounded to the 16-bit type before they
  * multiply the values, and the output once at the end.
  *
