@@ -381,11 +381,23 @@ def _vec(t, name, dtype, n):
     return t.data_ptr()
 
 
-def _fresh(out, stream):
-    """`out` was allocated on the current stream and is written on `stream`."""
+def _empty(shape, dtype, device, stream):
+    """A tensor that a call writes on `stream`. The allocator hands out memory
+    in the order of the stream that is current: a block freed there may still be
+    in use by what that stream has queued, for which another one would not wait.
+    So it comes from `stream`'s own blocks, and goes back to them only when the
+    current stream, where the caller goes on, is done with it too."""
     import torch
-    if stream is not None and out.is_cuda:
-        out.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(here)
     return out
 
 
@@ -490,9 +502,8 @@ class Attention:
 
     def _out(self, q, out, stream):
         """The output and its row stride."""
-        import torch
         if out is None:
-            return _fresh(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream), self._q_len
+            return _empty(q.shape, q.dtype, q.device, stream), self._q_len
         if out.shape != q.shape:
             raise ValueError("out: the shape of q")
         return out, _rows(out, "out", self._dt, self._q_row, self._q_len)
@@ -548,7 +559,7 @@ def token_probs(logits, temperature: float = 1.0, out=None, stream=None):
     import torch
     V = logits.shape[-1]
     if out is None:
-        out = _fresh(torch.empty(logits.shape, dtype=torch.float32, device=logits.device), stream)
+        out = _empty(logits.shape, torch.float32, logits.device, stream)
     elif out.shape != logits.shape:
         raise ValueError("out: the shape of logits")
     one = logits.dim() == 1
@@ -578,11 +589,11 @@ def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_acc
             raise ValueError("draft: [n_seq, max_draft, vocab]")
         ds = _rows(draft, "draft", f32, (V,), V)
     if n_accepted is None:
-        n_accepted = _fresh(torch.empty(B, dtype=i32, device=target.device), stream)
+        n_accepted = _empty((B,), i32, target.device, stream)
     else:
         _vec(n_accepted, "n_accepted", i32, B)
     if tokens_out is None:
-        tokens_out = _fresh(torch.empty((B, G + 1), dtype=i32, device=target.device), stream)
+        tokens_out = _empty((B, G + 1), i32, target.device, stream)
     else:
         _vec(tokens_out, "tokens_out", i32, B * (G + 1))
     _check(_lib.ds4moe_verify_drafts(
