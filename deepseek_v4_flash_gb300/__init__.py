@@ -486,6 +486,8 @@ class Attention:
         (the keys only). kv_len int32 [n_seq] counts the new tokens."""
         import torch
         n_seq = kv_len.numel()
+        if cu_q is None and k.dim() == 4 and k.shape[0] != n_seq:
+            raise ValueError("k: [n_seq, n_new, ...] for the sequences of kv_len")
         dt = torch.float32 if k.dtype == torch.float32 else self._dt
         ks = _rows(k, "k", dt, self._kv_row, self._kv_len)
         vs = 0
