@@ -450,7 +450,12 @@ class KVCache:
 
 
 class Attention:
-    """Append to, and attention over, a paged key-value cache (ds4moe_attn_*)."""
+    """Append to, and attention over, a paged key-value cache (ds4moe_attn_*).
+    One serves all layers of its shape that run one after another on a stream.
+
+    A call with `stream` does not wait for the current stream, nor that for the
+    call: order them. Its outputs may be used on either; the tensors passed in
+    must live until it is done."""
 
     def __init__(self, desc: AttentionDesc):
         h = ctypes.c_void_p()

@@ -19,8 +19,8 @@
 //     most 16 rows the instruction's legacy rate is far above what the memory
 //     feeds, and scores, weights and O stay in registers.
 // Measured: 24 sequences of 300 to 65537 positions, 8 heads of 128 (1.39 GB):
-// 229 us, 6.1 TB/s, 0.91 of the copy rate; one sequence of 701: 9.4 us, a chain
-// of dependent reads and the join's round trips.
+// 228 to 235 us, 5.9 to 6.1 TB/s, 0.88 to 0.91 of the copy rate; one sequence of
+// 701: 8.8 us, a chain of dependent reads and the join's round trips.
 // Rows of the cache that no query row sees are zero-filled on their way in, so
 // that a weight of 0 never meets what they hold.
 #include "attn.cuh"

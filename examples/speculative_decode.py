@@ -49,6 +49,8 @@ class Decoder:
         per_seq = pages // seqs
         table = torch.arange(pages, dtype=torch.int32)[torch.randperm(pages, generator=g)]
         self.table = table[:per_seq * seqs].view(seqs, per_seq).contiguous().cuda()
+        # one handle for all layers: they run one after another
+        self.attn = ds4.Attention(ds4.AttentionDesc(heads, kv_heads, dim, "bf16", window, n_sink, None, seqs, max_tokens))
         for i in range(layers):
             w = {k: torch.from_numpy(np.ascontiguousarray(v)).cuda() for k, v in synth.gen_layer(spec, seed, i).items()}
             desc = ds4.LayerDesc(H, spec.n_experts, spec.top_k, spec.ffn, spec.n_shared, ds4.ROUTE_LEARNED, spec.vocab,
@@ -58,9 +60,7 @@ class Decoder:
             self.layers.append(dict(
                 moe=ds4.Layer(desc, w), q=dense(heads * dim, H, 10 * i + 2, 0.1), k=dense(kv_heads * dim, H, 10 * i + 3, 0.1),
                 v=dense(kv_heads * dim, H, 10 * i + 4, 0.05), o=dense(H, heads * dim, 10 * i + 5, 0.05),
-                cache=ds4.KVCache(pool[0], pool[1], self.table),
-                attn=ds4.Attention(ds4.AttentionDesc(heads, kv_heads, dim, "bf16", window, n_sink, None, seqs,
-                                                     max_tokens))))
+                cache=ds4.KVCache(pool[0], pool[1], self.table)))
 
     def _rows(self, tokens, kv_len, shape, cu_q):
         h = self.emb[tokens.reshape(-1).long()]
@@ -70,11 +70,11 @@ class Decoder:
             q = L["q"].forward(n).bfloat16().view(*shape, self.heads, self.dim)
             k = L["k"].forward(n).view(*shape, self.kv_heads, self.dim)
             v = L["v"].forward(n).view(*shape, self.kv_heads, self.dim)
-            L["attn"].append(L["cache"], k, v, kv_len, cu_q=cu_q)
+            self.attn.append(L["cache"], k, v, kv_len, cu_q=cu_q)
             if cu_q is None:
-                o = L["attn"].decode(L["cache"], q, kv_len)
+                o = self.attn.decode(L["cache"], q, kv_len)
             else:
-                o = L["attn"].prefill(L["cache"], q, cu_q, kv_len)
+                o = self.attn.prefill(L["cache"], q, cu_q, kv_len)
             h += L["o"].forward(o.float().view(-1, self.heads * self.dim))
             L["moe"].forward_rmsnorm(h, h)
         ds4.rmsnorm(h, n)
@@ -95,7 +95,7 @@ class Decoder:
         return logits.view(*tokens.shape, self.vocab)
 
     def device_errors(self):
-        return [e for L in self.layers for e in (L["moe"].device_error(), L["attn"].device_error())]
+        return [L["moe"].device_error() for L in self.layers] + [self.attn.device_error()]
 
 
 def look_up(seq, drafts):
