@@ -11,7 +11,8 @@ Entry points mirror the C ABI in include/ds4moe.h:
 ds4moe_forward_rmsnorm, ``Layer.forward_host`` = ds4moe_forward_host,
 ``rmsnorm`` = ds4moe_rmsnorm, ``route_noalloc`` =
 ds4moe_route_noalloc, ``Dense`` = the ds4moe_dense_* calls, ``Attention`` (with
-``AttentionDesc`` and ``KVCache``) = ds4moe_attn_* and ds4moe_kv_append,
+``AttentionDesc``, ``KVCache`` and ``Rope``) = ds4moe_attn_*, ds4moe_kv_append and
+ds4moe_kv_append_rope,
 ``token_probs`` = ds4moe_token_probs, ``verify_drafts`` = ds4moe_verify_drafts.
 """
 from __future__ import annotations
@@ -70,6 +71,11 @@ class _KvCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("offset", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -115,6 +121,8 @@ def lib():
             "ds4moe_attn_create": (i32, [ctypes.POINTER(_AttnDesc), ctypes.POINTER(vp)]),
             "ds4moe_attn_destroy": (None, [vp]),
             "ds4moe_kv_append": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i64, i32, vp, vp, i32, i32, vp]),
+            "ds4moe_kv_append_rope": (i32, [vp, ctypes.POINTER(_KvCache), ctypes.POINTER(_Rope), vp, i64, vp, i64, vp,
+                                            i64, vp, i64, i32, vp, vp, i32, i32, vp]),
             "ds4moe_attn_decode": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i32, i32, vp, i64, vp]),
             "ds4moe_attn_prefill": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, vp, i32, i32, vp, i64, vp]),
             "ds4moe_attn_get_device_error": (i32, [vp, vp, ctypes.POINTER(u32)]),
@@ -449,6 +457,21 @@ class KVCache:
         self.ref = ctypes.byref(self.c)
 
 
+class Rope:
+    """Position rotation (ds4moe_rope): `inv_freq` fp32 CUDA tensor [rot_dim / 2],
+    radians per position; the rotated elements of a head start at `offset`, pair
+    i is (i, i + rot_dim / 2) of them, or with `interleaved` (2i, 2i + 1). Keeps
+    the tensor."""
+
+    def __init__(self, inv_freq, offset: int = 0, interleaved: bool = False, scale: float = 1.0):
+        import torch
+        _need(isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda and inv_freq.dtype == torch.float32 and
+              inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq: a contiguous CUDA fp32 tensor [rot_dim / 2]")
+        self.inv_freq = inv_freq
+        self.c = _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(offset), int(bool(interleaved)), scale)
+        self.ref = ctypes.byref(self.c)
+
+
 class Attention:
     """Append to, and attention over, a paged key-value cache (ds4moe_attn_*).
     One serves all layers of its shape that run one after another on a stream.
@@ -485,10 +508,15 @@ class Attention:
             raise ValueError("cache: a block-table row for every sequence")
         return cache.ref
 
-    def append(self, cache, k, v, kv_len, cu_q=None, stream=None):
+    def append(self, cache, k, v, kv_len, cu_q=None, stream=None, rope=None, q=None, q_out=None):
         """Write new keys and values (ds4moe_kv_append): k, v [n_tok, n_kv_heads,
         head_dim] or [n_seq, n_new, ...], fp32 or the cache's type; v may be None
-        (the keys only). kv_len int32 [n_seq] counts the new tokens."""
+        (the keys only). kv_len int32 [n_seq] counts the new tokens.
+
+        With `rope` (a Rope) the keys are rotated by their positions on the way,
+        and so are the queries `q` [..., n_heads, head_dim] of the same tokens and
+        k's type, into q_out (the cache's type; may be q itself if it is of that),
+        which is returned (ds4moe_kv_append_rope)."""
         import torch
         n_seq = kv_len.numel()
         if cu_q is None and k.dim() == 4 and k.shape[0] != n_seq:
@@ -500,12 +528,36 @@ class Attention:
             vs = _rows(v, "v", dt, self._kv_row, self._kv_len)
             if v.shape != k.shape:
                 raise ValueError("v: the shape of k")
-        _check(_lib.ds4moe_kv_append(
-            self._h, self._cache(cache, n_seq), k.data_ptr(), ks, None if v is None else v.data_ptr(), vs,
-            DT_F32 if dt == torch.float32 else self._code,
-            None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, n_seq + 1),
-            _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, k.numel() // self._kv_len, _stream(stream)),
-            "ds4moe_kv_append")
+        code = DT_F32 if dt == torch.float32 else self._code
+        cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, n_seq + 1)
+        n_tok, vp = k.numel() // self._kv_len, None if v is None else v.data_ptr()
+        if rope is None:
+            if q is not None or q_out is not None:
+                raise ValueError("q: only with rope")
+            _check(_lib.ds4moe_kv_append(
+                self._h, self._cache(cache, n_seq), k.data_ptr(), ks, vp, vs, code, cu,
+                _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_tok, _stream(stream)), "ds4moe_kv_append")
+            return None
+        if not isinstance(rope, Rope):
+            raise ValueError("rope: a Rope")
+        qs = os_ = 0
+        if q is not None:
+            qs = _rows(q, "q", dt, self._q_row, self._q_len)
+            if q.shape[:-2] != k.shape[:-2]:
+                raise ValueError("q: the tokens of k")
+            if q_out is None:
+                q_out, os_ = _empty(q.shape, self._dt, q.device, stream), self._q_len
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out: the shape of q")
+            else:
+                os_ = _rows(q_out, "q_out", self._dt, self._q_row, self._q_len)
+        elif q_out is not None:
+            raise ValueError("q_out: only with q")
+        _check(_lib.ds4moe_kv_append_rope(
+            self._h, self._cache(cache, n_seq), rope.ref, None if q is None else q.data_ptr(), qs,
+            None if q is None else q_out.data_ptr(), os_, k.data_ptr(), ks, vp, vs, code, cu,
+            _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_tok, _stream(stream)), "ds4moe_kv_append_rope")
+        return q_out
 
     def _out(self, q, out, stream):
         """The output and its row stride."""

@@ -46,6 +46,62 @@ __global__ void __launch_bounds__(1024) k_clean_rows(const int32_t *cu, int n_se
   if (bad) raise_flag(err, DS4MOE_DEVERR_LENGTH);
 }
 
+// The row bounds of a ragged append, ascending: in shared memory (s_cu) by a
+// whole block of 128 threads, or (more than AP_SEQS sequences) as they are, for
+// k_clean_rows has been there. Null: no bounds.
+__device__ __forceinline__ const int *append_bounds(const int32_t *cu_q, int n_seq, int n_tok, int *s_cu, uint32_t *err) {
+  if (!cu_q || n_seq > AP_SEQS) return cu_q;
+  bool bad = false;
+  int last = 0;
+  for (int i = threadIdx.x; i <= n_seq; i += 128) {
+    const int raw = cu_q[i], c = clamp_row(raw, n_tok);
+    bad |= raw != c || (i > 0 && clamp_row(cu_q[i - 1], n_tok) > c);
+    s_cu[i] = c;
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      if (blockIdx.x == 0) raise_flag(err, DS4MOE_DEVERR_LENGTH);
+      for (int i = 0; i <= n_seq; i++) s_cu[i] = last = max(last, s_cu[i]);
+    }
+    __syncthreads();
+  }
+  return s_cu;
+}
+
+// Sequence and position of new row t; false for a row of no sequence.
+__device__ __forceinline__ bool append_seq(const int32_t *kv_len, const int *cu, int n_seq, int n_new, int t, int &b,
+                                          long long &pos) {
+  int at, n;
+  if (!cu) {
+    b = t / n_new, at = t - b * n_new, n = n_new;
+  } else {
+    // the last sequence that starts at or before row t
+    int lo = 0, hi = n_seq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    const int c0 = cu[b], c1 = cu[b + 1];
+    if (t < c0 || t >= c1) return false;
+    at = t - c0, n = c1 - c0;
+  }
+  pos = (long long)kv_len[b] - n + at;
+  return true;
+}
+
+// Page of a position to be written; false, with the flag, where there is none.
+__device__ __forceinline__ bool append_page(const KvView &kv, int b, long long pos, uint32_t *err, int &page) {
+  if (pos < 0 || pos >= (long long)kv.width * kv.page_size) {
+    raise_flag(err, DS4MOE_DEVERR_LENGTH);
+    return false;
+  }
+  page = page_of(kv, b, (int)pos);
+  if (page < 0) raise_flag(err, DS4MOE_DEVERR_PAGE);
+  return page >= 0;
+}
+
 template <int DT, bool F32, int P>
 __global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
   __shared__ int s_cu[AP_SEQS + 1];
@@ -69,54 +125,14 @@ __global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
     if (F32) y[j] = reinterpret_cast<const uint4 *>(p)[1];
     row_t[j] = t, row_e[j] = e;
   }
-  const int *cu = a.cu_q;
-  if (a.cu_q && a.n_seq <= AP_SEQS) {
-    bool bad = false;
-    int last = 0;
-    for (int i = threadIdx.x; i <= a.n_seq; i += 128) {
-      const int raw = a.cu_q[i], c = clamp_row(raw, a.n_tok);
-      bad |= raw != c || (i > 0 && clamp_row(a.cu_q[i - 1], a.n_tok) > c);
-      s_cu[i] = c;
-    }
-    if (__syncthreads_or(bad)) {
-      if (threadIdx.x == 0) {
-        if (blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
-        for (int i = 0; i <= a.n_seq; i++) s_cu[i] = last = max(last, s_cu[i]);
-      }
-      __syncthreads();
-    }
-    cu = s_cu;
-  }
+  const int *cu = append_bounds(a.cu_q, a.n_seq, a.n_tok, s_cu, a.err);
 #pragma unroll
   for (int j = 0; j < P; j++) {
     if (row_t[j] < 0) continue;
     const int t = row_t[j], e = row_e[j];
-    int b, at, n;
-    if (!a.cu_q) {
-      b = t / a.n_new, at = t - b * a.n_new, n = a.n_new;
-    } else {
-      // the last sequence that starts at or before row t
-      int lo = 0, hi = a.n_seq;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
-      const int c0 = cu[b], c1 = cu[b + 1];
-      if (t < c0 || t >= c1) continue;  // a row of no sequence
-      at = t - c0, n = c1 - c0;
-    }
-    const long long pos = (long long)a.kv_len[b] - n + at;
-    if (pos < 0 || pos >= (long long)a.kv.width * a.kv.page_size) {
-      raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
-      continue;
-    }
-    const int page = page_of(a.kv, b, (int)pos);
-    if (page < 0) {
-      raise_flag(a.err, DS4MOE_DEVERR_PAGE);
-      continue;
-    }
+    int b, page;
+    long long pos;
+    if (!append_seq(a.kv_len, cu, a.n_seq, a.n_new, t, b, pos) || !append_page(a.kv, b, pos, a.err, page)) continue;
     const int row = (int)pos - page_index(a.kv, (int)pos) * a.kv.page_size, h = e / a.D, d = e - h * a.D;
     dst[j] = const_cast<uint16_t *>(kv ? a.kv.v : a.kv.k);
     dst[j] += kv ? (long long)page * a.kv.v_page + (long long)row * a.kv.v_row + (long long)h * a.kv.v_head + d
@@ -132,6 +148,168 @@ __global__ void __launch_bounds__(128) k_kv_append(const AppendArgs a) {
                      Half16<DT>::down(f(y[j].x), f(y[j].y)), Half16<DT>::down(f(y[j].z), f(y[j].w)));
     }
     *reinterpret_cast<uint4 *>(dst[j]) = o;
+  }
+}
+
+// The append with the positions' rotation on the way, for the keys and, in the
+// same launch, the queries. Pair (x, y) of a head at position p becomes
+//   (x cos - y sin, y cos + x sin),  angle p * inv_freq[i],
+// in 32 bits, rounded once. A thread takes 16 elements (two pieces of 8, so
+// that it holds both halves of its pairs) of `per` rows of one token: the
+// angles' sines are computed once for all of them. Bound by the bytes: 12291
+// tokens of 32 + 2 x 8 heads of 128 from fp32: see DESIGN's table.
+//
+// Angles: p * inv_freq / 2 pi in turns, modulo one turn, in 64-bit fixed point
+// (a phase accumulator): the product with the integer p wraps by itself. An
+// fp32 frequency is m 2^e, and 2^64 / 2 pi a constant of 64 bits, so the phase of
+// position 2^31 is off by inv_freq 2^-33 turns at most, where fp32 would leave
+// nothing of the angle. FP64, of which this GPU has little, is not needed.
+struct RopeArgs {
+  KvView kv;
+  const void *q, *k, *v;  // q, v may be null
+  uint16_t *q_out;
+  long long q_stride, k_stride, v_stride, qo_stride;
+  const int32_t *kv_len, *cu_q;
+  int32_t n_seq, n_tok, n_new, nq, n_kv, rows;  // rows of a token: nq queries, n_kv keys, n_kv (or no) values
+  int32_t D, ish;                               // log2 of the 16-element items of a row
+  int32_t rot, off, interleaved;
+  int32_t per, slices;                          // rows of a thread, threads of a token's item
+  const float *inv_freq;
+  float scale;
+  uint32_t *err;
+};
+
+// inv_freq / 2 pi in turns, modulo 1, times 2^64 (f finite).
+__device__ __forceinline__ unsigned long long turns_of(float f) {
+  const uint32_t u = __float_as_uint(f), ex = u >> 23 & 255;
+  const unsigned long long m = ex ? (u & 0x7FFFFF) | 0x800000 : u & 0x7FFFFF;
+  // 2^66 / 2 pi = 2^64 * 2 / pi, so inv_freq / 2 pi = m * C * 2^(e - 2), e = ex - 150
+  constexpr unsigned long long C = 0xA2F9836E4E441529ull;
+  const unsigned long long lo = m * C, hi = __umul64hi(m, C);
+  const int s = 152 - (int)max(ex, 1u);
+  const unsigned long long t = s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? hi << (64 - s) | lo >> s : lo << -s;
+  return u >> 31 ? 0ull - t : t;
+}
+
+// Cosine and sine of position p at frequency f.
+__device__ __forceinline__ void rope_angle(float f, int p, float scale, float &c, float &s) {
+  const unsigned long long phase = turns_of(f) * (unsigned long long)(long long)p;
+  // the nearest quarter turn, and what is left of at most an eighth
+  const int q = (int)((phase + (1ull << 61)) >> 62);
+  const int r = (int)((long long)(phase - ((unsigned long long)q << 62)) >> 32);
+  float c0, s0;
+  sincospif((float)r * 0x1p-31f, &s0, &c0);
+  if (!isfinite(f)) c0 = s0 = __int_as_float(0x7FC00000);
+  c0 *= scale, s0 *= scale;
+  c = q & 1 ? s0 : c0, s = q & 1 ? c0 : s0;
+  if (q == 1 || q == 2) c = -c;
+  if (q & 2) s = -s;
+}
+
+template <int DT, bool F32, int U>
+__global__ void __launch_bounds__(128) k_append_rope(const RopeArgs a) {
+  __shared__ int s_cu[AP_SEQS + 1];
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long idx = (long long)blockIdx.x * 128 + threadIdx.x, rest = idx >> a.ish;
+  const int i = (int)(idx & ((1 << a.ish) - 1));
+  const long long tt = rest / a.slices;
+  const int sl = (int)(rest - tt * a.slices), t = (int)min(tt, (long long)a.n_tok);
+  const int r1 = t < a.n_tok ? min(a.rows, (sl + 1) * a.per) : 0;
+  // the two pieces: of the turned part first (item i < rot / 16), then what passes
+  const bool turns = i < a.rot >> 4;
+  int ea, eb;
+  if (turns) {
+    ea = a.off + (a.interleaved ? 16 * i : 8 * i), eb = ea + (a.interleaved ? 8 : a.rot >> 1);
+  } else {
+    ea = 16 * i - a.rot, eb = ea + 8;
+    if (ea >= a.off) ea += a.rot;
+    if (eb >= a.off) eb += a.rot;
+  }
+  constexpr int W = F32 ? 2 : 1;  // 16-byte words of a piece
+  uint4 x[U][2 * W];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      const int r = r0 + j;
+      if (r >= r1) continue;
+      const char *p;
+      if (r < a.nq) p = (const char *)a.q + ((long long)t * a.q_stride + (long long)r * a.D) * (F32 ? 4 : 2);
+      else if (r < a.nq + a.n_kv) p = (const char *)a.k + ((long long)t * a.k_stride + (long long)(r - a.nq) * a.D) * (F32 ? 4 : 2);
+      else p = (const char *)a.v + ((long long)t * a.v_stride + (long long)(r - a.nq - a.n_kv) * a.D) * (F32 ? 4 : 2);
+#pragma unroll
+      for (int w = 0; w < W; w++) {
+        x[j][w] = reinterpret_cast<const uint4 *>(p + ea * (F32 ? 4 : 2))[w];
+        x[j][W + w] = reinterpret_cast<const uint4 *>(p + eb * (F32 ? 4 : 2))[w];
+      }
+    }
+  };
+  load(sl * a.per);
+  const int *cu = append_bounds(a.cu_q, a.n_seq, a.n_tok, s_cu, a.err);
+  int b, page = 0, row = 0;
+  long long pos;
+  if (sl * a.per >= r1 || !append_seq(a.kv_len, cu, a.n_seq, a.n_new, t, b, pos)) return;
+  bool store = true;  // the cache has a place for the token
+  if (r1 > a.nq) {
+    store = append_page(a.kv, b, pos, a.err, page);
+    if (store) row = (int)pos - page_index(a.kv, (int)pos) * a.kv.page_size;
+  }
+  float cs[8], sn[8];
+  if (turns) {
+    const float4 f0 = reinterpret_cast<const float4 *>(a.inv_freq + 8 * i)[0], f1 = reinterpret_cast<const float4 *>(a.inv_freq + 8 * i)[1];
+    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+    for (int e = 0; e < 8; e++) rope_angle(f[e], (int)pos, a.scale, cs[e], sn[e]);
+  }
+  for (int r0 = sl * a.per; r0 < r1; r0 += U) {
+    if (r0 != sl * a.per) load(r0);
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      const int r = r0 + j;
+      if (r >= r1) continue;
+      const bool is_q = r < a.nq, is_v = r >= a.nq + a.n_kv;
+      uint16_t *dst;
+      if (is_q) {
+        dst = a.q_out + (long long)t * a.qo_stride + (long long)r * a.D;
+      } else {
+        if (!store) continue;
+        dst = is_v ? const_cast<uint16_t *>(a.kv.v) + (long long)page * a.kv.v_page + (long long)row * a.kv.v_row + (long long)(r - a.nq - a.n_kv) * a.kv.v_head
+                   : const_cast<uint16_t *>(a.kv.k) + (long long)page * a.kv.k_page + (long long)row * a.kv.k_row + (long long)(r - a.nq) * a.kv.k_head;
+      }
+      if (!F32 && (is_v || !turns)) {  // bits are copied
+        *reinterpret_cast<uint4 *>(dst + ea) = x[j][0];
+        *reinterpret_cast<uint4 *>(dst + eb) = x[j][W];
+        continue;
+      }
+      float v[16];
+      const uint32_t *u = reinterpret_cast<const uint32_t *>(x[j]);
+      if (F32) {
+#pragma unroll
+        for (int e = 0; e < 16; e++) v[e] = __uint_as_float(u[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float2 y = Half16<DT>::up(u[e]);
+          v[2 * e] = y.x, v[2 * e + 1] = y.y;
+        }
+      }
+      if (turns && !is_v) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          if (a.interleaved) {
+            const float p = v[2 * e], q = v[2 * e + 1];
+            v[2 * e] = fmaf(p, cs[e], -(q * sn[e])), v[2 * e + 1] = fmaf(q, cs[e], p * sn[e]);
+          } else {
+            const float p = v[e], q = v[8 + e];
+            v[e] = fmaf(p, cs[e], -(q * sn[e])), v[8 + e] = fmaf(q, cs[e], p * sn[e]);
+          }
+        }
+      }
+      *reinterpret_cast<uint4 *>(dst + ea) = make_uint4(Half16<DT>::down(v[0], v[1]), Half16<DT>::down(v[2], v[3]),
+                                                        Half16<DT>::down(v[4], v[5]), Half16<DT>::down(v[6], v[7]));
+      *reinterpret_cast<uint4 *>(dst + eb) = make_uint4(Half16<DT>::down(v[8], v[9]), Half16<DT>::down(v[10], v[11]),
+                                                        Half16<DT>::down(v[12], v[13]), Half16<DT>::down(v[14], v[15]));
+    }
   }
 }
 
@@ -192,6 +370,21 @@ const void *append_fn(bool bf, bool f32, bool two) {
   if (two)
     return !f32 ? (const void *)k_kv_append<B, false, 2> : bf ? (const void *)k_kv_append<B, true, 2> : (const void *)k_kv_append<F, true, 2>;
   return !f32 ? (const void *)k_kv_append<B, false, 1> : bf ? (const void *)k_kv_append<B, true, 1> : (const void *)k_kv_append<F, true, 1>;
+}
+
+const void *rope_fn(bool bf, bool f32, bool four) {
+  constexpr int B = DS4MOE_DT_BF16, F = DS4MOE_DT_F16;
+  if (four)
+    return bf ? f32 ? (const void *)k_append_rope<B, true, 4> : (const void *)k_append_rope<B, false, 4>
+              : f32 ? (const void *)k_append_rope<F, true, 4> : (const void *)k_append_rope<F, false, 4>;
+  return bf ? f32 ? (const void *)k_append_rope<B, true, 1> : (const void *)k_append_rope<B, false, 1>
+            : f32 ? (const void *)k_append_rope<F, true, 1> : (const void *)k_append_rope<F, false, 1>;
+}
+
+// Whether [p, p + n) and [q, q + m) share a byte.
+bool overlap(const void *p, long long n, const void *q, long long m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + (uintptr_t)m && b < a + (uintptr_t)n;
 }
 
 ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
@@ -335,6 +528,69 @@ ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, con
   }
   e = launch_pdl(fn, dim3((unsigned)(((long long)n_tok * a.per_tok + per - 1) / per), v_new ? 2 : 1),
                                    dim3(128), 0, (cudaStream_t)stream, args, true);
+  h->launches++;
+  return at_status(e);
+}
+
+ds4moe_status ds4moe_kv_append_rope(ds4moe_attn *h, const ds4moe_kv_cache *cache, const ds4moe_rope *rope,
+                                    const void *q_new, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                    const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                                    int32_t src_dtype, const int32_t *cu_q, const int32_t *kv_len, int32_t n_seq,
+                                    int32_t n_tok, void *stream) {
+  if (!h || n_seq < 0 || n_seq > h->d.max_seqs || n_tok < 0 || n_tok > h->d.max_tokens) return DS4MOE_ERR_INVALID_ARG;
+  if (src_dtype != DS4MOE_DT_F32 && src_dtype != h->d.dtype) return DS4MOE_ERR_INVALID_ARG;
+  const int D = h->d.head_dim;
+  if (!rope || rope->rot_dim < 16 || rope->rot_dim % 16 || rope->offset < 0 || rope->offset % 8 || rope->rot_dim > D ||
+      rope->offset > D - rope->rot_dim || (rope->interleaved != 0 && rope->interleaved != 1) || !isfinite(rope->scale))
+    return DS4MOE_ERR_INVALID_ARG;
+  if (!q_new != !q_out) return DS4MOE_ERR_INVALID_ARG;
+  if (n_seq == 0 || n_tok == 0) return DS4MOE_OK;
+  if (!cu_q && n_tok % n_seq) return DS4MOE_ERR_INVALID_ARG;
+  const long long row = (long long)h->d.n_kv_heads * D, q_row = (long long)h->d.n_heads * D;
+  const bool f32 = src_dtype == DS4MOE_DT_F32;
+  RopeArgs a = {};
+  if (!view_of(h, cache, a.kv)) return DS4MOE_ERR_INVALID_ARG;
+  if (n_tok == 1) k_stride = v_stride = row, q_stride = q_out_stride = q_row;
+  if (!stride_ok(k_stride, row) || !al16(k_new) || !at_dev_ptr(k_new)) return DS4MOE_ERR_INVALID_ARG;
+  if (v_new && (!stride_ok(v_stride, row) || !al16(v_new) || !at_dev_ptr(v_new))) return DS4MOE_ERR_INVALID_ARG;
+  if (q_new) {
+    if (!stride_ok(q_stride, q_row) || !al16(q_new) || !at_dev_ptr(q_new)) return DS4MOE_ERR_INVALID_ARG;
+    if (!stride_ok(q_out_stride, q_row) || !al16(q_out) || !at_dev_ptr(q_out)) return DS4MOE_ERR_INVALID_ARG;
+    // in place: every element is read and written by the same thread
+    const bool same = q_new == q_out && !f32 && q_stride == q_out_stride;
+    const long long n = n_tok - 1, src = f32 ? 4 : 2;
+    const long long out_bytes = (n * q_out_stride + q_row) * 2;
+    if (!same && overlap(q_out, out_bytes, q_new, (n * q_stride + q_row) * src)) return DS4MOE_ERR_INVALID_ARG;
+    if (overlap(q_out, out_bytes, k_new, (n * k_stride + row) * src) ||
+        (v_new && overlap(q_out, out_bytes, v_new, (n * v_stride + row) * src)))
+      return DS4MOE_ERR_INVALID_ARG;
+  }
+  if (!at_dev_ptr(kv_len) || (cu_q && !at_dev_ptr(cu_q)) || !at_dev_ptr(rope->inv_freq) || !al16(rope->inv_freq))
+    return DS4MOE_ERR_INVALID_ARG;
+  a.q = q_new, a.k = k_new, a.v = v_new, a.q_out = (uint16_t *)q_out;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.qo_stride = q_out_stride;
+  a.kv_len = kv_len, a.cu_q = cu_q, a.n_seq = n_seq, a.n_tok = n_tok, a.n_new = cu_q ? 0 : n_tok / n_seq;
+  a.nq = q_new ? h->d.n_heads : 0, a.n_kv = h->d.n_kv_heads, a.rows = a.nq + a.n_kv * (v_new ? 2 : 1);
+  a.D = D;
+  while (16 << a.ish < D) a.ish++;
+  a.rot = rope->rot_dim, a.off = rope->offset, a.interleaved = rope->interleaved;
+  a.inv_freq = rope->inv_freq, a.scale = rope->scale, a.err = h->err;
+  const long long items = (long long)n_tok * a.rows << a.ish;
+  const bool four = items > (long long)h->n_sm * 2048;
+  a.per = four ? 8 : 1;
+  a.slices = (a.rows + a.per - 1) / a.per;
+  cudaError_t e = cudaSuccess;
+  if (cu_q && n_seq > AP_SEQS) {
+    a.cu_q = h->tile.cu;
+    void *clean[] = {(void *)&cu_q, &n_seq, &n_tok, &h->tile.cu, &h->err};
+    e = launch_pdl((const void *)k_clean_rows, dim3(1), dim3(1024), 0, (cudaStream_t)stream, clean, true);
+    h->launches++;
+    if (e != cudaSuccess) return at_status(e);
+  }
+  void *args[] = {&a};
+  const long long threads = (long long)n_tok * a.slices << a.ish;
+  e = launch_pdl(rope_fn(h->d.dtype == DS4MOE_DT_BF16, f32, four), dim3((unsigned)((threads + 127) / 128)), dim3(128), 0,
+                 (cudaStream_t)stream, args, true);
   h->launches++;
   return at_status(e);
 }

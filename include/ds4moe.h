@@ -446,6 +446,39 @@ ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, con
                                const void *v_new, int64_t v_stride, int32_t src_dtype, const int32_t *cu_q,
                                const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *stream);
 
+/* The same append with the position rotation on the way, for the keys and, in
+ * the same launch, the queries of the new tokens. (The pages run rope as calls
+ * of its own: "DeepSeek V4 Flash -- DFlash Integration", Forward Pass.)
+ * The pair (x, y) number i of a head's rotated elements becomes, at position p,
+ *   x' = scale * (x cos - y sin),  y' = scale * (y cos + x sin),
+ *   angle = p * inv_freq[i],
+ * in 32 bits, rounded once to the cache's type; elements outside
+ * [offset, offset + rot_dim) and values pass as in ds4moe_kv_append. Angles are
+ * those of the fp32 frequencies as they are, at any position: p * inv_freq / 2 pi
+ * is reduced to one turn in 64-bit fixed point, exact to |inv_freq| * 2^-33 turns
+ * at p = 2^31. A frequency that is not finite gives NaN.
+ *   q_new   [n_tok][n_heads][head_dim], rows q_stride elements apart, of
+ *           src_dtype; may be NULL (then q_out too)
+ *   q_out   the same rows in the cache's type, q_out_stride apart; may be q_new
+ *           itself (of the cache's type, with the same stride), must not overlap
+ *           the inputs otherwise. Rows of no sequence are left as they are; a
+ *           row whose position the cache has no place for is rotated all the same.
+ * Other arguments, flags and errors as ds4moe_kv_append; INVALID_ARG also for a
+ * rope that is not as below. */
+typedef struct {
+  const float *inv_freq; /* device, [rot_dim / 2], 16-byte aligned: radians per position */
+  int32_t rot_dim;       /* rotated elements of a head: a multiple of 16, 16..head_dim  */
+  int32_t offset;        /* the first of them: a multiple of 8                          */
+  int32_t interleaved;   /* pair i: 0: elements i and i + rot_dim/2; 1: 2i and 2i + 1   */
+  float scale;           /* of cosine and sine, usually 1                               */
+} ds4moe_rope;
+
+ds4moe_status ds4moe_kv_append_rope(ds4moe_attn *h, const ds4moe_kv_cache *cache, const ds4moe_rope *rope,
+                                    const void *q_new, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                    const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                                    int32_t src_dtype, const int32_t *cu_q, const int32_t *kv_len, int32_t n_seq,
+                                    int32_t n_tok, void *stream);
+
 /* Attention of n_new (1..DS4MOE_ATTN_MAX_NEW) new tokens of every sequence.
  *   q, out  [n_seq * n_new][n_heads][head_dim], rows q_stride / out_stride
  *           elements apart, 16-byte aligned; out must not overlap q or the
