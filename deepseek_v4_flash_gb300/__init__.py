@@ -10,7 +10,7 @@ Entry points mirror the C ABI in include/ds4moe.h:
 ``Layer.forward`` = ds4moe_forward, ``Layer.forward_rmsnorm`` =
 ds4moe_forward_rmsnorm, ``Layer.forward_host`` = ds4moe_forward_host,
 ``rmsnorm`` = ds4moe_rmsnorm, ``route_noalloc`` =
-ds4moe_route_noalloc, ``Dense`` = the ds4moe_dense_* calls, ``Attention`` (with
+ds4moe_route_noalloc, ``Dense`` = the ds4moe_dense_* calls, ``Adapters`` = ds4moe_adapters_*, ``Attention`` (with
 ``AttentionDesc``, ``KVCache`` and ``Rope``) = ds4moe_attn_*, ds4moe_kv_append and
 ds4moe_kv_append_rope,
 ``token_probs`` = ds4moe_token_probs, ``verify_drafts`` = ds4moe_verify_drafts.
@@ -28,7 +28,8 @@ F32, Q8_0, Q2S, Q4S = 0, 1, 2, 3
 FMT = {"f32": F32, "q8_0": Q8_0, "q2s": Q2S, "q4s": Q4S}
 ROUTE_LEARNED, ROUTE_HASH = 0, 1
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED", 3: "ERR_OOM", 4: "ERR_CUDA", 5: "ERR_DEVICE"}
-DEVERR_TOKEN_ID, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_INTERNAL, DEVERR_PAGE, DEVERR_LENGTH = 1, 2, 4, 8, 16, 32
+DEVERR_TOKEN_ID, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_INTERNAL, DEVERR_PAGE, DEVERR_LENGTH, DEVERR_ADAPTER = \
+    1, 2, 4, 8, 16, 32, 64
 DT_F32, DT_BF16, DT_F16 = 0, 1, 2
 DTYPE = {"fp32": DT_F32, "bf16": DT_BF16, "fp16": DT_F16}
 ATTN_MAX_NEW, MAX_DRAFT = 16, 64
@@ -118,6 +119,13 @@ def lib():
             "ds4moe_dense_device_bytes": (ctypes.c_uint64, [vp]),
             "ds4moe_dense_launch_count": (ctypes.c_uint64, [vp]),
             "ds4moe_dense_debug_config": (i32, [vp, i32, i32, i32, i32]),
+            "ds4moe_adapters_create": (i32, [i32, i32, i32, i32, i32, i32, ctypes.POINTER(vp)]),
+            "ds4moe_adapters_set": (i32, [vp, i32, i32, vp, vp, ctypes.c_float, vp]),
+            "ds4moe_adapters_forward": (i32, [vp, vp, i64, i32, vp, i32, vp, i64, vp, i64, vp]),
+            "ds4moe_adapters_get_device_error": (i32, [vp, vp, ctypes.POINTER(u32)]),
+            "ds4moe_adapters_destroy": (None, [vp]),
+            "ds4moe_adapters_device_bytes": (ctypes.c_uint64, [vp]),
+            "ds4moe_adapters_launch_count": (ctypes.c_uint64, [vp]),
             "ds4moe_attn_create": (i32, [ctypes.POINTER(_AttnDesc), ctypes.POINTER(vp)]),
             "ds4moe_attn_destroy": (None, [vp]),
             "ds4moe_kv_append": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i64, i32, vp, vp, i32, i32, vp]),
@@ -317,13 +325,26 @@ class Dense:
         except Exception:
             pass
 
-    def forward(self, x, y=None, stream=None, n_tok=None):
-        """y = W x (ds4moe_dense_forward); returns y."""
+    def forward(self, x, y=None, stream=None, n_tok=None, adapters=None, slots=None):
+        """y = W x (ds4moe_dense_forward); returns y. With `adapters` (an Adapters
+        of the same shape) and `slots` the tokens' low-rank adapters are added
+        (ds4moe_adapters_forward)."""
         import torch
         n = x.shape[0] if n_tok is None else n_tok
+        if adapters is not None:
+            _need(isinstance(adapters, Adapters) and (adapters.n_out, adapters.n_in) == (self.n_out, self.n_in),
+                  "adapters: Adapters of this matrix's shape")
+        elif slots is not None:
+            raise ValueError("slots: only with adapters")
         if y is None:
             y = torch.empty((n, self.n_out), dtype=torch.float32, device=x.device)
+        if adapters is None:
+            _check(lib().ds4moe_dense_forward(self._h, _ptr(x), n, _ptr(y), _stream(stream)), "ds4moe_dense_forward")
+            return y
+        _need(x.is_contiguous() and y.is_contiguous() and x.dtype == torch.float32, "x and y: contiguous, x fp32")
+        call = adapters._args(x[:n], slots, y[:n], None)  # refused before anything is enqueued
         _check(lib().ds4moe_dense_forward(self._h, _ptr(x), n, _ptr(y), _stream(stream)), "ds4moe_dense_forward")
+        adapters._forward(call, stream)
         return y
 
     def device_error(self, stream=None) -> int:
@@ -412,6 +433,84 @@ def _empty(shape, dtype, device, stream):
 def _torch_dtype(dt):
     import torch
     return {DT_F32: torch.float32, DT_BF16: torch.bfloat16, DT_F16: torch.float16}[dt]
+
+
+class Adapters:
+    """Low-rank adapters of many requests beside a shared projection
+    (ds4moe_adapters_*): `n_slots` places for adapters of up to `max_rank`, whose
+    weights are of `dtype` ("bf16" | "fp16")."""
+
+    def __init__(self, n_out: int, n_in: int, n_slots: int, max_rank: int, dtype: str = "bf16", max_tokens: int = 1):
+        h = ctypes.c_void_p()
+        _check(lib().ds4moe_adapters_create(n_out, n_in, n_slots, max_rank, DTYPE[dtype], max_tokens, ctypes.byref(h)),
+               "ds4moe_adapters_create")
+        self._h, self.n_out, self.n_in, self.n_slots, self.max_rank = h, n_out, n_in, n_slots, max_rank
+        self._dt, self._code = _torch_dtype(DTYPE[dtype]), DTYPE[dtype]
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ds4moe_adapters_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def set(self, slot: int, a, b, scale: float = 1.0, stream=None):
+        """Copy an adapter into a slot (ds4moe_adapters_set): a [rank, n_in], b
+        [n_out, rank] contiguous, which must live until the copy is done. Later
+        calls on the stream use it."""
+        for t, name in ((a, "a"), (b, "b")):
+            _need(hasattr(t, "is_cuda") and t.is_cuda and t.dim() == 2 and t.dtype == self._dt and t.is_contiguous(),
+                  f"{name}: a contiguous CUDA matrix of {self._dt}")
+        _need(a.shape[1] == self.n_in and b.shape == (self.n_out, a.shape[0]), "a [rank, n_in] and b [n_out, rank]")
+        _check(_lib.ds4moe_adapters_set(self._h, slot, a.shape[0], a.data_ptr(), b.data_ptr(), scale, _stream(stream)),
+               "ds4moe_adapters_set")
+
+    def clear(self, slot: int, stream=None):
+        """Empty a slot: it adds nothing."""
+        _check(_lib.ds4moe_adapters_set(self._h, slot, 0, None, None, 0.0, _stream(stream)), "ds4moe_adapters_set")
+
+    def _args(self, x, slots, y, base):
+        import torch
+        f32 = torch.float32
+        dt = f32 if x.dtype == f32 else self._dt
+        n = x.numel() // self.n_in
+        xs = _rows(x, "x", dt, (self.n_in,), self.n_in)
+        ys, bs = _rows(y, "y", f32, (self.n_out,), self.n_out), 0
+        _need(y.shape[:-1] == x.shape[:-1], "y: the tokens of x")
+        if base is not None:
+            bs = _rows(base, "base", f32, (self.n_out,), self.n_out)
+            _need(base.shape == y.shape, "base: the shape of y")
+        return (x.data_ptr(), xs, DT_F32 if dt == f32 else self._code, _vec(slots, "slots", torch.int32, n), n,
+                None if base is None else base.data_ptr(), bs, y.data_ptr(), ys)
+
+    def _forward(self, args, stream):
+        _check(_lib.ds4moe_adapters_forward(self._h, *args, _stream(stream)), "ds4moe_adapters_forward")
+
+    def forward(self, x, slots, y, base=None, stream=None):
+        """y = base + scale B (A x) with each token's adapter
+        (ds4moe_adapters_forward): x [..., n_in] fp32 or the adapters' type, slots
+        int32, one per token (-1: none), y and base fp32 [..., n_out]; base None:
+        y is added to. Returns y."""
+        self._forward(self._args(x, slots, y, base), stream)
+        return y
+
+    def device_error(self, stream=None) -> int:
+        """Synchronise, read and clear the device error flags (0 = none)."""
+        f = ctypes.c_uint32(0)
+        st = lib().ds4moe_adapters_get_device_error(self._h, _stream(stream), ctypes.byref(f))
+        if st not in (0, 5):
+            raise Ds4MoeError(st, "ds4moe_adapters_get_device_error")
+        return int(f.value)
+
+    def device_bytes(self) -> int:
+        return int(lib().ds4moe_adapters_device_bytes(self._h))
+
+    def launch_count(self) -> int:
+        return int(lib().ds4moe_adapters_launch_count(self._h))
 
 
 @dataclass

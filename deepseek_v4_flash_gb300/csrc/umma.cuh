@@ -77,4 +77,68 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)
   for (int i = 0; i < 16; i++) a[i] = __uint_as_float(r[i]), b[i] = __uint_as_float(r[16 + i]);
 }
 
+// Descriptor of a 128-byte swizzled operand: 8-row atoms of 1024 bytes, `lbo`
+// the distance of 64-element columns (used by the operand whose rows run
+// along K, i.e. V).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= 1ull << 46;
+  d |= 2ull << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// Waits for this thread's loads; the values pass through so that no use can
+// be moved before the wait.
+__device__ __forceinline__ void tmem_wait_ld(float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// One lane of a converged warp, the way the compiler knows to be one: operands
+// of the instructions it issues stay in uniform registers (a branch on the
+// lane number made every product and every copy cost a loop over lanes: a
+// product step 700 cycles instead of its 512 on the tensor cores).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Eight 16-byte pieces per lane, exchanged within groups of eight lanes: lane
+// j's piece i becomes piece j of lane i. A row per lane turns into eight rows
+// whose 128 bytes lie across the lanes, so that a store writes four whole
+// lines instead of an eighth of 32.
+__device__ __forceinline__ void transpose8(uint32_t (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int c = 0; c < 8; c++)
+      if (!(c & d)) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[4 * c + k] : x[4 * (c | d) + k], d);
+          x[4 * c + k] = up ? got : x[4 * c + k];
+          x[4 * (c | d) + k] = up ? x[4 * (c | d) + k] : got;
+        }
+      }
+  }
+}
+
 }  // namespace ds4

@@ -77,6 +77,9 @@ typedef enum { DS4MOE_F32 = 0, DS4MOE_Q8_0 = 1, DS4MOE_Q2S = 2, DS4MOE_Q4S = 3 }
 
 typedef enum { DS4MOE_ROUTE_LEARNED = 0, DS4MOE_ROUTE_HASH = 1 } ds4moe_route_kind;
 
+/* Element types of activations (and of 16-bit weights and caches). */
+typedef enum { DS4MOE_DT_F32 = 0, DS4MOE_DT_BF16 = 1, DS4MOE_DT_F16 = 2 } ds4moe_dtype;
+
 /* Device error flag bits (ds4moe_get_device_error). */
 #define DS4MOE_DEVERR_TOKEN_ID 1u   /* hash token id outside [0, vocab)     */
 #define DS4MOE_DEVERR_NONFINITE 2u  /* non-finite activation quantised      */
@@ -84,6 +87,7 @@ typedef enum { DS4MOE_ROUTE_LEARNED = 0, DS4MOE_ROUTE_HASH = 1 } ds4moe_route_ki
 #define DS4MOE_DEVERR_INTERNAL 8u   /* an internal consistency check failed */
 #define DS4MOE_DEVERR_PAGE 16u      /* block-table entry outside the cache  */
 #define DS4MOE_DEVERR_LENGTH 32u    /* length or count outside its buffers  */
+#define DS4MOE_DEVERR_ADAPTER 64u   /* adapter slot outside [-1, n_slots)   */
 
 typedef struct {
   uint32_t abi_version; /* = DS4MOE_ABI_VERSION */
@@ -355,6 +359,53 @@ uint64_t ds4moe_dense_launch_count(const ds4moe_dense *h);
 ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst, int32_t ns, int32_t tc);
 
 /* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection: every token
+ * brings the slot of its request's adapter,
+ *   y[t] = base[t] + scale_s * B_s (A_s x[t]),  s = slots[t];  s = -1: base[t].
+ * (The pages have no adapters; the projection is ds4moe_dense_forward, whose
+ * output is the base.) x and weights as they are, products and sums in 32 bits:
+ * no rounding to fewer bits on the way (many tokens: a product's fp32 operand
+ * is taken as the sum of two 11-bit numbers, off by 2^-21 of it at most).
+ *
+ * ds4moe_adapters_create: places for n_slots (1..4096) adapters of up to max_rank
+ *   (1..256) in `dtype` (DS4MOE_DT_BF16 or DS4MOE_DT_F16) on the current device,
+ *   all empty; n_out 1..2^24, n_in a multiple of 32 up to 65536, max_tokens
+ *   1..65536. Device memory: n_slots * 2 bytes * (max_rank to 32 * n_in + max_rank
+ *   to 8 * n_out), and max_tokens * (max_rank to 32) * 4 of workspace.
+ *   Synchronises. Errors: INVALID_ARG, UNSUPPORTED (more slots or a larger rank),
+ *   OOM, CUDA; on error *out is NULL.
+ * ds4moe_adapters_set: copies an adapter of `rank` (0..max_rank; 0 empties the
+ *   slot, a and b may be NULL) into a slot: a [rank][n_in], b [n_out][rank],
+ *   contiguous, device. scale finite. Enqueued on `stream`: calls there before
+ *   it use the old adapter, calls after it the new one. Ranks of the slots may
+ *   differ.
+ * ds4moe_adapters_forward: n_tok 0..max_tokens.
+ *   x      [n_tok][n_in] of x_dtype (DS4MOE_DT_F32 or the adapters' type), rows
+ *          x_stride elements apart: 16-byte aligned rows
+ *   slots  [n_tok] int32, in any order; an empty slot adds nothing; one outside
+ *          [-1, n_slots) adds nothing and raises DS4MOE_DEVERR_ADAPTER
+ *   base   [n_tok][n_out] fp32, base_stride apart; NULL or y itself (with its
+ *          stride): y is added to
+ *   y      [n_tok][n_out] fp32, y_stride apart; must not overlap x, nor base
+ *          otherwise
+ *   Enqueued on `stream` (one launch up to 64 tokens, else three), no allocation,
+ *   no synchronisation. Calls on one handle must not run concurrently (shared
+ *   workspace). Errors: INVALID_ARG, CUDA.
+ * The others as their ds4moe_dense_* namesakes. */
+typedef struct ds4moe_adapters ds4moe_adapters;
+ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slots, int32_t max_rank, int32_t dtype,
+                                     int32_t max_tokens, ds4moe_adapters **out);
+ds4moe_status ds4moe_adapters_set(ds4moe_adapters *h, int32_t slot, int32_t rank, const void *a, const void *b,
+                                  float scale, void *stream);
+ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t x_stride, int32_t x_dtype,
+                                      const int32_t *slots, int32_t n_tok, const float *base, int64_t base_stride,
+                                      float *y, int64_t y_stride, void *stream);
+ds4moe_status ds4moe_adapters_get_device_error(ds4moe_adapters *h, void *stream, uint32_t *flags_out);
+void ds4moe_adapters_destroy(ds4moe_adapters *h);
+uint64_t ds4moe_adapters_device_bytes(const ds4moe_adapters *h);
+uint64_t ds4moe_adapters_launch_count(const ds4moe_adapters *h);
+
+/* ---------------------------------------------------------------------------
  * Attention beside the MoE: a paged key-value cache, its append, and the
  * attention that reads it. Forward only.
  * Passages: "DeepSeek V4 Flash -- DFlash Integration", Model Architecture (64
@@ -391,8 +442,6 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  * [0, n_tok]: each entry is clamped to that and raised to the largest before
  * it, so that sequences never share a row; a row appended at a position
  * outside the table is dropped). */
-typedef enum { DS4MOE_DT_F32 = 0, DS4MOE_DT_BF16 = 1, DS4MOE_DT_F16 = 2 } ds4moe_dtype;
-
 #define DS4MOE_ATTN_MAX_NEW 16 /* new tokens per sequence of a decode call */
 
 typedef struct {
