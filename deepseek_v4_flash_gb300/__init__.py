@@ -132,6 +132,9 @@ def lib():
             "ds4moe_kv_append_rope": (i32, [vp, ctypes.POINTER(_KvCache), ctypes.POINTER(_Rope), vp, i64, vp, i64, vp,
                                             i64, vp, i64, i32, vp, vp, i32, i32, vp]),
             "ds4moe_attn_decode": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i32, i32, vp, i64, vp]),
+            "ds4moe_attn_reserve_shared": (i32, [vp, i32]),
+            "ds4moe_attn_decode_shared": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, vp, vp, i32, i32, i32, vp,
+                                                i64, vp]),
             "ds4moe_attn_prefill": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, vp, i32, i32, vp, i64, vp]),
             "ds4moe_attn_get_device_error": (i32, [vp, vp, ctypes.POINTER(u32)]),
             "ds4moe_attn_device_bytes": (ctypes.c_uint64, [vp]),
@@ -516,7 +519,8 @@ class Adapters:
 @dataclass
 class AttentionDesc:
     """Shape of the attention beside the MoE (ds4moe_attn_desc). `scale` None:
-    1 / sqrt(head_dim)."""
+    1 / sqrt(head_dim). `max_shared_tokens`: largest n_seq * n_new of decode calls
+    with shared positions (ds4moe_attn_reserve_shared)."""
     n_heads: int
     n_kv_heads: int
     head_dim: int
@@ -526,6 +530,7 @@ class AttentionDesc:
     scale: float | None = None
     max_seqs: int = 1
     max_tokens: int = 1
+    max_shared_tokens: int = 0
 
     def c(self) -> _AttnDesc:
         scale = self.scale if self.scale is not None else max(self.head_dim, 1) ** -0.5
@@ -583,6 +588,8 @@ class Attention:
         h = ctypes.c_void_p()
         _check(lib().ds4moe_attn_create(ctypes.byref(desc.c()), ctypes.byref(h)), "ds4moe_attn_create")
         self.desc, self._h = desc, h
+        if desc.max_shared_tokens:
+            _check(_lib.ds4moe_attn_reserve_shared(h, desc.max_shared_tokens), "ds4moe_attn_reserve_shared")
         self._dt, self._code = _torch_dtype(DTYPE[desc.dtype]), DTYPE[desc.dtype]
         self._q_row, self._q_len = (desc.n_heads, desc.head_dim), desc.n_heads * desc.head_dim
         self._kv_row, self._kv_len = (desc.n_kv_heads, desc.head_dim), desc.n_kv_heads * desc.head_dim
@@ -666,18 +673,33 @@ class Attention:
             raise ValueError("out: the shape of q")
         return out, _rows(out, "out", self._dt, self._q_row, self._q_len)
 
-    def decode(self, cache, q, kv_len, out=None, stream=None):
+    def decode(self, cache, q, kv_len, out=None, stream=None, shared_len=None, group_start=None):
         """Attention of the last n_new tokens of every sequence
-        (ds4moe_attn_decode): q [n_seq, n_new, n_heads, head_dim]; returns out."""
+        (ds4moe_attn_decode): q [n_seq, n_new, n_heads, head_dim]; returns out.
+
+        With `shared_len` (int32 [n_groups]) the sequences of a group have that
+        many first positions in common, which are read once for all of them
+        (ds4moe_attn_decode_shared). `group_start` int32 [n_groups + 1] holds the
+        groups' first sequences; None: one group of all."""
         import torch
         if q.dim() != 4:
             raise ValueError("q: [n_seq, n_new, n_heads, head_dim]")
         n_seq, n_new = q.shape[:2]
         qs = _rows(q, "q", self._dt, self._q_row, self._q_len)
         out, os_ = self._out(q, out, stream)
-        _check(_lib.ds4moe_attn_decode(self._h, self._cache(cache, n_seq), q.data_ptr(), qs,
-                                       _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_new, out.data_ptr(), os_,
-                                       _stream(stream)), "ds4moe_attn_decode")
+        if shared_len is None:
+            if group_start is not None:
+                raise ValueError("group_start: only with shared_len")
+            _check(_lib.ds4moe_attn_decode(self._h, self._cache(cache, n_seq), q.data_ptr(), qs,
+                                           _vec(kv_len, "kv_len", torch.int32, n_seq), n_seq, n_new, out.data_ptr(), os_,
+                                           _stream(stream)), "ds4moe_attn_decode")
+            return out
+        n_groups = shared_len.numel()
+        _check(_lib.ds4moe_attn_decode_shared(
+            self._h, self._cache(cache, n_seq), q.data_ptr(), qs, _vec(kv_len, "kv_len", torch.int32, n_seq),
+            _vec(shared_len, "shared_len", torch.int32, n_groups),
+            None if group_start is None else _vec(group_start, "group_start", torch.int32, n_groups + 1), n_groups, n_seq,
+            n_new, out.data_ptr(), os_, _stream(stream)), "ds4moe_attn_decode_shared")
         return out
 
     def prefill(self, cache, q, cu_q, kv_len, out=None, stream=None):

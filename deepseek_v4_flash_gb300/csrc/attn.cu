@@ -389,7 +389,8 @@ bool overlap(const void *p, long long n, const void *q, long long m) {
 
 ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
                         const int32_t *cu_q, bool ragged, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
-                        int32_t n_new, void *out, int64_t out_stride, void *stream) {
+                        int32_t n_new, void *out, int64_t out_stride, void *stream, const int32_t *shared_len = nullptr,
+                        const int32_t *group_start = nullptr, int32_t n_groups = 0) {
   const ds4moe_attn_desc &d = h->d;
   AttnArgs a = {};
   if (!view_of(h, cache, a.kv)) return DS4MOE_ERR_INVALID_ARG;
@@ -405,14 +406,33 @@ ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void
   a.window = d.window, a.n_sink = d.window ? d.n_sink : 0;
   a.scale_log2 = d.scale * 1.44269504088896340736f;  // log2(e)
   a.err = h->err;
+  const bool rows16 = !ragged && n_new * a.group <= AD_MAX_ROWS && d.head_dim <= 128;
+  if (shared_len) {
+    if (!at_dev_ptr(shared_len) || (group_start && !at_dev_ptr(group_start))) return DS4MOE_ERR_INVALID_ARG;
+    // With a window a row sees few of the shared positions, or none: the plain call.
+    if (d.window == 0 && n_seq > 1) {
+      a.shared_len = shared_len, a.batch = n_seq, a.pre = h->shared.pre, a.pre_log = h->shared.pre_log;
+      int launches = 0;
+      cudaError_t e = launch_attn_prefix(a, group_start, n_groups, d.head_dim, d.dtype, h->tile, h->shared, h->n_sm, &launches,
+                                         (cudaStream_t)stream);
+      if (e == cudaSuccess && rows16) {
+        e = launch_attn_decode(a, d.head_dim, d.dtype, true, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
+        launches++;
+      } else if (e == cudaSuccess) {
+        e = launch_attn_own(a, d.head_dim, d.dtype, h->tile, h->n_sm, &launches, (cudaStream_t)stream);
+      }
+      h->launches += launches;
+      return at_status(e);
+    }
+  }
   // Few rows of a short head: the streaming kernel (a unit's 16-row product
   // there costs what a quarter of a 128-row tile does here, and needs no
   // tensor memory, descriptors or second launch). All else: tiles of 128 rows.
   // Both at dimension 128, one key-value head, streaming against tiles, us: 4
   // rows, 1 sequence of 8192 14 and 25, 24 of them 35 and 39; 16 rows 18 and 25,
   // 39 and 39. 20 rows (two products of 16 in the streaming kernel): tiles, 25 and 39.
-  if (!ragged && n_new * a.group <= AD_MAX_ROWS && d.head_dim <= 128) {
-    const cudaError_t e = launch_attn_decode(a, d.head_dim, d.dtype, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
+  if (rows16) {
+    const cudaError_t e = launch_attn_decode(a, d.head_dim, d.dtype, false, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
     h->launches++;
     return at_status(e);
   }
@@ -488,7 +508,35 @@ void ds4moe_attn_destroy(ds4moe_attn *h) {
   if (!h) return;
   cudaDeviceSynchronize();
   cudaFree(h->mem);
+  if (h->shared_mem) cudaFree(h->shared_mem);
   delete h;
+}
+
+ds4moe_status ds4moe_attn_reserve_shared(ds4moe_attn *h, int32_t max_tokens) {
+  if (!h || max_tokens < 0 || max_tokens > h->d.max_tokens) return DS4MOE_ERR_INVALID_ARG;
+  if (max_tokens <= h->shared_tokens) return DS4MOE_OK;
+  const size_t rows = (size_t)max_tokens * h->d.n_heads;
+  size_t at = 0;
+  auto place = [&](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return p;
+  };
+  const size_t o_start = place((size_t)h->d.max_seqs * 4), o_plen = place((size_t)h->d.max_seqs * 4);
+  const size_t o_ptab = place((size_t)h->d.max_seqs * 4), o_log = place(rows * 4), o_pre = place(rows * h->d.head_dim * 4);
+  uint8_t *mem = nullptr;
+  cudaError_t e = attn_shared_set_attributes(h->d.dtype, h->d.head_dim);
+  if (e == cudaSuccess) e = cudaMalloc((void **)&mem, at);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();  // calls that use the old one
+  if (e != cudaSuccess) {
+    if (mem) cudaFree(mem);
+    return at_status(e);
+  }
+  if (h->shared_mem) cudaFree(h->shared_mem);
+  h->shared_mem = mem, h->shared_tokens = max_tokens, h->shared_bytes = at;
+  h->shared.start = (int32_t *)(mem + o_start), h->shared.plen = (int32_t *)(mem + o_plen), h->shared.ptab = (int32_t *)(mem + o_ptab);
+  h->shared.pre = (float *)(mem + o_pre), h->shared.pre_log = (float *)(mem + o_log);
+  return DS4MOE_OK;
 }
 
 ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *k_new, int64_t k_stride,
@@ -605,6 +653,21 @@ ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, c
   return attn_call(h, cache, q, q_stride, nullptr, false, kv_len, n_seq, n_seq * n_new, n_new, out, out_stride, stream);
 }
 
+ds4moe_status ds4moe_attn_decode_shared(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                                        const int32_t *kv_len, const int32_t *shared_len, const int32_t *group_start,
+                                        int32_t n_groups, int32_t n_seq, int32_t n_new, void *out, int64_t out_stride,
+                                        void *stream) {
+  if (!h || n_seq < 0 || n_seq > h->d.max_seqs || n_new < 1 || n_new > DS4MOE_ATTN_MAX_NEW ||
+      (long long)n_seq * n_new > h->d.max_tokens)
+    return DS4MOE_ERR_INVALID_ARG;
+  if (n_groups < 1 || (n_seq > 0 && n_groups > n_seq) || (!group_start && n_groups != 1)) return DS4MOE_ERR_INVALID_ARG;
+  if (n_seq * n_new > h->shared_tokens) return DS4MOE_ERR_INVALID_ARG;
+  if (n_seq == 0) return DS4MOE_OK;
+  if (!shared_len) return DS4MOE_ERR_INVALID_ARG;
+  return attn_call(h, cache, q, q_stride, nullptr, false, kv_len, n_seq, n_seq * n_new, n_new, out, out_stride, stream,
+                   shared_len, group_start, n_groups);
+}
+
 ds4moe_status ds4moe_attn_prefill(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
                                   const int32_t *cu_q, const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *out,
                                   int64_t out_stride, void *stream) {
@@ -624,7 +687,7 @@ ds4moe_status ds4moe_attn_get_device_error(ds4moe_attn *h, void *stream, uint32_
   return f ? DS4MOE_ERR_DEVICE : DS4MOE_OK;
 }
 
-uint64_t ds4moe_attn_device_bytes(const ds4moe_attn *h) { return h ? h->bytes : 0; }
+uint64_t ds4moe_attn_device_bytes(const ds4moe_attn *h) { return h ? h->bytes + h->shared_bytes : 0; }
 uint64_t ds4moe_attn_launch_count(const ds4moe_attn *h) { return h ? h->launches : 0; }
 
 }  // extern "C"

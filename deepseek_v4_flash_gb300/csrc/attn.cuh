@@ -103,6 +103,66 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs &a, int b, bool &bad)
   return s;
 }
 
+// ---- a batch with shared positions
+
+// Whether a group's shared positions are read once for all: with fewer, or for a
+// single sequence, the second part reads them just as fast.
+__device__ __forceinline__ bool shared_worth(int s, int seqs) { return seqs >= 2 && s >= 128; }
+
+// Shared positions of group g, within what the table holds.
+__device__ __forceinline__ int shared_of(const AttnArgs &a, int g, bool &bad) {
+  const int l = a.shared_len[g], s = min(max(l, 0), a.kv.width * a.kv.page_size);
+  bad |= s != l;
+  return s;
+}
+
+// Where sequence b's own positions begin. It shares the group's positions when
+// its first new token sees all of them.
+__device__ __forceinline__ int own_start(const AttnArgs &a, int b, int len) {
+  if (a.start) return a.start[b];
+  bool bad = false;
+  const int s = shared_of(a, 0, bad);
+  return shared_worth(s, a.batch) && len - a.n_new + 1 >= s ? s : 0;
+}
+
+// The rows of group g, no rows where nothing is read once; its positions; the
+// table's row through which they are read.
+__device__ __forceinline__ SeqInfo prefix_info(const AttnArgs &a, int g, int *tab) {
+  SeqInfo i = {0, 0, 0};
+  if (a.start) {
+    i.tok0 = a.cu_q[g], i.len = a.plen[g];
+    if (i.len > 0) i.n = a.cu_q[g + 1] - i.tok0;
+    if (tab) *tab = a.ptab[g];
+    return i;
+  }
+  bool bad = false;
+  const int s = shared_of(a, 0, bad);
+  if (bad && blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
+  if (!shared_worth(s, a.batch)) return i;
+  for (int b = 0; b < a.batch; b++) {  // (the first, unless a place in the batch is empty)
+    if (seq_len(a, b, bad) - a.n_new + 1 < s) continue;
+    if (tab) *tab = b;
+    i.n = a.batch * a.n_new, i.len = s;
+    break;
+  }
+  return i;
+}
+
+// log2 of a sum of weights l relative to 2^m.
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : m + __log2f(l); }
+
+// Joins a result with log2 sum `lp` and an accumulator relative to 2^m with sum
+// l: the factors of the two. Both 0: no score above -infinity.
+__device__ __forceinline__ void join_two(float lp, float m, float l, float &from, float &inv) {
+  if (l == 0.0f) {
+    from = lp == -INFINITY ? 0.0f : lp == lp ? 1.0f : lp, inv = 0.0f;
+    return;
+  }
+  const float top = fmaxf(lp, log_sum(m, l));
+  const float p = lp == -INFINITY ? 0.0f : ex2(lp - top), o = ex2(m - top), z = 1.0f / fmaf(o, l, p);
+  from = p * z, inv = o * z;
+}
+
 // First position of the window of the query at position i >= 0, and the
 // number of first positions visible before it.
 __device__ __forceinline__ int window_lo(const AttnArgs &a, int i) {

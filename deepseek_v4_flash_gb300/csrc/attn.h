@@ -37,6 +37,14 @@ struct AttnArgs {
   // of a group's positions; which of its blocks have marked rows
   int32_t span, gsh;
   int *marked;
+  // A batch with shared positions (attn_shared.cu): their number for each group,
+  // then, from its planning launch or null (one group of all sequences), what of
+  // it is read once, by which table row, and where each sequence's own positions
+  // begin; sequences of the call; the results over the shared positions,
+  // [n_tok][n_heads][head_dim], and log2 of their sums of weights.
+  const int32_t *shared_len, *plen, *ptab, *start;
+  int32_t batch;
+  float *pre, *pre_log;
   uint32_t *err;
 };
 
@@ -52,6 +60,13 @@ struct TileWork {
   int pairs;         // pairs of blocks that run at once
 };
 
+// Workspace of calls with shared positions (ds4moe_attn_reserve_shared).
+struct SharedWork {
+  int32_t *start;         // [max_seqs]
+  int32_t *plen, *ptab;   // [max_seqs] by group
+  float *pre, *pre_log;
+};
+
 }  // namespace ds4
 
 struct ds4moe_attn {
@@ -62,7 +77,10 @@ struct ds4moe_attn {
   float *part;       // partial results of the blocks that share a (sequence, head)
   int *ticket;       // arrivals of those blocks, by the first of them (self-resetting)
   ds4::TileWork tile;  // the tile kernel's share (its partials are `part`)
-  uint64_t bytes, launches;
+  uint8_t *shared_mem;      // one allocation, or null
+  int shared_tokens;        // rows that it serves
+  ds4::SharedWork shared;
+  uint64_t bytes, shared_bytes, launches;
 };
 
 namespace ds4 {
@@ -71,7 +89,7 @@ namespace ds4 {
 constexpr int AD_MAX_ROWS = 16;
 size_t attn_decode_part_floats(int n_sm);
 cudaError_t attn_decode_set_attributes();
-cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
+cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, bool shared, float *part, int *ticket, int n_sm,
                                cudaStream_t s);
 // attn_tile.cu: tiles of 128 rows on the tensor cores, every shape.
 size_t attn_tile_part_floats(int head_dim, int n_sm);
@@ -80,4 +98,11 @@ cudaError_t attn_tile_set_attributes(int dtype, int head_dim);
 int attn_tile_pairs(int dtype, int head_dim);
 cudaError_t launch_attn_tile(const AttnArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
                              cudaStream_t s);
+// attn_shared.cu: the shared positions of every group, planning launch first
+// where it needs one (which it notes in `a`), then every sequence's own ones.
+cudaError_t attn_shared_set_attributes(int dtype, int head_dim);
+cudaError_t launch_attn_prefix(AttnArgs &a, const int32_t *group_start, int n_groups, int head_dim, int dtype,
+                               const TileWork &w, const SharedWork &sw, int n_sm, int *launches, cudaStream_t s);
+cudaError_t launch_attn_own(const AttnArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
+                            cudaStream_t s);
 }  // namespace ds4

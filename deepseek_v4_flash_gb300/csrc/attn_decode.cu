@@ -73,15 +73,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // A sequence's part in a decode call.
 struct DecSeq {
   int first, last, len;  // positions of its first and last new token
+  int own;               // SHARED: where its own positions begin
   Groups gr;
   int units;             // at least one, so that every row is written
 };
+template <bool SHARED>
 __device__ __forceinline__ DecSeq dec_seq(const AttnArgs &a, int b, bool &bad) {
   DecSeq s;
   const SeqInfo si = seq_info(a, b, bad);
   s.len = si.len, s.first = si.len - si.n, s.last = si.len - 1;
   s.gr = Groups{0, 0, 0};
   if (s.last >= 0) s.gr = groups_of(a, max(s.first, 0), s.last);
+  s.own = 0;
+  if (SHARED) {
+    s.own = own_start(a, b, si.len);
+    s.gr.win0 = s.own >> 4, s.gr.n = s.last < s.own ? 0 : s.gr.n - s.gr.win0;  // (no window)
+  }
   s.units = max(1, (s.gr.n + AD_UNIT - 1) / AD_UNIT);
   return s;
 }
@@ -91,20 +98,22 @@ struct DecCursor {
   DecSeq s;
   int b, kvh, lu;  // sequence, key-value head, unit of that pair
 };
+template <bool SHARED>
 __device__ __forceinline__ void dec_next(const AttnArgs &a, DecCursor &c) {
   if (++c.lu < c.s.units) return;
   c.lu = 0;
   if (++c.kvh < a.n_kv) return;
   c.kvh = 0;
   bool bad = false;
-  if (++c.b < a.n_seq) c.s = dec_seq(a, c.b, bad);
+  if (++c.b < a.n_seq) c.s = dec_seq<SHARED>(a, c.b, bad);
 }
 
 // A sequence's units by lane (sequences b0 .. b0 + 31), inclusive prefix and
 // the warp's sum.
+template <bool SHARED>
 __device__ __forceinline__ long long dec_prefix(const AttnArgs &a, int b0, bool &bad, long long &incl, long long &sum) {
   const int lane = threadIdx.x & 31;
-  const long long n = b0 + lane < a.n_seq ? (long long)dec_seq(a, b0 + lane, bad).units * a.n_kv : 0;
+  const long long n = b0 + lane < a.n_seq ? (long long)dec_seq<SHARED>(a, b0 + lane, bad).units * a.n_kv : 0;
   incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -116,15 +125,16 @@ __device__ __forceinline__ long long dec_prefix(const AttnArgs &a, int b0, bool 
 }
 // The block's run of units [u0, u1) out of U, dealt to N blocks, and the
 // cursor at u0 (whole warp). False when there is nothing for this block.
+template <bool SHARED>
 __device__ __forceinline__ bool dec_start(const AttnArgs &a, int n_cta, long long &U, long long &N, long long &u0,
                                         long long &u1, DecCursor &c) {
   long long incl, sum, n;
   bool bad = false;
-  n = dec_prefix(a, 0, bad, incl, sum);  // up to 32 sequences: the only pass
+  n = dec_prefix<SHARED>(a, 0, bad, incl, sum);  // up to 32 sequences: the only pass
   U = sum;
   for (int b0 = 32; b0 < a.n_seq; b0 += 32) {
     long long i, s;
-    dec_prefix(a, b0, bad, i, s);
+    dec_prefix<SHARED>(a, b0, bad, i, s);
     U += s;
   }
   if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
@@ -134,13 +144,13 @@ __device__ __forceinline__ bool dec_start(const AttnArgs &a, int n_cta, long lon
   u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
   long long u = u0;
   for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-    if (b0) n = dec_prefix(a, b0, bad, incl, sum);
+    if (b0) n = dec_prefix<SHARED>(a, b0, bad, incl, sum);
     const unsigned hit = __ballot_sync(0xffffffffu, u < incl);
     if (hit) {
       const int l = __ffs(hit) - 1;
       const long long rem = u - __shfl_sync(0xffffffffu, incl - n, l);
       c.b = b0 + l;
-      c.s = dec_seq(a, c.b, bad);
+      c.s = dec_seq<SHARED>(a, c.b, bad);
       c.kvh = (int)(rem / c.s.units), c.lu = (int)(rem - (long long)c.kvh * c.s.units);
       break;
     }
@@ -165,7 +175,9 @@ __device__ __noinline__ void redo_row(const AttnArgs &a, int t, int h, int b, in
     o[(threadIdx.x & 31) + 32 * c] = l == 0.0f ? 0u : Half16<DT>::down(acc[c].x * inv, acc[c].y * inv);
 }
 
-template <int DT, int D>
+// SHARED: the positions before each sequence's own ones are in a.pre, whose
+// result joins the row's as it is stored (attn_shared.cu).
+template <int DT, int D, bool SHARED>
 __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs a, float *part, int *ticket, int n_cta) {
   constexpr int STAGE = 64 * D;  // a warp's 16 keys and 16 values; also 16 rows of O in 32 bits
   constexpr int NST = AD_RING / (AD_WARPS * STAGE);
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
 
   long long U, N, u0, u1;
   DecCursor lc, cc;  // where loading and computing stand
-  if (!dec_start(a, n_cta, U, N, u0, u1, lc)) return;
+  if (!dec_start<SHARED>(a, n_cta, U, N, u0, u1, lc)) return;
   cc = lc;
 
   // one unit's 16 positions of this warp into ring slot `slot`
@@ -205,7 +217,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       if (page < 0) bad_page = true;
       // rows some query row sees: within the length, in the first query's
       // window or after it, or among the first positions
-      const int lo = window_lo(a, max(lc.s.first, 0)), sink = min(a.n_sink, window_lo(a, lc.s.last));
+      const int lo = SHARED ? lc.s.own : window_lo(a, max(lc.s.first, 0)), sink = min(a.n_sink, window_lo(a, lc.s.last));
       // this lane's piece of the row (lane / CH), and of every (32 / CH)-th after it
       constexpr int STEP = 32 / CH;
       const int r0 = lane / CH, c = lane % CH;
@@ -241,7 +253,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
   for (int i = 0; i < NST - 1; i++) {
     if (i < n_it) {
       load(i);
-      dec_next(a, lc);
+      dec_next<SHARED>(a, lc);
       look();
     } else {
       cp_commit();
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
     // the next unit into the slot that the last iteration emptied
     if (it + NST - 1 < n_it) {
       load((it + NST - 1) % NST);
-      dec_next(a, lc);
+      dec_next<SHARED>(a, lc);
       look();
     } else {
       cp_commit();
@@ -310,8 +322,8 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
 #pragma unroll
         for (int i = 0; i < 4; i++) s[n][i] = (s[n][i] + s2[n][i]) * a.scale_log2;
       // some position not seen by some row (rows past the last take any mask)
-      if (p0 + 15 > cc.s.first || (a.window > 0 && p0 < window_lo(a, max(cc.s.last, 0)) && p0 + 15 >= min(a.n_sink, window_lo(a, max(cc.s.first, 0))))) {
-        const int la = window_lo(a, max(pa, 0)), lb = window_lo(a, max(pb, 0));
+      if (p0 + 15 > cc.s.first || (SHARED && p0 < cc.s.own) || (a.window > 0 && p0 < window_lo(a, max(cc.s.last, 0)) && p0 + 15 >= min(a.n_sink, window_lo(a, max(cc.s.first, 0))))) {
+        const int la = SHARED ? cc.s.own : window_lo(a, max(pa, 0)), lb = SHARED ? cc.s.own : window_lo(a, max(pb, 0));
 #pragma unroll
         for (int n = 0; n < 2; n++)
 #pragma unroll
@@ -397,12 +409,18 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       const int slot = 2 * blockIdx.x + (item0 < u0 ? 0 : 1);
       float *pp = part + (size_t)slot * (16 * (D + 2));
       const int nan_rows_possible = a.n_new > 1;
-      auto store = [&](int r, int c, float4 x, float l) {
+      auto store = [&](int r, int c, float4 x, float m, float l) {
         const int t = cc.b * a.n_new + r / a.group, h = cc.kvh * a.group + r % a.group;
-        const float inv = 1.0f / l;
+        float inv = 1.0f / l, from = 0.0f;
+        const long long pre = (long long)t * a.n_heads + h;
+        if (SHARED) join_two(cc.s.own > 0 ? a.pre_log[pre] : -INFINITY, m, l, from, inv);
         x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
         // no score above -infinity (whatever the values: 0 x NaN is NaN)
         if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (SHARED && from != 0.0f) {
+          const float4 p = *reinterpret_cast<const float4 *>(a.pre + pre * D + c);
+          x.x = fmaf(from, p.x, x.x), x.y = fmaf(from, p.y, x.y), x.z = fmaf(from, p.z, x.z), x.w = fmaf(from, p.w, x.w);
+        }
         const uint2 u = make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
         *reinterpret_cast<uint2 *>(a.out + (long long)t * a.out_stride + (long long)h * D + c) = u;
         if (nan_rows_possible && l == l) {
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
                                                              4 * (r * D + (c ^ ((r & 7) << 3))));
           x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
         }
-        if (whole) store(r, c, x, s_lt[r]);
+        if (whole) store(r, c, x, s_mt[r], s_lt[r]);
         else *reinterpret_cast<float4 *>(pp + r * D + c) = x;
       }
       bool done = whole;
@@ -458,7 +476,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
             }
 #pragma unroll
             for (int k = 16; k; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
-            if (lane == 0) s_lt[r] = lt;
+            if (lane == 0) s_lt[r] = lt, s_mt[r] = mt;
           }
           __syncthreads();
           for (int i = tid; i < rows * (D / 4); i += AD_WARPS * 32) {
@@ -470,7 +488,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
               const float f = s_f[p][r];
               x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
             }
-            store(r, c, x, s_lt[r]);
+            store(r, c, x, s_mt[r], s_lt[r]);
           }
         }
       }
@@ -481,39 +499,41 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
           if ((s_nan >> r & 1) &&
               unseen_nonfinite<DT>(a, cc.b, cc.kvh, pos, pos, window_lo(a, max(cc.s.first, 0)), 0, cc.s.last + 1, 0, D) &&
               !own_nan<DT>(a, a.out + (long long)t * a.out_stride + (long long)h * D, cc.b, cc.kvh, pos, 0, D))
-            redo_row<DT, D>(a, t, h, cc.b, pos, cc.s.gr);
+            redo_row<DT, D>(a, t, h, cc.b, pos, SHARED ? groups_of(a, max(pos, 0), max(pos, 0)) : cc.s.gr);
         }
         __syncthreads();
       }
       item0 = end;
       fresh = true;
     }
-    dec_next(a, cc);
+    dec_next<SHARED>(a, cc);
   }
   if (bad_page) raise_flag(a.err, DS4MOE_DEVERR_PAGE);
 }
 
 template <int DT>
-static const void *dec_fn(int D) {
-  return D == 64 ? (const void *)k_attn_decode<DT, 64> : (const void *)k_attn_decode<DT, 128>;
+static const void *dec_fn(int D, bool shared) {
+  if (shared) return D == 64 ? (const void *)k_attn_decode<DT, 64, true> : (const void *)k_attn_decode<DT, 128, true>;
+  return D == 64 ? (const void *)k_attn_decode<DT, 64, false> : (const void *)k_attn_decode<DT, 128, false>;
 }
 
 size_t attn_decode_part_floats(int n_sm) { return (size_t)2 * n_sm * 16 * (128 + 2); }
 
 cudaError_t attn_decode_set_attributes() {
-  for (const void *fn : {dec_fn<DS4MOE_DT_BF16>(64), dec_fn<DS4MOE_DT_BF16>(128), dec_fn<DS4MOE_DT_F16>(64),
-                         dec_fn<DS4MOE_DT_F16>(128)}) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, AD_RING);
-    if (e != cudaSuccess) return e;
-  }
+  for (bool shared : {false, true})
+    for (int D : {64, 128})
+      for (const void *fn : {dec_fn<DS4MOE_DT_BF16>(D, shared), dec_fn<DS4MOE_DT_F16>(D, shared)}) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, AD_RING);
+        if (e != cudaSuccess) return e;
+      }
   return cudaSuccess;
 }
 
-cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
+cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, bool shared, float *part, int *ticket, int n_sm,
                                cudaStream_t s) {
   if (n_sm > AD_MAX_BLOCKS) n_sm = AD_MAX_BLOCKS;
   void *args[] = {(void *)&a, &part, &ticket, &n_sm};
-  const void *fn = dtype == DS4MOE_DT_BF16 ? dec_fn<DS4MOE_DT_BF16>(head_dim) : dec_fn<DS4MOE_DT_F16>(head_dim);
+  const void *fn = dtype == DS4MOE_DT_BF16 ? dec_fn<DS4MOE_DT_BF16>(head_dim, shared) : dec_fn<DS4MOE_DT_F16>(head_dim, shared);
   return launch_pdl(fn, dim3(n_sm), dim3(AD_WARPS * 32), AD_RING, s, args, true);
 }
 

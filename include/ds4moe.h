@@ -537,6 +537,34 @@ ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, c
                                  const int32_t *kv_len, int32_t n_seq, int32_t n_new, void *out, int64_t out_stride,
                                  void *stream);
 
+/* The same, of a batch whose sequences begin with the same positions (a system
+ * prompt, a document): the same formula and results, but the shared keys and
+ * values are read once for all sequences of a group.
+ *   shared_len  [n_groups] positions that the group's sequences have in common:
+ *           all their tables lead to the same keys and values there (the same
+ *           pages, or copies: shared_len may lie inside a page). They are read
+ *           through the table of the first sequence that shares. A sequence whose
+ *           first new token does not see all of them (kv_len - n_new + 1 <
+ *           shared_len) shares nothing. 0: nothing is shared.
+ *   group_start [n_groups + 1] ascending: group g is sequences group_start[g] ..
+ *           group_start[g+1] - 1; a sequence of no group shares nothing. NULL:
+ *           one group of all (n_groups = 1).
+ * n_groups 1..n_seq. Both are read on the device as kv_len is; DS4MOE_DEVERR_LENGTH
+ * for shared_len outside the table (clamped) and bounds out of order (as cu_q).
+ * Few shared positions, single sequences, and handles with a window, which see
+ * little of what is shared, take the plain path: the argument never changes a
+ * result but by its roundings.
+ * ds4moe_attn_reserve_shared: workspace for such calls of up to max_tokens
+ * (n_seq * n_new) rows, at most the handle's: max_tokens * n_heads * (head_dim +
+ * 1) * 4 bytes. Allocates, synchronises; a smaller number than before changes
+ * nothing. Calls captured before it must not be replayed after it. Errors:
+ * INVALID_ARG, OOM, CUDA. A call of more rows than reserved: INVALID_ARG. */
+ds4moe_status ds4moe_attn_reserve_shared(ds4moe_attn *h, int32_t max_tokens);
+ds4moe_status ds4moe_attn_decode_shared(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
+                                        const int32_t *kv_len, const int32_t *shared_len, const int32_t *group_start,
+                                        int32_t n_groups, int32_t n_seq, int32_t n_new, void *out, int64_t out_stride,
+                                        void *stream);
+
 /* Attention of ragged runs of new tokens: sequence b has rows cu_q[b] ..
  * cu_q[b+1] - 1 (none is allowed), the last of them at position
  * kv_len[b] - 1. Rows of no sequence are left as they are. */

@@ -40,3 +40,8 @@ def test_rope_wants_device_memory():
     for bad in (torch.ones(8), torch.ones(8, dtype=torch.float64), [1.0] * 8):
         with pytest.raises(ValueError):
             ds4.Rope(bad)
+
+
+def test_shared_attention_null_arguments(L):
+    assert L.ds4moe_attn_reserve_shared(None, 1) == 1
+    assert L.ds4moe_attn_decode_shared(None, None, None, 0, None, None, None, 1, 1, 1, None, 0, None) == 1
