@@ -298,13 +298,30 @@ __device__ __forceinline__ void put_wide(uint32_t at, int r, int p, const uint4 
   sts4(at + sw128(r, 2 * p), lo), sts4(at + sw128(r, 2 * p + 1), hi);
 }
 
+// Accumulators of a block of k_adapt_shrink. The tensor cores add a product to
+// an accumulator with the sum cut, not rounded, to 24 bits, so a long chain of
+// additions drifts: 256 of them (1024 columns) were off by 4e-6 of the result,
+// five times what 32-bit sums are. So chunks go round several accumulators, the
+// small low parts of x to one of their own, added up in 32 bits at the end.
+// Tensor memory: half of an SM's for ranks up to 64, where two blocks share it,
+// else all of it.
+__host__ __device__ constexpr int shrink_accs(int r32) {
+  const int n = (r32 <= 64 ? 256 : 512) / r32;
+  return n < 4 ? n : 4;
+}
+__host__ __device__ constexpr int shrink_cols(int r32) { return r32 <= 32 ? 128 : r32 <= 64 ? 256 : 512; }
+
 constexpr int LR_HALF = 128 * 128;  // 128 rows of 32 tf32 numbers
 
 // Bytes of a stage of k_adapt_shrink: hi (and lo) of x, r32 rows of A.
 __host__ __device__ constexpr int shrink_stage(bool f32, int r32) { return LR_HALF * (f32 ? 2 : 1) + r32 * 128; }
+// At least as large a part of an SM's shared memory as of its tensor memory:
+// blocks of clusters that wait for one another must never wait for tensor
+// memory that another cluster's blocks hold.
 __host__ __device__ constexpr int shrink_smem(bool f32, int r32) {
   const int ring = 2 * shrink_stage(f32, r32), sums = 128 * (r32 + 4) * 4;
-  return (ring > sums ? ring : sums) + 1024;
+  const int need = (ring > sums ? ring : sums) + 1024, least = (shrink_cols(r32) == 512 ? 225 : 104) * 1024;
+  return need > least ? need : least;
 }
 
 // V = scale A x of one tile per cluster at a time. Block k of the cluster takes
@@ -320,8 +337,9 @@ __global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int 
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int stage_bytes = shrink_stage(F32, a.R32);
   const uint32_t bar0 = smem_u32(s_bar);
-  uint32_t cols = 32;
-  while ((int)cols < a.R32) cols <<= 1;
+  const uint32_t cols = shrink_cols(a.R32);
+  // accumulators of the high parts; the low parts' one comes after them
+  const int n_acc = shrink_accs(a.R32) - (F32 ? 1 : 0);
   if (w == 0) {
     if (lane == 0) {
       mbar_init(bar0, 1), mbar_init(bar0 + 8, 1);
@@ -390,14 +408,15 @@ __global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int 
         const int us = __shfl_sync(0xffffffffu, st, 0);
         const uint32_t sa = base + us * stage_bytes;
         const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + LR_HALF * (F32 ? 2 : 1), 0);
-        const uint32_t more = __shfl_sync(0xffffffffu, c, 0) != 0;
+        const int uc = __shfl_sync(0xffffffffu, c, 0);
+        const uint32_t acc = tmem + uc % n_acc * a.R32, low = tmem + n_acc * a.R32;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) umma_tf32(tmem, dh + 2 * q, dw + 2 * q, id, more || q != 0);
+          for (int q = 0; q < 4; q++) umma_tf32(acc, dh + 2 * q, dw + 2 * q, id, uc >= n_acc || q != 0);
           if (F32) {
 #pragma unroll
-            for (int q = 0; q < 4; q++) umma_tf32(tmem, dl + 2 * q, dw + 2 * q, id, 1);
+            for (int q = 0; q < 4; q++) umma_tf32(low, dl + 2 * q, dw + 2 * q, id, uc != 0 || q != 0);
           }
           umma_commit(bar0 + 8 * us);
         }
@@ -421,12 +440,16 @@ __global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int 
     for (int c = (w >> 2) * 32; c < r32; c += 64) {
       float v[32];
       const int row = (w & 3) * 32 + lane;
-      if (nc) {
-        tmem_ld32(tmem + ((uint32_t)((w & 3) * 32) << 16) + c, v);
-        tmem_wait_ld(v);
-      } else {
 #pragma unroll
-        for (int e = 0; e < 32; e++) v[e] = 0.0f;
+      for (int e = 0; e < 32; e++) v[e] = 0.0f;
+      for (int i = 0; i < n_acc + (F32 ? 1 : 0); i++) {
+        if (i >= nc && i < n_acc) continue;  // not written
+        if (nc == 0) break;
+        float z[32];
+        tmem_ld32(tmem + ((uint32_t)((w & 3) * 32) << 16) + i * a.R32 + c, z);
+        tmem_wait_ld(z);
+#pragma unroll
+        for (int e = 0; e < 32; e++) v[e] += z[e];
       }
 #pragma unroll
       for (int e = 0; e < 32; e += 4)
@@ -715,7 +738,7 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
     const AdaptFns f = adapt_fns(dtype, f32);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f.token, cudaFuncAttributeMaxDynamicSharedMemorySize, ((1 << 16) / LR_CLUSTER + 8) * 4);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, shrink_smem(f32, LR_MAX_RANK));
+      e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f.expand, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
   }
   if (e == cudaSuccess) e = cudaMalloc((void **)&h->mem, at);
@@ -793,11 +816,9 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   void *plan[] = {&a};
   cudaError_t e = launch_pdl((const void *)k_adapt_plan, dim3(1), dim3(1024), 0, s, plan, true);
   if (e == cudaSuccess) {
-    // as many blocks of a tile as fill the SMs (two blocks each) with the least number of tiles that there can be
     int ks = LR_CLUSTER;
-    while (ks > 1 && (n_tok / 128 + 1) * ks > 2 * h->n_sm) ks >>= 1;
-    const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1;
-    int grid = std::min(2 * h->n_sm / ks, most) * ks;
+    const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1, per_sm = shrink_cols(h->R32) == 512 ? 1 : 2;
+    int grid = std::min(per_sm * h->n_sm / ks, most) * ks;
     void *args[] = {&a, &ks};
     e = launch_cluster(f.shrink, grid, ks, 256, (size_t)shrink_smem(f32, h->R32), s, args);
     if (e == cudaSuccess) {

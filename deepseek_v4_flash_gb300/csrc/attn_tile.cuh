@@ -253,10 +253,19 @@ struct Seg {
   int pos0;          // position of the first token
   int len;           // cached positions of the sequence
   int last;          // last position that any row of the list's range sees
-  int lo;            // AT_OWN: the first position that counts
   Groups gr;
   int kt0, kt1;      // empty: nothing is visible, the rows are 0; kt1 < 0: no more work
   int starts, ends;  // the run holds the item's first, last tile
+};
+
+// With AT_OWN's first position that counts.
+template <int MODE>
+struct SegOf : Seg {
+  static constexpr int lo = 0;
+};
+template <>
+struct SegOf<AT_OWN> : Seg {
+  int lo;
 };
 
 __device__ __forceinline__ int tiles_of(const Groups &g, int sh) { return ((g.n << sh) + 127) >> 7; }
@@ -328,9 +337,9 @@ struct Sched {
   }
 
   // the current item's sequence and rows; its tiles
-  __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, Seg &s) const {
+  __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, SegOf<MODE> &s) const {
     const SeqInfo si = seq(a, t, b);
-    s.b = b, s.kvh = kvh, s.len = si.len, s.lo = 0;
+    s.b = b, s.kvh = kvh, s.len = si.len;
     if (MODE == AT_PREFIX) {
       if (t.first) prefix_info(a, b, &s.b);
       else s.b = __shfl_sync(0xffffffffu, stab, b);
@@ -348,7 +357,7 @@ struct Sched {
       // every row tile of the sequence reads the same positions
       s.last = si.len - 1;
       s.gr = range_groups(a, si.len - si.n, s.last, t.gsh);
-      if (MODE == AT_OWN) s.lo = own_start(a, b, si.len), s.gr = own_groups(s.lo, s.last, t.gsh);
+      if constexpr (MODE == AT_OWN) s.lo = own_start(a, b, si.len), s.gr = own_groups(s.lo, s.last, t.gsh);
       s.row0 = si.tok0 + member_rt * t.tpt;
       s.n = min(t.tpt, si.n - member_rt * t.tpt);
       s.pos0 = si.len - si.n + member_rt * t.tpt;
@@ -500,7 +509,7 @@ struct Sched {
     }
   }
 
-  __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, Seg &s) {
+  __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, SegOf<MODE> &s) {
     if (u >= u1 || (!t.whole && u1 < item1 && u1 - item0 <= AT_ITEM)) return false;  // (the next gang's from its start)
     const int n_kt = load(a, t, member_rt, s);
     const long long e = t.whole || item1 < u1 ? item1 : u1;
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   struct Misc {
     uint64_t bars[2 * 12 + 2 * AT_SEGS + 13 + 8];
-    Seg segs[AT_SEGS];
+    SegOf<MODE> segs[AT_SEGS];
     uint32_t tmem;
     // what the two threads of a row tell each other. Two row tiles: a row's S
     // follows both threads' P, so the next value cannot overtake the last.
@@ -740,7 +749,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
   // The block's segments in order, from the scheduling warp; false after the
   // last one.
   int seg_n = 0;
-  auto next_seg = [&](Seg &s) {
+  auto next_seg = [&](SegOf<MODE> &s) {
     const int i = seg_n % AT_SEGS;
     if (!wait_warp(seg_full(i), (seg_n / AT_SEGS) & 1)) return ok = false;
     s = ms.segs[i];
@@ -758,7 +767,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     bool more = sc.init(a, t, gang, C::SPAN, bad);
     if (bad && blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
     while (ok) {
-      Seg s;
+      SegOf<MODE> s;
       s.kt1 = -1;
       if (more) more = sc.next(a, t, rt, s);
       if (!more) s.kt1 = -1;
@@ -839,7 +848,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       const int ng = min(gpt, s.gr.n - kt * gpt);
       load_tile(s, pl, &maps.v, C::VST, C::VC, AT_CHUNK, half * (C::DV / 64) + rank, PAIR ? 2 : C::VC, 0, ng);
     };
-    Seg s;
+    SegOf<MODE> s;
     while (ok && next_seg(s)) {
       if (s.kt0 >= s.kt1) continue;
       Place kp = lookup(s, s.kt0);
@@ -897,7 +906,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
     const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq = desc_sw128(q_sm, 0), dk = desc_sw128(ring, 0), dv = desc_sw128(ring, AT_CHUNK);
     int kst0 = 0, vst0 = 0;  // ring stages of the current key and value tile
-    Seg s = {};
+    SegOf<MODE> s = {};
     auto wait_stage = [&](int i) {
       if (!wait_warp(full(i % C::NST), (i / C::NST) & 1)) ok = false;
     };
@@ -1077,7 +1086,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       return true;
     };
     int items = 0;  // segments with tiles so far
-    Seg s;
+    SegOf<MODE> s;
     while (ok && next_seg(s)) {
       const bool valid = my_tok < s.n;
       const int pos = valid ? s.pos0 + (MODE == AT_PREFIX ? 0 : my_tok) : -1;
@@ -1477,7 +1486,7 @@ __global__ void __launch_bounds__(AJ_THREADS)
   const int half = PAIR ? member >> 1 & 1 : member % C::HALVES, rt = PAIR ? (member >> 2) * 2 + rank : member / C::HALVES;
   const int tile0 = PAIR && ragged<MODE>(a) ? rank * t.tpt : 0;
   Sched<MODE> sc;
-  Seg s;
+  SegOf<MODE> s;
   bool bad = false;
   bool more = sc.init(a, t, gang, C::SPAN, bad);
   while (more && sc.next(a, t, rt, s)) {
