@@ -133,6 +133,7 @@ def lib():
                                             i64, vp, i64, i32, vp, vp, i32, i32, vp]),
             "ds4moe_attn_decode": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, i32, i32, vp, i64, vp]),
             "ds4moe_attn_reserve_shared": (i32, [vp, i32]),
+            "ds4moe_attn_debug_share": (i32, [vp, i32]),
             "ds4moe_attn_decode_shared": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, vp, vp, i32, i32, i32, vp,
                                                 i64, vp]),
             "ds4moe_attn_prefill": (i32, [vp, ctypes.POINTER(_KvCache), vp, i64, vp, vp, i32, i32, vp, i64, vp]),
@@ -701,6 +702,11 @@ class Attention:
             None if group_start is None else _vec(group_start, "group_start", torch.int32, n_groups + 1), n_groups, n_seq,
             n_new, out.data_ptr(), os_, _stream(stream)), "ds4moe_attn_decode_shared")
         return out
+
+    def debug_share(self, always: bool = True):
+        """Share wherever it is possible, not only where it gains; a test hook
+        (ds4moe_attn_debug_share)."""
+        _check(_lib.ds4moe_attn_debug_share(self._h, int(bool(always))), "ds4moe_attn_debug_share")
 
     def prefill(self, cache, q, cu_q, kv_len, out=None, stream=None):
         """Attention of ragged runs of new tokens (ds4moe_attn_prefill): q

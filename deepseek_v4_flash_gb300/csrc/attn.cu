@@ -452,12 +452,14 @@ ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void
   const bool rows16 = !ragged && n_new * a.group <= AD_MAX_ROWS && d.head_dim <= 128;
   if (shared_len) {
     if (!at_dev_ptr(shared_len) || (group_start && !at_dev_ptr(group_start))) return DS4MOE_ERR_INVALID_ARG;
-    // With a window a row sees few of the shared positions, or none: the plain call.
-    if (d.window == 0 && n_seq > 1) {
-      a.shared_len = shared_len, a.batch = n_seq, a.pre = h->shared.pre, a.pre_log = h->shared.pre_log;
+    // With a window a row sees few of the shared positions, or none; and where
+    // even a table full of them would gain nothing: the plain call.
+    a.cost = h->share_always ? ShareCost{1.0f, 0.0f, 0.0f, 0.0f} : share_cost(d, n_seq, n_new);
+    if (d.window == 0 && a.cost.gain(a.kv.width * a.kv.page_size, n_seq) > a.cost.least) {
+      a.shared_len = shared_len, a.group_start = group_start, a.n_groups = n_groups, a.batch = n_seq;
+      a.pre = h->shared.pre, a.pre_log = h->shared.pre_log;
       int launches = 0;
-      cudaError_t e = launch_attn_prefix(a, group_start, n_groups, d.head_dim, d.dtype, h->tile, h->shared, h->n_sm, &launches,
-                                         (cudaStream_t)stream);
+      cudaError_t e = launch_attn_prefix(a, d.head_dim, d.dtype, h->tile, h->shared, h->n_sm, &launches, (cudaStream_t)stream);
       if (e == cudaSuccess && rows16) {
         e = launch_attn_decode(a, d.head_dim, d.dtype, true, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
         launches++;
@@ -520,7 +522,7 @@ ds4moe_status ds4moe_attn_create(const ds4moe_attn_desc *desc, ds4moe_attn **out
     at += (bytes + 255) & ~(size_t)255;
     return p;
   };
-  const size_t o_err = place(64), o_ticket = place((size_t)h->n_sm * 4), o_marked = place((size_t)h->n_sm * 4);
+  const size_t o_err = place(64), o_ticket = place((size_t)2 * h->n_sm * 4), o_marked = place((size_t)h->n_sm * 4);
   const size_t o_split = place((size_t)h->n_sm * 32);
   const size_t o_count = place(4), o_seq = place((size_t)d.max_seqs * 4), o_cu = place(((size_t)d.max_seqs + 1) * 4);
   const size_t o_first = place((groups + 1) * 8);
@@ -694,6 +696,12 @@ ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, c
     return DS4MOE_ERR_INVALID_ARG;
   if (n_seq == 0) return DS4MOE_OK;
   return attn_call(h, cache, q, q_stride, nullptr, false, kv_len, n_seq, n_seq * n_new, n_new, out, out_stride, stream);
+}
+
+ds4moe_status ds4moe_attn_debug_share(ds4moe_attn *h, int32_t always) {
+  if (!h || (always != 0 && always != 1)) return DS4MOE_ERR_INVALID_ARG;
+  h->share_always = always;
+  return DS4MOE_OK;
 }
 
 ds4moe_status ds4moe_attn_decode_shared(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,

@@ -105,10 +105,6 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs &a, int b, bool &bad)
 
 // ---- a batch with shared positions
 
-// Whether a group's shared positions are read once for all: with fewer, or for a
-// single sequence, the second part reads them just as fast.
-__device__ __forceinline__ bool shared_worth(int s, int seqs) { return seqs >= 2 && s >= 128; }
-
 // Shared positions of group g, within what the table holds.
 __device__ __forceinline__ int shared_of(const AttnArgs &a, int g, bool &bad) {
   const int l = a.shared_len[g], s = min(max(l, 0), a.kv.width * a.kv.page_size);
@@ -116,13 +112,26 @@ __device__ __forceinline__ int shared_of(const AttnArgs &a, int g, bool &bad) {
   return s;
 }
 
-// Where sequence b's own positions begin. It shares the group's positions when
+// The group of a call without a planning launch: its sequences (the bounds
+// brought into the batch and in order, as clean_rows does), and the shared
+// positions that are read once.
+__device__ __forceinline__ int2 one_group(const AttnArgs &a, int &s, bool &bad) {
+  const int r0 = a.group_start ? a.group_start[0] : 0, r1 = a.group_start ? a.group_start[1] : a.batch;
+  s = shared_of(a, 0, bad);
+  const int c0 = clamp_row(r0, a.batch), c1 = max(clamp_row(r1, a.batch), c0);
+  bad |= c0 != r0 || c1 != r1;
+  if (a.cost.gain(s, c1 - c0) <= a.cost.least) s = 0;
+  return make_int2(c0, c1);
+}
+
+// Where sequence b's own positions begin. It shares its group's positions when
 // its first new token sees all of them.
 __device__ __forceinline__ int own_start(const AttnArgs &a, int b, int len) {
   if (a.start) return a.start[b];
   bool bad = false;
-  const int s = shared_of(a, 0, bad);
-  return shared_worth(s, a.batch) && len - a.n_new + 1 >= s ? s : 0;
+  int s;
+  const int2 c = one_group(a, s, bad);
+  return b >= c.x && b < c.y && len - a.n_new + 1 >= s ? s : 0;
 }
 
 // The rows of group g, no rows where nothing is read once; its positions; the
@@ -135,14 +144,16 @@ __device__ __forceinline__ SeqInfo prefix_info(const AttnArgs &a, int g, int *ta
     if (tab) *tab = a.ptab[g];
     return i;
   }
-  bool bad = false;
-  const int s = shared_of(a, 0, bad);
+  bool bad = false, ignored = false;
+  int s;
+  const int2 c = one_group(a, s, bad);
   if (bad && blockIdx.x == 0) raise_flag(a.err, DS4MOE_DEVERR_LENGTH);
-  if (!shared_worth(s, a.batch)) return i;
-  for (int b = 0; b < a.batch; b++) {  // (the first, unless a place in the batch is empty)
-    if (seq_len(a, b, bad) - a.n_new + 1 < s) continue;
+  i.tok0 = c.x * a.n_new;
+  if (s == 0) return i;
+  for (int b = c.x; b < c.y; b++) {  // (the first, unless a place in the batch is empty)
+    if (seq_len(a, b, ignored) - a.n_new + 1 < s) continue;
     if (tab) *tab = b;
-    i.n = a.batch * a.n_new, i.len = s;
+    i.n = (c.y - c.x) * a.n_new, i.len = s;
     break;
   }
   return i;

@@ -19,6 +19,21 @@ struct KvView {
   uint32_t div_mul, div_sh;  // page number of a position (page_index)
 };
 
+// What reading a group's shared positions once for all gains (attn_shared.cu).
+struct ShareCost {
+  float seq;    // ns of a position of one sequence in the plain kernels
+  float read;   // ns of a shared position: at least this, for its bytes,
+  float rows;   // and this for every sequence of the group, for its rows' products
+  float least;  // ns of launches, partials and joins that sharing adds
+#ifdef __CUDACC__
+  __host__ __device__
+#endif
+  float gain(int positions, int seqs) const {
+    const float once = rows * (float)seqs;
+    return seqs < 2 ? 0.0f : (float)positions * (seq * (float)seqs - (once > read ? once : read));
+  }
+};
+
 // One attention call. Tokens of sequence b are rows tok0(b) .. tok0(b) +
 // n_b - 1 of q; the j-th has position len(b) - n_b + j.
 struct AttnArgs {
@@ -37,14 +52,17 @@ struct AttnArgs {
   // of a group's positions; which of its blocks have marked rows
   int32_t span, gsh;
   int *marked;
-  // A batch with shared positions (attn_shared.cu): their number for each group,
-  // then, from its planning launch or null (one group of all sequences), what of
-  // it is read once, by which table row, and where each sequence's own positions
-  // begin; sequences of the call; the results over the shared positions,
-  // [n_tok][n_heads][head_dim], and log2 of their sums of weights.
-  const int32_t *shared_len, *plen, *ptab, *start;
-  int32_t batch;
+  // A batch with shared positions (attn_shared.cu): their number for each group
+  // and the groups' bounds (null: one group of all sequences); then, from the
+  // planning launch of a call of several groups or null, what of it is read once,
+  // by which table row, and where each sequence's own positions begin; sequences
+  // and groups of the call;
+  // the results over the shared positions, [n_tok][n_heads][head_dim], and log2
+  // of their sums of weights.
+  const int32_t *shared_len, *group_start, *plen, *ptab, *start;
+  int32_t batch, n_groups;
   float *pre, *pre_log;
+  ShareCost cost;
   uint32_t *err;
 };
 
@@ -79,6 +97,7 @@ struct ds4moe_attn {
   ds4::TileWork tile;  // the tile kernel's share (its partials are `part`)
   uint8_t *shared_mem;      // one allocation, or null
   int shared_tokens;        // rows that it serves
+  int share_always;         // ds4moe_attn_debug_share
   ds4::SharedWork shared;
   uint64_t bytes, shared_bytes, launches;
 };
@@ -100,9 +119,10 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int head_dim, int dtype, const T
                              cudaStream_t s);
 // attn_shared.cu: the shared positions of every group, planning launch first
 // where it needs one (which it notes in `a`), then every sequence's own ones.
+ShareCost share_cost(const ds4moe_attn_desc &d, int n_seq, int n_new);
 cudaError_t attn_shared_set_attributes(int dtype, int head_dim);
-cudaError_t launch_attn_prefix(AttnArgs &a, const int32_t *group_start, int n_groups, int head_dim, int dtype,
-                               const TileWork &w, const SharedWork &sw, int n_sm, int *launches, cudaStream_t s);
+cudaError_t launch_attn_prefix(AttnArgs &a, int head_dim, int dtype, const TileWork &w, const SharedWork &sw, int n_sm,
+                               int *launches, cudaStream_t s);
 cudaError_t launch_attn_own(const AttnArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
                             cudaStream_t s);
 }  // namespace ds4

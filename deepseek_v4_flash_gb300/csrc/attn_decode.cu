@@ -28,12 +28,18 @@
 
 namespace ds4 {
 
-constexpr int AD_WARPS = 8, AD_UNIT = 8;  // a unit: 8 groups of 16 positions, one per warp
+// Warps of a block; a unit has a group of 16 positions for each. Eight, and one
+// block per SM; with shared positions two blocks of four: there the items, of
+// the sequences' own positions, are short, and while one block joins its warps'
+// results the other one streams.
+template <bool SHARED>
+constexpr int AD_WARPS = SHARED ? 4 : 8;
 // A block's least run: below two units the join costs more than the split
 // gains (1 sequence of 8192, 8 heads on 1: 16.9 us with one, 13.0 with two, 14.6 with four).
 constexpr int AD_LEAST = 2;
-constexpr int AD_MAX_BLOCKS = 160;  // one per SM; the joining block's table of factors
-constexpr int AD_RING = 192 * 1024;
+constexpr int AD_MAX_BLOCKS = 160;  // blocks of eight warps (one per SM): the joining block's table of factors
+template <bool SHARED>
+constexpr int AD_RING = AD_WARPS<SHARED> * 24 * 1024;
 // fp16 weights are scaled by 2^14 (the largest is 16384): a weight then
 // vanishes below 2^-39 of the largest instead of 2^-25, and a long cache's
 // many small weights are not lost.
@@ -89,7 +95,7 @@ __device__ __forceinline__ DecSeq dec_seq(const AttnArgs &a, int b, bool &bad) {
     s.own = own_start(a, b, si.len);
     s.gr.win0 = s.own >> 4, s.gr.n = s.last < s.own ? 0 : s.gr.n - s.gr.win0;  // (no window)
   }
-  s.units = max(1, (s.gr.n + AD_UNIT - 1) / AD_UNIT);
+  s.units = max(1, (s.gr.n + AD_WARPS<SHARED> - 1) / AD_WARPS<SHARED>);
   return s;
 }
 
@@ -178,13 +184,13 @@ __device__ __noinline__ void redo_row(const AttnArgs &a, int t, int h, int b, in
 // SHARED: the positions before each sequence's own ones are in a.pre, whose
 // result joins the row's as it is stored (attn_shared.cu).
 template <int DT, int D, bool SHARED>
-__global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs a, float *part, int *ticket, int n_cta) {
+__global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_decode(const AttnArgs a, float *part, int *ticket, int n_cta) {
   constexpr int STAGE = 64 * D;  // a warp's 16 keys and 16 values; also 16 rows of O in 32 bits
-  constexpr int NST = AD_RING / (AD_WARPS * STAGE);
+  constexpr int NST = AD_RING<SHARED> / (AD_WARPS<SHARED> * STAGE);
   constexpr int CH = D / 8;      // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[AD_WARPS][16], s_l[AD_WARPS][16], s_mt[16], s_lt[16];
-  __shared__ float s_f[AD_MAX_BLOCKS][16];
+  __shared__ float s_m[AD_WARPS<SHARED>][16], s_l[AD_WARPS<SHARED>][16], s_mt[16], s_lt[16];
+  __shared__ float s_f[SHARED ? 1 : AD_MAX_BLOCKS][16];  // (SHARED: two blocks' tables would not fit beside their rings)
   __shared__ int s_last, s_nan;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int rows = a.n_new * a.group;
@@ -203,14 +209,14 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
   // the table's entry for the next unit is read one unit ahead
   int entry = 0, row0 = 0;
   auto look = [&]() {
-    const int g = lc.lu * AD_UNIT + w;
+    const int g = lc.lu * AD_WARPS<SHARED> + w;
     if (lc.b < a.n_seq && g < lc.s.gr.n) {
       const int p0 = group_pos(lc.s.gr, g), pi = page_index(a.kv, p0);
       entry = a.kv.table[(long long)lc.b * a.kv.table_stride + pi], row0 = p0 - pi * a.kv.page_size;
     }
   };
   auto load = [&](int slot) {
-    const int g = lc.lu * AD_UNIT + w;
+    const int g = lc.lu * AD_WARPS<SHARED> + w;
     if (g < lc.s.gr.n) {
       const int p0 = group_pos(lc.s.gr, g);
       const int page = entry >= 0 && entry < a.kv.n_pages ? entry : -1;
@@ -260,6 +266,11 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
     }
   }
 
+  // SHARED: this thread's pieces of the item's results over the shared positions,
+  // requested when the item begins
+  constexpr int PIECES = SHARED ? 16 * (D / 4) / (AD_WARPS<SHARED> * 32) : 1;
+  float4 pre[PIECES];
+  float pre_log[PIECES];
   uint32_t qf[D / 16][4];
   float o[D / 8][4], m[2], l[2];
   const int r0 = lane >> 2, r1 = r0 + 8, c2 = (lane & 3) * 2;
@@ -288,6 +299,16 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
         qf[k][2] = *reinterpret_cast<const uint32_t *>(qa + k * 16 + 8 + c2);
         qf[k][3] = *reinterpret_cast<const uint32_t *>(qb + k * 16 + 8 + c2);
       }
+      if (SHARED) {
+#pragma unroll
+        for (int j = 0; j < PIECES; j++) {
+          const int i = tid + j * AD_WARPS<SHARED> * 32, r = i / (D / 4), c = (i % (D / 4)) * 4;
+          pre_log[j] = -INFINITY, pre[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (r >= rows || cc.s.own == 0) continue;
+          const long long at = (long long)(t0 + r / a.group) * a.n_heads + h0 + r % a.group;
+          pre_log[j] = a.pre_log[at], pre[j] = *reinterpret_cast<const float4 *>(a.pre + at * D + c);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < D / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
       m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.0f;
@@ -295,7 +316,7 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
     cp_wait<NST - 1>();
     __syncwarp();
     const uint32_t kb = ring_u + (it % NST) * STAGE, vb = kb + 32 * D;
-    const int g = cc.lu * AD_UNIT + w;
+    const int g = cc.lu * AD_WARPS<SHARED> + w;
     if (g < cc.s.gr.n) {
       // two chains of products each (even and odd steps): half the latency
       float s[2][4] = {}, s2[2][4] = {};
@@ -395,8 +416,8 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       __syncthreads();
       if (tid < 16) {
         float mt = -INFINITY, lt = 0.0f;
-        for (int i = 0; i < AD_WARPS; i++) mt = fmaxf(mt, s_m[i][tid]);
-        for (int i = 0; i < AD_WARPS; i++) {
+        for (int i = 0; i < AD_WARPS<SHARED>; i++) mt = fmaxf(mt, s_m[i][tid]);
+        for (int i = 0; i < AD_WARPS<SHARED>; i++) {
           const float f = s_m[i][tid] == -INFINITY ? 0.0f : ex2(s_m[i][tid] - mt);
           lt += s_l[i][tid] * f;
           s_m[i][tid] = f;
@@ -409,16 +430,15 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
       const int slot = 2 * blockIdx.x + (item0 < u0 ? 0 : 1);
       float *pp = part + (size_t)slot * (16 * (D + 2));
       const int nan_rows_possible = a.n_new > 1;
-      auto store = [&](int r, int c, float4 x, float m, float l) {
+      auto store = [&](int r, int c, float4 x, float m, float l, int piece) {
         const int t = cc.b * a.n_new + r / a.group, h = cc.kvh * a.group + r % a.group;
         float inv = 1.0f / l, from = 0.0f;
-        const long long pre = (long long)t * a.n_heads + h;
-        if (SHARED) join_two(cc.s.own > 0 ? a.pre_log[pre] : -INFINITY, m, l, from, inv);
+        if (SHARED) join_two(pre_log[piece], m, l, from, inv);
         x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
         // no score above -infinity (whatever the values: 0 x NaN is NaN)
         if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (SHARED && from != 0.0f) {
-          const float4 p = *reinterpret_cast<const float4 *>(a.pre + pre * D + c);
+          const float4 p = pre[piece];
           x.x = fmaf(from, p.x, x.x), x.y = fmaf(from, p.y, x.y), x.z = fmaf(from, p.z, x.z), x.w = fmaf(from, p.w, x.w);
         }
         const uint2 u = make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
@@ -428,19 +448,30 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
           if (z != z) atomicOr(&s_nan, 1 << r);
         }
       };
-      for (int i = tid; i < rows * (D / 4); i += AD_WARPS * 32) {
+      auto sum_warps = [&](int i, int piece) {
         const int r = i / (D / 4), c = (i % (D / 4)) * 4;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int v = 0; v < AD_WARPS; v++) {
+        for (int v = 0; v < AD_WARPS<SHARED>; v++) {
           const float f = s_m[v][r];
           const float4 y = *reinterpret_cast<const float4 *>(smem + (size_t)(v * NST + it % NST) * STAGE +
                                                              4 * (r * D + (c ^ ((r & 7) << 3))));
           x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
         }
-        if (whole) store(r, c, x, s_mt[r], s_lt[r]);
+        if (whole) store(r, c, x, s_mt[r], s_lt[r], piece);
         else *reinterpret_cast<float4 *>(pp + r * D + c) = x;
-      }
+      };
+      // (SHARED: pieces are numbered at compile time, or they would not stay in registers)
+      auto each_piece = [&](auto f) {
+        if (SHARED) {
+#pragma unroll
+          for (int j = 0; j < PIECES; j++)
+            if (tid + j * AD_WARPS<SHARED> * 32 < rows * (D / 4)) f(tid + j * AD_WARPS<SHARED> * 32, j);
+        } else {
+          for (int i = tid; i < rows * (D / 4); i += AD_WARPS<SHARED> * 32) f(i, 0);
+        }
+      };
+      each_piece(sum_warps);
       bool done = whole;
       if (!whole) {
         if (tid < 16) pp[16 * D + tid] = s_mt[tid], pp[16 * D + 16 + tid] = s_lt[tid];
@@ -461,17 +492,18 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
           // the block where the item starts holds it in its second slot, the others in their first
           auto at = [&](int p) { return part + (size_t)(2 * (b0 + p) + (p == 0 ? 1 : 0)) * (16 * (D + 2)); };
           // a row's factors 2^(m_p - m) / l: lanes over the partials
-          for (int r = w; r < rows; r += AD_WARPS) {
+          for (int r = w; r < rows; r += AD_WARPS<SHARED>) {
             float mt = -INFINITY, lt = 0.0f;
             for (int p = lane; p < np; p += 32) {
               const float mp = __ldcg(at(p) + 16 * D + r);
-              s_f[p][r] = mp;
+              if (!SHARED) s_f[p][r] = mp;
               mt = fmaxf(mt, mp);
             }
             mt = warp_max(mt);
             for (int p = lane; p < np; p += 32) {
-              const float f = s_f[p][r] == -INFINITY ? 0.0f : ex2(s_f[p][r] - mt);
-              s_f[p][r] = f;
+              const float mp = SHARED ? __ldcg(at(p) + 16 * D + r) : s_f[p][r];
+              const float f = mp == -INFINITY ? 0.0f : ex2(mp - mt);
+              if (!SHARED) s_f[p][r] = f;
               lt = fmaf(f, __ldcg(at(p) + 16 * D + 16 + r), lt);
             }
 #pragma unroll
@@ -479,22 +511,23 @@ __global__ void __launch_bounds__(AD_WARPS * 32, 1) k_attn_decode(const AttnArgs
             if (lane == 0) s_lt[r] = lt, s_mt[r] = mt;
           }
           __syncthreads();
-          for (int i = tid; i < rows * (D / 4); i += AD_WARPS * 32) {
+          each_piece([&](int i, int piece) {
             const int r = i / (D / 4), c = (i % (D / 4)) * 4;
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 16
             for (int p = 0; p < np; p++) {
               const float4 y = __ldcg(reinterpret_cast<const float4 *>(at(p) + r * D + c));
-              const float f = s_f[p][r];
+              const float mp = SHARED ? __ldcg(at(p) + 16 * D + r) : 0.0f;
+              const float f = SHARED ? mp == -INFINITY ? 0.0f : ex2(mp - s_mt[r]) : s_f[p][r];
               x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
             }
-            store(r, c, x, s_mt[r], s_lt[r]);
-          }
+            store(r, c, x, s_mt[r], s_lt[r], piece);
+          });
         }
       }
       __syncthreads();
       if (nan_rows_possible && done && s_nan) {
-        for (int r = w; r < rows; r += AD_WARPS) {
+        for (int r = w; r < rows; r += AD_WARPS<SHARED>) {
           const int pos = cc.s.first + r / a.group, t = cc.b * a.n_new + r / a.group, h = cc.kvh * a.group + r % a.group;
           if ((s_nan >> r & 1) &&
               unseen_nonfinite<DT>(a, cc.b, cc.kvh, pos, pos, window_lo(a, max(cc.s.first, 0)), 0, cc.s.last + 1, 0, D) &&
@@ -517,13 +550,14 @@ static const void *dec_fn(int D, bool shared) {
   return D == 64 ? (const void *)k_attn_decode<DT, 64, false> : (const void *)k_attn_decode<DT, 128, false>;
 }
 
-size_t attn_decode_part_floats(int n_sm) { return (size_t)2 * n_sm * 16 * (128 + 2); }
+size_t attn_decode_part_floats(int n_sm) { return (size_t)2 * 2 * n_sm * 16 * (128 + 2); }
 
 cudaError_t attn_decode_set_attributes() {
   for (bool shared : {false, true})
     for (int D : {64, 128})
       for (const void *fn : {dec_fn<DS4MOE_DT_BF16>(D, shared), dec_fn<DS4MOE_DT_F16>(D, shared)}) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, AD_RING);
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   shared ? AD_RING<true> : AD_RING<false>);
         if (e != cudaSuccess) return e;
       }
   return cudaSuccess;
@@ -531,10 +565,12 @@ cudaError_t attn_decode_set_attributes() {
 
 cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, bool shared, float *part, int *ticket, int n_sm,
                                cudaStream_t s) {
-  if (n_sm > AD_MAX_BLOCKS) n_sm = AD_MAX_BLOCKS;
-  void *args[] = {(void *)&a, &part, &ticket, &n_sm};
+  int n_cta = shared ? 2 * n_sm : n_sm;
+  if (!shared && n_cta > AD_MAX_BLOCKS) n_cta = AD_MAX_BLOCKS;
+  void *args[] = {(void *)&a, &part, &ticket, &n_cta};
   const void *fn = dtype == DS4MOE_DT_BF16 ? dec_fn<DS4MOE_DT_BF16>(head_dim, shared) : dec_fn<DS4MOE_DT_F16>(head_dim, shared);
-  return launch_pdl(fn, dim3(n_sm), dim3(AD_WARPS * 32), AD_RING, s, args, true);
+  const int threads = 32 * (shared ? AD_WARPS<true> : AD_WARPS<false>);
+  return launch_pdl(fn, dim3(n_cta), dim3(threads), shared ? AD_RING<true> : AD_RING<false>, s, args, true);
 }
 
 }  // namespace ds4

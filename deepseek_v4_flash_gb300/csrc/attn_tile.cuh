@@ -129,6 +129,7 @@ struct TileArgs {
   int members;       // blocks that work on the same (item, key tiles): row tiles (decode calls, pairs) x halves
   int gangs;
   int whole;         // items are not split: each goes to the block whose run holds its first unit
+  int join;          // AT_PREFIX: blocks of k_attn_join share the gangs among so many
   long long *first;  // ragged: first unit of each row group, then the total (k_attn_plan); null: no plan
   int2 *info;        // ragged: {sequence, first token of the row group in it}
   int *count;        // ragged: number of row groups
@@ -1217,6 +1218,28 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       }
       if (!ok) break;
       const bool whole = s.starts && s.ends, none = s.kt0 >= s.kt1;
+      const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
+      // each warpgroup stores half of O's columns (64: the first all of them)
+      const int c0 = C::DV == 64 ? 0 : ch * (C::DV / 2), c1 = C::DV == 64 ? (ch ? 0 : 64) : c0 + C::DV / 2;
+      const long long pre = valid ? (long long)tq * a.n_heads + hq : 0;  // the row among the AT_PREFIX results
+      // AT_OWN: the rows' AT_PREFIX results, 32 columns at a time, the first
+      // while the last product runs, the others one step ahead
+      const long long pre_at = MODE == AT_OWN && whole && valid && s.lo > 0 ? pre * D + half * C::DV : -1;
+      uint32_t z[32];
+      float pre_log = -INFINITY;
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const long long at = __shfl_sync(0xffffffffu, pre_at, (lane & 24) + i);
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (at >= 0 && c < c1) u = *reinterpret_cast<const uint4 *>(a.pre + at + c + 4 * (lane & 7));
+          z[4 * i] = u.x, z[4 * i + 1] = u.y, z[4 * i + 2] = u.z, z[4 * i + 3] = u.w;
+        }
+      };
+      if (MODE == AT_OWN) {
+        if (pre_at >= 0) pre_log = a.pre_log[pre];
+        fetch(c0);
+      }
       if (!none) {
         // the item's last product (two row tiles: the only one this barrier counts)
         if (!wait_warp(b_of + 8 * r, (NT == 1 ? steps - 1 : items) & 1)) {
@@ -1230,14 +1253,10 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         if (!hear(other) || !meet()) break;  // both have read l when the next item writes
         l += other;
       }
-      const int tq = s.row0 + my_tok, hq = s.kvh * a.group + head;
       float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
-      const long long pre = valid ? (long long)tq * a.n_heads + hq : 0;  // the row among the AT_PREFIX results
-      float from = 0.0f;  // AT_OWN: the factor of that result
-      if (MODE == AT_OWN && whole) join_two(valid && s.lo > 0 ? a.pre_log[pre] : -INFINITY, m, none ? 0.0f : l, from, inv);
+      float from = 0.0f;  // AT_OWN: the factor of the AT_PREFIX result
+      if (MODE == AT_OWN && whole) join_two(pre_log, m, none ? 0.0f : l, from, inv);
       const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
-      // each warpgroup stores half of O's columns (64: the first all of them)
-      const int c0 = C::DV == 64 ? 0 : ch * (C::DV / 2), c1 = C::DV == 64 ? (ch ? 0 : 64) : c0 + C::DV / 2;
       // rows 8 (lane / 8) + i are this lane's to store, 16 bytes at piece lane % 8
       float *pp = t.part + ((size_t)(slot * NT + r) * 128 + (w & 3) * 32 + (lane & 24)) * C::PITCH + 4 * (lane & 7);
       const long long own = valid ? (long long)tq * a.out_stride + (long long)hq * D + half * C::DV : -1;
@@ -1265,16 +1284,12 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         } else if (whole) {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
-            uint32_t z[32];  // AT_OWN: the row's AT_PREFIX result
+            uint32_t zc[32];
             if (MODE == AT_OWN) {
 #pragma unroll
-              for (int i = 0; i < 8; i++) {
-                const long long at = __shfl_sync(0xffffffffu, valid && s.lo > 0 ? pre : -1, (lane & 24) + i);
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (at >= 0) u = *reinterpret_cast<const uint4 *>(a.pre + at * D + half * C::DV + c + 32 * h + 4 * (lane & 7));
-                z[4 * i] = u.x, z[4 * i + 1] = u.y, z[4 * i + 2] = u.z, z[4 * i + 3] = u.w;
-              }
-              transpose8(z);
+              for (int i = 0; i < 32; i++) zc[i] = z[i];
+              fetch(c + 32 * h + 32);
+              transpose8(zc);
             }
             if (none) {
 #pragma unroll
@@ -1289,7 +1304,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
               if (MODE == AT_OWN) {
                 // (a row without own positions: whatever the values, 0 x NaN is NaN)
                 if (l == 0.0f) x0 = x1 = 0.0f;
-                if (from != 0.0f) x0 = fmaf(from, __uint_as_float(z[2 * i]), x0), x1 = fmaf(from, __uint_as_float(z[2 * i + 1]), x1);
+                if (from != 0.0f) x0 = fmaf(from, __uint_as_float(zc[2 * i]), x0), x1 = fmaf(from, __uint_as_float(zc[2 * i + 1]), x1);
               }
               nan |= x0 != x0 || x1 != x1;
               y[16 * h + i] = Half16<DT>::down(x0, x1);
@@ -1392,23 +1407,46 @@ __global__ void __launch_bounds__(AJ_THREADS, D * R < 512 || D == 128 ? 4 : D * 
   __shared__ unsigned long long s_nan;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
-  const int bid = blockIdx.x / (128 / ROWS * NT);
-  const int gang = bid / t.members, member = bid % t.members;
+  const int jid = blockIdx.x / (128 / ROWS * NT), member = jid % t.members;
   const int half = PAIR ? member >> 1 & 1 : member % C::HALVES;
   const int rt = PAIR ? (member >> 2) * 2 + (member & 1) : member / C::HALVES;
   pdl_launch_dependents();
   pdl_wait();
+  // The gang in whose run a split item starts: this block's, or (AT_PREFIX, whose
+  // items are few, so that most gangs have none) those of a part of the gangs.
+  int gang = jid / t.members, gang1 = gang + 1;
+  if (MODE == AT_PREFIX) {
+    const int j = gang;
+    gang = t.gangs * j / t.join, gang1 = t.gangs * (j + 1) / t.join;
+  }
+  for (; gang < gang1; gang++) {
+  const int bid = gang * t.members + member;
   const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
   const int parts = d0.x;
+  if (MODE == AT_PREFIX && parts == 0) continue;
   if (parts == 0) return;
   const int tok0 = (rt + r) * t.tpt;  // one of the two is 0
   const int rows = min(t.tpt, d1.y - tok0) * a.group;
+  if (MODE == AT_PREFIX && r0 >= rows) continue;
   if (r0 >= rows) return;
   if (tid == 0) s_nan = 0;
   __syncthreads();
   const int row0 = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
   float m[R], l[R];
   float4 x[R];
+  // AT_OWN: the rows' AT_PREFIX results (R = 1)
+  float pre_log[R];
+  float4 pre_x[R];
+  auto pre_of = [&](int k) {
+    const int row = row0 + k * STEP;
+    return (long long)(d1.x + tok0 + row / a.group) * a.n_heads + d0.z * a.group + row % a.group;
+  };
+#pragma unroll
+  for (int k = 0; k < R; k++) {
+    pre_log[k] = -INFINITY, pre_x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (MODE == AT_OWN && d1.z > 0 && row0 + k * STEP < rows)
+      pre_log[k] = a.pre_log[pre_of(k)], pre_x[k] = *reinterpret_cast<const float4 *>(a.pre + pre_of(k) * D + half * C::DV + c);
+  }
 #pragma unroll
   for (int k = 0; k < R; k++) m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int p0 = 0; p0 < parts; p0 += P) {
@@ -1449,17 +1487,16 @@ __global__ void __launch_bounds__(AJ_THREADS, D * R < 512 || D == 128 ? 4 : D * 
     const int row = row0 + k * STEP;
     if (row >= rows) continue;
     float inv = 1.0f / l[k], from = 0.0f;
-    const long long pre = (long long)(d1.x + tok0 + row / a.group) * a.n_heads + d0.z * a.group + row % a.group;
-    if (MODE == AT_OWN) join_two(d1.z > 0 ? a.pre_log[pre] : -INFINITY, m[k], l[k], from, inv);
+    if (MODE == AT_OWN) join_two(pre_log[k], m[k], l[k], from, inv);
     float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
     if (l[k] == 0.0f) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (MODE == AT_PREFIX) {
-      *reinterpret_cast<float4 *>(a.pre + pre * D + half * C::DV + c) = z;
-      if (c == 0 && half == 0) a.pre_log[pre] = log_sum(m[k], l[k]);
+      *reinterpret_cast<float4 *>(a.pre + pre_of(k) * D + half * C::DV + c) = z;
+      if (c == 0 && half == 0) a.pre_log[pre_of(k)] = log_sum(m[k], l[k]);
       continue;
     }
     if (MODE == AT_OWN && from != 0.0f) {
-      const float4 p = *reinterpret_cast<const float4 *>(a.pre + pre * D + half * C::DV + c);
+      const float4 p = pre_x[k];
       z.x = fmaf(from, p.x, z.x), z.y = fmaf(from, p.y, z.y), z.z = fmaf(from, p.z, z.z), z.w = fmaf(from, p.w, z.w);
     }
     if (l[k] == l[k] && (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w)) atomicOr(&s_nan, 1ull << (row - r0));
@@ -1470,6 +1507,7 @@ __global__ void __launch_bounds__(AJ_THREADS, D * R < 512 || D == 128 ? 4 : D * 
   __syncthreads();
   const unsigned long long again = s_nan;
   if (MODE != AT_PREFIX && again) join_again<DT, D, NT, PAIR, MODE, ROWS>(a, t, again);
+  }
 }
 
 // The marked rows (AT_MARK), all in items that a block of the tile kernel did
@@ -1555,7 +1593,8 @@ TileFns fns() {
   using C = TileCfg<D, NT, PAIR>;
   // a key tile's stages are freed one by one, a value tile's are all held at once
   static_assert(C::NST > C::VST && (NT == 1 || C::NST > 2 * C::KST) && C::NST <= 12, "ring");
-  constexpr int R = RAGGED ? 4 : 1;
+  // (AT_PREFIX: few items of many partials, as a decode call)
+  constexpr int R = RAGGED && MODE != AT_PREFIX ? 4 : 1;
   // (rows of AT_PREFIX see all that the products read: none is computed once more)
   const void *mend = nullptr;
   if constexpr (MODE != AT_PREFIX) mend = (const void *)k_attn_mend<DT, D, NT, PAIR, MODE>;
@@ -1617,6 +1656,8 @@ cudaError_t launch_tile(const AttnArgs &a, int D, int dtype, const TileWork &w, 
   // block, and there is nothing to join.
   const long long reach = (long long)a.window + (ragged ? f.span * t.tpt : a.n_new) + a.n_sink + (2 << t.gsh);
   t.whole = a.window > 0 && reach <= AT_WHOLE * 128;
+  // (a split item is a row group's, of at most so many)
+  t.join = (int)std::min<long long>(t.gangs, 2ll * a.n_kv * (a.n_tok / (f.span * t.tpt) + a.n_seq));
   t.first = w.first, t.info = (int2 *)w.info, t.count = w.count, t.part = w.part, t.split = (int4 *)w.split;
   TileMaps maps;
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_tok};
@@ -1654,7 +1695,8 @@ cudaError_t launch_tile(const AttnArgs &a, int D, int dtype, const TileWork &w, 
   }
   if (e == cudaSuccess && !t.whole) {
     void *args[] = {&p, &t};
-    e = launch_pdl(f.join, dim3(t.gangs * t.members * f.nt * (128 / f.jrows)), dim3(AJ_THREADS), 0, s, args, true);
+    e = launch_pdl(f.join, dim3((MODE == AT_PREFIX ? t.join : t.gangs) * t.members * f.nt * (128 / f.jrows)), dim3(AJ_THREADS), 0,
+                   s, args, true);
     ++*launches;
   }
   if (e == cudaSuccess && f.mend && !t.whole && (long long)a.kv.width * a.kv.page_size >= AT_REDO &&

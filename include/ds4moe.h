@@ -551,9 +551,10 @@ ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, c
  *           one group of all (n_groups = 1).
  * n_groups 1..n_seq. Both are read on the device as kv_len is; DS4MOE_DEVERR_LENGTH
  * for shared_len outside the table (clamped) and bounds out of order (as cu_q).
- * Few shared positions, single sequences, and handles with a window, which see
- * little of what is shared, take the plain path: the argument never changes a
- * result but by its roundings.
+ * Where sharing would gain nothing (few shared positions or sequences; shapes whose
+ * sequences fill the products' tiles by themselves; handles with a window, which
+ * see little of what is shared) the plain path is taken, decided on the device
+ * for every group: the argument never changes a result but by its roundings.
  * ds4moe_attn_reserve_shared: workspace for such calls of up to max_tokens
  * (n_seq * n_new) rows, at most the handle's: max_tokens * n_heads * (head_dim +
  * 1) * 4 bytes. Allocates, synchronises; a smaller number than before changes
@@ -564,6 +565,11 @@ ds4moe_status ds4moe_attn_decode_shared(ds4moe_attn *h, const ds4moe_kv_cache *c
                                         const int32_t *kv_len, const int32_t *shared_len, const int32_t *group_start,
                                         int32_t n_groups, int32_t n_seq, int32_t n_new, void *out, int64_t out_stride,
                                         void *stream);
+
+/* ds4moe_attn_debug_share(h, 1): later calls share wherever two sequences have a
+ *   position in common, whether it gains anything or not (a test hook); 0: as
+ *   above. Errors: INVALID_ARG. */
+ds4moe_status ds4moe_attn_debug_share(ds4moe_attn *h, int32_t always);
 
 /* Attention of ragged runs of new tokens: sequence b has rows cu_q[b] ..
  * cu_q[b+1] - 1 (none is allowed), the last of them at position

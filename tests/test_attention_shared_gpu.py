@@ -64,13 +64,14 @@ def _check(out, q, k, v, table, lens, new, what=""):
                                   f"{float(over.max())} (error {float((got - ref).abs().max())})"
 
 
-def _run(kind, heads, kv, dim, page, groups, lens, new, seed=0, bounds=True):
+def _run(kind, heads, kv, dim, page, groups, lens, new, seed=0, bounds=True, share=True):
     ds4 = _ds4()
     k, v, table = _batch(kind, kv, dim, page, groups, lens, seed)
     g = torch.Generator().manual_seed(seed + 1)
     q = (torch.randn(len(lens), new, heads, dim, generator=g) * 1.5).to(DTYPES[kind]).cuda()
     n_tok = len(lens) * new
     at = ds4.Attention(ds4.AttentionDesc(heads, kv, dim, kind, max_seqs=len(lens), max_tokens=n_tok, max_shared_tokens=n_tok))
+    at.debug_share(share)
     cache, kv_len = ds4.KVCache(k, v, table.cuda()), _ints(lens)
     shared = _ints([s for _, _, s in groups])
     start = _ints([a for a, _, _ in groups] + [groups[-1][1]]) if bounds else None
@@ -122,6 +123,22 @@ def test_many_sequences(heads, kv, dim):
     _run("bf16", heads, kv, dim, 16, [(0, 700, 250)], lens, 1, seed=6, bounds=False)
 
 
+@pytest.mark.parametrize("heads,kv,dim,new", [(32, 8, 128, 1), (16, 4, 64, 2), (64, 8, 128, 4), (8, 2, 256, 1), (64, 1, 512, 1), (64, 1, 512, 4)])
+def test_where_it_gains(heads, kv, dim, new):
+    """Without the test hook: groups that share and groups that do not in one
+    batch, and a batch that gains nothing, which is the plain call."""
+    _run("bf16", heads, kv, dim, 64, [(0, 12, 9000), (12, 14, 300), (14, 15, 3000), (15, 30, 8000)],
+         [s + 10 + (37 * b) % 200 for a, e, s in ((0, 12, 9000), (12, 14, 300), (14, 15, 3000), (15, 30, 8000)) for b in range(a, e)],
+         new, seed=15, share=False)
+    ds4, at, cache, k, v, table, q, lens = _setup(heads, kv, dim, new, own=(5, 30, 64, max(2, new)))
+    at.debug_share(False)
+    counts = [at.launch_count()]
+    plain = at.decode(cache, q, _ints(lens))
+    counts.append(at.launch_count())
+    assert torch.equal(plain, at.decode(cache, q, _ints(lens), shared_len=_ints([200])))
+    assert at.launch_count() - counts[1] == counts[1] - counts[0]
+
+
 def test_pages():
     for page in (16, 48, 256, 1024):
         for heads, kv, dim, new in ((8, 2, 128, 1), (64, 1, 512, 1), (32, 2, 64, 4)):
@@ -136,6 +153,7 @@ def _setup(heads=8, kv=2, dim=128, new=2, s=200, own=(5, 30, 64, 2), page=16, ki
     q = (torch.randn(len(lens), new, heads, dim, generator=torch.Generator().manual_seed(seed)) * 1.5).to(DTYPES[kind]).cuda()
     n = len(lens) * new
     at = ds4.Attention(ds4.AttentionDesc(heads, kv, dim, kind, max_seqs=len(lens), max_tokens=n + 4, max_shared_tokens=n, **kw))
+    at.debug_share()
     return ds4, at, ds4.KVCache(k, v, table.cuda()), k, v, table, q, lens
 
 
@@ -211,6 +229,7 @@ def test_a_nan_that_long_rows_do_not_see():
         k, v, table = _batch("bf16", kv, dim, 1024, [(0, 2, s)], lens, 21)
         q = (torch.randn(2, new, heads, dim, generator=torch.Generator().manual_seed(2)) * 1.5).bfloat16().cuda()
         at = ds4.Attention(ds4.AttentionDesc(heads, kv, dim, max_seqs=2, max_tokens=4, max_shared_tokens=4))
+        at.debug_share()
         p = lens[0] - 1
         v[int(table[0, p // 1024]), p % 1024] = math.nan
         out = at.decode(ds4.KVCache(k, v, table.cuda()), q, _ints(lens), shared_len=_ints([s]))
@@ -222,7 +241,7 @@ def test_a_nan_that_long_rows_do_not_see():
 
 def test_lengths_bounds_and_pages_out_of_range():
     ds4, at, cache, k, v, table, q, lens = _setup(own=(5, 30, 64, 2, 9, 40))
-    plain = at.decode(cache, q, _ints(lens))
+    assert ds4.lib().ds4moe_attn_debug_share(None, 1) == 1 and ds4.lib().ds4moe_attn_debug_share(at._h, 2) == 1
     # bounds out of order: each is raised to the largest before it, sequences never belong to two groups
     out = at.decode(cache, q, _ints(lens), shared_len=_ints([200, 190, 150]), group_start=_ints([0, 4, 2, 6]))
     _check(out, q, k, v, table, lens, 2)
@@ -236,7 +255,8 @@ def test_lengths_bounds_and_pages_out_of_range():
     assert at.device_error() == 0
     for s, flag in ((-5, ds4.DEVERR_LENGTH), (10 ** 9, ds4.DEVERR_LENGTH), (0, 0)):
         out = at.decode(cache, q, _ints(lens), shared_len=_ints([s]))
-        assert torch.equal(out, plain) and at.device_error() == flag
+        _check(out, q, k, v, table, lens, 2)
+        assert at.device_error() == flag
     # a bad page under the shared positions reads as zeros
     bad = table.clone()
     bad[:, 3] = 10 ** 6
@@ -331,6 +351,7 @@ def test_refusals():
     with pytest.raises(ds4.Ds4MoeError):
         bare.decode(cache, q, n, shared_len=s)  # more rows than reserved
     assert L.ds4moe_attn_reserve_shared(bare._h, 8) == 0 and L.ds4moe_attn_reserve_shared(bare._h, 2) == 0
+    bare.debug_share()
     assert torch.equal(bare.decode(cache, q, n, shared_len=s), at.decode(cache, q, n, shared_len=s))
     p = ctypes.c_void_p
     row = 8 * 128
