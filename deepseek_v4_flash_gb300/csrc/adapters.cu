@@ -16,7 +16,7 @@
 // (a cluster per tile, the columns of A split over its blocks); k_adapt_expand
 // y = base + B V per tile and 128 columns. Products are tcgen05.mma kind::tf32:
 // a 16-bit weight is exact in tf32, and an fp32 operand is the sum of two tf32
-// numbers to 2^-21, so two products give what fp32 would.
+// numbers to 2^-20, so two products give what fp32 would.
 #include <math.h>
 #include <string.h>
 
@@ -37,9 +37,10 @@ struct ds4moe_adapters {
   uint16_t *A;       // [slots][R32][K]
   uint16_t *B;       // [slots] of [N][rank rounded up to 8]
   int *perm;         // [max_tokens] tokens in the order of their adapters
-  int4 *tiles;       // {slot, first place in perm, tokens, rank}
+  int4 *tiles;       // {slot, first place in perm, tokens | rank << 16, bits of the scale}
   int *n_tiles;
   float *v;          // [max_tokens][R32] scale A x by place in perm
+  int clusters[9];   // clusters of so many blocks of k_adapt_shrink that run at once
   uint64_t bytes, launches;
 };
 
@@ -199,21 +200,25 @@ __global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
 // Many tokens.
 
 // Tokens by adapter (no adapter last, only where base has to be copied), and
-// the tiles. One block.
+// the tiles. One block; a thread keeps the slots of its first LR_KEEP tokens.
+constexpr int LR_KEEP = 8;
 __global__ void __launch_bounds__(1024) k_adapt_plan(const AdaptArgs a) {
   __shared__ int s_n[LR_MAX_SLOTS + 1], s_at[LR_MAX_SLOTS + 1];
   __shared__ int w_rows[32], w_tiles[32];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
-  for (int s = tid; s <= a.slots; s += 1024) s_n[s] = 0;
+  int raw[LR_KEEP];
+#pragma unroll
+  for (int i = 0; i < LR_KEEP; i++) raw[i] = tid + 1024 * i < a.T ? a.slot_of[tid + 1024 * i] : -1;
+  for (int s = tid; s <= a.slots; s += 1024) s_n[s] = 0, s_at[s] = s < a.slots ? a.info[s].x : 0;  // (ranks, for now)
   __syncthreads();
   bool bad = false;
   // a token's bucket, -1 for none; a.slots: base is copied
-  auto bucket = [&](int t) {
+  auto bucket = [&](int t, int s) {
     if (t >= a.T) return -1;
-    int s = slot_at(a, t, bad);
-    if (s >= 0 && a.info[s].x == 0) s = -1;
+    if (s < -1 || s >= a.slots) bad = true, s = -1;
+    if (s >= 0 && s_at[s] == 0) s = -1;
     return s >= 0 ? s : a.base ? a.slots : -1;
   };
   auto count = [&](int *at, int s) {  // the warp's tokens of one bucket together; a token's place
@@ -223,14 +228,22 @@ __global__ void __launch_bounds__(1024) k_adapt_plan(const AdaptArgs a) {
     if (lane == first && s >= 0) p = atomicAdd(at + s, __popc(m));
     return __shfl_sync(0xffffffffu, p, first) + __popc(m & ((1u << lane) - 1));
   };
-  for (int t0 = 0; t0 < a.T; t0 += 1024) count(s_n, bucket(t0 + tid));
+#pragma unroll
+  for (int i = 0; i < LR_KEEP; i++) {
+    if (1024 * i >= a.T) break;
+    raw[i] = bucket(tid + 1024 * i, raw[i]);
+    count(s_n, raw[i]);
+  }
+  for (int t = 1024 * LR_KEEP + tid; t - tid < a.T; t += 1024) count(s_n, bucket(t, t < a.T ? a.slot_of[t] : -1));
   __syncthreads();
   // exclusive sums of rows and tiles over the buckets, five per thread
   constexpr int PER = (LR_MAX_SLOTS + 1 + 1023) / 1024;
-  int rows = 0, tiles = 0;
+  int rows = 0, tiles = 0, rank[PER];
+#pragma unroll
   for (int i = 0; i < PER; i++) {
     const int s = tid * PER + i;
-    if (s <= a.slots) rows += s_n[s], tiles += (s_n[s] + 127) / 128;
+    rank[i] = 0;
+    if (s <= a.slots) rows += s_n[s], tiles += (s_n[s] + 127) / 128, rank[i] = s_at[s];
   }
   int ri = rows, ti = tiles;
 #pragma unroll
@@ -242,19 +255,31 @@ __global__ void __launch_bounds__(1024) k_adapt_plan(const AdaptArgs a) {
   __syncthreads();
   int r0 = ri - rows, t0 = ti - tiles;
   for (int i = 0; i < w; i++) r0 += w_rows[i], t0 += w_tiles[i];
+  // tokens beyond the kept ones need the ranks once more
+  int places[PER];
+#pragma unroll
   for (int i = 0; i < PER; i++) {
     const int s = tid * PER + i;
-    if (s > a.slots) break;
-    s_at[s] = r0;
-    const int rank = s < a.slots ? a.info[s].x : 0;
-    for (int k = 0; k < s_n[s]; k += 128) a.tiles[t0++] = make_int4(s, r0 + k, min(128, s_n[s] - k), rank);
+    places[i] = r0;
+    if (s > a.slots) continue;
+    const int scale = s < a.slots && s_n[s] ? a.info[s].y : 0;
+    for (int k = 0; k < s_n[s]; k += 128) a.tiles[t0++] = make_int4(s, r0 + k, min(128, s_n[s] - k) | rank[i] << 16, scale);
     r0 += s_n[s];
   }
   if (tid == 1023) *a.n_tiles = t0;
+#pragma unroll
+  for (int i = 0; i < PER; i++)
+    if (tid * PER + i <= a.slots) s_n[tid * PER + i] = places[i];
   __syncthreads();
-  for (int b = 0; b < a.T; b += 1024) {
-    const int s = bucket(b + tid), p = count(s_at, s);
-    if (s >= 0) a.perm[p] = b + tid;
+#pragma unroll
+  for (int i = 0; i < LR_KEEP; i++) {
+    if (1024 * i >= a.T) break;
+    const int p = count(s_n, raw[i]);
+    if (raw[i] >= 0) a.perm[p] = tid + 1024 * i;
+  }
+  for (int t = 1024 * LR_KEEP + tid; t - tid < a.T; t += 1024) {
+    const int s = bucket(t, t < a.T ? a.slot_of[t] : -1), p = count(s_n, s);
+    if (s >= 0) a.perm[p] = t;
   }
   if (bad) raise_flag(a.err, DS4MOE_DEVERR_ADAPTER);
 }
@@ -270,83 +295,91 @@ __device__ __forceinline__ void umma_tf32(uint32_t d, uint64_t x, uint64_t y, ui
       "l"(x), "l"(y), "r"(id), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void sts4(uint32_t addr, const uint32_t *v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void named_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
 }
 // Byte of 16-byte piece p (0..7) of row r in a 128-byte swizzled operand.
 __device__ __forceinline__ uint32_t sw128(int r, int p) { return (uint32_t)(r * 128 + ((p ^ (r & 7)) << 4)); }
 
-// x = hi + lo: hi the leading 11 bits, lo the rest, rounded to 11 bits (an
-// error of 2^-21 of x at most). An infinity stays one (lo would be NaN).
-__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
-  hi = __float_as_uint(x) & 0xFFFFE000u;
-  const float d = x - __uint_as_float(hi);
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(isinf(x) ? 0.0f : d));
+// Four floats as a 16-byte piece of the two operands: x = hi + lo, each cut to
+// the 11 bits of a tf32 number (an error of 2^-20 of x at most). For an infinity
+// lo is NaN: either sums whose high part is not finite leave the low part out
+// (add_low), or it is made 0 (INF).
+constexpr uint32_t TF32 = 0xFFFFE000u;
+template <bool INF>
+__device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const uint4 &x) {
+  const uint32_t h0 = x.x & TF32, h1 = x.y & TF32, h2 = x.z & TF32, h3 = x.w & TF32;
+  auto rest = [](uint32_t v, uint32_t h) {
+    const float d = __uint_as_float(v) - __uint_as_float(h);
+    return INF && isinf(__uint_as_float(v)) ? 0u : __float_as_uint(d) & TF32;
+  };
+  sts4(hi_at, h0, h1, h2, h3);
+  sts4(lo_at, rest(x.x, h0), rest(x.y, h1), rest(x.z, h2), rest(x.w, h3));
 }
-// Four floats as a 16-byte piece of the two operands.
-__device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const float4 &x) {
-  uint32_t h[4], l[4];
-  split(x.x, h[0], l[0]), split(x.y, h[1], l[1]), split(x.z, h[2], l[2]), split(x.w, h[3], l[3]);
-  sts4(hi_at, h), sts4(lo_at, l);
-}
+__device__ __forceinline__ float add_low(float hi, float lo) { return isfinite(hi) ? hi + lo : hi; }
 // Eight 16-bit numbers as two pieces of one operand: pieces 2 p and 2 p + 1 of row r.
 template <int DT>
 __device__ __forceinline__ void put_wide(uint32_t at, int r, int p, const uint4 &w) {
+  auto f = [](float v) { return __float_as_uint(v); };
   const float2 f0 = Half16<DT>::up(w.x), f1 = Half16<DT>::up(w.y), f2 = Half16<DT>::up(w.z), f3 = Half16<DT>::up(w.w);
-  const uint32_t lo[4] = {__float_as_uint(f0.x), __float_as_uint(f0.y), __float_as_uint(f1.x), __float_as_uint(f1.y)};
-  const uint32_t hi[4] = {__float_as_uint(f2.x), __float_as_uint(f2.y), __float_as_uint(f3.x), __float_as_uint(f3.y)};
-  sts4(at + sw128(r, 2 * p), lo), sts4(at + sw128(r, 2 * p + 1), hi);
+  sts4(at + sw128(r, 2 * p), f(f0.x), f(f0.y), f(f1.x), f(f1.y));
+  sts4(at + sw128(r, 2 * p + 1), f(f2.x), f(f2.y), f(f3.x), f(f3.y));
 }
 
-// Accumulators of a block of k_adapt_shrink. The tensor cores add a product to
-// an accumulator with the sum cut, not rounded, to 24 bits, so a long chain of
-// additions drifts: 256 of them (1024 columns) were off by 4e-6 of the result,
-// five times what 32-bit sums are. So chunks go round several accumulators, the
-// small low parts of x to one of their own, added up in 32 bits at the end.
-// Tensor memory: half of an SM's for ranks up to 64, where two blocks share it,
-// else all of it.
-__host__ __device__ constexpr int shrink_accs(int r32) {
-  const int n = (r32 <= 64 ? 256 : 512) / r32;
-  return n < 4 ? n : 4;
-}
-__host__ __device__ constexpr int shrink_cols(int r32) { return r32 <= 32 ? 128 : r32 <= 64 ? 256 : 512; }
+// After a wait has run out the others that follow from it are short.
+struct Waits {
+  bool ok = true;
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
+    if (!mbar_wait_bounded(bar, parity, ok ? WAIT_LIMIT : 1000)) ok = false;
+  }
+};
 
 constexpr int LR_HALF = 128 * 128;  // 128 rows of 32 tf32 numbers
+constexpr int LR_SMEM = 224 * 1024;  // a block has an SM (and all of its tensor memory) to itself
 
-// Bytes of a stage of k_adapt_shrink: hi (and lo) of x, r32 rows of A.
+// ---- V = scale A x. One tile per cluster at a time; block k of the cluster
+// takes a part of the columns, 32 at a time. Sixteen warps split x (and widen
+// A) on the way from registers, where the next AHEAD chunks are under way, to
+// a ring in shared memory; one warp issues the products.
+//
+// The tensor cores add a product to an accumulator with the sum cut, not rounded,
+// to 24 bits, so a long chain of additions drifts: 256 of them (1024 columns)
+// were off by 4e-6 of the result, five times what 32-bit sums are. So chunks go
+// round several accumulators, the low parts of x to one of their own, added up
+// in 32 bits at the end.
+constexpr int LR_WARPS = 16;
 __host__ __device__ constexpr int shrink_stage(bool f32, int r32) { return LR_HALF * (f32 ? 2 : 1) + r32 * 128; }
-// At least as large a part of an SM's shared memory as of its tensor memory:
-// blocks of clusters that wait for one another must never wait for tensor
-// memory that another cluster's blocks hold.
-__host__ __device__ constexpr int shrink_smem(bool f32, int r32) {
-  const int ring = 2 * shrink_stage(f32, r32), sums = 128 * (r32 + 4) * 4;
-  const int need = (ring > sums ? ring : sums) + 1024, least = (shrink_cols(r32) == 512 ? 225 : 104) * 1024;
-  return need > least ? need : least;
+__host__ __device__ constexpr int shrink_stages(bool f32, int r32) {
+  const int n = (LR_SMEM - 1024) / shrink_stage(f32, r32);
+  return n < 6 ? n : 6;
 }
+__host__ __device__ constexpr int shrink_accs(int r32) { return 512 / r32 < 8 ? 512 / r32 : 8; }
 
-// V = scale A x of one tile per cluster at a time. Block k of the cluster takes
-// a part of the columns, 32 at a time: x is split into tf32 numbers on its way
-// from registers to shared memory, two chunks ahead of the products.
-template <int DT, bool F32>
-__global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int ks) {
+// WP: pieces of A per thread and chunk: one for ranks up to 128, else two.
+template <int DT, bool F32, int WP>
+__global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const AdaptArgs a, int ks) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2];
+  __shared__ __align__(8) uint64_t s_bar[2 * 6 + 1];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_row[128];
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const int stage_bytes = shrink_stage(F32, a.R32);
+  const int stage_bytes = shrink_stage(F32, a.R32), nst = shrink_stages(F32, a.R32);
   const uint32_t bar0 = smem_u32(s_bar);
-  const uint32_t cols = shrink_cols(a.R32);
-  // accumulators of the high parts; the low parts' one comes after them
-  const int n_acc = shrink_accs(a.R32) - (F32 ? 1 : 0);
-  if (w == 0) {
+  auto full = [&](int i) { return bar0 + 8 * i; };
+  auto empty = [&](int i) { return bar0 + 8 * (6 + i); };
+  const uint32_t b_done = bar0 + 8 * 12;
+  if (w == LR_WARPS) {
     if (lane == 0) {
-      mbar_init(bar0, 1), mbar_init(bar0 + 8, 1);
+      for (int i = 0; i < 6; i++) mbar_init(full(i), LR_WARPS), mbar_init(empty(i), 1);
+      mbar_init(b_done, 1);
       fence_mbar_init();
     }
     __syncwarp();
-    tmem_alloc(smem_u32(&s_tmem), cols);
+    tmem_alloc(smem_u32(&s_tmem), 512);
   }
   tc_fence_before();
   __syncthreads();
@@ -356,61 +389,96 @@ __global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int 
   pdl_wait();
   const int k = (int)cluster_rank(), n_tiles = *a.n_tiles, n_cl = gridDim.x / ks;
   const int ch0 = (a.K / 32) * k / ks, nc = (a.K / 32) * (k + 1) / ks - ch0;  // chunks of 32 columns
-  bool ok = true;
-  int used = 0;  // chunks so far
-  for (int i = blockIdx.x / ks; i < n_tiles; i += n_cl) {
-    const int4 tile = a.tiles[i];
-    const int rank = tile.w;
-    if (rank == 0) continue;
-    const int r32 = (rank + 31) & ~31;
-    if (tid < 128) s_row[tid] = tid < tile.z ? a.perm[tile.y + tid] : -1;
-    __syncthreads();
-    // this thread's pieces of a chunk: x rows, 16 bytes each, and rows of A
-    constexpr int XP = F32 ? 4 : 2, PR = F32 ? 8 : 4;  // pieces of x per thread; pieces of a row
-    const char *xp[XP];
+  // accumulators of the high parts; the low parts' one comes after them
+  const int n_acc = shrink_accs(a.R32) - (F32 ? 1 : 0);
+  Waits ws;
+  constexpr int XP = F32 ? 2 : 1, PR = F32 ? 8 : 4;  // 16-byte pieces of x per thread and chunk; pieces of a row
+  constexpr int AHEAD = WP == 1 ? 4 : 2;
+  uint4 x[AHEAD][XP], wt[AHEAD][WP];
+  const char *xp[XP];
+  const uint16_t *ap;
+  int r32 = 0;
+  // the next tile with a rank, from i on, and this thread's part of it
+  auto begin = [&](int i) {
+    int4 tile = make_int4(0, 0, 0, 0);
+    for (; i < n_tiles; i += n_cl) {
+      tile = a.tiles[i];
+      if (tile.z >> 16) break;
+    }
+    if (i >= n_tiles || w == LR_WARPS) return i;
+    r32 = ((tile.z >> 16) + 31) & ~31;
 #pragma unroll
     for (int j = 0; j < XP; j++) {
-      const int t = s_row[tid / PR + j * (256 / PR)];
-      xp[j] = t < 0 ? nullptr : (const char *)a.x + (long long)t * a.x_stride * (F32 ? 4 : 2) + (long long)ch0 * (F32 ? 128 : 64) + tid % PR * 16;
+      const int r = tid / PR + j * (LR_WARPS * 32 / PR);
+      xp[j] = nullptr;
+      if (r < (tile.z & 0xFFFF))
+        xp[j] = (const char *)a.x + ((long long)a.perm[tile.y + r] * a.x_stride + ch0 * 32) * (F32 ? 4 : 2) + tid % PR * 16;
     }
-    const uint16_t *ap = a.A + (long long)tile.x * a.R32 * a.K + (long long)(tid / 4) * a.K + ch0 * 32 + tid % 4 * 8;
-    uint4 x0[XP], x1[XP], w0[4], w1[4];
-    auto fetch = [&](int c, uint4 (&x)[XP], uint4 (&wt)[4]) {
+    ap = a.A + ((long long)tile.x * a.R32 + tid / 4) * a.K + ch0 * 32 + tid % 4 * 8;
+    return i;
+  };
+  auto fetch = [&](int c, uint4 (&x)[XP], uint4 (&wt)[WP]) {
 #pragma unroll
-      for (int j = 0; j < XP; j++)
-        x[j] = xp[j] && c < nc ? __ldcs(reinterpret_cast<const uint4 *>(xp[j] + (long long)c * (F32 ? 128 : 64))) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < XP; j++)
+      x[j] = xp[j] && c < nc ? __ldcs(reinterpret_cast<const uint4 *>(xp[j] + (long long)c * (F32 ? 128 : 64))) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        if (64 * j + tid / 4 < r32 && c < nc) wt[j] = *reinterpret_cast<const uint4 *>(ap + (long long)64 * j * a.K + c * 32);
-    };
-    const uint32_t id = idesc_tf32(__shfl_sync(0xffffffffu, r32, 0));
-    auto step = [&](int c, uint4 (&x)[XP], uint4 (&wt)[4]) {
-      const int u = used + c, st = u & 1;
-      if (u >= 2 && !mbar_wait_bounded(bar0 + 8 * st, (u / 2 - 1) & 1)) ok = false;
-      const uint32_t at = base + st * stage_bytes, lo = at + LR_HALF, wa = at + LR_HALF * (F32 ? 2 : 1);
+    for (int j = 0; j < WP; j++)
+      if (128 * j + tid / 4 < r32 && c < nc) wt[j] = *reinterpret_cast<const uint4 *>(ap + (long long)128 * j * a.K + c * 32);
+  };
+  int used = 0, tiles = 0;  // chunks, tiles so far
+  int i = begin(blockIdx.x / ks);
+  if (i < n_tiles && w < LR_WARPS) {
 #pragma unroll
-      for (int j = 0; j < XP; j++) {
-        const int r = tid / PR + j * (256 / PR);
-        if (F32) {
-          const uint32_t o = sw128(r, tid % PR);
-          put_split(at + o, lo + o, make_float4(__uint_as_float(x[j].x), __uint_as_float(x[j].y), __uint_as_float(x[j].z), __uint_as_float(x[j].w)));
-        } else {
-          put_wide<DT>(at, r, tid % PR, x[j]);
+    for (int c = 0; c < AHEAD; c++) fetch(c, x[c], wt[c]);
+  }
+  while (i < n_tiles) {
+    const int4 tile = a.tiles[i];
+    const int rank = tile.z >> 16, rows = tile.z & 0xFFFF, r32_now = (rank + 31) & ~31;
+    int next;
+    if (w < LR_WARPS) {
+      for (int c0 = 0; c0 < nc; c0 += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; j++) {
+          const int c = c0 + j;
+          if (c >= nc) break;
+          const int u = used + c, st = u % nst;
+          if (u >= nst) ws.wait(empty(st), (u / nst - 1) & 1);
+          const uint32_t at = base + st * stage_bytes, wa = at + LR_HALF * (F32 ? 2 : 1);
+#pragma unroll
+          for (int p = 0; p < XP; p++) {
+            const int r = tid / PR + p * (LR_WARPS * 32 / PR);
+            if (F32) {
+              const uint32_t o = sw128(r, tid % PR);
+              put_split<false>(at + o, at + LR_HALF + o, x[j][p]);
+            } else {
+              put_wide<DT>(at, r, tid % PR, x[j][p]);
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < WP; p++)
+            if (128 * p + tid / 4 < r32_now) put_wide<DT>(wa, 128 * p + tid / 4, tid % 4, wt[j][p]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full(st));
+          fetch(c + AHEAD, x[j], wt[j]);
         }
       }
+      // the next tile's first chunks come in while this one is added up
+      next = begin(i + n_cl);
+      if (next < n_tiles) {
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        if (64 * j + tid / 4 < r32) put_wide<DT>(wa, 64 * j + tid / 4, tid % 4, wt[j]);
-      fetch(c + 2, x, wt);
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (w == 0) {
-        const int us = __shfl_sync(0xffffffffu, st, 0);
-        const uint32_t sa = base + us * stage_bytes;
-        const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + LR_HALF * (F32 ? 2 : 1), 0);
-        const int uc = __shfl_sync(0xffffffffu, c, 0);
-        const uint32_t acc = tmem + uc % n_acc * a.R32, low = tmem + n_acc * a.R32;
+        for (int c = 0; c < AHEAD; c++) fetch(c, x[c], wt[c]);
+      }
+    } else {
+      const uint32_t id = idesc_tf32(__shfl_sync(0xffffffffu, r32_now, 0));
+      for (int c = 0; c < nc; c++) {
+        const int u = __shfl_sync(0xffffffffu, used + c, 0), uc = __shfl_sync(0xffffffffu, c, 0), st = u % nst;
+        ws.wait(full(st), (u / nst) & 1);
+        __syncwarp();
         tc_fence_after();
+        const uint32_t sa = base + st * stage_bytes;
+        const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + LR_HALF * (F32 ? 2 : 1), 0);
+        const uint32_t acc = tmem + uc % n_acc * a.R32, low = tmem + n_acc * a.R32;
         if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < 4; q++) umma_tf32(acc, dh + 2 * q, dw + 2 * q, id, uc >= n_acc || q != 0);
@@ -418,53 +486,51 @@ __global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int 
 #pragma unroll
             for (int q = 0; q < 4; q++) umma_tf32(low, dl + 2 * q, dw + 2 * q, id, uc != 0 || q != 0);
           }
-          umma_commit(bar0 + 8 * us);
+          umma_commit(empty(st));
+          if (uc + 1 == nc) umma_commit(b_done);
         }
         __syncwarp();
       }
-    };
-    fetch(0, x0, w0);
-    fetch(1, x1, w1);
-    for (int c = 0; c < nc; c += 2) {
-      step(c, x0, w0);
-      if (c + 1 < nc) step(c + 1, x1, w1);
+      next = begin(i + n_cl);
     }
-    used += nc;
-    // all products are done when the last chunk's are
-    if (nc && !mbar_wait_bounded(bar0 + 8 * ((used - 1) & 1), ((used - 1) / 2) & 1)) ok = false;
-    // (their operands too: the sums go over them)
-    __syncthreads();
+    if (nc) ws.wait(b_done, tiles & 1);
+    __syncwarp();
     tc_fence_after();
+    // the block's sums, over the ring
     float *sums = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));
-    const int pitch = r32 + 4;
-    for (int c = (w >> 2) * 32; c < r32; c += 64) {
-      float v[32];
-      const int row = (w & 3) * 32 + lane;
+    const int pitch = r32_now + 4;
+    if (w < LR_WARPS)
+      for (int c = (w >> 2) * 16; c < r32_now; c += 64) {
+        float v[16];
+        const int row = (w & 3) * 32 + lane, n_high = min(nc, n_acc);  // (the others are not written)
+        const uint32_t t0 = tmem + ((uint32_t)((w & 3) * 32) << 16) + c;
 #pragma unroll
-      for (int e = 0; e < 32; e++) v[e] = 0.0f;
-      for (int i = 0; i < n_acc + (F32 ? 1 : 0); i++) {
-        if (i >= nc && i < n_acc) continue;  // not written
-        if (nc == 0) break;
-        float z[32];
-        tmem_ld32(tmem + ((uint32_t)((w & 3) * 32) << 16) + i * a.R32 + c, z);
-        tmem_wait_ld(z);
+        for (int e = 0; e < 16; e++) v[e] = 0.0f;
+        for (int q = 0; q < n_high; q += 2) {
+          float y[16], z[16];
+          tmem_ld16x2(t0 + q * a.R32, t0 + min(q + 1, n_high - 1) * a.R32, y, z);
 #pragma unroll
-        for (int e = 0; e < 32; e++) v[e] += z[e];
+          for (int e = 0; e < 16; e++) v[e] += q + 1 < n_high ? y[e] + z[e] : y[e];
+        }
+        if (F32 && nc) {
+          float y[16], z[16];
+          tmem_ld16x2(t0 + n_acc * a.R32, t0 + n_acc * a.R32, y, z);
+#pragma unroll
+          for (int e = 0; e < 16; e++) v[e] = add_low(v[e], y[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4 *>(sums + row * pitch + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
       }
-#pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        *reinterpret_cast<float4 *>(sums + row * pitch + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    }
     tc_fence_before();
-    __syncthreads();
     cluster_arrive();
     cluster_wait();
     // this block's rows of the cluster's sum
-    const float scale = __int_as_float(a.info[tile.x].y);
-    const int q4 = r32 / 4, m = 128 / ks;
-    for (int e = tid; e < m * q4; e += 256) {
-      const int row = k * m + e / q4, c = e % q4 * 4;
-      if (row >= tile.z) continue;
+    const float scale = __int_as_float(tile.w);
+    const int q4 = r32_now / 4, m0 = 128 * k / ks, m1 = 128 * (k + 1) / ks;
+    for (int e = tid; e < (m1 - m0) * q4; e += LR_WARPS * 32 + 32) {
+      const int row = m0 + e / q4, c = e % q4 * 4;
+      if (row >= rows) continue;
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int b = 0; b < ks; b++) {
         const float4 o = remote_f32x4(smem_u32(sums + row * pitch + c), b);
@@ -477,34 +543,45 @@ __global__ void __launch_bounds__(256, 2) k_adapt_shrink(const AdaptArgs a, int 
     }
     cluster_arrive();
     cluster_wait();
+    tc_fence_after();
+    used += nc, tiles += nc != 0;
+    i = next;
   }
-  if (!ok) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
+  if (!ws.ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (w == 0) {
+  if (w == LR_WARPS) {
     tc_fence_after();
-    tmem_dealloc(tmem, cols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-constexpr int LR_STAGE = 3 * LR_HALF, LR_SMEM = 2 * LR_STAGE + 1024;
+// ---- y = base + B V, 128 tokens of a tile and 128 columns at a time; a block
+// takes a run of them. Four warps bring V (split) and B (widened) chunk by chunk
+// of 32 ranks into a ring and issue the products, into two accumulators in turn;
+// sixteen add base, which they request an item ahead, and store y. Bound by the
+// bytes of base and y.
+constexpr int LE_STAGE = 3 * LR_HALF, LE_NST = 4, LE_FEED = 128, LE_THREADS = LE_FEED + 512;
 
-// y = base + B V: 128 tokens of a tile and 128 columns at a time.
 template <int DT>
-__global__ void __launch_bounds__(256, 2) k_adapt_expand(const AdaptArgs a) {
+__global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2];
+  __shared__ __align__(8) uint64_t s_bar[LE_NST + 4];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
   const uint32_t bar0 = smem_u32(s_bar);
+  auto empty = [&](int i) { return bar0 + 8 * i; };
+  auto acc_full = [&](int i) { return bar0 + 8 * (LE_NST + i); };
+  auto acc_empty = [&](int i) { return bar0 + 8 * (LE_NST + 2 + i); };
   if (w == 0) {
     if (lane == 0) {
-      mbar_init(bar0, 1), mbar_init(bar0 + 8, 1);
+      for (int i = 0; i < LE_NST; i++) mbar_init(empty(i), 1);
+      for (int i = 0; i < 2; i++) mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), 16);
       fence_mbar_init();
     }
     __syncwarp();
-    tmem_alloc(smem_u32(&s_tmem), 128);
+    tmem_alloc(smem_u32(&s_tmem), 256);
   }
   tc_fence_before();
   __syncthreads();
@@ -512,29 +589,111 @@ __global__ void __launch_bounds__(256, 2) k_adapt_expand(const AdaptArgs a) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_launch_dependents();
   pdl_wait();
-  const int n_tiles = *a.n_tiles, n_col = (a.N + 127) / 128;
-  const float *from = a.base ? a.base : a.y;
-  const long long from_stride = a.base ? a.base_stride : a.y_stride;
-  bool ok = true;
-  int used = 0;
-  const uint32_t id = idesc_tf32(128);
-  for (long long i = blockIdx.x; i < (long long)n_tiles * n_col; i += gridDim.x) {
-    const int4 tile = a.tiles[i / n_col];
-    const int n0 = (int)(i % n_col) * 128, rank = tile.w, r8 = (rank + 7) & ~7, r32 = (rank + 31) & ~31;
-    // this lane's pieces of y: row (lane & 24) + j of the warp's 32, 16 bytes at
-    // piece lane % 8 of the 32 columns
-    const int row0 = (w & 3) * 32 + (lane & 24), col = n0 + (w >> 2) * 64 + 4 * (lane & 7);
-    int tok[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) tok[j] = row0 + j < tile.z ? a.perm[tile.y + row0 + j] : -1;
-    float4 b[8];
-    auto load = [&](int h) {
-      const int n = col + 32 * h;
+  const int n_col = (a.N + 127) / 128;
+  const long long total = (long long)*a.n_tiles * n_col;
+  const long long i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
+  Waits ws;
+  if (w < LE_FEED / 32) {
+    const uint32_t id = idesc_tf32(128);
+    int used = 0, accs = 0;
+    uint4 v[8], wt[4];
+    // the chunk of 32 ranks from c on of item i
+    auto fetch = [&](const int4 &tile, int n0, int c) {
+      const int rows = tile.z & 0xFFFF, r8 = ((tile.z >> 16) + 7) & ~7;
 #pragma unroll
       for (int j = 0; j < 8; j++) {
+        const int r = tid / 8 + 16 * j;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (r < rows) v[j] = *reinterpret_cast<const uint4 *>(a.v + (long long)(tile.y + r) * a.R32 + c + tid % 8 * 4);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int r = tid / 4 + 32 * j, e = c + tid % 4 * 8;
+        wt[j] = make_uint4(0, 0, 0, 0);
+        if (n0 + r < a.N && e < r8) wt[j] = *reinterpret_cast<const uint4 *>(a.B + (long long)tile.x * a.b_slot + (long long)(n0 + r) * r8 + e);
+      }
+    };
+    int at_tile = -1;
+    int4 tile = make_int4(0, 0, 0, 0);
+    auto load_tile = [&](long long i) {
+      const int t = (int)(i / n_col);
+      if (t != at_tile) at_tile = t, tile = a.tiles[t];
+    };
+    long long i = i0;
+    int c = 0;
+    auto skip = [&]() {  // to an item with products
+      for (; i < i1; i++) {
+        load_tile(i);
+        if (tile.z >> 16) break;
+        i = (long long)(at_tile + 1) * n_col - 1;  // (a tile without: all of its columns)
+      }
+    };
+    skip();
+    if (i < i1) fetch(tile, (int)(i % n_col) * 128, 0);
+    while (i < i1) {
+      const int r32 = ((tile.z >> 16) + 31) & ~31, buf = accs & 1, st = used % LE_NST;
+      const bool first = c == 0, last = c + 32 >= r32;
+      if (used >= LE_NST) ws.wait(empty(st), (used / LE_NST - 1) & 1);
+      const uint32_t at = base + st * LE_STAGE;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const uint32_t o = sw128(tid / 8 + 16 * j, tid % 8);
+        put_split<true>(at + o, at + LR_HALF + o, v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) put_wide<DT>(at + 2 * LR_HALF, tid / 4 + 32 * j, tid % 4, wt[j]);
+      // the next chunk under way
+      if (last) {
+        i++, c = 0;
+        skip();
+      } else {
+        c += 32;
+      }
+      if (i < i1) fetch(tile, (int)(i % n_col) * 128, c);
+      if (first && accs >= 2) ws.wait(acc_empty(buf), (accs / 2 - 1) & 1);
+      fence_proxy_async_smem();
+      named_sync<LE_FEED>(1);
+      if (w == 0) {
+        const uint32_t sa = base + __shfl_sync(0xffffffffu, st, 0) * LE_STAGE, d = tmem + __shfl_sync(0xffffffffu, buf, 0) * 128;
+        const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + 2 * LR_HALF, 0);
+        const uint32_t more = __shfl_sync(0xffffffffu, (int)!first, 0), ends = __shfl_sync(0xffffffffu, (int)last, 0);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) umma_tf32(d, dh + 2 * q, dw + 2 * q, id, more || q != 0);
+#pragma unroll
+          for (int q = 0; q < 4; q++) umma_tf32(d, dl + 2 * q, dw + 2 * q, id, 1);
+          umma_commit(empty(st));
+          if (ends) umma_commit(acc_full(buf));
+        }
+        __syncwarp();
+      }
+      used++, accs += last;
+    }
+    // nothing is in flight when the block leaves
+    if (used) ws.wait(empty((used - 1) % LE_NST), ((used - 1) / LE_NST) & 1);
+  } else {
+    const int q = w & 3, g = (w - LE_FEED / 32) >> 2;  // the warp's quarter of the rows, of the columns
+    const float *from = a.base ? a.base : a.y;
+    const long long from_stride = a.base ? a.base_stride : a.y_stride;
+    int at_tile = -1, tok = -1, accs = 0;
+    int4 tile = make_int4(0, 0, 0, 0);
+    // this lane's pieces of y: row (lane & 24) + j of the warp's 32, 16 bytes at
+    // piece lane % 8 of its 32 columns
+    float4 b[8];
+    auto load = [&](long long i) {
+      const int t = (int)(i / n_col), n = (int)(i % n_col) * 128 + 32 * g + 4 * (lane & 7);
+      if (t != at_tile) {
+        at_tile = t, tile = a.tiles[t];
+        const int row = 32 * q + lane;
+        tok = row < (tile.z & 0xFFFF) ? a.perm[tile.y + row] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int t_j = __shfl_sync(0xffffffffu, tok, (lane & 24) + j);
         b[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (tok[j] < 0) continue;
-        const float *p = from + (long long)tok[j] * from_stride + n;
+        if (t_j < 0) continue;
+        const float *p = from + (long long)t_j * from_stride + n;
         if (a.wide) {
           if (n < a.N) b[j] = __ldcs(reinterpret_cast<const float4 *>(p));
         } else {
@@ -545,92 +704,54 @@ __global__ void __launch_bounds__(256, 2) k_adapt_expand(const AdaptArgs a) {
         }
       }
     };
-    load(0);
-    for (int c = 0; c < r32; c += 32, used++) {
-      const int st = used & 1;
-      if (used >= 2 && !mbar_wait_bounded(bar0 + 8 * st, (used / 2 - 1) & 1)) ok = false;
-      const uint32_t at = base + st * LR_STAGE;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int r = tid / 8 + 32 * j;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r < tile.z) v = *reinterpret_cast<const float4 *>(a.v + (long long)(tile.y + r) * a.R32 + c + tid % 8 * 4);
-        const uint32_t o = sw128(r, tid % 8);
-        put_split(at + o, at + LR_HALF + o, v);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; j++) {
-        const int r = tid / 4 + 64 * j, e = c + tid % 4 * 8;
-        uint4 wt = make_uint4(0, 0, 0, 0);
-        if (n0 + r < a.N && e < r8) wt = *reinterpret_cast<const uint4 *>(a.B + (long long)tile.x * a.b_slot + (long long)(n0 + r) * r8 + e);
-        put_wide<DT>(at + 2 * LR_HALF, r, tid % 4, wt);
-      }
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (w == 0) {
-        const int us = __shfl_sync(0xffffffffu, st, 0);
-        const uint32_t sa = base + us * LR_STAGE;
-        const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + 2 * LR_HALF, 0);
-        const uint32_t more = __shfl_sync(0xffffffffu, c, 0) != 0;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int q = 0; q < 4; q++) umma_tf32(tmem, dh + 2 * q, dw + 2 * q, id, more || q != 0);
-#pragma unroll
-          for (int q = 0; q < 4; q++) umma_tf32(tmem, dl + 2 * q, dw + 2 * q, id, 1);
-          umma_commit(bar0 + 8 * us);
-        }
-        __syncwarp();
-      }
-    }
-    if (r32 && !mbar_wait_bounded(bar0 + 8 * ((used - 1) & 1), ((used - 1) / 2) & 1)) ok = false;
-    __syncwarp();
-    tc_fence_after();
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      float v[32];
-      if (h) load(1);
-      if (r32) {
-        tmem_ld32(tmem + ((uint32_t)((w & 3) * 32) << 16) + (w >> 2) * 64 + 32 * h, v);
-        tmem_wait_ld(v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; e++) v[e] = 0.0f;
-      }
+    if (i0 < i1) load(i0);
+    for (long long i = i0; i < i1; i++) {
+      const int n = (int)(i % n_col) * 128 + 32 * g + 4 * (lane & 7), mine = tok;
       uint32_t u[32];
+      if (tile.z >> 16) {
+        const int buf = accs & 1;
+        ws.wait(acc_full(buf), (accs / 2) & 1);
+        __syncwarp();
+        tc_fence_after();
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * 128 + 32 * g, v);
+        tmem_wait_ld(v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(buf));
+        accs++;
 #pragma unroll
-      for (int e = 0; e < 32; e++) u[e] = __float_as_uint(v[e]);
-      transpose8(u);
-      const int n = col + 32 * h;
+        for (int e = 0; e < 32; e++) u[e] = __float_as_uint(v[e]);
+        transpose8(u);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          b[j].x += __uint_as_float(u[4 * j]), b[j].y += __uint_as_float(u[4 * j + 1]);
+          b[j].z += __uint_as_float(u[4 * j + 2]), b[j].w += __uint_as_float(u[4 * j + 3]);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        if (tok[j] < 0) continue;
-        float4 o = b[j];
-        if (r32) {
-          o.x += __uint_as_float(u[4 * j]), o.y += __uint_as_float(u[4 * j + 1]);
-          o.z += __uint_as_float(u[4 * j + 2]), o.w += __uint_as_float(u[4 * j + 3]);
-        }
-        float *p = a.y + (long long)tok[j] * a.y_stride + n;
+        const int t_j = __shfl_sync(0xffffffffu, mine, (lane & 24) + j);
+        if (t_j < 0) continue;
+        float *p = a.y + (long long)t_j * a.y_stride + n;
         if (a.wide) {
-          if (n < a.N) __stcs(reinterpret_cast<float4 *>(p), o);
+          if (n < a.N) __stcs(reinterpret_cast<float4 *>(p), b[j]);
         } else {
-          if (n < a.N) p[0] = o.x;
-          if (n + 1 < a.N) p[1] = o.y;
-          if (n + 2 < a.N) p[2] = o.z;
-          if (n + 3 < a.N) p[3] = o.w;
+          if (n < a.N) p[0] = b[j].x;
+          if (n + 1 < a.N) p[1] = b[j].y;
+          if (n + 2 < a.N) p[2] = b[j].z;
+          if (n + 3 < a.N) p[3] = b[j].w;
         }
       }
+      if (i + 1 < i1) load(i + 1);
     }
-    tc_fence_before();
-    __syncthreads();  // the next product overwrites the accumulator
-    tc_fence_after();
   }
-  if (!ok) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
+  if (!ws.ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   if (w == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -677,14 +798,15 @@ ds4moe_status ap_status(cudaError_t e) {
 struct AdaptFns {
   const void *token, *shrink, *expand;
 };
-template <int DT>
-AdaptFns fns_of(bool f32) {
-  return {f32 ? (const void *)k_adapt_token<DT, true> : (const void *)k_adapt_token<DT, false>,
-          f32 ? (const void *)k_adapt_shrink<DT, true> : (const void *)k_adapt_shrink<DT, false>,
+template <int DT, bool F32>
+AdaptFns fns_of(bool two) {
+  return {(const void *)k_adapt_token<DT, F32>, two ? (const void *)k_adapt_shrink<DT, F32, 2> : (const void *)k_adapt_shrink<DT, F32, 1>,
           (const void *)k_adapt_expand<DT>};
 }
-AdaptFns adapt_fns(int dtype, bool f32) {
-  return dtype == DS4MOE_DT_BF16 ? fns_of<DS4MOE_DT_BF16>(f32) : fns_of<DS4MOE_DT_F16>(f32);
+AdaptFns adapt_fns(int dtype, bool f32, int r32) {
+  constexpr int B = DS4MOE_DT_BF16, F = DS4MOE_DT_F16;
+  const bool two = r32 > 128;
+  return dtype == B ? f32 ? fns_of<B, true>(two) : fns_of<B, false>(two) : f32 ? fns_of<F, true>(two) : fns_of<F, false>(two);
 }
 
 cudaError_t launch_cluster(const void *fn, int grid, int cluster, int threads, size_t smem, cudaStream_t s, void **args) {
@@ -735,11 +857,21 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device);
   for (bool f32 : {false, true}) {
-    const AdaptFns f = adapt_fns(dtype, f32);
+    const AdaptFns f = adapt_fns(dtype, f32, h->R32);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f.token, cudaFuncAttributeMaxDynamicSharedMemorySize, ((1 << 16) / LR_CLUSTER + 8) * 4);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+      e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f.expand, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
+    for (int ks = 1; ks <= LR_CLUSTER && e == cudaSuccess; ks++) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      cfg.gridDim = dim3(ks), cfg.blockDim = dim3(LR_WARPS * 32 + 32), cfg.dynamicSmemBytes = LR_SMEM;
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = ks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr, cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&h->clusters[ks], f.shrink, &cfg);
+      if (e == cudaSuccess && h->clusters[ks] < 1) h->clusters[ks] = 1;
+    }
   }
   if (e == cudaSuccess) e = cudaMalloc((void **)&h->mem, at);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->mem, 0, zeroed, 0);
@@ -805,7 +937,7 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   a.slot_of = slots, a.info = h->info, a.A = h->A, a.B = h->B;
   a.perm = h->perm, a.tiles = h->tiles, a.n_tiles = h->n_tiles, a.v = h->v, a.err = h->err;
   a.wide = N % 4 == 0 && y_stride % 4 == 0 && !((uintptr_t)y & 15) && (!base || (base_stride % 4 == 0 && !((uintptr_t)base & 15)));
-  const AdaptFns f = adapt_fns(h->dtype, f32);
+  const AdaptFns f = adapt_fns(h->dtype, f32, h->R32);
   const cudaStream_t s = (cudaStream_t)stream;
   if (n_tok <= LR_TOKENS) {
     void *args[] = {&a};
@@ -816,14 +948,23 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   void *plan[] = {&a};
   cudaError_t e = launch_pdl((const void *)k_adapt_plan, dim3(1), dim3(1024), 0, s, plan, true);
   if (e == cudaSuccess) {
+    // Blocks of a tile: the fewest chunks of 32 columns one after another, six
+    // more for a tile's start and sum, with some tiles that are not full; and
+    // chains of additions that stay exact (11 chunks per accumulator, see k_adapt_shrink).
+    const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1, full = n_tok / 128 + 1, guess = full + std::min(h->slots, full) / 2;
+    const int n_acc = shrink_accs(h->R32) - (f32 ? 1 : 0);
     int ks = LR_CLUSTER;
-    const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1, per_sm = shrink_cols(h->R32) == 512 ? 1 : 2;
-    int grid = std::min(per_sm * h->n_sm / ks, most) * ks;
+    long long best = -1;
+    for (int c = LR_CLUSTER; c >= 1; c--) {
+      const long long chunks = (K / 32 + c - 1) / c, cost = (guess + h->clusters[c] - 1) / h->clusters[c] * (chunks + 6);
+      if (best < 0 || (cost < best && chunks <= 11 * n_acc)) best = cost, ks = c;
+    }
+    const int grid = std::min(h->clusters[ks], most) * ks;
     void *args[] = {&a, &ks};
-    e = launch_cluster(f.shrink, grid, ks, 256, (size_t)shrink_smem(f32, h->R32), s, args);
+    e = launch_cluster(f.shrink, grid, ks, LR_WARPS * 32 + 32, LR_SMEM, s, args);
     if (e == cudaSuccess) {
       const long long items = (long long)most * ((N + 127) / 128);
-      e = launch_pdl(f.expand, dim3((unsigned)std::min<long long>(items, 2 * h->n_sm)), dim3(256), LR_SMEM, s, plan, true);
+      e = launch_pdl(f.expand, dim3((unsigned)std::min<long long>(items, h->n_sm)), dim3(LE_THREADS), LR_SMEM, s, plan, true);
     }
   }
   h->launches += 3;
