@@ -53,7 +53,8 @@ constexpr int LR_TOKENS = 64;
 
 struct AdaptArgs {
   int N, K, slots, T, R32;
-  long long b_slot, x_stride, y_stride, base_stride;
+  int x_stride, y_stride, base_stride;
+  long long b_slot;
   const void *x;
   const float *base;  // null: y itself
   float *y;
@@ -88,6 +89,11 @@ __device__ __forceinline__ float4 remote_f32x4(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(r) : "memory");
   return v;
+}
+
+// Asks L2 for `bytes` from p on (multiples of 16).
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // Slot of a token, -1 for none (and, with the flag, for one that there is not).
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
   const uint16_t *A = a.A + (long long)s * a.R32 * a.K, *B = a.B + (long long)s * a.b_slot;
   if (tid == 0) {  // this block's part of B on its way
     const uint32_t bytes = (uint32_t)min((long long)(n1 - n0) * r8 * 2, 1ll << 20);
-    if (bytes) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(B + (long long)n0 * r8), "r"(bytes) : "memory");
+    if (bytes) prefetch_l2(B + (long long)n0 * r8, bytes);
   }
   // pieces of eight columns
   const int u0 = (int)((long long)(a.K / 8) * c / LR_CLUSTER), nu = (int)((long long)(a.K / 8) * (c + 1) / LR_CLUSTER) - u0;
@@ -306,19 +312,18 @@ __device__ __forceinline__ void named_sync(int id) {
 __device__ __forceinline__ uint32_t sw128(int r, int p) { return (uint32_t)(r * 128 + ((p ^ (r & 7)) << 4)); }
 
 // Four floats as a 16-byte piece of the two operands: x = hi + lo, each cut to
-// the 11 bits of a tf32 number (an error of 2^-20 of x at most). For an infinity
-// lo is NaN: either sums whose high part is not finite leave the low part out
-// (add_low), or it is made 0 (INF).
-constexpr uint32_t TF32 = 0xFFFFE000u;
+// the 11 bits of a tf32 number (an error of 2^-20 of x at most). The products
+// leave the low 13 bits of a word out themselves. For an infinity lo is NaN:
+// either sums whose high part is not finite leave the low part out (add_low), or
+// it is made 0 (INF).
 template <bool INF>
 __device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const uint4 &x) {
-  const uint32_t h0 = x.x & TF32, h1 = x.y & TF32, h2 = x.z & TF32, h3 = x.w & TF32;
-  auto rest = [](uint32_t v, uint32_t h) {
-    const float d = __uint_as_float(v) - __uint_as_float(h);
-    return INF && isinf(__uint_as_float(v)) ? 0u : __float_as_uint(d) & TF32;
+  auto rest = [](uint32_t v) {
+    const float d = __uint_as_float(v) - __uint_as_float(v & 0xFFFFE000u);
+    return INF && isinf(__uint_as_float(v)) ? 0u : __float_as_uint(d);
   };
-  sts4(hi_at, h0, h1, h2, h3);
-  sts4(lo_at, rest(x.x, h0), rest(x.y, h1), rest(x.z, h2), rest(x.w, h3));
+  sts4(hi_at, x.x, x.y, x.z, x.w);
+  sts4(lo_at, rest(x.x), rest(x.y), rest(x.z), rest(x.w));
 }
 __device__ __forceinline__ float add_low(float hi, float lo) { return isfinite(hi) ? hi + lo : hi; }
 // Eight 16-bit numbers as two pieces of one operand: pieces 2 p and 2 p + 1 of row r.
@@ -342,39 +347,47 @@ constexpr int LR_HALF = 128 * 128;  // 128 rows of 32 tf32 numbers
 constexpr int LR_SMEM = 224 * 1024;  // a block has an SM (and all of its tensor memory) to itself
 
 // ---- V = scale A x. One tile per cluster at a time; block k of the cluster
-// takes a part of the columns, 32 at a time. Sixteen warps split x (and widen
-// A) on the way from registers, where the next AHEAD chunks are under way, to
-// a ring in shared memory; one warp issues the products.
+// takes a part of the columns, in chunks of CH * 32. Two groups of four warps take
+// the chunks in turn: they split x (and widen A) on the way from registers, where
+// the group's next chunk is under way, to a ring in shared memory; one warp
+// issues the products. What bounds it is issuing that work: sixteen warps that
+// all took a part of every chunk of 32 columns passed too many barriers and proxy
+// fences (73 us for the prompts of 6.6 thousand tokens; groups of them 57).
 //
 // The tensor cores add a product to an accumulator with the sum cut, not rounded,
 // to 24 bits, so a long chain of additions drifts: 256 of them (1024 columns)
 // were off by 4e-6 of the result, five times what 32-bit sums are. So chunks go
 // round several accumulators, the low parts of x to one of their own, added up
 // in 32 bits at the end.
-constexpr int LR_WARPS = 16;
-__host__ __device__ constexpr int shrink_stage(bool f32, int r32) { return LR_HALF * (f32 ? 2 : 1) + r32 * 128; }
+constexpr int LR_WARPS = 8, LR_GROUPS = 2, LR_FEED = LR_WARPS * 32 / LR_GROUPS;
+// 32-column parts of a chunk: two, while two stages of them fit.
+__host__ __device__ constexpr int shrink_ch(int r32) { return r32 <= 128 ? 2 : 1; }
+// A part: the high numbers of x, the low ones (fp32), the rows of A.
+__host__ __device__ constexpr int shrink_part(bool f32, int r32) { return LR_HALF * (f32 ? 2 : 1) + r32 * 128; }
+__host__ __device__ constexpr int shrink_stage(bool f32, int r32) { return shrink_ch(r32) * shrink_part(f32, r32); }
 __host__ __device__ constexpr int shrink_stages(bool f32, int r32) {
   const int n = (LR_SMEM - 1024) / shrink_stage(f32, r32);
-  return n < 6 ? n : 6;
+  return n < 6 ? n : 6;  // (two at least)
 }
 __host__ __device__ constexpr int shrink_accs(int r32) { return 512 / r32 < 8 ? 512 / r32 : 8; }
 
-// WP: pieces of A per thread and chunk: one for ranks up to 128, else two.
+// WP: 16-byte pieces of A per thread and part, a 32nd of the largest rank.
 template <int DT, bool F32, int WP>
 __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const AdaptArgs a, int ks) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[2 * 6 + 1];
   __shared__ uint32_t s_tmem;
+  constexpr int CH = shrink_ch(WP * 32);
   const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const int stage_bytes = shrink_stage(F32, a.R32), nst = shrink_stages(F32, a.R32);
+  const int part_bytes = shrink_part(F32, a.R32), nst = shrink_stages(F32, a.R32);
   const uint32_t bar0 = smem_u32(s_bar);
   auto full = [&](int i) { return bar0 + 8 * i; };
   auto empty = [&](int i) { return bar0 + 8 * (6 + i); };
   const uint32_t b_done = bar0 + 8 * 12;
   if (w == LR_WARPS) {
     if (lane == 0) {
-      for (int i = 0; i < 6; i++) mbar_init(full(i), LR_WARPS), mbar_init(empty(i), 1);
+      for (int i = 0; i < 6; i++) mbar_init(full(i), LR_FEED / 32), mbar_init(empty(i), 1);
       mbar_init(b_done, 1);
       fence_mbar_init();
     }
@@ -388,14 +401,15 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
   pdl_launch_dependents();
   pdl_wait();
   const int k = (int)cluster_rank(), n_tiles = *a.n_tiles, n_cl = gridDim.x / ks;
-  const int ch0 = (a.K / 32) * k / ks, nc = (a.K / 32) * (k + 1) / ks - ch0;  // chunks of 32 columns
+  // this block's parts of 32 columns and chunks
+  const int p0 = (a.K / 32) * k / ks, np = (a.K / 32) * (k + 1) / ks - p0, nc = (np + CH - 1) / CH;
   // accumulators of the high parts; the low parts' one comes after them
   const int n_acc = shrink_accs(a.R32) - (F32 ? 1 : 0);
   Waits ws;
-  constexpr int XP = F32 ? 2 : 1, PR = F32 ? 8 : 4;  // 16-byte pieces of x per thread and chunk; pieces of a row
-  constexpr int AHEAD = WP == 1 ? 4 : 2;
-  uint4 x[AHEAD][XP], wt[AHEAD][WP];
-  const char *xp[XP];
+  constexpr int PR = F32 ? 8 : 4, XP = 128 * PR / LR_FEED;  // 16-byte pieces of a row's part of x; of a thread
+  const int ft = tid & (LR_FEED - 1), group = tid / LR_FEED;
+  uint4 x[CH][XP], wt[CH][WP];
+  int tok[XP];
   const uint16_t *ap;
   int r32 = 0;
   // the next tile with a rank, from i on, and this thread's part of it
@@ -409,84 +423,120 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     r32 = ((tile.z >> 16) + 31) & ~31;
 #pragma unroll
     for (int j = 0; j < XP; j++) {
-      const int r = tid / PR + j * (LR_WARPS * 32 / PR);
-      xp[j] = nullptr;
-      if (r < (tile.z & 0xFFFF))
-        xp[j] = (const char *)a.x + ((long long)a.perm[tile.y + r] * a.x_stride + ch0 * 32) * (F32 ? 4 : 2) + tid % PR * 16;
+      const int r = ft / PR + j * (LR_FEED / PR);
+      tok[j] = a.perm[tile.y + min(r, (tile.z & 0xFFFF) - 1)];  // (rows past the last are not stored)
     }
-    ap = a.A + ((long long)tile.x * a.R32 + tid / 4) * a.K + ch0 * 32 + tid % 4 * 8;
+    ap = a.A + ((long long)tile.x * a.R32 + ft / 4) * a.K + p0 * 32 + ft % 4 * 8;
     return i;
   };
-  auto fetch = [&](int c, uint4 (&x)[XP], uint4 (&wt)[WP]) {
+  auto fetch = [&](int c) {
+    const char *p = (const char *)a.x + (p0 + c * CH) * (F32 ? 128 : 64) + ft % PR * 16;
+    const bool two = c * CH + 1 < np;
+    if (c * CH >= np) return;
 #pragma unroll
-    for (int j = 0; j < XP; j++)
-      x[j] = xp[j] && c < nc ? __ldcs(reinterpret_cast<const uint4 *>(xp[j] + (long long)c * (F32 ? 128 : 64))) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < XP; j++) {
+      const char *row = p + (long long)tok[j] * (a.x_stride * (F32 ? 4ll : 2ll));
+      x[0][j] = __ldcs(reinterpret_cast<const uint4 *>(row));
+      if (CH == 2 && two) x[CH - 1][j] = __ldcs(reinterpret_cast<const uint4 *>(row + (F32 ? 128 : 64)));
+    }
 #pragma unroll
     for (int j = 0; j < WP; j++)
-      if (128 * j + tid / 4 < r32 && c < nc) wt[j] = *reinterpret_cast<const uint4 *>(ap + (long long)128 * j * a.K + c * 32);
+      if (32 * j + ft / 4 < r32) {
+        const uint16_t *row = ap + (long long)32 * j * a.K + c * CH * 32;
+        wt[0][j] = *reinterpret_cast<const uint4 *>(row);
+        if (CH == 2 && two) wt[CH - 1][j] = *reinterpret_cast<const uint4 *>(row + 32);
+      }
   };
-  int used = 0, tiles = 0;  // chunks, tiles so far
+  // Rows of x lie far apart and a chunk takes 128 bytes or two of each: the rows'
+  // next SPAN chunks are asked for at once, SPAN to 2 SPAN chunks ahead (thread: row).
+  constexpr int SPAN = 8 / CH, CHUNK = CH * (F32 ? 128 : 64);
+  const char *row_x = nullptr;
+  auto ask = [&](int c) {
+    if (row_x && c < nc) prefetch_l2(row_x + (long long)c * CHUNK, (uint32_t)min(SPAN * CHUNK, (np - c * CH) * (CHUNK / CH)));
+  };
+  auto ask_first = [&](int i) {
+    const int4 tile = a.tiles[i];
+    row_x = nullptr;
+    if (tid < (tile.z & 0xFFFF)) row_x = (const char *)a.x + ((long long)a.perm[tile.y + tid] * a.x_stride + p0 * 32) * (F32 ? 4 : 2);
+    ask(0), ask(SPAN);
+  };
+  // the ring: stage and lap of the warp's next chunk (of the group's, or of the products')
+  int st = 0, lap = 0;
+  auto advance = [&](int n) {
+    for (st += n; st >= nst; st -= nst) lap++;
+    for (; st < 0; st += nst) lap--;
+  };
+  int tiles = 0;
   int i = begin(blockIdx.x / ks);
-  if (i < n_tiles && w < LR_WARPS) {
-#pragma unroll
-    for (int c = 0; c < AHEAD; c++) fetch(c, x[c], wt[c]);
+  if (w < LR_WARPS) {
+    if (i < n_tiles) {
+      if (group == 0) ask_first(i);
+      fetch(group);
+    }
+    advance(group);
   }
   while (i < n_tiles) {
     const int4 tile = a.tiles[i];
     const int rank = tile.z >> 16, rows = tile.z & 0xFFFF, r32_now = (rank + 31) & ~31;
     int next;
     if (w < LR_WARPS) {
-      for (int c0 = 0; c0 < nc; c0 += AHEAD) {
+      int c = group;
+      for (; c < nc; c += LR_GROUPS, advance(LR_GROUPS)) {
+        if (group == 0 && c % SPAN == 0) ask(c + 2 * SPAN);
+        if (lap > 0) ws.wait(empty(st), (lap - 1) & 1);
 #pragma unroll
-        for (int j = 0; j < AHEAD; j++) {
-          const int c = c0 + j;
-          if (c >= nc) break;
-          const int u = used + c, st = u % nst;
-          if (u >= nst) ws.wait(empty(st), (u / nst - 1) & 1);
-          const uint32_t at = base + st * stage_bytes, wa = at + LR_HALF * (F32 ? 2 : 1);
+        for (int h = 0; h < CH; h++) {
+          if (c * CH + h >= np) break;
+          const uint32_t at = base + (st * CH + h) * part_bytes, wa = at + LR_HALF * (F32 ? 2 : 1);
 #pragma unroll
           for (int p = 0; p < XP; p++) {
-            const int r = tid / PR + p * (LR_WARPS * 32 / PR);
+            const int r = ft / PR + p * (LR_FEED / PR);
             if (F32) {
-              const uint32_t o = sw128(r, tid % PR);
-              put_split<false>(at + o, at + LR_HALF + o, x[j][p]);
+              const uint32_t o = sw128(r, ft % PR);
+              put_split<false>(at + o, at + LR_HALF + o, x[h][p]);
             } else {
-              put_wide<DT>(at, r, tid % PR, x[j][p]);
+              put_wide<DT>(at, r, ft % PR, x[h][p]);
             }
           }
 #pragma unroll
           for (int p = 0; p < WP; p++)
-            if (128 * p + tid / 4 < r32_now) put_wide<DT>(wa, 128 * p + tid / 4, tid % 4, wt[j][p]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full(st));
-          fetch(c + AHEAD, x[j], wt[j]);
+            if (32 * p + ft / 4 < r32_now) put_wide<DT>(wa, 32 * p + ft / 4, ft % 4, wt[h][p]);
         }
+        fetch(c + LR_GROUPS);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(st));
       }
+      advance(nc + group - c);  // all warps' chunks follow on the tile's nc chunks
       // the next tile's first chunks come in while this one is added up
       next = begin(i + n_cl);
       if (next < n_tiles) {
-#pragma unroll
-        for (int c = 0; c < AHEAD; c++) fetch(c, x[c], wt[c]);
+        if (group == 0) ask_first(next);
+        fetch(group);
       }
     } else {
       const uint32_t id = idesc_tf32(__shfl_sync(0xffffffffu, r32_now, 0));
-      for (int c = 0; c < nc; c++) {
-        const int u = __shfl_sync(0xffffffffu, used + c, 0), uc = __shfl_sync(0xffffffffu, c, 0), st = u % nst;
-        ws.wait(full(st), (u / nst) & 1);
+      for (int c = 0; c < nc; c++, advance(1)) {
+        const int uc = __shfl_sync(0xffffffffu, c, 0), us = __shfl_sync(0xffffffffu, st, 0);
+        ws.wait(full(us), lap & 1);
         __syncwarp();
         tc_fence_after();
-        const uint32_t sa = base + st * stage_bytes;
-        const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + LR_HALF * (F32 ? 2 : 1), 0);
-        const uint32_t acc = tmem + uc % n_acc * a.R32, low = tmem + n_acc * a.R32;
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) umma_tf32(acc, dh + 2 * q, dw + 2 * q, id, uc >= n_acc || q != 0);
-          if (F32) {
+          for (int h = 0; h < CH; h++) {
+            const int part = uc * CH + h;
+            if (part >= np) break;
+            const uint32_t sa = base + (us * CH + h) * part_bytes;
+            const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + LR_HALF * (F32 ? 2 : 1), 0);
+            const uint32_t acc = tmem + part % n_acc * a.R32, low = tmem + n_acc * a.R32;
 #pragma unroll
-            for (int q = 0; q < 4; q++) umma_tf32(low, dl + 2 * q, dw + 2 * q, id, uc != 0 || q != 0);
+            for (int q = 0; q < 4; q++) umma_tf32(acc, dh + 2 * q, dw + 2 * q, id, part >= n_acc || q != 0);
+            if (F32) {
+#pragma unroll
+              for (int q = 0; q < 4; q++) umma_tf32(low, dl + 2 * q, dw + 2 * q, id, part != 0 || q != 0);
+            }
           }
-          umma_commit(empty(st));
+          umma_commit(empty(us));
           if (uc + 1 == nc) umma_commit(b_done);
         }
         __syncwarp();
@@ -500,9 +550,9 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     float *sums = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));
     const int pitch = r32_now + 4;
     if (w < LR_WARPS)
-      for (int c = (w >> 2) * 16; c < r32_now; c += 64) {
+      for (int c = (w >> 2) * 16; c < r32_now; c += 32) {
         float v[16];
-        const int row = (w & 3) * 32 + lane, n_high = min(nc, n_acc);  // (the others are not written)
+        const int row = (w & 3) * 32 + lane, n_high = min(np, n_acc);  // (the others are not written)
         const uint32_t t0 = tmem + ((uint32_t)((w & 3) * 32) << 16) + c;
 #pragma unroll
         for (int e = 0; e < 16; e++) v[e] = 0.0f;
@@ -529,7 +579,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     const float scale = __int_as_float(tile.w);
     const int q4 = r32_now / 4, m0 = 128 * k / ks, m1 = 128 * (k + 1) / ks;
     for (int e = tid; e < (m1 - m0) * q4; e += LR_WARPS * 32 + 32) {
-      const int row = m0 + e / q4, c = e % q4 * 4;
+      const int row = m0 + e / q4, c = (e - (row - m0) * q4) * 4;
       if (row >= rows) continue;
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int b = 0; b < ks; b++) {
@@ -544,7 +594,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     cluster_arrive();
     cluster_wait();
     tc_fence_after();
-    used += nc, tiles += nc != 0;
+    tiles += nc != 0;
     i = next;
   }
   if (!ws.ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
@@ -557,13 +607,15 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
 }
 
 // ---- y = base + B V, 128 tokens of a tile and 128 columns at a time; a block
-// takes a run of them. Four warps bring V (split) and B (widened) chunk by chunk
-// of 32 ranks into a ring and issue the products, into two accumulators in turn;
-// sixteen add base, which they request an item ahead, and store y. Bound by the
-// bytes of base and y.
-constexpr int LE_STAGE = 3 * LR_HALF, LE_NST = 4, LE_FEED = 128, LE_THREADS = LE_FEED + 512;
+// takes a run of them. Four warps bring B (widened) into a ring, by 64 ranks, and
+// V (split), which stays for all columns of a tile, and issue the products, into
+// two accumulators in turn; sixteen add base, which they request an item ahead,
+// and store y. Bound by the bytes of base and y. Ranks above 128 leave no room for
+// V: there (not KEEP) the ring has it too, by 32 ranks. (So for all ranks, the
+// four warps were what bound it: 64 us for the prompts of 6.6 thousand tokens.)
+constexpr int LE_STAGE = 3 * LR_HALF, LE_NST = 4, LE_FEED = 128, LE_THREADS = LE_FEED + 512, LE_ASK = 4;
 
-template <int DT>
+template <int DT, bool KEEP>
 __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[LE_NST + 4];
@@ -592,122 +644,169 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
   const int n_col = (a.N + 127) / 128;
   const long long total = (long long)*a.n_tiles * n_col;
   const long long i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int t0 = (int)(i0 / n_col), c0 = (int)(i0 - (long long)t0 * n_col);
   Waits ws;
   if (w < LE_FEED / 32) {
     const uint32_t id = idesc_tf32(128);
-    int used = 0, accs = 0;
-    uint4 v[8], wt[4];
-    // the chunk of 32 ranks from c on of item i
-    auto fetch = [&](const int4 &tile, int n0, int c) {
-      const int rows = tile.z & 0xFFFF, r8 = ((tile.z >> 16) + 7) & ~7;
+    // KEEP: V, 32 ranks of it after another (high, low), then stages of two parts of B
+    const uint32_t ring = KEEP ? base + a.R32 / 32 * (2 * LR_HALF) : base;
+    const int nst = KEEP ? (LR_SMEM - 1024 - a.R32 / 32 * (2 * LR_HALF)) / (2 * LR_HALF) < LE_NST ? 2 : LE_NST : LE_NST;
+    constexpr int STEP = KEEP ? 64 : 32, PARTS = STEP / 32, STAGE = KEEP ? 2 * LR_HALF : LE_STAGE;
+    int used = 0, accs = 0, st = 0, lap = 0;
+    uint4 v[8], wt[PARTS][4];
+    auto fetch_v = [&](const int4 &tile, int c) {
+      const int rows = tile.z & 0xFFFF;
+      const float *p = a.v + (long long)tile.y * a.R32 + c + tid % 8 * 4;
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        const int r = tid / 8 + 16 * j;
         v[j] = make_uint4(0, 0, 0, 0);
-        if (r < rows) v[j] = *reinterpret_cast<const uint4 *>(a.v + (long long)(tile.y + r) * a.R32 + c + tid % 8 * 4);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int r = tid / 4 + 32 * j, e = c + tid % 4 * 8;
-        wt[j] = make_uint4(0, 0, 0, 0);
-        if (n0 + r < a.N && e < r8) wt[j] = *reinterpret_cast<const uint4 *>(a.B + (long long)tile.x * a.b_slot + (long long)(n0 + r) * r8 + e);
+        if (tid / 8 + 16 * j < rows) v[j] = *reinterpret_cast<const uint4 *>(p + (tid / 8 + 16 * j) * a.R32);
       }
     };
-    int at_tile = -1;
-    int4 tile = make_int4(0, 0, 0, 0);
-    auto load_tile = [&](long long i) {
-      const int t = (int)(i / n_col);
-      if (t != at_tile) at_tile = t, tile = a.tiles[t];
-    };
-    long long i = i0;
-    int c = 0;
-    auto skip = [&]() {  // to an item with products
-      for (; i < i1; i++) {
-        load_tile(i);
-        if (tile.z >> 16) break;
-        i = (long long)(at_tile + 1) * n_col - 1;  // (a tile without: all of its columns)
-      }
-    };
-    skip();
-    if (i < i1) fetch(tile, (int)(i % n_col) * 128, 0);
-    while (i < i1) {
-      const int r32 = ((tile.z >> 16) + 31) & ~31, buf = accs & 1, st = used % LE_NST;
-      const bool first = c == 0, last = c + 32 >= r32;
-      if (used >= LE_NST) ws.wait(empty(st), (used / LE_NST - 1) & 1);
-      const uint32_t at = base + st * LE_STAGE;
+    auto put_v = [&](uint32_t at) {
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const uint32_t o = sw128(tid / 8 + 16 * j, tid % 8);
         put_split<true>(at + o, at + LR_HALF + o, v[j]);
       }
+    };
+    // STEP ranks from c on of B's rows
+    auto fetch = [&](const int4 &tile, int n0, int c) {
+      const int r8 = ((tile.z >> 16) + 7) & ~7;
+      const uint16_t *p = a.B + (long long)tile.x * a.b_slot + (long long)(n0 + tid / 4) * r8 + c + tid % 4 * 8;
 #pragma unroll
-      for (int j = 0; j < 4; j++) put_wide<DT>(at + 2 * LR_HALF, tid / 4 + 32 * j, tid % 4, wt[j]);
+      for (int h = 0; h < PARTS; h++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          wt[h][j] = make_uint4(0, 0, 0, 0);
+          if (n0 + tid / 4 + 32 * j < a.N && c + 32 * h + tid % 4 * 8 < r8)
+            wt[h][j] = *reinterpret_cast<const uint4 *>(p + (long long)32 * j * r8 + 32 * h);
+        }
+      if (!KEEP) fetch_v(tile, c);
+    };
+    int t = t0, col = c0, c = 0, kept = -1;  // tile, its part of the columns, of its ranks; the tile whose V is kept
+    long long i = i0;
+    int4 tile = make_int4(0, 0, 0, 0);
+    if (i < i1) tile = a.tiles[t];
+    auto skip = [&]() {  // to an item with products
+      while (i < i1 && (col == n_col || !(tile.z >> 16))) {
+        i += n_col - col, col = 0;  // (a tile without: all of its columns)
+        if (i < i1) tile = a.tiles[++t];
+      }
+    };
+    skip();
+    if (i < i1) fetch(tile, col * 128, 0);
+    // base for the other warps: a tile's rows lie far apart, so L2 is asked for
+    // each row's part (thread: row) LE_ASK items ahead
+    const float *from = a.base ? a.base : a.y;
+    const int from_stride = a.base ? a.base_stride : a.y_stride;
+    long long pi = i0;
+    int pt = t0 - 1, pcol = n_col, ptok = -1;
+    auto ask = [&](long long until) {
+      for (; pi < min(until, i1); pi++, pcol++) {
+        if (pcol == n_col || pi == i0) {
+          pt++, pcol = pi == i0 ? c0 : 0;
+          const int4 p = a.tiles[pt];
+          ptok = tid < (p.z & 0xFFFF) ? a.perm[p.y + tid] : -1;
+        }
+        if (ptok >= 0 && a.wide) prefetch_l2(from + (long long)ptok * from_stride + pcol * 128, (uint32_t)min(128, a.N - pcol * 128) * 4);
+      }
+    };
+    ask(i0 + LE_ASK);
+    while (i < i1) {
+      const int r32 = ((tile.z >> 16) + 31) & ~31, buf = accs & 1, c_now = c;
+      const bool first = c == 0, last = c + STEP >= r32;
+      if (KEEP && t != kept) {
+        // the products with the last tile's V are done
+        if (used) ws.wait(empty(st == 0 ? nst - 1 : st - 1), (st == 0 ? lap - 1 : lap) & 1);
+        for (int e = 0; e < r32; e += 32) {
+          fetch_v(tile, e);
+          put_v(base + e / 32 * (2 * LR_HALF));
+        }
+        kept = t;
+      }
+      if (lap > 0) ws.wait(empty(st), (lap - 1) & 1);
+      const uint32_t at = ring + st * STAGE;
+      if (!KEEP) put_v(at);
+#pragma unroll
+      for (int h = 0; h < PARTS; h++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) put_wide<DT>(at + (KEEP ? h : 2) * LR_HALF, tid / 4 + 32 * j, tid % 4, wt[h][j]);
       // the next chunk under way
       if (last) {
-        i++, c = 0;
+        i++, col++, c = 0;
+        ask(i + LE_ASK);
         skip();
       } else {
-        c += 32;
+        c += STEP;
       }
-      if (i < i1) fetch(tile, (int)(i % n_col) * 128, c);
+      if (i < i1) fetch(tile, col * 128, c);
       if (first && accs >= 2) ws.wait(acc_empty(buf), (accs / 2 - 1) & 1);
       fence_proxy_async_smem();
       named_sync<LE_FEED>(1);
       if (w == 0) {
-        const uint32_t sa = base + __shfl_sync(0xffffffffu, st, 0) * LE_STAGE, d = tmem + __shfl_sync(0xffffffffu, buf, 0) * 128;
-        const uint64_t dh = desc_sw128(sa, 0), dl = desc_sw128(sa + LR_HALF, 0), dw = desc_sw128(sa + 2 * LR_HALF, 0);
-        const uint32_t more = __shfl_sync(0xffffffffu, (int)!first, 0), ends = __shfl_sync(0xffffffffu, (int)last, 0);
+        const int us = __shfl_sync(0xffffffffu, st, 0), uc = __shfl_sync(0xffffffffu, c_now, 0), ur = __shfl_sync(0xffffffffu, r32, 0);
+        const uint32_t sa = ring + us * STAGE, d = tmem + __shfl_sync(0xffffffffu, buf, 0) * 128;
+        const uint32_t ends = __shfl_sync(0xffffffffu, (int)last, 0);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) umma_tf32(d, dh + 2 * q, dw + 2 * q, id, more || q != 0);
+          for (int h = 0; h < PARTS; h++) {
+            if (uc + 32 * h >= ur) break;
+            const uint32_t va = KEEP ? base + (uc / 32 + h) * (2 * LR_HALF) : sa;
+            const uint64_t dh = desc_sw128(va, 0), dl = desc_sw128(va + LR_HALF, 0), dw = desc_sw128(sa + (KEEP ? h : 2) * LR_HALF, 0);
 #pragma unroll
-          for (int q = 0; q < 4; q++) umma_tf32(d, dl + 2 * q, dw + 2 * q, id, 1);
-          umma_commit(empty(st));
+            for (int q = 0; q < 4; q++) umma_tf32(d, dh + 2 * q, dw + 2 * q, id, uc != 0 || h != 0 || q != 0);
+#pragma unroll
+            for (int q = 0; q < 4; q++) umma_tf32(d, dl + 2 * q, dw + 2 * q, id, 1);
+          }
+          umma_commit(empty(us));
           if (ends) umma_commit(acc_full(buf));
         }
         __syncwarp();
       }
       used++, accs += last;
+      if (++st == nst) st = 0, lap++;
     }
     // nothing is in flight when the block leaves
-    if (used) ws.wait(empty((used - 1) % LE_NST), ((used - 1) / LE_NST) & 1);
+    if (used) ws.wait(empty(st == 0 ? nst - 1 : st - 1), (st == 0 ? lap - 1 : lap) & 1);
   } else {
     const int q = w & 3, g = (w - LE_FEED / 32) >> 2;  // the warp's quarter of the rows, of the columns
-    const float *from = a.base ? a.base : a.y;
-    const long long from_stride = a.base ? a.base_stride : a.y_stride;
-    int at_tile = -1, tok = -1, accs = 0;
-    int4 tile = make_int4(0, 0, 0, 0);
     // this lane's pieces of y: row (lane & 24) + j of the warp's 32, 16 bytes at
     // piece lane % 8 of its 32 columns
-    float4 b[8];
-    auto load = [&](long long i) {
-      const int t = (int)(i / n_col), n = (int)(i % n_col) * 128 + 32 * g + 4 * (lane & 7);
-      if (t != at_tile) {
-        at_tile = t, tile = a.tiles[t];
-        const int row = 32 * q + lane;
-        tok = row < (tile.z & 0xFFFF) ? a.perm[tile.y + row] : -1;
-      }
+    const float *from = (a.base ? a.base : a.y) + 32 * g + 4 * (lane & 7);
+    float *to = a.y + 32 * g + 4 * (lane & 7);
+    const int from_stride = a.base ? a.base_stride : a.y_stride;
+    int accs = 0, t = t0, col = c0, tok[8];  // tile, its part of the columns; tokens of the lane's rows
+    int4 tile = make_int4(0, 0, 0, 0);
+    auto load_tile = [&]() {
+      tile = a.tiles[t];
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        const int t_j = __shfl_sync(0xffffffffu, tok, (lane & 24) + j);
+        const int row = 32 * q + (lane & 24) + j;
+        tok[j] = row < (tile.z & 0xFFFF) ? a.perm[tile.y + row] : -1;
+      }
+    };
+    float4 b[8];
+    auto load = [&]() {
+      const int n = col * 128, left = a.N - n - 32 * g - 4 * (lane & 7);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
         b[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (t_j < 0) continue;
-        const float *p = from + (long long)t_j * from_stride + n;
+        if (tok[j] < 0) continue;
+        const float *p = from + (long long)tok[j] * from_stride + n;
         if (a.wide) {
-          if (n < a.N) b[j] = __ldcs(reinterpret_cast<const float4 *>(p));
+          if (left > 0) b[j] = __ldcs(reinterpret_cast<const float4 *>(p));
         } else {
-          if (n < a.N) b[j].x = p[0];
-          if (n + 1 < a.N) b[j].y = p[1];
-          if (n + 2 < a.N) b[j].z = p[2];
-          if (n + 3 < a.N) b[j].w = p[3];
+          if (left > 0) b[j].x = p[0];
+          if (left > 1) b[j].y = p[1];
+          if (left > 2) b[j].z = p[2];
+          if (left > 3) b[j].w = p[3];
         }
       }
     };
-    if (i0 < i1) load(i0);
+    if (i0 < i1) load_tile(), load();
     for (long long i = i0; i < i1; i++) {
-      const int n = (int)(i % n_col) * 128 + 32 * g + 4 * (lane & 7), mine = tok;
-      uint32_t u[32];
       if (tile.z >> 16) {
         const int buf = accs & 1;
         ws.wait(acc_full(buf), (accs / 2) & 1);
@@ -720,6 +819,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buf));
         accs++;
+        uint32_t u[32];
 #pragma unroll
         for (int e = 0; e < 32; e++) u[e] = __float_as_uint(v[e]);
         transpose8(u);
@@ -729,21 +829,26 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
           b[j].z += __uint_as_float(u[4 * j + 2]), b[j].w += __uint_as_float(u[4 * j + 3]);
         }
       }
+      const int n = col * 128, left = a.N - n - 32 * g - 4 * (lane & 7);
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        const int t_j = __shfl_sync(0xffffffffu, mine, (lane & 24) + j);
-        if (t_j < 0) continue;
-        float *p = a.y + (long long)t_j * a.y_stride + n;
+        if (tok[j] < 0) continue;
+        float *p = to + (long long)tok[j] * a.y_stride + n;
         if (a.wide) {
-          if (n < a.N) __stcs(reinterpret_cast<float4 *>(p), b[j]);
+          if (left > 0) __stcs(reinterpret_cast<float4 *>(p), b[j]);
         } else {
-          if (n < a.N) p[0] = b[j].x;
-          if (n + 1 < a.N) p[1] = b[j].y;
-          if (n + 2 < a.N) p[2] = b[j].z;
-          if (n + 3 < a.N) p[3] = b[j].w;
+          if (left > 0) p[0] = b[j].x;
+          if (left > 1) p[1] = b[j].y;
+          if (left > 2) p[2] = b[j].z;
+          if (left > 3) p[3] = b[j].w;
         }
       }
-      if (i + 1 < i1) load(i + 1);
+      if (i + 1 == i1) break;
+      if (++col == n_col) {
+        col = 0, t++;
+        load_tile();
+      }
+      load();
     }
   }
   if (!ws.ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
@@ -799,14 +904,15 @@ struct AdaptFns {
   const void *token, *shrink, *expand;
 };
 template <int DT, bool F32>
-AdaptFns fns_of(bool two) {
-  return {(const void *)k_adapt_token<DT, F32>, two ? (const void *)k_adapt_shrink<DT, F32, 2> : (const void *)k_adapt_shrink<DT, F32, 1>,
-          (const void *)k_adapt_expand<DT>};
+AdaptFns fns_of(int r32) {
+  const void *shrink = r32 <= 64 ? (const void *)k_adapt_shrink<DT, F32, 2> : r32 <= 128 ? (const void *)k_adapt_shrink<DT, F32, 4>
+                                                                                        : (const void *)k_adapt_shrink<DT, F32, 8>;
+  return {(const void *)k_adapt_token<DT, F32>, shrink,
+          r32 <= 128 ? (const void *)k_adapt_expand<DT, true> : (const void *)k_adapt_expand<DT, false>};
 }
 AdaptFns adapt_fns(int dtype, bool f32, int r32) {
   constexpr int B = DS4MOE_DT_BF16, F = DS4MOE_DT_F16;
-  const bool two = r32 > 128;
-  return dtype == B ? f32 ? fns_of<B, true>(two) : fns_of<B, false>(two) : f32 ? fns_of<F, true>(two) : fns_of<F, false>(two);
+  return dtype == B ? f32 ? fns_of<B, true>(r32) : fns_of<B, false>(r32) : f32 ? fns_of<F, true>(r32) : fns_of<F, false>(r32);
 }
 
 cudaError_t launch_cluster(const void *fn, int grid, int cluster, int threads, size_t smem, cudaStream_t s, void **args) {
@@ -921,7 +1027,7 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   if (x_dtype != DS4MOE_DT_F32 && x_dtype != h->dtype) return DS4MOE_ERR_INVALID_ARG;
   if (n_tok == 0) return DS4MOE_OK;
   const bool f32 = x_dtype == DS4MOE_DT_F32;
-  const long long K = h->K, N = h->N, lim = 1ll << 39;
+  const long long K = h->K, N = h->N, lim = 1ll << 31;  // strides are 32-bit numbers on the device
   if (n_tok == 1) x_stride = K, base_stride = y_stride = N;
   if (x_stride < K || x_stride >= lim || x_stride % (f32 ? 4 : 8) || ((uintptr_t)x & 15)) return DS4MOE_ERR_INVALID_ARG;
   if (y_stride < N || y_stride >= lim || ((uintptr_t)y & 3)) return DS4MOE_ERR_INVALID_ARG;
@@ -933,7 +1039,7 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   if (base && rows_overlap(y, y_bytes, base, (n * base_stride + N) * 4)) return DS4MOE_ERR_INVALID_ARG;
   AdaptArgs a = {};
   a.N = h->N, a.K = h->K, a.slots = h->slots, a.T = n_tok, a.R32 = h->R32, a.b_slot = h->b_slot;
-  a.x = x, a.x_stride = x_stride, a.base = base, a.base_stride = base_stride, a.y = y, a.y_stride = y_stride;
+  a.x = x, a.x_stride = (int)x_stride, a.base = base, a.base_stride = (int)base_stride, a.y = y, a.y_stride = (int)y_stride;
   a.slot_of = slots, a.info = h->info, a.A = h->A, a.B = h->B;
   a.perm = h->perm, a.tiles = h->tiles, a.n_tiles = h->n_tiles, a.v = h->v, a.err = h->err;
   a.wide = N % 4 == 0 && y_stride % 4 == 0 && !((uintptr_t)y & 15) && (!base || (base_stride % 4 == 0 && !((uintptr_t)base & 15)));
