@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "internal.h"
@@ -161,30 +162,37 @@ __global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
     reinterpret_cast<float4 *>(s_x)[2 * u] = lo, reinterpret_cast<float4 *>(s_x)[2 * u + 1] = hi;
   }
   __syncthreads();
-  // four rows of A per warp at a time
-  for (int r0 = 4 * w; r0 < rank; r0 += 32) {
-    float sum[4] = {};
-    const uint4 *p = reinterpret_cast<const uint4 *>(A + (long long)r0 * a.K) + u0;
-    for (int u = lane; u < nu; u += 32) {
-      float x[8];
-      *reinterpret_cast<float4 *>(x) = reinterpret_cast<const float4 *>(s_x)[2 * u];
-      *reinterpret_cast<float4 *>(x + 4) = reinterpret_cast<const float4 *>(s_x)[2 * u + 1];
+  // J rows of A per warp at a time (rows past the rank are zeros up to a multiple of 32)
+  auto rows_of_a = [&](auto per_warp) {
+    constexpr int J = decltype(per_warp)::value;
+    for (int r0 = J * w; r0 < rank; r0 += 8 * J) {
+      float sum[J] = {};
+      const uint4 *p = reinterpret_cast<const uint4 *>(A + (long long)r0 * a.K) + u0;
+#pragma unroll 2
+      for (int u = lane; u < nu; u += 32) {
+        float x[8];
+        *reinterpret_cast<float4 *>(x) = reinterpret_cast<const float4 *>(s_x)[2 * u];
+        *reinterpret_cast<float4 *>(x + 4) = reinterpret_cast<const float4 *>(s_x)[2 * u + 1];
 #pragma unroll
-      for (int j = 0; j < 4; j++) sum[j] = dot8<DT>(p[(long long)j * (a.K / 8) + u], x, sum[j]);  // (rows past the rank are zeros)
+        for (int j = 0; j < J; j++) sum[j] = dot8<DT>(p[(long long)j * (a.K / 8) + u], x, sum[j]);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < J; j++) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < J; j++) s_part[r0 + j] = sum[j];
+      }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < 4; j++) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-    if (lane == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; j++) s_part[r0 + j] = sum[j];
-    }
-  }
+  };
+  if (rank <= 16) rows_of_a(std::integral_constant<int, 2>());
+  else if (rank <= 32) rows_of_a(std::integral_constant<int, 4>());
+  else rows_of_a(std::integral_constant<int, 8>());
   cluster_arrive();
   cluster_wait();
   const float scale = __int_as_float(in.y);
-  for (int r = tid; r < r8; r += 256) {
+  for (int r = tid; r < r8; r += 256) {  // (r8 is at most 256)
     float v = 0.0f;
     if (r < rank)
 #pragma unroll
@@ -193,12 +201,46 @@ __global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
   }
   __syncthreads();
   cluster_arrive();  // the others' sums are read: they may leave
-  for (int n = n0 + tid; n < n1; n += 256) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(B + (long long)n * r8);
-    float sum = 0.0f;
-    for (int u = 0; u < r8 / 8; u++) sum = dot8<DT>(p[u], s_v + 8 * u, sum);
-    y[n] = base[n] + sum;
-  }
+  // U lanes per row of B, so that a load takes whole lines: the lane's piece of
+  // eight ranks is the same for all rows. A warp takes 32 rows, 32 / U at a time,
+  // of which lane l ends up with row (l % U) * (32 / U) + l / U.
+  const int units = r8 / 8;
+  auto rows_of_b = [&](auto lanes) {
+    constexpr int U = decltype(lanes)::value, G = 32 / U;
+    const int u = lane % U, g = lane / U;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = u < units ? s_v[8 * u + e] : 0.0f;
+    for (int r0 = n0 + 32 * w; r0 < n1; r0 += 256) {
+      const int mine = r0 + u * G + g;
+      const float from = mine < n1 ? base[mine] : 0.0f;
+      float keep = 0.0f;
+#pragma unroll
+      for (int b = 0; b < U; b += 8) {
+        uint4 wt[U < 8 ? U : 8];
+#pragma unroll
+        for (int k = 0; k < (U < 8 ? U : 8); k++) {
+          const int n = r0 + (b + k) * G + g;
+          wt[k] = make_uint4(0, 0, 0, 0);
+          if (n < n1 && u < units) wt[k] = *reinterpret_cast<const uint4 *>(B + (long long)n * r8 + 8 * u);
+        }
+#pragma unroll
+        for (int k = 0; k < (U < 8 ? U : 8); k++) {
+          float sum = dot8<DT>(wt[k], v, 0.0f);
+#pragma unroll
+          for (int o = U / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (b + k == u) keep = sum;
+        }
+      }
+      if (mine < n1) y[mine] = from + keep;
+    }
+  };
+  if (units == 1) rows_of_b(std::integral_constant<int, 1>());
+  else if (units == 2) rows_of_b(std::integral_constant<int, 2>());
+  else if (units <= 4) rows_of_b(std::integral_constant<int, 4>());
+  else if (units <= 8) rows_of_b(std::integral_constant<int, 8>());
+  else if (units <= 16) rows_of_b(std::integral_constant<int, 16>());
+  else rows_of_b(std::integral_constant<int, 32>());
   cluster_wait();
 }
 
