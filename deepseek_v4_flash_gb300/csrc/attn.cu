@@ -198,9 +198,12 @@ __device__ __forceinline__ bool append_page(const KvView &kv, int b, long long p
 // same launch, the queries. Pair (x, y) of a head at position p becomes
 //   (x cos - y sin, y cos + x sin),  angle p * inv_freq[i],
 // in 32 bits, rounded once. A thread takes 16 elements (two pieces of 8, so
-// that it holds both halves of its pairs) of `per` rows of one token: the
-// angles' sines are computed once for all of them. Bound by the bytes: 12291
-// tokens of 32 + 2 x 8 heads of 128 from fp32: see DESIGN's table.
+// that it holds both halves of its pairs) of `per` rows of one token; a block
+// computes the sines of its tokens' angles once, for all their heads (every
+// thread its own eight: 12291 tokens of 32 + 2 x 8 heads of 128 from fp32 81 us
+// instead of 74, 1064 rows of 48 heads of 64 13.0 us instead of 9.0). Bound by the
+// bytes: 6.1 TB/s, of 6.8 for a copy. Rows one at a time: four of them in
+// registers took 151 of these and 104 us, for fewer blocks fit.
 //
 // Angles: p * inv_freq / 2 pi in turns, modulo one turn, in 64-bit fixed point
 // (a phase accumulator): the product with the integer p wraps by itself. An
@@ -249,9 +252,14 @@ __device__ __forceinline__ void rope_angle(float f, int p, float scale, float &c
   if (q & 2) s = -s;
 }
 
-template <int DT, bool F32, int U>
+// Angles that a block's 128 threads need at most: its tokens (128 / (D / 16) and
+// two begun ones) times rot / 2.
+constexpr int AR_ANGLES = 1024 + 512;
+
+template <int DT, bool F32>
 __global__ void __launch_bounds__(128) k_append_rope(const RopeArgs a) {
   __shared__ int s_cu[AP_SEQS + 1];
+  __shared__ __align__(16) float s_cos[AR_ANGLES], s_sin[AR_ANGLES];
   pdl_launch_dependents();
   pdl_wait();
   const long long idx = (long long)blockIdx.x * 128 + threadIdx.x, rest = idx >> a.ish;
@@ -269,29 +277,37 @@ __global__ void __launch_bounds__(128) k_append_rope(const RopeArgs a) {
     if (ea >= a.off) ea += a.rot;
     if (eb >= a.off) eb += a.rot;
   }
+  int angle0 = 0;
   constexpr int W = F32 ? 2 : 1;  // 16-byte words of a piece
-  uint4 x[U][2 * W];
-  auto load = [&](int r0) {
+  uint4 x[2 * W];
+  auto load = [&](int r) {
+    if (r >= r1) return;
+    const char *p;
+    if (r < a.nq) p = (const char *)a.q + ((long long)t * a.q_stride + (long long)r * a.D) * (F32 ? 4 : 2);
+    else if (r < a.nq + a.n_kv) p = (const char *)a.k + ((long long)t * a.k_stride + (long long)(r - a.nq) * a.D) * (F32 ? 4 : 2);
+    else p = (const char *)a.v + ((long long)t * a.v_stride + (long long)(r - a.nq - a.n_kv) * a.D) * (F32 ? 4 : 2);
 #pragma unroll
-    for (int j = 0; j < U; j++) {
-      const int r = r0 + j;
-      if (r >= r1) continue;
-      const char *p;
-      if (r < a.nq) p = (const char *)a.q + ((long long)t * a.q_stride + (long long)r * a.D) * (F32 ? 4 : 2);
-      else if (r < a.nq + a.n_kv) p = (const char *)a.k + ((long long)t * a.k_stride + (long long)(r - a.nq) * a.D) * (F32 ? 4 : 2);
-      else p = (const char *)a.v + ((long long)t * a.v_stride + (long long)(r - a.nq - a.n_kv) * a.D) * (F32 ? 4 : 2);
-#pragma unroll
-      for (int w = 0; w < W; w++) {
-        x[j][w] = reinterpret_cast<const uint4 *>(p + ea * (F32 ? 4 : 2))[w];
-        x[j][W + w] = reinterpret_cast<const uint4 *>(p + eb * (F32 ? 4 : 2))[w];
-      }
+    for (int w = 0; w < W; w++) {
+      x[w] = reinterpret_cast<const uint4 *>(p + ea * (F32 ? 4 : 2))[w];
+      x[W + w] = reinterpret_cast<const uint4 *>(p + eb * (F32 ? 4 : 2))[w];
     }
   };
   load(sl * a.per);
   const int *cu = append_bounds(a.cu_q, a.n_seq, a.n_tok, s_cu, a.err);
   int b, page = 0, row = 0;
   long long pos;
-  if (sl * a.per >= r1 || !append_seq(a.kv_len, cu, a.n_seq, a.n_new, t, b, pos)) return;
+  {
+    // angles by token and frequency
+    const int half = a.rot >> 1, t0 = (int)min(((long long)blockIdx.x * 128 >> a.ish) / a.slices, (long long)a.n_tok);
+    const int t1 = (int)min((((long long)blockIdx.x * 128 + 127) >> a.ish) / a.slices + 1, (long long)a.n_tok);
+    for (int e = threadIdx.x; e < (t1 - t0) * half; e += 128) {
+      const int k = e / half;
+      if (append_seq(a.kv_len, cu, a.n_seq, a.n_new, t0 + k, b, pos)) rope_angle(a.inv_freq[e - k * half], (int)pos, a.scale, s_cos[e], s_sin[e]);
+    }
+    __syncthreads();
+    if (sl * a.per >= r1 || !append_seq(a.kv_len, cu, a.n_seq, a.n_new, t, b, pos)) return;
+    if (turns) angle0 = (t - t0) * half + 8 * i;
+  }
   bool store = true;  // the cache has a place for the token
   if (r1 > a.nq) {
     store = append_page(a.kv, b, pos, a.err, page);
@@ -299,60 +315,56 @@ __global__ void __launch_bounds__(128) k_append_rope(const RopeArgs a) {
   }
   float cs[8], sn[8];
   if (turns) {
-    const float4 f0 = reinterpret_cast<const float4 *>(a.inv_freq + 8 * i)[0], f1 = reinterpret_cast<const float4 *>(a.inv_freq + 8 * i)[1];
-    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-    for (int e = 0; e < 8; e++) rope_angle(f[e], (int)pos, a.scale, cs[e], sn[e]);
-  }
-  for (int r0 = sl * a.per; r0 < r1; r0 += U) {
-    if (r0 != sl * a.per) load(r0);
-#pragma unroll
-    for (int j = 0; j < U; j++) {
-      const int r = r0 + j;
-      if (r >= r1) continue;
-      const bool is_q = r < a.nq, is_v = r >= a.nq + a.n_kv;
-      uint16_t *dst;
-      if (is_q) {
-        dst = a.q_out + (long long)t * a.qo_stride + (long long)r * a.D;
-      } else {
-        if (!store) continue;
-        dst = is_v ? const_cast<uint16_t *>(a.kv.v) + (long long)page * a.kv.v_page + (long long)row * a.kv.v_row + (long long)(r - a.nq - a.n_kv) * a.kv.v_head
-                   : const_cast<uint16_t *>(a.kv.k) + (long long)page * a.kv.k_page + (long long)row * a.kv.k_row + (long long)(r - a.nq) * a.kv.k_head;
-      }
-      if (!F32 && (is_v || !turns)) {  // bits are copied
-        *reinterpret_cast<uint4 *>(dst + ea) = x[j][0];
-        *reinterpret_cast<uint4 *>(dst + eb) = x[j][W];
-        continue;
-      }
-      float v[16];
-      const uint32_t *u = reinterpret_cast<const uint32_t *>(x[j]);
-      if (F32) {
-#pragma unroll
-        for (int e = 0; e < 16; e++) v[e] = __uint_as_float(u[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const float2 y = Half16<DT>::up(u[e]);
-          v[2 * e] = y.x, v[2 * e + 1] = y.y;
-        }
-      }
-      if (turns && !is_v) {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-          if (a.interleaved) {
-            const float p = v[2 * e], q = v[2 * e + 1];
-            v[2 * e] = fmaf(p, cs[e], -(q * sn[e])), v[2 * e + 1] = fmaf(q, cs[e], p * sn[e]);
-          } else {
-            const float p = v[e], q = v[8 + e];
-            v[e] = fmaf(p, cs[e], -(q * sn[e])), v[8 + e] = fmaf(q, cs[e], p * sn[e]);
-          }
-        }
-      }
-      *reinterpret_cast<uint4 *>(dst + ea) = make_uint4(Half16<DT>::down(v[0], v[1]), Half16<DT>::down(v[2], v[3]),
-                                                        Half16<DT>::down(v[4], v[5]), Half16<DT>::down(v[6], v[7]));
-      *reinterpret_cast<uint4 *>(dst + eb) = make_uint4(Half16<DT>::down(v[8], v[9]), Half16<DT>::down(v[10], v[11]),
-                                                        Half16<DT>::down(v[12], v[13]), Half16<DT>::down(v[14], v[15]));
+    for (int e = 0; e < 8; e += 4) {
+      *reinterpret_cast<float4 *>(cs + e) = *reinterpret_cast<const float4 *>(s_cos + angle0 + e);
+      *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(s_sin + angle0 + e);
     }
+  }
+  for (int r = sl * a.per; r < r1; r++) {
+    if (r != sl * a.per) load(r);
+    const bool is_q = r < a.nq, is_v = r >= a.nq + a.n_kv;
+    uint16_t *dst;
+    if (is_q) {
+      dst = a.q_out + (long long)t * a.qo_stride + (long long)r * a.D;
+    } else {
+      if (!store) continue;
+      dst = is_v ? const_cast<uint16_t *>(a.kv.v) + (long long)page * a.kv.v_page + (long long)row * a.kv.v_row + (long long)(r - a.nq - a.n_kv) * a.kv.v_head
+                 : const_cast<uint16_t *>(a.kv.k) + (long long)page * a.kv.k_page + (long long)row * a.kv.k_row + (long long)(r - a.nq) * a.kv.k_head;
+    }
+    if (!F32 && (is_v || !turns)) {  // bits are copied
+      *reinterpret_cast<uint4 *>(dst + ea) = x[0];
+      *reinterpret_cast<uint4 *>(dst + eb) = x[W];
+      continue;
+    }
+    float v[16];
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(x);
+    if (F32) {
+#pragma unroll
+      for (int e = 0; e < 16; e++) v[e] = __uint_as_float(u[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const float2 y = Half16<DT>::up(u[e]);
+        v[2 * e] = y.x, v[2 * e + 1] = y.y;
+      }
+    }
+    if (turns && !is_v) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        if (a.interleaved) {
+          const float p = v[2 * e], q = v[2 * e + 1];
+          v[2 * e] = fmaf(p, cs[e], -(q * sn[e])), v[2 * e + 1] = fmaf(q, cs[e], p * sn[e]);
+        } else {
+          const float p = v[e], q = v[8 + e];
+          v[e] = fmaf(p, cs[e], -(q * sn[e])), v[8 + e] = fmaf(q, cs[e], p * sn[e]);
+        }
+      }
+    }
+    *reinterpret_cast<uint4 *>(dst + ea) = make_uint4(Half16<DT>::down(v[0], v[1]), Half16<DT>::down(v[2], v[3]),
+                                                      Half16<DT>::down(v[4], v[5]), Half16<DT>::down(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(dst + eb) = make_uint4(Half16<DT>::down(v[8], v[9]), Half16<DT>::down(v[10], v[11]),
+                                                      Half16<DT>::down(v[12], v[13]), Half16<DT>::down(v[14], v[15]));
   }
 }
 
@@ -415,13 +427,10 @@ const void *append_fn(bool bf, bool f32, bool two) {
   return !f32 ? (const void *)k_kv_append<B, false, 1> : bf ? (const void *)k_kv_append<B, true, 1> : (const void *)k_kv_append<F, true, 1>;
 }
 
-const void *rope_fn(bool bf, bool f32, bool four) {
+const void *rope_fn(bool bf, bool f32) {
   constexpr int B = DS4MOE_DT_BF16, F = DS4MOE_DT_F16;
-  if (four)
-    return bf ? f32 ? (const void *)k_append_rope<B, true, 4> : (const void *)k_append_rope<B, false, 4>
-              : f32 ? (const void *)k_append_rope<F, true, 4> : (const void *)k_append_rope<F, false, 4>;
-  return bf ? f32 ? (const void *)k_append_rope<B, true, 1> : (const void *)k_append_rope<B, false, 1>
-            : f32 ? (const void *)k_append_rope<F, true, 1> : (const void *)k_append_rope<F, false, 1>;
+  return bf ? f32 ? (const void *)k_append_rope<B, true> : (const void *)k_append_rope<B, false>
+            : f32 ? (const void *)k_append_rope<F, true> : (const void *)k_append_rope<F, false>;
 }
 
 // Whether [p, p + n) and [q, q + m) share a byte.
@@ -668,9 +677,10 @@ ds4moe_status ds4moe_kv_append_rope(ds4moe_attn *h, const ds4moe_kv_cache *cache
   while (16 << a.ish < D) a.ish++;
   a.rot = rope->rot_dim, a.off = rope->offset, a.interleaved = rope->interleaved;
   a.inv_freq = rope->inv_freq, a.scale = rope->scale, a.err = h->err;
+  // More than one wave of threads: six rows of a token per thread (12291 tokens of
+  // 48 rows 74 us; one 81, two 81, four 75, sixteen 76); else one.
   const long long items = (long long)n_tok * a.rows << a.ish;
-  const bool four = items > (long long)h->n_sm * 2048;
-  a.per = four ? 8 : 1;
+  a.per = items > (long long)h->n_sm * 2048 ? 6 : 1;
   a.slices = (a.rows + a.per - 1) / a.per;
   cudaError_t e = cudaSuccess;
   if (cu_q && n_seq > AP_SEQS) {
@@ -682,7 +692,7 @@ ds4moe_status ds4moe_kv_append_rope(ds4moe_attn *h, const ds4moe_kv_cache *cache
   }
   void *args[] = {&a};
   const long long threads = (long long)n_tok * a.slices << a.ish;
-  e = launch_pdl(rope_fn(h->d.dtype == DS4MOE_DT_BF16, f32, four), dim3((unsigned)((threads + 127) / 128)), dim3(128), 0,
+  e = launch_pdl(rope_fn(h->d.dtype == DS4MOE_DT_BF16, f32), dim3((unsigned)((threads + 127) / 128)), dim3(128), 0,
                  (cudaStream_t)stream, args, true);
   h->launches++;
   return at_status(e);
