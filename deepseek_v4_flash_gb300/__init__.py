@@ -21,6 +21,9 @@ import ctypes
 import os
 from dataclasses import dataclass
 
+import torch
+from torch import _C
+
 from . import build as _build
 
 ABI_VERSION = 1
@@ -163,7 +166,6 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        from torch import _C
         # torch.cuda.current_stream() without building a Stream object (a
         # quarter of a small call's host time)
         return ctypes.c_void_p(_C._cuda_getCurrentRawStream(_C._cuda_getDevice()))
@@ -271,7 +273,6 @@ class Layer:
 
     def route(self, x=None, token_ids=None, ids_out=None, w_out=None, stream=None, n_tok=None):
         """Expert ids and weights (ds4moe_route). Returns (ids_out, w_out)."""
-        import torch
         n = n_tok if n_tok is not None else (x.shape[0] if x is not None else token_ids.shape[0])
         dev = (x if x is not None else token_ids).device
         if ids_out is None:
@@ -300,7 +301,6 @@ class Layer:
 
     def scratch(self, name: str):
         """Torch view (treat as read-only) of an intermediate buffer (ds4moe_debug_scratch), flat."""
-        import torch
         which, typestr = self._SCRATCH[name]
         p, n = ctypes.c_void_p(), ctypes.c_uint64()
         _check(lib().ds4moe_debug_scratch(self._h, which, ctypes.byref(p), ctypes.byref(n)), "ds4moe_debug_scratch")
@@ -333,7 +333,6 @@ class Dense:
         """y = W x (ds4moe_dense_forward); returns y. With `adapters` (an Adapters
         of the same shape) and `slots` the tokens' low-rank adapters are added
         (ds4moe_adapters_forward)."""
-        import torch
         n = x.shape[0] if n_tok is None else n_tok
         if adapters is not None:
             _need(isinstance(adapters, Adapters) and (adapters.n_out, adapters.n_in) == (self.n_out, self.n_in),
@@ -378,8 +377,7 @@ def _rows(t, name, dtype, shape, inner=None):
     """Elements from one row of `t` to the next: `shape` after the leading
     dimensions, contiguous, the leading dimensions evenly spaced. `inner`: the
     elements of a row, where the caller has them."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype):
         raise ValueError(f"{name}: a CUDA tensor of {dtype}")
     size = t.shape
     lead = len(size) - len(shape)
@@ -408,8 +406,7 @@ def _rows(t, name, dtype, shape, inner=None):
 
 
 def _vec(t, name, dtype, n):
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous CUDA tensor of {n} {dtype}")
     return t.data_ptr()
 
@@ -420,7 +417,6 @@ def _empty(shape, dtype, device, stream):
     in use by what that stream has queued, for which another one would not wait.
     So it comes from `stream`'s own blocks, and goes back to them only when the
     current stream, where the caller goes on, is done with it too."""
-    import torch
     if stream is None or torch.device(device).type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
@@ -435,7 +431,6 @@ def _empty(shape, dtype, device, stream):
 
 
 def _torch_dtype(dt):
-    import torch
     return {DT_F32: torch.float32, DT_BF16: torch.bfloat16, DT_F16: torch.float16}[dt]
 
 
@@ -478,7 +473,6 @@ class Adapters:
         _check(_lib.ds4moe_adapters_set(self._h, slot, 0, None, None, 0.0, _stream(stream)), "ds4moe_adapters_set")
 
     def _args(self, x, slots, y, base):
-        import torch
         f32 = torch.float32
         dt = f32 if x.dtype == f32 else self._dt
         n = x.numel() // self.n_in
@@ -546,7 +540,6 @@ class KVCache:
     may change between calls."""
 
     def __init__(self, k, v, block_table):
-        import torch
         for t, name in ((k, "k"), (v, "v")):
             _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.stride(3) == 1,
                   f"{name}: a CUDA tensor [n_pages, page_size, n_kv_heads, head_dim], head_dim contiguous")
@@ -569,7 +562,6 @@ class Rope:
     the tensor."""
 
     def __init__(self, inv_freq, offset: int = 0, interleaved: bool = False, scale: float = 1.0):
-        import torch
         _need(isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda and inv_freq.dtype == torch.float32 and
               inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq: a contiguous CUDA fp32 tensor [rot_dim / 2]")
         self.inv_freq = inv_freq
@@ -624,20 +616,23 @@ class Attention:
         and so are the queries `q` [..., n_heads, head_dim] of the same tokens and
         k's type, into q_out (the cache's type; may be q itself if it is of that),
         which is returned (ds4moe_kv_append_rope)."""
-        import torch
-        n_seq = kv_len.numel()
-        if cu_q is None and k.dim() == 4 and k.shape[0] != n_seq:
+        n_seq, dims = kv_len.numel(), k.dim()
+        if cu_q is None and dims == 4 and k.shape[0] != n_seq:
             raise ValueError("k: [n_seq, n_new, ...] for the sequences of kv_len")
-        dt = torch.float32 if k.dtype == torch.float32 else self._dt
+        dt = torch.float32 if k.dtype is torch.float32 else self._dt
         ks = _rows(k, "k", dt, self._kv_row, self._kv_len)
+        n_tok = k.numel() // self._kv_len
+
+        def same(t, row_len):  # the same tokens: of one leading dimension their number says it
+            return t.dim() == dims and t.numel() == n_tok * row_len and (dims == 3 or t.shape[:-2] == k.shape[:-2])
         vs = 0
         if v is not None:
             vs = _rows(v, "v", dt, self._kv_row, self._kv_len)
-            if v.shape != k.shape:
+            if not same(v, self._kv_len):
                 raise ValueError("v: the shape of k")
         code = DT_F32 if dt == torch.float32 else self._code
         cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, n_seq + 1)
-        n_tok, vp = k.numel() // self._kv_len, None if v is None else v.data_ptr()
+        vp = None if v is None else v.data_ptr()
         if rope is None:
             if q is not None or q_out is not None:
                 raise ValueError("q: only with rope")
@@ -650,14 +645,14 @@ class Attention:
         qs = os_ = 0
         if q is not None:
             qs = _rows(q, "q", dt, self._q_row, self._q_len)
-            if q.shape[:-2] != k.shape[:-2]:
+            if not same(q, self._q_len):
                 raise ValueError("q: the tokens of k")
             if q_out is None:
                 q_out, os_ = _empty(q.shape, self._dt, q.device, stream), self._q_len
-            elif q_out.shape != q.shape:
-                raise ValueError("q_out: the shape of q")
             else:
                 os_ = _rows(q_out, "q_out", self._dt, self._q_row, self._q_len)
+                if not same(q_out, self._q_len):
+                    raise ValueError("q_out: the shape of q")
         elif q_out is not None:
             raise ValueError("q_out: only with q")
         _check(_lib.ds4moe_kv_append_rope(
@@ -682,7 +677,6 @@ class Attention:
         many first positions in common, which are read once for all of them
         (ds4moe_attn_decode_shared). `group_start` int32 [n_groups + 1] holds the
         groups' first sequences; None: one group of all."""
-        import torch
         if q.dim() != 4:
             raise ValueError("q: [n_seq, n_new, n_heads, head_dim]")
         n_seq, n_new = q.shape[:2]
@@ -711,7 +705,6 @@ class Attention:
     def prefill(self, cache, q, cu_q, kv_len, out=None, stream=None):
         """Attention of ragged runs of new tokens (ds4moe_attn_prefill): q
         [n_tok, n_heads, head_dim], cu_q int32 [n_seq + 1]; returns out."""
-        import torch
         if q.dim() != 3:
             raise ValueError("q: [n_tok, n_heads, head_dim]")
         n_seq = kv_len.numel()
@@ -742,7 +735,6 @@ def token_probs(logits, temperature: float = 1.0, out=None, stream=None):
     """softmax(logits / temperature) over the last dimension of an fp32 CUDA
     tensor (ds4moe_token_probs); temperature 0: one at the lowest index of the
     maximum. `out` may be `logits`; returns out."""
-    import torch
     V = logits.shape[-1]
     if out is None:
         out = _empty(logits.shape, torch.float32, logits.device, stream)
@@ -762,7 +754,6 @@ def verify_drafts(target, draft, tokens, u_accept, u_sample, n_draft=None, n_acc
     (ds4moe_verify_drafts): target fp32 [n_seq, max_draft + 1, vocab], draft
     fp32 [n_seq, max_draft, vocab] or None, tokens int32 [n_seq, max_draft].
     Returns (n_accepted int32 [n_seq], tokens_out int32 [n_seq, max_draft + 1])."""
-    import torch
     lib()
     i32, f32 = torch.int32, torch.float32
     if target.dim() != 3:
@@ -805,7 +796,6 @@ def route_noalloc(desc: LayerDesc, weights: dict, x=None, token_ids=None, ids_ou
     router_bias or hash_table; CUDA tensors) with no handle and no device
     allocation by the library (ds4moe_route_noalloc). ids_out / w_out are
     allocated here by torch when not given. Returns (ids_out, w_out)."""
-    import torch
     n = n_tok if n_tok is not None else (x.shape[0] if x is not None else token_ids.shape[0])
     dev = (x if x is not None else token_ids).device
     if ids_out is None:

@@ -365,7 +365,7 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  * (The pages have no adapters; the projection is ds4moe_dense_forward, whose
  * output is the base.) x and weights as they are, products and sums in 32 bits:
  * no rounding to fewer bits on the way (many tokens: a product's fp32 operand
- * is taken as the sum of two 11-bit numbers, off by 2^-21 of it at most).
+ * is taken as the sum of two 11-bit numbers, off by 2^-20 of it at most).
  *
  * ds4moe_adapters_create: places for n_slots (1..4096) adapters of up to max_rank
  *   (1..256) in `dtype` (DS4MOE_DT_BF16 or DS4MOE_DT_F16) on the current device,
@@ -388,6 +388,7 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  *          stride): y is added to
  *   y      [n_tok][n_out] fp32, y_stride apart; must not overlap x, nor base
  *          otherwise
+ *   Strides are below 2^31 elements.
  *   Enqueued on `stream` (one launch up to 64 tokens, else three), no allocation,
  *   no synchronisation. Calls on one handle must not run concurrently (shared
  *   workspace). Errors: INVALID_ARG, CUDA.

@@ -34,10 +34,11 @@ def _handle(ranks, n_out, n_in, kind, n_tok, seed, max_rank=None):
 def _expect(x, slots, base, a, b, s):
     """y in 64 bits and the error that 32-bit sums may make.
 
-    h = A x: with products exact to 2^-21 (an operand as two 11-bit numbers) and
-    at most n_in / 4 additions of partial sums, each cut (not rounded) to 24 bits,
-    the error is below (2^-21 + n_in / 4 2^-23) of sum |a x|; y likewise over the
-    rank, plus what h's error brings, plus a rounding of scale h and of y."""
+    h = A x: an operand is taken as its leading 11 bits and the leading 11 of the
+    rest, which is below 2^-10 of it, so 2^-20 of it is left out; at most n_in / 4
+    additions of partial sums, each cut (not rounded) to 24 bits: the error is
+    below (2^-20 + n_in / 4 2^-23) of sum |a x|; y likewise over the rank, plus
+    what h's error brings, plus a rounding of scale h and of y."""
     y, tol = base.double().clone(), 2.0 ** -23 * base.double().abs()
     for i in set(slots.tolist()):
         if not 0 <= i < len(a):
@@ -46,7 +47,7 @@ def _expect(x, slots, base, a, b, s):
         xx, A, B = x[rows].double(), a[i].double(), b[i].double()
         h, hs = xx @ A.T, xx.abs() @ A.abs().T
         n_in, r = A.shape[1], A.shape[0]
-        eh = (2.0 ** -21 + n_in / 4 * 2.0 ** -23) * hs
+        eh = (2.0 ** -20 + n_in / 4 * 2.0 ** -23) * hs
         size = hs @ B.abs().T
         y[rows] += s[i] * (h @ B.T)
         tol[rows] += abs(s[i]) * (eh @ B.abs().T + (2.0 ** -20 + (r / 4 + 8) * 2.0 ** -23) * size)
