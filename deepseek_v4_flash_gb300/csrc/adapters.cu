@@ -120,16 +120,33 @@ __device__ __forceinline__ float dot8(const uint4 &w, const float *x, float s) {
   return s;
 }
 
+// (four blocks per SM: all of 64 tokens' blocks run at once)
 template <int DT, bool F32>
-__global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
+__global__ void __launch_bounds__(256, 4) k_adapt_token(const AdaptArgs a) {
   extern __shared__ __align__(16) float s_x[];  // this block's columns of x
   __shared__ float s_part[LR_MAX_RANK];
   __shared__ __align__(16) float s_v[LR_MAX_RANK];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, c = (int)cluster_rank(), t = blockIdx.x / LR_CLUSTER;
   pdl_launch_dependents();
   pdl_wait();
+  // Loads that do not wait for one another go first: the slot's own chain (slot,
+  // rank, weights) runs beside x's.
   bool bad = false;
   const int s = slot_at(a, t, bad);
+  // pieces of eight columns
+  const int u0 = (int)((long long)(a.K / 8) * c / LR_CLUSTER), nu = (int)((long long)(a.K / 8) * (c + 1) / LR_CLUSTER) - u0;
+  for (int u = tid; u < nu; u += 256) {
+    float4 lo, hi;
+    if (F32) {
+      const float4 *p = reinterpret_cast<const float4 *>((const float *)a.x + (long long)t * a.x_stride) + 2 * (u0 + u);
+      lo = p[0], hi = p[1];
+    } else {
+      const uint4 q = reinterpret_cast<const uint4 *>((const uint16_t *)a.x + (long long)t * a.x_stride)[u0 + u];
+      const float2 f0 = Half16<DT>::up(q.x), f1 = Half16<DT>::up(q.y), f2 = Half16<DT>::up(q.z), f3 = Half16<DT>::up(q.w);
+      lo = make_float4(f0.x, f0.y, f1.x, f1.y), hi = make_float4(f2.x, f2.y, f3.x, f3.y);
+    }
+    reinterpret_cast<float4 *>(s_x)[2 * u] = lo, reinterpret_cast<float4 *>(s_x)[2 * u + 1] = hi;
+  }
   if (bad && c == 0 && tid == 0) raise_flag(a.err, DS4MOE_DEVERR_ADAPTER);
   const int2 in = s >= 0 ? a.info[s] : make_int2(0, 0);
   const int rank = in.x;
@@ -147,34 +164,39 @@ __global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
     const uint32_t bytes = (uint32_t)min((long long)(n1 - n0) * r8 * 2, 1ll << 20);
     if (bytes) prefetch_l2(B + (long long)n0 * r8, bytes);
   }
-  // pieces of eight columns
-  const int u0 = (int)((long long)(a.K / 8) * c / LR_CLUSTER), nu = (int)((long long)(a.K / 8) * (c + 1) / LR_CLUSTER) - u0;
-  for (int u = tid; u < nu; u += 256) {
-    float4 lo, hi;
-    if (F32) {
-      const float4 *p = reinterpret_cast<const float4 *>((const float *)a.x + (long long)t * a.x_stride) + 2 * (u0 + u);
-      lo = p[0], hi = p[1];
-    } else {
-      const uint4 q = reinterpret_cast<const uint4 *>((const uint16_t *)a.x + (long long)t * a.x_stride)[u0 + u];
-      const float2 f0 = Half16<DT>::up(q.x), f1 = Half16<DT>::up(q.y), f2 = Half16<DT>::up(q.z), f3 = Half16<DT>::up(q.w);
-      lo = make_float4(f0.x, f0.y, f1.x, f1.y), hi = make_float4(f2.x, f2.y, f3.x, f3.y);
-    }
-    reinterpret_cast<float4 *>(s_x)[2 * u] = lo, reinterpret_cast<float4 *>(s_x)[2 * u + 1] = hi;
-  }
-  __syncthreads();
-  // J rows of A per warp at a time (rows past the rank are zeros up to a multiple of 32)
+  // J rows of A per warp at a time (rows past the rank are zeros up to a multiple
+  // of 32); the first pieces are requested before x is waited for
   auto rows_of_a = [&](auto per_warp) {
     constexpr int J = decltype(per_warp)::value;
-    for (int r0 = J * w; r0 < rank; r0 += 8 * J) {
-      float sum[J] = {};
-      const uint4 *p = reinterpret_cast<const uint4 *>(A + (long long)r0 * a.K) + u0;
-#pragma unroll 2
-      for (int u = lane; u < nu; u += 32) {
-        float x[8];
-        *reinterpret_cast<float4 *>(x) = reinterpret_cast<const float4 *>(s_x)[2 * u];
-        *reinterpret_cast<float4 *>(x + 4) = reinterpret_cast<const float4 *>(s_x)[2 * u + 1];
+    const uint4 *p = reinterpret_cast<const uint4 *>(A + (long long)(J * w) * a.K) + u0;
+    const long long row = a.K / 8;
+    uint4 first[J];
 #pragma unroll
-        for (int j = 0; j < J; j++) sum[j] = dot8<DT>(p[(long long)j * (a.K / 8) + u], x, sum[j]);
+    for (int j = 0; j < J; j++) {
+      first[j] = make_uint4(0, 0, 0, 0);
+      if (J * w < rank && lane < nu) first[j] = p[j * row + lane];
+    }
+    __syncthreads();
+    auto add = [&](const uint4 (&wt)[J], int u, float (&sum)[J]) {
+      float x[8];
+      *reinterpret_cast<float4 *>(x) = reinterpret_cast<const float4 *>(s_x)[2 * u];
+      *reinterpret_cast<float4 *>(x + 4) = reinterpret_cast<const float4 *>(s_x)[2 * u + 1];
+#pragma unroll
+      for (int j = 0; j < J; j++) sum[j] = dot8<DT>(wt[j], x, sum[j]);
+    };
+    for (int r0 = J * w; r0 < rank; r0 += 8 * J, p += 8 * J * row) {
+      float sum[J] = {};
+      int u = lane;
+      if (r0 == J * w) {
+        if (u < nu) add(first, u, sum);
+        u += 32;
+      }
+#pragma unroll 2
+      for (; u < nu; u += 32) {
+        uint4 wt[J];
+#pragma unroll
+        for (int j = 0; j < J; j++) wt[j] = p[j * row + u];
+        add(wt, u, sum);
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1)
@@ -187,52 +209,59 @@ __global__ void __launch_bounds__(256) k_adapt_token(const AdaptArgs a) {
     }
   };
   if (rank <= 16) rows_of_a(std::integral_constant<int, 2>());
-  else if (rank <= 32) rows_of_a(std::integral_constant<int, 4>());
-  else rows_of_a(std::integral_constant<int, 8>());
+  else rows_of_a(std::integral_constant<int, 4>());
   cluster_arrive();
-  cluster_wait();
   const float scale = __int_as_float(in.y);
-  for (int r = tid; r < r8; r += 256) {  // (r8 is at most 256)
-    float v = 0.0f;
-    if (r < rank)
-#pragma unroll
-      for (int i = 0; i < LR_CLUSTER; i++) v += remote_f32(smem_u32(s_part + r), i);
-    s_v[r] = v * scale;
-  }
-  __syncthreads();
-  cluster_arrive();  // the others' sums are read: they may leave
   // U lanes per row of B, so that a load takes whole lines: the lane's piece of
   // eight ranks is the same for all rows. A warp takes 32 rows, 32 / U at a time,
-  // of which lane l ends up with row (l % U) * (32 / U) + l / U.
+  // of which lane l ends up with row (l % U) * (32 / U) + l / U. The first pieces
+  // are requested before the other blocks' sums are waited for.
   const int units = r8 / 8;
   auto rows_of_b = [&](auto lanes) {
-    constexpr int U = decltype(lanes)::value, G = 32 / U;
+    constexpr int U = decltype(lanes)::value, G = 32 / U, H = U < 4 ? U : 4;
     const int u = lane % U, g = lane / U;
+    uint4 wt[H];
+    auto request = [&](int r0, int b) {
+#pragma unroll
+      for (int k = 0; k < H; k++) {
+        const int n = r0 + (b + k) * G + g;
+        wt[k] = make_uint4(0, 0, 0, 0);
+        if (n < n1 && u < units) wt[k] = *reinterpret_cast<const uint4 *>(B + (long long)n * r8 + 8 * u);
+      }
+    };
+    int r0 = n0 + 32 * w;
+    float from = r0 + u * G + g < n1 ? base[r0 + u * G + g] : 0.0f;
+    request(r0, 0);
+    cluster_wait();
+    if (tid < r8) {
+      float v = 0.0f;
+      if (tid < rank)
+#pragma unroll
+        for (int i = 0; i < LR_CLUSTER; i++) v += remote_f32(smem_u32(s_part + tid), i);
+      s_v[tid] = v * scale;
+    }
+    __syncthreads();
+    cluster_arrive();  // the others' sums are read: they may leave
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) v[e] = u < units ? s_v[8 * u + e] : 0.0f;
-    for (int r0 = n0 + 32 * w; r0 < n1; r0 += 256) {
+    for (; r0 < n1; r0 += 256) {
       const int mine = r0 + u * G + g;
-      const float from = mine < n1 ? base[mine] : 0.0f;
       float keep = 0.0f;
 #pragma unroll
-      for (int b = 0; b < U; b += 8) {
-        uint4 wt[U < 8 ? U : 8];
+      for (int b = 0; b < U; b += H) {
 #pragma unroll
-        for (int k = 0; k < (U < 8 ? U : 8); k++) {
-          const int n = r0 + (b + k) * G + g;
-          wt[k] = make_uint4(0, 0, 0, 0);
-          if (n < n1 && u < units) wt[k] = *reinterpret_cast<const uint4 *>(B + (long long)n * r8 + 8 * u);
-        }
-#pragma unroll
-        for (int k = 0; k < (U < 8 ? U : 8); k++) {
+        for (int k = 0; k < H; k++) {
           float sum = dot8<DT>(wt[k], v, 0.0f);
 #pragma unroll
           for (int o = U / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           if (b + k == u) keep = sum;
         }
+        if (b + H < U) request(r0, b + H);
+        else if (r0 + 256 < n1) request(r0 + 256, 0);
       }
       if (mine < n1) y[mine] = from + keep;
+      from = mine + 256 < n1 ? base[mine + 256] : 0.0f;
     }
   };
   if (units == 1) rows_of_b(std::integral_constant<int, 1>());

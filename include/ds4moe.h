@@ -497,8 +497,9 @@ ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, con
                                const int32_t *kv_len, int32_t n_seq, int32_t n_tok, void *stream);
 
 /* The same append with the position rotation on the way, for the keys and, in
- * the same launch, the queries of the new tokens. (The pages run rope as calls
- * of its own: "DeepSeek V4 Flash -- DFlash Integration", Forward Pass.)
+ * the same launch, the queries of the new tokens. Passage: "DeepSeek V4 Flash --
+ * DFlash Integration", Model Architecture (partial rope of 64 of 512 elements;
+ * YaRN, whose frequencies and factor are the caller's here).
  * The pair (x, y) number i of a head's rotated elements becomes, at position p,
  *   x' = scale * (x cos - y sin),  y' = scale * (y cos + x sin),
  *   angle = p * inv_freq[i],
