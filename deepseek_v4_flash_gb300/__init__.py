@@ -125,6 +125,7 @@ def lib():
             "ds4moe_adapters_create": (i32, [i32, i32, i32, i32, i32, i32, ctypes.POINTER(vp)]),
             "ds4moe_adapters_set": (i32, [vp, i32, i32, vp, vp, ctypes.c_float, vp]),
             "ds4moe_adapters_forward": (i32, [vp, vp, i64, i32, vp, i32, vp, i64, vp, i64, vp]),
+            "ds4moe_adapters_debug_path": (i32, [vp, i32]),
             "ds4moe_adapters_get_device_error": (i32, [vp, vp, ctypes.POINTER(u32)]),
             "ds4moe_adapters_destroy": (None, [vp]),
             "ds4moe_adapters_device_bytes": (ctypes.c_uint64, [vp]),
@@ -495,6 +496,11 @@ class Adapters:
         y is added to. Returns y."""
         self._forward(self._args(x, slots, y, base), stream)
         return y
+
+    def debug_path(self, path: int):
+        """1: later calls token by token, 2: by tiles, 0: by the number of tokens; a
+        test hook (ds4moe_adapters_debug_path)."""
+        _check(_lib.ds4moe_adapters_debug_path(self._h, path), "ds4moe_adapters_debug_path")
 
     def device_error(self, stream=None) -> int:
         """Synchronise, read and clear the device error flags (0 = none)."""

@@ -4,7 +4,7 @@
 // A_s is [rank][n_in], B_s [n_out][rank] in 16 bits, x, base and y rows of tokens.
 // Sums are in 32 bits, A x stays in 32 bits between the two products.
 //
-// Few tokens (LR_TOKENS): k_adapt_token, a cluster of eight blocks per token,
+// Few tokens (takes_tokens): k_adapt_token, a cluster of eight blocks per token,
 // one launch. A block takes an eighth of the columns of A, the eight exchange
 // their partial sums through distributed shared memory, then each computes an
 // eighth of y. Bound by the latency of that chain and, with many adapters, by
@@ -41,6 +41,7 @@ struct ds4moe_adapters {
   int4 *tiles;       // {slot, first place in perm, tokens | rank << 16, bits of the scale}
   int *n_tiles;
   float *v;          // [max_tokens][R32] scale A x by place in perm
+  int path;          // ds4moe_adapters_debug_path
   int clusters[9];   // clusters of so many blocks of k_adapt_shrink that run at once
   uint64_t bytes, launches;
 };
@@ -49,8 +50,6 @@ namespace ds4 {
 
 constexpr int LR_CLUSTER = 8;
 constexpr int LR_MAX_RANK = 256, LR_MAX_SLOTS = 4096;
-// Largest call of k_adapt_token.
-constexpr int LR_TOKENS = 64;
 
 struct AdaptArgs {
   int N, K, slots, T, R32;
@@ -1024,6 +1023,20 @@ cudaError_t launch_cluster(const void *fn, int grid, int cluster, int threads, s
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// Whether a call goes token by token or by tiles. Measured with up to 512 tokens
+// (us), m = max_rank * (n_in + n_out) in millions: token by token a wave of four
+// blocks per SM takes 2.9 + 11 m; tiles take 15 + 13 m and 0.6 for every adapter
+// that there may be. 4096 x 4096, rank 64, 4 adapters: 64 tokens 12 and 22, 128 22
+// and 23, 256 39 and 23; 64 adapters: 256 44 and 88, 512 81 and 90; rank 16, 4
+// adapters: 256 18 and 21, 512 34 and 24; 8192 x 8192, rank 128, 8 adapters: 64 32
+// and 43, 128 60 and 45.
+bool takes_tokens(const ds4moe_adapters *h, int n_tok) {
+  if (h->path) return h->path == 1;
+  const double m = 1e-6 * h->max_rank * (double)(h->K + h->N);
+  const int waves = (n_tok * LR_CLUSTER + 4 * h->n_sm - 1) / (4 * h->n_sm);
+  return waves * (2.9 + 11.0 * m) <= 15.0 + 13.0 * m + 0.6 * (std::min(h->slots, n_tok) - 1);
+}
+
 bool rows_overlap(const void *p, long long n, const void *q, long long m) {
   const uintptr_t x = (uintptr_t)p, y = (uintptr_t)q;
   return x < y + (uintptr_t)m && y < x + (uintptr_t)n;
@@ -1142,7 +1155,7 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   a.wide = N % 4 == 0 && y_stride % 4 == 0 && !((uintptr_t)y & 15) && (!base || (base_stride % 4 == 0 && !((uintptr_t)base & 15)));
   const AdaptFns f = adapt_fns(h->dtype, f32, h->R32);
   const cudaStream_t s = (cudaStream_t)stream;
-  if (n_tok <= LR_TOKENS) {
+  if (takes_tokens(h, n_tok)) {
     void *args[] = {&a};
     const cudaError_t e = launch_cluster(f.token, LR_CLUSTER * n_tok, LR_CLUSTER, 256, (size_t)(K / 8 / LR_CLUSTER + 1) * 32, s, args);
     h->launches++;
@@ -1172,6 +1185,12 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   }
   h->launches += 3;
   return ap_status(e);
+}
+
+ds4moe_status ds4moe_adapters_debug_path(ds4moe_adapters *h, int32_t path) {
+  if (!h || path < 0 || path > 2) return DS4MOE_ERR_INVALID_ARG;
+  h->path = path;
+  return DS4MOE_OK;
 }
 
 ds4moe_status ds4moe_adapters_get_device_error(ds4moe_adapters *h, void *stream, uint32_t *flags_out) {

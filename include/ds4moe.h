@@ -389,9 +389,12 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  *   y      [n_tok][n_out] fp32, y_stride apart; must not overlap x, nor base
  *          otherwise
  *   Strides are below 2^31 elements.
- *   Enqueued on `stream` (one launch up to 64 tokens, else three), no allocation,
+ *   Enqueued on `stream` (one launch for few tokens, else three), no allocation,
  *   no synchronisation. Calls on one handle must not run concurrently (shared
  *   workspace). Errors: INVALID_ARG, CUDA.
+ * ds4moe_adapters_debug_path: 1: every later call token by token, 2: by tiles of
+ *   tokens of one adapter, 0: by the number of tokens (a test hook; results differ by
+ *   roundings). Errors: INVALID_ARG.
  * The others as their ds4moe_dense_* namesakes. */
 typedef struct ds4moe_adapters ds4moe_adapters;
 ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slots, int32_t max_rank, int32_t dtype,
@@ -401,6 +404,7 @@ ds4moe_status ds4moe_adapters_set(ds4moe_adapters *h, int32_t slot, int32_t rank
 ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t x_stride, int32_t x_dtype,
                                       const int32_t *slots, int32_t n_tok, const float *base, int64_t base_stride,
                                       float *y, int64_t y_stride, void *stream);
+ds4moe_status ds4moe_adapters_debug_path(ds4moe_adapters *h, int32_t path);
 ds4moe_status ds4moe_adapters_get_device_error(ds4moe_adapters *h, void *stream, uint32_t *flags_out);
 void ds4moe_adapters_destroy(ds4moe_adapters *h);
 uint64_t ds4moe_adapters_device_bytes(const ds4moe_adapters *h);

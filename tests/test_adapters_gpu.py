@@ -23,11 +23,13 @@ def _weights(ranks, n_out, n_in, dt, seed):
     return a, b, [0.25 + 1.5 * i for i in range(len(ranks))]
 
 
-def _handle(ranks, n_out, n_in, kind, n_tok, seed, max_rank=None):
+def _handle(ranks, n_out, n_in, kind, n_tok, seed, max_rank=None, path=None):
     a, b, s = _weights(ranks, n_out, n_in, DTYPES[kind], seed)
     h = _ds4().Adapters(n_out, n_in, len(ranks), max_rank or max(ranks), kind, max_tokens=n_tok)
     for i in range(len(ranks)):
         h.set(i, a[i].cuda(), b[i].cuda(), s[i])
+    # few tokens one by one, more by tiles, whatever the automatic choice
+    h.debug_path(path or (1 if n_tok <= 64 else 2))
     return h, a, b, s
 
 
@@ -62,9 +64,9 @@ def _close(got, ref, tol, what=""):
                               f"{float((got - ref).abs().nan_to_num().max())}"
 
 
-def _run(kind, source, n_out, n_in, ranks, slots, seed=0, max_rank=None):
+def _run(kind, source, n_out, n_in, ranks, slots, seed=0, max_rank=None, path=None):
     n = len(slots)
-    h, a, b, s = _handle(ranks, n_out, n_in, kind, n, seed, max_rank)
+    h, a, b, s = _handle(ranks, n_out, n_in, kind, n, seed, max_rank, path)
     g = torch.Generator().manual_seed(seed + 1)
     x = torch.randn(n, n_in, generator=g).to(torch.float32 if source == "fp32" else DTYPES[kind])
     base = torch.randn(n, n_out, generator=g)
@@ -119,6 +121,29 @@ def test_many_slots():
     _run("bf16", "fp32", 100, 128, ranks, [(17 * t) % 300 for t in range(500)], 8)
 
 
+@pytest.mark.parametrize("n", [1, 2, 63, 65, 130, 700])
+def test_either_way_for_any_number_of_tokens(n):
+    for path in (1, 2):
+        _run("bf16", "fp32", 260, 352, [33, 3, 9], [(5 * t) % 4 - 1 for t in range(n)], n, path=path)
+
+
+def test_the_automatic_choice():
+    """One launch for a step, three for a prompt, and the same results but for roundings."""
+    n = 900
+    h, a, b, s = _handle([16, 8], 512, 512, "bf16", n, 18)
+    h.debug_path(0)
+    x, base = torch.randn(n, 512), torch.randn(n, 512)
+    for m, launches in ((1, 1), (64, 1), (900, 3)):
+        slots = torch.tensor([t % 3 - 1 for t in range(m)], dtype=torch.int32)
+        before = h.launch_count()
+        y = h.forward(x[:m].cuda(), slots.cuda(), torch.empty(m, 512).cuda(), base=base[:m].cuda())
+        assert h.launch_count() - before == launches
+        ref, tol = _expect(x[:m], slots, base[:m], a, b, s)
+        _close(y, ref, tol)
+    with pytest.raises(_ds4().Ds4MoeError):
+        h.debug_path(3)
+
+
 def test_long_prompt():
     """More tiles than clusters run at once, and one that all blocks share."""
     _run("bf16", "fp32", 512, 1024, [64, 16], [0] * 9000 + [1] * 3001, 9)
@@ -131,6 +156,7 @@ def test_set_replaces_and_clear_empties():
     g = torch.Generator().manual_seed(11)
     h = ds4.Adapters(n_out, n_in, 3, 40, "bf16", max_tokens=200)
     for n in (4, 200):
+        h.debug_path(1 if n == 4 else 2)
         x = torch.randn(n, n_in, generator=g).cuda()
         y = torch.randn(n, n_out, generator=g).cuda()
         slots = torch.tensor([t % 3 for t in range(n)], dtype=torch.int32).cuda()
