@@ -197,11 +197,16 @@ __global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_
   uint8_t *ring = smem + w * NST * STAGE;
   const uint32_t ring_u = smem_u32(ring);
   pdl_launch_dependents();
-  pdl_wait();
+  // (SHARED: when this kernel starts, all that came before the call is done, see
+  // k_attn_tile; only results of the call's own kernels are waited for, below)
+  if (!SHARED) pdl_wait();
 
   long long U, N, u0, u1;
   DecCursor lc, cc;  // where loading and computing stand
-  if (!dec_start<SHARED>(a, n_cta, U, N, u0, u1, lc)) return;
+  if (!dec_start<SHARED>(a, n_cta, U, N, u0, u1, lc)) {
+    if (SHARED) pdl_wait();  // (a kernel that is done stands for all before it)
+    return;
+  }
   cc = lc;
 
   // one unit's 16 positions of this warp into ring slot `slot`
@@ -265,6 +270,8 @@ __global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_
       cp_commit();
     }
   }
+
+  if (SHARED) pdl_wait();
 
   // SHARED: this thread's pieces of the item's results over the shared positions,
   // requested when the item begins

@@ -739,6 +739,9 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
   tc_fence_after();
   if (PAIR) cluster_sync_all();  // barriers are set up before the other block reaches for them
   const uint32_t tmem = ms.tmem;
+  // AT_PREFIX: what follows the call's other kernels may then rely on all that
+  // came before the call (the streaming kernel reads the cache before it waits)
+  if (MODE == AT_PREFIX) pdl_wait();
   pdl_launch_dependents();
   pdl_wait();
 
@@ -1400,10 +1403,10 @@ __device__ __noinline__ void join_again(const AttnArgs &a, const TileArgs &t, un
 }
 
 template <int DT, int D, int NT, bool PAIR, int MODE, int R>
-__global__ void __launch_bounds__(AJ_THREADS, D * R < 512 || D == 128 ? 4 : D * R <= 1024 ? 3 : 2)
+__global__ void __launch_bounds__(AJ_THREADS, MODE == AT_PREFIX ? 2 : D * R < 512 || D == 128 ? 4 : D * R <= 1024 ? 3 : 2)
     k_attn_join(const __grid_constant__ AttnArgs a, const __grid_constant__ TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
-  constexpr int ROWS = C::JROWS * R, STEP = C::JROWS, P = 8 / R;  // rows of the block; distance of a thread's rows
+  constexpr int ROWS = C::JROWS * R, STEP = C::JROWS, P = MODE == AT_PREFIX ? 16 : 8 / R;  // rows of the block; distance of a thread's rows
   __shared__ unsigned long long s_nan;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x % (128 / ROWS) * ROWS, r = blockIdx.x / (128 / ROWS) % NT;
