@@ -42,7 +42,7 @@ struct ds4moe_adapters {
   int *n_tiles;
   float *v;          // [max_tokens][R32] scale A x by place in perm
   int path;          // ds4moe_adapters_debug_path
-  int clusters[9];   // clusters of so many blocks of k_adapt_shrink that run at once
+  int clusters[17];  // clusters of so many blocks of k_adapt_shrink that run at once
   uint64_t bytes, launches;
 };
 
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
 // ---- y = base + B V, 128 tokens of a tile and 128 columns at a time; a block
 // takes a run of them. Four warps bring B (widened) into a ring, by 64 ranks, and
 // V (split), which stays for all columns of a tile, and issue the products, into
-// two accumulators in turn; sixteen add base, which they request an item ahead,
+// two pairs of accumulators (high and low parts) in turn; sixteen add base, which they request an item ahead,
 // and store y. Base comes through shared memory where that has room (ranks up to
 // 64), so that an item's is under way all the time that the one before it takes,
 // not only after its stores (57 -> 52 us). Bound by the bytes of base and y. Ranks
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
       fence_mbar_init();
     }
     __syncwarp();
-    tmem_alloc(smem_u32(&s_tmem), 256);
+    tmem_alloc(smem_u32(&s_tmem), 512);
   }
   tc_fence_before();
   __syncthreads();
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
 #pragma unroll
             for (int q = 0; q < 4; q++) umma_tf32(d, dh + 2 * q, dw + 2 * q, id, uc != 0 || h != 0 || q != 0);
 #pragma unroll
-            for (int q = 0; q < 4; q++) umma_tf32(d, dl + 2 * q, dw + 2 * q, id, 1);
+            for (int q = 0; q < 4; q++) umma_tf32(d + 256, dl + 2 * q, dw + 2 * q, id, uc != 0 || h != 0 || q != 0);
           }
           umma_commit(empty(us));
           if (ends) umma_commit(acc_full(buf));
@@ -851,16 +851,19 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
         ws.wait(acc_full(buf), (accs / 2) & 1);
         __syncwarp();
         tc_fence_after();
-        float v[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * 128 + 32 * g, v);
-        tmem_wait_ld(v);
+        uint32_t u[32];
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * 128 + 32 * g;
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+          float hi[16], lo[16];
+          tmem_ld16x2(at + e, at + 256 + e, hi, lo);
+#pragma unroll
+          for (int k = 0; k < 16; k++) u[e + k] = __float_as_uint(hi[k] + lo[k]);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buf));
         accs++;
-        uint32_t u[32];
-#pragma unroll
-        for (int e = 0; e < 32; e++) u[e] = __float_as_uint(v[e]);
         transpose8(u);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
   __syncthreads();
   if (w == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -1078,7 +1081,8 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f.expand, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
-    for (int ks = 1; ks <= LR_CLUSTER && e == cudaSuccess; ks++) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int ks = 1; ks <= 2 * LR_CLUSTER && e == cudaSuccess; ks += ks < LR_CLUSTER ? 1 : LR_CLUSTER) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       cfg.gridDim = dim3(ks), cfg.blockDim = dim3(LR_WARPS * 32 + 32), cfg.dynamicSmemBytes = LR_SMEM;
@@ -1086,7 +1090,7 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
       attr[0].val.clusterDim.x = ks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
       cfg.attrs = attr, cfg.numAttrs = 1;
       e = cudaOccupancyMaxActiveClusters(&h->clusters[ks], f.shrink, &cfg);
-      if (e == cudaSuccess && h->clusters[ks] < 1) h->clusters[ks] = 1;
+      if (e == cudaSuccess && h->clusters[ks] < 1 && ks <= LR_CLUSTER) h->clusters[ks] = 1;
     }
   }
   if (e == cudaSuccess) e = cudaMalloc((void **)&h->mem, at);
@@ -1165,16 +1169,19 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   cudaError_t e = launch_pdl((const void *)k_adapt_plan, dim3(1), dim3(1024), 0, s, plan, true);
   if (e == cudaSuccess) {
     // Blocks of a tile: the fewest chunks of 32 columns one after another, six
-    // more for a tile's start and sum, with some tiles that are not full; and
-    // chains of additions that stay exact (11 chunks per accumulator, see k_adapt_shrink).
+    // more for a tile's start and sum, with some tiles that are not full; but chains
+    // of additions that stay exact (four of each chunk, up to 37 to an accumulator,
+    // see k_adapt_shrink: 41 were off by 1.06e-6, twice what 32-bit sums are), where
+    // need be with twice the largest portable cluster.
     const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1, full = n_tok / 128 + 1, guess = full + std::min(h->slots, full) / 2;
     const int n_acc = shrink_accs(h->R32) - (f32 ? 1 : 0);
-    int ks = LR_CLUSTER;
-    long long best = -1;
+    int ks = 0;
+    long long best = 0;
     for (int c = LR_CLUSTER; c >= 1; c--) {
       const long long chunks = (K / 32 + c - 1) / c, cost = (guess + h->clusters[c] - 1) / h->clusters[c] * (chunks + 6);
-      if (best < 0 || (cost < best && chunks <= 11 * n_acc)) best = cost, ks = c;
+      if (4 * chunks <= 37 * n_acc && (!ks || cost < best)) best = cost, ks = c;
     }
+    if (!ks) ks = h->clusters[2 * LR_CLUSTER] ? 2 * LR_CLUSTER : LR_CLUSTER;
     const int grid = std::min(h->clusters[ks], most) * ks;
     void *args[] = {&a, &ks};
     e = launch_cluster(f.shrink, grid, ks, LR_WARPS * 32 + 32, LR_SMEM, s, args);

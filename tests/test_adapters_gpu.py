@@ -114,6 +114,22 @@ def test_ranks(rank, n):
     _run("bf16", "fp32", 384, 1056, [rank, 2], [t % 2 for t in range(n)], rank)
 
 
+@pytest.mark.parametrize("rank,n_in", [(100, 8192), (250, 4096), (64, 16384), (16, 65536)])
+def test_long_sums(rank, n_in):
+    """Sums over so many columns stay as exact as 32-bit ones: the result as a
+    whole is off by less than 2^-19 (the operands' split alone may take 2^-20)."""
+    n, n_out = 200, 256
+    h, a, b, s = _handle([rank], n_out, n_in, "bf16", n, 19)
+    x, base = torch.randn(n, n_in), torch.zeros(n, n_out)
+    slots = torch.zeros(n, dtype=torch.int32)
+    y = h.forward(x.cuda(), slots.cuda(), torch.empty(n, n_out).cuda(), base=base.cuda())
+    ref, tol = _expect(x, slots, base, a, b, s)
+    _close(y, ref, tol)
+    off = float((y.double().cpu() - ref).norm() / ref.norm())
+    print(f"rank {rank}, {n_in} columns: off by {off:.2e}")
+    assert off < 2.0 ** -19
+
+
 def test_many_slots():
     """A batch of more adapters than a warp has lanes, most with one token."""
     ranks = [1 + (3 * i) % 17 for i in range(300)]
