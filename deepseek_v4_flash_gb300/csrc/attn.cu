@@ -463,17 +463,19 @@ ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void
     if (!at_dev_ptr(shared_len) || (group_start && !at_dev_ptr(group_start))) return DS4MOE_ERR_INVALID_ARG;
     // With a window a row sees few of the shared positions, or none; and where
     // even a table full of them would gain nothing: the plain call.
-    a.cost = h->share_always ? ShareCost{1.0f, 0.0f, 0.0f, 0.0f} : share_cost(d, n_seq, n_new);
-    if (d.window == 0 && a.cost.gain(a.kv.width * a.kv.page_size, n_seq) > a.cost.least) {
-      a.shared_len = shared_len, a.group_start = group_start, a.n_groups = n_groups, a.batch = n_seq;
-      a.pre = h->shared.pre, a.pre_log = h->shared.pre_log;
+    const ShareCost cost = h->share_always ? ShareCost{1.0f, 0.0f, 0.0f, 0.0f} : share_cost(d, n_seq, n_new);
+    if (d.window == 0 && cost.gain(a.kv.width * a.kv.page_size, n_seq) > cost.least) {
+      SharedArgs sa = {};
+      static_cast<AttnArgs &>(sa) = a;
+      sa.cost = cost, sa.shared_len = shared_len, sa.group_start = group_start, sa.n_groups = n_groups, sa.batch = n_seq;
+      sa.pre = h->shared.pre, sa.pre_log = h->shared.pre_log;
       int launches = 0;
-      cudaError_t e = launch_attn_prefix(a, d.head_dim, d.dtype, h->tile, h->shared, h->n_sm, &launches, (cudaStream_t)stream);
+      cudaError_t e = launch_attn_prefix(sa, d.head_dim, d.dtype, h->tile, h->shared, h->n_sm, &launches, (cudaStream_t)stream);
       if (e == cudaSuccess && rows16) {
-        e = launch_attn_decode(a, d.head_dim, d.dtype, true, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
+        e = launch_attn_decode(sa, d.head_dim, d.dtype, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
         launches++;
       } else if (e == cudaSuccess) {
-        e = launch_attn_own(a, d.head_dim, d.dtype, h->tile, h->n_sm, &launches, (cudaStream_t)stream);
+        e = launch_attn_own(sa, d.head_dim, d.dtype, h->tile, h->n_sm, &launches, (cudaStream_t)stream);
       }
       h->launches += launches;
       return at_status(e);
@@ -486,7 +488,7 @@ ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void
   // rows, 1 sequence of 8192 14 and 25, 24 of them 35 and 39; 16 rows 18 and 25,
   // 39 and 39. 20 rows (two products of 16 in the streaming kernel): tiles, 25 and 39.
   if (rows16) {
-    const cudaError_t e = launch_attn_decode(a, d.head_dim, d.dtype, false, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
+    const cudaError_t e = launch_attn_decode(a, d.head_dim, d.dtype, h->part, h->ticket, h->n_sm, (cudaStream_t)stream);
     h->launches++;
     return at_status(e);
   }

@@ -106,7 +106,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs &a, int b, bool &bad)
 // ---- a batch with shared positions
 
 // Shared positions of group g, within what the table holds.
-__device__ __forceinline__ int shared_of(const AttnArgs &a, int g, bool &bad) {
+__device__ __forceinline__ int shared_of(const SharedArgs &a, int g, bool &bad) {
   const int l = a.shared_len[g], s = min(max(l, 0), a.kv.width * a.kv.page_size);
   bad |= s != l;
   return s;
@@ -115,7 +115,7 @@ __device__ __forceinline__ int shared_of(const AttnArgs &a, int g, bool &bad) {
 // The group of a call without a planning launch: its sequences (the bounds
 // brought into the batch and in order, as clean_rows does), and the shared
 // positions that are read once.
-__device__ __forceinline__ int2 one_group(const AttnArgs &a, int &s, bool &bad) {
+__device__ __forceinline__ int2 one_group(const SharedArgs &a, int &s, bool &bad) {
   const int r0 = a.group_start ? a.group_start[0] : 0, r1 = a.group_start ? a.group_start[1] : a.batch;
   s = shared_of(a, 0, bad);
   const int c0 = clamp_row(r0, a.batch), c1 = max(clamp_row(r1, a.batch), c0);
@@ -126,7 +126,7 @@ __device__ __forceinline__ int2 one_group(const AttnArgs &a, int &s, bool &bad) 
 
 // Where sequence b's own positions begin. It shares its group's positions when
 // its first new token sees all of them.
-__device__ __forceinline__ int own_start(const AttnArgs &a, int b, int len) {
+__device__ __forceinline__ int own_start(const SharedArgs &a, int b, int len) {
   if (a.start) return a.start[b];
   bool bad = false;
   int s;
@@ -136,7 +136,7 @@ __device__ __forceinline__ int own_start(const AttnArgs &a, int b, int len) {
 
 // The rows of group g, no rows where nothing is read once; its positions; the
 // table's row through which they are read.
-__device__ __forceinline__ SeqInfo prefix_info(const AttnArgs &a, int g, int *tab) {
+__device__ __forceinline__ SeqInfo prefix_info(const SharedArgs &a, int g, int *tab) {
   SeqInfo i = {0, 0, 0};
   if (a.start) {
     i.tok0 = a.cu_q[g], i.len = a.plen[g];
@@ -158,6 +158,15 @@ __device__ __forceinline__ SeqInfo prefix_info(const AttnArgs &a, int g, int *ta
   }
   return i;
 }
+
+// (calls without shared positions)
+__device__ __forceinline__ int own_start(const AttnArgs &, int, int) { return 0; }
+__device__ __forceinline__ SeqInfo prefix_info(const AttnArgs &, int, int *) { return {0, 0, 0}; }
+// The results over the shared positions and log2 of their sums.
+__device__ __forceinline__ float *pre_results(const SharedArgs &a) { return a.pre; }
+__device__ __forceinline__ float *pre_results(const AttnArgs &) { return nullptr; }
+__device__ __forceinline__ float *pre_logs(const SharedArgs &a) { return a.pre_log; }
+__device__ __forceinline__ float *pre_logs(const AttnArgs &) { return nullptr; }
 
 // log2 of a sum of weights l relative to 2^m.
 __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : m + __log2f(l); }

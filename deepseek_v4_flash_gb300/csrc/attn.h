@@ -52,8 +52,13 @@ struct AttnArgs {
   // of a group's positions; which of its blocks have marked rows
   int32_t span, gsh;
   int *marked;
-  // A batch with shared positions (attn_shared.cu): their number for each group
-  // and the groups' bounds (null: one group of all sequences); then, from the
+  uint32_t *err;
+};
+
+// A call with shared positions (attn_shared.cu). (A type of its own: the other
+// calls' kernels keep their parameters, a small call 9.06 -> 8.8 us.)
+struct SharedArgs : AttnArgs {
+  // The positions' number for each group and the groups' bounds (null: one group of all sequences); then, from the
   // planning launch of a call of several groups or null, what of it is read once,
   // by which table row, and where each sequence's own positions begin; sequences
   // and groups of the call;
@@ -63,7 +68,6 @@ struct AttnArgs {
   int32_t batch, n_groups;
   float *pre, *pre_log;
   ShareCost cost;
-  uint32_t *err;
 };
 
 // Workspace of the tile kernel.
@@ -108,7 +112,9 @@ namespace ds4 {
 constexpr int AD_MAX_ROWS = 16;
 size_t attn_decode_part_floats(int n_sm);
 cudaError_t attn_decode_set_attributes();
-cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, bool shared, float *part, int *ticket, int n_sm,
+cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
+                               cudaStream_t s);
+cudaError_t launch_attn_decode(const SharedArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
                                cudaStream_t s);
 // attn_tile.cu: tiles of 128 rows on the tensor cores, every shape.
 size_t attn_tile_part_floats(int head_dim, int n_sm);
@@ -121,8 +127,8 @@ cudaError_t launch_attn_tile(const AttnArgs &a, int head_dim, int dtype, const T
 // where it needs one (which it notes in `a`), then every sequence's own ones.
 ShareCost share_cost(const ds4moe_attn_desc &d, int n_seq, int n_new);
 cudaError_t attn_shared_set_attributes(int dtype, int head_dim);
-cudaError_t launch_attn_prefix(AttnArgs &a, int head_dim, int dtype, const TileWork &w, const SharedWork &sw, int n_sm,
+cudaError_t launch_attn_prefix(SharedArgs &a, int head_dim, int dtype, const TileWork &w, const SharedWork &sw, int n_sm,
                                int *launches, cudaStream_t s);
-cudaError_t launch_attn_own(const AttnArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
+cudaError_t launch_attn_own(const SharedArgs &a, int head_dim, int dtype, const TileWork &w, int n_sm, int *launches,
                             cudaStream_t s);
 }  // namespace ds4

@@ -23,6 +23,8 @@
 // 701: 8.8 us, a chain of dependent reads and the join's round trips.
 // Rows of the cache that no query row sees are zero-filled on their way in, so
 // that a weight of 0 never meets what they hold.
+#include <type_traits>
+
 #include "attn.cuh"
 #include "internal.h"
 
@@ -76,6 +78,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+template <bool SHARED>
+using DecArgs = typename std::conditional<SHARED, SharedArgs, AttnArgs>::type;
+
 // A sequence's part in a decode call.
 struct DecSeq {
   int first, last, len;  // positions of its first and last new token
@@ -84,7 +89,7 @@ struct DecSeq {
   int units;             // at least one, so that every row is written
 };
 template <bool SHARED>
-__device__ __forceinline__ DecSeq dec_seq(const AttnArgs &a, int b, bool &bad) {
+__device__ __forceinline__ DecSeq dec_seq(const DecArgs<SHARED> &a, int b, bool &bad) {
   DecSeq s;
   const SeqInfo si = seq_info(a, b, bad);
   s.len = si.len, s.first = si.len - si.n, s.last = si.len - 1;
@@ -105,7 +110,7 @@ struct DecCursor {
   int b, kvh, lu;  // sequence, key-value head, unit of that pair
 };
 template <bool SHARED>
-__device__ __forceinline__ void dec_next(const AttnArgs &a, DecCursor &c) {
+__device__ __forceinline__ void dec_next(const DecArgs<SHARED> &a, DecCursor &c) {
   if (++c.lu < c.s.units) return;
   c.lu = 0;
   if (++c.kvh < a.n_kv) return;
@@ -117,7 +122,7 @@ __device__ __forceinline__ void dec_next(const AttnArgs &a, DecCursor &c) {
 // A sequence's units by lane (sequences b0 .. b0 + 31), inclusive prefix and
 // the warp's sum.
 template <bool SHARED>
-__device__ __forceinline__ long long dec_prefix(const AttnArgs &a, int b0, bool &bad, long long &incl, long long &sum) {
+__device__ __forceinline__ long long dec_prefix(const DecArgs<SHARED> &a, int b0, bool &bad, long long &incl, long long &sum) {
   const int lane = threadIdx.x & 31;
   const long long n = b0 + lane < a.n_seq ? (long long)dec_seq<SHARED>(a, b0 + lane, bad).units * a.n_kv : 0;
   incl = n;
@@ -132,7 +137,7 @@ __device__ __forceinline__ long long dec_prefix(const AttnArgs &a, int b0, bool 
 // The block's run of units [u0, u1) out of U, dealt to N blocks, and the
 // cursor at u0 (whole warp). False when there is nothing for this block.
 template <bool SHARED>
-__device__ __forceinline__ bool dec_start(const AttnArgs &a, int n_cta, long long &U, long long &N, long long &u0,
+__device__ __forceinline__ bool dec_start(const DecArgs<SHARED> &a, int n_cta, long long &U, long long &N, long long &u0,
                                         long long &u1, DecCursor &c) {
   long long incl, sum, n;
   bool bad = false;
@@ -184,7 +189,7 @@ __device__ __noinline__ void redo_row(const AttnArgs &a, int t, int h, int b, in
 // SHARED: the positions before each sequence's own ones are in a.pre, whose
 // result joins the row's as it is stored (attn_shared.cu).
 template <int DT, int D, bool SHARED>
-__global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_decode(const AttnArgs a, float *part, int *ticket, int n_cta) {
+__global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_decode(const DecArgs<SHARED> a, float *part, int *ticket, int n_cta) {
   constexpr int STAGE = 64 * D;  // a warp's 16 keys and 16 values; also 16 rows of O in 32 bits
   constexpr int NST = AD_RING<SHARED> / (AD_WARPS<SHARED> * STAGE);
   constexpr int CH = D / 8;      // 16-byte pieces of a row
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_
           pre_log[j] = -INFINITY, pre[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (r >= rows || cc.s.own == 0) continue;
           const long long at = (long long)(t0 + r / a.group) * a.n_heads + h0 + r % a.group;
-          pre_log[j] = a.pre_log[at], pre[j] = *reinterpret_cast<const float4 *>(a.pre + at * D + c);
+          pre_log[j] = pre_logs(a)[at], pre[j] = *reinterpret_cast<const float4 *>(pre_results(a) + at * D + c);
         }
       }
 #pragma unroll
@@ -570,14 +575,21 @@ cudaError_t attn_decode_set_attributes() {
   return cudaSuccess;
 }
 
-cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, bool shared, float *part, int *ticket, int n_sm,
-                               cudaStream_t s) {
-  int n_cta = shared ? 2 * n_sm : n_sm;
-  if (!shared && n_cta > AD_MAX_BLOCKS) n_cta = AD_MAX_BLOCKS;
+template <bool SHARED>
+static cudaError_t launch(const DecArgs<SHARED> &a, int head_dim, int dtype, float *part, int *ticket, int n_cta, cudaStream_t s) {
   void *args[] = {(void *)&a, &part, &ticket, &n_cta};
-  const void *fn = dtype == DS4MOE_DT_BF16 ? dec_fn<DS4MOE_DT_BF16>(head_dim, shared) : dec_fn<DS4MOE_DT_F16>(head_dim, shared);
-  const int threads = 32 * (shared ? AD_WARPS<true> : AD_WARPS<false>);
-  return launch_pdl(fn, dim3(n_cta), dim3(threads), shared ? AD_RING<true> : AD_RING<false>, s, args, true);
+  const void *fn = dtype == DS4MOE_DT_BF16 ? dec_fn<DS4MOE_DT_BF16>(head_dim, SHARED) : dec_fn<DS4MOE_DT_F16>(head_dim, SHARED);
+  return launch_pdl(fn, dim3(n_cta), dim3(AD_WARPS<SHARED> * 32), AD_RING<SHARED>, s, args, true);
+}
+
+cudaError_t launch_attn_decode(const AttnArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
+                               cudaStream_t s) {
+  return launch<false>(a, head_dim, dtype, part, ticket, n_sm > AD_MAX_BLOCKS ? AD_MAX_BLOCKS : n_sm, s);
+}
+
+cudaError_t launch_attn_decode(const SharedArgs &a, int head_dim, int dtype, float *part, int *ticket, int n_sm,
+                               cudaStream_t s) {
+  return launch<true>(a, head_dim, dtype, part, ticket, 2 * n_sm, s);
 }
 
 }  // namespace ds4

@@ -22,7 +22,7 @@ constexpr float SHARE_LEAST = 20000.0f;
 // Groups' bounds, ascending in [0, n_seq] (see clean_rows), as rows; the shared
 // positions that are read once, and the first sequence that reaches past them,
 // through whose table that happens; where each sequence's own positions begin.
-__global__ void __launch_bounds__(1024) k_shared_plan(const AttnArgs a, int32_t *cu, int32_t *plen, int32_t *ptab, int32_t *start) {
+__global__ void __launch_bounds__(1024) k_shared_plan(const SharedArgs a, int32_t *cu, int32_t *plen, int32_t *ptab, int32_t *start) {
   __shared__ int s_top[32], s_base;
   __shared__ float s_gain[32];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, n_groups = a.n_groups;
@@ -102,7 +102,7 @@ cudaError_t attn_shared_set_attributes(int dtype, int D) {
   return e == cudaSuccess ? set_tile_attributes<AT_OWN>(dtype, D) : e;
 }
 
-cudaError_t launch_attn_prefix(AttnArgs &a, int D, int dtype, const TileWork &w, const SharedWork &sw, int n_sm, int *launches,
+cudaError_t launch_attn_prefix(SharedArgs &a, int D, int dtype, const TileWork &w, const SharedWork &sw, int n_sm, int *launches,
                                cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   // one group, of no more than AT_WALK row groups of a row at least: no planning launch (3 us)
@@ -113,13 +113,13 @@ cudaError_t launch_attn_prefix(AttnArgs &a, int D, int dtype, const TileWork &w,
     ++*launches;
     a.plen = sw.plen, a.ptab = sw.ptab, a.start = sw.start;
   }
-  AttnArgs p = a;
+  SharedArgs p = a;
   p.n_seq = a.n_groups, p.cu_q = a.start ? w.cu : nullptr;
   if (e == cudaSuccess) e = launch_tile<AT_PREFIX>(p, D, dtype, w, n_sm, launches, s);
   return e;
 }
 
-cudaError_t launch_attn_own(const AttnArgs &a, int D, int dtype, const TileWork &w, int n_sm, int *launches, cudaStream_t s) {
+cudaError_t launch_attn_own(const SharedArgs &a, int D, int dtype, const TileWork &w, int n_sm, int *launches, cudaStream_t s) {
   return launch_tile<AT_OWN>(a, D, dtype, w, n_sm, launches, s);
 }
 

@@ -49,6 +49,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "internal.h"
@@ -65,6 +66,9 @@ namespace ds4 {
 //   AT_OWN     there, every sequence over its positions behind the shared
 //              ones, joined with its rows' AT_PREFIX results.
 enum { AT_ALL = 0, AT_PREFIX = 1, AT_OWN = 2 };
+
+template <int MODE>
+using Args = typename std::conditional<MODE == AT_ALL, AttnArgs, SharedArgs>::type;
 
 // Whether row groups come from row bounds (ragged) or are the new tokens of
 // every sequence.
@@ -301,7 +305,7 @@ struct Sched {
   long long U, N;                 // the call's units, the gangs that have some
 
   // Rows and length of a sequence (whole warp, the same one).
-  __device__ __forceinline__ SeqInfo seq(const AttnArgs &a, const TileArgs &t, int bb) const {
+  __device__ __forceinline__ SeqInfo seq(const Args<MODE> &a, const TileArgs &t, int bb) const {
     if (ragged<MODE>(a) && !t.first) {
       SeqInfo s;
       s.tok0 = __shfl_sync(0xffffffffu, row0, bb), s.n = __shfl_sync(0xffffffffu, row1, bb) - s.tok0;
@@ -314,7 +318,7 @@ struct Sched {
   }
   // A ragged call without a plan (up to 32 sequences): its row bounds, made
   // ascending as k_attn_plan does.
-  __device__ __forceinline__ void read_rows(const AttnArgs &a, bool &bad) {
+  __device__ __forceinline__ void read_rows(const Args<MODE> &a, bool &bad) {
     const int lane = threadIdx.x & 31;
     const bool in = lane < a.n_seq;
     if (MODE == AT_PREFIX) {
@@ -338,7 +342,7 @@ struct Sched {
   }
 
   // the current item's sequence and rows; its tiles
-  __device__ __forceinline__ int load(const AttnArgs &a, const TileArgs &t, int member_rt, SegOf<MODE> &s) const {
+  __device__ __forceinline__ int load(const Args<MODE> &a, const TileArgs &t, int member_rt, SegOf<MODE> &s) const {
     const SeqInfo si = seq(a, t, b);
     s.b = b, s.kvh = kvh, s.len = si.len;
     if (MODE == AT_PREFIX) {
@@ -367,12 +371,12 @@ struct Sched {
   }
 
   // units of the tokens t0 .. t0 + n - 1 of a sequence
-  static __device__ __forceinline__ int units(const AttnArgs &a, int gsh, const SeqInfo &si, int t0, int n) {
+  static __device__ __forceinline__ int units(const Args<MODE> &a, int gsh, const SeqInfo &si, int t0, int n) {
     if (MODE == AT_PREFIX) return AT_ITEM + max(1, tiles_of(range_groups(a, si.len - 1, si.len - 1, gsh), gsh));
     const int p0 = si.len - si.n + t0;
     return AT_ITEM + max(1, tiles_of(range_groups(a, p0, p0 + n - 1, gsh), gsh));
   }
-  __device__ __forceinline__ int seq_units(const AttnArgs &a, int gsh, int bb, bool &bad) const {
+  __device__ __forceinline__ int seq_units(const Args<MODE> &a, int gsh, int bb, bool &bad) const {
     const SeqInfo si = seq_info(a, bb, bad);
     if (MODE == AT_OWN) return AT_ITEM + max(1, tiles_of(own_groups(own_start(a, bb, si.len), si.len - 1, gsh), gsh));
     return units(a, gsh, si, 0, si.n);
@@ -380,7 +384,7 @@ struct Sched {
 
   // Row groups of all sequences in order: their units' sum, or (r >= 0) the
   // one that holds unit r, into b, t0 and item0 (relative to the sum's start).
-  __device__ long long walk(const AttnArgs &a, const TileArgs &t, long long r) {
+  __device__ long long walk(const Args<MODE> &a, const TileArgs &t, long long r) {
     const int lane = threadIdx.x & 31;
     long long base = 0, mine = 0;
     for (int l = 0; l < a.n_seq; l++) {
@@ -414,7 +418,7 @@ struct Sched {
   }
 
   // Whole warp. False when gang g has no tiles.
-  __device__ bool init(const AttnArgs &a, const TileArgs &t, int g, int nt, bool &bad) {
+  __device__ bool init(const Args<MODE> &a, const TileArgs &t, int g, int nt, bool &bad) {
     const int lane = threadIdx.x & 31;
     long long head = 0;  // ragged: units of one key-value head
     int n_idx = 0;
@@ -489,7 +493,7 @@ struct Sched {
   }
 
   // The next item; item0 = U after the last one.
-  __device__ __forceinline__ void advance(const AttnArgs &a, const TileArgs &t) {
+  __device__ __forceinline__ void advance(const Args<MODE> &a, const TileArgs &t) {
     bool bad = false;
     item0 = item1;
     if (item0 >= U) return;
@@ -510,7 +514,7 @@ struct Sched {
     }
   }
 
-  __device__ __forceinline__ bool next(const AttnArgs &a, const TileArgs &t, int member_rt, SegOf<MODE> &s) {
+  __device__ __forceinline__ bool next(const Args<MODE> &a, const TileArgs &t, int member_rt, SegOf<MODE> &s) {
     if (u >= u1 || (!t.whole && u1 < item1 && u1 - item0 <= AT_ITEM)) return false;  // (the next gang's from its start)
     const int n_kt = load(a, t, member_rt, s);
     const long long e = t.whole || item1 < u1 ? item1 : u1;
@@ -528,7 +532,7 @@ struct Sched {
 // calls do without (Sched::walk, in every block): up to AT_WALK groups of up to
 // 32 sequences a block's walk is shorter than this kernel's 4 to 6 us.
 template <int MODE>
-__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, const int32_t *cu, int32_t *clean, int span, int gsh,
+__global__ void __launch_bounds__(1024) k_attn_plan(const Args<MODE> a, const int32_t *cu, int32_t *clean, int span, int gsh,
                                                 long long *first, int2 *info, int *count, int *seq_first) {
   __shared__ long long warp_sum[32];
   __shared__ long long s_base;
@@ -681,7 +685,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 template <int DT, int D, int NT, bool PAIR, int MODE>
 __global__ void __launch_bounds__(128 + 256 * NT, 1)
-    k_attn_tile(const __grid_constant__ TileMaps maps, const AttnArgs a, const TileArgs t) {
+    k_attn_tile(const __grid_constant__ TileMaps maps, const Args<MODE> a, const TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
   // One window of dynamic shared memory, exactly what an SM has: a TMA tile
   // in the 128-byte swizzle starts on a multiple of 1024 bytes.
@@ -1235,12 +1239,12 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         for (int i = 0; i < 8; i++) {
           const long long at = __shfl_sync(0xffffffffu, pre_at, (lane & 24) + i);
           uint4 u = make_uint4(0, 0, 0, 0);
-          if (at >= 0 && c < c1) u = *reinterpret_cast<const uint4 *>(a.pre + at + c + 4 * (lane & 7));
+          if (at >= 0 && c < c1) u = *reinterpret_cast<const uint4 *>(pre_results(a) + at + c + 4 * (lane & 7));
           z[4 * i] = u.x, z[4 * i + 1] = u.y, z[4 * i + 2] = u.z, z[4 * i + 3] = u.w;
         }
       };
       if (MODE == AT_OWN) {
-        if (pre_at >= 0) pre_log = a.pre_log[pre];
+        if (pre_at >= 0) pre_log = pre_logs(a)[pre];
         fetch(c0);
       }
       if (!none) {
@@ -1280,7 +1284,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
             for (int i = 0; i < 8; i++) {
               const long long at = __shfl_sync(0xffffffffu, valid ? pre : -1, (lane & 24) + i);
               if (at >= 0)
-                *reinterpret_cast<uint4 *>(a.pre + at * D + half * C::DV + c + 32 * h + 4 * (lane & 7)) =
+                *reinterpret_cast<uint4 *>(pre_results(a) + at * D + half * C::DV + c + 32 * h + 4 * (lane & 7)) =
                     make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
             }
           }
@@ -1340,7 +1344,7 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
         float *ml = t.part + ((size_t)(slot * NT + r) * 128 + row) * C::PITCH + C::DV;
         ml[0] = m, ml[1] = l;
       }
-      if (MODE == AT_PREFIX && valid && whole && ch == 0 && half == 0) a.pre_log[pre] = log_sum(m, l);
+      if (MODE == AT_PREFIX && valid && whole && ch == 0 && half == 0) pre_logs(a)[pre] = log_sum(m, l);
       tc_fence_before();
       __syncwarp();  // other lanes have stored parts of these rows
       if (MODE == AT_PREFIX) continue;  // (a row sees all that the products read)
@@ -1404,7 +1408,7 @@ __device__ __noinline__ void join_again(const AttnArgs &a, const TileArgs &t, un
 
 template <int DT, int D, int NT, bool PAIR, int MODE, int R>
 __global__ void __launch_bounds__(AJ_THREADS, MODE == AT_PREFIX ? 2 : D * R < 512 || D == 128 ? 4 : D * R <= 1024 ? 3 : 2)
-    k_attn_join(const __grid_constant__ AttnArgs a, const __grid_constant__ TileArgs t) {
+    k_attn_join(const __grid_constant__ Args<MODE> a, const __grid_constant__ TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
   constexpr int ROWS = C::JROWS * R, STEP = C::JROWS, P = MODE == AT_PREFIX ? 16 : 8 / R;  // rows of the block; distance of a thread's rows
   __shared__ unsigned long long s_nan;
@@ -1420,104 +1424,104 @@ __global__ void __launch_bounds__(AJ_THREADS, MODE == AT_PREFIX ? 2 : D * R < 51
   int gang = jid / t.members, gang1 = gang + 1;
   if (MODE == AT_PREFIX) {
     const int j = gang;
-    gang = t.gangs * j / t.join, gang1 = t.gangs * (j + 1) / t.join;
+    gang = t.gangs * j / t.join, gang1 = t.gangs * (j + 1) / t.join;  // (one at least)
   }
-  for (; gang < gang1; gang++) {
-  const int bid = gang * t.members + member;
-  const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
-  const int parts = d0.x;
-  if (MODE == AT_PREFIX && parts == 0) continue;
-  if (parts == 0) return;
-  const int tok0 = (rt + r) * t.tpt;  // one of the two is 0
-  const int rows = min(t.tpt, d1.y - tok0) * a.group;
-  if (MODE == AT_PREFIX && r0 >= rows) continue;
-  if (r0 >= rows) return;
-  if (tid == 0) s_nan = 0;
-  __syncthreads();
-  const int row0 = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
-  float m[R], l[R];
-  float4 x[R];
-  // AT_OWN: the rows' AT_PREFIX results (R = 1)
-  float pre_log[R];
-  float4 pre_x[R];
-  auto pre_of = [&](int k) {
-    const int row = row0 + k * STEP;
-    return (long long)(d1.x + tok0 + row / a.group) * a.n_heads + d0.z * a.group + row % a.group;
-  };
+  do {
+    const int bid = gang * t.members + member;
+    const int4 d0 = t.split[2 * gang], d1 = t.split[2 * gang + 1];
+    const int parts = d0.x;
+    if (MODE == AT_PREFIX && parts == 0) continue;
+    if (parts == 0) return;
+    const int tok0 = (rt + r) * t.tpt;  // one of the two is 0
+    const int rows = min(t.tpt, d1.y - tok0) * a.group;
+    if (MODE == AT_PREFIX && r0 >= rows) continue;
+    if (r0 >= rows) return;
+    if (tid == 0) s_nan = 0;
+    __syncthreads();
+    const int row0 = r0 + tid / (C::DV / 4), c = tid % (C::DV / 4) * 4;
+    float m[R], l[R];
+    float4 x[R];
+    // AT_OWN: the rows' AT_PREFIX results (R = 1)
+    float pre_log[R];
+    float4 pre_x[R];
+    auto pre_of = [&](int k) {
+      const int row = row0 + k * STEP;
+      return (long long)(d1.x + tok0 + row / a.group) * a.n_heads + d0.z * a.group + row % a.group;
+    };
 #pragma unroll
-  for (int k = 0; k < R; k++) {
-    pre_log[k] = -INFINITY, pre_x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (MODE == AT_OWN && d1.z > 0 && row0 + k * STEP < rows)
-      pre_log[k] = a.pre_log[pre_of(k)], pre_x[k] = *reinterpret_cast<const float4 *>(a.pre + pre_of(k) * D + half * C::DV + c);
-  }
+    for (int k = 0; k < R; k++) {
+      pre_log[k] = -INFINITY, pre_x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (MODE == AT_OWN && d1.z > 0 && row0 + k * STEP < rows)
+        pre_log[k] = pre_logs(a)[pre_of(k)], pre_x[k] = *reinterpret_cast<const float4 *>(pre_results(a) + pre_of(k) * D + half * C::DV + c);
+    }
 #pragma unroll
-  for (int k = 0; k < R; k++) m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int p0 = 0; p0 < parts; p0 += P) {
-    float2 ml[R][P];
-    float4 y[R][P];
+    for (int k = 0; k < R; k++) m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = 0; p0 < parts; p0 += P) {
+      float2 ml[R][P];
+      float4 y[R][P];
 #pragma unroll
-    for (int i = 0; i < P; i++) {
-      // the block where the item starts holds it in its second slot, the others in their first
-      const int slot = 2 * (bid + (p0 + i) * t.members) + (p0 + i == 0 ? 1 : 0);
-      const float *q0 = t.part + ((size_t)(slot * NT + r) * 128 + row0) * C::PITCH;
+      for (int i = 0; i < P; i++) {
+        // the block where the item starts holds it in its second slot, the others in their first
+        const int slot = 2 * (bid + (p0 + i) * t.members) + (p0 + i == 0 ? 1 : 0);
+        const float *q0 = t.part + ((size_t)(slot * NT + r) * 128 + row0) * C::PITCH;
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+          ml[k][i] = make_float2(-INFINITY, 0.0f), y[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (p0 + i < parts && row0 + k * STEP < rows) {
+            const float *q = q0 + (size_t)k * STEP * C::PITCH;
+            ml[k][i] = *reinterpret_cast<const float2 *>(q + C::DV), y[k][i] = *reinterpret_cast<const float4 *>(q + c);
+          }
+        }
+      }
 #pragma unroll
       for (int k = 0; k < R; k++) {
-        ml[k][i] = make_float2(-INFINITY, 0.0f), y[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (p0 + i < parts && row0 + k * STEP < rows) {
-          const float *q = q0 + (size_t)k * STEP * C::PITCH;
-          ml[k][i] = *reinterpret_cast<const float2 *>(q + C::DV), y[k][i] = *reinterpret_cast<const float4 *>(q + c);
+        float mn = m[k];
+#pragma unroll
+        for (int i = 0; i < P; i++) mn = fmaxf(mn, ml[k][i].x);
+        const float f = mn == -INFINITY ? 1.0f : ex2(m[k] - mn);
+        m[k] = mn, l[k] *= f, x[k].x *= f, x[k].y *= f, x[k].z *= f, x[k].w *= f;
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          const float g = ml[k][i].x == -INFINITY ? 0.0f : ex2(ml[k][i].x - mn);
+          const float4 z = y[k][i];
+          l[k] = fmaf(g, ml[k][i].y, l[k]);
+          x[k].x = fmaf(g, z.x, x[k].x), x[k].y = fmaf(g, z.y, x[k].y), x[k].z = fmaf(g, z.z, x[k].z), x[k].w = fmaf(g, z.w, x[k].w);
         }
       }
     }
 #pragma unroll
     for (int k = 0; k < R; k++) {
-      float mn = m[k];
-#pragma unroll
-      for (int i = 0; i < P; i++) mn = fmaxf(mn, ml[k][i].x);
-      const float f = mn == -INFINITY ? 1.0f : ex2(m[k] - mn);
-      m[k] = mn, l[k] *= f, x[k].x *= f, x[k].y *= f, x[k].z *= f, x[k].w *= f;
-#pragma unroll
-      for (int i = 0; i < P; i++) {
-        const float g = ml[k][i].x == -INFINITY ? 0.0f : ex2(ml[k][i].x - mn);
-        const float4 z = y[k][i];
-        l[k] = fmaf(g, ml[k][i].y, l[k]);
-        x[k].x = fmaf(g, z.x, x[k].x), x[k].y = fmaf(g, z.y, x[k].y), x[k].z = fmaf(g, z.z, x[k].z), x[k].w = fmaf(g, z.w, x[k].w);
+      const int row = row0 + k * STEP;
+      if (row >= rows) continue;
+      float inv = 1.0f / l[k], from = 0.0f;
+      if (MODE == AT_OWN) join_two(pre_log[k], m[k], l[k], from, inv);
+      float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
+      if (l[k] == 0.0f) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (MODE == AT_PREFIX) {
+        *reinterpret_cast<float4 *>(pre_results(a) + pre_of(k) * D + half * C::DV + c) = z;
+        if (c == 0 && half == 0) pre_logs(a)[pre_of(k)] = log_sum(m[k], l[k]);
+        continue;
       }
+      if (MODE == AT_OWN && from != 0.0f) {
+        const float4 p = pre_x[k];
+        z.x = fmaf(from, p.x, z.x), z.y = fmaf(from, p.y, z.y), z.z = fmaf(from, p.z, z.z), z.w = fmaf(from, p.w, z.w);
+      }
+      if (l[k] == l[k] && (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w)) atomicOr(&s_nan, 1ull << (row - r0));
+      const int tok = row / a.group, h = d0.z * a.group + row % a.group;
+      *reinterpret_cast<uint2 *>(a.out + (long long)(d1.x + tok0 + tok) * a.out_stride + (long long)h * D + half * C::DV + c) =
+          make_uint2(Half16<DT>::down(z.x, z.y), Half16<DT>::down(z.z, z.w));
     }
-  }
-#pragma unroll
-  for (int k = 0; k < R; k++) {
-    const int row = row0 + k * STEP;
-    if (row >= rows) continue;
-    float inv = 1.0f / l[k], from = 0.0f;
-    if (MODE == AT_OWN) join_two(pre_log[k], m[k], l[k], from, inv);
-    float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
-    if (l[k] == 0.0f) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (MODE == AT_PREFIX) {
-      *reinterpret_cast<float4 *>(a.pre + pre_of(k) * D + half * C::DV + c) = z;
-      if (c == 0 && half == 0) a.pre_log[pre_of(k)] = log_sum(m[k], l[k]);
-      continue;
-    }
-    if (MODE == AT_OWN && from != 0.0f) {
-      const float4 p = pre_x[k];
-      z.x = fmaf(from, p.x, z.x), z.y = fmaf(from, p.y, z.y), z.z = fmaf(from, p.z, z.z), z.w = fmaf(from, p.w, z.w);
-    }
-    if (l[k] == l[k] && (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w)) atomicOr(&s_nan, 1ull << (row - r0));
-    const int tok = row / a.group, h = d0.z * a.group + row % a.group;
-    *reinterpret_cast<uint2 *>(a.out + (long long)(d1.x + tok0 + tok) * a.out_stride + (long long)h * D + half * C::DV + c) =
-        make_uint2(Half16<DT>::down(z.x, z.y), Half16<DT>::down(z.z, z.w));
-  }
-  __syncthreads();
-  const unsigned long long again = s_nan;
-  if (MODE != AT_PREFIX && again) join_again<DT, D, NT, PAIR, MODE, ROWS>(a, t, again);
-  }
+    __syncthreads();
+    const unsigned long long again = s_nan;
+    if (MODE != AT_PREFIX && again) join_again<DT, D, NT, PAIR, MODE, ROWS>(a, t, again);
+  } while (MODE == AT_PREFIX && ++gang < gang1);
 }
 
 // The marked rows (AT_MARK), all in items that a block of the tile kernel did
 // alone: a block for each of its blocks.
 template <int DT, int D, int NT, bool PAIR, int MODE>
 __global__ void __launch_bounds__(AJ_THREADS)
-    k_attn_mend(const __grid_constant__ AttnArgs a, const __grid_constant__ TileArgs t) {
+    k_attn_mend(const __grid_constant__ Args<MODE> a, const __grid_constant__ TileArgs t) {
   using C = TileCfg<D, NT, PAIR>;
   pdl_launch_dependents();
   pdl_wait();
@@ -1640,7 +1644,7 @@ cudaError_t set_tile_attributes(int dtype, int D) {
 }
 
 template <int MODE>
-cudaError_t launch_tile(const AttnArgs &a, int D, int dtype, const TileWork &w, int n_sm, int *launches, cudaStream_t s) {
+cudaError_t launch_tile(const Args<MODE> &a, int D, int dtype, const TileWork &w, int n_sm, int *launches, cudaStream_t s) {
   const bool ragged = MODE == AT_ALL ? a.cu_q != nullptr : MODE == AT_PREFIX;
   TileArgs t = {};
   t.tpt = 128 / a.group;
@@ -1674,7 +1678,7 @@ cudaError_t launch_tile(const AttnArgs &a, int D, int dtype, const TileWork &w, 
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   int span = f.span * t.tpt;
-  AttnArgs p = a;
+  Args<MODE> p = a;
   p.span = ragged ? span : a.n_new, p.gsh = t.gsh, p.marked = w.marked;
   if (ragged && a.n_seq <= 32 && a.n_tok / span + a.n_seq <= AT_WALK) t.first = nullptr;
   if (ragged && t.first) {
