@@ -389,8 +389,9 @@ __device__ __forceinline__ uint32_t sw128(int r, int p) { return (uint32_t)(r * 
 template <bool INF>
 __device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const uint4 &x) {
   auto rest = [](uint32_t v) {
-    const float d = __uint_as_float(v) - __uint_as_float(v & 0xFFFFE000u);
-    return INF && isinf(__uint_as_float(v)) ? 0u : __float_as_uint(d);
+    const float f = __uint_as_float(v), d = f - __uint_as_float(v & 0xFFFFE000u);
+    if (!INF) return __float_as_uint(d);
+    return isinf(f) ? v : __float_as_uint(d == 0.0f ? f * 0x1p-30f : d);
   };
   sts4(hi_at, x.x, x.y, x.z, x.w);
   sts4(lo_at, rest(x.x), rest(x.y), rest(x.z), rest(x.w));

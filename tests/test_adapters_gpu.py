@@ -230,6 +230,34 @@ def test_numbers_that_are_not_finite(n):
     _close(y[rest], ref, torch.where(torch.isfinite(ref), tol, 0.0))
 
 
+@pytest.mark.parametrize("path", [1, 2])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("where", ["a", "b", "x"])
+@pytest.mark.parametrize("rank", [1, 40, 200])
+def test_infinities_beside_short_numbers(rank, where, kind, path):
+    """Operands of few bits, of which an infinity is one: the others' products
+    are exact, and what they leave out is 0, not 0 times infinity."""
+    dt, n_in, n_out = DTYPES[kind], 64, 140
+    a, b = torch.ones(rank, n_in, dtype=dt), torch.ones(n_out, rank, dtype=dt)
+    x, base = torch.ones(130, n_in), torch.zeros(130, n_out)
+    want = torch.full((130, n_out), float(n_in * rank))
+    if where == "a":
+        a[rank - 1, 3] = math.inf
+        want[:] = math.inf
+    elif where == "b":
+        b[7, rank - 1], b[131, 0] = math.inf, -math.inf
+        want[:, 7], want[:, 131] = math.inf, -math.inf
+    else:
+        x[5, 63], x[129, 0] = math.inf, -math.inf
+        want[5], want[129] = math.inf, -math.inf
+    h = _ds4().Adapters(n_out, n_in, 1, rank, kind, max_tokens=130)
+    h.set(0, a.cuda(), b.cuda(), 1.0)
+    h.debug_path(path)
+    y = torch.empty(130, n_out).cuda()
+    h.forward(x.cuda(), torch.zeros(130, dtype=torch.int32).cuda(), y, base=base.cuda())
+    assert torch.equal(y.cpu(), want)
+
+
 @pytest.mark.parametrize("n", [9, 150])
 def test_strided_rows_and_other_rows_left_alone(n):
     """x, base and y as parts of wider rows, y not 16-byte aligned."""
