@@ -233,7 +233,7 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
   constexpr unsigned long long C = 0xA2F9836E4E441529ull;
   const unsigned long long lo = m * C, hi = __umul64hi(m, C);
   const int s = 152 - (int)max(ex, 1u);
-  const unsigned long long t = s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? hi << (64 - s) | lo >> s : lo << -s;
+  const unsigned long long t = s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? hi << (64 - s) | lo >> s : s > -64 ? lo << -s : 0;
   return u >> 31 ? 0ull - t : t;
 }
 

@@ -176,6 +176,21 @@ def test_strided_rows():
     assert (wide[:, :2] == 3).all() and (wide[:, 6:] == 3).all()
 
 
+def test_frequencies_of_any_size():
+    """From the smallest to the largest fp32 numbers: turns of a whole number of
+    2^64ths, so that cosine and sine stay on the circle."""
+    freq = torch.tensor([1e-45, 1e-38, 1e-10, 1e8, 1e20, 5e26, 1e30, 3e38], dtype=torch.float32)
+    t = _setup("fp16", "fp32", 2, 1, 64, 16, [5], [5], 5, freq=freq, rot=16)
+    q = t["new"][0].cuda()
+    out = t["at"].append(t["cache"], t["new"][1].cuda(), t["new"][2].cuda(), t["kv_len"], rope=t["rope"], q=q)
+    size = (q[..., :8].double() ** 2 + q[..., 8:16].double() ** 2).sqrt()
+    got = (out[..., :8].double() ** 2 + out[..., 8:16].double() ** 2).sqrt()
+    # two roundings to fp16 of numbers up to size, and 2^-20 of cosine and sine
+    assert ((got - size).abs() <= size * (2.0 ** -10.5 + 2.0 ** -20) + 2.0 ** -24).all()
+    # the first three turn by 4e-10 at most: numbers up to 8 change by less than 1e-8
+    assert ((out - q)[..., :3].abs().double() <= q[..., :3].abs().double() * 2.0 ** -11 + 2.0 ** -25 + 1e-8).all()
+
+
 def test_rows_of_no_sequence_and_bad_places():
     """Rows behind the last sequence stay as they are; a row that the cache has
     no place for raises a flag and is rotated all the same."""
