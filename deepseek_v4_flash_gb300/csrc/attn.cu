@@ -433,12 +433,6 @@ const void *rope_fn(bool bf, bool f32) {
             : f32 ? (const void *)k_append_rope<F, true> : (const void *)k_append_rope<F, false>;
 }
 
-// Whether [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void *p, long long n, const void *q, long long m) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + (uintptr_t)m && b < a + (uintptr_t)n;
-}
-
 ds4moe_status attn_call(ds4moe_attn *h, const ds4moe_kv_cache *cache, const void *q, int64_t q_stride,
                         const int32_t *cu_q, bool ragged, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
                         int32_t n_new, void *out, int64_t out_stride, void *stream, const int32_t *shared_len = nullptr,
@@ -662,11 +656,11 @@ ds4moe_status ds4moe_kv_append_rope(ds4moe_attn *h, const ds4moe_kv_cache *cache
     if (!stride_ok(q_out_stride, q_row) || !al16(q_out) || !at_dev_ptr(q_out)) return DS4MOE_ERR_INVALID_ARG;
     // in place: every element is read and written by the same thread
     const bool same = q_new == q_out && !f32 && q_stride == q_out_stride;
-    const long long n = n_tok - 1, src = f32 ? 4 : 2;
-    const long long out_bytes = (n * q_out_stride + q_row) * 2;
-    if (!same && overlap(q_out, out_bytes, q_new, (n * q_stride + q_row) * src)) return DS4MOE_ERR_INVALID_ARG;
-    if (overlap(q_out, out_bytes, k_new, (n * k_stride + row) * src) ||
-        (v_new && overlap(q_out, out_bytes, v_new, (n * v_stride + row) * src)))
+    const int src = f32 ? 4 : 2;
+    auto over = [&](const void *p, long long stride, long long len) {
+      return rows_overlap(q_out, q_row * 2, q_out_stride * 2, p, len * src, stride * src, n_tok);
+    };
+    if ((!same && over(q_new, q_stride, q_row)) || over(k_new, k_stride, row) || (v_new && over(v_new, v_stride, row)))
       return DS4MOE_ERR_INVALID_ARG;
   }
   if (!at_dev_ptr(kv_len) || (cu_q && !at_dev_ptr(cu_q)) || !at_dev_ptr(rope->inv_freq) || !al16(rope->inv_freq))

@@ -56,7 +56,7 @@ struct AttnArgs {
 };
 
 // A call with shared positions (attn_shared.cu). (A type of its own: the other
-// calls' kernels keep their parameters, a small call 9.06 -> 8.8 us.)
+// calls' kernels keep their parameters.)
 struct SharedArgs : AttnArgs {
   // The positions' number for each group and the groups' bounds (null: one group of all sequences); then, from the
   // planning launch of a call of several groups or null, what of it is read once,

@@ -80,6 +80,17 @@ struct ds4moe_layer {
 
 namespace ds4 {
 
+// Whether two sets of n rows share a byte: rows of pb bytes, ps >= pb apart, and of
+// qb, qs apart. Sets with one distance may lie in each other's gaps (columns of
+// one matrix); of others whose ranges meet it is taken for granted.
+inline bool rows_overlap(const void *p, long long pb, long long ps, const void *q, long long qb, long long qs, int n) {
+  const long long d = (long long)((uintptr_t)q - (uintptr_t)p);
+  if (d >= (n - 1) * ps + pb || -d >= (n - 1) * qs + qb) return false;
+  if (ps != qs) return true;
+  const long long at = ((d % ps) + ps) % ps;
+  return at < pb || at + qb > ps;
+}
+
 // repack.cu
 cudaError_t repack_q2s(const uint8_t *src, uint8_t *dst, int n_mat, int rows, int K, int pair, int which,
                        cudaStream_t s);

@@ -259,6 +259,24 @@ def test_infinities_beside_short_numbers(rank, where, kind, path):
 
 
 @pytest.mark.parametrize("n", [9, 150])
+def test_columns_of_one_matrix(n):
+    """x, base and y as columns of the same rows."""
+    h, a, b, s = _handle([8, 20], 64, 96, "fp16", n, 21)
+    rows = torch.randn(n, 240).cuda()
+    before = rows.cpu()
+    x, base, y = rows[:, :96], rows[:, 100:164], rows[:, 172:236]
+    slots = torch.tensor([t % 3 - 1 for t in range(n)], dtype=torch.int32)
+    h.forward(x, slots.cuda(), y, base=base)
+    ref, tol = _expect(before[:, :96], slots, before[:, 100:164], a, b, s)
+    _close(y, ref, tol)
+    before[:, 172:236] = y.cpu()
+    assert torch.equal(rows.cpu(), before)
+    for bad in (rows[:, 95:159], rows[:, 163:227]):
+        with pytest.raises(_ds4().Ds4MoeError):
+            h.forward(x, slots.cuda(), bad, base=base)
+
+
+@pytest.mark.parametrize("n", [9, 150])
 def test_strided_rows_and_other_rows_left_alone(n):
     """x, base and y as parts of wider rows, y not 16-byte aligned."""
     for n_out, wide, off in ((64, 200, 8), (64, 131, 1), (33, 77, 3)):

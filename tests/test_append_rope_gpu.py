@@ -176,6 +176,21 @@ def test_strided_rows():
     assert (wide[:, :2] == 3).all() and (wide[:, 6:] == 3).all()
 
 
+@pytest.mark.parametrize("lens, runs", [([20, 9, 40], [5, 2, 30]), ([17], [1])])
+def test_columns_of_one_matrix_in_place(lens, runs):
+    """q, k and v as columns of one 16-bit matrix, q turned where it is."""
+    t = _setup("bf16", "bf16", 4, 2, 64, 16, lens, runs, 14, rot=32)
+    rows = torch.cat([x.flatten(1) for x in t["new"]], 1).cuda()
+    before = rows.clone()
+    q, k, v = rows[:, :256].unflatten(1, (4, 64)), rows[:, 256:384].unflatten(1, (2, 64)), rows[:, 384:].unflatten(1, (2, 64))
+    got = t["at"].append(t["cache"], k, v, t["kv_len"], cu_q=t["cu"].cuda(), rope=t["rope"], q=q, q_out=q)
+    _check(t, got)
+    assert torch.equal(rows[:, 256:], before[:, 256:])
+    for bad in (rows[:, 128:384], rows[:, 64:320]):  # over the keys; over the queries by part
+        with pytest.raises(t["ds4"].Ds4MoeError):
+            t["at"].append(t["cache"], k, v, t["kv_len"], cu_q=t["cu"].cuda(), rope=t["rope"], q=q, q_out=bad.unflatten(1, (4, 64)))
+
+
 def test_frequencies_of_any_size():
     """From the smallest to the largest fp32 numbers: turns of a whole number of
     2^64ths, so that cosine and sine stay on the circle."""
