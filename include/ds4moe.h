@@ -387,7 +387,8 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  *   base   [n_tok][n_out] fp32, base_stride apart; NULL or y itself (with its
  *          stride): y is added to
  *   y      [n_tok][n_out] fp32, y_stride apart; must not overlap x, nor base
- *          otherwise
+ *          otherwise (columns of one matrix do not; rows in gaps of another
+ *          distance in bytes are taken for overlapping: INVALID_ARG)
  *   Strides are below 2^31 elements.
  *   Enqueued on `stream` (one launch for few tokens, else three), no allocation,
  *   no synchronisation. Calls on one handle must not run concurrently (shared
@@ -516,7 +517,8 @@ ds4moe_status ds4moe_kv_append(ds4moe_attn *h, const ds4moe_kv_cache *cache, con
  *           src_dtype; may be NULL (then q_out too)
  *   q_out   the same rows in the cache's type, q_out_stride apart; may be q_new
  *           itself (of the cache's type, with the same stride), must not overlap
- *           the inputs otherwise. Rows of no sequence are left as they are; a
+ *           the inputs otherwise (columns of one matrix do not; rows in gaps of
+ *           another distance in bytes are taken for overlapping). Rows of no sequence are left as they are; a
  *           row whose position the cache has no place for is rotated all the same.
  * Other arguments, flags and errors as ds4moe_kv_append; INVALID_ARG also for a
  * rope that is not as below. */
