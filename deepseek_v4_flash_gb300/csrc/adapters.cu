@@ -431,7 +431,12 @@ constexpr int LR_SMEM = 224 * 1024;  // a block has an SM (and all of its tensor
 // to 24 bits, so a long chain of additions drifts: 256 of them (1024 columns)
 // were off by 4e-6 of the result, five times what 32-bit sums are. So chunks go
 // round several accumulators, the low parts of x to one of their own, added up
-// in 32 bits at the end.
+// in 32 bits at the end. Where the accumulators that there is room for would take
+// more than 37 additions each (ranks above 64 over wide inputs), a block takes its
+// columns in `rounds`, whose sums meet in 32 bits in V. Measured, error of the result
+// and time of 4096 tokens, in one round and so: rank 256, 8192 columns and 8192
+// outputs 1.8e-6 322 us, 1.2e-6 367 us; 65536 columns and 512 outputs 1.0e-5 729 us,
+// 1.2e-6 1512 us.
 constexpr int LR_WARPS = 8, LR_GROUPS = 2, LR_FEED = LR_WARPS * 32 / LR_GROUPS;
 // 32-column parts of a chunk: two, while two stages of them fit.
 __host__ __device__ constexpr int shrink_ch(int r32) { return r32 <= 128 ? 2 : 1; }
@@ -444,9 +449,10 @@ __host__ __device__ constexpr int shrink_stages(bool f32, int r32) {
 }
 __host__ __device__ constexpr int shrink_accs(int r32) { return 512 / r32 < 8 ? 512 / r32 : 8; }
 
-// WP: 16-byte pieces of A per thread and part, a 32nd of the largest rank.
-template <int DT, bool F32, int WP>
-__global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const AdaptArgs a, int ks) {
+// WP: 16-byte pieces of A per thread and part, a 32nd of the largest rank. MANY:
+// more than one round (of its own: the others' registers are all in use).
+template <int DT, bool F32, int WP, bool MANY>
+__global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const AdaptArgs a, int ks, int n_rounds) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[2 * 6 + 1];
   __shared__ uint32_t s_tmem;
@@ -474,8 +480,15 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
   pdl_launch_dependents();
   pdl_wait();
   const int k = (int)cluster_rank(), n_tiles = *a.n_tiles, n_cl = gridDim.x / ks;
-  // this block's parts of 32 columns and chunks
-  const int p0 = (a.K / 32) * k / ks, np = (a.K / 32) * (k + 1) / ks - p0, nc = (np + CH - 1) / CH;
+  // this block's parts of 32 columns; those of a round, and its chunks
+  const int all0 = (a.K / 32) * k / ks, all = (a.K / 32) * (k + 1) / ks - all0;
+  const int rounds = MANY ? n_rounds : 1;
+  int p0, np, nc;
+  auto set_round = [&](int r) {
+    const int from = all * r / rounds;
+    p0 = all0 + from, np = all * (r + 1) / rounds - from, nc = (np + CH - 1) / CH;
+  };
+  set_round(0);
   // accumulators of the high parts; the low parts' one comes after them
   const int n_acc = shrink_accs(a.R32) - (F32 ? 1 : 0);
   Waits ws;
@@ -485,9 +498,10 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
   int tok[XP];
   const uint16_t *ap;
   int r32 = 0;
-  // the next tile with a rank, from i on, and this thread's part of it
-  auto begin = [&](int i) {
+  // the next tile with a rank, from i on, round r of it, and this thread's part of that
+  auto begin = [&](int i, int r) {
     int4 tile = make_int4(0, 0, 0, 0);
+    if (MANY) set_round(r);
     for (; i < n_tiles; i += n_cl) {
       tile = a.tiles[i];
       if (tile.z >> 16) break;
@@ -540,7 +554,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     for (; st < 0; st += nst) lap--;
   };
   int tiles = 0;
-  int i = begin(blockIdx.x / ks);
+  int i = begin(blockIdx.x / ks, 0), round = 0;
   if (w < LR_WARPS) {
     if (i < n_tiles) {
       if (group == 0) ask_first(i);
@@ -551,6 +565,8 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
   while (i < n_tiles) {
     const int4 tile = a.tiles[i];
     const int rank = tile.z >> 16, rows = tile.z & 0xFFFF, r32_now = (rank + 31) & ~31;
+    const int np_now = np, nc_now = nc;
+    const bool again = MANY && round + 1 < rounds;  // the tile's next round follows
     int next;
     if (w < LR_WARPS) {
       int c = group;
@@ -581,8 +597,8 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
         if (lane == 0) mbar_arrive(full(st));
       }
       advance(nc + group - c);  // all warps' chunks follow on the tile's nc chunks
-      // the next tile's first chunks come in while this one is added up
-      next = begin(i + n_cl);
+      // the next tile's (or round's) first chunks come in while this one is added up
+      next = begin(again ? i : i + n_cl, again ? round + 1 : 0);
       if (next < n_tiles) {
         if (group == 0) ask_first(next);
         fetch(group);
@@ -614,9 +630,9 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
         }
         __syncwarp();
       }
-      next = begin(i + n_cl);
+      next = begin(again ? i : i + n_cl, again ? round + 1 : 0);
     }
-    if (nc) ws.wait(b_done, tiles & 1);
+    if (nc_now) ws.wait(b_done, tiles & 1);
     __syncwarp();
     tc_fence_after();
     // the block's sums, over the ring
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     if (w < LR_WARPS)
       for (int c = (w >> 2) * 16; c < r32_now; c += 32) {
         float v[16];
-        const int row = (w & 3) * 32 + lane, n_high = min(np, n_acc);  // (the others are not written)
+        const int row = (w & 3) * 32 + lane, n_high = min(np_now, n_acc);  // (the others are not written)
         const uint32_t t0 = tmem + ((uint32_t)((w & 3) * 32) << 16) + c;
 #pragma unroll
         for (int e = 0; e < 16; e++) v[e] = 0.0f;
@@ -635,7 +651,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
 #pragma unroll
           for (int e = 0; e < 16; e++) v[e] += q + 1 < n_high ? y[e] + z[e] : y[e];
         }
-        if (F32 && nc) {
+        if (F32 && nc_now) {
           float y[16], z[16];
           tmem_ld16x2(t0 + n_acc * a.R32, t0 + n_acc * a.R32, y, z);
 #pragma unroll
@@ -662,13 +678,18 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
       // what lies past the rank may be 0 x infinity
       s.x = c < rank ? s.x * scale : 0.0f, s.y = c + 1 < rank ? s.y * scale : 0.0f;
       s.z = c + 2 < rank ? s.z * scale : 0.0f, s.w = c + 3 < rank ? s.w * scale : 0.0f;
-      *reinterpret_cast<float4 *>(a.v + (long long)(tile.y + row) * a.R32 + c) = s;
+      float4 *v = reinterpret_cast<float4 *>(a.v + (long long)(tile.y + row) * a.R32 + c);
+      if (MANY && round) {  // (this thread stored the rounds before)
+        const float4 o = *v;
+        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+      }
+      *v = s;
     }
     cluster_arrive();
     cluster_wait();
     tc_fence_after();
-    tiles += nc != 0;
-    i = next;
+    tiles += nc_now != 0;
+    i = next, round = again ? round + 1 : 0;
   }
   if (!ws.ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
   tc_fence_before();
@@ -1003,13 +1024,16 @@ ds4moe_status ap_status(cudaError_t e) {
 }
 
 struct AdaptFns {
-  const void *token, *shrink, *expand;
+  const void *token, *shrink, *shrink_many, *expand;
 };
+template <int DT, bool F32, bool MANY>
+const void *shrink_of(int r32) {
+  return r32 <= 64 ? (const void *)k_adapt_shrink<DT, F32, 2, MANY> : r32 <= 128 ? (const void *)k_adapt_shrink<DT, F32, 4, MANY>
+                                                                                  : (const void *)k_adapt_shrink<DT, F32, 8, MANY>;
+}
 template <int DT, bool F32>
 AdaptFns fns_of(int r32) {
-  const void *shrink = r32 <= 64 ? (const void *)k_adapt_shrink<DT, F32, 2> : r32 <= 128 ? (const void *)k_adapt_shrink<DT, F32, 4>
-                                                                                        : (const void *)k_adapt_shrink<DT, F32, 8>;
-  return {(const void *)k_adapt_token<DT, F32>, shrink,
+  return {(const void *)k_adapt_token<DT, F32>, shrink_of<DT, F32, false>(r32), shrink_of<DT, F32, true>(r32),
           r32 <= 128 ? (const void *)k_adapt_expand<DT, true> : (const void *)k_adapt_expand<DT, false>};
 }
 AdaptFns adapt_fns(int dtype, bool f32, int r32) {
@@ -1076,10 +1100,10 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
   for (bool f32 : {false, true}) {
     const AdaptFns f = adapt_fns(dtype, f32, h->R32);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f.token, cudaFuncAttributeMaxDynamicSharedMemorySize, ((1 << 16) / LR_CLUSTER + 8) * 4);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f.expand, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f.shrink, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (const void *fn : {f.shrink, f.shrink_many, f.expand})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
+    for (const void *fn : {f.shrink, f.shrink_many})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int ks = 1; ks <= 2 * LR_CLUSTER && e == cudaSuccess; ks += ks < LR_CLUSTER ? 1 : LR_CLUSTER) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
@@ -1169,7 +1193,8 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
     // more for a tile's start and sum, with some tiles that are not full; but chains
     // of additions that stay exact (four of each chunk, up to 37 to an accumulator,
     // see k_adapt_shrink: 41 were off by 1.06e-6, twice what 32-bit sums are), where
-    // need be with twice the largest portable cluster.
+    // need be with twice the largest portable cluster and in rounds of eight chunks to
+    // an accumulator.
     const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1, full = n_tok / 128 + 1, guess = full + std::min(h->slots, full) / 2;
     const int n_acc = shrink_accs(h->R32) - (f32 ? 1 : 0);
     int ks = 0;
@@ -1178,10 +1203,14 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
       const long long chunks = (K / 32 + c - 1) / c, cost = (guess + h->clusters[c] - 1) / h->clusters[c] * (chunks + 6);
       if (4 * chunks <= 37 * n_acc && (!ks || cost < best)) best = cost, ks = c;
     }
-    if (!ks) ks = h->clusters[2 * LR_CLUSTER] ? 2 * LR_CLUSTER : LR_CLUSTER;
+    int rounds = 1;
+    if (!ks) {
+      ks = h->clusters[2 * LR_CLUSTER] ? 2 * LR_CLUSTER : LR_CLUSTER;
+      rounds = ((h->K / 32 + ks - 1) / ks + 8 * n_acc - 1) / (8 * n_acc);
+    }
     const int grid = std::min(h->clusters[ks], most) * ks;
-    void *args[] = {&a, &ks};
-    e = launch_cluster(f.shrink, grid, ks, LR_WARPS * 32 + 32, LR_SMEM, s, args);
+    void *args[] = {&a, &ks, &rounds};
+    e = launch_cluster(rounds > 1 ? f.shrink_many : f.shrink, grid, ks, LR_WARPS * 32 + 32, LR_SMEM, s, args);
     if (e == cudaSuccess) {
       const long long items = (long long)most * ((N + 127) / 128);
       e = launch_pdl(f.expand, dim3((unsigned)std::min<long long>(items, h->n_sm)), dim3(LE_THREADS), LR_SMEM, s, plan, true);
