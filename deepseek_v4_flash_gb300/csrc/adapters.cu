@@ -432,8 +432,9 @@ constexpr int LR_SMEM = 224 * 1024;  // a block has an SM (and all of its tensor
 // were off by 4e-6 of the result, five times what 32-bit sums are. So chunks go
 // round several accumulators, the low parts of x to one of their own, added up
 // in 32 bits at the end. Where the accumulators that there is room for would take
-// more than 37 additions each (ranks above 64 over wide inputs), a block takes its
-// columns in `rounds`, whose sums meet in 32 bits in V. Measured, error of the result
+// more than 37 additions each (fp32 inputs: ranks above 128 from 4128 columns on,
+// above 64 from 12320, others from 28704; 16-bit ones, which need no accumulator for
+// low parts: 8224, 16416, 32800), a block takes its columns in `rounds`, whose sums meet in 32 bits in V. Measured, error of the result
 // and time of 4096 tokens, in one round and so: rank 256, 8192 columns and 8192
 // outputs 1.8e-6 322 us, 1.2e-6 367 us; 65536 columns and 512 outputs 1.0e-5 729 us,
 // 1.2e-6 1512 us.
