@@ -172,8 +172,12 @@ __device__ __forceinline__ float *pre_logs(const AttnArgs &) { return nullptr; }
 __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : m + __log2f(l); }
 
 // Joins a result with log2 sum `lp` and an accumulator relative to 2^m with sum
-// l: the factors of the two. Both 0: no score above -infinity.
-__device__ __forceinline__ void join_two(float lp, float m, float l, float &from, float &inv) {
+// l: the factors of the two, 0 for one without a score above -infinity. Both
+// results are multiplied and added whatever the factors, for 0 times a NaN or an
+// infinity that a row sees is NaN, as it is among the positions of one call;
+// `zero`: the row has no score above -infinity at all, and is 0 whatever the values.
+__device__ __forceinline__ void join_two(float lp, float m, float l, float &from, float &inv, bool &zero) {
+  zero = l == 0.0f && lp == -INFINITY;
   if (l == 0.0f) {
     from = lp == -INFINITY ? 0.0f : lp == lp ? 1.0f : lp, inv = 0.0f;
     return;

@@ -445,14 +445,14 @@ __global__ void __launch_bounds__(AD_WARPS<SHARED> * 32, SHARED ? 2 : 1) k_attn_
       auto store = [&](int r, int c, float4 x, float m, float l, int piece) {
         const int t = cc.b * a.n_new + r / a.group, h = cc.kvh * a.group + r % a.group;
         float inv = 1.0f / l, from = 0.0f;
-        if (SHARED) join_two(pre_log[piece], m, l, from, inv);
+        bool zero = l == 0.0f;  // no score above -infinity (whatever the values: 0 x NaN is NaN)
+        if (SHARED) join_two(pre_log[piece], m, l, from, inv, zero);
         x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-        // no score above -infinity (whatever the values: 0 x NaN is NaN)
-        if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (SHARED && from != 0.0f) {
+        if (SHARED) {
           const float4 p = pre[piece];
           x.x = fmaf(from, p.x, x.x), x.y = fmaf(from, p.y, x.y), x.z = fmaf(from, p.z, x.z), x.w = fmaf(from, p.w, x.w);
         }
+        if (zero) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const uint2 u = make_uint2(Half16<DT>::down(x.x, x.y), Half16<DT>::down(x.z, x.w));
         *reinterpret_cast<uint2 *>(a.out + (long long)t * a.out_stride + (long long)h * D + c) = u;
         if (nan_rows_possible && l == l) {

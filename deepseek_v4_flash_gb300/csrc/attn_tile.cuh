@@ -1262,7 +1262,8 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
       }
       float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
       float from = 0.0f;  // AT_OWN: the factor of the AT_PREFIX result
-      if (MODE == AT_OWN && whole) join_two(pre_log, m, none ? 0.0f : l, from, inv);
+      bool zero = false;       // AT_OWN: no score above -infinity, neither here nor there
+      if (MODE == AT_OWN && whole) join_two(pre_log, m, none ? 0.0f : l, from, inv, zero);
       const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
       // rows 8 (lane / 8) + i are this lane's to store, 16 bytes at piece lane % 8
       float *pp = t.part + ((size_t)(slot * NT + r) * 128 + (w & 3) * 32 + (lane & 24)) * C::PITCH + 4 * (lane & 7);
@@ -1309,9 +1310,8 @@ __global__ void __launch_bounds__(128 + 256 * NT, 1)
             for (int i = 0; i < 16; i++) {
               float x0 = x[2 * i] * inv, x1 = x[2 * i + 1] * inv;
               if (MODE == AT_OWN) {
-                // (a row without own positions: whatever the values, 0 x NaN is NaN)
-                if (l == 0.0f) x0 = x1 = 0.0f;
-                if (from != 0.0f) x0 = fmaf(from, __uint_as_float(zc[2 * i]), x0), x1 = fmaf(from, __uint_as_float(zc[2 * i + 1]), x1);
+                x0 = fmaf(from, __uint_as_float(zc[2 * i]), x0), x1 = fmaf(from, __uint_as_float(zc[2 * i + 1]), x1);
+                if (zero) x0 = x1 = 0.0f;
               }
               nan |= x0 != x0 || x1 != x1;
               y[16 * h + i] = Half16<DT>::down(x0, x1);
@@ -1493,18 +1493,21 @@ __global__ void __launch_bounds__(AJ_THREADS, MODE == AT_PREFIX ? 2 : D * R < 51
     for (int k = 0; k < R; k++) {
       const int row = row0 + k * STEP;
       if (row >= rows) continue;
-      float inv = 1.0f / l[k], from = 0.0f;
-      if (MODE == AT_OWN) join_two(pre_log[k], m[k], l[k], from, inv);
+      // (AT_PREFIX without a score above -infinity: a value's NaN stays for the join)
+      float inv = MODE == AT_PREFIX && l[k] == 0.0f ? 0.0f : 1.0f / l[k], from = 0.0f;
+      bool zero = MODE != AT_PREFIX && l[k] == 0.0f;
+      if (MODE == AT_OWN) join_two(pre_log[k], m[k], l[k], from, inv, zero);
       float4 z = make_float4(x[k].x * inv, x[k].y * inv, x[k].z * inv, x[k].w * inv);
-      if (l[k] == 0.0f) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (MODE != AT_OWN && zero) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (MODE == AT_PREFIX) {
         *reinterpret_cast<float4 *>(pre_results(a) + pre_of(k) * D + half * C::DV + c) = z;
         if (c == 0 && half == 0) pre_logs(a)[pre_of(k)] = log_sum(m[k], l[k]);
         continue;
       }
-      if (MODE == AT_OWN && from != 0.0f) {
+      if (MODE == AT_OWN) {
         const float4 p = pre_x[k];
         z.x = fmaf(from, p.x, z.x), z.y = fmaf(from, p.y, z.y), z.z = fmaf(from, p.z, z.z), z.w = fmaf(from, p.w, z.w);
+        if (zero) z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
       if (l[k] == l[k] && (z.x != z.x || z.y != z.y || z.z != z.z || z.w != z.w)) atomicOr(&s_nan, 1ull << (row - r0));
       const int tok = row / a.group, h = d0.z * a.group + row % a.group;
