@@ -346,7 +346,12 @@ class Dense:
             _check(lib().ds4moe_dense_forward(self._h, _ptr(x), n, _ptr(y), _stream(stream)), "ds4moe_dense_forward")
             return y
         _need(x.is_contiguous() and y.is_contiguous() and x.dtype == torch.float32, "x and y: contiguous, x fp32")
-        call = adapters._args(x[:n], slots, y[:n], None)  # refused before anything is enqueued
+        # refused before anything is enqueued: the arguments, then what
+        # ds4moe_adapters_forward would refuse behind the product
+        call = adapters._args(x[:n], slots, y[:n], None)
+        xp, yp = x.data_ptr(), y.data_ptr()
+        _check(int(n > adapters.max_tokens or xp % 16 != 0 or (xp < yp + 4 * n * self.n_out and yp < xp + 4 * n * self.n_in)),
+               "ds4moe_adapters_forward")
         _check(lib().ds4moe_dense_forward(self._h, _ptr(x), n, _ptr(y), _stream(stream)), "ds4moe_dense_forward")
         adapters._forward(call, stream)
         return y
@@ -445,6 +450,7 @@ class Adapters:
         _check(lib().ds4moe_adapters_create(n_out, n_in, n_slots, max_rank, DTYPE[dtype], max_tokens, ctypes.byref(h)),
                "ds4moe_adapters_create")
         self._h, self.n_out, self.n_in, self.n_slots, self.max_rank = h, n_out, n_in, n_slots, max_rank
+        self.max_tokens = max_tokens
         self._dt, self._code = _torch_dtype(DTYPE[dtype]), DTYPE[dtype]
 
     def close(self):
