@@ -341,7 +341,7 @@ class Dense:
         elif slots is not None:
             raise ValueError("slots: only with adapters")
         if y is None:
-            y = torch.empty((n, self.n_out), dtype=torch.float32, device=x.device)
+            y = _empty((n, self.n_out), torch.float32, x.device, stream)
         if adapters is None:
             _check(lib().ds4moe_dense_forward(self._h, _ptr(x), n, _ptr(y), _stream(stream)), "ds4moe_dense_forward")
             return y

@@ -1,9 +1,13 @@
 """Dense.forward(adapters=): what is refused is refused before anything is
-enqueued."""
+enqueued, and an output that it allocates for another stream comes from that
+stream's memory."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+SLEEP = 100_000_000  # cycles: some 50 ms
+
 
 def _dense(n_out, n_in, n_tok, adapter_tokens=None):
     import deepseek_v4_flash_gb300 as ds4
@@ -44,3 +48,51 @@ def test_refused_before_anything_is_enqueued():
     assert dense.forward(x[:4], y[:4], adapters=h, slots=slots[:4]) is not None
     assert (y[:4] != 3).any() and (y[4:] == 3).all()
     assert torch.equal(dense.forward(x, y, adapters=h, slots=slots[:3], n_tok=3)[:3], dense.forward(x[:3], adapters=h, slots=slots[:3]))
+
+
+@pytest.mark.parametrize("with_adapters", [False, True])
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_freed_on_the_current_stream(raw, with_adapters):
+    """A block of the output's size is freed while the current stream has yet to
+    read it: the call on the other stream must not get it."""
+    n_out, n_in, n = 4096, 256, 64
+    ds4, dense, h, x = _dense(n_out, n_in, n)
+    kw = dict(adapters=h, slots=torch.tensor([t % 3 - 1 for t in range(n)], dtype=torch.int32).cuda()) if with_adapters else {}
+    want = dense.forward(x, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    kept = [torch.empty_like(want) for _ in range(16)]  # noqa: F841 (blocks of the size that were free before)
+    held = torch.full_like(want, 7)
+    torch.cuda.synchronize()
+    where = held.data_ptr()
+    torch.cuda._sleep(SLEEP)
+    copy = held.clone()  # queued behind the sleep
+    del held
+    got = dense.forward(x, stream=side.cuda_stream if raw else side, **kw)
+    assert got.data_ptr() != where
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and (copy == 7).all()
+
+
+@pytest.mark.parametrize("with_adapters", [False, True])
+@pytest.mark.parametrize("raw", [False, True])
+def test_output_dropped_while_the_current_stream_reads_it(raw, with_adapters):
+    n_out, n_in, n = 4096, 256, 64
+    ds4, dense, h, x = _dense(n_out, n_in, n)
+    kw = dict(adapters=h, slots=torch.tensor([t % 3 - 1 for t in range(n)], dtype=torch.int32).cuda()) if with_adapters else {}
+    want = dense.forward(x, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if raw else side
+    kept = [torch.empty_like(want) for _ in range(16)]  # noqa: F841 (blocks of the size that were free before)
+    first = dense.forward(x, stream=s, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    where = first.data_ptr()
+    torch.cuda._sleep(SLEEP)
+    copy = first.clone()
+    del first
+    second = dense.forward(x, stream=s, **kw)
+    assert second.data_ptr() != where
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and torch.equal(second, want)
