@@ -277,9 +277,9 @@ class Layer:
         n = n_tok if n_tok is not None else (x.shape[0] if x is not None else token_ids.shape[0])
         dev = (x if x is not None else token_ids).device
         if ids_out is None:
-            ids_out = torch.empty((n, self.desc.top_k), dtype=torch.int32, device=dev)
+            ids_out = _empty((n, self.desc.top_k), torch.int32, dev, stream)
         if w_out is None:
-            w_out = torch.empty((n, self.desc.top_k), dtype=torch.float32, device=dev)
+            w_out = _empty((n, self.desc.top_k), torch.float32, dev, stream)
         _check(lib().ds4moe_route(self._h, _ptr(x), _ptr(token_ids), n, _ptr(ids_out), _ptr(w_out),
                                   _stream(stream)), "ds4moe_route")
         return ids_out, w_out
@@ -811,9 +811,9 @@ def route_noalloc(desc: LayerDesc, weights: dict, x=None, token_ids=None, ids_ou
     n = n_tok if n_tok is not None else (x.shape[0] if x is not None else token_ids.shape[0])
     dev = (x if x is not None else token_ids).device
     if ids_out is None:
-        ids_out = torch.empty((n, desc.top_k), dtype=torch.int32, device=dev)
+        ids_out = _empty((n, desc.top_k), torch.int32, dev, stream)
     if w_out is None:
-        w_out = torch.empty((n, desc.top_k), dtype=torch.float32, device=dev)
+        w_out = _empty((n, desc.top_k), torch.float32, dev, stream)
     w = _Weights(*[_ptr(weights.get(name)) for name, _ in _Weights._fields_])
     _check(lib().ds4moe_route_noalloc(ctypes.byref(desc.c()), ctypes.byref(w), _ptr(x), _ptr(token_ids), n,
                                       _ptr(ids_out), _ptr(w_out), _ptr(err_flags), _stream(stream)),
