@@ -21,10 +21,25 @@ import ctypes
 import os
 from dataclasses import dataclass
 
-import torch
-from torch import _C
-
 from . import build as _build
+
+
+class _Later:
+    """torch, imported when a call first needs it: a host that only builds the
+    library, or calls it on pointers, has none. From then on the names are the
+    modules themselves, so that calls pay nothing for it."""
+
+    def __init__(self, inner: bool):
+        self._inner = inner
+
+    def __getattr__(self, name):
+        global torch, _C
+        import torch
+        _C = torch._C
+        return getattr(_C if self._inner else torch, name)
+
+
+torch, _C = _Later(False), _Later(True)
 
 ABI_VERSION = 1
 F32, Q8_0, Q2S, Q4S = 0, 1, 2, 3
