@@ -4,7 +4,7 @@
 // A_s is [rank][n_in], B_s [n_out][rank] in 16 bits, x, base and y rows of tokens.
 // Sums are in 32 bits, A x stays in 32 bits between the two products.
 //
-// Few tokens (takes_tokens): k_adapt_token, a cluster of eight blocks per token,
+// Few tokens (choose_way): k_adapt_token, a cluster of eight blocks per token,
 // one launch. A block takes an eighth of the columns of A, the eight exchange
 // their partial sums through distributed shared memory, then each computes an
 // eighth of y. Bound by the latency of that chain and, with many adapters, by
@@ -39,10 +39,11 @@ struct ds4moe_adapters {
   uint16_t *B;       // [slots] of [N][rank rounded up to 8]
   int *perm;         // [max_tokens] tokens in the order of their adapters
   int4 *tiles;       // {slot, first place in perm, tokens | rank << 16, bits of the scale}
-  int *n_tiles;
+  int *n_tiles;      // then, for calls that decide on the device: whether they go token by token, tokens given out
   float *v;          // [max_tokens][R32] scale A x by place in perm
   int path;          // ds4moe_adapters_debug_path
   int clusters[17];  // clusters of so many blocks of k_adapt_shrink that run at once
+  int token_clusters[2];  // clusters of k_adapt_token that run at once, by the type of x
   uint64_t bytes, launches;
 };
 
@@ -66,6 +67,7 @@ struct AdaptArgs {
   int *n_tiles;
   float *v;
   int wide;  // y and base take 16-byte accesses
+  int most;  // tiles above which the call goes token by token (k_adapt_plan decides), or 0: by tiles
   uint32_t *err;
 };
 
@@ -82,6 +84,11 @@ __device__ __forceinline__ float remote_f32(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
   return v;
+}
+__device__ __forceinline__ void remote_store(uint32_t addr, int rank, int v) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(r), "r"(v) : "memory");
 }
 __device__ __forceinline__ float4 remote_f32x4(uint32_t addr, int rank) {
   uint32_t r;
@@ -119,157 +126,175 @@ __device__ __forceinline__ float dot8(const uint4 &w, const float *x, float s) {
   return s;
 }
 
-// (four blocks per SM: all of 64 tokens' blocks run at once)
-template <int DT, bool F32>
+// (four blocks per SM: all of 64 tokens' blocks run at once) LOOP: if k_adapt_plan
+// has decided so, by as many clusters as run at once.
+template <int DT, bool F32, bool LOOP>
 __global__ void __launch_bounds__(256, 4) k_adapt_token(const AdaptArgs a) {
   extern __shared__ __align__(16) float s_x[];  // this block's columns of x
   __shared__ float s_part[LR_MAX_RANK];
   __shared__ __align__(16) float s_v[LR_MAX_RANK];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, c = (int)cluster_rank(), t = blockIdx.x / LR_CLUSTER;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, c = (int)cluster_rank();
+  int t = blockIdx.x / LR_CLUSTER, turn = 0;
+  __shared__ int s_then[2];  // LOOP: the cluster's next token, from its first block, in turns
   pdl_launch_dependents();
   pdl_wait();
-  // Loads that do not wait for one another go first: the slot's own chain (slot,
-  // rank, weights) runs beside x's.
-  bool bad = false;
-  const int s = slot_at(a, t, bad);
-  // pieces of eight columns
-  const int u0 = (int)((long long)(a.K / 8) * c / LR_CLUSTER), nu = (int)((long long)(a.K / 8) * (c + 1) / LR_CLUSTER) - u0;
-  for (int u = tid; u < nu; u += 256) {
-    float4 lo, hi;
-    if (F32) {
-      const float4 *p = reinterpret_cast<const float4 *>((const float *)a.x + (long long)t * a.x_stride) + 2 * (u0 + u);
-      lo = p[0], hi = p[1];
-    } else {
-      const uint4 q = reinterpret_cast<const uint4 *>((const uint16_t *)a.x + (long long)t * a.x_stride)[u0 + u];
-      const float2 f0 = Half16<DT>::up(q.x), f1 = Half16<DT>::up(q.y), f2 = Half16<DT>::up(q.z), f3 = Half16<DT>::up(q.w);
-      lo = make_float4(f0.x, f0.y, f1.x, f1.y), hi = make_float4(f2.x, f2.y, f3.x, f3.y);
+  if (LOOP && !a.n_tiles[1]) return;
+  // Tokens go to clusters as they come free (dealt out ahead: 1000 adapters of rank
+  // 64, 1000 tokens 339 us instead of 286). A block writes a buffer that another
+  // token's values were in when all who read them have passed a barrier since.
+  do {
+    // Loads that do not wait for one another go first: the slot's own chain (slot,
+    // rank, weights) runs beside x's.
+    bool bad = false;
+    const int s = slot_at(a, t, bad);
+    if (LOOP && c == 0 && tid < LR_CLUSTER) {
+      int then = 0;
+      if (tid == 0) then = gridDim.x / LR_CLUSTER + atomicAdd(a.n_tiles + 2, 1);
+      remote_store(smem_u32(s_then + turn), tid, __shfl_sync((1 << LR_CLUSTER) - 1, then, 0));
     }
-    reinterpret_cast<float4 *>(s_x)[2 * u] = lo, reinterpret_cast<float4 *>(s_x)[2 * u + 1] = hi;
-  }
-  if (bad && c == 0 && tid == 0) raise_flag(a.err, DS4MOE_DEVERR_ADAPTER);
-  const int2 in = s >= 0 ? a.info[s] : make_int2(0, 0);
-  const int rank = in.x;
-  const int n0 = (int)((long long)a.N * c / LR_CLUSTER), n1 = (int)((long long)a.N * (c + 1) / LR_CLUSTER);
-  const float *base = a.base ? a.base + (long long)t * a.base_stride : a.y + (long long)t * a.y_stride;
-  float *y = a.y + (long long)t * a.y_stride;
-  if (rank == 0) {  // (the same for all blocks of the cluster)
-    if (a.base)
-      for (int n = n0 + tid; n < n1; n += 256) y[n] = base[n];
-    return;
-  }
-  const int r8 = (rank + 7) & ~7;
-  const uint16_t *A = a.A + (long long)s * a.R32 * a.K, *B = a.B + (long long)s * a.b_slot;
-  if (tid == 0) {  // this block's part of B on its way
-    const uint32_t bytes = (uint32_t)min((long long)(n1 - n0) * r8 * 2, 1ll << 20);
-    if (bytes) prefetch_l2(B + (long long)n0 * r8, bytes);
-  }
-  // J rows of A per warp at a time (rows past the rank are zeros up to a multiple
-  // of 32); the first pieces are requested before x is waited for
-  auto rows_of_a = [&](auto per_warp) {
-    constexpr int J = decltype(per_warp)::value;
-    const uint4 *p = reinterpret_cast<const uint4 *>(A + (long long)(J * w) * a.K) + u0;
-    const long long row = a.K / 8;
-    uint4 first[J];
-#pragma unroll
-    for (int j = 0; j < J; j++) {
-      first[j] = make_uint4(0, 0, 0, 0);
-      if (J * w < rank && lane < nu) first[j] = p[j * row + lane];
-    }
-    __syncthreads();
-    auto add = [&](const uint4 (&wt)[J], int u, float (&sum)[J]) {
-      float x[8];
-      *reinterpret_cast<float4 *>(x) = reinterpret_cast<const float4 *>(s_x)[2 * u];
-      *reinterpret_cast<float4 *>(x + 4) = reinterpret_cast<const float4 *>(s_x)[2 * u + 1];
-#pragma unroll
-      for (int j = 0; j < J; j++) sum[j] = dot8<DT>(wt[j], x, sum[j]);
-    };
-    for (int r0 = J * w; r0 < rank; r0 += 8 * J, p += 8 * J * row) {
-      float sum[J] = {};
-      int u = lane;
-      if (r0 == J * w) {
-        if (u < nu) add(first, u, sum);
-        u += 32;
+    // pieces of eight columns
+    const int u0 = (int)((long long)(a.K / 8) * c / LR_CLUSTER), nu = (int)((long long)(a.K / 8) * (c + 1) / LR_CLUSTER) - u0;
+    for (int u = tid; u < nu; u += 256) {
+      float4 lo, hi;
+      if (F32) {
+        const float4 *p = reinterpret_cast<const float4 *>((const float *)a.x + (long long)t * a.x_stride) + 2 * (u0 + u);
+        lo = p[0], hi = p[1];
+      } else {
+        const uint4 q = reinterpret_cast<const uint4 *>((const uint16_t *)a.x + (long long)t * a.x_stride)[u0 + u];
+        const float2 f0 = Half16<DT>::up(q.x), f1 = Half16<DT>::up(q.y), f2 = Half16<DT>::up(q.z), f3 = Half16<DT>::up(q.w);
+        lo = make_float4(f0.x, f0.y, f1.x, f1.y), hi = make_float4(f2.x, f2.y, f3.x, f3.y);
       }
+      reinterpret_cast<float4 *>(s_x)[2 * u] = lo, reinterpret_cast<float4 *>(s_x)[2 * u + 1] = hi;
+    }
+    if (bad && c == 0 && tid == 0) raise_flag(a.err, DS4MOE_DEVERR_ADAPTER);
+    const int2 in = s >= 0 ? a.info[s] : make_int2(0, 0);
+    const int rank = in.x;
+    const int n0 = (int)((long long)a.N * c / LR_CLUSTER), n1 = (int)((long long)a.N * (c + 1) / LR_CLUSTER);
+    const float *base = a.base ? a.base + (long long)t * a.base_stride : a.y + (long long)t * a.y_stride;
+    float *y = a.y + (long long)t * a.y_stride;
+    if (rank == 0) {  // (the same for all blocks of the cluster)
+      if (a.base)
+        for (int n = n0 + tid; n < n1; n += 256) y[n] = base[n];
+      if (LOOP) {
+        cluster_arrive();
+        cluster_wait();
+      }
+      continue;
+    }
+    const int r8 = (rank + 7) & ~7;
+    const uint16_t *A = a.A + (long long)s * a.R32 * a.K, *B = a.B + (long long)s * a.b_slot;
+    if (tid == 0) {  // this block's part of B on its way
+      const uint32_t bytes = (uint32_t)min((long long)(n1 - n0) * r8 * 2, 1ll << 20);
+      if (bytes) prefetch_l2(B + (long long)n0 * r8, bytes);
+    }
+    // J rows of A per warp at a time (rows past the rank are zeros up to a multiple
+    // of 32); the first pieces are requested before x is waited for
+    auto rows_of_a = [&](auto per_warp) {
+      constexpr int J = decltype(per_warp)::value;
+      const uint4 *p = reinterpret_cast<const uint4 *>(A + (long long)(J * w) * a.K) + u0;
+      const long long row = a.K / 8;
+      uint4 first[J];
+#pragma unroll
+      for (int j = 0; j < J; j++) {
+        first[j] = make_uint4(0, 0, 0, 0);
+        if (J * w < rank && lane < nu) first[j] = p[j * row + lane];
+      }
+      __syncthreads();
+      auto add = [&](const uint4 (&wt)[J], int u, float (&sum)[J]) {
+        float x[8];
+        *reinterpret_cast<float4 *>(x) = reinterpret_cast<const float4 *>(s_x)[2 * u];
+        *reinterpret_cast<float4 *>(x + 4) = reinterpret_cast<const float4 *>(s_x)[2 * u + 1];
+#pragma unroll
+        for (int j = 0; j < J; j++) sum[j] = dot8<DT>(wt[j], x, sum[j]);
+      };
+      for (int r0 = J * w; r0 < rank; r0 += 8 * J, p += 8 * J * row) {
+        float sum[J] = {};
+        int u = lane;
+        if (r0 == J * w) {
+          if (u < nu) add(first, u, sum);
+          u += 32;
+        }
 #pragma unroll 2
-      for (; u < nu; u += 32) {
-        uint4 wt[J];
+        for (; u < nu; u += 32) {
+          uint4 wt[J];
 #pragma unroll
-        for (int j = 0; j < J; j++) wt[j] = p[j * row + u];
-        add(wt, u, sum);
-      }
+          for (int j = 0; j < J; j++) wt[j] = p[j * row + u];
+          add(wt, u, sum);
+        }
 #pragma unroll
-      for (int o = 16; o; o >>= 1)
+        for (int o = 16; o; o >>= 1)
 #pragma unroll
-        for (int j = 0; j < J; j++) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-      if (lane == 0) {
+          for (int j = 0; j < J; j++) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+        if (lane == 0) {
 #pragma unroll
-        for (int j = 0; j < J; j++) s_part[r0 + j] = sum[j];
-      }
-    }
-  };
-  if (rank <= 16) rows_of_a(std::integral_constant<int, 2>());
-  else rows_of_a(std::integral_constant<int, 4>());
-  cluster_arrive();
-  const float scale = __int_as_float(in.y);
-  // U lanes per row of B, so that a load takes whole lines: the lane's piece of
-  // eight ranks is the same for all rows. A warp takes 32 rows, 32 / U at a time,
-  // of which lane l ends up with row (l % U) * (32 / U) + l / U. The first pieces
-  // are requested before the other blocks' sums are waited for.
-  const int units = r8 / 8;
-  auto rows_of_b = [&](auto lanes) {
-    constexpr int U = decltype(lanes)::value, G = 32 / U, H = U < 4 ? U : 4;
-    const int u = lane % U, g = lane / U;
-    uint4 wt[H];
-    auto request = [&](int r0, int b) {
-#pragma unroll
-      for (int k = 0; k < H; k++) {
-        const int n = r0 + (b + k) * G + g;
-        wt[k] = make_uint4(0, 0, 0, 0);
-        if (n < n1 && u < units) wt[k] = *reinterpret_cast<const uint4 *>(B + (long long)n * r8 + 8 * u);
+          for (int j = 0; j < J; j++) s_part[r0 + j] = sum[j];
+        }
       }
     };
-    int r0 = n0 + 32 * w;
-    float from = r0 + u * G + g < n1 ? base[r0 + u * G + g] : 0.0f;
-    request(r0, 0);
-    cluster_wait();
-    if (tid < r8) {
-      float v = 0.0f;
-      if (tid < rank)
-#pragma unroll
-        for (int i = 0; i < LR_CLUSTER; i++) v += remote_f32(smem_u32(s_part + tid), i);
-      s_v[tid] = v * scale;
-    }
-    __syncthreads();
-    cluster_arrive();  // the others' sums are read: they may leave
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[e] = u < units ? s_v[8 * u + e] : 0.0f;
-    for (; r0 < n1; r0 += 256) {
-      const int mine = r0 + u * G + g;
-      float keep = 0.0f;
-#pragma unroll
-      for (int b = 0; b < U; b += H) {
+    if (rank <= 16) rows_of_a(std::integral_constant<int, 2>());
+    else rows_of_a(std::integral_constant<int, 4>());
+    cluster_arrive();
+    const float scale = __int_as_float(in.y);
+    // U lanes per row of B, so that a load takes whole lines: the lane's piece of
+    // eight ranks is the same for all rows. A warp takes 32 rows, 32 / U at a time,
+    // of which lane l ends up with row (l % U) * (32 / U) + l / U. The first pieces
+    // are requested before the other blocks' sums are waited for.
+    const int units = r8 / 8;
+    auto rows_of_b = [&](auto lanes) {
+      constexpr int U = decltype(lanes)::value, G = 32 / U, H = U < 4 ? U : 4;
+      const int u = lane % U, g = lane / U;
+      uint4 wt[H];
+      auto request = [&](int r0, int b) {
 #pragma unroll
         for (int k = 0; k < H; k++) {
-          float sum = dot8<DT>(wt[k], v, 0.0f);
-#pragma unroll
-          for (int o = U / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (b + k == u) keep = sum;
+          const int n = r0 + (b + k) * G + g;
+          wt[k] = make_uint4(0, 0, 0, 0);
+          if (n < n1 && u < units) wt[k] = *reinterpret_cast<const uint4 *>(B + (long long)n * r8 + 8 * u);
         }
-        if (b + H < U) request(r0, b + H);
-        else if (r0 + 256 < n1) request(r0 + 256, 0);
+      };
+      int r0 = n0 + 32 * w;
+      float from = r0 + u * G + g < n1 ? base[r0 + u * G + g] : 0.0f;
+      request(r0, 0);
+      cluster_wait();
+      if (tid < r8) {
+        float v = 0.0f;
+        if (tid < rank)
+#pragma unroll
+          for (int i = 0; i < LR_CLUSTER; i++) v += remote_f32(smem_u32(s_part + tid), i);
+        s_v[tid] = v * scale;
       }
-      if (mine < n1) y[mine] = from + keep;
-      from = mine + 256 < n1 ? base[mine + 256] : 0.0f;
-    }
-  };
-  if (units == 1) rows_of_b(std::integral_constant<int, 1>());
-  else if (units == 2) rows_of_b(std::integral_constant<int, 2>());
-  else if (units <= 4) rows_of_b(std::integral_constant<int, 4>());
-  else if (units <= 8) rows_of_b(std::integral_constant<int, 8>());
-  else if (units <= 16) rows_of_b(std::integral_constant<int, 16>());
-  else rows_of_b(std::integral_constant<int, 32>());
-  cluster_wait();
+      __syncthreads();
+      cluster_arrive();  // the others' sums are read: they may leave
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[e] = u < units ? s_v[8 * u + e] : 0.0f;
+      for (; r0 < n1; r0 += 256) {
+        const int mine = r0 + u * G + g;
+        float keep = 0.0f;
+#pragma unroll
+        for (int b = 0; b < U; b += H) {
+#pragma unroll
+          for (int k = 0; k < H; k++) {
+            float sum = dot8<DT>(wt[k], v, 0.0f);
+#pragma unroll
+            for (int o = U / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (b + k == u) keep = sum;
+          }
+          if (b + H < U) request(r0, b + H);
+          else if (r0 + 256 < n1) request(r0 + 256, 0);
+        }
+        if (mine < n1) y[mine] = from + keep;
+        from = mine + 256 < n1 ? base[mine + 256] : 0.0f;
+      }
+    };
+    if (units == 1) rows_of_b(std::integral_constant<int, 1>());
+    else if (units == 2) rows_of_b(std::integral_constant<int, 2>());
+    else if (units <= 4) rows_of_b(std::integral_constant<int, 4>());
+    else if (units <= 8) rows_of_b(std::integral_constant<int, 8>());
+    else if (units <= 16) rows_of_b(std::integral_constant<int, 16>());
+    else rows_of_b(std::integral_constant<int, 32>());
+    cluster_wait();
+  } while (LOOP && (t = s_then[turn], turn ^= 1, t < a.T));
 }
 
 // ---------------------------------------------------------------------------
@@ -342,7 +367,10 @@ __global__ void __launch_bounds__(1024) k_adapt_plan(const AdaptArgs a) {
     for (int k = 0; k < s_n[s]; k += 128) a.tiles[t0++] = make_int4(s, r0 + k, min(128, s_n[s] - k) | rank[i] << 16, scale);
     r0 += s_n[s];
   }
-  if (tid == 1023) *a.n_tiles = t0;
+  if (tid == 1023) {
+    const bool tokens = a.most && t0 > a.most;
+    a.n_tiles[0] = tokens ? 0 : t0, a.n_tiles[1] = tokens, a.n_tiles[2] = 0;
+  }
 #pragma unroll
   for (int i = 0; i < PER; i++)
     if (tid * PER + i <= a.slots) s_n[tid * PER + i] = places[i];
@@ -1025,7 +1053,7 @@ ds4moe_status ap_status(cudaError_t e) {
 }
 
 struct AdaptFns {
-  const void *token, *shrink, *shrink_many, *expand;
+  const void *token, *token_loop, *shrink, *shrink_many, *expand;
 };
 template <int DT, bool F32, bool MANY>
 const void *shrink_of(int r32) {
@@ -1034,7 +1062,7 @@ const void *shrink_of(int r32) {
 }
 template <int DT, bool F32>
 AdaptFns fns_of(int r32) {
-  return {(const void *)k_adapt_token<DT, F32>, shrink_of<DT, F32, false>(r32), shrink_of<DT, F32, true>(r32),
+  return {(const void *)k_adapt_token<DT, F32, false>, (const void *)k_adapt_token<DT, F32, true>, shrink_of<DT, F32, false>(r32), shrink_of<DT, F32, true>(r32),
           r32 <= 128 ? (const void *)k_adapt_expand<DT, true> : (const void *)k_adapt_expand<DT, false>};
 }
 AdaptFns adapt_fns(int dtype, bool f32, int r32) {
@@ -1054,18 +1082,36 @@ cudaError_t launch_cluster(const void *fn, int grid, int cluster, int threads, s
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-// Whether a call goes token by token or by tiles. Measured with up to 512 tokens
-// (us), m = max_rank * (n_in + n_out) in millions: token by token a wave of four
-// blocks per SM takes 2.9 + 11 m; tiles take 15 + 13 m and 0.6 for every adapter
-// that there may be. 4096 x 4096, rank 64, 4 adapters: 64 tokens 12 and 22, 128 22
-// and 23, 256 39 and 23; 64 adapters: 256 44 and 88, 512 81 and 90; rank 16, 4
-// adapters: 256 18 and 21, 512 34 and 24; 8192 x 8192, rank 128, 8 adapters: 64 32
-// and 43, 128 60 and 45.
-bool takes_tokens(const ds4moe_adapters *h, int n_tok) {
-  if (h->path) return h->path == 1;
-  const double m = 1e-6 * h->max_rank * (double)(h->K + h->N);
+size_t token_smem(int n_in) { return (size_t)(n_in / 8 / LR_CLUSTER + 1) * 32; }
+
+// Whether a call goes token by token (-1), by tiles (0), or whichever is shorter
+// once the number of tiles is known on the device: the most for which tiles are.
+//
+// Tiles are a 128th of the tokens if all have one adapter, and with as many adapters
+// as there are slots or tokens one more for each. Times in us, measured with 64 to
+// 4096 tokens (tokens, tiles): token by token a wave of four blocks per SM reads the
+// adapter again, out of L2; by tiles every tile costs its turn in three kernels.
+//   4096 x 4096, rank 16    512 tokens of 1 adapter 37, 25; of 64 37, 88; of 512 52, 529; 4096 of 1 289, 71
+//                rank 64    64 of 1 20, 25; 512 of 1 74, 27; of 64 82, 96; of 512 128, 567; 4096 of 512 603, 719
+//                rank 256   64 of 1 39, 36; 512 of 1 231, 40; of 64 270, 330; 4096 of 512 2015, 2405
+//   512 x 512, rank 16      512 of 1 28, 23; of 512 29, 160; 4096 of 1 191, 24; of 512 193, 89
+//   8192 x 8192, rank 128   64 of 1 35, 31; 512 of 64 235, 240; of 512 497, 1586
+// A decision on the device takes launches that find nothing to do (2 to 3 us for tiles;
+// some 10 token by token, and blocks that take several tokens, 1.3 times the time at
+// most: 256 to 1000 of rank 64 and as many adapters 69, 90 and 243, 286). It is left to the
+// device where tiles may take 0.6 of the time or less.
+int choose_way(const ds4moe_adapters *h, int n_tok) {
+  if (h->path) return h->path == 1 ? -1 : 0;
+  const double r = h->max_rank, size = (double)h->K + h->N;
   const int waves = (n_tok * LR_CLUSTER + 4 * h->n_sm - 1) / (4 * h->n_sm);
-  return waves * (2.9 + 11.0 * m) <= 15.0 + 13.0 * m + 0.6 * (std::min(h->slots, n_tok) - 1);
+  const double tokens = waves * (2.9 + 0.05 * r + 1e-6 * r * (14.0 * h->N + 5.8 * h->K));
+  const double start = 20.0 + size * (6e-4 + 4.5e-7 * n_tok), tile = 0.2 + size * (h->R32 <= 64 ? 1e-4 : h->R32 <= 128 ? 1.6e-4 : 4.6e-4);
+  const int full = n_tok / 128, least = (n_tok + 127) / 128, most = full + std::min(h->slots + 1, n_tok);
+  const double surely = start + tile * (most - 1), at_best = start + tile * (least - 1);
+  if (tokens >= surely) return 0;
+  if (tokens <= 1.7 * at_best) return -1;
+  if (tokens + 10.0 >= surely) return 0;
+  return 1 + (int)((tokens - start) / tile);
 }
 
 }  // namespace
@@ -1092,7 +1138,7 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
     return p;
   };
   const size_t o_err = place(64), o_info = place((size_t)n_slots * 8), zeroed = at;
-  const size_t o_perm = place((size_t)max_tokens * 4), o_n = place(4);
+  const size_t o_perm = place((size_t)max_tokens * 4), o_n = place(12);
   const size_t o_tiles = place(((size_t)max_tokens / 128 + std::min(n_slots + 1, max_tokens) + 1) * 16);
   const size_t o_v = place((size_t)max_tokens * h->R32 * 4);
   const size_t o_a = place((size_t)n_slots * h->R32 * n_in * 2), o_b = place((size_t)n_slots * h->b_slot * 2);
@@ -1100,11 +1146,22 @@ ds4moe_status ds4moe_adapters_create(int32_t n_out, int32_t n_in, int32_t n_slot
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device);
   for (bool f32 : {false, true}) {
     const AdaptFns f = adapt_fns(dtype, f32, h->R32);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f.token, cudaFuncAttributeMaxDynamicSharedMemorySize, ((1 << 16) / LR_CLUSTER + 8) * 4);
+    for (const void *fn : {f.token, f.token_loop})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ((1 << 16) / LR_CLUSTER + 8) * 4);
     for (const void *fn : {f.shrink, f.shrink_many, f.expand})
       if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LR_SMEM);
     for (const void *fn : {f.shrink, f.shrink_many})
       if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      cfg.gridDim = dim3(LR_CLUSTER), cfg.blockDim = dim3(256), cfg.dynamicSmemBytes = token_smem(n_in);
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = LR_CLUSTER, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr, cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&h->token_clusters[f32], f.token_loop, &cfg);
+      if (e == cudaSuccess && h->token_clusters[f32] < 1) h->token_clusters[f32] = 1;
+    }
     for (int ks = 1; ks <= 2 * LR_CLUSTER && e == cudaSuccess; ks += ks < LR_CLUSTER ? 1 : LR_CLUSTER) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
@@ -1181,14 +1238,20 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
   a.wide = N % 4 == 0 && y_stride % 4 == 0 && !((uintptr_t)y & 15) && (!base || (base_stride % 4 == 0 && !((uintptr_t)base & 15)));
   const AdaptFns f = adapt_fns(h->dtype, f32, h->R32);
   const cudaStream_t s = (cudaStream_t)stream;
-  if (takes_tokens(h, n_tok)) {
+  const int way = choose_way(h, n_tok);
+  if (way < 0) {
     void *args[] = {&a};
-    const cudaError_t e = launch_cluster(f.token, LR_CLUSTER * n_tok, LR_CLUSTER, 256, (size_t)(K / 8 / LR_CLUSTER + 1) * 32, s, args);
+    const cudaError_t e = launch_cluster(f.token, LR_CLUSTER * n_tok, LR_CLUSTER, 256, token_smem(h->K), s, args);
     h->launches++;
     return ap_status(e);
   }
+  a.most = way;
   void *plan[] = {&a};
   cudaError_t e = launch_pdl((const void *)k_adapt_plan, dim3(1), dim3(1024), 0, s, plan, true);
+  if (e == cudaSuccess && way) {
+    e = launch_cluster(f.token_loop, h->token_clusters[f32] * LR_CLUSTER, LR_CLUSTER, 256, token_smem(h->K), s, plan);
+    h->launches++;
+  }
   if (e == cudaSuccess) {
     // Blocks of a tile: the fewest chunks of 32 columns one after another, six
     // more for a tile's start and sum, with some tiles that are not full; but chains

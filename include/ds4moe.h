@@ -393,8 +393,9 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  *          otherwise (columns of one matrix do not; rows in gaps of another
  *          distance in bytes are taken for overlapping: INVALID_ARG)
  *   Strides are below 2^31 elements.
- *   Enqueued on `stream` (one launch for few tokens, else three), no allocation,
- *   no synchronisation. Calls on one handle must not run concurrently (shared
+ *   Enqueued on `stream` (one launch for few tokens, three for many, four where the
+ *   number of adapters that the call uses decides, on the device; the slots that
+ *   the handle has do not), no allocation, no synchronisation. Calls on one handle must not run concurrently (shared
  *   workspace). Errors: INVALID_ARG, CUDA.
  * ds4moe_adapters_debug_path: 1: every later call token by token, 2: by tiles of
  *   tokens of one adapter, 0: by the number of tokens (a test hook; results differ by
