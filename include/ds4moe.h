@@ -565,8 +565,18 @@ ds4moe_status ds4moe_attn_decode(ds4moe_attn *h, const ds4moe_kv_cache *cache, c
  * for shared_len outside the table (clamped) and bounds out of order (as cu_q).
  * Where sharing would gain nothing (few shared positions or sequences; shapes whose
  * sequences fill the products' tiles by themselves; handles with a window, which
- * see little of what is shared) the plain path is taken, decided on the device
- * for every group: the argument never changes a result but by its roundings.
+ * see little of what is shared) every sequence reads its positions itself: the
+ * argument never changes a result but by its roundings (the weights of shared
+ * positions of fp16 are scaled as ds4moe_attn_prefill does it: one below 2^-31 of
+ * the largest is 0, in ds4moe_attn_decode's kernel of few rows one below 2^-39).
+ * That is decided twice. On the host, by the table's capacity max_pages *
+ * page_size, the most that can be shared: where that would gain nothing, and with
+ * a window, the call is ds4moe_attn_decode, launch for launch and bit for bit, and
+ * neither array is read or flagged. Else on the device for every group, and a call
+ * that shares nothing there still has the launches of one that does (8 sequences
+ * of 1700, 32/8 heads of 128: 16 us plain, 28 to 31 so; 8 of 25000: 134 and 148;
+ * 64 of 5000: 196 and 211). So give max_pages no larger than the batch's longest
+ * sequence needs, in a table of any table_stride.
  * ds4moe_attn_reserve_shared: workspace for such calls of up to max_tokens
  * (n_seq * n_new) rows, at most the handle's: max_tokens * n_heads * (head_dim +
  * 1) * 4 bytes. Allocates, synchronises; a smaller number than before changes
