@@ -1013,7 +1013,9 @@ __global__ void __launch_bounds__(LE_THREADS, 1) k_adapt_expand(const AdaptArgs 
 }
 
 // A slot's weights into its place: rows of A padded with zeros to r32, rows of B
-// to r8.
+// to r8. Two bytes a thread: up to 4 MB of weights (rank 128, 8192 x 8192) a call takes
+// the 5.7 to 6 us of its host side, 8 MB 8.6, 9.4 MB 11.2 (read and written, 1.7 to 2.0
+// TB/s): what one adapter of a step's next request costs, not every step.
 __global__ void __launch_bounds__(256) k_adapt_set(const uint16_t *A, const uint16_t *B, int rank, float scale, int K, int N,
                                                uint16_t *dA, uint16_t *dB, int2 *info) {
   pdl_launch_dependents();

@@ -200,10 +200,10 @@ __device__ __forceinline__ bool append_page(const KvView &kv, int b, long long p
 // in 32 bits, rounded once. A thread takes 16 elements (two pieces of 8, so
 // that it holds both halves of its pairs) of `per` rows of one token; a block
 // computes the sines of its tokens' angles once, for all their heads (every
-// thread its own eight: 12291 tokens of 32 + 2 x 8 heads of 128 from fp32 81 us
-// instead of 74, 1064 rows of 48 heads of 64 13.0 us instead of 9.0). Bound by the
-// bytes: 6.1 TB/s, of 6.8 for a copy. Rows one at a time: four of them in
-// registers took 151 of these and 104 us, for fewer blocks fit.
+// thread its own eight: 1.1 times as long for 12291 tokens of 32 + 2 x 8 heads of 128
+// from fp32, 1064 rows of 48 heads of 64 13.0 us instead of 9.0). Bound by the
+// bytes: 12291 tokens 76 us, 5.9 TB/s, of 6.8 for a copy. Rows one at a time: four of
+// them in registers took 151 of these and 1.4 times as long, for fewer blocks fit.
 //
 // Angles: p * inv_freq / 2 pi in turns, modulo one turn, in 64-bit fixed point
 // (a phase accumulator): the product with the integer p wraps by itself. An
@@ -677,7 +677,7 @@ ds4moe_status ds4moe_kv_append_rope(ds4moe_attn *h, const ds4moe_kv_cache *cache
   a.rot = rope->rot_dim, a.off = rope->offset, a.interleaved = rope->interleaved;
   a.inv_freq = rope->inv_freq, a.scale = rope->scale, a.err = h->err;
   // More than one wave of threads: six rows of a token per thread (12291 tokens of
-  // 48 rows 74 us; one 81, two 81, four 75, sixteen 76); else one.
+  // 48 rows, in one run of all: 74 us; one 81, two 81, four 75, sixteen 76); else one.
   const long long items = (long long)n_tok * a.rows << a.ish;
   a.per = items > (long long)h->n_sm * 2048 ? 6 : 1;
   a.slices = (a.rows + a.per - 1) / a.per;
