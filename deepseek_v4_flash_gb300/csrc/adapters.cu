@@ -460,12 +460,12 @@ constexpr int LR_SMEM = 224 * 1024;  // a block has an SM (and all of its tensor
 // were off by 4e-6 of the result, five times what 32-bit sums are. So chunks go
 // round several accumulators, the low parts of x to one of their own, added up
 // in 32 bits at the end. Where the accumulators that there is room for would take
-// more than 37 additions each (fp32 inputs: ranks above 128 from 4128 columns on,
-// above 64 from 12320, others from 28704; 16-bit ones, which need no accumulator for
-// low parts: 8224, 16416, 32800), a block takes its columns in `rounds`, whose sums meet in 32 bits in V. Measured, error of the result
-// and time of 4096 tokens, in one round and so: rank 256, 8192 columns and 8192
-// outputs 1.8e-6 322 us, 1.2e-6 367 us; 65536 columns and 512 outputs 1.0e-5 729 us,
-// 1.2e-6 1512 us.
+// more than 37 additions each (fp32 inputs: ranks of 161 to 256 from 4128 columns on,
+// of 128 from 12320, up to 64 from 28704; 16-bit ones, which need no accumulator for
+// low parts: 8224, 16416, 32800), a block takes its columns in `passes`, whose sums
+// meet in 32 bits in V. Measured, error of the result and time of 4096 tokens, in one
+// pass and so: rank 256, 8192 columns and 8192 outputs 1.8e-6 322 us, 1.2e-6 367 us;
+// 65536 columns and 512 outputs 1.0e-5 729 us, 1.2e-6 1512 us.
 constexpr int LR_WARPS = 8, LR_GROUPS = 2, LR_FEED = LR_WARPS * 32 / LR_GROUPS;
 // 32-column parts of a chunk: two, while two stages of them fit.
 __host__ __device__ constexpr int shrink_ch(int r32) { return r32 <= 128 ? 2 : 1; }
@@ -479,9 +479,9 @@ __host__ __device__ constexpr int shrink_stages(bool f32, int r32) {
 __host__ __device__ constexpr int shrink_accs(int r32) { return 512 / r32 < 8 ? 512 / r32 : 8; }
 
 // WP: 16-byte pieces of A per thread and part, a 32nd of the largest rank. MANY:
-// more than one round (of its own: the others' registers are all in use).
+// more than one pass (of its own: the others' registers are all in use).
 template <int DT, bool F32, int WP, bool MANY>
-__global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const AdaptArgs a, int ks, int n_rounds) {
+__global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const AdaptArgs a, int ks, int n_passes) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[2 * 6 + 1];
   __shared__ uint32_t s_tmem;
@@ -509,15 +509,15 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
   pdl_launch_dependents();
   pdl_wait();
   const int k = (int)cluster_rank(), n_tiles = *a.n_tiles, n_cl = gridDim.x / ks;
-  // this block's parts of 32 columns; those of a round, and its chunks
+  // this block's parts of 32 columns; those of a pass, and its chunks
   const int all0 = (a.K / 32) * k / ks, all = (a.K / 32) * (k + 1) / ks - all0;
-  const int rounds = MANY ? n_rounds : 1;
+  const int passes = MANY ? n_passes : 1;
   int p0, np, nc;
-  auto set_round = [&](int r) {
-    const int from = all * r / rounds;
-    p0 = all0 + from, np = all * (r + 1) / rounds - from, nc = (np + CH - 1) / CH;
+  auto set_pass = [&](int r) {
+    const int from = all * r / passes;
+    p0 = all0 + from, np = all * (r + 1) / passes - from, nc = (np + CH - 1) / CH;
   };
-  set_round(0);
+  set_pass(0);
   // accumulators of the high parts; the low parts' one comes after them
   const int n_acc = shrink_accs(a.R32) - (F32 ? 1 : 0);
   Waits ws;
@@ -527,10 +527,10 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
   int tok[XP];
   const uint16_t *ap;
   int r32 = 0;
-  // the next tile with a rank, from i on, round r of it, and this thread's part of that
+  // the next tile with a rank, from i on, pass r of it, and this thread's part of that
   auto begin = [&](int i, int r) {
     int4 tile = make_int4(0, 0, 0, 0);
-    if (MANY) set_round(r);
+    if (MANY) set_pass(r);
     for (; i < n_tiles; i += n_cl) {
       tile = a.tiles[i];
       if (tile.z >> 16) break;
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     for (; st < 0; st += nst) lap--;
   };
   int tiles = 0;
-  int i = begin(blockIdx.x / ks, 0), round = 0;
+  int i = begin(blockIdx.x / ks, 0), pass = 0;
   if (w < LR_WARPS) {
     if (i < n_tiles) {
       if (group == 0) ask_first(i);
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     const int4 tile = a.tiles[i];
     const int rank = tile.z >> 16, rows = tile.z & 0xFFFF, r32_now = (rank + 31) & ~31;
     const int np_now = np, nc_now = nc;
-    const bool again = MANY && round + 1 < rounds;  // the tile's next round follows
+    const bool again = MANY && pass + 1 < passes;  // the tile's next pass follows
     int next;
     if (w < LR_WARPS) {
       int c = group;
@@ -626,8 +626,8 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
         if (lane == 0) mbar_arrive(full(st));
       }
       advance(nc + group - c);  // all warps' chunks follow on the tile's nc chunks
-      // the next tile's (or round's) first chunks come in while this one is added up
-      next = begin(again ? i : i + n_cl, again ? round + 1 : 0);
+      // the next tile's (or pass's) first chunks come in while this one is added up
+      next = begin(again ? i : i + n_cl, again ? pass + 1 : 0);
       if (next < n_tiles) {
         if (group == 0) ask_first(next);
         fetch(group);
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
         }
         __syncwarp();
       }
-      next = begin(again ? i : i + n_cl, again ? round + 1 : 0);
+      next = begin(again ? i : i + n_cl, again ? pass + 1 : 0);
     }
     if (nc_now) ws.wait(b_done, tiles & 1);
     __syncwarp();
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
       s.x = c < rank ? s.x * scale : 0.0f, s.y = c + 1 < rank ? s.y * scale : 0.0f;
       s.z = c + 2 < rank ? s.z * scale : 0.0f, s.w = c + 3 < rank ? s.w * scale : 0.0f;
       float4 *v = reinterpret_cast<float4 *>(a.v + (long long)(tile.y + row) * a.R32 + c);
-      if (MANY && round) {  // (this thread stored the rounds before)
+      if (MANY && pass) {  // (this thread stored the passes before)
         const float4 o = *v;
         s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
       }
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(LR_WARPS * 32 + 32, 1) k_adapt_shrink(const Ad
     cluster_wait();
     tc_fence_after();
     tiles += nc_now != 0;
-    i = next, round = again ? round + 1 : 0;
+    i = next, pass = again ? pass + 1 : 0;
   }
   if (!ws.ok && lane == 0) raise_flag(a.err, DS4MOE_DEVERR_TIMEOUT);
   tc_fence_before();
@@ -1259,7 +1259,7 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
     // more for a tile's start and sum, with some tiles that are not full; but chains
     // of additions that stay exact (four of each chunk, up to 37 to an accumulator,
     // see k_adapt_shrink: 41 were off by 1.06e-6, twice what 32-bit sums are), where
-    // need be with twice the largest portable cluster and in rounds of eight chunks to
+    // need be with twice the largest portable cluster and in passes of eight chunks to
     // an accumulator.
     const int most = n_tok / 128 + std::min(h->slots + 1, n_tok) + 1, full = n_tok / 128 + 1, guess = full + std::min(h->slots, full) / 2;
     const int n_acc = shrink_accs(h->R32) - (f32 ? 1 : 0);
@@ -1269,14 +1269,14 @@ ds4moe_status ds4moe_adapters_forward(ds4moe_adapters *h, const void *x, int64_t
       const long long chunks = (K / 32 + c - 1) / c, cost = (guess + h->clusters[c] - 1) / h->clusters[c] * (chunks + 6);
       if (4 * chunks <= 37 * n_acc && (!ks || cost < best)) best = cost, ks = c;
     }
-    int rounds = 1;
+    int passes = 1;
     if (!ks) {
       ks = h->clusters[2 * LR_CLUSTER] ? 2 * LR_CLUSTER : LR_CLUSTER;
-      rounds = ((h->K / 32 + ks - 1) / ks + 8 * n_acc - 1) / (8 * n_acc);
+      passes = ((h->K / 32 + ks - 1) / ks + 8 * n_acc - 1) / (8 * n_acc);
     }
     const int grid = std::min(h->clusters[ks], most) * ks;
-    void *args[] = {&a, &ks, &rounds};
-    e = launch_cluster(rounds > 1 ? f.shrink_many : f.shrink, grid, ks, LR_WARPS * 32 + 32, LR_SMEM, s, args);
+    void *args[] = {&a, &ks, &passes};
+    e = launch_cluster(passes > 1 ? f.shrink_many : f.shrink, grid, ks, LR_WARPS * 32 + 32, LR_SMEM, s, args);
     if (e == cudaSuccess) {
       const long long items = (long long)most * ((N + 127) / 128);
       e = launch_pdl(f.expand, dim3((unsigned)std::min<long long>(items, h->n_sm)), dim3(LE_THREADS), LR_SMEM, s, plan, true);
