@@ -366,9 +366,9 @@ ds4moe_status ds4moe_dense_debug_config(ds4moe_dense *h, int32_t ks, int32_t nst
  * output is the base.) x and weights as they are, products and sums in 32 bits:
  * no rounding to fewer bits on the way (many tokens: a product's fp32 operand
  * is taken as the sum of two 11-bit numbers, off by 2^-20 of it at most, and the
- * tensor cores cut sums to 24 bits instead of rounding them: what is added to
- * base, as a whole, is off by less than 2^-19 at any rank and width; token by
- * token by less than 2^-20).
+ * tensor cores cut sums to 24 bits instead of rounding them: for terms of random
+ * sign the matrix that is added to base is off by less than 2^-19 of its norm at
+ * any rank and width; token by token by less than 2^-20).
  *
  * ds4moe_adapters_create: places for n_slots (1..4096) adapters of up to max_rank
  *   (1..256) in `dtype` (DS4MOE_DT_BF16 or DS4MOE_DT_F16) on the current device,
